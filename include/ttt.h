@@ -291,6 +291,120 @@ int ttt_stream_ex(int32_t heads, int32_t d, int32_t m,
                   int64_t n, int64_t chunk, float lr, int32_t steps, int32_t dtype, uint32_t flags,
                   void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The gated delta rule: the per-token fast-weight layer f_W(x) = W x.
+ *
+ * [Scal3R] eqs. (3), (4) with the squared loss at every token (LaCT's chunk-wise step is
+ * ttt_update): after the decay a_t = e^(g_t), one gradient step of size beta_t on
+ * 1/2 |W k_t - v_t|^2, and the output from the new weights,
+ *   e_t = v_t - a_t W k_t,   W <- a_t W + beta_t e_t k_t^T,   o_t = scale * W q_t.
+ *
+ * Shapes.  heads H, key_heads Hk with H % Hk == 0: head h uses columns of key head
+ *   h / (H / Hk) of q and k.  dk in {64, 128, 256}; dv a multiple of 64 in [64, 1024].
+ * W: fp32, [sequences][H][dv][dk] contiguous, 16-byte aligned (row j of head h multiplies
+ *   the key).  q, k rows hold Hk*dk columns, v and o rows H*dv (row conventions above).
+ * Rates: fp32; beta[h * beta_head_stride + i], decay (g, normally <= 0; NULL: no decay)
+ *   [h * decay_head_stride + i]; stride 0 shares one rate per token across heads.  In the
+ *   chunked calls a g below -200 counts as -200 (e^-200 is 0 in fp32), -infinity included.
+ * cu_seqlens: int32 DEVICE, [sequences + 1] row offsets of the packed sequences, or NULL
+ *   (sequences = 1, all n rows).  Offsets are read on the device: they are clamped to [0, n]
+ *   and to a running maximum, so that any values name disjoint rows.  A sequence may be
+ *   empty (its state passes through).  Rows of no sequence are not read; of o they are
+ *   left as they were, or set to zero with TTT_DELTA_ZERO_UNUSED; gradients of them are zero.
+ * Precision: fp32 states and sums.  fp32 tokens run on fp32 MFMA.  Beside bf16 tokens the
+ *   computed operands keep 17 bits (two bf16 parts), so states and rate gradients are good
+ *   to about 1e-5 relative; o and token gradients are rounded to bf16 once.
+ * Deterministic: the same inputs give the same bits.  n <= 2^31 - 65; chunks x H and
+ *   sequences x H x dv/16 below 2^24.
+ */
+enum { TTT_DELTA_ZERO_UNUSED = 1 };
+/* Bytes of workspace of ttt_delta (backward = 0) or ttt_delta_backward (backward = 1). */
+int ttt_delta_workspace_bytes(int32_t heads, int32_t key_heads, int32_t dk, int32_t dv, int64_t n,
+                              int32_t sequences, int32_t dtype, int32_t backward, size_t *bytes);
+/* The rule over every sequence, in chunks of 64 tokens.  w_out: final states, equal to w
+ * (in place) or disjoint from it.  o must not overlap q, k or v. */
+int ttt_delta(int32_t heads, int32_t key_heads, int32_t dk, int32_t dv, const float *w, float *w_out,
+              const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+              const float *beta, int64_t beta_head_stride, const float *decay, int64_t decay_head_stride,
+              void *o, int64_t ld_o, int64_t n, const int32_t *cu_seqlens, int32_t sequences, float scale,
+              int32_t dtype, uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);
+/* Gradient of ttt_delta.  grad_o: gradient of o; grad_w_out: of the final states (NULL: zero).
+ * grad_q, grad_k, grad_v: token rows like q, k, v (a key head's gradient sums the heads that
+ * share it); grad_beta, grad_decay: fp32 [H][n], or [n] (the sum over heads) of a shared rate;
+ * grad_decay is required exactly when decay is given; grad_w: like w.  The
+ * forward is computed again from the inputs; nothing is kept between calls.  No output may
+ * overlap an input or another output. */
+int ttt_delta_backward(int32_t heads, int32_t key_heads, int32_t dk, int32_t dv, const float *w,
+                       const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                       const float *beta, int64_t beta_head_stride, const float *decay, int64_t decay_head_stride,
+                       const void *grad_o, int64_t ld_grad_o, const float *grad_w_out,
+                       void *grad_q, int64_t ld_grad_q, void *grad_k, int64_t ld_grad_k,
+                       void *grad_v, int64_t ld_grad_v, float *grad_beta, float *grad_decay, float *grad_w,
+                       int64_t n, const int32_t *cu_seqlens, int32_t sequences, float scale, int32_t dtype,
+                       void *workspace, size_t workspace_bytes, void *stream);
+/* One token for each of n rows, in place on a pool of states w [pool][H][dv][dk]: row i uses
+ * state slots[i] (int32, DEVICE) or state i (slots = NULL, n <= pool).  A row whose slot is
+ * outside [0, pool) is padding: nothing is read or written for it (TTT_DELTA_ZERO_UNUSED sets
+ * its o to zero).  Rows that name the same state are applied in row order.  No workspace. */
+int ttt_delta_step(int32_t heads, int32_t key_heads, int32_t dk, int32_t dv, float *w, int32_t pool,
+                   const int32_t *slots, const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                   const void *v, int64_t ld_v, const float *beta, int64_t beta_head_stride,
+                   const float *decay, int64_t decay_head_stride, void *o, int64_t ld_o, int64_t n,
+                   float scale, int32_t dtype, uint32_t flags, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ttt_gated_residual -- the tail of a block around a fast-weight layer: [ZipMap] 关键设计 3's
+ * normalised, gated output, [Scal3R] eqs. (5)-(7)'s scaled residual alpha o GCM(X) + X, and the
+ * norm before the next block:
+ *   u = RMSNorm(o; gamma, groups of norm_width channels) * SiLU(z)
+ *   y = x + alpha * u,      h = RMSNorm(y; gamma_next, the whole row)
+ * with RMSNorm(a)[c] = gamma[c] a[c] / sqrt(mean(a^2) + eps).  Here the gate z is given (a
+ * projection of the block's input); ttt_output_gate computes its own from o.
+ *
+ * x, o, z : [n][ld] device rows, `dtype`, columns [0, channels); z may be NULL (no gate).
+ * gamma, alpha, gamma_next: [channels] fp32, device, 16-byte aligned; gamma, alpha NULL: 1;
+ *           gamma_next NULL: no h (h must be NULL then, and only then).
+ * y, h    : outputs; y may be x (same pointer and row stride); no other overlap.
+ * Requires channels % 8 == 0, channels <= 8192, norm_width % 8 == 0, channels % norm_width == 0,
+ * and the row alignment of the conventions above.  h is computed from the unrounded y.
+ */
+int ttt_gated_residual(int32_t channels, int32_t norm_width, const void *x, int64_t ld_x, const void *o, int64_t ld_o,
+                       const void *z, int64_t ld_z, const float *gamma, const float *alpha, const float *gamma_next,
+                       float eps, void *y, int64_t ld_y, void *h, int64_t ld_h, int64_t n, int32_t dtype,
+                       void *stream);
+/* Gradient.  grad_y, grad_h: gradients of y and h (either may be NULL: zero; grad_h needs
+ * gamma_next given and y); y: the forward's output.  grad_x, grad_o, grad_z (NULL exactly when z is):
+ * rows; grad_gamma, grad_alpha, grad_gamma_next: [channels] fp32, each may be NULL.  The sums over
+ * rows are taken in a fixed order.  grad_x may be grad_y; no other overlap. */
+int ttt_gated_residual_backward_workspace_bytes(int32_t channels, int64_t n, size_t *bytes);
+int ttt_gated_residual_backward(int32_t channels, int32_t norm_width, const void *grad_y, int64_t ld_grad_y,
+                                const void *grad_h, int64_t ld_grad_h, const void *y, int64_t ld_y,
+                                const void *o, int64_t ld_o, const void *z, int64_t ld_z, const float *gamma,
+                                const float *alpha, const float *gamma_next, float eps,
+                                void *grad_x, int64_t ld_grad_x, void *grad_o, int64_t ld_grad_o,
+                                void *grad_z, int64_t ld_grad_z, float *grad_gamma, float *grad_alpha,
+                                float *grad_gamma_next, int64_t n, int32_t dtype, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ttt_orthogonalise -- Muon's Newton-Schulz step ([ZipMap] 关键设计 3, [VGG-T3] 损失函数与训练)
+ * on `batch` matrices of any size, as the optimiser of a layer's projections applies it; ttt_update
+ * does the same inside for its own gradients.  X = G / (||G||_F + 1e-7), transposed while it has
+ * more rows than columns, then `steps` times
+ *   A = X X^T,  X <- a X + (b A + c A A) X,  (a, b, c) = (3.4445, -4.7750, 2.0315).
+ *
+ * g, out  : [batch][rows][cols] device, `dtype`; element (i, r, c) at i * bs + r * ld + c
+ *           (bs >= 0, ld >= cols).  out may be g with the same strides, or must not overlap it.
+ * steps   : >= 0 (0: only the normalisation).
+ * Precision: every product accumulates in fp32 on operands of 17 bits (bf16 matrices) or
+ *           24 bits (fp32 matrices); the norm is summed in 64 bits.  Deterministic.
+ * workspace: >= ttt_orthogonalise_workspace_bytes(rows, cols, batch, dtype).
+ */
+int ttt_orthogonalise_workspace_bytes(int32_t rows, int32_t cols, int32_t batch, int32_t dtype, size_t *bytes);
+int ttt_orthogonalise(int32_t rows, int32_t cols, int32_t batch, const void *g, int64_t ld_g, int64_t bs_g,
+                      void *out, int64_t ld_out, int64_t bs_out, int32_t steps, int32_t dtype,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * Process-wide tuning / testing switches.
  *   TTT_OPT_FORCE_GENERAL: value != 0 routes every call through the general
@@ -315,7 +429,8 @@ int ttt_set_option(int32_t option, int64_t value);
  */
 typedef enum {
   TTT_K_CONV = 0, TTT_K_CAST = 1, TTT_K_GRAD = 2, TTT_K_REDUCE = 3,
-  TTT_K_NS = 4, TTT_K_APPLY = 5, TTT_K_GATE = 6, TTT_K_COUNT = 7
+  TTT_K_NS = 4, TTT_K_APPLY = 5, TTT_K_GATE = 6,
+  TTT_K_DELTA = 7, TTT_K_RESIDUAL = 8, TTT_K_ORTH = 9, TTT_K_COUNT = 10
 } ttt_kernel_kind;
 int ttt_profile_enable(int32_t on);
 int ttt_profile_reset(void);

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "ttt.h"
+#include "api_util.h"
 #include "kernels.h"
 
 using namespace ttt;
@@ -23,16 +24,6 @@ static __device__ __align__(256) unsigned char scratch[kNoAllocScratchBytes];
 namespace {
 
 thread_local std::string g_err;
-
-int fail(int status, const char *fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return status;
-}
 
 // ----------------------------------------------------------------- options
 int64_t g_force_general = 0;   // 1: use the general kernels even where a fast one exists
@@ -66,25 +57,57 @@ hipEvent_t take_event() {
 // recorded in it, whatever ttt_profile_enable says.
 thread_local bool t_no_events = false;
 
-template <class F>
-int run(int kind, const char *what, hipStream_t s, F &&f) {
-  hipEvent_t e0 = nullptr, e1 = nullptr;
-  const bool prof = g_prof && !t_no_events;
-  if (prof) {
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    e0 = take_event();
-    e1 = take_event();
-    if (e0) hipEventRecord(e0, s);
-  }
-  const hipError_t err = f();
-  if (prof && e0 && e1) {
-    hipEventRecord(e1, s);
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    g_pending.push_back({kind, e0, e1});
-  }
-  if (err != hipSuccess) return fail(TTT_EHIP, "%s: %s", what, hipGetErrorString(err));
+}  // namespace
+
+namespace ttt {
+
+int fail(int status, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return status;
+}
+
+Timing timing_begin(hipStream_t s) {
+  Timing t{};
+  if (!g_prof || t_no_events) return t;
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  t.e0 = take_event();
+  t.e1 = take_event();
+  if (t.e0) hipEventRecord(t.e0, s);
+  return t;
+}
+
+void timing_end(int kind, const Timing &t, hipStream_t s) {
+  if (!t.e0 || !t.e1) return;
+  hipEventRecord(t.e1, s);
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  g_pending.push_back({kind, t.e0, t.e1});
+}
+
+size_t esize(int dtype) { return dtype == TTT_BF16 ? 2 : 4; }
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+  return x < y + nb && y < x + na;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int check_ws(void *ws, size_t have, size_t need) {
+  if (need == 0) return TTT_OK;
+  if (!ws) return fail(TTT_EWORKSPACE, "workspace is null (need %zu bytes)", need);
+  if (((uintptr_t)ws) % 256 != 0) return fail(TTT_EINVAL, "workspace must be 256-byte aligned");
+  if (have < need) return fail(TTT_EWORKSPACE, "workspace has %zu bytes, needs %zu", have, need);
   return TTT_OK;
 }
+
+}  // namespace ttt
+
+namespace {
 
 // ----------------------------------------------------------------- checks
 // Every head width that is a multiple of the 64-wide tile, up to 1024.  d in {64, 128,
@@ -99,8 +122,6 @@ int check_shape(int heads, int d, int m, int dtype) {
   if (m < 64 || m % 64 != 0) return fail(TTT_EUNSUPPORTED, "m=%d must be a positive multiple of 64", m);
   return TTT_OK;
 }
-
-size_t esize(int dtype) { return dtype == TTT_BF16 ? 2 : 4; }
 
 int check_rows(const void *p, int64_t ld, int heads, int d, int dtype, const char *name) {
   if (!p) return fail(TTT_EINVAL, "%s is null", name);
@@ -120,13 +141,6 @@ int check_token_limits(int64_t n, int64_t ld, int dtype, const char *name) {
     return fail(TTT_EUNSUPPORTED, "row stride of %s too large (32 rows must span < 2 GiB)", name);
   return TTT_OK;
 }
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-  const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
-  return x < y + nb && y < x + na;
-}
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // ----------------------------------------------------------------- update plan
 struct UpdatePlan {
@@ -472,14 +486,6 @@ int do_apply(int H, int d, int m, W3 w, const void *q, int64_t ldq, void *o, int
     ap.w1 = w.w1, ap.w3 = w.w3, ap.w2 = w.w2;
   }
   return run(TTT_K_APPLY, "apply", s, [&] { return launch_apply(ap, d, bf16, fast, s); });
-}
-
-int check_ws(void *ws, size_t have, size_t need) {
-  if (need == 0) return TTT_OK;
-  if (!ws) return fail(TTT_EWORKSPACE, "workspace is null (need %zu bytes)", need);
-  if (((uintptr_t)ws) % 256 != 0) return fail(TTT_EINVAL, "workspace must be 256-byte aligned");
-  if (have < need) return fail(TTT_EWORKSPACE, "workspace has %zu bytes, needs %zu", have, need);
-  return TTT_OK;
 }
 
 int check_weights(const float *w1, const float *w3, const float *w2) {

@@ -1,0 +1,506 @@
+// Gated delta rule: the fast-weight layer f_W(x) = W x, one step of size beta_t per token on
+// 1/2 |W k_t - v_t|^2 after the decay a_t = e^(g_t):
+//   e_t = v_t - a_t W k_t,   W <- a_t W + beta_t e_t k_t^T,   o_t = scale W q_t.
+//
+// Chunked form (64 tokens; gamma_i = g_1 + .. + g_i inside the chunk, D_ij = e^(gamma_i - gamma_j)
+// for j <= i, W0 the state before the chunk):
+//   L_ij = beta_i D_ij k_i.k_j (j < i),  T = (I + L)^-1,  A_ij = scale D_ij q_i.k_j (j <= i)
+//   R = beta o (V - e^gamma o (K W0^T)),  U = T R
+//   O = scale e^gamma o (Q W0^T) + A U
+//   W = e^gamma_last W0 + (e^(gamma_last - gamma) o U)^T K
+// Three kernels: the packed sequences are laid out in chunks (plan), T and A of every chunk at
+// once (chunk), then the states in order of the chunks, split over heads and 16-column slices of
+// dv, which do not depend on one another (states).
+#include "delta.h"
+#include "split.h"
+
+namespace ttt {
+namespace {
+
+constexpr int C = kDeltaChunk;
+constexpr int SL = kDeltaSlice;
+
+// ------------------------------------------------------------------ plan
+// Row offsets -> sequences and chunks.  The running maximum of the clamped offsets makes any
+// offsets into disjoint ranges inside [0, n): nothing is read or written outside the rows.
+__global__ __launch_bounds__(256) void delta_plan_kernel(DeltaParams p) {
+  __shared__ int s_a[256], s_b[256];
+  const int t = threadIdx.x;
+  if (p.cu == nullptr) {
+    if (t == 0) {
+      p.seqs[0] = DeltaSeq{0, p.n, 0, 0};
+      *p.used = p.n;
+    }
+    for (int c = t; c < p.nchunk; c += 256) {
+      const int t0 = c * C;
+      p.chunks[c] = DeltaChunk{t0, p.n - t0 < C ? p.n - t0 : C, 0, 0};
+    }
+    return;
+  }
+  auto off = [&](int i) { const int x = p.cu[i]; return x < 0 ? 0 : (x > p.n ? p.n : x); };
+  int carry_max = off(0), carry_chunks = 0;
+  for (int b0 = 0; b0 < p.nseq; b0 += 256) {
+    const int b = b0 + t;
+    // inclusive running maximum of the end offsets
+    s_a[t] = b < p.nseq ? off(b + 1) : 0;
+    __syncthreads();
+    for (int d = 1; d < 256; d <<= 1) {
+      const int x = t >= d ? s_a[t - d] : 0;
+      __syncthreads();
+      s_a[t] = s_a[t] > x ? s_a[t] : x;
+      __syncthreads();
+    }
+    const int end = s_a[t] > carry_max ? s_a[t] : carry_max;
+    const int prev = t > 0 ? s_a[t - 1] : carry_max;
+    const int start = prev > carry_max ? prev : carry_max;
+    const int len = b < p.nseq ? end - start : 0;
+    const int nc = (len + C - 1) / C;
+    s_b[t] = nc;
+    __syncthreads();
+    for (int d = 1; d < 256; d <<= 1) {
+      const int x = t >= d ? s_b[t - d] : 0;
+      __syncthreads();
+      s_b[t] += x;
+      __syncthreads();
+    }
+    if (b < p.nseq) p.seqs[b] = DeltaSeq{start, len, carry_chunks + s_b[t] - nc, 0};
+    carry_max = s_a[255] > carry_max ? s_a[255] : carry_max;
+    carry_chunks += s_b[255];
+    __syncthreads();
+  }
+  if (t == 0) *p.used = carry_max;
+  __threadfence_block();
+  __syncthreads();
+  for (int c = t; c < p.nchunk; c += 256) {
+    if (c >= carry_chunks) {
+      p.chunks[c] = DeltaChunk{0, 0, 0, 0};
+      continue;
+    }
+    int lo = 0, hi = p.nseq - 1;      // the last sequence whose chunk0 <= c (empty ones share it with their successor)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.seqs[mid].chunk0 <= c) lo = mid; else hi = mid - 1;
+    }
+    const DeltaSeq sq = p.seqs[lo];
+    const int r = (c - sq.chunk0) * C;
+    p.chunks[c] = DeltaChunk{sq.start + r, sq.len - r < C ? sq.len - r : C, lo, 0};
+  }
+}
+
+// Zeros in the rows behind the last sequence (and before the first).
+template <typename T>
+__global__ __launch_bounds__(256) void delta_zero_rows_kernel(DeltaParams p, T *rows, int64_t ld, int width) {
+  const int first = p.nseq > 0 ? p.seqs[0].start : 0, used = *p.used;
+  const int total = first + (p.n - used);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)total * width; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / width, row = r < first ? r : used + (r - first);
+    rows[row * ld + i % width] = from_f32<T>(0.0f);
+  }
+}
+
+// ------------------------------------------------------------------ chunk terms
+// One workgroup per chunk and head: e^gamma, T = (I + L)^-1 by block substitution in fp32 and A,
+// and (once per key head) the transposed tokens that the later kernels read as matrix operands.
+// Substitution, not products of powers of L: those grow without bound where keys repeat.
+template <typename T, int DK, bool BWD>
+__global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
+  __shared__ double s_gam[C];
+  __shared__ float s_beta[C];
+  __shared__ float s_l[C][C + 1], s_t[C][C + 1], s_x[32][33];
+  const int h = blockIdx.x % p.heads, c = blockIdx.x / p.heads;
+  const DeltaChunk ck = p.chunks[c];
+  if (ck.len == 0) return;
+  const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
+  const int kh = h / (p.heads / p.key_heads);
+  const int64_t ch = (int64_t)c * p.heads + h;
+  const T *K = static_cast<const T *>(p.k) + (int64_t)ck.tok0 * p.ldk + kh * DK;
+  const T *Q = static_cast<const T *>(p.q) + (int64_t)ck.tok0 * p.ldq + kh * DK;
+  if (t < C) {
+    const bool ok = t < ck.len;
+    double gam = 0.0;
+    if (ok && p.decay) {
+      const float x = p.decay[h * p.decay_hs + ck.tok0 + t];
+      gam = x < -200.0f ? -200.0 : (double)x;      // e^-200 is 0 in fp32; -inf would leave inf - inf
+    }
+    for (int d = 1; d < C; d <<= 1) {
+      const double x = __shfl_up(gam, d);
+      if (t >= d) gam += x;
+    }
+    s_gam[t] = gam;
+    s_beta[t] = ok ? p.beta[h * p.beta_hs + ck.tok0 + t] : 0.0f;
+    if (BWD) p.gam[ch * C + t] = gam;
+    p.eg[ch * C + t] = exp_of(gam);
+    p.el[ch * C + t] = exp_of(__shfl(gam, 63) - gam);
+  }
+  __syncthreads();
+  // K K^T and Q K^T: wave w has rows 16w .. 16w+15, four column tiles
+  f32x4 kk[4], qk[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) kk[j] = qk[j] = zero4();
+  const int last = ck.len - 1;
+  const int ra = 16 * w + li < last ? 16 * w + li : last;     // rows past the chunk repeat its last one, and are masked below
+#pragma unroll 2
+  for (int ks = 0; ks < DK; ks += 32) {
+    const auto ka = ld8(K + (int64_t)ra * p.ldk + ks + 8 * g);
+    const auto qa = ld8(Q + (int64_t)ra * p.ldq + ks + 8 * g);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > w) continue;                                    // above the diagonal
+      const int rb = 16 * j + li < last ? 16 * j + li : last;
+      const auto kb = ld8(K + (int64_t)rb * p.ldk + ks + 8 * g);
+      kk[j] = mm(ka, kb, kk[j]);
+      qk[j] = mm(qa, kb, qk[j]);
+    }
+  }
+  const int64_t mat = ch * (C * C * 4), plane = C * C * 2;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int col = 16 * j + li;
+    f32x4 a;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * w + 4 * g + r;
+      const float d = exp_of(row >= col ? s_gam[row] - s_gam[col] : 0.0);
+      const bool in = row < ck.len && col <= row;
+      s_l[row][col] = in && col < row ? s_beta[row] * d * kk[j][r] : 0.0f;
+      a[r] = in ? p.scale * d * qk[j][r] : 0.0f;
+      if (!BWD) Sp<T>::st1(p.am + mat, plane, row * C + col, a[r]);
+    }
+    if (BWD) Sp<T>::st4(p.am + mat, plane, col * C + 16 * w + 4 * g, a);   // A^T
+  }
+  __syncthreads();
+  // T = (I + L)^-1.  Diagonal 16 x 16 blocks: wave w has block w, one column a lane.
+  if (li == l) {
+    float x[16];
+    const int o = 16 * w;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = i == li ? 1.0f : 0.0f;
+#pragma unroll
+      for (int m = 0; m < i; ++m) v -= s_l[o + i][o + m] * x[m];
+      x[i] = v;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s_t[o + i][o + li] = x[i];
+  }
+  for (int e = t; e < 16 * 48; e += 256) {      // zero above the diagonal blocks
+    const int r = e / 48, x = e % 48;
+    s_t[r][16 + x] = 0.0f;
+    if (x < 32) s_t[16 + r][32 + x] = 0.0f;
+    if (x < 16) s_t[32 + r][48 + x] = 0.0f;
+  }
+  __syncthreads();
+  // below-diagonal blocks: T21 = -T22 (L21 T11), first 16-wide (two pairs), then 32-wide
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int o = 32 * q, r = t >> 4, x = t & 15;
+    float v = 0.0f;
+#pragma unroll
+    for (int m = 0; m < 16; ++m) v += s_l[o + 16 + r][o + m] * s_t[o + m][o + x];
+    s_x[16 * q + r][x] = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int o = 32 * q, r = t >> 4, x = t & 15;
+    float v = 0.0f;
+#pragma unroll
+    for (int m = 0; m < 16; ++m) v += s_t[o + 16 + r][o + 16 + m] * s_x[16 * q + m][x];
+    s_t[o + 16 + r][o + x] = -v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int e = t + 256 * q, r = e >> 5, x = e & 31;
+    float v = 0.0f;
+#pragma unroll
+    for (int m = 0; m < 32; ++m) v += s_l[32 + r][m] * s_t[m][x];
+    s_x[r][x] = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int e = t + 256 * q, r = e >> 5, x = e & 31;
+    float v = 0.0f;
+#pragma unroll
+    for (int m = 0; m < 32; ++m) v += s_t[32 + r][32 + m] * s_x[m][x];
+    s_t[32 + r][x] = -v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int e = (t + 256 * q) * 4, r = e >> 6, x = e & 63;
+    Sp<T>::st4(p.tm + mat, plane, e, f32x4{s_t[r][x], s_t[r][x + 1], s_t[r][x + 2], s_t[r][x + 3]});
+    if (BWD) Sp<T>::st4(p.tt + mat, plane, e, f32x4{s_t[x][r], s_t[x + 1][r], s_t[x + 2][r], s_t[x + 3][r]});
+  }
+  // transposed tokens [dk][64], rows past the chunk zero: the first head of each key head writes them
+  if (h % (p.heads / p.key_heads) == 0) {
+    const int64_t o = ((int64_t)c * p.key_heads + kh) * DK * C;
+    T *kt = static_cast<T *>(p.kt) + o, *qt = BWD ? static_cast<T *>(p.qt) + o : nullptr;
+    for (int e = t; e < DK * C / 4; e += 256) {
+      const int col = e % DK, r0 = e / DK * 4;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool ok = r0 + r < ck.len;
+        kt[col * C + r0 + r] = ok ? K[(int64_t)(r0 + r) * p.ldk + col] : from_f32<T>(0.0f);
+        if (BWD) qt[col * C + r0 + r] = ok ? Q[(int64_t)(r0 + r) * p.ldq + col] : from_f32<T>(0.0f);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ states
+// One workgroup per sequence, head and 16-column slice of dv, over the chunks in order.  The
+// slice of W stays in fp32 accumulators: lane (g, li) of wave w holds W[dv = li][dk = w DK/4 +
+// 16 i + 4 g + r].  Between the products only R, U and the state pass through LDS; tokens and
+// chunk terms go from memory straight into operand registers (each is used once).
+// BWD writes the states and U that the gradient needs, in place of the outputs.
+template <typename T, int DK, bool BWD>
+__global__ __launch_bounds__(256, 1) void delta_state_kernel(DeltaParams p) {
+  __shared__ __attribute__((aligned(16))) SpTile<T, SL, DK> s_w;
+  __shared__ __attribute__((aligned(16))) SpTile<T, SL, C> s_r, s_u, s_ul;
+  constexpr int NT = DK / 64;
+  const int slices = p.dv / SL;
+  const int sl = blockIdx.x % slices, h = blockIdx.x / slices % p.heads, b = blockIdx.x / slices / p.heads;
+  const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
+  const int kh = h / (p.heads / p.key_heads);
+  const DeltaSeq sq = p.seqs[b];
+  const int64_t wrow = (((int64_t)b * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
+  f32x4 st[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    st[i] = *reinterpret_cast<const f32x4 *>(p.w + wrow + 16 * i);
+    s_w.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
+  }
+  __syncthreads();
+  const int64_t plane = C * C * 2;
+  for (int c0 = 0; c0 < sq.len; c0 += C) {
+    const int len = sq.len - c0 < C ? sq.len - c0 : C;
+    const int64_t c = sq.chunk0 + c0 / C, ch = c * p.heads + h;
+    const int64_t tok0 = sq.start + c0;
+    const int row = 16 * w + li < len ? 16 * w + li : len - 1;
+    const T *K = static_cast<const T *>(p.k) + (tok0 + row) * p.ldk + kh * DK + 8 * g;
+    const T *Q = static_cast<const T *>(p.q) + (tok0 + row) * p.ldq + kh * DK + 8 * g;
+    f32x4 pa = zero4(), qa = zero4();
+#pragma unroll
+    for (int ks = 0; ks < DK; ks += 32) {
+      const auto wf = s_w.ld(li, ks + 8 * g);
+      pa = mm(ld8(K + ks), wf, pa);
+      if (!BWD) qa = mm(ld8(Q + ks), wf, qa);
+    }
+    if (BWD) {      // the state before the chunk, [dk][dv]
+      char *o = p.w0t + ch * ((int64_t)DK * p.dv * 4);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          Sp<T>::st1(o, (int64_t)DK * p.dv * 2, (int64_t)(w * (DK / 4) + 16 * i + 4 * g + r) * p.dv + sl * SL + li,
+                     st[i][r]);
+    }
+    const int t4 = 16 * w + 4 * g;      // this lane's four rows of every 64 x 16 product
+    const f32x4 eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + t4);
+    const f32x4 el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + t4);
+    f32x4 rr;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool ok = t4 + r < len;
+      const int64_t tk = tok0 + (ok ? t4 + r : len - 1);
+      const float v = to_f32(static_cast<const T *>(p.v)[tk * p.ldv + h * p.dv + sl * SL + li]);
+      rr[r] = ok ? p.beta[h * p.beta_hs + tk] * (v - eg[r] * pa[r]) : 0.0f;
+    }
+    s_r.st4(li, t4, rr);
+    __syncthreads();
+    f32x4 u = zero4();
+    const char *tm = p.tm + ch * (C * C * 4);
+#pragma unroll
+    for (int ks = 0; ks < C; ks += 32)
+      if (ks <= 16 * w) u = mm(Sp<T>::ld(tm, plane, (16 * w + li) * C + ks + 8 * g), s_r.ld(li, ks + 8 * g), u);
+    s_ul.st4(li, t4, u * el);
+    if (!BWD) {
+      s_u.st4(li, t4, u);
+    } else {
+      char *o = p.u + ch * ((int64_t)C * p.dv * 4);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) Sp<T>::st1(o, (int64_t)C * p.dv * 2, (int64_t)(t4 + r) * p.dv + sl * SL + li, u[r]);
+    }
+    __syncthreads();
+    if (!BWD) {
+      f32x4 o = qa * eg * p.scale;
+      const char *am = p.am + ch * (C * C * 4);
+#pragma unroll
+      for (int ks = 0; ks < C; ks += 32)
+        if (ks <= 16 * w) o = mm(Sp<T>::ld(am, plane, (16 * w + li) * C + ks + 8 * g), s_u.ld(li, ks + 8 * g), o);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (t4 + r < len)
+          static_cast<T *>(p.o)[(tok0 + t4 + r) * p.ldo + h * p.dv + sl * SL + li] = from_f32<T>(o[r]);
+    }
+    const float ec = p.eg[ch * C + C - 1];
+    const T *kt = static_cast<const T *>(p.kt) + (c * p.key_heads + kh) * (DK * C) + (w * (DK / 4) + li) * C + 8 * g;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      st[i] = st[i] * ec;
+#pragma unroll
+      for (int ks = 0; ks < C; ks += 32) st[i] = mm(ld8(kt + 16 * i * C + ks), s_ul.ld(li, ks + 8 * g), st[i]);
+      s_w.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
+    }
+    __syncthreads();
+  }
+  if (!BWD)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(p.w_out + wrow + 16 * i) = st[i];
+}
+
+// ------------------------------------------------------------------ one token
+// The recurrent form for one token of each row's sequence: one read and one write of the state.
+//   o = scale (a W q + beta e (k.q)),  W <- a W + beta e k^T,  e = v - a W k
+// 16 lanes hold one dv row of W; rows that name the same state are applied in row order by the
+// workgroups of the first of them.
+template <typename T, int DK>
+__global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
+  constexpr int V4 = DK / 64;           // float4 a lane and dv row
+  constexpr int NR = 4;                 // dv rows of a 16-lane group
+  __shared__ int s_hit;
+  const int t = threadIdx.x, li = t & 15, grp = t >> 4;
+  const int blocks = p.dv / 64;
+  const int db = blockIdx.x % blocks, h = blockIdx.x / blocks % p.heads, row0 = blockIdx.x / blocks / p.heads;
+  const int kh = h / (p.heads / p.key_heads);
+  const int slot = p.slots ? p.slots[row0] : row0;
+  const bool valid = slot >= 0 && slot < p.nslots;
+  if (!valid) {
+    if (p.zero_unused && t < 64) static_cast<T *>(p.o)[(int64_t)row0 * p.ldo + h * p.dv + db * 64 + t] = from_f32<T>(0.0f);
+    return;
+  }
+  int rows_left = 0;
+  if (p.slots) {
+    if (t == 0) s_hit = 0;
+    __syncthreads();
+    int hit = 0;
+    for (int i = t; i < p.n; i += 256)
+      if (p.slots[i] == slot && i != row0) hit |= i < row0 ? 1 : 2;
+    if (hit) atomicOr(&s_hit, hit);
+    __syncthreads();
+    if (s_hit & 1) return;              // an earlier row's workgroups apply this one too
+    rows_left = s_hit;
+  }
+  f32x4 st[NR][V4];
+  float *W = p.w + (((int64_t)slot * p.heads + h) * p.dv + db * 64 + grp * NR) * DK + li * 4;
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int j = 0; j < V4; ++j) st[i][j] = *reinterpret_cast<const f32x4 *>(W + i * DK + j * 64);
+  for (int row = row0;;) {
+    const T *K = static_cast<const T *>(p.k) + (int64_t)row * p.ldk + kh * DK + li * 4;
+    const T *Q = static_cast<const T *>(p.q) + (int64_t)row * p.ldq + kh * DK + li * 4;
+    const float a = p.decay ? __builtin_amdgcn_exp2f(p.decay[h * p.decay_hs + row] * 1.4426950408889634f) : 1.0f;
+    const float be = p.beta[h * p.beta_hs + row];
+    f32x4 kf[V4], qf[V4];
+    float kq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        kf[j][e] = to_f32(K[j * 64 + e]);
+        qf[j][e] = to_f32(Q[j * 64 + e]);
+        kq += kf[j][e] * qf[j][e];
+      }
+    float wk[NR], wq[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      wk[i] = wq[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          wk[i] += st[i][j][e] * kf[j][e];
+          wq[i] += st[i][j][e] * qf[j][e];
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+      kq += __shfl_xor(kq, m);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        wk[i] += __shfl_xor(wk[i], m);
+        wq[i] += __shfl_xor(wq[i], m);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int d = h * p.dv + db * 64 + grp * NR + i;
+      const float v = to_f32(static_cast<const T *>(p.v)[(int64_t)row * p.ldv + d]);
+      const float be_e = be * (v - a * wk[i]);
+      if (li == i) static_cast<T *>(p.o)[(int64_t)row * p.ldo + d] = from_f32<T>(p.scale * (a * wq[i] + be_e * kq));
+#pragma unroll
+      for (int j = 0; j < V4; ++j) st[i][j] = st[i][j] * a + kf[j] * be_e;
+    }
+    if (!rows_left) break;
+    do ++row; while (row < p.n && p.slots[row] != slot);
+    if (row >= p.n) break;
+  }
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int j = 0; j < V4; ++j) *reinterpret_cast<f32x4 *>(W + i * DK + j * 64) = st[i][j];
+}
+
+template <typename T, int DK>
+hipError_t step_impl(const DeltaStepParams &p, hipStream_t s) {
+  hipLaunchKernelGGL((delta_step_kernel<T, DK>), dim3((unsigned)((int64_t)p.n * p.heads * (p.dv / 64))), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, int DK>
+hipError_t chunk_impl(const DeltaParams &p, bool backward, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.nchunk * p.heads));
+  if (backward)
+    hipLaunchKernelGGL((delta_chunk_kernel<T, DK, true>), grid, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((delta_chunk_kernel<T, DK, false>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, int DK>
+hipError_t states_impl(const DeltaParams &p, bool backward, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.nseq * p.heads * (p.dv / SL)));
+  if (backward)
+    hipLaunchKernelGGL((delta_state_kernel<T, DK, true>), grid, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((delta_state_kernel<T, DK, false>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_plan(const DeltaParams &p, hipStream_t s) {
+  hipLaunchKernelGGL(delta_plan_kernel, dim3(1), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+hipError_t launch_delta_chunk(const DeltaParams &p, bool bf16, bool backward, hipStream_t s) {
+  if (p.nchunk == 0) return hipSuccess;
+  return TTT_DELTA_BY_DK(chunk_impl, p, p, backward, s);
+}
+hipError_t launch_delta_states(const DeltaParams &p, bool bf16, bool backward, hipStream_t s) {
+  return TTT_DELTA_BY_DK(states_impl, p, p, backward, s);
+}
+hipError_t launch_delta_zero_rows(const DeltaParams &p, void *rows, int64_t ld, int width, bool bf16, hipStream_t s) {
+  if (p.cu == nullptr || p.n == 0) return hipSuccess;      // one sequence covers every row
+  if (bf16)
+    hipLaunchKernelGGL(delta_zero_rows_kernel<__bf16>, dim3(256), dim3(256), 0, s, p, static_cast<__bf16 *>(rows), ld, width);
+  else
+    hipLaunchKernelGGL(delta_zero_rows_kernel<float>, dim3(256), dim3(256), 0, s, p, static_cast<float *>(rows), ld, width);
+  return hipGetLastError();
+}
+hipError_t launch_delta_forward(const DeltaParams &p, bool bf16, hipStream_t s) {
+  hipError_t e = launch_delta_plan(p, s);
+  if (e == hipSuccess) e = launch_delta_chunk(p, bf16, false, s);
+  if (e == hipSuccess) e = launch_delta_states(p, bf16, false, s);
+  if (e == hipSuccess && p.zero_unused) e = launch_delta_zero_rows(p, p.o, p.ldo, p.heads * p.dv, bf16, s);
+  return e;
+}
+hipError_t launch_delta_step(const DeltaStepParams &p, bool bf16, hipStream_t s) {
+  if (p.n == 0) return hipSuccess;
+  return TTT_DELTA_BY_DK(step_impl, p, p, s);
+}
+
+}  // namespace ttt

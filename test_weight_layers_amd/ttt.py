@@ -19,12 +19,16 @@ LIB_PATH = os.path.join(_HERE, "libttt.so")
 
 TTT_F32, TTT_BF16 = 0, 1
 OPT_FORCE_GENERAL, OPT_SPLITS, OPT_NS_UNFUSED = 0, 1, 2
-KERNEL_KINDS = ("conv", "cast", "grad", "reduce", "ns", "apply", "gate")
+KERNEL_KINDS = ("conv", "cast", "grad", "reduce", "ns", "apply", "gate", "delta", "residual", "orthogonalise")
 NORM_PRESERVE = 1
+DELTA_ZERO_UNUSED = 1
 EXPORTS = ("ttt_last_error", "ttt_update_workspace_bytes", "ttt_apply_workspace_bytes", "ttt_update",
            "ttt_update_ex", "ttt_update_host_workspace_bytes", "ttt_update_host", "ttt_apply", "ttt_output_gate", "ttt_shortconv2d", "ttt_stream_workspace_bytes",
            "ttt_stream", "ttt_stream_ex", "ttt_set_option", "ttt_profile_enable", "ttt_profile_reset",
-           "ttt_profile_read", "ttt_update_noalloc", "ttt_noalloc_scratch_bytes", "ttt_mfma_rate_probe")
+           "ttt_profile_read", "ttt_update_noalloc", "ttt_noalloc_scratch_bytes", "ttt_mfma_rate_probe",
+           "ttt_delta_workspace_bytes", "ttt_delta", "ttt_delta_backward", "ttt_delta_step", "ttt_gated_residual",
+           "ttt_gated_residual_backward_workspace_bytes", "ttt_gated_residual_backward",
+           "ttt_orthogonalise_workspace_bytes", "ttt_orthogonalise")
 
 _lib = None
 
@@ -69,6 +73,22 @@ def load() -> ctypes.CDLL:
         "ttt_profile_enable": (ctypes.c_int, [i32]),
         "ttt_profile_reset": (ctypes.c_int, []),
         "ttt_profile_read": (ctypes.c_int, [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)]),
+        "ttt_delta_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i32, i64, i32, i32, i32, szp]),
+        "ttt_delta": (ctypes.c_int, [i32, i32, i32, i32, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                     i64, vp, i32, f32, i32, u32, vp, sz, vp]),
+        "ttt_delta_backward": (ctypes.c_int, [i32, i32, i32, i32, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+                                              i64, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i32, f32, i32,
+                                              vp, sz, vp]),
+        "ttt_delta_step": (ctypes.c_int, [i32, i32, i32, i32, vp, i32, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                          vp, i64, i64, f32, i32, u32, vp]),
+        "ttt_gated_residual": (ctypes.c_int, [i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, f32, vp, i64, vp, i64,
+                                              i64, i32, vp]),
+        "ttt_gated_residual_backward_workspace_bytes": (ctypes.c_int, [i32, i64, szp]),
+        "ttt_gated_residual_backward": (ctypes.c_int, [i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp,
+                                                       vp, f32, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, i32, vp,
+                                                       sz, vp]),
+        "ttt_orthogonalise_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i32, szp]),
+        "ttt_orthogonalise": (ctypes.c_int, [i32, i32, i32, vp, i64, i64, vp, i64, i64, i32, i32, vp, sz, vp]),
         "ttt_mfma_rate_probe": (ctypes.c_int, [i32, vp, ctypes.POINTER(ctypes.c_double)]),
     }
     for name, (res, args) in sig.items():
@@ -376,6 +396,265 @@ def output_gate(o: torch.Tensor, wg: torch.Tensor, gamma: torch.Tensor, eps: flo
     ldo = _same_rows(out, o, o.shape[0], C, "out")
     _check(load().ttt_output_gate(C, o.data_ptr(), ldi, wg.data_ptr(), gamma.data_ptr(), float(eps), out.data_ptr(),
                                   ldo, o.shape[0], code, _stream()))
+    return out
+
+
+# ------------------------------------------------------------------ gated delta rule
+def _here(like: torch.Tensor, **tensors) -> None:
+    """`like` and every given tensor live on the current GPU (the library launches on its current stream)."""
+    if not like.is_cuda or like.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current GPU, got {like.device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+
+
+def _states(w: torch.Tensor, name: str) -> None:
+    if w.dtype != torch.float32 or w.dim() != 4 or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor [sequences, heads, dv, dk]")
+
+
+def _delta_args(w, q, k, v, beta, decay, key_heads, scale):
+    """Checks shared by the delta-rule calls: (S, H, Hk, dv, dk, n, row strides, rate strides, scale, dtype code)."""
+    _states(w, "w")
+    S, H, dv, dk = w.shape
+    Hk = H if key_heads is None else int(key_heads)
+    _here(w, q=q, k=k, v=v, beta=beta, decay=decay)
+    code = _dtype_code(q)
+    if q.dim() != 2:
+        raise ValueError("q must be a 2-D tensor of token rows")
+    n = q.shape[0]
+    lds = (_same_rows(q, q, n, Hk * dk, "q"), _same_rows(k, q, n, Hk * dk, "k"), _same_rows(v, q, n, H * dv, "v"))
+    bhs = _eta_stride(beta, H, n, w.device)
+    dhs = 0 if decay is None else _eta_stride(decay, H, n, w.device)
+    return S, H, Hk, dv, dk, n, lds, bhs, dhs, (1.0 if scale is None else float(scale)), code
+
+
+def _offsets(cu, sequences: int, device) -> None:
+    if cu is None:
+        if sequences != 1:
+            raise ValueError(f"w holds {sequences} states: cu_seqlens is needed for more than one sequence")
+        return
+    if cu.dtype != torch.int32 or tuple(cu.shape) != (sequences + 1,) or not cu.is_contiguous() or cu.device != device:
+        raise ValueError(f"cu_seqlens must be a contiguous int32 tensor [{sequences + 1}] on {device}")
+
+
+def delta_workspace_bytes(heads: int, key_heads: int, dk: int, dv: int, n: int, sequences: int, dtype: torch.dtype,
+                          backward: bool = False) -> int:
+    out = ctypes.c_size_t()
+    code = TTT_BF16 if dtype == torch.bfloat16 else TTT_F32
+    _check(load().ttt_delta_workspace_bytes(heads, key_heads, dk, dv, n, sequences, code, int(backward),
+                                            ctypes.byref(out)))
+    return out.value
+
+
+def delta(w: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
+          decay: Optional[torch.Tensor] = None, *, key_heads: Optional[int] = None,
+          cu_seqlens: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+          out: Optional[torch.Tensor] = None, w_out: Optional[torch.Tensor] = None,
+          workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Gated delta rule over packed sequences; returns (o, final states).
+
+    w [sequences, H, dv, dk] float32 starting states; q, k rows of key_heads * dk, v rows of H * dv columns;
+    beta and decay (log decay, None: no decay) [H, >=n] or shared [>=n].  ``w_out`` may be ``w`` (in place).
+    Rows outside the sequences stay as they are in a given ``out`` and are zero in a new one.
+    """
+    S, H, Hk, dv, dk, n, lds, bhs, dhs, scale, code = _delta_args(w, q, k, v, beta, decay, key_heads, scale)
+    _offsets(cu_seqlens, S, w.device)
+    flags = 0
+    if out is None:
+        out = torch.empty((n, H * dv), dtype=q.dtype, device=q.device)
+        flags = DELTA_ZERO_UNUSED
+    ldo = _same_rows(out, q, n, H * dv, "out")
+    if w_out is None:
+        w_out = torch.empty_like(w)
+    _states(w_out, "w_out")
+    if w_out.shape != w.shape or w_out.device != w.device:
+        raise ValueError("w_out must have w's shape and device")
+    if workspace is None:
+        workspace = _workspace(delta_workspace_bytes(H, Hk, dk, dv, n, S, q.dtype), w.device)
+    _here(w, workspace=workspace)
+    _check(load().ttt_delta(H, Hk, dk, dv, w.data_ptr(), w_out.data_ptr(), q.data_ptr(), lds[0], k.data_ptr(), lds[1],
+                            v.data_ptr(), lds[2], beta.data_ptr(), bhs, _ptr(decay), dhs, out.data_ptr(), ldo, n,
+                            _ptr(cu_seqlens), S, scale, code, flags, workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), _stream()))
+    return out, w_out
+
+
+def delta_backward(w: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
+                   decay: Optional[torch.Tensor], grad_o: torch.Tensor, grad_w_out: Optional[torch.Tensor] = None, *,
+                   key_heads: Optional[int] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                   scale: Optional[float] = None, out: Optional[Sequence[torch.Tensor]] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``delta``: (grad_q, grad_k, grad_v, grad_beta, grad_decay, grad_w).
+
+    ``out`` gives (grad_q, grad_k, grad_v) rows to write to (slices of one buffer, say).  grad_beta and
+    grad_decay are [H, n], or [n] for shared rates; grad_decay is None without decay.
+    """
+    S, H, Hk, dv, dk, n, lds, bhs, dhs, scale, code = _delta_args(w, q, k, v, beta, decay, key_heads, scale)
+    _offsets(cu_seqlens, S, w.device)
+    ldgo = _same_rows(grad_o, q, n, H * dv, "grad_o")
+    if grad_w_out is not None:
+        _states(grad_w_out, "grad_w_out")
+        if grad_w_out.shape != w.shape or grad_w_out.device != w.device:
+            raise ValueError("grad_w_out must have w's shape and device")
+    if out is None:
+        out = tuple(torch.empty((n, x), dtype=q.dtype, device=q.device) for x in (Hk * dk, Hk * dk, H * dv))
+    gq, gk, gv = out
+    ldg = (_same_rows(gq, q, n, Hk * dk, "grad_q"), _same_rows(gk, q, n, Hk * dk, "grad_k"),
+           _same_rows(gv, q, n, H * dv, "grad_v"))
+    rate = lambda t: torch.empty((H, n) if t.dim() == 2 else (n,), dtype=torch.float32, device=w.device)
+    gb = rate(beta)
+    gd = None if decay is None else rate(decay)
+    # a 2-D rate broadcast over heads (stride 0) still gets a gradient for each head
+    bhs, dhs = (-1 if t is not None and t.dim() == 2 and s == 0 else s for t, s in ((beta, bhs), (decay, dhs)))
+    if bhs < 0:
+        beta, bhs = beta[:, :n].contiguous(), n
+    if dhs < 0:
+        decay, dhs = decay[:, :n].contiguous(), n
+    gw = torch.empty_like(w)
+    if workspace is None:
+        workspace = _workspace(delta_workspace_bytes(H, Hk, dk, dv, n, S, q.dtype, True), w.device)
+    _here(w, workspace=workspace)
+    _check(load().ttt_delta_backward(H, Hk, dk, dv, w.data_ptr(), q.data_ptr(), lds[0], k.data_ptr(), lds[1],
+                                     v.data_ptr(), lds[2], beta.data_ptr(), bhs, _ptr(decay), dhs, grad_o.data_ptr(),
+                                     ldgo, _ptr(grad_w_out), gq.data_ptr(), ldg[0], gk.data_ptr(), ldg[1],
+                                     gv.data_ptr(), ldg[2], gb.data_ptr(), _ptr(gd), gw.data_ptr(), n,
+                                     _ptr(cu_seqlens), S, scale, code, workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream()))
+    return gq, gk, gv, gb, gd, gw
+
+
+def delta_step(w: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
+               decay: Optional[torch.Tensor] = None, *, slots: Optional[torch.Tensor] = None,
+               key_heads: Optional[int] = None, scale: Optional[float] = None,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token for each row, its state in the pool ``w`` [pool, H, dv, dk] updated in place; returns o.
+
+    Row i uses state ``slots[i]`` (int32; None: state i).  Slots outside the pool are padding: such rows
+    stay as they are in a given ``out`` and are zero in a new one.  Rows of one state apply in row order.
+    """
+    S, H, Hk, dv, dk, n, lds, bhs, dhs, scale, code = _delta_args(w, q, k, v, beta, decay, key_heads, scale)
+    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (n,) or not slots.is_contiguous()
+                              or slots.device != w.device):
+        raise ValueError(f"slots must be a contiguous int32 tensor [{n}] on {w.device}")
+    flags = 0
+    if out is None:
+        out = torch.empty((n, H * dv), dtype=q.dtype, device=q.device)
+        flags = DELTA_ZERO_UNUSED
+    ldo = _same_rows(out, q, n, H * dv, "out")
+    _check(load().ttt_delta_step(H, Hk, dk, dv, w.data_ptr(), S, _ptr(slots), q.data_ptr(), lds[0], k.data_ptr(),
+                                 lds[1], v.data_ptr(), lds[2], beta.data_ptr(), bhs, _ptr(decay), dhs, out.data_ptr(),
+                                 ldo, n, scale, code, flags, _stream()))
+    return out
+
+
+# ------------------------------------------------------------------ gated residual tail
+def _channel(t: Optional[torch.Tensor], C: int, name: str) -> None:
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (C,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 [{C}] tensor")
+
+
+def gated_residual(x: torch.Tensor, o: torch.Tensor, z: Optional[torch.Tensor] = None,
+                   gamma: Optional[torch.Tensor] = None, alpha: Optional[torch.Tensor] = None,
+                   gamma_next: Optional[torch.Tensor] = None, eps: float = 1e-6, *, norm_width: Optional[int] = None,
+                   out: Optional[torch.Tensor] = None, h_out: Optional[torch.Tensor] = None):
+    """y = x + alpha * RMSNorm(o; gamma) * SiLU(z), h = RMSNorm(y; gamma_next); returns (y, h).
+
+    The first norm runs over groups of ``norm_width`` channels (default: the row).  z None: no gate;
+    gamma or alpha None: 1; gamma_next None: h is None.  ``out`` may be ``x`` (in place).
+    """
+    code = _dtype_code(x)
+    _here(x, o=o, z=z, gamma=gamma, alpha=alpha, gamma_next=gamma_next, out=out, h_out=h_out)
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor of rows")
+    n, C = x.shape
+    ldx, ldo = _same_rows(x, x, n, C, "x"), _same_rows(o, x, n, C, "o")
+    ldz = 0 if z is None else _same_rows(z, x, n, C, "z")
+    for t, name in ((gamma, "gamma"), (alpha, "alpha"), (gamma_next, "gamma_next")):
+        _channel(t, C, name)
+    if out is None:
+        out = torch.empty((n, C), dtype=x.dtype, device=x.device)
+    ldy = _same_rows(out, x, n, C, "out")
+    if gamma_next is None and h_out is not None:
+        raise ValueError("h_out needs gamma_next")
+    if gamma_next is not None and h_out is None:
+        h_out = torch.empty((n, C), dtype=x.dtype, device=x.device)
+    ldh = 0 if h_out is None else _same_rows(h_out, x, n, C, "h_out")
+    _check(load().ttt_gated_residual(C, C if norm_width is None else int(norm_width), x.data_ptr(), ldx, o.data_ptr(),
+                                     ldo, _ptr(z), ldz, _ptr(gamma), _ptr(alpha), _ptr(gamma_next), float(eps),
+                                     out.data_ptr(), ldy, _ptr(h_out), ldh, n, code, _stream()))
+    return out, h_out
+
+
+def gated_residual_backward_workspace_bytes(channels: int, n: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().ttt_gated_residual_backward_workspace_bytes(channels, n, ctypes.byref(out)))
+    return out.value
+
+
+def gated_residual_backward(grad_y: Optional[torch.Tensor], grad_h: Optional[torch.Tensor], y: torch.Tensor,
+                            o: torch.Tensor, z: Optional[torch.Tensor] = None, gamma: Optional[torch.Tensor] = None,
+                            alpha: Optional[torch.Tensor] = None, gamma_next: Optional[torch.Tensor] = None,
+                            eps: float = 1e-6, *, norm_width: Optional[int] = None,
+                            workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``gated_residual``: (grad_x, grad_o, grad_z, grad_gamma, grad_alpha, grad_gamma_next).
+
+    ``y`` is the forward's output.  grad_y or grad_h None: zero.  The gradients of what was not given
+    are None.
+    """
+    code = _dtype_code(y)
+    _here(y, grad_y=grad_y, grad_h=grad_h, o=o, z=z, gamma=gamma, alpha=alpha, gamma_next=gamma_next,
+          workspace=workspace)
+    if y.dim() != 2:
+        raise ValueError("y must be a 2-D tensor of rows")
+    n, C = y.shape
+    ld = lambda t, name: 0 if t is None else _same_rows(t, y, n, C, name)
+    new = lambda like: None if like is None else torch.empty((n, C), dtype=y.dtype, device=y.device)
+    for t, name in ((gamma, "gamma"), (alpha, "alpha"), (gamma_next, "gamma_next")):
+        _channel(t, C, name)
+    gx, go, gz = new(y), new(o), new(z)
+    row = lambda like: None if like is None else torch.empty(C, dtype=torch.float32, device=y.device)
+    gg, ga, gn = row(gamma), row(alpha), row(gamma_next)
+    if workspace is None:
+        workspace = _workspace(gated_residual_backward_workspace_bytes(C, n), y.device)
+    _check(load().ttt_gated_residual_backward(
+        C, C if norm_width is None else int(norm_width), _ptr(grad_y), ld(grad_y, "grad_y"), _ptr(grad_h),
+        ld(grad_h, "grad_h"), y.data_ptr(), ld(y, "y"), o.data_ptr(), ld(o, "o"), _ptr(z), ld(z, "z"), _ptr(gamma),
+        _ptr(alpha), _ptr(gamma_next), float(eps), gx.data_ptr(), C, go.data_ptr(), C, _ptr(gz), C, _ptr(gg), _ptr(ga),
+        _ptr(gn), n, code, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream()))
+    return gx, go, gz, gg, ga, gn
+
+
+# ------------------------------------------------------------------ orthogonalisation
+def orthogonalise_workspace_bytes(rows: int, cols: int, batch: int, dtype: torch.dtype) -> int:
+    out = ctypes.c_size_t()
+    code = TTT_BF16 if dtype == torch.bfloat16 else TTT_F32
+    _check(load().ttt_orthogonalise_workspace_bytes(rows, cols, batch, code, ctypes.byref(out)))
+    return out.value
+
+
+def orthogonalise(g: torch.Tensor, steps: int = 5, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Muon's Newton-Schulz orthogonalisation of g [rows, cols] or of every matrix of g [batch, rows, cols].
+
+    ``out`` may be ``g`` (in place).
+    """
+    code = _dtype_code(g)
+    _here(g, out=out, workspace=workspace)
+    if out is None:
+        out = torch.empty(g.shape, dtype=g.dtype, device=g.device)
+    for t, name in ((g, "g"), (out, "out")):
+        if t.dim() not in (2, 3) or t.stride(-1) != 1 or t.dtype != g.dtype or t.shape != g.shape:
+            raise ValueError(f"{name} must be [rows, cols] or [batch, rows, cols] of one dtype with unit column stride")
+    B, R, C = (1, *g.shape) if g.dim() == 2 else g.shape
+    bs = lambda t: t.stride(0) if t.dim() == 3 else 0
+    if workspace is None:
+        workspace = _workspace(orthogonalise_workspace_bytes(R, C, B, g.dtype), g.device)
+    _check(load().ttt_orthogonalise(R, C, B, g.data_ptr(), g.stride(-2), bs(g), out.data_ptr(), out.stride(-2), bs(out),
+                                    int(steps), code, _ptr(workspace),
+                                    0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                    _stream()))
     return out
 
 
