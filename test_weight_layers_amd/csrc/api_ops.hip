@@ -76,8 +76,8 @@ int check_delta_shape(int H, int Hk, int dk, int dv, int dtype) {
 
 struct DeltaPlan {
   int nchunk;
-  size_t off_seqs, off_chunks, off_used, off_eg, off_el, off_gam, off_tm, off_am, off_tt, off_kt, off_qt;
-  size_t off_w0t, off_gwt, off_u, off_dr, off_gqp, off_gkp, off_gb, off_gd, total;
+  size_t off_seqs, off_chunks, off_used, off_eg, off_el, off_be, off_gam, off_tm, off_am, off_tt, off_kp, off_qp, off_kt, off_qt;
+  size_t off_gop, off_w0t, off_gwt, off_u, off_dr, off_gqp, off_gkp, off_gb, off_gd, total;
 };
 
 int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype, bool backward, DeltaPlan *out) {
@@ -95,7 +95,8 @@ int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype
     o = align256(o + bytes);
     return at;
   };
-  const size_t cc = (size_t)nc * H, mat = (size_t)kDeltaChunk * kDeltaChunk * 4;
+  const size_t cc = (size_t)nc * H, sb = delta_split_bytes(dtype == TTT_BF16);
+  const size_t mat = (size_t)kDeltaChunk * kDeltaChunk * sb;
   const size_t tok = (size_t)nc * Hk * dk * kDeltaChunk * esize(dtype);
   P.off_seqs = take((size_t)nseq * sizeof(DeltaSeq));
   P.off_chunks = take((size_t)nc * sizeof(DeltaChunk));
@@ -104,15 +105,19 @@ int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype
   P.off_el = take(cc * kDeltaChunk * 4);
   P.off_tm = take(cc * mat);
   P.off_am = take(cc * mat);
+  P.off_be = take(cc * kDeltaChunk * 4);
+  P.off_kp = take(tok);
+  P.off_qp = take(tok);
   P.off_kt = take(tok);
   if (backward) {
+    P.off_gop = take(cc * kDeltaChunk * dv * esize(dtype));
     P.off_gam = take(cc * kDeltaChunk * 8);
     P.off_tt = take(cc * mat);
     P.off_qt = take(tok);
-    P.off_w0t = take(cc * dk * dv * 4);
-    P.off_gwt = take(cc * dk * dv * 4);
-    P.off_u = take(cc * kDeltaChunk * dv * 4);
-    P.off_dr = take(cc * kDeltaChunk * dv * 4);
+    P.off_w0t = take(cc * dk * dv * sb);
+    P.off_gwt = take(cc * dk * dv * sb);
+    P.off_u = take(cc * kDeltaChunk * dv * sb);
+    P.off_dr = take(cc * kDeltaChunk * dv * sb);
     if (H != Hk) {
       P.off_gqp = take((size_t)n * H * dk * 4);
       P.off_gkp = take((size_t)n * H * dk * 4);
@@ -152,8 +157,11 @@ int delta_params(int H, int Hk, int dk, int dv, const float *w, const Rows &q, c
   p->eg = reinterpret_cast<float *>(b + P.off_eg);
   p->el = reinterpret_cast<float *>(b + P.off_el);
   p->tm = b + P.off_tm, p->am = b + P.off_am, p->kt = b + P.off_kt;
+  p->be = reinterpret_cast<float *>(b + P.off_be);
+  p->kp = b + P.off_kp, p->qp = b + P.off_qp;
   if (backward) {
     p->gam = reinterpret_cast<double *>(b + P.off_gam);
+    p->gop = b + P.off_gop;
     p->tt = b + P.off_tt, p->qt = b + P.off_qt, p->w0t = b + P.off_w0t, p->gwt = b + P.off_gwt;
     p->u = b + P.off_u, p->dr = b + P.off_dr;
     if (H != Hk) {

@@ -100,73 +100,118 @@ __global__ __launch_bounds__(256) void delta_zero_rows_kernel(DeltaParams p, T *
 
 // ------------------------------------------------------------------ chunk terms
 // One workgroup per chunk and head: e^gamma, T = (I + L)^-1 by block substitution in fp32 and A,
-// and (once per key head) the transposed tokens that the later kernels read as matrix operands.
+// and (once per key head) the tokens and their transposes in fragment order.
 // Substitution, not products of powers of L: those grow without bound where keys repeat.
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
+  constexpr int kPitch = DK + Sp<T>::kPad, NK = DK / 32, kA = C + 4;
+  constexpr int kTokBytes = C * kPitch * (int)sizeof(T), kABytes = C * kA * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char s_raw[kTokBytes > kABytes ? kTokBytes : kABytes];
   __shared__ double s_gam[C];
   __shared__ float s_beta[C];
-  __shared__ float s_l[C][C + 1], s_t[C][C + 1], s_x[32][33];
-  const int h = blockIdx.x % p.heads, c = blockIdx.x / p.heads;
+  __shared__ __attribute__((aligned(16))) float s_l[C][kA], s_t[C][kA];
+  __shared__ float s_x[32][33];
+  typedef typename FragOf<T>::type Tok;
+  T *s_tok = reinterpret_cast<T *>(s_raw);              // [64][kPitch]
+  float *s_a = reinterpret_cast<float *>(s_raw);        // [64][kA], after the tokens
+  const int item = xcd_item(), h = item % p.heads, c = item / p.heads;
   const DeltaChunk ck = p.chunks[c];
   if (ck.len == 0) return;
   const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
-  const int kh = h / (p.heads / p.key_heads);
+  const int grp = p.heads / p.key_heads, kh = h / grp;
+  const bool writer = h % grp == 0;                     // of the key head's operands
   const int64_t ch = (int64_t)c * p.heads + h;
-  const T *K = static_cast<const T *>(p.k) + (int64_t)ck.tok0 * p.ldk + kh * DK;
-  const T *Q = static_cast<const T *>(p.q) + (int64_t)ck.tok0 * p.ldq + kh * DK;
+  const int64_t tokens = ((int64_t)c * p.key_heads + kh) * (DK * C);
   if (t < C) {
     const bool ok = t < ck.len;
     double gam = 0.0;
     if (ok && p.decay) {
       const float x = p.decay[h * p.decay_hs + ck.tok0 + t];
-      gam = x < -200.0f ? -200.0 : (double)x;      // e^-200 is 0 in fp32; -inf would leave inf - inf
+      gam = x < -200.0f ? -200.0 : (double)x;           // e^-200 is 0 in fp32; -inf would leave inf - inf
     }
     for (int d = 1; d < C; d <<= 1) {
       const double x = __shfl_up(gam, d);
       if (t >= d) gam += x;
     }
     s_gam[t] = gam;
-    s_beta[t] = ok ? p.beta[h * p.beta_hs + ck.tok0 + t] : 0.0f;
+    const float be = ok ? p.beta[h * p.beta_hs + ck.tok0 + t] : 0.0f;
+    s_beta[t] = be;
+    p.be[ch * C + t] = be;
     if (BWD) p.gam[ch * C + t] = gam;
     p.eg[ch * C + t] = exp_of(gam);
     p.el[ch * C + t] = exp_of(__shfl(gam, 63) - gam);
   }
+  constexpr int V = 16 / (int)sizeof(T);                // elements of a 16-byte piece
+  const auto stage = [&](const T *src, int64_t ld) {    // rows past the chunk are zero
+    const T *x = src + (int64_t)ck.tok0 * ld + kh * DK;
+#pragma unroll
+    for (int i = 0; i < C * DK / V / 256; ++i) {
+      const int e = t + 256 * i, r = e / (DK / V), col = e % (DK / V) * V;
+      u32x4 v = u32x4{0, 0, 0, 0};
+      if (r < ck.len) v = *reinterpret_cast<const u32x4 *>(x + r * ld + col);
+      *reinterpret_cast<u32x4 *>(s_tok + r * kPitch + col) = v;
+    }
+  };
+  // the transposed operand: row = column of the tokens, k = token
+  const auto write_transposed = [&](T *dst) {
+#pragma unroll
+    for (int i = 0; i < DK / 64; ++i) {
+      const int rt = w * (DK / 64) + i;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int k0 = 32 * x + 8 * g;
+        Tok f;
+        if constexpr (sizeof(T) == 2) {
+          const unsigned char *b = s_raw + ((k0 + (li >> 2)) * kPitch + 16 * rt + 4 * (li & 3)) * 2;
+          f = cat8(lds_read_tr16(b), lds_read_tr16(b + 4 * kPitch * 2));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = s_tok[(k0 + e) * kPitch + 16 * rt + li];
+        }
+        *reinterpret_cast<Tok *>(dst + tokens + frag_of(rt, x, 2)) = f;
+      }
+    }
+  };
+  stage(static_cast<const T *>(p.q), p.ldq);
   __syncthreads();
-  // K K^T and Q K^T: wave w has rows 16w .. 16w+15, four column tiles
-  f32x4 kk[4], qk[4];
+  Tok qa[NK];                                           // wave w has rows 16 w .. 16 w + 15
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    qa[i] = ld8(s_tok + (16 * w + li) * kPitch + 32 * i + 8 * g);
+    if (writer) *reinterpret_cast<Tok *>(static_cast<T *>(p.qp) + tokens + frag_of(w, i, NK)) = qa[i];
+  }
+  if (BWD && writer) write_transposed(static_cast<T *>(p.qt));
+  __syncthreads();
+  stage(static_cast<const T *>(p.k), p.ldk);
+  __syncthreads();
+  f32x4 kk[4], qk[4];                                   // K K^T and Q K^T, four column tiles
 #pragma unroll
   for (int j = 0; j < 4; ++j) kk[j] = qk[j] = zero4();
-  const int last = ck.len - 1;
-  const int ra = 16 * w + li < last ? 16 * w + li : last;     // rows past the chunk repeat its last one, and are masked below
-#pragma unroll 2
-  for (int ks = 0; ks < DK; ks += 32) {
-    const auto ka = ld8(K + (int64_t)ra * p.ldk + ks + 8 * g);
-    const auto qa = ld8(Q + (int64_t)ra * p.ldq + ks + 8 * g);
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const Tok ka = ld8(s_tok + (16 * w + li) * kPitch + 32 * i + 8 * g);
+    if (writer) *reinterpret_cast<Tok *>(static_cast<T *>(p.kp) + tokens + frag_of(w, i, NK)) = ka;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j > w) continue;                                    // above the diagonal
-      const int rb = 16 * j + li < last ? 16 * j + li : last;
-      const auto kb = ld8(K + (int64_t)rb * p.ldk + ks + 8 * g);
+      if (j > w) continue;                              // above the diagonal
+      const Tok kb = ld8(s_tok + (16 * j + li) * kPitch + 32 * i + 8 * g);
       kk[j] = mm(ka, kb, kk[j]);
-      qk[j] = mm(qa, kb, qk[j]);
+      qk[j] = mm(qa[i], kb, qk[j]);
     }
   }
-  const int64_t mat = ch * (C * C * 4), plane = C * C * 2;
+  if (writer) write_transposed(static_cast<T *>(p.kt));
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int col = 16 * j + li;
-    f32x4 a;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * w + 4 * g + r;
       const float d = exp_of(row >= col ? s_gam[row] - s_gam[col] : 0.0);
       const bool in = row < ck.len && col <= row;
       s_l[row][col] = in && col < row ? s_beta[row] * d * kk[j][r] : 0.0f;
-      a[r] = in ? p.scale * d * qk[j][r] : 0.0f;
-      if (!BWD) Sp<T>::st1(p.am + mat, plane, row * C + col, a[r]);
+      s_a[row * kA + col] = in ? p.scale * d * qk[j][r] : 0.0f;
     }
-    if (BWD) Sp<T>::st4(p.am + mat, plane, col * C + 16 * w + 4 * g, a);   // A^T
   }
   __syncthreads();
   // T = (I + L)^-1.  Diagonal 16 x 16 blocks: wave w has block w, one column a lane.
@@ -183,7 +228,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) s_t[o + i][o + li] = x[i];
   }
-  for (int e = t; e < 16 * 48; e += 256) {      // zero above the diagonal blocks
+  for (int e = t; e < 16 * 48; e += 256) {              // zero above the diagonal blocks
     const int r = e / 48, x = e % 48;
     s_t[r][16 + x] = 0.0f;
     if (x < 32) s_t[16 + r][32 + x] = 0.0f;
@@ -227,24 +272,31 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
     s_t[32 + r][x] = -v;
   }
   __syncthreads();
+  const int64_t mat = ch * split_bytes<T>(C * C), plane = C * C * 2;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = (t + 256 * q) * 4, r = e >> 6, x = e & 63;
-    Sp<T>::st4(p.tm + mat, plane, e, f32x4{s_t[r][x], s_t[r][x + 1], s_t[r][x + 2], s_t[r][x + 3]});
-    if (BWD) Sp<T>::st4(p.tt + mat, plane, e, f32x4{s_t[x][r], s_t[x + 1][r], s_t[x + 2][r], s_t[x + 3][r]});
+  for (int q = 0; q < 2; ++q) {                         // fragment w + 4 q: rows 16 rt, k 32 kt
+    const int f = w + 4 * q, row = 16 * (f >> 1) + li, k0 = 32 * (f & 1) + 8 * g, e = f * 512 + l * 8;
+    float x[8];
+    Sp<T>::st8(p.tm + mat, plane, e, &s_t[row][k0]);
+    if (BWD) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = s_t[k0 + i][row];
+      Sp<T>::st8(p.tt + mat, plane, e, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = s_a[(k0 + i) * kA + row];
+      Sp<T>::st8(p.am + mat, plane, e, x);
+    } else {
+      Sp<T>::st8(p.am + mat, plane, e, s_a + row * kA + k0);
+    }
   }
-  // transposed tokens [dk][64], rows past the chunk zero: the first head of each key head writes them
-  if (h % (p.heads / p.key_heads) == 0) {
-    const int64_t o = ((int64_t)c * p.key_heads + kh) * DK * C;
-    T *kt = static_cast<T *>(p.kt) + o, *qt = BWD ? static_cast<T *>(p.qt) + o : nullptr;
-    for (int e = t; e < DK * C / 4; e += 256) {
-      const int col = e % DK, r0 = e / DK * 4;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bool ok = r0 + r < ck.len;
-        kt[col * C + r0 + r] = ok ? K[(int64_t)(r0 + r) * p.ldk + col] : from_f32<T>(0.0f);
-        if (BWD) qt[col * C + r0 + r] = ok ? Q[(int64_t)(r0 + r) * p.ldq + col] : from_f32<T>(0.0f);
-      }
+  if (BWD) {
+    const int row = 16 * w + li, nk = p.dv / 32;
+    const T *go = static_cast<const T *>(p.go) + (int64_t)(ck.tok0 + (row < ck.len ? row : 0)) * p.ldgo + h * p.dv + 8 * g;
+    T *o = static_cast<T *>(p.gop) + ch * C * p.dv;
+    for (int i = 0; i < nk; ++i) {
+      Tok v = ld8(go + 32 * i);
+      if (row >= ck.len) v = zero8<T>();
+      *reinterpret_cast<Tok *>(o + frag_of(w, i, nk)) = v;
     }
   }
 }
@@ -253,15 +305,20 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
 // One workgroup per sequence, head and 16-column slice of dv, over the chunks in order.  The
 // slice of W stays in fp32 accumulators: lane (g, li) of wave w holds W[dv = li][dk = w DK/4 +
 // 16 i + 4 g + r].  Between the products only R, U and the state pass through LDS; tokens and
-// chunk terms go from memory straight into operand registers (each is used once).
+// chunk terms go from memory straight into operand registers (each is used once), the next
+// chunk's as soon as this chunk's have been used, so that a chunk waits for no load.
+// Bound by the order of the chunks: three products that depend on one another, each ended by an
+// exchange through LDS.
 // BWD writes the states and U that the gradient needs, in place of the outputs.
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(256, 1) void delta_state_kernel(DeltaParams p) {
   __shared__ __attribute__((aligned(16))) SpTile<T, SL, DK> s_w;
   __shared__ __attribute__((aligned(16))) SpTile<T, SL, C> s_r, s_u, s_ul;
-  constexpr int NT = DK / 64;
-  const int slices = p.dv / SL;
-  const int sl = blockIdx.x % slices, h = blockIdx.x / slices % p.heads, b = blockIdx.x / slices / p.heads;
+  typedef typename FragOf<T>::type Tok;
+  typedef typename Sp<T>::Frag Frag;
+  constexpr int NT = DK / 64, NK = DK / 32;
+  const int slices = p.dv / SL, item = xcd_item();
+  const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
   const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
   const DeltaSeq sq = p.seqs[b];
@@ -272,79 +329,118 @@ __global__ __launch_bounds__(256, 1) void delta_state_kernel(DeltaParams p) {
     st[i] = *reinterpret_cast<const f32x4 *>(p.w + wrow + 16 * i);
     s_w.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
   }
-  __syncthreads();
+  const int t4 = 16 * w + 4 * g;        // this lane's four rows of every 64 x 16 product
   const int64_t plane = C * C * 2;
-  for (int c0 = 0; c0 < sq.len; c0 += C) {
+  const int last_c0 = sq.len > 0 ? (sq.len - 1) / C * C : 0;
+
+  // operands of the chunk at row offset c0
+  Tok kf[NK], qf[BWD ? 1 : NK], ktf[NT][2];
+  Frag tf[2], af[2];
+  T v[4];
+  float ec = 0.0f;
+  f32x4 eg, el, be;
+  const auto load_tokens = [&](int c0) {
+    const int64_t o = ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * (DK * C);
+    const T *K = static_cast<const T *>(p.kp) + o, *Q = static_cast<const T *>(p.qp) + o;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      kf[i] = ld8(K + frag_of(w, i, NK));
+      if (!BWD) qf[i] = ld8(Q + frag_of(w, i, NK));
+    }
+  };
+  const auto load_values = [&](int c0) {
     const int len = sq.len - c0 < C ? sq.len - c0 : C;
-    const int64_t c = sq.chunk0 + c0 / C, ch = c * p.heads + h;
-    const int64_t tok0 = sq.start + c0;
-    const int row = 16 * w + li < len ? 16 * w + li : len - 1;
-    const T *K = static_cast<const T *>(p.k) + (tok0 + row) * p.ldk + kh * DK + 8 * g;
-    const T *Q = static_cast<const T *>(p.q) + (tok0 + row) * p.ldq + kh * DK + 8 * g;
-    f32x4 pa = zero4(), qa = zero4();
-#pragma unroll
-    for (int ks = 0; ks < DK; ks += 32) {
-      const auto wf = s_w.ld(li, ks + 8 * g);
-      pa = mm(ld8(K + ks), wf, pa);
-      if (!BWD) qa = mm(ld8(Q + ks), wf, qa);
-    }
-    if (BWD) {      // the state before the chunk, [dk][dv]
-      char *o = p.w0t + ch * ((int64_t)DK * p.dv * 4);
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          Sp<T>::st1(o, (int64_t)DK * p.dv * 2, (int64_t)(w * (DK / 4) + 16 * i + 4 * g + r) * p.dv + sl * SL + li,
-                     st[i][r]);
-    }
-    const int t4 = 16 * w + 4 * g;      // this lane's four rows of every 64 x 16 product
-    const f32x4 eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + t4);
-    const f32x4 el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + t4);
-    f32x4 rr;
+    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
+    eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + t4);
+    el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + t4);
+    be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + t4);
+    ec = p.eg[ch * C + C - 1];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const bool ok = t4 + r < len;
-      const int64_t tk = tok0 + (ok ? t4 + r : len - 1);
-      const float v = to_f32(static_cast<const T *>(p.v)[tk * p.ldv + h * p.dv + sl * SL + li]);
-      rr[r] = ok ? p.beta[h * p.beta_hs + tk] * (v - eg[r] * pa[r]) : 0.0f;
+      const int64_t tk = (int64_t)sq.start + c0 + (t4 + r < len ? t4 + r : len - 1);
+      v[r] = static_cast<const T *>(p.v)[tk * p.ldv + h * p.dv + sl * SL + li];
     }
+  };
+  const auto load_square = [&](const char *m, int c0, Frag (&f)[2]) {
+    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)         // the second half is above the diagonal for the first two waves
+      if (i == 0 || w >= 2) f[i] = Sp<T>::ld(m + ch * split_bytes<T>(C * C), plane, frag_of(w, i, 2));
+  };
+  const auto load_transposed = [&](int c0) {
+    const T *kt = static_cast<const T *>(p.kt) + ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * (DK * C);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      ktf[i][0] = ld8(kt + frag_of(w * NT + i, 0, 2));
+      ktf[i][1] = ld8(kt + frag_of(w * NT + i, 1, 2));
+    }
+  };
+  if (sq.len > 0) {
+    load_tokens(0);
+    load_values(0);
+    load_square(p.tm, 0, tf);
+    if (!BWD) load_square(p.am, 0, af);
+    load_transposed(0);
+  }
+  lds_barrier();
+  for (int c0 = 0; c0 < sq.len; c0 += C) {
+    const int len = sq.len - c0 < C ? sq.len - c0 : C, nx = c0 < last_c0 ? c0 + C : c0;
+    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
+    const int64_t tok0 = sq.start + c0;
+    f32x4 pa = zero4(), pb = zero4(), qa = zero4();
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const Frag wf = s_w.ld(li, 32 * i + 8 * g);
+      if (i & 1) pb = mm(kf[i], wf, pb); else pa = mm(kf[i], wf, pa);
+      if (!BWD) qa = mm(qf[i], wf, qa);
+    }
+    load_tokens(nx);
+    if (BWD) {      // the state before the chunk, dk x dv
+      char *o = p.w0t + ch * split_bytes<T>((int64_t)DK * p.dv);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        s_w.copy_t4(0, (w * NT + i) * 16, o, (int64_t)DK * p.dv * 2,
+                    frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
+    }
+    f32x4 rr;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) rr[r] = t4 + r < len ? be[r] * (to_f32(v[r]) - eg[r] * (pa[r] + pb[r])) : 0.0f;
+    const f32x4 eg_now = eg, el_now = el;
+    const float ec_now = ec;
+    load_values(nx);
     s_r.st4(li, t4, rr);
-    __syncthreads();
+    lds_barrier();
     f32x4 u = zero4();
-    const char *tm = p.tm + ch * (C * C * 4);
+    u = mm(tf[0], s_r.ld(li, 8 * g), u);
+    if (w >= 2) u = mm(tf[1], s_r.ld(li, 32 + 8 * g), u);
+    load_square(p.tm, nx, tf);
+    s_ul.st4(li, t4, u * el_now);
+    s_u.st4(li, t4, u);
+    lds_barrier();
+    {
+      const Frag u0 = s_ul.ld(li, 8 * g), u1 = s_ul.ld(li, 32 + 8 * g);
 #pragma unroll
-    for (int ks = 0; ks < C; ks += 32)
-      if (ks <= 16 * w) u = mm(Sp<T>::ld(tm, plane, (16 * w + li) * C + ks + 8 * g), s_r.ld(li, ks + 8 * g), u);
-    s_ul.st4(li, t4, u * el);
-    if (!BWD) {
-      s_u.st4(li, t4, u);
-    } else {
-      char *o = p.u + ch * ((int64_t)C * p.dv * 4);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) Sp<T>::st1(o, (int64_t)C * p.dv * 2, (int64_t)(t4 + r) * p.dv + sl * SL + li, u[r]);
+      for (int i = 0; i < NT; ++i) {
+        st[i] = mm(ktf[i][0], u0, st[i] * ec_now);
+        st[i] = mm(ktf[i][1], u1, st[i]);
+        s_w.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
+      }
     }
-    __syncthreads();
-    if (!BWD) {
-      f32x4 o = qa * eg * p.scale;
-      const char *am = p.am + ch * (C * C * 4);
-#pragma unroll
-      for (int ks = 0; ks < C; ks += 32)
-        if (ks <= 16 * w) o = mm(Sp<T>::ld(am, plane, (16 * w + li) * C + ks + 8 * g), s_u.ld(li, ks + 8 * g), o);
+    load_transposed(nx);
+    if (BWD) {
+      s_u.copy_t4(0, 16 * w, p.u + ch * split_bytes<T>((int64_t)C * p.dv), (int64_t)C * p.dv * 2,
+                  frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
+    } else {
+      f32x4 o = qa * eg_now * p.scale;
+      o = mm(af[0], s_u.ld(li, 8 * g), o);
+      if (w >= 2) o = mm(af[1], s_u.ld(li, 32 + 8 * g), o);
+      load_square(p.am, nx, af);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (t4 + r < len)
           static_cast<T *>(p.o)[(tok0 + t4 + r) * p.ldo + h * p.dv + sl * SL + li] = from_f32<T>(o[r]);
     }
-    const float ec = p.eg[ch * C + C - 1];
-    const T *kt = static_cast<const T *>(p.kt) + (c * p.key_heads + kh) * (DK * C) + (w * (DK / 4) + li) * C + 8 * g;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      st[i] = st[i] * ec;
-#pragma unroll
-      for (int ks = 0; ks < C; ks += 32) st[i] = mm(ld8(kt + 16 * i * C + ks), s_ul.ld(li, ks + 8 * g), st[i]);
-      s_w.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
-    }
-    __syncthreads();
+    lds_barrier();
   }
   if (!BWD)
 #pragma unroll

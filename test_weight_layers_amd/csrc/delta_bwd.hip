@@ -22,14 +22,16 @@ constexpr int C = kDeltaChunk;
 constexpr int SL = kDeltaSlice;
 
 // ------------------------------------------------------------------ state gradients
-// The reverse of the states kernel, with the same split and layout.
+// The reverse of the states kernel, with the same split, layout and order of loads.
 template <typename T, int DK>
 __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
   __shared__ __attribute__((aligned(16))) SpTile<T, SL, DK> s_g;
-  __shared__ __attribute__((aligned(16))) SpTile<T, SL, C> s_go, s_goe, s_du, s_dp;
-  constexpr int NT = DK / 64;
-  const int slices = p.dv / SL;
-  const int sl = blockIdx.x % slices, h = blockIdx.x / slices % p.heads, b = blockIdx.x / slices / p.heads;
+  __shared__ __attribute__((aligned(16))) SpTile<T, SL, C> s_go, s_goe[2], s_du, s_dr, s_dp;
+  typedef typename FragOf<T>::type Tok;
+  typedef typename Sp<T>::Frag Frag;
+  constexpr int NT = DK / 64, NK = DK / 32;
+  const int slices = p.dv / SL, item = xcd_item();
+  const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
   const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
   const DeltaSeq sq = p.seqs[b];
@@ -42,75 +44,126 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
   }
   const int64_t plane = C * C * 2;
   const int t4 = 16 * w + 4 * g;
-  for (int c0 = (sq.len - 1) / C * C; c0 >= 0 && sq.len > 0; c0 -= C) {
+
+  Tok kf[NK], ktf[NT][2], qtf[NT][2];
+  Frag tf[2], af[2];
+  T gv[4];
+  float ec = 0.0f;
+  f32x4 be, eg, el;
+  const auto load_tokens = [&](int c0) {
+    const T *K = static_cast<const T *>(p.kp) + ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * (DK * C);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) kf[i] = ld8(K + frag_of(w, i, NK));
+  };
+  const auto load_values = [&](int c0) {
     const int len = sq.len - c0 < C ? sq.len - c0 : C;
-    const int64_t c = sq.chunk0 + c0 / C, ch = c * p.heads + h;
-    const int64_t tok0 = sq.start + c0;
-    const f32x4 eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + t4);
-    const f32x4 el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + t4);
-    f32x4 go, be;
+    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
+    eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + t4);
+    el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + t4);
+    be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + t4);
+    ec = p.eg[ch * C + C - 1];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const bool ok = t4 + r < len;
-      const int64_t tk = tok0 + (ok ? t4 + r : len - 1);
-      const float x = to_f32(static_cast<const T *>(p.go)[tk * p.ldgo + h * p.dv + sl * SL + li]);
-      go[r] = ok ? x : 0.0f;
-      be[r] = ok ? p.beta[h * p.beta_hs + tk] : 0.0f;
+      const int64_t tk = (int64_t)sq.start + c0 + (t4 + r < len ? t4 + r : len - 1);
+      gv[r] = static_cast<const T *>(p.go)[tk * p.ldgo + h * p.dv + sl * SL + li];
     }
+  };
+  // the chunk's go, 0 past its end, to LDS (as it is, and as the state's update takes it)
+  const auto store_go = [&](int c0, int buf) {
+    const int len = sq.len - c0 < C ? sq.len - c0 : C;
+    f32x4 go;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) go[r] = t4 + r < len ? to_f32(gv[r]) : 0.0f;
     s_go.st4(li, t4, go);
-    s_goe.st4(li, t4, go * eg * p.scale);
-    __syncthreads();
-    const int row = 16 * w + li < len ? 16 * w + li : len - 1;
-    const T *K = static_cast<const T *>(p.k) + (tok0 + row) * p.ldk + kh * DK + 8 * g;
-    f32x4 du = zero4();
+    s_goe[buf].st4(li, t4, go * eg * p.scale);
+  };
+  const auto load_square = [&](const char *m, int c0, Frag (&f)[2]) {
+    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
 #pragma unroll
-    for (int ks = 0; ks < DK; ks += 32) du = mm(ld8(K + ks), s_g.ld(li, ks + 8 * g), du);
+    for (int i = 0; i < 2; ++i)         // the first half is below the diagonal for the last two waves
+      if (i == 1 || w < 2) f[i] = Sp<T>::ld(m + ch * split_bytes<T>(C * C), plane, frag_of(w, i, 2));
+  };
+  const auto load_transposed = [&](int c0) {
+    const int64_t o = ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * (DK * C);
+    const T *kt = static_cast<const T *>(p.kt) + o, *qt = static_cast<const T *>(p.qt) + o;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) du[r] = t4 + r < len ? du[r] * el[r] : 0.0f;
-    const char *am = p.am + ch * (C * C * 4), *tt = p.tt + ch * (C * C * 4);
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int ks = 0; ks < C; ks += 32)
-      if (ks + 32 > 16 * w) du = mm(Sp<T>::ld(am, plane, (16 * w + li) * C + ks + 8 * g), s_go.ld(li, ks + 8 * g), du);
-    s_du.st4(li, t4, du);
-    {                                   // the gradient after the chunk, [dk][dv]
-      char *o = p.gwt + ch * ((int64_t)DK * p.dv * 4);
+      for (int x = 0; x < 2; ++x) {
+        ktf[i][x] = ld8(kt + frag_of(w * NT + i, x, 2));
+        qtf[i][x] = ld8(qt + frag_of(w * NT + i, x, 2));
+      }
+  };
+  const int first = sq.len > 0 ? (sq.len - 1) / C * C : -1;
+  if (first >= 0) {
+    load_tokens(first);
+    load_values(first);
+    load_square(p.am, first, af);
+    load_square(p.tt, first, tf);
+    load_transposed(first);
+    store_go(first, 0);
+  }
+  lds_barrier();
+  int buf = 0;
+  for (int c0 = first; c0 >= 0; c0 -= C, buf ^= 1) {
+    const int len = sq.len - c0 < C ? sq.len - c0 : C, nx = c0 > 0 ? c0 - C : 0;
+    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
+    const int64_t tok0 = sq.start + c0;
+    f32x4 du = zero4(), db = zero4();
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      if (i & 1) db = mm(kf[i], s_g.ld(li, 32 * i + 8 * g), db);
+      else du = mm(kf[i], s_g.ld(li, 32 * i + 8 * g), du);
+    }
+    load_tokens(nx);
+    {                                   // the gradient after the chunk, dk x dv
+      char *o = p.gwt + ch * split_bytes<T>((int64_t)DK * p.dv);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          Sp<T>::st1(o, (int64_t)DK * p.dv * 2, (int64_t)(w * (DK / 4) + 16 * i + 4 * g + r) * p.dv + sl * SL + li,
-                     st[i][r]);
+        s_g.copy_t4(0, (w * NT + i) * 16, o, (int64_t)DK * p.dv * 2,
+                    frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
     }
-    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) du[r] = t4 + r < len ? (du[r] + db[r]) * el[r] : 0.0f;
+    if (w < 2) du = mm(af[0], s_go.ld(li, 8 * g), du);
+    du = mm(af[1], s_go.ld(li, 32 + 8 * g), du);
+    load_square(p.am, nx, af);
+    s_du.st4(li, t4, du);
+    const float ec_now = ec;
+    f32x4 dp;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) dp[r] = -be[r] * eg[r];
+    const f32x4 be_now = be;
+    load_values(nx);
+    lds_barrier();
     f32x4 dr = zero4();
+    if (w < 2) dr = mm(tf[0], s_du.ld(li, 8 * g), dr);
+    dr = mm(tf[1], s_du.ld(li, 32 + 8 * g), dr);
+    load_square(p.tt, nx, tf);
+    s_dp.st4(li, t4, dr * dp);
+    s_dr.st4(li, t4, dr);
 #pragma unroll
-    for (int ks = 0; ks < C; ks += 32)
-      if (ks + 32 > 16 * w) dr = mm(Sp<T>::ld(tt, plane, (16 * w + li) * C + ks + 8 * g), s_du.ld(li, ks + 8 * g), dr);
-    s_dp.st4(li, t4, dr * be * eg * -1.0f);
+    for (int r = 0; r < 4; ++r)
+      if (t4 + r < len)
+        static_cast<T *>(p.gv)[(tok0 + t4 + r) * p.ldgv + h * p.dv + sl * SL + li] = from_f32<T>(be_now[r] * dr[r]);
+    lds_barrier();
     {
-      char *o = p.dr + ch * ((int64_t)C * p.dv * 4);
+      const Frag p0 = s_dp.ld(li, 8 * g), p1 = s_dp.ld(li, 32 + 8 * g);
+      const Frag g0 = s_goe[buf].ld(li, 8 * g), g1 = s_goe[buf].ld(li, 32 + 8 * g);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        Sp<T>::st1(o, (int64_t)C * p.dv * 2, (int64_t)(t4 + r) * p.dv + sl * SL + li, dr[r]);
-        if (t4 + r < len)
-          static_cast<T *>(p.gv)[(tok0 + t4 + r) * p.ldgv + h * p.dv + sl * SL + li] = from_f32<T>(be[r] * dr[r]);
+      for (int i = 0; i < NT; ++i) {
+        st[i] = mm(ktf[i][0], p0, st[i] * ec_now);
+        st[i] = mm(ktf[i][1], p1, st[i]);
+        st[i] = mm(qtf[i][0], g0, st[i]);
+        st[i] = mm(qtf[i][1], g1, st[i]);
+        s_g.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
       }
     }
-    __syncthreads();
-    const float ec = p.eg[ch * C + C - 1];
-    const int64_t to = (c * p.key_heads + kh) * (DK * C) + (w * (DK / 4) + li) * C + 8 * g;
-    const T *kt = static_cast<const T *>(p.kt) + to, *qt = static_cast<const T *>(p.qt) + to;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      st[i] = st[i] * ec;
-#pragma unroll
-      for (int ks = 0; ks < C; ks += 32) {
-        st[i] = mm(ld8(kt + 16 * i * C + ks), s_dp.ld(li, ks + 8 * g), st[i]);
-        st[i] = mm(ld8(qt + 16 * i * C + ks), s_goe.ld(li, ks + 8 * g), st[i]);
-      }
-      s_g.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
-    }
-    __syncthreads();
+    load_transposed(nx);
+    s_dr.copy_t4(0, 16 * w, p.dr + ch * split_bytes<T>((int64_t)C * p.dv), (int64_t)C * p.dv * 2,
+                 frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
+    store_go(nx, buf ^ 1);
+    lds_barrier();
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(p.gw + wrow + 16 * i) = st[i];
@@ -126,19 +179,21 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
   __shared__ float s_row[5][4][C];      // per-wave partials: q.(go W0), k.(dR W0), k.(U G), row / column sums of M
   __shared__ float s_db[C], s_red[4];
   typedef typename Sp<T>::Frag Frag;
-  constexpr int NT = DK / 64;
-  const int h = blockIdx.x % p.heads, c = blockIdx.x / p.heads;
+  constexpr int NT = DK / 64, TP = NT > 1 ? 2 : 1;      // column tiles of a wave, and at once
+  const int item = xcd_item(), h = item % p.heads, c = item / p.heads;
   const DeltaChunk ck = p.chunks[c];
   if (ck.len == 0) return;
   const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
   const int grp = p.heads / p.key_heads, kh = h / grp;
   const int64_t ch = (int64_t)c * p.heads + h;
   const int last = ck.len - 1;
-  const T *K = static_cast<const T *>(p.k) + (int64_t)ck.tok0 * p.ldk + kh * DK;
-  const T *Q = static_cast<const T *>(p.q) + (int64_t)ck.tok0 * p.ldq + kh * DK;
+  const int nv = p.dv / 32;
+  const int64_t to = ((int64_t)c * p.key_heads + kh) * (DK * C);
+  const T *K = static_cast<const T *>(p.kp) + to, *Q = static_cast<const T *>(p.qp) + to;
+  const T *KT = static_cast<const T *>(p.kt) + to, *QT = static_cast<const T *>(p.qt) + to;
   const T *V = static_cast<const T *>(p.v) + (int64_t)ck.tok0 * p.ldv + h * p.dv;
-  const T *GO = static_cast<const T *>(p.go) + (int64_t)ck.tok0 * p.ldgo + h * p.dv;
-  const int64_t uo = ch * ((int64_t)C * p.dv * 4), up = (int64_t)C * p.dv * 2;
+  const T *GO = static_cast<const T *>(p.gop) + ch * C * p.dv;
+  const int64_t uo = ch * split_bytes<T>((int64_t)C * p.dv), up = (int64_t)C * p.dv * 2;
   const char *U = p.u + uo, *DR = p.dr + uo;
 
   // ---- X, Y and the sums over them
@@ -148,29 +203,28 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
     for (int j = 0; j < 4; ++j) kk[j] = qk[j] = da[j] = dl[j] = zero4();
     const int ra = 16 * w + li, rac = ra < last ? ra : last;
 #pragma unroll 2
-    for (int ks = 0; ks < DK; ks += 32) {
-      const auto ka = ld8(K + (int64_t)rac * p.ldk + ks + 8 * g);
-      const auto qa = ld8(Q + (int64_t)rac * p.ldq + ks + 8 * g);
+    for (int i = 0; i < DK / 32; ++i) {
+      const auto ka = ld8(K + frag_of(w, i, DK / 32)), qa = ld8(Q + frag_of(w, i, DK / 32));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j > w) continue;
-        const int rb = 16 * j + li < last ? 16 * j + li : last;
-        const auto kb = ld8(K + (int64_t)rb * p.ldk + ks + 8 * g);
+        const auto kb = ld8(K + frag_of(j, i, DK / 32));
         kk[j] = mm(ka, kb, kk[j]);
         qk[j] = mm(qa, kb, qk[j]);
       }
     }
     float drv = 0.0f;                                   // dR_i . V_i
-    for (int ks = 0; ks < p.dv; ks += 32) {
-      const auto ga = ld8(GO + (int64_t)rac * p.ldgo + ks + 8 * g);
-      const Frag ra_f = Sp<T>::ld(DR, up, (int64_t)ra * p.dv + ks + 8 * g);
-      const auto va = ld8(V + (int64_t)rac * p.ldv + ks + 8 * g);
+#pragma unroll 2
+    for (int i = 0; i < nv; ++i) {
+      const auto ga = ld8(GO + frag_of(w, i, nv));
+      const Frag ra_f = Sp<T>::ld(DR, up, frag_of(w, i, nv));
+      const auto va = ld8(V + (int64_t)rac * p.ldv + 32 * i + 8 * g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) drv += Sp<T>::at(ra_f, i) * (float)va[i];
+      for (int e = 0; e < 8; ++e) drv += Sp<T>::at(ra_f, e) * (float)va[e];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j > w) continue;
-        const Frag ub = Sp<T>::ld(U, up, (int64_t)(16 * j + li) * p.dv + ks + 8 * g);
+        const Frag ub = Sp<T>::ld(U, up, frag_of(j, i, nv));
         da[j] = mm(ga, ub, da[j]);
         dl[j] = mm(ra_f, ub, dl[j]);
       }
@@ -189,7 +243,7 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
         const int row = 16 * w + 4 * g + r;
         const bool in = row < ck.len && col <= row;
         const float d = in ? exp_of(p.gam[ch * C + row] - p.gam[ch * C + col]) : 0.0f;
-        const float be = in ? p.beta[h * p.beta_hs + ck.tok0 + row] : 0.0f;
+        const float be = p.be[ch * C + row];
         x[r] = in ? p.scale * d * da[j][r] : 0.0f;
         const float dn = in && col < row ? -d * dl[j][r] : 0.0f;
         y[r] = be * dn;
@@ -231,62 +285,77 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) dq_dot[a][r] = dr_dot[a][r] = du_dot[a][r] = 0.0f;
   float wg = 0.0f;                                      // <W0, G>
-  const int64_t so = ch * ((int64_t)DK * p.dv * 4), sp = (int64_t)DK * p.dv * 2;
-  const int64_t to = ((int64_t)c * p.key_heads + kh) * (DK * C);
-  const T *KT = static_cast<const T *>(p.kt) + to, *QT = static_cast<const T *>(p.qt) + to;
+  const int64_t so = ch * split_bytes<T>((int64_t)DK * p.dv), sp = (int64_t)DK * p.dv * 2;
 #pragma unroll 1
-  for (int i = 0; i < NT; ++i) {
-    const int d0 = w * (DK / 4) + 16 * i;
+  for (int i = 0; i < NT; i += TP) {
     int base = li;                      // opaque: keeps the LDS operands below out of registers between tiles
     asm volatile("" : "+v"(base));
-    f32x4 aq[4], ar[4], au[4];
+    const int rt = w * NT + i;          // 16-wide column tiles rt .. rt + TP - 1
+    f32x4 aq[TP][4], ar[TP][4], au[TP][4];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) aq[a] = ar[a] = au[a] = zero4();
-    for (int ks = 0; ks < p.dv; ks += 32) {
-      const Frag wf = Sp<T>::ld(p.w0t + so, sp, (int64_t)(d0 + li) * p.dv + ks + 8 * g);
-      const Frag gf = Sp<T>::ld(p.gwt + so, sp, (int64_t)(d0 + li) * p.dv + ks + 8 * g);
+    for (int x = 0; x < TP; ++x)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) wg += Sp<T>::at(wf, e) * Sp<T>::at(gf, e);
+      for (int a = 0; a < 4; ++a) aq[x][a] = ar[x][a] = au[x][a] = zero4();
+#pragma unroll 1
+    for (int ks = 0; ks < nv; ++ks) {
+      Frag wf[TP], gf[TP];
+#pragma unroll
+      for (int x = 0; x < TP; ++x) {
+        wf[x] = Sp<T>::ld(p.w0t + so, sp, frag_of(rt + x, ks, nv));
+        gf[x] = Sp<T>::ld(p.gwt + so, sp, frag_of(rt + x, ks, nv));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wg += Sp<T>::at(wf[x], e) * Sp<T>::at(gf[x], e);
+      }
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        const int row = 16 * a + li, rc = row < last ? row : last;
-        aq[a] = mm(ld8(GO + (int64_t)rc * p.ldgo + ks + 8 * g), wf, aq[a]);
-        ar[a] = mm(Sp<T>::ld(DR, up, (int64_t)row * p.dv + ks + 8 * g), wf, ar[a]);
-        au[a] = mm(Sp<T>::ld(U, up, (int64_t)row * p.dv + ks + 8 * g), gf, au[a]);
+        const auto ga = ld8(GO + frag_of(a, ks, nv));
+        const Frag ra = Sp<T>::ld(DR, up, frag_of(a, ks, nv)), ua = Sp<T>::ld(U, up, frag_of(a, ks, nv));
+#pragma unroll
+        for (int x = 0; x < TP; ++x) {
+          aq[x][a] = mm(ga, wf[x], aq[x][a]);
+          ar[x][a] = mm(ra, wf[x], ar[x][a]);
+          au[x][a] = mm(ua, gf[x], au[x][a]);
+        }
       }
     }
-    const auto k0 = ld8(KT + (d0 + li) * C + 8 * g), k1 = ld8(KT + (d0 + li) * C + 32 + 8 * g);
-    const auto q0 = ld8(QT + (d0 + li) * C + 8 * g), q1 = ld8(QT + (d0 + li) * C + 32 + 8 * g);
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      f32x4 xq = zero4(), xk = zero4();
-      const int row = 16 * a + base;
-      xq = mm(s_x.ld(row, 8 * g), k0, xq);
-      xq = mm(s_x.ld(row, 32 + 8 * g), k1, xq);
-      xk = mm(s_xt.ld(row, 8 * g), q0, xk);
-      xk = mm(s_xt.ld(row, 32 + 8 * g), q1, xk);
-      xk = mm(s_y.ld(row, 8 * g), k0, xk);
-      xk = mm(s_y.ld(row, 32 + 8 * g), k1, xk);
-      xk = mm(s_yt.ld(row, 8 * g), k0, xk);
-      xk = mm(s_yt.ld(row, 32 + 8 * g), k1, xk);
-      const int r0 = 16 * a + 4 * g, col = d0 + li;
+    for (int x = 0; x < TP; ++x) {
+      const auto k0 = ld8(KT + frag_of(rt + x, 0, 2)), k1 = ld8(KT + frag_of(rt + x, 1, 2));
+      const auto q0 = ld8(QT + frag_of(rt + x, 0, 2)), q1 = ld8(QT + frag_of(rt + x, 1, 2));
+      const int col = (rt + x) * 16 + li;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (r0 + r >= ck.len) continue;
-        const int64_t tk = ck.tok0 + r0 + r;
-        const float eg = p.eg[ch * C + r0 + r], el = p.el[ch * C + r0 + r], be = p.beta[h * p.beta_hs + tk];
-        const float qv = to_f32(Q[(int64_t)(r0 + r) * p.ldq + col]), kv = to_f32(K[(int64_t)(r0 + r) * p.ldk + col]);
-        const float dqi = p.scale * eg * aq[a][r], dui = el * au[a][r];
-        dq_dot[a][r] += qv * dqi;
-        dr_dot[a][r] += kv * ar[a][r];
-        du_dot[a][r] += kv * dui;
-        const float dq = dqi + xq[r], dk = dui - be * eg * ar[a][r] + xk[r];
-        if (p.gqp) {
-          p.gqp[(tk * p.heads + h) * DK + col] = dq;
-          p.gkp[(tk * p.heads + h) * DK + col] = dk;
-        } else {
-          static_cast<T *>(p.gq)[tk * p.ldgq + kh * DK + col] = from_f32<T>(dq);
-          static_cast<T *>(p.gk)[tk * p.ldgk + kh * DK + col] = from_f32<T>(dk);
+      for (int a = 0; a < 4; ++a) {
+        f32x4 xq = zero4(), xk = zero4();
+        const int row = 16 * a + base;
+        xq = mm(s_x.ld(row, 8 * g), k0, xq);
+        xq = mm(s_x.ld(row, 32 + 8 * g), k1, xq);
+        xk = mm(s_xt.ld(row, 8 * g), q0, xk);
+        xk = mm(s_xt.ld(row, 32 + 8 * g), q1, xk);
+        xk = mm(s_y.ld(row, 8 * g), k0, xk);
+        xk = mm(s_y.ld(row, 32 + 8 * g), k1, xk);
+        xk = mm(s_yt.ld(row, 8 * g), k0, xk);
+        xk = mm(s_yt.ld(row, 32 + 8 * g), k1, xk);
+        const int r0 = 16 * a + 4 * g;
+        const f32x4 eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + r0);
+        const f32x4 el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + r0);
+        const f32x4 be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + r0);
+        const T *kv = KT + frag_at(col, r0, 2), *qv = QT + frag_at(col, r0, 2);     // four tokens' elements
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (r0 + r >= ck.len) continue;
+          const int64_t tk = ck.tok0 + r0 + r;
+          const float dqi = p.scale * eg[r] * aq[x][a][r], dui = el[r] * au[x][a][r];
+          dq_dot[a][r] += to_f32(qv[r]) * dqi;
+          dr_dot[a][r] += to_f32(kv[r]) * ar[x][a][r];
+          du_dot[a][r] += to_f32(kv[r]) * dui;
+          const float dq = dqi + xq[r], dk = dui - be[r] * eg[r] * ar[x][a][r] + xk[r];
+          if (p.gqp) {
+            p.gqp[(tk * p.heads + h) * DK + col] = dq;
+            p.gkp[(tk * p.heads + h) * DK + col] = dk;
+          } else {
+            static_cast<T *>(p.gq)[tk * p.ldgq + kh * DK + col] = from_f32<T>(dq);
+            static_cast<T *>(p.gk)[tk * p.ldgk + kh * DK + col] = from_f32<T>(dk);
+          }
         }
       }
     }
@@ -318,7 +387,7 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
 #pragma unroll
     for (int j = 0; j < 3; ++j) s[j] = s_row[j][0][t] + s_row[j][1][t] + s_row[j][2][t] + s_row[j][3][t];
     const bool ok = t < ck.len;
-    const float eg = p.eg[ch * C + t], be = ok ? p.beta[h * p.beta_hs + ck.tok0 + t] : 0.0f;
+    const float eg = p.eg[ch * C + t], be = p.be[ch * C + t];
     float cs = 0.0f;
     for (int x = t >> 4; x < 4; ++x) cs += s_row[4][x][t];      // rows of waves below this column's tile
     if (ok) p.gbeta[h * p.gbeta_hs + ck.tok0 + t] = s_db[t] - eg * s[1];
