@@ -302,149 +302,166 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
 }
 
 // ------------------------------------------------------------------ states
-// One workgroup per sequence, head and 16-column slice of dv, over the chunks in order.  The
-// slice of W stays in fp32 accumulators: lane (g, li) of wave w holds W[dv = li][dk = w DK/4 +
-// 16 i + 4 g + r].  Between the products only R, U and the state pass through LDS; tokens and
-// chunk terms go from memory straight into operand registers (each is used once), the next
-// chunk's as soon as this chunk's have been used, so that a chunk waits for no load.
-// Bound by the order of the chunks: three products that depend on one another, each ended by an
-// exchange through LDS.
+// One workgroup per sequence, head and 16-column slice of dv, over the chunks in order.  Its first
+// four waves have the rows of the chunk (wave w rows 16 w ..), the last four the state: lane
+// (g, li) of wave w holds W[dv = li][dk = w DK/4 + 16 i + 4 g + r] in fp32 accumulators.  A chunk
+// is three steps, each ended by an exchange through LDS:
+//   rows: P = K W0^T, R        rows: U = T R        state: W += (el o U)^T K;  rows: O = Q W0^T, A U
+// so two waves share a SIMD and one works while the other waits or loads.  Tokens and chunk terms
+// go from memory straight into operand registers (each is used once), the next chunk's as soon
+// as this chunk's have been used.  Bound by the order of the chunks, and within one by the 64
+// bytes a clock at which a CU takes its operands.
 // BWD writes the states and U that the gradient needs, in place of the outputs.
 template <typename T, int DK, bool BWD>
-__global__ __launch_bounds__(256, 1) void delta_state_kernel(DeltaParams p) {
-  __shared__ __attribute__((aligned(16))) SpTile<T, SL, DK> s_w;
+__global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
+  __shared__ __attribute__((aligned(16))) SpTile<T, SL, DK> s_w[2];
   __shared__ __attribute__((aligned(16))) SpTile<T, SL, C> s_r, s_u, s_ul;
   typedef typename FragOf<T>::type Tok;
   typedef typename Sp<T>::Frag Frag;
   constexpr int NT = DK / 64, NK = DK / 32;
   const int slices = p.dv / SL, item = xcd_item();
   const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
-  const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
+  const int t = threadIdx.x, w = (t >> 6) & 3, l = t & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
   const DeltaSeq sq = p.seqs[b];
-  const int64_t wrow = (((int64_t)b * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
-  f32x4 st[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    st[i] = *reinterpret_cast<const f32x4 *>(p.w + wrow + 16 * i);
-    s_w.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
-  }
-  const int t4 = 16 * w + 4 * g;        // this lane's four rows of every 64 x 16 product
+  const int chunks = (sq.len + C - 1) / C;
+  const int64_t ch0 = (int64_t)sq.chunk0 * p.heads + h, ck0 = (int64_t)sq.chunk0 * p.key_heads + kh;
   const int64_t plane = C * C * 2;
-  const int last_c0 = sq.len > 0 ? (sq.len - 1) / C * C : 0;
-
-  // operands of the chunk at row offset c0
-  Tok kf[NK], qf[BWD ? 1 : NK], ktf[NT][2];
-  Frag tf[2], af[2];
-  T v[4];
-  float ec = 0.0f;
-  f32x4 eg, el, be;
-  const auto load_tokens = [&](int c0) {
-    const int64_t o = ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * (DK * C);
-    const T *K = static_cast<const T *>(p.kp) + o, *Q = static_cast<const T *>(p.qp) + o;
+  if (t < 256) {
+    const int t4 = 16 * w + 4 * g;      // this lane's four rows of every 64 x 16 product
+    Tok kf[NK], qf[BWD ? 1 : NK];
+    Frag tf[2], af[2];
+    T v[4];
+    f32x4 eg, el, be;
+    const auto load_token = [&](const void *tok, int c, int i) {
+      return ld8(static_cast<const T *>(tok) + (ck0 + (int64_t)c * p.key_heads) * (DK * C) + frag_of(w, i, NK));
+    };
+    const auto load_values = [&](int c) {
+      const int64_t o = (ch0 + (int64_t)c * p.heads) * C + t4;
+      eg = *reinterpret_cast<const f32x4 *>(p.eg + o);
+      el = *reinterpret_cast<const f32x4 *>(p.el + o);
+      be = *reinterpret_cast<const f32x4 *>(p.be + o);
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      kf[i] = ld8(K + frag_of(w, i, NK));
-      if (!BWD) qf[i] = ld8(Q + frag_of(w, i, NK));
+      for (int r = 0; r < 4; ++r) {
+        const int x = c * C + t4 + r;
+        const int64_t tk = (int64_t)sq.start + (x < sq.len ? x : sq.len - 1);
+        v[r] = static_cast<const T *>(p.v)[tk * p.ldv + h * p.dv + sl * SL + li];
+      }
+    };
+    const auto load_square = [&](const char *m, int c, Frag (&f)[2]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)       // the second half is above the diagonal for the first two waves
+        if (i == 0 || w >= 2)
+          f[i] = Sp<T>::ld(m + (ch0 + (int64_t)c * p.heads) * split_bytes<T>(C * C), plane, frag_of(w, i, 2));
+    };
+    if (chunks > 0) {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) kf[i] = load_token(p.kp, 0, i);
+      load_values(0);
+      load_square(p.tm, 0, tf);
+      if (!BWD) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) qf[i] = load_token(p.qp, 0, i);
+        load_square(p.am, 0, af);
+      }
     }
-  };
-  const auto load_values = [&](int c0) {
-    const int len = sq.len - c0 < C ? sq.len - c0 : C;
-    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
-    eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + t4);
-    el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + t4);
-    be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + t4);
-    ec = p.eg[ch * C + C - 1];
+    lds_barrier();
+    for (int c = 0; c < chunks; ++c) {
+      const int len = sq.len - c * C < C ? sq.len - c * C : C, nx = c + 1 < chunks ? c + 1 : c;
+      const SpTile<T, SL, DK> &W0 = s_w[BWD ? 0 : c & 1];
+      f32x4 pa[2] = {zero4(), zero4()};
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t tk = (int64_t)sq.start + c0 + (t4 + r < len ? t4 + r : len - 1);
-      v[r] = static_cast<const T *>(p.v)[tk * p.ldv + h * p.dv + sl * SL + li];
+      for (int i = 0; i < NK; ++i) {
+        pa[i & 1] = mm(kf[i], W0.ld(li, 32 * i + 8 * g), pa[i & 1]);
+        kf[i] = load_token(p.kp, nx, i);
+      }
+      f32x4 rr;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        rr[r] = t4 + r < len ? be[r] * (to_f32(v[r]) - eg[r] * (pa[0][r] + pa[1][r])) : 0.0f;
+      const f32x4 eg_now = eg, el_now = el;
+      s_r.st4(li, t4, rr);
+      lds_barrier();
+      load_values(nx);
+      f32x4 u = zero4();
+      u = mm(tf[0], s_r.ld(li, 8 * g), u);
+      if (w >= 2) u = mm(tf[1], s_r.ld(li, 32 + 8 * g), u);
+      s_ul.st4(li, t4, u * el_now);
+      s_u.st4(li, t4, u);
+      load_square(p.tm, nx, tf);
+      lds_barrier();
+      if (BWD) {
+        s_u.copy_t4(0, 16 * w, p.u + (ch0 + (int64_t)c * p.heads) * split_bytes<T>((int64_t)C * p.dv),
+                    (int64_t)C * p.dv * 2, frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
+      } else {
+        f32x4 qa[2] = {zero4(), zero4()};
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          qa[i & 1] = mm(qf[i], W0.ld(li, 32 * i + 8 * g), qa[i & 1]);
+          qf[i] = load_token(p.qp, nx, i);
+        }
+        f32x4 o = (qa[0] + qa[1]) * eg_now * p.scale;
+        o = mm(af[0], s_u.ld(li, 8 * g), o);
+        if (w >= 2) o = mm(af[1], s_u.ld(li, 32 + 8 * g), o);
+        load_square(p.am, nx, af);
+        T *out = static_cast<T *>(p.o) + ((int64_t)sq.start + c * C + t4) * p.ldo + h * p.dv + sl * SL + li;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (t4 + r < len) out[r * p.ldo] = from_f32<T>(o[r]);
+      }
+      lds_barrier();
     }
-  };
-  const auto load_square = [&](const char *m, int c0, Frag (&f)[2]) {
-    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)         // the second half is above the diagonal for the first two waves
-      if (i == 0 || w >= 2) f[i] = Sp<T>::ld(m + ch * split_bytes<T>(C * C), plane, frag_of(w, i, 2));
-  };
-  const auto load_transposed = [&](int c0) {
-    const T *kt = static_cast<const T *>(p.kt) + ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * (DK * C);
+  } else {
+    const int64_t wrow = (((int64_t)b * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
+    f32x4 st[NT];
+    Tok ktf[NT][2];
+    float ec = 0.0f;
+    const auto load_transposed = [&](int c, int i, int x) {
+      return ld8(static_cast<const T *>(p.kt) + (ck0 + (int64_t)c * p.key_heads) * (DK * C) + frag_of(w * NT + i, x, 2));
+    };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      ktf[i][0] = ld8(kt + frag_of(w * NT + i, 0, 2));
-      ktf[i][1] = ld8(kt + frag_of(w * NT + i, 1, 2));
+      st[i] = *reinterpret_cast<const f32x4 *>(p.w + wrow + 16 * i);
+      s_w[0].st4(li, (w * NT + i) * 16 + 4 * g, st[i]);
     }
-  };
-  if (sq.len > 0) {
-    load_tokens(0);
-    load_values(0);
-    load_square(p.tm, 0, tf);
-    if (!BWD) load_square(p.am, 0, af);
-    load_transposed(0);
-  }
-  lds_barrier();
-  for (int c0 = 0; c0 < sq.len; c0 += C) {
-    const int len = sq.len - c0 < C ? sq.len - c0 : C, nx = c0 < last_c0 ? c0 + C : c0;
-    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
-    const int64_t tok0 = sq.start + c0;
-    f32x4 pa = zero4(), pb = zero4(), qa = zero4();
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const Frag wf = s_w.ld(li, 32 * i + 8 * g);
-      if (i & 1) pb = mm(kf[i], wf, pb); else pa = mm(kf[i], wf, pa);
-      if (!BWD) qa = mm(qf[i], wf, qa);
-    }
-    load_tokens(nx);
-    if (BWD) {      // the state before the chunk, dk x dv
-      char *o = p.w0t + ch * split_bytes<T>((int64_t)DK * p.dv);
+    if (chunks > 0) {
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        s_w.copy_t4(0, (w * NT + i) * 16, o, (int64_t)DK * p.dv * 2,
-                    frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
-    }
-    f32x4 rr;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) rr[r] = t4 + r < len ? be[r] * (to_f32(v[r]) - eg[r] * (pa[r] + pb[r])) : 0.0f;
-    const f32x4 eg_now = eg, el_now = el;
-    const float ec_now = ec;
-    load_values(nx);
-    s_r.st4(li, t4, rr);
+        for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(0, i, x);
+      ec = p.eg[ch0 * C + C - 1];
+    }
     lds_barrier();
-    f32x4 u = zero4();
-    u = mm(tf[0], s_r.ld(li, 8 * g), u);
-    if (w >= 2) u = mm(tf[1], s_r.ld(li, 32 + 8 * g), u);
-    load_square(p.tm, nx, tf);
-    s_ul.st4(li, t4, u * el_now);
-    s_u.st4(li, t4, u);
-    lds_barrier();
-    {
+    for (int c = 0; c < chunks; ++c) {
+      const int nx = c + 1 < chunks ? c + 1 : c;
+      if (BWD) {    // the state before the chunk, dk x dv
+        char *o = p.w0t + (ch0 + (int64_t)c * p.heads) * split_bytes<T>((int64_t)DK * p.dv);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          s_w[0].copy_t4(0, (w * NT + i) * 16, o, (int64_t)DK * p.dv * 2,
+                         frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
+      }
+      lds_barrier();
+      lds_barrier();
+      SpTile<T, SL, DK> &W1 = s_w[BWD ? 0 : ~c & 1];
       const Frag u0 = s_ul.ld(li, 8 * g), u1 = s_ul.ld(li, 32 + 8 * g);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        st[i] = mm(ktf[i][0], u0, st[i] * ec_now);
+        st[i] = mm(ktf[i][0], u0, st[i] * ec);
         st[i] = mm(ktf[i][1], u1, st[i]);
-        s_w.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
+        W1.st4(li, (w * NT + i) * 16 + 4 * g, st[i]);
       }
-    }
-    load_transposed(nx);
-    if (BWD) {
-      s_u.copy_t4(0, 16 * w, p.u + ch * split_bytes<T>((int64_t)C * p.dv), (int64_t)C * p.dv * 2,
-                  frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
-    } else {
-      f32x4 o = qa * eg_now * p.scale;
-      o = mm(af[0], s_u.ld(li, 8 * g), o);
-      if (w >= 2) o = mm(af[1], s_u.ld(li, 32 + 8 * g), o);
-      load_square(p.am, nx, af);
+      lds_barrier();
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (t4 + r < len)
-          static_cast<T *>(p.o)[(tok0 + t4 + r) * p.ldo + h * p.dv + sl * SL + li] = from_f32<T>(o[r]);
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(nx, i, x);
+      ec = p.eg[(ch0 + (int64_t)nx * p.heads) * C + C - 1];
     }
-    lds_barrier();
+    if (!BWD)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(p.w_out + wrow + 16 * i) = st[i];
   }
-  if (!BWD)
-#pragma unroll
-    for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(p.w_out + wrow + 16 * i) = st[i];
 }
 
 // ------------------------------------------------------------------ one token
@@ -560,9 +577,9 @@ template <typename T, int DK>
 hipError_t states_impl(const DeltaParams &p, bool backward, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)p.nseq * p.heads * (p.dv / SL)));
   if (backward)
-    hipLaunchKernelGGL((delta_state_kernel<T, DK, true>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_state_kernel<T, DK, true>), grid, dim3(512), 0, s, p);
   else
-    hipLaunchKernelGGL((delta_state_kernel<T, DK, false>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_state_kernel<T, DK, false>), grid, dim3(512), 0, s, p);
   return hipGetLastError();
 }
 
