@@ -26,23 +26,12 @@
 namespace ttt {
 namespace {
 
-
 // Launch-order block -> work item: blocks go round-robin over the 8 XCDs, so
 // item (b % 8) * per + b / 8 puts consecutive items (which share operand rows)
 // on one XCD and its L2.
 __device__ __forceinline__ int64_t xcd_work_item(int64_t total) {
   const int64_t per = (total + 7) >> 3;
   return (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-}
-
-// copy16_to_lds (global_load_lds_dwordx4) issued through inline asm, so that the
-// compiler does not count it: its waits for LDS reads cannot tell which stage a
-// pending copy writes once the copies stay in flight across a loop's back edge, and
-// it then waits for all of them.  The caller waits for these copies itself
-// (s_waitcnt vmcnt) before reading their data.
-__device__ __forceinline__ void copy16_to_lds_untracked(const void *gsrc, unsigned char *lds_wave_base) {
-  const unsigned m0v = (unsigned)(uintptr_t)(__attribute__((address_space(3))) unsigned char *)lds_wave_base;
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(gsrc), "{m0}"(m0v) : "memory");
 }
 
 // ------------------------------------------------------------------ NT tiles

@@ -117,7 +117,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # the raw handle of torch.cuda.current_stream(), without building its object (several us a call)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
@@ -400,43 +401,74 @@ def output_gate(o: torch.Tensor, wg: torch.Tensor, gamma: torch.Tensor, eps: flo
 
 
 # ------------------------------------------------------------------ gated delta rule
-def _here(like: torch.Tensor, **tensors) -> None:
-    """`like` and every given tensor live on the current GPU (the library launches on its current stream)."""
-    if not like.is_cuda or like.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current GPU, got {like.device}")
-    for name, t in tensors.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+# A call of one token takes a few microseconds on the GPU: the checks below ask each tensor for few
+# things, in one expression where all is well, and look for what is wrong only where it is not.
+def _gpu(t: torch.Tensor, name: str) -> int:
+    """The current GPU's index; `t` must live there (the library launches on its current stream)."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current GPU, got {t.device}")
+    return dev
 
 
-def _states(w: torch.Tensor, name: str) -> None:
+def _row(t: torch.Tensor, dtype: torch.dtype, dev: int, n: int, width: int, name: str) -> int:
+    """`t` is [n, >=width] rows of `dtype` on GPU `dev` with unit column stride; returns its row stride."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2 and shape[0] == n and shape[1] >= width and stride[1] == 1 and t.dtype == dtype \
+            and t.get_device() == dev:
+        return stride[0]
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be [{n}, >={width}] with unit column stride, got {tuple(shape)}")
+
+
+def _rate(t: torch.Tensor, H: int, n: int, dev: int) -> int:
+    """Head stride of a rate tensor (as _eta_stride)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2 and shape[0] == H and shape[1] >= n and stride[1] == 1 and t.dtype == torch.float32 \
+            and t.get_device() == dev:
+        return stride[0]
+    return _eta_stride(t, H, n, torch.device("cuda", dev))
+
+
+def _bytes(workspace: torch.Tensor, dev: int) -> int:
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+    return workspace.numel() * workspace.element_size()
+
+
+def _states(w: torch.Tensor, like: Optional[torch.Tensor], name: str) -> None:
     if w.dtype != torch.float32 or w.dim() != 4 or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor [sequences, heads, dv, dk]")
+    if like is not None and (w.shape != like.shape or w.get_device() != like.get_device()):
+        raise ValueError(f"{name} must have w's shape and device")
 
 
-def _delta_args(w, q, k, v, beta, decay, key_heads, scale):
-    """Checks shared by the delta-rule calls: (S, H, Hk, dv, dk, n, row strides, rate strides, scale, dtype code)."""
-    _states(w, "w")
+def _delta_args(w, q, k, v, beta, decay, key_heads):
+    """Checks shared by the delta-rule calls."""
+    _states(w, None, "w")
+    dev = _gpu(w, "w")
     S, H, dv, dk = w.shape
     Hk = H if key_heads is None else int(key_heads)
-    _here(w, q=q, k=k, v=v, beta=beta, decay=decay)
     code = _dtype_code(q)
+    dtype = q.dtype
     if q.dim() != 2:
         raise ValueError("q must be a 2-D tensor of token rows")
     n = q.shape[0]
-    lds = (_same_rows(q, q, n, Hk * dk, "q"), _same_rows(k, q, n, Hk * dk, "k"), _same_rows(v, q, n, H * dv, "v"))
-    bhs = _eta_stride(beta, H, n, w.device)
-    dhs = 0 if decay is None else _eta_stride(decay, H, n, w.device)
-    return S, H, Hk, dv, dk, n, lds, bhs, dhs, (1.0 if scale is None else float(scale)), code
+    return (dev, S, H, Hk, dv, dk, n, code, _row(q, dtype, dev, n, Hk * dk, "q"), _row(k, dtype, dev, n, Hk * dk, "k"),
+            _row(v, dtype, dev, n, H * dv, "v"), _rate(beta, H, n, dev),
+            0 if decay is None else _rate(decay, H, n, dev))
 
 
-def _offsets(cu, sequences: int, device) -> None:
+def _offsets(cu, sequences: int, dev: int) -> None:
     if cu is None:
         if sequences != 1:
             raise ValueError(f"w holds {sequences} states: cu_seqlens is needed for more than one sequence")
-        return
-    if cu.dtype != torch.int32 or tuple(cu.shape) != (sequences + 1,) or not cu.is_contiguous() or cu.device != device:
-        raise ValueError(f"cu_seqlens must be a contiguous int32 tensor [{sequences + 1}] on {device}")
+    elif cu.dtype != torch.int32 or tuple(cu.shape) != (sequences + 1,) or not cu.is_contiguous() \
+            or cu.get_device() != dev:
+        raise ValueError(f"cu_seqlens must be a contiguous int32 tensor [{sequences + 1}] on cuda:{dev}")
 
 
 def delta_workspace_bytes(heads: int, key_heads: int, dk: int, dv: int, n: int, sequences: int, dtype: torch.dtype,
@@ -459,25 +491,24 @@ def delta(w: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, be
     beta and decay (log decay, None: no decay) [H, >=n] or shared [>=n].  ``w_out`` may be ``w`` (in place).
     Rows outside the sequences stay as they are in a given ``out`` and are zero in a new one.
     """
-    S, H, Hk, dv, dk, n, lds, bhs, dhs, scale, code = _delta_args(w, q, k, v, beta, decay, key_heads, scale)
-    _offsets(cu_seqlens, S, w.device)
-    flags = 0
+    dev, S, H, Hk, dv, dk, n, code, ldq, ldk, ldv, bhs, dhs = _delta_args(w, q, k, v, beta, decay, key_heads)
+    _offsets(cu_seqlens, S, dev)
+    flags, ldo = 0, H * dv
     if out is None:
         out = torch.empty((n, H * dv), dtype=q.dtype, device=q.device)
         flags = DELTA_ZERO_UNUSED
-    ldo = _same_rows(out, q, n, H * dv, "out")
+    else:
+        ldo = _row(out, q.dtype, dev, n, H * dv, "out")
     if w_out is None:
         w_out = torch.empty_like(w)
-    _states(w_out, "w_out")
-    if w_out.shape != w.shape or w_out.device != w.device:
-        raise ValueError("w_out must have w's shape and device")
+    else:
+        _states(w_out, w, "w_out")
     if workspace is None:
         workspace = _workspace(delta_workspace_bytes(H, Hk, dk, dv, n, S, q.dtype), w.device)
-    _here(w, workspace=workspace)
-    _check(load().ttt_delta(H, Hk, dk, dv, w.data_ptr(), w_out.data_ptr(), q.data_ptr(), lds[0], k.data_ptr(), lds[1],
-                            v.data_ptr(), lds[2], beta.data_ptr(), bhs, _ptr(decay), dhs, out.data_ptr(), ldo, n,
-                            _ptr(cu_seqlens), S, scale, code, flags, workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), _stream()))
+    _check(load().ttt_delta(H, Hk, dk, dv, w.data_ptr(), w_out.data_ptr(), q.data_ptr(), ldq, k.data_ptr(), ldk,
+                            v.data_ptr(), ldv, beta.data_ptr(), bhs, _ptr(decay), dhs, out.data_ptr(), ldo, n,
+                            _ptr(cu_seqlens), S, 1.0 if scale is None else float(scale), code, flags,
+                            workspace.data_ptr(), _bytes(workspace, dev), _stream()))
     return out, w_out
 
 
@@ -491,37 +522,33 @@ def delta_backward(w: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.T
     ``out`` gives (grad_q, grad_k, grad_v) rows to write to (slices of one buffer, say).  grad_beta and
     grad_decay are [H, n], or [n] for shared rates; grad_decay is None without decay.
     """
-    S, H, Hk, dv, dk, n, lds, bhs, dhs, scale, code = _delta_args(w, q, k, v, beta, decay, key_heads, scale)
-    _offsets(cu_seqlens, S, w.device)
-    ldgo = _same_rows(grad_o, q, n, H * dv, "grad_o")
+    dev, S, H, Hk, dv, dk, n, code, ldq, ldk, ldv, bhs, dhs = _delta_args(w, q, k, v, beta, decay, key_heads)
+    _offsets(cu_seqlens, S, dev)
+    dtype = q.dtype
+    ldgo = _row(grad_o, dtype, dev, n, H * dv, "grad_o")
     if grad_w_out is not None:
-        _states(grad_w_out, "grad_w_out")
-        if grad_w_out.shape != w.shape or grad_w_out.device != w.device:
-            raise ValueError("grad_w_out must have w's shape and device")
+        _states(grad_w_out, w, "grad_w_out")
     if out is None:
-        out = tuple(torch.empty((n, x), dtype=q.dtype, device=q.device) for x in (Hk * dk, Hk * dk, H * dv))
+        out = tuple(torch.empty((n, x), dtype=dtype, device=q.device) for x in (Hk * dk, Hk * dk, H * dv))
     gq, gk, gv = out
-    ldg = (_same_rows(gq, q, n, Hk * dk, "grad_q"), _same_rows(gk, q, n, Hk * dk, "grad_k"),
-           _same_rows(gv, q, n, H * dv, "grad_v"))
-    rate = lambda t: torch.empty((H, n) if t.dim() == 2 else (n,), dtype=torch.float32, device=w.device)
-    gb = rate(beta)
-    gd = None if decay is None else rate(decay)
     # a 2-D rate broadcast over heads (stride 0) still gets a gradient for each head
-    bhs, dhs = (-1 if t is not None and t.dim() == 2 and s == 0 else s for t, s in ((beta, bhs), (decay, dhs)))
-    if bhs < 0:
+    if beta.dim() == 2 and bhs == 0:
         beta, bhs = beta[:, :n].contiguous(), n
-    if dhs < 0:
+    if decay is not None and decay.dim() == 2 and dhs == 0:
         decay, dhs = decay[:, :n].contiguous(), n
+    gb = torch.empty((H, n) if beta.dim() == 2 else (n,), dtype=torch.float32, device=w.device)
+    gd = None if decay is None else torch.empty((H, n) if decay.dim() == 2 else (n,), dtype=torch.float32,
+                                                device=w.device)
     gw = torch.empty_like(w)
     if workspace is None:
-        workspace = _workspace(delta_workspace_bytes(H, Hk, dk, dv, n, S, q.dtype, True), w.device)
-    _here(w, workspace=workspace)
-    _check(load().ttt_delta_backward(H, Hk, dk, dv, w.data_ptr(), q.data_ptr(), lds[0], k.data_ptr(), lds[1],
-                                     v.data_ptr(), lds[2], beta.data_ptr(), bhs, _ptr(decay), dhs, grad_o.data_ptr(),
-                                     ldgo, _ptr(grad_w_out), gq.data_ptr(), ldg[0], gk.data_ptr(), ldg[1],
-                                     gv.data_ptr(), ldg[2], gb.data_ptr(), _ptr(gd), gw.data_ptr(), n,
-                                     _ptr(cu_seqlens), S, scale, code, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream()))
+        workspace = _workspace(delta_workspace_bytes(H, Hk, dk, dv, n, S, dtype, True), w.device)
+    _check(load().ttt_delta_backward(H, Hk, dk, dv, w.data_ptr(), q.data_ptr(), ldq, k.data_ptr(), ldk,
+                                     v.data_ptr(), ldv, beta.data_ptr(), bhs, _ptr(decay), dhs, grad_o.data_ptr(),
+                                     ldgo, _ptr(grad_w_out), gq.data_ptr(), _row(gq, dtype, dev, n, Hk * dk, "grad_q"),
+                                     gk.data_ptr(), _row(gk, dtype, dev, n, Hk * dk, "grad_k"), gv.data_ptr(),
+                                     _row(gv, dtype, dev, n, H * dv, "grad_v"), gb.data_ptr(), _ptr(gd),
+                                     gw.data_ptr(), n, _ptr(cu_seqlens), S, 1.0 if scale is None else float(scale),
+                                     code, workspace.data_ptr(), _bytes(workspace, dev), _stream()))
     return gq, gk, gv, gb, gd, gw
 
 
@@ -534,25 +561,29 @@ def delta_step(w: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     Row i uses state ``slots[i]`` (int32; None: state i).  Slots outside the pool are padding: such rows
     stay as they are in a given ``out`` and are zero in a new one.  Rows of one state apply in row order.
     """
-    S, H, Hk, dv, dk, n, lds, bhs, dhs, scale, code = _delta_args(w, q, k, v, beta, decay, key_heads, scale)
-    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (n,) or not slots.is_contiguous()
-                              or slots.device != w.device):
-        raise ValueError(f"slots must be a contiguous int32 tensor [{n}] on {w.device}")
-    flags = 0
+    dev, S, H, Hk, dv, dk, n, code, ldq, ldk, ldv, bhs, dhs = _delta_args(w, q, k, v, beta, decay, key_heads)
+    if slots is not None and (slots.dtype != torch.int32 or slots.shape != (n,) or not slots.is_contiguous()
+                              or slots.get_device() != dev):
+        raise ValueError(f"slots must be a contiguous int32 tensor [{n}] on cuda:{dev}")
+    flags, ldo = 0, H * dv
     if out is None:
         out = torch.empty((n, H * dv), dtype=q.dtype, device=q.device)
         flags = DELTA_ZERO_UNUSED
-    ldo = _same_rows(out, q, n, H * dv, "out")
-    _check(load().ttt_delta_step(H, Hk, dk, dv, w.data_ptr(), S, _ptr(slots), q.data_ptr(), lds[0], k.data_ptr(),
-                                 lds[1], v.data_ptr(), lds[2], beta.data_ptr(), bhs, _ptr(decay), dhs, out.data_ptr(),
-                                 ldo, n, scale, code, flags, _stream()))
+    else:
+        ldo = _row(out, q.dtype, dev, n, H * dv, "out")
+    _check(load().ttt_delta_step(H, Hk, dk, dv, w.data_ptr(), S, _ptr(slots), q.data_ptr(), ldq, k.data_ptr(), ldk,
+                                 v.data_ptr(), ldv, beta.data_ptr(), bhs, _ptr(decay), dhs, out.data_ptr(), ldo, n,
+                                 1.0 if scale is None else float(scale), code, flags, _stream()))
     return out
 
 
 # ------------------------------------------------------------------ gated residual tail
-def _channel(t: Optional[torch.Tensor], C: int, name: str) -> None:
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (C,) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous float32 [{C}] tensor")
+def _channel(t: Optional[torch.Tensor], C: int, dev: int, name: str) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.shape != (C,) or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous float32 [{C}] tensor on cuda:{dev}")
+    return t.data_ptr()
 
 
 def gated_residual(x: torch.Tensor, o: torch.Tensor, z: Optional[torch.Tensor] = None,
@@ -564,26 +595,28 @@ def gated_residual(x: torch.Tensor, o: torch.Tensor, z: Optional[torch.Tensor] =
     The first norm runs over groups of ``norm_width`` channels (default: the row).  z None: no gate;
     gamma or alpha None: 1; gamma_next None: h is None.  ``out`` may be ``x`` (in place).
     """
-    code = _dtype_code(x)
-    _here(x, o=o, z=z, gamma=gamma, alpha=alpha, gamma_next=gamma_next, out=out, h_out=h_out)
+    code, dtype, dev = _dtype_code(x), x.dtype, _gpu(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be a 2-D tensor of rows")
     n, C = x.shape
-    ldx, ldo = _same_rows(x, x, n, C, "x"), _same_rows(o, x, n, C, "o")
-    ldz = 0 if z is None else _same_rows(z, x, n, C, "z")
-    for t, name in ((gamma, "gamma"), (alpha, "alpha"), (gamma_next, "gamma_next")):
-        _channel(t, C, name)
+    ldx, ldo = _row(x, dtype, dev, n, C, "x"), _row(o, dtype, dev, n, C, "o")
+    ldz = 0 if z is None else _row(z, dtype, dev, n, C, "z")
+    gamma, alpha = _channel(gamma, C, dev, "gamma"), _channel(alpha, C, dev, "alpha")
+    gamma_next = _channel(gamma_next, C, dev, "gamma_next")
+    ldy = ldh = C
     if out is None:
-        out = torch.empty((n, C), dtype=x.dtype, device=x.device)
-    ldy = _same_rows(out, x, n, C, "out")
-    if gamma_next is None and h_out is not None:
-        raise ValueError("h_out needs gamma_next")
-    if gamma_next is not None and h_out is None:
-        h_out = torch.empty((n, C), dtype=x.dtype, device=x.device)
-    ldh = 0 if h_out is None else _same_rows(h_out, x, n, C, "h_out")
+        out = torch.empty((n, C), dtype=dtype, device=x.device)
+    else:
+        ldy = _row(out, dtype, dev, n, C, "out")
+    if h_out is not None:
+        if gamma_next is None:
+            raise ValueError("h_out needs gamma_next")
+        ldh = _row(h_out, dtype, dev, n, C, "h_out")
+    elif gamma_next is not None:
+        h_out = torch.empty((n, C), dtype=dtype, device=x.device)
     _check(load().ttt_gated_residual(C, C if norm_width is None else int(norm_width), x.data_ptr(), ldx, o.data_ptr(),
-                                     ldo, _ptr(z), ldz, _ptr(gamma), _ptr(alpha), _ptr(gamma_next), float(eps),
-                                     out.data_ptr(), ldy, _ptr(h_out), ldh, n, code, _stream()))
+                                     ldo, _ptr(z), ldz, gamma, alpha, gamma_next, float(eps), out.data_ptr(), ldy,
+                                     _ptr(h_out), ldh, n, code, _stream()))
     return out, h_out
 
 
@@ -603,26 +636,25 @@ def gated_residual_backward(grad_y: Optional[torch.Tensor], grad_h: Optional[tor
     ``y`` is the forward's output.  grad_y or grad_h None: zero.  The gradients of what was not given
     are None.
     """
-    code = _dtype_code(y)
-    _here(y, grad_y=grad_y, grad_h=grad_h, o=o, z=z, gamma=gamma, alpha=alpha, gamma_next=gamma_next,
-          workspace=workspace)
+    code, dtype, dev = _dtype_code(y), y.dtype, _gpu(y, "y")
     if y.dim() != 2:
         raise ValueError("y must be a 2-D tensor of rows")
     n, C = y.shape
-    ld = lambda t, name: 0 if t is None else _same_rows(t, y, n, C, name)
-    new = lambda like: None if like is None else torch.empty((n, C), dtype=y.dtype, device=y.device)
-    for t, name in ((gamma, "gamma"), (alpha, "alpha"), (gamma_next, "gamma_next")):
-        _channel(t, C, name)
-    gx, go, gz = new(y), new(o), new(z)
-    row = lambda like: None if like is None else torch.empty(C, dtype=torch.float32, device=y.device)
-    gg, ga, gn = row(gamma), row(alpha), row(gamma_next)
+    ld = lambda t, name: 0 if t is None else _row(t, dtype, dev, n, C, name)
+    ldgy, ldgh, ldy = ld(grad_y, "grad_y"), ld(grad_h, "grad_h"), ld(y, "y")
+    ldo, ldz = _row(o, dtype, dev, n, C, "o"), ld(z, "z")
+    given = gamma is not None, alpha is not None, gamma_next is not None
+    gamma, alpha = _channel(gamma, C, dev, "gamma"), _channel(alpha, C, dev, "alpha")
+    gamma_next = _channel(gamma_next, C, dev, "gamma_next")
+    gx, go = torch.empty((n, C), dtype=dtype, device=y.device), torch.empty((n, C), dtype=dtype, device=y.device)
+    gz = None if z is None else torch.empty((n, C), dtype=dtype, device=y.device)
+    gg, ga, gn = (torch.empty(C, dtype=torch.float32, device=y.device) if g else None for g in given)
     if workspace is None:
         workspace = _workspace(gated_residual_backward_workspace_bytes(C, n), y.device)
     _check(load().ttt_gated_residual_backward(
-        C, C if norm_width is None else int(norm_width), _ptr(grad_y), ld(grad_y, "grad_y"), _ptr(grad_h),
-        ld(grad_h, "grad_h"), y.data_ptr(), ld(y, "y"), o.data_ptr(), ld(o, "o"), _ptr(z), ld(z, "z"), _ptr(gamma),
-        _ptr(alpha), _ptr(gamma_next), float(eps), gx.data_ptr(), C, go.data_ptr(), C, _ptr(gz), C, _ptr(gg), _ptr(ga),
-        _ptr(gn), n, code, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream()))
+        C, C if norm_width is None else int(norm_width), _ptr(grad_y), ldgy, _ptr(grad_h), ldgh, y.data_ptr(), ldy,
+        o.data_ptr(), ldo, _ptr(z), ldz, gamma, alpha, gamma_next, float(eps), gx.data_ptr(), C, go.data_ptr(), C,
+        _ptr(gz), C, _ptr(gg), _ptr(ga), _ptr(gn), n, code, workspace.data_ptr(), _bytes(workspace, dev), _stream()))
     return gx, go, gz, gg, ga, gn
 
 
@@ -640,21 +672,21 @@ def orthogonalise(g: torch.Tensor, steps: int = 5, out: Optional[torch.Tensor] =
 
     ``out`` may be ``g`` (in place).
     """
-    code = _dtype_code(g)
-    _here(g, out=out, workspace=workspace)
+    code, dev = _dtype_code(g), _gpu(g, "g")
     if out is None:
         out = torch.empty(g.shape, dtype=g.dtype, device=g.device)
     for t, name in ((g, "g"), (out, "out")):
-        if t.dim() not in (2, 3) or t.stride(-1) != 1 or t.dtype != g.dtype or t.shape != g.shape:
-            raise ValueError(f"{name} must be [rows, cols] or [batch, rows, cols] of one dtype with unit column stride")
+        if t.dim() not in (2, 3) or t.stride(-1) != 1 or t.dtype != g.dtype or t.shape != g.shape \
+                or t.get_device() != dev:
+            raise ValueError(f"{name} must be [rows, cols] or [batch, rows, cols] of one dtype and device with unit "
+                             f"column stride")
     B, R, C = (1, *g.shape) if g.dim() == 2 else g.shape
     bs = lambda t: t.stride(0) if t.dim() == 3 else 0
     if workspace is None:
         workspace = _workspace(orthogonalise_workspace_bytes(R, C, B, g.dtype), g.device)
     _check(load().ttt_orthogonalise(R, C, B, g.data_ptr(), g.stride(-2), bs(g), out.data_ptr(), out.stride(-2), bs(out),
                                     int(steps), code, _ptr(workspace),
-                                    0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                    _stream()))
+                                    0 if workspace is None else _bytes(workspace, dev), _stream()))
     return out
 
 
