@@ -17,58 +17,81 @@
 namespace ttt {
 namespace {
 
-constexpr int KS = 32;              // reduction elements a stage: 64-byte rows in LDS
+constexpr int KS = 32;              // reduction elements a stage
 
-struct Mat {                        // split matrix: `parts` planes of [rows][ld], one after another
+// Split matrix: one plane a part.  A plane is cut in fragments of 16 rows x 32 columns, 1 KB each in
+// the order in which lanes take them (lane = 16 (column / 8 % 4) + row % 16, eight columns a lane),
+// the nrt fragments of 32 columns one after another: a stage's panel is one piece of memory.  (With
+// plain rows a copy of 16 rows meets one channel of the L2 where the row length is a power of two:
+// 93 against 91 us for the symmetric
+// products of four 1024 x 4096 matrices, 64 x 64 tiles of 512-wide ones 13.7 against 11.9.)
+struct Mat {
   char *p;
   int64_t plane, bs;                // bytes from plane to plane, from matrix to matrix
-  int ld;
+  int nrt;                          // fragments of rows
 };
+__device__ __forceinline__ int64_t frag_byte(const Mat &m, int rt, int kt) { return ((int64_t)kt * m.nrt + rt) * 1024; }
 
-template <int P> __device__ __forceinline__ void put4(char *p, int64_t plane, int64_t e, f32x4 v) {
+// Eight values as one lane's piece of a fragment, part by part.
+template <int P> __device__ __forceinline__ void put8(char *p, int64_t plane, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    bf16x4 h;
+    bf16x8 h;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < 8; ++r) {
       h[r] = (__bf16)v[r];
       v[r] -= (float)h[r];
     }
-    *reinterpret_cast<bf16x4 *>(reinterpret_cast<__bf16 *>(p + i * plane) + e) = h;
+    *reinterpret_cast<bf16x8 *>(p + i * plane) = h;
   }
 }
-template <int P> __device__ __forceinline__ f32x4 get4(const char *p, int64_t plane, int64_t e) {
+// Elements (row, col .. col + 3), col % 4 == 0.
+template <int P> __device__ __forceinline__ f32x4 get4(const Mat &m, int64_t base, int row, int col) {
+  const char *p = m.p + base + frag_byte(m, row >> 4, col >> 5) + (((col >> 3) & 3) * 16 + (row & 15)) * 16 + (col & 7) * 2;
   f32x4 v = f32x4{0, 0, 0, 0};
 #pragma unroll
   for (int i = P - 1; i >= 0; --i) {
-    const bf16x4 h = *reinterpret_cast<const bf16x4 *>(reinterpret_cast<const __bf16 *>(p + i * plane) + e);
+    const bf16x4 h = *reinterpret_cast<const bf16x4 *>(p + i * m.plane);
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] += (float)h[r];
   }
   return v;
 }
 
-// Partial sums of squares, in 64 bits: block x of matrix y.
-template <typename T>
+// Partial sums of squares, in 64 bits: block x of matrix y, V elements (a 16-byte piece, or one) a load.
+template <typename T, int V>
 __global__ __launch_bounds__(256) void orth_norm_kernel(OrthParams p, double *part) {
   __shared__ double red[4];
   const T *g = static_cast<const T *>(p.g) + (int64_t)blockIdx.y * p.bsg;
-  // thread e, e + step, ..: row and column move by a fixed amount, with a carry
-  const int64_t step = (int64_t)gridDim.x * 256, e0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int cols = p.plan.cols, dr = (int)(step / cols), dc = (int)(step % cols);
-  int64_t r = e0 / cols;
-  int c = (int)(e0 % cols);
+  // thread e, e + step, ..: row and piece move by a fixed amount, with a carry
+  const unsigned step = gridDim.x * 256, e0 = blockIdx.x * 256 + threadIdx.x, np = p.plan.cols / V;
+  const unsigned dr = step / np, dc = step % np, rows = p.plan.rows;
+  unsigned r = e0 / np, c = e0 % np;
   double s = 0.0;
-  while (r < p.plan.rows) {
-    float x[8];
+  while (r < rows) {
+    float x[4][V];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = r < p.plan.rows ? to_f32(g[r * p.ldg + c]) : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      const T *at = g + (int64_t)r * p.ldg + c * V;
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[i][k] = 0.0f;
+      if (r < rows) {
+        if constexpr (V == 1) {
+          x[i][0] = to_f32(*at);
+        } else {
+          typedef T piece __attribute__((ext_vector_type(V)));
+          const piece v = *reinterpret_cast<const piece *>(at);
+#pragma unroll
+          for (int k = 0; k < V; ++k) x[i][k] = (float)v[k];
+        }
+      }
       r += dr, c += dc;
-      if (c >= cols) c -= cols, ++r;
+      if (c >= np) c -= np, ++r;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += (double)x[i] * (double)x[i];
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) s += (double)x[i][k] * (double)x[i][k];
   }
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
@@ -92,29 +115,30 @@ __global__ __launch_bounds__(256) void orth_load_kernel(OrthParams p, const doub
   __shared__ float tile[64][65];
   const OrthPlan &q = p.plan;
   const int b = blockIdx.z;
-  const float scale = orth_scale(p, part, b);
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tx = (threadIdx.x & 15) * 4, ty = threadIdx.x >> 4;
+  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tx = threadIdx.x & 63, w = threadIdx.x >> 6;
   const T *g = static_cast<const T *>(p.g) + b * p.bsg;
-  const Mat &m = q.tall ? xt : x, &mt = q.tall ? x : xt;      // G's own layout, and its transpose
+  float in[16];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + ty + 16 * i;
-    f32x4 v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int c = c0 + tx + e;
-      v[e] = r < q.rows && c < q.cols ? to_f32(g[(int64_t)r * p.ldg + c]) * scale : 0.0f;
-      tile[ty + 16 * i][tx + e] = v[e];
-    }
-    put4<P>(m.p + b * m.bs, m.plane, (int64_t)r * m.ld + c0 + tx, v);
+  for (int i = 0; i < 16; ++i) {
+    const int r = r0 + w + 4 * i, c = c0 + tx;
+    in[i] = r < q.rows && c < q.cols ? to_f32(g[(int64_t)r * p.ldg + c]) : 0.0f;
   }
+  const float scale = orth_scale(p, part, b);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) tile[w + 4 * i][tx] = in[i] * scale;
   __syncthreads();
+  const Mat &m = q.tall ? xt : x, &mt = q.tall ? x : xt;      // G's own layout, and its transpose
+  const int gr = tx >> 4, li = tx & 15;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f32x4 v;
+  for (int k = 0; k < 2; ++k) {                               // wave w: fragment rows w
+    float v[8], u[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = tile[tx + e][ty + 16 * i];
-    put4<P>(mt.p + b * mt.bs, mt.plane, (int64_t)(c0 + ty + 16 * i) * mt.ld + r0 + tx, v);
+    for (int e = 0; e < 8; ++e) {
+      v[e] = tile[16 * w + li][32 * k + 8 * gr + e];
+      u[e] = tile[32 * k + 8 * gr + e][16 * w + li];
+    }
+    put8<P>(m.p + b * m.bs + frag_byte(m, r0 / 16 + w, c0 / 32 + k) + tx * 16, m.plane, v);
+    put8<P>(mt.p + b * mt.bs + frag_byte(mt, c0 / 16 + w, r0 / 32 + k) + tx * 16, mt.plane, u);
   }
 }
 
@@ -131,14 +155,16 @@ struct Product {
 // Both operands pass through LDS once a stage; a wave's fragment reads against its MFMAs fall
 // with the wave tile, which sets the sizes (reads and copies share the LDS with 128 bytes a clock,
 // 16 clocks an MFMA and SIMD): 256 x 256 where such tiles fill the card, 128 x 128 where those do,
-// else 64 x 64.
+// else 64 x 64.  Two waves share a SIMD (of one workgroup, or of two 64 x 64 ones on a CU), so that one's
+// reads fall on the other's products; reading a stage ahead into registers instead, with a wave a SIMD,
+// was slower (112 against 84 us for the symmetric products of four 1024 x 4096 matrices).
 template <int TM_, int TN_, int WR_, int WC_, int NST_> struct Geo {
   static constexpr int TM = TM_, TN = TN_, WR = WR_, WC = WC_, NST = NST_, kThreads = WR * WC * 64;
   static constexpr int WM = TM / WR, WN = TN / WC, FM = WM / 16, FN = WN / 16;
 };
 template <int TILE, int P> struct GeoOf;
-template <int P> struct GeoOf<64, P> { typedef Geo<64, 64, 2, 2, P == 2 ? 4 : 3> type; };
-template <int P> struct GeoOf<128, P> { typedef Geo<128, 128, 2, 2, P == 2 ? 4 : 3> type; };
+template <int P> struct GeoOf<64, P> { typedef Geo<64, 64, 2, 2, P == 2 ? 5 : 3> type; };
+template <int P> struct GeoOf<128, P> { typedef Geo<128, 128, 4, 2, P == 2 ? 4 : 3> type; };
 template <> struct GeoOf<256, 2> { typedef Geo<256, 256, 4, 2, 2> type; };
 template <> struct GeoOf<256, 3> { typedef Geo<256, 128, 4, 2, 2> type; };
 
@@ -162,23 +188,21 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
   } else {
     bi = e % q.ti, bj = e / q.ti;
   }
-  const char *pp = q.P.p + b * q.P.bs + (int64_t)bi * G::TM * q.P.ld * 2;
-  const char *pq = q.Q.p + b * q.Q.bs + (int64_t)bj * G::TN * q.Q.ld * 2;
-  // A stage holds, part by part, the rows of the P panel, then those of the Q panel.  A copy is 16
-  // rows of 64 bytes: lane = 4 * row + position, and the piece at position a is chunk a ^ swz_64(row).
-  const int cr = l >> 2, cc = ((l & 3) ^ swz_64(cr)) * 16;
+  // A stage holds, part by part, the fragments of the P panel, then those of the Q panel.
   const char *src[PPW];
+  int64_t step_bytes[2] = {(int64_t)q.P.nrt * 1024, (int64_t)q.Q.nrt * 1024};
 #pragma unroll
   for (int x = 0; x < PPW; ++x) {
-    const int row = (w * PPW + x) * 16;           // of the stage
-    const bool second = row >= G::TM * P;
-    const int r = second ? row - G::TM * P : row, rows = second ? G::TN : G::TM;
+    const int f = w * PPW + x;                    // fragment of the stage
+    const bool second = f >= G::TM / 16 * P;
+    const int r = second ? f - G::TM / 16 * P : f, nf = second ? G::TN / 16 : G::TM / 16;
     const Mat &m = second ? q.Q : q.P;
-    src[x] = (second ? pq : pp) + (r / rows) * m.plane + (int64_t)(r % rows + cr) * m.ld * 2 + cc;
+    src[x] = m.p + b * m.bs + r / nf * m.plane + frag_byte(m, (second ? bj : bi) * nf + r % nf, 0) + l * 16;
   }
   const int nk = q.K / KS;
   const auto copy = [&](int x, int kc) {
-    copy16_to_lds_untracked(src[x] + kc * (KS * 2), s + kc % G::NST * kStage + (w * PPW + x) * 1024);
+    const bool second = w * PPW + x >= G::TM / 16 * P;
+    copy16_to_lds_untracked(src[x] + kc * step_bytes[second], s + kc % G::NST * kStage + (w * PPW + x) * 1024);
   };
   f32x4 acc[G::FM][G::FN];
 #pragma unroll
@@ -186,55 +210,58 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   const int wi = (w / G::WC) * G::WM, wj = (w % G::WC) * G::WN;
-  const int fo = li * 64 + ((g ^ swz_64(li)) * 16);
 #pragma unroll
   for (int k = 0; k < G::NST - 1; ++k)
     if (k < nk)
 #pragma unroll
       for (int x = 0; x < PPW; ++x) copy(x, k);
+  const auto read = [&](const unsigned char *st, int row) {     // the fragment of a stage's row
+    return *reinterpret_cast<const bf16x8 *>(st + row * 64 + l * 16);
+  };
+  // products with the fragments of one column tile, the small ones first
+  const auto products = [&](int j, const bf16x8 (&fa)[G::FM][P], const bf16x8 (&fb)[P]) {
+#pragma unroll
+    for (int d = P - 1; d >= 0; --d)
+#pragma unroll
+      for (int x = 0; x <= d; ++x)
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) acc[i][j] = mma(fb[d - x], fa[i][x], acc[i][j]);
+  };
   for (int kc = 0; kc < nk; ++kc) {
     // this wave's copies of stage kc have arrived (those of the NST - 2 stages after it may be in flight)
     if (kc + G::NST - 2 < nk) wait_vmcnt<(G::NST - 2) * PPW>(); else wait_vmcnt<0>();
-    bare_barrier();                               // everyone's have, and the stage before is free
+    bare_barrier();                             // everyone's have, and the stage before is free
     const unsigned char *st = s + kc % G::NST * kStage;
     const bool more = kc + G::NST - 1 < nk;
     bf16x8 fa[G::FM][P], fb[2][P];
-    const auto read_b = [&](int j, bf16x8 (&f)[P]) {
 #pragma unroll
-      for (int x = 0; x < P; ++x)
-        f[x] = *reinterpret_cast<const bf16x8 *>(st + ((G::TM * P + x * G::TN + wj + 16 * j) * 64 + fo));
-    };
+    for (int x = 0; x < P; ++x) {
 #pragma unroll
-    for (int i = 0; i < G::FM; ++i)
-#pragma unroll
-      for (int x = 0; x < P; ++x) fa[i][x] = *reinterpret_cast<const bf16x8 *>(st + ((x * G::TM + wi + 16 * i) * 64 + fo));
-    read_b(0, fb[0]);
+      for (int i = 0; i < G::FM; ++i) fa[i][x] = read(st, x * G::TM + wi + 16 * i);
+      fb[0][x] = read(st, G::TM * P + x * G::TN + wj);
+    }
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) {
-      if (j + 1 < G::FN) read_b(j + 1, fb[(j + 1) & 1]);
+      if (j + 1 < G::FN)
+#pragma unroll
+        for (int x = 0; x < P; ++x) fb[(j + 1) & 1][x] = read(st, G::TM * P + x * G::TN + wj + 16 * (j + 1));
       // the next stage's copies, spread over the products
 #pragma unroll
       for (int x = 0; x < PPW; ++x)
         if (x * G::FN / PPW == j && more) copy(x, kc + G::NST - 1);
-#pragma unroll
-      for (int d = P - 1; d >= 0; --d)            // the small products first
-#pragma unroll
-        for (int x = 0; x <= d; ++x)
-#pragma unroll
-          for (int i = 0; i < G::FM; ++i) acc[i][j] = mma(fb[j & 1][d - x], fa[i][x], acc[i][j]);
+      products(j, fa, fb[j & 1]);
     }
   }
   __syncthreads();                                // the ring is free
   // lane (g, li) holds C[16 i + li][16 j + 4 g + r], r = 0 .. 3, of the wave's tile
   const int r0 = bi * G::TM + wi, c0 = bj * G::TN + wj;
   if constexpr (KIND == kPoly) {
-    const char *pa = q.P.p + b * q.P.bs;
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
 #pragma unroll
       for (int j = 0; j < G::FN; ++j) {
         const int row = r0 + 16 * i + li, col = c0 + 16 * j + 4 * g;
-        const f32x4 a = get4<P>(pa, q.P.plane, (int64_t)row * q.P.ld + col);
+        const f32x4 a = get4<P>(q.P, b * q.P.bs, row, col);
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[i][j][r] = p.c * acc[i][j][r] + (p.b * a[r] + (row == col + r ? p.a : 0.0f));
       }
@@ -272,22 +299,21 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
         }
         *reinterpret_cast<bf16x4 *>(mine + (16 * i + li) * kPitch + (16 * j + 4 * g) * 2) = h;
       }
-    constexpr int RC = G::WN / 8;                 // 16-byte pieces of a row
-    __bf16 *c = reinterpret_cast<__bf16 *>(q.c.p + b * q.c.bs + x * q.c.plane);
+    char *c = q.c.p + b * q.c.bs + x * q.c.plane + l * 16;
 #pragma unroll
-    for (int y = 0; y < G::WM * RC / 64; ++y) {
-      const int u = l + 64 * y, r = u / RC, k = u % RC;
-      *reinterpret_cast<u32x4 *>(c + (int64_t)(r0 + r) * q.c.ld + c0 + 8 * k) =
-          *reinterpret_cast<const u32x4 *>(mine + r * kPitch + 16 * k);
-    }
+    for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+      for (int k = 0; k < G::WN / 32; ++k)        // columns 32 k + 8 g .. + 7 of row 16 i + li
+        *reinterpret_cast<u32x4 *>(c + frag_byte(q.c, r0 / 16 + i, c0 / 32 + k)) =
+            *reinterpret_cast<const u32x4 *>(mine + (16 * i + li) * kPitch + (32 * k + 8 * g) * 2);
     if (both) {
-      __bf16 *ct = reinterpret_cast<__bf16 *>(q.ct.p + b * q.ct.bs + x * q.ct.plane);
+      char *ct = q.ct.p + b * q.ct.bs + x * q.ct.plane + l * 16;
 #pragma unroll
       for (int i = 0; i < G::WM / 32; ++i)
 #pragma unroll
         for (int j = 0; j < G::FN; ++j) {         // rows 32 i + 8 g .. + 7 of column 16 j + li
           const unsigned char *a = mine + (32 * i + 8 * g + (li >> 2)) * kPitch + (16 * j + 4 * (li & 3)) * 2;
-          *reinterpret_cast<bf16x8 *>(ct + (int64_t)(c0 + 16 * j + li) * q.ct.ld + r0 + 32 * i + 8 * g) =
+          *reinterpret_cast<bf16x8 *>(ct + frag_byte(q.ct, c0 / 16 + j, r0 / 32 + i)) =
               cat8(lds_read_tr16(a), lds_read_tr16(a + 4 * kPitch));
         }
     }
@@ -330,10 +356,10 @@ template <typename T, int P> hipError_t steps_of(const OrthParams &p, hipStream_
   const int64_t xb = (int64_t)q.rp * q.cp * 2, ab = (int64_t)q.rp * q.rp * 2;
   Mat x[2], xt[2];
   for (int i = 0; i < 2; ++i) {
-    x[i] = Mat{p.ws + q.off_x[i], xb, xb * P, q.cp};
-    xt[i] = Mat{p.ws + q.off_xt[i], xb, xb * P, q.rp};
+    x[i] = Mat{p.ws + q.off_x[i], xb, xb * P, q.rp / 16};
+    xt[i] = Mat{p.ws + q.off_xt[i], xb, xb * P, q.cp / 16};
   }
-  const Mat A{p.ws + q.off_a, ab, ab * P, q.rp}, B{p.ws + q.off_b, ab, ab * P, q.rp};
+  const Mat A{p.ws + q.off_a, ab, ab * P, q.rp / 16}, B{p.ws + q.off_b, ab, ab * P, q.rp / 16};
   const double *part = reinterpret_cast<const double *>(p.ws + q.off_norm);
   const int pr = q.tall ? q.cp : q.rp, pc = q.tall ? q.rp : q.cp;       // padded sizes of G
   hipLaunchKernelGGL((orth_load_kernel<T, P>), dim3(pc / 64, pr / 64, q.batch), dim3(256), 0, s, p, part, x[0], xt[0]);
@@ -353,7 +379,11 @@ template <typename T, int P> hipError_t steps_of(const OrthParams &p, hipStream_
 template <typename T, int P> hipError_t run_orth(const OrthParams &p, hipStream_t s) {
   const OrthPlan &q = p.plan;
   double *part = reinterpret_cast<double *>(p.ws + q.off_norm);
-  hipLaunchKernelGGL(orth_norm_kernel<T>, dim3(q.norm_blocks, q.batch), dim3(256), 0, s, p, part);
+  constexpr int V = 16 / (int)sizeof(T);
+  if ((uintptr_t)p.g % 16 == 0 && q.cols % V == 0 && p.ldg % V == 0 && p.bsg % V == 0)
+    hipLaunchKernelGGL((orth_norm_kernel<T, V>), dim3(q.norm_blocks, q.batch), dim3(256), 0, s, p, part);
+  else
+    hipLaunchKernelGGL((orth_norm_kernel<T, 1>), dim3(q.norm_blocks, q.batch), dim3(256), 0, s, p, part);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.steps == 0) {
