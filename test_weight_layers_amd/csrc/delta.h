@@ -9,6 +9,8 @@ namespace ttt {
 
 // Tokens per chunk of the chunked form.
 constexpr int kDeltaChunk = 64;
+// Sequences that a wave lays out for itself.
+constexpr int kDeltaLaneSeqs = 63;
 // dv columns of the state that one workgroup of the sequential kernels holds.
 constexpr int kDeltaSlice = 16;
 
@@ -95,6 +97,5 @@ hipError_t launch_delta_step(const DeltaStepParams &p, bool bf16, hipStream_t s)
 hipError_t launch_delta_plan(const DeltaParams &p, hipStream_t s);
 hipError_t launch_delta_chunk(const DeltaParams &p, bool bf16, bool backward, hipStream_t s);
 hipError_t launch_delta_states(const DeltaParams &p, bool bf16, bool backward, hipStream_t s);
-hipError_t launch_delta_zero_rows(const DeltaParams &p, void *rows, int64_t ld, int width, bool bf16, hipStream_t s);
 
 }  // namespace ttt

@@ -12,6 +12,7 @@
 // once (chunk), then the states in order of the chunks, split over heads and 16-column slices of
 // dv, which do not depend on one another (states).
 #include "delta.h"
+#include "delta_layout.h"
 #include "split.h"
 
 namespace ttt {
@@ -21,23 +22,11 @@ constexpr int C = kDeltaChunk;
 constexpr int SL = kDeltaSlice;
 
 // ------------------------------------------------------------------ plan
-// Row offsets -> sequences and chunks.  The running maximum of the clamped offsets makes any
-// offsets into disjoint ranges inside [0, n): nothing is read or written outside the rows.
+// Tables of the sequences and chunks, for more sequences than a wave has lanes.
 __global__ __launch_bounds__(256) void delta_plan_kernel(DeltaParams p) {
   __shared__ int s_a[256], s_b[256];
   const int t = threadIdx.x;
-  if (p.cu == nullptr) {
-    if (t == 0) {
-      p.seqs[0] = DeltaSeq{0, p.n, 0, 0};
-      *p.used = p.n;
-    }
-    for (int c = t; c < p.nchunk; c += 256) {
-      const int t0 = c * C;
-      p.chunks[c] = DeltaChunk{t0, p.n - t0 < C ? p.n - t0 : C, 0, 0};
-    }
-    return;
-  }
-  auto off = [&](int i) { const int x = p.cu[i]; return x < 0 ? 0 : (x > p.n ? p.n : x); };
+  const auto off = [&](int i) { return delta_offset(p, i); };
   int carry_max = off(0), carry_chunks = 0;
   for (int b0 = 0; b0 < p.nseq; b0 += 256) {
     const int b = b0 + t;
@@ -87,41 +76,78 @@ __global__ __launch_bounds__(256) void delta_plan_kernel(DeltaParams p) {
   }
 }
 
-// Zeros in the rows behind the last sequence (and before the first).
+// Zeros in the rows before the first sequence and behind the last: rows [n][ld] of `width`.
 template <typename T>
-__global__ __launch_bounds__(256) void delta_zero_rows_kernel(DeltaParams p, T *rows, int64_t ld, int width) {
-  const int first = p.nseq > 0 ? p.seqs[0].start : 0, used = *p.used;
-  const int total = first + (p.n - used);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)total * width; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / width, row = r < first ? r : used + (r - first);
-    rows[row * ld + i % width] = from_f32<T>(0.0f);
+__device__ void zero_rows(const DeltaParams &p, int2 used, void *rows, int64_t ld, int width, int block, int blocks) {
+  const int total = used.x + (p.n - used.y);
+  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < (int64_t)total * width; i += (int64_t)blocks * 256) {
+    const int64_t r = i / width, row = r < used.x ? r : used.y + (r - used.x);
+    static_cast<T *>(rows)[row * ld + i % width] = from_f32<T>(0.0f);
   }
 }
+constexpr int kZeroBlocks = 64;     // workgroups of the chunk kernel's launch that write those zeros
 
 // ------------------------------------------------------------------ chunk terms
 // One workgroup per chunk and head: e^gamma, T = (I + L)^-1 by block substitution in fp32 and A,
 // and (once per key head) the tokens and their transposes in fragment order.
 // Substitution, not products of powers of L: those grow without bound where keys repeat.
 template <typename T, int DK, bool BWD>
-__global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
+__global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaParams p) {
   constexpr int kPitch = DK + Sp<T>::kPad, NK = DK / 32, kA = C + 4;
   constexpr int kTokBytes = C * kPitch * (int)sizeof(T), kABytes = C * kA * 4;
   __shared__ __attribute__((aligned(16))) unsigned char s_raw[kTokBytes > kABytes ? kTokBytes : kABytes];
   __shared__ double s_gam[C];
   __shared__ float s_beta[C];
-  __shared__ __attribute__((aligned(16))) float s_l[C][kA], s_t[C][kA];
-  __shared__ float s_x[32][33];
+  __shared__ __attribute__((aligned(16))) float s_l[C][kA], s_t[C][kA], s_x[32][36];
   typedef typename FragOf<T>::type Tok;
   T *s_tok = reinterpret_cast<T *>(s_raw);              // [64][kPitch]
   float *s_a = reinterpret_cast<float *>(s_raw);        // [64][kA], after the tokens
-  const int item = xcd_item(), h = item % p.heads, c = item / p.heads;
-  const DeltaChunk ck = p.chunks[c];
+  const int items = p.nchunk * p.heads;
+  if ((int)blockIdx.x >= items) {                       // rows of no sequence
+    const int blk = blockIdx.x - items;
+    const int2 used = rows_of(p);
+    if (!BWD) {
+      zero_rows<T>(p, used, p.o, p.ldo, p.heads * p.dv, blk, kZeroBlocks);
+      return;
+    }
+    zero_rows<T>(p, used, p.gq, p.ldgq, p.key_heads * DK, blk, kZeroBlocks);
+    zero_rows<T>(p, used, p.gk, p.ldgk, p.key_heads * DK, blk, kZeroBlocks);
+    zero_rows<T>(p, used, p.gv, p.ldgv, p.heads * p.dv, blk, kZeroBlocks);
+    for (int h = blk; h < p.heads; h += kZeroBlocks) {
+      zero_rows<float>(p, used, p.gbeta + h * p.gbeta_hs, 1, 1, 0, 1);
+      if (p.gdecay) zero_rows<float>(p, used, p.gdecay + h * p.gdecay_hs, 1, 1, 0, 1);
+    }
+    return;
+  }
+  const int item = items % 8 == 0 ? (blockIdx.x & 7) * (items >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+  const int h = item % p.heads, c = item / p.heads;
+  const DeltaChunk ck = chunk_of(p, c);
   if (ck.len == 0) return;
   const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
   const int grp = p.heads / p.key_heads, kh = h / grp;
   const bool writer = h % grp == 0;                     // of the key head's operands
   const int64_t ch = (int64_t)c * p.heads + h;
   const int64_t tokens = ((int64_t)c * p.key_heads + kh) * (DK * C);
+  constexpr int V = 16 / (int)sizeof(T), NP = C * DK / V / 256;      // 16-byte pieces: elements, and a thread's
+  const auto fetch = [&](const void *src, int64_t ld, u32x4 (&x)[NP]) {
+    const T *b = static_cast<const T *>(src) + (int64_t)ck.tok0 * ld + kh * DK;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int e = t + 256 * i, r = e / (DK / V), col = e % (DK / V) * V;
+      x[i] = u32x4{0, 0, 0, 0};                         // rows past the chunk are zero
+      if (r < ck.len) x[i] = *reinterpret_cast<const u32x4 *>(b + r * ld + col);
+    }
+  };
+  const auto stage = [&](const u32x4 (&x)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int e = t + 256 * i, r = e / (DK / V), col = e % (DK / V) * V;
+      *reinterpret_cast<u32x4 *>(s_tok + r * kPitch + col) = x[i];
+    }
+  };
+  u32x4 xq[NP], xk[NP];
+  fetch(p.q, p.ldq, xq);
+  fetch(p.k, p.ldk, xk);
   if (t < C) {
     const bool ok = t < ck.len;
     double gam = 0.0;
@@ -141,17 +167,6 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
     p.eg[ch * C + t] = exp_of(gam);
     p.el[ch * C + t] = exp_of(__shfl(gam, 63) - gam);
   }
-  constexpr int V = 16 / (int)sizeof(T);                // elements of a 16-byte piece
-  const auto stage = [&](const T *src, int64_t ld) {    // rows past the chunk are zero
-    const T *x = src + (int64_t)ck.tok0 * ld + kh * DK;
-#pragma unroll
-    for (int i = 0; i < C * DK / V / 256; ++i) {
-      const int e = t + 256 * i, r = e / (DK / V), col = e % (DK / V) * V;
-      u32x4 v = u32x4{0, 0, 0, 0};
-      if (r < ck.len) v = *reinterpret_cast<const u32x4 *>(x + r * ld + col);
-      *reinterpret_cast<u32x4 *>(s_tok + r * kPitch + col) = v;
-    }
-  };
   // the transposed operand: row = column of the tokens, k = token
   const auto write_transposed = [&](T *dst) {
 #pragma unroll
@@ -172,7 +187,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
       }
     }
   };
-  stage(static_cast<const T *>(p.q), p.ldq);
+  stage(xq);
   __syncthreads();
   Tok qa[NK];                                           // wave w has rows 16 w .. 16 w + 15
 #pragma unroll
@@ -182,7 +197,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
   }
   if (BWD && writer) write_transposed(static_cast<T *>(p.qt));
   __syncthreads();
-  stage(static_cast<const T *>(p.k), p.ldk);
+  stage(xk);
   __syncthreads();
   f32x4 kk[4], qk[4];                                   // K K^T and Q K^T, four column tiles
 #pragma unroll
@@ -211,65 +226,68 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaParams p) {
       const bool in = row < ck.len && col <= row;
       s_l[row][col] = in && col < row ? s_beta[row] * d * kk[j][r] : 0.0f;
       s_a[row * kA + col] = in ? p.scale * d * qk[j][r] : 0.0f;
+      s_t[row][col] = 0.0f;
     }
   }
   __syncthreads();
-  // T = (I + L)^-1.  Diagonal 16 x 16 blocks: wave w has block w, one column a lane.
-  if (li == l) {
+  // T = (I + L)^-1.  Diagonal 16 x 16 blocks: wave w has block w, one column a lane (four lanes alike).
+  {
     float x[16];
     const int o = 16 * w;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float v = i == li ? 1.0f : 0.0f;
+      f32x4 row[4];
 #pragma unroll
-      for (int m = 0; m < i; ++m) v -= s_l[o + i][o + m] * x[m];
-      x[i] = v;
+      for (int m = 0; m < (i + 3) / 4; ++m) row[m] = *reinterpret_cast<const f32x4 *>(&s_l[o + i][o + 4 * m]);
+      float v = i == li ? 1.0f : 0.0f, u = 0.0f;        // two sums: half the chain
+#pragma unroll
+      for (int m = 0; m < i; ++m) {
+        if (m & 1) u -= row[m >> 2][m & 3] * x[m];
+        else v -= row[m >> 2][m & 3] * x[m];
+      }
+      x[i] = u + v;
     }
+    if (g == 0)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s_t[o + i][o + li] = x[i];
-  }
-  for (int e = t; e < 16 * 48; e += 256) {              // zero above the diagonal blocks
-    const int r = e / 48, x = e % 48;
-    s_t[r][16 + x] = 0.0f;
-    if (x < 32) s_t[16 + r][32 + x] = 0.0f;
-    if (x < 16) s_t[32 + r][48 + x] = 0.0f;
+      for (int i = 0; i < 16; ++i) s_t[o + i][o + li] = x[i];
   }
   __syncthreads();
-  // below-diagonal blocks: T21 = -T22 (L21 T11), first 16-wide (two pairs), then 32-wide
+  // Blocks below the diagonal: T21 = -T22 (L21 T11), first 16 wide (two pairs, waves 0 and 1), then
+  // 32 wide (four 16 x 16 tiles, one a wave), on fp32 MFMA.
+  const auto tile = [&](const float *a, int lda, const float *b, int ldb, int k) {      // 16 x 16, k = 16 or 32
+    f32x4 s = zero4();
+    const int n = k / 4;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int o = 32 * q, r = t >> 4, x = t & 15;
-    float v = 0.0f;
+    for (int i = 0; i < 8; ++i)
+      if (i < n)      // reduction elements n g .. n g + n - 1 of lane group g
+        s = __builtin_amdgcn_mfma_f32_16x16x4f32(a[li * lda + n * g + i], b[(n * g + i) * ldb + li], s, 0, 0, 0);
+    return s;
+  };
+  if (w < 2) {
+    const int o = 32 * w;
+    const f32x4 s = tile(&s_l[o + 16][o], kA, &s_t[o][o], kA, 16);
 #pragma unroll
-    for (int m = 0; m < 16; ++m) v += s_l[o + 16 + r][o + m] * s_t[o + m][o + x];
-    s_x[16 * q + r][x] = v;
+    for (int r = 0; r < 4; ++r) s_x[16 * w + 4 * g + r][li] = s[r];
   }
   __syncthreads();
+  if (w < 2) {
+    const int o = 32 * w;
+    const f32x4 s = tile(&s_t[o + 16][o + 16], kA, &s_x[16 * w][0], 36, 16);
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int o = 32 * q, r = t >> 4, x = t & 15;
-    float v = 0.0f;
-#pragma unroll
-    for (int m = 0; m < 16; ++m) v += s_t[o + 16 + r][o + 16 + m] * s_x[16 * q + m][x];
-    s_t[o + 16 + r][o + x] = -v;
+    for (int r = 0; r < 4; ++r) s_t[o + 16 + 4 * g + r][o + li] = -s[r];
   }
   __syncthreads();
+  const int ti = 16 * (w >> 1), tj = 16 * (w & 1);
+  {
+    const f32x4 s = tile(&s_l[32 + ti][0], kA, &s_t[0][tj], kA, 32);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = t + 256 * q, r = e >> 5, x = e & 31;
-    float v = 0.0f;
-#pragma unroll
-    for (int m = 0; m < 32; ++m) v += s_l[32 + r][m] * s_t[m][x];
-    s_x[r][x] = v;
+    for (int r = 0; r < 4; ++r) s_x[ti + 4 * g + r][tj + li] = s[r];
   }
   __syncthreads();
+  {
+    const f32x4 s = tile(&s_t[32 + ti][32], kA, &s_x[0][tj], 36, 32);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = t + 256 * q, r = e >> 5, x = e & 31;
-    float v = 0.0f;
-#pragma unroll
-    for (int m = 0; m < 32; ++m) v += s_t[32 + r][32 + m] * s_x[m][x];
-    s_t[32 + r][x] = -v;
+    for (int r = 0; r < 4; ++r) s_t[32 + ti + 4 * g + r][tj + li] = -s[r];
   }
   __syncthreads();
   const int64_t mat = ch * split_bytes<T>(C * C), plane = C * C * 2;
@@ -323,7 +341,7 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
   const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
   const int t = threadIdx.x, w = (t >> 6) & 3, l = t & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
-  const DeltaSeq sq = p.seqs[b];
+  const DeltaSeq sq = seq_of(p, b);
   const int chunks = (sq.len + C - 1) / C;
   const int64_t ch0 = (int64_t)sq.chunk0 * p.heads + h, ck0 = (int64_t)sq.chunk0 * p.key_heads + kh;
   const int64_t plane = C * C * 2;
@@ -369,16 +387,15 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
     for (int c = 0; c < chunks; ++c) {
       const int len = sq.len - c * C < C ? sq.len - c * C : C, nx = c + 1 < chunks ? c + 1 : c;
       const SpTile<T, SL, DK> &W0 = s_w[BWD ? 0 : c & 1];
-      f32x4 pa[2] = {zero4(), zero4()};
+      Sums<T> pa[2];
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
-        pa[i & 1] = mm(kf[i], W0.ld(li, 32 * i + 8 * g), pa[i & 1]);
+        pa[i & 1].add(kf[i], W0.ld(li, 32 * i + 8 * g));
         kf[i] = load_token(p.kp, nx, i);
       }
-      f32x4 rr;
+      f32x4 rr = pa[0].sum() + pa[1].sum();
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        rr[r] = t4 + r < len ? be[r] * (to_f32(v[r]) - eg[r] * (pa[0][r] + pa[1][r])) : 0.0f;
+      for (int r = 0; r < 4; ++r) rr[r] = t4 + r < len ? be[r] * (to_f32(v[r]) - eg[r] * rr[r]) : 0.0f;
       const f32x4 eg_now = eg, el_now = el;
       s_r.st4(li, t4, rr);
       lds_barrier();
@@ -394,13 +411,13 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
         s_u.copy_t4(0, 16 * w, p.u + (ch0 + (int64_t)c * p.heads) * split_bytes<T>((int64_t)C * p.dv),
                     (int64_t)C * p.dv * 2, frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
       } else {
-        f32x4 qa[2] = {zero4(), zero4()};
+        Sums<T> qa[2];
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-          qa[i & 1] = mm(qf[i], W0.ld(li, 32 * i + 8 * g), qa[i & 1]);
+          qa[i & 1].add(qf[i], W0.ld(li, 32 * i + 8 * g));
           qf[i] = load_token(p.qp, nx, i);
         }
-        f32x4 o = (qa[0] + qa[1]) * eg_now * p.scale;
+        f32x4 o = (qa[0].sum() + qa[1].sum()) * eg_now * p.scale;
         o = mm(af[0], s_u.ld(li, 8 * g), o);
         if (w >= 2) o = mm(af[1], s_u.ld(li, 32 + 8 * g), o);
         load_square(p.am, nx, af);
@@ -447,8 +464,10 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
       const Frag u0 = s_ul.ld(li, 8 * g), u1 = s_ul.ld(li, 32 + 8 * g);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        st[i] = mm(ktf[i][0], u0, st[i] * ec);
-        st[i] = mm(ktf[i][1], u1, st[i]);
+        Sums<T> d;
+        d.add(ktf[i][0], u0);
+        d.add(ktf[i][1], u1);
+        st[i] = st[i] * ec + d.sum();
         W1.st4(li, (w * NT + i) * 16 + 4 * g, st[i]);
       }
       lds_barrier();
@@ -565,7 +584,8 @@ hipError_t step_impl(const DeltaStepParams &p, hipStream_t s) {
 
 template <typename T, int DK>
 hipError_t chunk_impl(const DeltaParams &p, bool backward, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.nchunk * p.heads));
+  const bool zero = p.cu && p.n > 0 && (backward || p.zero_unused);     // without offsets every row has a sequence
+  const dim3 grid((unsigned)((int64_t)p.nchunk * p.heads) + (zero ? kZeroBlocks : 0));
   if (backward)
     hipLaunchKernelGGL((delta_chunk_kernel<T, DK, true>), grid, dim3(256), 0, s, p);
   else
@@ -586,6 +606,7 @@ hipError_t states_impl(const DeltaParams &p, bool backward, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_delta_plan(const DeltaParams &p, hipStream_t s) {
+  if (p.cu == nullptr || p.nseq <= kDeltaLaneSeqs) return hipSuccess;
   hipLaunchKernelGGL(delta_plan_kernel, dim3(1), dim3(256), 0, s, p);
   return hipGetLastError();
 }
@@ -596,19 +617,10 @@ hipError_t launch_delta_chunk(const DeltaParams &p, bool bf16, bool backward, hi
 hipError_t launch_delta_states(const DeltaParams &p, bool bf16, bool backward, hipStream_t s) {
   return TTT_DELTA_BY_DK(states_impl, p, p, backward, s);
 }
-hipError_t launch_delta_zero_rows(const DeltaParams &p, void *rows, int64_t ld, int width, bool bf16, hipStream_t s) {
-  if (p.cu == nullptr || p.n == 0) return hipSuccess;      // one sequence covers every row
-  if (bf16)
-    hipLaunchKernelGGL(delta_zero_rows_kernel<__bf16>, dim3(256), dim3(256), 0, s, p, static_cast<__bf16 *>(rows), ld, width);
-  else
-    hipLaunchKernelGGL(delta_zero_rows_kernel<float>, dim3(256), dim3(256), 0, s, p, static_cast<float *>(rows), ld, width);
-  return hipGetLastError();
-}
 hipError_t launch_delta_forward(const DeltaParams &p, bool bf16, hipStream_t s) {
   hipError_t e = launch_delta_plan(p, s);
   if (e == hipSuccess) e = launch_delta_chunk(p, bf16, false, s);
   if (e == hipSuccess) e = launch_delta_states(p, bf16, false, s);
-  if (e == hipSuccess && p.zero_unused) e = launch_delta_zero_rows(p, p.o, p.ldo, p.heads * p.dv, bf16, s);
   return e;
 }
 hipError_t launch_delta_step(const DeltaStepParams &p, bool bf16, hipStream_t s) {

@@ -13,6 +13,7 @@
 //   dgamma_last += e^gamma_last <W0, G> + sum_j k_j.(second of dk)_j,   dg_i = sum_{j >= i} dgamma_j
 // (k_i.(dR W0)_i is dR_i.P_i, so P itself is not needed).
 #include "delta.h"
+#include "delta_layout.h"
 #include "split.h"
 
 namespace ttt {
@@ -34,7 +35,7 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
   const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
   const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
-  const DeltaSeq sq = p.seqs[b];
+  const DeltaSeq sq = seq_of(p, b);
   const int64_t wrow = (((int64_t)b * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
   f32x4 st[NT];
 #pragma unroll
@@ -109,12 +110,12 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
     const int len = sq.len - c0 < C ? sq.len - c0 : C, nx = c0 > 0 ? c0 - C : 0;
     const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
     const int64_t tok0 = sq.start + c0;
-    f32x4 du = zero4(), db = zero4();
+    Sums<T> kg[2];
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-      if (i & 1) db = mm(kf[i], s_g.ld(li, 32 * i + 8 * g), db);
-      else du = mm(kf[i], s_g.ld(li, 32 * i + 8 * g), du);
+      kg[i & 1].add(kf[i], s_g.ld(li, 32 * i + 8 * g));
     }
+    f32x4 du = kg[0].sum() + kg[1].sum();
     load_tokens(nx);
     {                                   // the gradient after the chunk, dk x dv
       char *o = p.gwt + ch * split_bytes<T>((int64_t)DK * p.dv);
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
                     frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) du[r] = t4 + r < len ? (du[r] + db[r]) * el[r] : 0.0f;
+    for (int r = 0; r < 4; ++r) du[r] = t4 + r < len ? du[r] * el[r] : 0.0f;
     if (w < 2) du = mm(af[0], s_go.ld(li, 8 * g), du);
     du = mm(af[1], s_go.ld(li, 32 + 8 * g), du);
     load_square(p.am, nx, af);
@@ -170,24 +171,26 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
 }
 
 // ------------------------------------------------------------------ token gradients
-// One workgroup per chunk and head.  First the 64 x 64 matrices X and Y (wave w has rows 16 w ..),
-// which pass through LDS as operands both ways round, then dq and dk, where wave w has dk / 4
-// columns, one 16-wide tile at a time, so that each state fragment is read by one wave.
+// One workgroup of eight waves per chunk and head.  First the 64 x 64 matrices X and Y (wave w has
+// row tile w % 4 and half of the column tiles), which pass through LDS as operands both ways round,
+// then dq and dk: wave w has the rows of half w / 4 and every fourth 16-wide column tile.  Operands
+// come from memory in fragment order; bound by their latency, so registers are kept few enough for
+// four waves a SIMD (one wave of 4 x 2 tiles a SIMD took 175 us where this takes %US% for 128 chunks
+// of 6 heads of 128).
 template <typename T, int DK>
-__global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
+__global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kernel(DeltaParams p) {
   __shared__ __attribute__((aligned(16))) SpTile<T, C, C> s_x, s_xt, s_y, s_yt;
-  __shared__ float s_row[5][4][C];      // per-wave partials: q.(go W0), k.(dR W0), k.(U G), row / column sums of M
-  __shared__ float s_db[C], s_red[4];
+  __shared__ float s_row[3][4][C];      // partials of q.(go W0), k.(dR W0), k.(U G)
+  __shared__ float s_rs[2][C], s_db[2][C], s_cs[4][C], s_red[4];
   typedef typename Sp<T>::Frag Frag;
-  constexpr int NT = DK / 64, TP = NT > 1 ? 2 : 1;      // column tiles of a wave, and at once
+  constexpr int NT = DK / 64;
   const int item = xcd_item(), h = item % p.heads, c = item / p.heads;
-  const DeltaChunk ck = p.chunks[c];
+  const DeltaChunk ck = chunk_of(p, c);
   if (ck.len == 0) return;
-  const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
-  const int grp = p.heads / p.key_heads, kh = h / grp;
+  const int t = threadIdx.x, w4 = (t >> 6) & 3, half = t >> 8, l = t & 63, g = l >> 4, li = l & 15;
+  const int kh = h / (p.heads / p.key_heads);
   const int64_t ch = (int64_t)c * p.heads + h;
-  const int last = ck.len - 1;
-  const int nv = p.dv / 32;
+  const int last = ck.len - 1, nv = p.dv / 32;
   const int64_t to = ((int64_t)c * p.key_heads + kh) * (DK * C);
   const T *K = static_cast<const T *>(p.kp) + to, *Q = static_cast<const T *>(p.qp) + to;
   const T *KT = static_cast<const T *>(p.kt) + to, *QT = static_cast<const T *>(p.qt) + to;
@@ -196,19 +199,19 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
   const int64_t uo = ch * split_bytes<T>((int64_t)C * p.dv), up = (int64_t)C * p.dv * 2;
   const char *U = p.u + uo, *DR = p.dr + uo;
 
-  // ---- X, Y and the sums over them
+  // ---- X, Y and the sums over them: row tile w4, column tiles 2 half, 2 half + 1
   {
-    f32x4 kk[4], qk[4], da[4], dl[4];
+    f32x4 kk[2], qk[2], da[2], dl[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) kk[j] = qk[j] = da[j] = dl[j] = zero4();
-    const int ra = 16 * w + li, rac = ra < last ? ra : last;
+    for (int j = 0; j < 2; ++j) kk[j] = qk[j] = da[j] = dl[j] = zero4();
+    const int ra = 16 * w4 + li, rac = ra < last ? ra : last;
 #pragma unroll 2
     for (int i = 0; i < DK / 32; ++i) {
-      const auto ka = ld8(K + frag_of(w, i, DK / 32)), qa = ld8(Q + frag_of(w, i, DK / 32));
+      const auto ka = ld8(K + frag_of(w4, i, DK / 32)), qa = ld8(Q + frag_of(w4, i, DK / 32));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j > w) continue;
-        const auto kb = ld8(K + frag_of(j, i, DK / 32));
+      for (int j = 0; j < 2; ++j) {
+        if (2 * half + j > w4) continue;                // above the diagonal
+        const auto kb = ld8(K + frag_of(2 * half + j, i, DK / 32));
         kk[j] = mm(ka, kb, kk[j]);
         qk[j] = mm(qa, kb, qk[j]);
       }
@@ -216,31 +219,33 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
     float drv = 0.0f;                                   // dR_i . V_i
 #pragma unroll 2
     for (int i = 0; i < nv; ++i) {
-      const auto ga = ld8(GO + frag_of(w, i, nv));
-      const Frag ra_f = Sp<T>::ld(DR, up, frag_of(w, i, nv));
-      const auto va = ld8(V + (int64_t)rac * p.ldv + 32 * i + 8 * g);
+      const auto ga = ld8(GO + frag_of(w4, i, nv));
+      const Frag ra_f = Sp<T>::ld(DR, up, frag_of(w4, i, nv));
+      if (half == 0) {
+        const auto va = ld8(V + (int64_t)rac * p.ldv + 32 * i + 8 * g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) drv += Sp<T>::at(ra_f, e) * (float)va[e];
+        for (int e = 0; e < 8; ++e) drv += Sp<T>::at(ra_f, e) * (float)va[e];
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j > w) continue;
-        const Frag ub = Sp<T>::ld(U, up, frag_of(j, i, nv));
+      for (int j = 0; j < 2; ++j) {
+        if (2 * half + j > w4) continue;
+        const Frag ub = Sp<T>::ld(U, up, frag_of(2 * half + j, i, nv));
         da[j] = mm(ga, ub, da[j]);
         dl[j] = mm(ra_f, ub, dl[j]);
       }
     }
     drv += __shfl_xor(drv, 16);
     drv += __shfl_xor(drv, 32);
-    if (g == 0) s_db[ra] = drv;
+    if (g == 0) s_db[half][ra] = drv;
     f32x4 rs = zero4(), dbs = zero4();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = 16 * j + li;
+    for (int j = 0; j < 2; ++j) {
+      const int col = 16 * (2 * half + j) + li;
       f32x4 x, y;
       float cs = 0.0f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * g + r;
+        const int row = 16 * w4 + 4 * g + r;
         const bool in = row < ck.len && col <= row;
         const float d = in ? exp_of(p.gam[ch * C + row] - p.gam[ch * C + col]) : 0.0f;
         const float be = p.be[ch * C + row];
@@ -255,11 +260,11 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
         s_x.st1(row, col, x[r]);
         s_y.st1(row, col, y[r]);
       }
-      s_xt.st4(col, 16 * w + 4 * g, x);
-      s_yt.st4(col, 16 * w + 4 * g, y);
+      s_xt.st4(col, 16 * w4 + 4 * g, x);
+      s_yt.st4(col, 16 * w4 + 4 * g, y);
       cs += __shfl_xor(cs, 16);
       cs += __shfl_xor(cs, 32);
-      if (g == 0) s_row[4][w][col] = cs;
+      if (g == 0) s_cs[w4][col] = cs;
     }
 #pragma unroll
     for (int m = 1; m < 16; m <<= 1)
@@ -271,97 +276,84 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
     if (li == 0)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * g + r;
-        s_row[3][0][row] = rs[r];
-        s_db[row] += dbs[r];           // written above by a lane of this wave
+        const int row = 16 * w4 + 4 * g + r;
+        s_rs[half][row] = rs[r];
+        s_db[half][row] += dbs[r];     // written above by a lane of this wave
       }
   }
   __syncthreads();
 
-  // ---- dq, dk
-  float dq_dot[4][4], dr_dot[4][4], du_dot[4][4];       // [row tile][r]: this lane's column of the row sums
+  // ---- dq, dk: rows 32 half .. + 31, column tiles w4, w4 + 4, ..
+  float dq_dot[2][4], dr_dot[2][4], du_dot[2][4];       // [row tile][r]: this lane's column of the row sums
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int a = 0; a < 2; ++a)
 #pragma unroll
     for (int r = 0; r < 4; ++r) dq_dot[a][r] = dr_dot[a][r] = du_dot[a][r] = 0.0f;
-  float wg = 0.0f;                                      // <W0, G>
+  float wg = 0.0f;                                      // <W0, G>, by the first half
   const int64_t so = ch * split_bytes<T>((int64_t)DK * p.dv), sp = (int64_t)DK * p.dv * 2;
 #pragma unroll 1
-  for (int i = 0; i < NT; i += TP) {
-    int base = li;                      // opaque: keeps the LDS operands below out of registers between tiles
-    asm volatile("" : "+v"(base));
-    const int rt = w * NT + i;          // 16-wide column tiles rt .. rt + TP - 1
-    f32x4 aq[TP][4], ar[TP][4], au[TP][4];
+  for (int i = 0; i < NT; ++i) {
+    int zero = 0;                       // opaque: keeps what is the same for every tile out of registers between them
+    asm volatile("" : "+v"(zero));
+    const int rt = w4 + 4 * i;
+    f32x4 aq[2], ar[2], au[2];
 #pragma unroll
-    for (int x = 0; x < TP; ++x)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) aq[x][a] = ar[x][a] = au[x][a] = zero4();
-#pragma unroll 1
+    for (int a = 0; a < 2; ++a) aq[a] = ar[a] = au[a] = zero4();
+#pragma unroll 2
     for (int ks = 0; ks < nv; ++ks) {
-      Frag wf[TP], gf[TP];
+      const Frag wf = Sp<T>::ld(p.w0t + so, sp, frag_of(rt, ks, nv)), gf = Sp<T>::ld(p.gwt + so, sp, frag_of(rt, ks, nv));
+      if (half == 0)
 #pragma unroll
-      for (int x = 0; x < TP; ++x) {
-        wf[x] = Sp<T>::ld(p.w0t + so, sp, frag_of(rt + x, ks, nv));
-        gf[x] = Sp<T>::ld(p.gwt + so, sp, frag_of(rt + x, ks, nv));
+        for (int e = 0; e < 8; ++e) wg += Sp<T>::at(wf, e) * Sp<T>::at(gf, e);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wg += Sp<T>::at(wf[x], e) * Sp<T>::at(gf[x], e);
-      }
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const auto ga = ld8(GO + frag_of(a, ks, nv));
-        const Frag ra = Sp<T>::ld(DR, up, frag_of(a, ks, nv)), ua = Sp<T>::ld(U, up, frag_of(a, ks, nv));
-#pragma unroll
-        for (int x = 0; x < TP; ++x) {
-          aq[x][a] = mm(ga, wf[x], aq[x][a]);
-          ar[x][a] = mm(ra, wf[x], ar[x][a]);
-          au[x][a] = mm(ua, gf[x], au[x][a]);
-        }
+      for (int a = 0; a < 2; ++a) {
+        const int f = frag_of(2 * half + a, ks, nv) + zero;
+        aq[a] = mm(ld8(GO + f), wf, aq[a]);
+        ar[a] = mm(Sp<T>::ld(DR, up, f), wf, ar[a]);
+        au[a] = mm(Sp<T>::ld(U, up, f), gf, au[a]);
       }
     }
+    const auto k0 = ld8(KT + frag_of(rt, 0, 2)), k1 = ld8(KT + frag_of(rt, 1, 2));
+    const auto q0 = ld8(QT + frag_of(rt, 0, 2)), q1 = ld8(QT + frag_of(rt, 1, 2));
+    const int col = rt * 16 + li;
 #pragma unroll
-    for (int x = 0; x < TP; ++x) {
-      const auto k0 = ld8(KT + frag_of(rt + x, 0, 2)), k1 = ld8(KT + frag_of(rt + x, 1, 2));
-      const auto q0 = ld8(QT + frag_of(rt + x, 0, 2)), q1 = ld8(QT + frag_of(rt + x, 1, 2));
-      const int col = (rt + x) * 16 + li;
+    for (int a = 0; a < 2; ++a) {
+      f32x4 xq = zero4(), xk = zero4();
+      const int row = 32 * half + 16 * a + li + zero;
+      xq = mm(s_x.ld(row, 8 * g), k0, xq);
+      xq = mm(s_x.ld(row, 32 + 8 * g), k1, xq);
+      xk = mm(s_xt.ld(row, 8 * g), q0, xk);
+      xk = mm(s_xt.ld(row, 32 + 8 * g), q1, xk);
+      xk = mm(s_y.ld(row, 8 * g), k0, xk);
+      xk = mm(s_y.ld(row, 32 + 8 * g), k1, xk);
+      xk = mm(s_yt.ld(row, 8 * g), k0, xk);
+      xk = mm(s_yt.ld(row, 32 + 8 * g), k1, xk);
+      const int r0 = 32 * half + 16 * a + 4 * g + zero;
+      const f32x4 eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + r0);
+      const f32x4 el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + r0);
+      const f32x4 be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + r0);
+      const T *kv = KT + frag_at(col, r0, 2), *qv = QT + frag_at(col, r0, 2);     // four tokens' elements
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        f32x4 xq = zero4(), xk = zero4();
-        const int row = 16 * a + base;
-        xq = mm(s_x.ld(row, 8 * g), k0, xq);
-        xq = mm(s_x.ld(row, 32 + 8 * g), k1, xq);
-        xk = mm(s_xt.ld(row, 8 * g), q0, xk);
-        xk = mm(s_xt.ld(row, 32 + 8 * g), q1, xk);
-        xk = mm(s_y.ld(row, 8 * g), k0, xk);
-        xk = mm(s_y.ld(row, 32 + 8 * g), k1, xk);
-        xk = mm(s_yt.ld(row, 8 * g), k0, xk);
-        xk = mm(s_yt.ld(row, 32 + 8 * g), k1, xk);
-        const int r0 = 16 * a + 4 * g;
-        const f32x4 eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + r0);
-        const f32x4 el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + r0);
-        const f32x4 be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + r0);
-        const T *kv = KT + frag_at(col, r0, 2), *qv = QT + frag_at(col, r0, 2);     // four tokens' elements
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (r0 + r >= ck.len) continue;
-          const int64_t tk = ck.tok0 + r0 + r;
-          const float dqi = p.scale * eg[r] * aq[x][a][r], dui = el[r] * au[x][a][r];
-          dq_dot[a][r] += to_f32(qv[r]) * dqi;
-          dr_dot[a][r] += to_f32(kv[r]) * ar[x][a][r];
-          du_dot[a][r] += to_f32(kv[r]) * dui;
-          const float dq = dqi + xq[r], dk = dui - be[r] * eg[r] * ar[x][a][r] + xk[r];
-          if (p.gqp) {
-            p.gqp[(tk * p.heads + h) * DK + col] = dq;
-            p.gkp[(tk * p.heads + h) * DK + col] = dk;
-          } else {
-            static_cast<T *>(p.gq)[tk * p.ldgq + kh * DK + col] = from_f32<T>(dq);
-            static_cast<T *>(p.gk)[tk * p.ldgk + kh * DK + col] = from_f32<T>(dk);
-          }
+      for (int r = 0; r < 4; ++r) {
+        if (r0 + r >= ck.len) continue;
+        const int64_t tk = ck.tok0 + r0 + r;
+        const float dqi = p.scale * eg[r] * aq[a][r], dui = el[r] * au[a][r];
+        dq_dot[a][r] += to_f32(qv[r]) * dqi;
+        dr_dot[a][r] += to_f32(kv[r]) * ar[a][r];
+        du_dot[a][r] += to_f32(kv[r]) * dui;
+        const float dq = dqi + xq[r], dk = dui - be[r] * eg[r] * ar[a][r] + xk[r];
+        if (p.gqp) {
+          p.gqp[(tk * p.heads + h) * DK + col] = dq;
+          p.gkp[(tk * p.heads + h) * DK + col] = dk;
+        } else {
+          static_cast<T *>(p.gq)[tk * p.ldgq + kh * DK + col] = from_f32<T>(dq);
+          static_cast<T *>(p.gk)[tk * p.ldgk + kh * DK + col] = from_f32<T>(dk);
         }
       }
     }
   }
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int a = 0; a < 2; ++a)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float x = dq_dot[a][r], y = dr_dot[a][r], z = du_dot[a][r];
@@ -372,15 +364,15 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
         z += __shfl_xor(z, m);
       }
       if (li == 0) {
-        const int row = 16 * a + 4 * g + r;
-        s_row[0][w][row] = x;
-        s_row[1][w][row] = y;
-        s_row[2][w][row] = z;
+        const int row = 32 * half + 16 * a + 4 * g + r;
+        s_row[0][w4][row] = x;
+        s_row[1][w4][row] = y;
+        s_row[2][w4][row] = z;
       }
     }
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) wg += __shfl_xor(wg, m);
-  if (l == 0) s_red[w] = wg;
+  if (l == 0 && half == 0) s_red[w4] = wg;
   __syncthreads();
   if (t < C) {
     float s[3];
@@ -389,10 +381,11 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
     const bool ok = t < ck.len;
     const float eg = p.eg[ch * C + t], be = p.be[ch * C + t];
     float cs = 0.0f;
-    for (int x = t >> 4; x < 4; ++x) cs += s_row[4][x][t];      // rows of waves below this column's tile
-    if (ok) p.gbeta[h * p.gbeta_hs + ck.tok0 + t] = s_db[t] - eg * s[1];
+    for (int x = t >> 4; x < 4; ++x) cs += s_cs[x][t];          // row tiles on and below this column's
+    if (ok) p.gbeta[h * p.gbeta_hs + ck.tok0 + t] = s_db[0][t] + s_db[1][t] - eg * s[1];
     // in 64 bits: the rows' terms cancel in part
-    double d = ok ? (double)s[0] - (double)(be * eg * s[1]) - (double)s[2] + ((double)s_row[3][0][t] - (double)cs) : 0.0;
+    double d = ok ? (double)s[0] - (double)(be * eg * s[1]) - (double)s[2] +
+                        ((double)s_rs[0][t] + (double)s_rs[1][t] - (double)cs) : 0.0;
     double us = ok ? (double)s[2] : 0.0;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) us += __shfl_xor(us, m);
@@ -412,7 +405,8 @@ __global__ __launch_bounds__(256, 1) void delta_gtoken_kernel(DeltaParams p) {
 template <typename T>
 __global__ __launch_bounds__(256) void delta_group_kernel(DeltaParams p) {
   const int grp = p.heads / p.key_heads, dk = p.dk;
-  const int first = p.seqs[0].start, used = *p.used;
+  const int2 rows = rows_of(p);
+  const int first = rows.x, used = rows.y;
   const int64_t per = (int64_t)p.key_heads * dk / 4;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)(used - first) * per; i += (int64_t)gridDim.x * 256) {
     const int64_t tk = first + i / per;
@@ -428,16 +422,6 @@ __global__ __launch_bounds__(256) void delta_group_kernel(DeltaParams p) {
       static_cast<T *>(p.gq)[tk * p.ldgq + e + r] = from_f32<T>(x[r]);
       static_cast<T *>(p.gk)[tk * p.ldgk + e + r] = from_f32<T>(y[r]);
     }
-  }
-}
-
-// Rows of no sequence have no gradient: zeros in the rates' gradients there.
-__global__ __launch_bounds__(256) void delta_zero_rates_kernel(DeltaParams p) {
-  const int first = p.seqs[0].start, used = *p.used, total = first + (p.n - used);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)total * p.heads; i += (int64_t)gridDim.x * 256) {
-    const int r = (int)(i % total), h = (int)(i / total), row = r < first ? r : used + (r - first);
-    p.gbeta[h * p.gbeta_hs + row] = 0.0f;
-    if (p.gdecay) p.gdecay[h * p.gdecay_hs + row] = 0.0f;
   }
 }
 
@@ -461,7 +445,7 @@ hipError_t gstate_impl(const DeltaParams &p, hipStream_t s) {
 }
 template <typename T, int DK>
 hipError_t gtoken_impl(const DeltaParams &p, hipStream_t s) {
-  hipLaunchKernelGGL((delta_gtoken_kernel<T, DK>), dim3((unsigned)((int64_t)p.nchunk * p.heads)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((delta_gtoken_kernel<T, DK>), dim3((unsigned)((int64_t)p.nchunk * p.heads)), dim3(512), 0, s, p);
   return hipGetLastError();
 }
 template <typename T>
@@ -480,16 +464,6 @@ hipError_t launch_delta_backward(const DeltaParams &p, bool bf16, hipStream_t s)
   if (e == hipSuccess && p.nchunk > 0) e = TTT_DELTA_BY_DK(gtoken_impl, p, p, s);
   if (e == hipSuccess && p.nchunk > 0 && p.gqp) e = bf16 ? group_impl<__bf16>(p, s) : group_impl<float>(p, s);
   if (p.n == 0) return e;
-  if (p.cu) {
-    const int kw = p.key_heads * p.dk;
-    if (e == hipSuccess) e = launch_delta_zero_rows(p, p.gq, p.ldgq, kw, bf16, s);
-    if (e == hipSuccess) e = launch_delta_zero_rows(p, p.gk, p.ldgk, kw, bf16, s);
-    if (e == hipSuccess) e = launch_delta_zero_rows(p, p.gv, p.ldgv, p.heads * p.dv, bf16, s);
-    if (e == hipSuccess) {
-      hipLaunchKernelGGL(delta_zero_rates_kernel, dim3(64), dim3(256), 0, s, p);
-      e = hipGetLastError();
-    }
-  }
   if (e == hipSuccess && (p.sum_beta || p.sum_decay)) {
     hipLaunchKernelGGL(delta_sum_rates_kernel, dim3((p.n + 255) / 256), dim3(256), 0, s, p);
     e = hipGetLastError();

@@ -35,6 +35,28 @@ __device__ __forceinline__ f32x4 mm(const Split8 &a, const Split8 &b, f32x4 c) {
 }
 __device__ __forceinline__ f32x4 mm(f32x8 a, f32x8 b, f32x4 c) { return mma(a, b, c); }
 
+// The products of one operand with every part of the other, each added to a sum of its own: products
+// that follow one another then do not wait for one another.
+template <typename T> struct Sums {
+  static constexpr int N = sizeof(T) == 2 ? kParts : 1;
+  f32x4 v[N];
+  __device__ __forceinline__ Sums() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = f32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void add(bf16x8 a, const Split8 &b) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = mma(a, b.p[i], v[i]);
+  }
+  __device__ __forceinline__ void add(f32x8 a, f32x8 b) { v[0] = mma(a, b, v[0]); }
+  __device__ __forceinline__ f32x4 sum() const {
+    f32x4 s = v[N - 1];
+#pragma unroll
+    for (int i = N - 2; i >= 0; --i) s += v[i];
+    return s;
+  }
+};
+
 // Split matrices beside T tokens: `plane` is the byte distance from one part's plane to the next.
 template <typename T> struct Sp;
 template <> struct Sp<__bf16> {
