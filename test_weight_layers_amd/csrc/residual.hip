@@ -18,13 +18,13 @@
 namespace ttt {
 namespace {
 
-template <typename T> __device__ __forceinline__ f32x8 load8(const T *p) {
-  const auto v = ld8(p);
+template <typename V> __device__ __forceinline__ f32x8 widen(const V v) {
   f32x8 r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) r[i] = (float)v[i];
   return r;
 }
+template <typename T> __device__ __forceinline__ f32x8 load8(const T *p) { return widen(ld8(p)); }
 __device__ __forceinline__ void store8(__bf16 *p, f32x8 v) {
   bf16x8 r;
 #pragma unroll
@@ -43,20 +43,25 @@ __device__ __forceinline__ float dot8(f32x8 a, f32x8 b) {
 }
 __device__ __forceinline__ f32x8 splat8(float x) { return f32x8{x, x, x, x, x, x, x, x}; }
 
-// Sums over the LPR lanes of a row (LPR = 256: the workgroup), and over groups of `norm` channels.
+// Threads of a workgroup: 256, or one row's lanes.
+constexpr int threads_of(int lpr) { return lpr > 256 ? lpr : 256; }
+
+// Sums over the LPR lanes of a row (from 256 on: the workgroup), and over groups of `norm` channels.
 // The three group forms: the row; a power of two of lanes (shuffles); any other width (LDS).
 template <int LPR, int NV> struct RowSums {
-  float *s_row;       // [4]
-  float *s_vec;       // [256 * NV]
+  float *s_row;       // [threads / 64]
+  float *s_vec;       // [threads * NV]
   int groups8, mode;  // norm / 8; 0 row, 1 lanes, 2 LDS
   __device__ float row(float v) const {
 #pragma unroll
     for (int m = 1; m < (LPR < 64 ? LPR : 64); m <<= 1) v += __shfl_xor(v, m);
-    if constexpr (LPR == 256) {
+    if constexpr (LPR >= 256) {
       __syncthreads();
       if ((threadIdx.x & 63) == 0) s_row[threadIdx.x >> 6] = v;
       __syncthreads();
-      v = (s_row[0] + s_row[1]) + (s_row[2] + s_row[3]);
+      v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < LPR / 64; ++i) v += s_row[i];
     }
     return v;
   }
@@ -99,9 +104,9 @@ int group_mode(int channels, int norm) {
 }
 
 template <typename T, int LPR, int NV>
-__global__ __launch_bounds__(256) void residual_kernel(ResidualParams p, int mode) {
-  __shared__ float s_row[4], s_vec[256 * NV];
-  constexpr int RPB = 256 / LPR;      // rows a workgroup has at once
+__global__ __launch_bounds__(threads_of(LPR)) void residual_kernel(ResidualParams p, int mode) {
+  constexpr int NTH = threads_of(LPR), RPB = NTH / LPR;      // rows a workgroup has at once
+  __shared__ float s_row[NTH / 64], s_vec[NTH * NV];
   const RowSums<LPR, NV> sums{s_row, s_vec, p.norm / 8, mode};
   const int lane = threadIdx.x % LPR;
   f32x8 ag[NV], gn[NV];
@@ -157,10 +162,10 @@ __global__ __launch_bounds__(256) void residual_kernel(ResidualParams p, int mod
 }
 
 template <typename T, int LPR, int NV>
-__global__ __launch_bounds__(256) void residual_backward_kernel(ResidualParams p, int mode) {
-  __shared__ float s_row[4], s_vec[256 * NV];
-  __shared__ __attribute__((aligned(16))) float s_acc[256 * NV * 8];
-  constexpr int RPB = 256 / LPR;
+__global__ __launch_bounds__(threads_of(LPR)) void residual_backward_kernel(ResidualParams p, int mode) {
+  constexpr int NTH = threads_of(LPR), RPB = NTH / LPR;
+  __shared__ float s_row[NTH / 64], s_vec[NTH * NV];
+  __shared__ __attribute__((aligned(16))) float s_acc[NTH * NV * 8];
   const RowSums<LPR, NV> sums{s_row, s_vec, p.norm / 8, mode};
   const int lane = threadIdx.x % LPR;
   f32x8 ag[NV], gn[NV], acc[NV], accn[NV];
@@ -176,27 +181,39 @@ __global__ __launch_bounds__(256) void residual_backward_kernel(ResidualParams p
     }
   }
   const float inv_norm = 1.0f / (float)p.norm, inv_c = 1.0f / (float)p.channels;
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.n; r0 += (int64_t)gridDim.x * RPB) {
+  // bf16: the next row's tensors are loaded while this one is worked on (44k rows of 1024: 148 against
+  // 235 us); fp32 rows would take the registers of a second wave a SIMD (8k rows of 768: 46 against 32)
+  constexpr bool kAhead = sizeof(T) == 2;
+  typedef typename FragOf<T>::type Raw;
+  Raw n_gy[NV], n_gh[NV], n_y[NV], n_o[NV], n_z[NV];
+  const auto fetch = [&](int64_t r0) {
     const int64_t row = r0 + threadIdx.x / LPR;
-    const bool live = row < p.n;
-    f32x8 gx[NV], o[NV], z[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * LPR + lane) * 8;
-      const bool in = live && c < p.channels;
-      gx[j] = in && p.gy ? load8(static_cast<const T *>(p.gy) + row * p.ldgy + c) : splat8(0.0f);
-      o[j] = in ? load8(static_cast<const T *>(p.o) + row * p.ldo + c) : splat8(0.0f);
-      if (p.z) z[j] = in ? load8(static_cast<const T *>(p.z) + row * p.ldz + c) : splat8(0.0f);
+      const bool in = row < p.n && c < p.channels;
+      n_gy[j] = in && p.gy ? ld8(static_cast<const T *>(p.gy) + row * p.ldgy + c) : zero8<T>();
+      n_gh[j] = in && p.gh ? ld8(static_cast<const T *>(p.gh) + row * p.ldgh + c) : zero8<T>();
+      n_y[j] = in && p.gh ? ld8(static_cast<const T *>(p.y) + row * p.ldy + c) : zero8<T>();
+      n_o[j] = in ? ld8(static_cast<const T *>(p.o) + row * p.ldo + c) : zero8<T>();
+      n_z[j] = in && p.z ? ld8(static_cast<const T *>(p.z) + row * p.ldz + c) : zero8<T>();
     }
+  };
+  if (kAhead) fetch((int64_t)blockIdx.x * RPB);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.n; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t row = r0 + threadIdx.x / LPR;
+    const bool live = row < p.n;
+    f32x8 gx[NV], o[NV], z[NV], y[NV], gh[NV];
+    if (!kAhead) fetch(r0);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      gx[j] = widen(n_gy[j]), gh[j] = widen(n_gh[j]), y[j] = widen(n_y[j]), o[j] = widen(n_o[j]), z[j] = widen(n_z[j]);
+    }
+    if (kAhead) fetch(r0 + (int64_t)gridDim.x * RPB);
     if (p.gh) {
-      f32x8 y[NV], gh[NV];
       float sy = 0.0f, sty = 0.0f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * LPR + lane) * 8;
-        const bool in = live && c < p.channels;
-        y[j] = in ? load8(static_cast<const T *>(p.y) + row * p.ldy + c) : splat8(0.0f);
-        gh[j] = in ? load8(static_cast<const T *>(p.gh) + row * p.ldgh + c) : splat8(0.0f);
         sy += dot8(y[j], y[j]);
         sty += dot8(y[j], gh[j] * gn[j]);
       }
@@ -255,7 +272,7 @@ __global__ __launch_bounds__(256) void residual_backward_kernel(ResidualParams p
     for (int j = 0; j < NV; ++j)
       store8(s_acc + (threadIdx.x / LPR) * (LPR * NV * 8) + (j * LPR + lane) * 8, k ? accn[j] : acc[j]);
     __syncthreads();
-    for (int c = threadIdx.x; c < p.channels; c += 256) {
+    for (int c = threadIdx.x; c < p.channels; c += NTH) {
       float s = 0.0f;
 #pragma unroll
       for (int r = 0; r < RPB; ++r) s += s_acc[r * (LPR * NV * 8) + c];
@@ -264,20 +281,20 @@ __global__ __launch_bounds__(256) void residual_backward_kernel(ResidualParams p
   }
 }
 
-// The workgroups' partials, in order: 16 channels x 16 interleaved sums a workgroup.
-__global__ __launch_bounds__(256) void residual_sum_kernel(ResidualParams p, int parts) {
-  __shared__ float s[16][17];
+// The workgroups' partials, in order: 16 channels x 64 interleaved sums a workgroup.
+__global__ __launch_bounds__(1024) void residual_sum_kernel(ResidualParams p, int parts) {
+  __shared__ float s[64][17];
   const int c = blockIdx.x * 16 + (threadIdx.x & 15), k = blockIdx.y, q = threadIdx.x >> 4;
   float v = 0.0f;
   if (c < p.channels)
-#pragma unroll 4
-    for (int i = q; i < parts; i += 16) v += p.part[((int64_t)i * 2 + k) * p.channels + c];
+#pragma unroll 8
+    for (int i = q; i < parts; i += 64) v += p.part[((int64_t)i * 2 + k) * p.channels + c];
   s[q][threadIdx.x & 15] = v;
   __syncthreads();
   if (q == 0 && c < p.channels) {
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum += s[i][threadIdx.x & 15];
+    for (int i = 0; i < 64; ++i) sum += s[i][threadIdx.x & 15];
     if (k == 1) {
       if (p.ggamma_next) p.ggamma_next[c] = sum;
     } else {
@@ -288,7 +305,8 @@ __global__ __launch_bounds__(256) void residual_sum_kernel(ResidualParams p, int
 }
 
 struct Shape { int lpr, nv; };
-// One wave (or a part of it) a row up to 2048 channels, then a workgroup a row.
+// One wave (or a part of it) a row up to 1024 channels, then a workgroup a row; two vectors a lane at
+// most (four leave one wave a SIMD).
 Shape shape_of(int channels) {
   const int v = (channels + 7) / 8;
   if (v <= 8) return {8, 1};
@@ -296,22 +314,22 @@ Shape shape_of(int channels) {
   if (v <= 32) return {32, 1};
   if (v <= 64) return {64, 1};
   if (v <= 128) return {64, 2};
-  if (v <= 256) return {64, 4};
+  if (v <= 256) return {256, 1};
   if (v <= 512) return {256, 2};
-  return {256, 4};
+  return {512, 2};
 }
 
 template <typename T, int LPR, int NV>
 hipError_t go(const ResidualParams &p, bool backward, hipStream_t s) {
   const int mode = group_mode(p.channels, p.norm), grid = residual_grid(p.n, p.channels);
   if (!backward) {
-    hipLaunchKernelGGL((residual_kernel<T, LPR, NV>), dim3(grid), dim3(256), 0, s, p, mode);
+    hipLaunchKernelGGL((residual_kernel<T, LPR, NV>), dim3(grid), dim3(threads_of(LPR)), 0, s, p, mode);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((residual_backward_kernel<T, LPR, NV>), dim3(grid), dim3(256), 0, s, p, mode);
+  hipLaunchKernelGGL((residual_backward_kernel<T, LPR, NV>), dim3(grid), dim3(threads_of(LPR)), 0, s, p, mode);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !(p.ggamma || p.galpha || p.ggamma_next)) return e;
-  hipLaunchKernelGGL(residual_sum_kernel, dim3((p.channels + 15) / 16, 2), dim3(256), 0, s, p, grid);
+  hipLaunchKernelGGL(residual_sum_kernel, dim3((p.channels + 15) / 16, 2), dim3(1024), 0, s, p, grid);
   return hipGetLastError();
 }
 
@@ -323,9 +341,9 @@ template <typename T> hipError_t pick(const ResidualParams &p, bool backward, hi
     case 321: return go<T, 32, 1>(p, backward, s);
     case 641: return go<T, 64, 1>(p, backward, s);
     case 642: return go<T, 64, 2>(p, backward, s);
-    case 644: return go<T, 64, 4>(p, backward, s);
+    case 2561: return go<T, 256, 1>(p, backward, s);
     case 2562: return go<T, 256, 2>(p, backward, s);
-    default: return go<T, 256, 4>(p, backward, s);
+    default: return go<T, 512, 2>(p, backward, s);
   }
 }
 
@@ -333,7 +351,8 @@ template <typename T> hipError_t pick(const ResidualParams &p, bool backward, hi
 
 // Four workgroups a CU loop over the rows (fewer for few rows).
 int residual_grid(int64_t n, int channels) {
-  const int64_t rpb = 256 / shape_of(channels).lpr, want = (n + rpb - 1) / rpb;
+  const int lpr = shape_of(channels).lpr;
+  const int64_t rpb = threads_of(lpr) / lpr, want = (n + rpb - 1) / rpb;
   return (int)(want < 1 ? 1 : (want < 1024 ? want : 1024));
 }
 hipError_t launch_residual(const ResidualParams &p, bool bf16, hipStream_t s) {
