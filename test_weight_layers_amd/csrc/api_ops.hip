@@ -95,9 +95,9 @@ int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype
     o = align256(o + bytes);
     return at;
   };
-  const size_t cc = (size_t)nc * H, sb = delta_split_bytes(dtype == TTT_BF16);
+  const size_t cc = (size_t)nc * H, sb = 2 * kDeltaParts, tb = 2 * delta_token_parts(dtype == TTT_BF16);
   const size_t mat = (size_t)kDeltaChunk * kDeltaChunk * sb;
-  const size_t tok = (size_t)nc * Hk * dk * kDeltaChunk * esize(dtype);
+  const size_t tok = (size_t)nc * Hk * dk * kDeltaChunk * tb;
   P.off_seqs = take((size_t)nseq * sizeof(DeltaSeq));
   P.off_chunks = take((size_t)nc * sizeof(DeltaChunk));
   P.off_used = take(4);
@@ -110,12 +110,12 @@ int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype
   P.off_qp = take(tok);
   P.off_kt = take(tok);
   if (backward) {
-    P.off_gop = take(cc * kDeltaChunk * dv * esize(dtype));
+    P.off_gop = take(cc * kDeltaChunk * dv * tb);
     P.off_gam = take(cc * kDeltaChunk * 8);
     P.off_tt = take(cc * mat);
     P.off_qt = take(tok);
-    P.off_w0t = take(cc * dk * dv * sb);
-    P.off_gwt = take(cc * dk * dv * sb);
+    P.off_w0t = take(cc * dk * dv * 4);
+    P.off_gwt = take(cc * dk * dv * 4);
     P.off_u = take(cc * kDeltaChunk * dv * sb);
     P.off_dr = take(cc * kDeltaChunk * dv * sb);
     if (H != Hk) {
@@ -162,7 +162,7 @@ int delta_params(int H, int Hk, int dk, int dv, const float *w, const Rows &q, c
   if (backward) {
     p->gam = reinterpret_cast<double *>(b + P.off_gam);
     p->gop = b + P.off_gop;
-    p->tt = b + P.off_tt, p->qt = b + P.off_qt, p->w0t = b + P.off_w0t, p->gwt = b + P.off_gwt;
+    p->tt = b + P.off_tt, p->qt = b + P.off_qt, p->w0t = reinterpret_cast<float *>(b + P.off_w0t), p->gwt = reinterpret_cast<float *>(b + P.off_gwt);
     p->u = b + P.off_u, p->dr = b + P.off_dr;
     if (H != Hk) {
       p->gqp = reinterpret_cast<float *>(b + P.off_gqp);

@@ -14,10 +14,9 @@ constexpr int kDeltaLaneSeqs = 63;
 // dv columns of the state that one workgroup of the sequential kernels holds.
 constexpr int kDeltaSlice = 16;
 
-// bf16 parts of a computed operand beside bf16 tokens.
-constexpr int kParts = 2;
-// Bytes of one element of a split matrix in the workspace (bf16 parts, or fp32).
-constexpr int delta_split_bytes(bool bf16) { return bf16 ? 2 * kParts : 4; }
+// bf16 parts of a computed operand (see split.h), and of a token.
+constexpr int kDeltaParts = 3;
+constexpr int delta_token_parts(bool bf16) { return bf16 ? 1 : 3; }
 
 struct DeltaSeq {      // one packed sequence: rows [start, start + len), its chunks from chunk0 on
   int start, len, chunk0, pad;
@@ -40,16 +39,16 @@ struct DeltaParams {
   int nchunk;                       // upper bound of the number of chunks
   float scale;
   int zero_unused;                  // write zeros to rows that belong to no sequence
-  // workspace (matrices in fragment order, see split.h)
+  // workspace (matrices in fragment order, split ones a plane a part: see split.h)
   DeltaSeq *seqs;                   // [nseq]
   DeltaChunk *chunks;               // [nchunk]
   int *used;                        // one past the last row of the last sequence
   float *eg, *el, *be;              // [nchunk][H][64]: e^gamma_i, e^(gamma_last - gamma_i), beta (0 past the chunk)
   double *gam;                      // gamma_i (backward)
-  char *tm, *am;                    // [nchunk][H] split 64 x 64 matrices: T, A (forward) or A^T (backward)
+  char *tm, *am;                    // [nchunk][H] split 64 x 64: T, A (forward) or A^T (backward)
   char *tt;                         // T^T (backward)
-  void *kp, *qp;                    // [nchunk][Hk] tokens 64 x dk, 0 past the chunk
-  void *kt, *qt;                    // [nchunk][Hk] the same transposed, dk x 64 (qt: backward)
+  char *kp, *qp;                    // [nchunk][Hk] split tokens 64 x dk, 0 past the chunk
+  char *kt, *qt;                    // [nchunk][Hk] the same transposed, dk x 64 (qt: backward)
   // backward
   const void *go;                   // gradient of o
   int64_t ldgo;
@@ -62,8 +61,8 @@ struct DeltaParams {
   float *gbeta_out, *gdecay_out;    // [n]
   int sum_beta, sum_decay;
   float *gw;                        // gradient of w
-  void *gop;                        // [nchunk][H] gradient of o, 64 x dv
-  char *w0t, *gwt;                  // [nchunk][H] split dk x dv: state before the chunk, its gradient after
+  char *gop;                        // [nchunk][H] split gradient of o, 64 x dv
+  float *w0t, *gwt;                 // [nchunk][H] fp32 dk x dv: state before the chunk, its gradient after
   char *u, *dr;                     // [nchunk][H] split 64 x dv: U and dR
   float *gqp, *gkp;                 // [n][H][dk] per-head partials (grouped key heads), or null
 };

@@ -85,6 +85,7 @@ __device__ void zero_rows(const DeltaParams &p, int2 used, void *rows, int64_t l
     static_cast<T *>(rows)[row * ld + i % width] = from_f32<T>(0.0f);
   }
 }
+constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 matrix
 constexpr int kZeroBlocks = 64;     // workgroups of the chunk kernel's launch that write those zeros
 
 // ------------------------------------------------------------------ chunk terms
@@ -92,14 +93,13 @@ constexpr int kZeroBlocks = 64;     // workgroups of the chunk kernel's launch t
 // and (once per key head) the tokens and their transposes in fragment order.
 // Substitution, not products of powers of L: those grow without bound where keys repeat.
 template <typename T, int DK, bool BWD>
-__global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaParams p) {
-  constexpr int kPitch = DK + Sp<T>::kPad, NK = DK / 32, kA = C + 4;
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kernel(DeltaParams p) {
+  constexpr int kPitch = DK + 16 / (int)sizeof(T), NK = DK / 32, kA = C + 4, TP = kTok<T>;
   constexpr int kTokBytes = C * kPitch * (int)sizeof(T), kABytes = C * kA * 4;
   __shared__ __attribute__((aligned(16))) unsigned char s_raw[kTokBytes > kABytes ? kTokBytes : kABytes];
   __shared__ double s_gam[C];
   __shared__ float s_beta[C];
   __shared__ __attribute__((aligned(16))) float s_l[C][kA], s_t[C][kA], s_x[32][36];
-  typedef typename FragOf<T>::type Tok;
   T *s_tok = reinterpret_cast<T *>(s_raw);              // [64][kPitch]
   float *s_a = reinterpret_cast<float *>(s_raw);        // [64][kA], after the tokens
   const int items = p.nchunk * p.heads;
@@ -119,15 +119,15 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaParams p) {
     }
     return;
   }
-  const int item = items % 8 == 0 ? (blockIdx.x & 7) * (items >> 3) + (blockIdx.x >> 3) : blockIdx.x;
-  const int h = item % p.heads, c = item / p.heads;
+  const int item = xcd_item(items), h = item % p.heads, c = item / p.heads;
   const DeltaChunk ck = chunk_of(p, c);
   if (ck.len == 0) return;
   const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
   const int grp = p.heads / p.key_heads, kh = h / grp;
   const bool writer = h % grp == 0;                     // of the key head's operands
   const int64_t ch = (int64_t)c * p.heads + h;
-  const int64_t tokens = ((int64_t)c * p.key_heads + kh) * (DK * C);
+  const int64_t tokens = ((int64_t)c * p.key_heads + kh) * (DK * C * 2 * TP);
+  constexpr int64_t tplane = DK * C * 2;
   constexpr int V = 16 / (int)sizeof(T), NP = C * DK / V / 256;      // 16-byte pieces: elements, and a thread's
   const auto fetch = [&](const void *src, int64_t ld, u32x4 (&x)[NP]) {
     const T *b = static_cast<const T *>(src) + (int64_t)ck.tok0 * ld + kh * DK;
@@ -168,14 +168,14 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaParams p) {
     p.el[ch * C + t] = exp_of(__shfl(gam, 63) - gam);
   }
   // the transposed operand: row = column of the tokens, k = token
-  const auto write_transposed = [&](T *dst) {
+  const auto write_transposed = [&](char *dst) {
 #pragma unroll
     for (int i = 0; i < DK / 64; ++i) {
       const int rt = w * (DK / 64) + i;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int k0 = 32 * x + 8 * g;
-        Tok f;
+        typename FragOf<T>::type f;
         if constexpr (sizeof(T) == 2) {
           const unsigned char *b = s_raw + ((k0 + (li >> 2)) * kPitch + 16 * rt + 4 * (li & 3)) * 2;
           f = cat8(lds_read_tr16(b), lds_read_tr16(b + 4 * kPitch * 2));
@@ -183,19 +183,19 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaParams p) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = s_tok[(k0 + e) * kPitch + 16 * rt + li];
         }
-        *reinterpret_cast<Tok *>(dst + tokens + frag_of(rt, x, 2)) = f;
+        store_split(dst + tokens, tplane, frag_of(rt, x, 2), token_of(f));
       }
     }
   };
   stage(xq);
   __syncthreads();
-  Tok qa[NK];                                           // wave w has rows 16 w .. 16 w + 15
+  Split<TP> qa[NK];                                     // wave w has rows 16 w .. 16 w + 15
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
-    qa[i] = ld8(s_tok + (16 * w + li) * kPitch + 32 * i + 8 * g);
-    if (writer) *reinterpret_cast<Tok *>(static_cast<T *>(p.qp) + tokens + frag_of(w, i, NK)) = qa[i];
+    qa[i] = token_of(ld8(s_tok + (16 * w + li) * kPitch + 32 * i + 8 * g));
+    if (writer) store_split(p.qp + tokens, tplane, frag_of(w, i, NK), qa[i]);
   }
-  if (BWD && writer) write_transposed(static_cast<T *>(p.qt));
+  if (BWD && writer) write_transposed(p.qt);
   __syncthreads();
   stage(xk);
   __syncthreads();
@@ -204,17 +204,17 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaParams p) {
   for (int j = 0; j < 4; ++j) kk[j] = qk[j] = zero4();
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
-    const Tok ka = ld8(s_tok + (16 * w + li) * kPitch + 32 * i + 8 * g);
-    if (writer) *reinterpret_cast<Tok *>(static_cast<T *>(p.kp) + tokens + frag_of(w, i, NK)) = ka;
+    const Split<TP> ka = token_of(ld8(s_tok + (16 * w + li) * kPitch + 32 * i + 8 * g));
+    if (writer) store_split(p.kp + tokens, tplane, frag_of(w, i, NK), ka);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j > w) continue;                              // above the diagonal
-      const Tok kb = ld8(s_tok + (16 * j + li) * kPitch + 32 * i + 8 * g);
+      const Split<TP> kb = token_of(ld8(s_tok + (16 * j + li) * kPitch + 32 * i + 8 * g));
       kk[j] = mm(ka, kb, kk[j]);
       qk[j] = mm(qa[i], kb, qk[j]);
     }
   }
-  if (writer) write_transposed(static_cast<T *>(p.kt));
+  if (writer) write_transposed(p.kt);
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -290,31 +290,32 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaParams p) {
     for (int r = 0; r < 4; ++r) s_t[32 + ti + 4 * g + r][tj + li] = -s[r];
   }
   __syncthreads();
-  const int64_t mat = ch * split_bytes<T>(C * C), plane = C * C * 2;
+  const int64_t mat = ch * kSquare, plane = C * C * 2;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {                         // fragment w + 4 q: rows 16 rt, k 32 kt
     const int f = w + 4 * q, row = 16 * (f >> 1) + li, k0 = 32 * (f & 1) + 8 * g, e = f * 512 + l * 8;
-    float x[8];
-    Sp<T>::st8(p.tm + mat, plane, e, &s_t[row][k0]);
+    store_split(p.tm + mat, plane, e, split_of<kFull>(ld8(&s_t[row][k0])));
     if (BWD) {
+      f32x8 x, y;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = s_t[k0 + i][row];
-      Sp<T>::st8(p.tt + mat, plane, e, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = s_a[(k0 + i) * kA + row];
-      Sp<T>::st8(p.am + mat, plane, e, x);
+      for (int i = 0; i < 8; ++i) {
+        x[i] = s_t[k0 + i][row];
+        y[i] = s_a[(k0 + i) * kA + row];
+      }
+      store_split(p.tt + mat, plane, e, split_of<kFull>(x));
+      store_split(p.am + mat, plane, e, split_of<kFull>(y));
     } else {
-      Sp<T>::st8(p.am + mat, plane, e, s_a + row * kA + k0);
+      store_split(p.am + mat, plane, e, split_of<kOut<T>>(ld8(s_a + row * kA + k0)));
     }
   }
   if (BWD) {
     const int row = 16 * w + li, nk = p.dv / 32;
     const T *go = static_cast<const T *>(p.go) + (int64_t)(ck.tok0 + (row < ck.len ? row : 0)) * p.ldgo + h * p.dv + 8 * g;
-    T *o = static_cast<T *>(p.gop) + ch * C * p.dv;
+    char *o = p.gop + ch * C * p.dv * 2 * TP;
     for (int i = 0; i < nk; ++i) {
-      Tok v = ld8(go + 32 * i);
+      auto v = ld8(go + 32 * i);
       if (row >= ck.len) v = zero8<T>();
-      *reinterpret_cast<Tok *>(o + frag_of(w, i, nk)) = v;
+      store_split(o, (int64_t)C * p.dv * 2, frag_of(w, i, nk), token_of(v));
     }
   }
 }
@@ -332,12 +333,14 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaParams p) {
 // BWD writes the states and U that the gradient needs, in place of the outputs.
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
-  __shared__ __attribute__((aligned(16))) SpTile<T, SL, DK> s_w[2];
-  __shared__ __attribute__((aligned(16))) SpTile<T, SL, C> s_r, s_u, s_ul;
-  typedef typename FragOf<T>::type Tok;
-  typedef typename Sp<T>::Frag Frag;
-  constexpr int NT = DK / 64, NK = DK / 32;
-  const int slices = p.dv / SL, item = xcd_item();
+  constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>, UP = BWD ? kFull : kOut<T>;
+  __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, DK> s_w[2];
+  __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, C> s_r, s_ul;
+  __shared__ __attribute__((aligned(16))) SplitTile<UP, SL, C> s_u;
+  constexpr int64_t tokens = DK * C * 2 * TP, tplane = DK * C * 2;      // bytes of a chunk's tokens and a part
+  // the operands of Q wait in registers too, but for fp32 tokens of 256, which would not fit
+  constexpr bool kHoldQ = !BWD && (TP == 1 || DK < 256);
+  const int slices = p.dv / SL, item = xcd_item(gridDim.x);
   const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
   const int t = threadIdx.x, w = (t >> 6) & 3, l = t & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
@@ -347,12 +350,13 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
   const int64_t plane = C * C * 2;
   if (t < 256) {
     const int t4 = 16 * w + 4 * g;      // this lane's four rows of every 64 x 16 product
-    Tok kf[NK], qf[BWD ? 1 : NK];
-    Frag tf[2], af[2];
+    Split<TP> kf[NK], qf[kHoldQ ? NK : 1];
+    Split<kFull> tf[2];
+    Split<kOut<T>> af[2];
     T v[4];
     f32x4 eg, el, be;
-    const auto load_token = [&](const void *tok, int c, int i) {
-      return ld8(static_cast<const T *>(tok) + (ck0 + (int64_t)c * p.key_heads) * (DK * C) + frag_of(w, i, NK));
+    const auto load_token = [&](const char *tok, int c, int i) {
+      return load_split<TP>(tok + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, frag_of(w, i, NK));
     };
     const auto load_values = [&](int c) {
       const int64_t o = (ch0 + (int64_t)c * p.heads) * C + t4;
@@ -366,28 +370,28 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
         v[r] = static_cast<const T *>(p.v)[tk * p.ldv + h * p.dv + sl * SL + li];
       }
     };
-    const auto load_square = [&](const char *m, int c, Frag (&f)[2]) {
+    const auto load_square = [&](const char *m, int c, auto &f) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)       // the second half is above the diagonal for the first two waves
         if (i == 0 || w >= 2)
-          f[i] = Sp<T>::ld(m + (ch0 + (int64_t)c * p.heads) * split_bytes<T>(C * C), plane, frag_of(w, i, 2));
+          f[i] = load_split<sizeof(f[0]) / 16>(m + (ch0 + (int64_t)c * p.heads) * kSquare, plane, frag_of(w, i, 2));
     };
     if (chunks > 0) {
 #pragma unroll
       for (int i = 0; i < NK; ++i) kf[i] = load_token(p.kp, 0, i);
       load_values(0);
       load_square(p.tm, 0, tf);
-      if (!BWD) {
+      if constexpr (kHoldQ) {
 #pragma unroll
         for (int i = 0; i < NK; ++i) qf[i] = load_token(p.qp, 0, i);
-        load_square(p.am, 0, af);
       }
+      if (!BWD) load_square(p.am, 0, af);
     }
     lds_barrier();
     for (int c = 0; c < chunks; ++c) {
       const int len = sq.len - c * C < C ? sq.len - c * C : C, nx = c + 1 < chunks ? c + 1 : c;
-      const SpTile<T, SL, DK> &W0 = s_w[BWD ? 0 : c & 1];
-      Sums<T> pa[2];
+      const SplitTile<kFull, SL, DK> &W0 = s_w[BWD ? 0 : c & 1];
+      Sums<kFull> pa[2];
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
         pa[i & 1].add(kf[i], W0.ld(li, 32 * i + 8 * g));
@@ -408,14 +412,18 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
       load_square(p.tm, nx, tf);
       lds_barrier();
       if (BWD) {
-        s_u.copy_t4(0, 16 * w, p.u + (ch0 + (int64_t)c * p.heads) * split_bytes<T>((int64_t)C * p.dv),
-                    (int64_t)C * p.dv * 2, frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
+        s_u.copy_t4(0, 16 * w, p.u + (ch0 + (int64_t)c * p.heads) * (C * p.dv * 2 * kFull), (int64_t)C * p.dv * 2,
+                    frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
       } else {
-        Sums<T> qa[2];
+        Sums<kOut<T>> qa[2];
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-          qa[i & 1].add(qf[i], W0.ld(li, 32 * i + 8 * g));
-          qf[i] = load_token(p.qp, nx, i);
+          if constexpr (kHoldQ) {
+            qa[i & 1].add(qf[i], W0.template ld<kOut<T>>(li, 32 * i + 8 * g));
+            qf[i] = load_token(p.qp, nx, i);
+          } else {
+            qa[i & 1].add(load_token(p.qp, c, i), W0.template ld<kOut<T>>(li, 32 * i + 8 * g));
+          }
         }
         f32x4 o = (qa[0].sum() + qa[1].sum()) * eg_now * p.scale;
         o = mm(af[0], s_u.ld(li, 8 * g), o);
@@ -431,10 +439,10 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
   } else {
     const int64_t wrow = (((int64_t)b * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
     f32x4 st[NT];
-    Tok ktf[NT][2];
+    Split<TP> ktf[NT][2];
     float ec = 0.0f;
     const auto load_transposed = [&](int c, int i, int x) {
-      return ld8(static_cast<const T *>(p.kt) + (ck0 + (int64_t)c * p.key_heads) * (DK * C) + frag_of(w * NT + i, x, 2));
+      return load_split<TP>(p.kt + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, frag_of(w * NT + i, x, 2));
     };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -452,19 +460,18 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
     for (int c = 0; c < chunks; ++c) {
       const int nx = c + 1 < chunks ? c + 1 : c;
       if (BWD) {    // the state before the chunk, dk x dv
-        char *o = p.w0t + (ch0 + (int64_t)c * p.heads) * split_bytes<T>((int64_t)DK * p.dv);
+        float *o = p.w0t + (ch0 + (int64_t)c * p.heads) * (DK * p.dv);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-          s_w[0].copy_t4(0, (w * NT + i) * 16, o, (int64_t)DK * p.dv * 2,
-                         frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
+          s_w[0].copy_t4(0, (w * NT + i) * 16, o + frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
       }
       lds_barrier();
       lds_barrier();
-      SpTile<T, SL, DK> &W1 = s_w[BWD ? 0 : ~c & 1];
-      const Frag u0 = s_ul.ld(li, 8 * g), u1 = s_ul.ld(li, 32 + 8 * g);
+      SplitTile<kFull, SL, DK> &W1 = s_w[BWD ? 0 : ~c & 1];
+      const Split<kFull> u0 = s_ul.ld(li, 8 * g), u1 = s_ul.ld(li, 32 + 8 * g);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        Sums<T> d;
+        Sums<kFull> d;
         d.add(ktf[i][0], u0);
         d.add(ktf[i][1], u1);
         st[i] = st[i] * ec + d.sum();

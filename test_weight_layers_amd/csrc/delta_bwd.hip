@@ -21,17 +21,18 @@ namespace {
 
 constexpr int C = kDeltaChunk;
 constexpr int SL = kDeltaSlice;
+constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 matrix
 
 // ------------------------------------------------------------------ state gradients
 // The reverse of the states kernel, with the same split, layout and order of loads.
 template <typename T, int DK>
 __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
-  __shared__ __attribute__((aligned(16))) SpTile<T, SL, DK> s_g;
-  __shared__ __attribute__((aligned(16))) SpTile<T, SL, C> s_go, s_goe[2], s_du, s_dr, s_dp;
-  typedef typename FragOf<T>::type Tok;
-  typedef typename Sp<T>::Frag Frag;
-  constexpr int NT = DK / 64, NK = DK / 32;
-  const int slices = p.dv / SL, item = xcd_item();
+  constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>;
+  __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, DK> s_g;
+  __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, C> s_goe[2], s_du, s_dr, s_dp;
+  __shared__ __attribute__((aligned(16))) SplitTile<TP, SL, C> s_go;
+  constexpr int64_t tokens = DK * C * 2 * TP, tplane = DK * C * 2;      // bytes of a chunk's tokens and a part
+  const int slices = p.dv / SL, item = xcd_item(gridDim.x);
   const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
   const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
@@ -46,15 +47,15 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
   const int64_t plane = C * C * 2;
   const int t4 = 16 * w + 4 * g;
 
-  Tok kf[NK], ktf[NT][2], qtf[NT][2];
-  Frag tf[2], af[2];
+  Split<TP> kf[NK], ktf[NT][2], qtf[NT][2];
+  Split<kFull> tf[2], af[2];
   T gv[4];
   float ec = 0.0f;
   f32x4 be, eg, el;
   const auto load_tokens = [&](int c0) {
-    const T *K = static_cast<const T *>(p.kp) + ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * (DK * C);
+    const char *K = p.kp + ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * tokens;
 #pragma unroll
-    for (int i = 0; i < NK; ++i) kf[i] = ld8(K + frag_of(w, i, NK));
+    for (int i = 0; i < NK; ++i) kf[i] = load_split<TP>(K, tplane, frag_of(w, i, NK));
   };
   const auto load_values = [&](int c0) {
     const int len = sq.len - c0 < C ? sq.len - c0 : C;
@@ -78,21 +79,20 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
     s_go.st4(li, t4, go);
     s_goe[buf].st4(li, t4, go * eg * p.scale);
   };
-  const auto load_square = [&](const char *m, int c0, Frag (&f)[2]) {
+  const auto load_square = [&](const char *m, int c0, Split<kFull> (&f)[2]) {
     const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
 #pragma unroll
     for (int i = 0; i < 2; ++i)         // the first half is below the diagonal for the last two waves
-      if (i == 1 || w < 2) f[i] = Sp<T>::ld(m + ch * split_bytes<T>(C * C), plane, frag_of(w, i, 2));
+      if (i == 1 || w < 2) f[i] = load_split<kFull>(m + ch * kSquare, plane, frag_of(w, i, 2));
   };
   const auto load_transposed = [&](int c0) {
-    const int64_t o = ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * (DK * C);
-    const T *kt = static_cast<const T *>(p.kt) + o, *qt = static_cast<const T *>(p.qt) + o;
+    const int64_t o = ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * tokens;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        ktf[i][x] = ld8(kt + frag_of(w * NT + i, x, 2));
-        qtf[i][x] = ld8(qt + frag_of(w * NT + i, x, 2));
+        ktf[i][x] = load_split<TP>(p.kt + o, tplane, frag_of(w * NT + i, x, 2));
+        qtf[i][x] = load_split<TP>(p.qt + o, tplane, frag_of(w * NT + i, x, 2));
       }
   };
   const int first = sq.len > 0 ? (sq.len - 1) / C * C : -1;
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
     const int len = sq.len - c0 < C ? sq.len - c0 : C, nx = c0 > 0 ? c0 - C : 0;
     const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
     const int64_t tok0 = sq.start + c0;
-    Sums<T> kg[2];
+    Sums<kFull> kg[2];
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
       kg[i & 1].add(kf[i], s_g.ld(li, 32 * i + 8 * g));
@@ -118,11 +118,10 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
     f32x4 du = kg[0].sum() + kg[1].sum();
     load_tokens(nx);
     {                                   // the gradient after the chunk, dk x dv
-      char *o = p.gwt + ch * split_bytes<T>((int64_t)DK * p.dv);
+      float *o = p.gwt + ch * (DK * p.dv);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        s_g.copy_t4(0, (w * NT + i) * 16, o, (int64_t)DK * p.dv * 2,
-                    frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
+        s_g.copy_t4(0, (w * NT + i) * 16, o + frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) du[r] = t4 + r < len ? du[r] * el[r] : 0.0f;
@@ -149,8 +148,8 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
         static_cast<T *>(p.gv)[(tok0 + t4 + r) * p.ldgv + h * p.dv + sl * SL + li] = from_f32<T>(be_now[r] * dr[r]);
     lds_barrier();
     {
-      const Frag p0 = s_dp.ld(li, 8 * g), p1 = s_dp.ld(li, 32 + 8 * g);
-      const Frag g0 = s_goe[buf].ld(li, 8 * g), g1 = s_goe[buf].ld(li, 32 + 8 * g);
+      const Split<kFull> p0 = s_dp.ld(li, 8 * g), p1 = s_dp.ld(li, 32 + 8 * g);
+      const Split<kFull> g0 = s_goe[buf].ld(li, 8 * g), g1 = s_goe[buf].ld(li, 32 + 8 * g);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         st[i] = mm(ktf[i][0], p0, st[i] * ec_now);
@@ -161,7 +160,7 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
       }
     }
     load_transposed(nx);
-    s_dr.copy_t4(0, 16 * w, p.dr + ch * split_bytes<T>((int64_t)C * p.dv), (int64_t)C * p.dv * 2,
+    s_dr.copy_t4(0, 16 * w, p.dr + ch * (C * p.dv * 2 * kFull), (int64_t)C * p.dv * 2,
                  frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
     store_go(nx, buf ^ 1);
     lds_barrier();
@@ -179,25 +178,23 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
 // of 6 heads of 128).
 template <typename T, int DK>
 __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kernel(DeltaParams p) {
-  __shared__ __attribute__((aligned(16))) SpTile<T, C, C> s_x, s_xt, s_y, s_yt;
+  constexpr int NT = DK / 64, TP = kTok<T>;
+  __shared__ __attribute__((aligned(16))) SplitTile<kOut<T>, C, C> s_x, s_xt, s_y, s_yt;
   __shared__ float s_row[3][4][C];      // partials of q.(go W0), k.(dR W0), k.(U G)
   __shared__ float s_rs[2][C], s_db[2][C], s_cs[4][C], s_red[4];
-  typedef typename Sp<T>::Frag Frag;
-  constexpr int NT = DK / 64;
-  const int item = xcd_item(), h = item % p.heads, c = item / p.heads;
+  const int item = xcd_item(gridDim.x), h = item % p.heads, c = item / p.heads;
   const DeltaChunk ck = chunk_of(p, c);
   if (ck.len == 0) return;
   const int t = threadIdx.x, w4 = (t >> 6) & 3, half = t >> 8, l = t & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
   const int64_t ch = (int64_t)c * p.heads + h;
   const int last = ck.len - 1, nv = p.dv / 32;
-  const int64_t to = ((int64_t)c * p.key_heads + kh) * (DK * C);
-  const T *K = static_cast<const T *>(p.kp) + to, *Q = static_cast<const T *>(p.qp) + to;
-  const T *KT = static_cast<const T *>(p.kt) + to, *QT = static_cast<const T *>(p.qt) + to;
+  const int64_t to = ((int64_t)c * p.key_heads + kh) * (DK * C * 2 * TP);
+  constexpr int64_t tplane = DK * C * 2;
+  const char *K = p.kp + to, *Q = p.qp + to, *KT = p.kt + to, *QT = p.qt + to;
   const T *V = static_cast<const T *>(p.v) + (int64_t)ck.tok0 * p.ldv + h * p.dv;
-  const T *GO = static_cast<const T *>(p.gop) + ch * C * p.dv;
-  const int64_t uo = ch * split_bytes<T>((int64_t)C * p.dv), up = (int64_t)C * p.dv * 2;
-  const char *U = p.u + uo, *DR = p.dr + uo;
+  const int64_t up = (int64_t)C * p.dv * 2;
+  const char *GO = p.gop + ch * up * TP, *U = p.u + ch * up * kFull, *DR = p.dr + ch * up * kFull;
 
   // ---- X, Y and the sums over them: row tile w4, column tiles 2 half, 2 half + 1
   {
@@ -207,11 +204,11 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
     const int ra = 16 * w4 + li, rac = ra < last ? ra : last;
 #pragma unroll 2
     for (int i = 0; i < DK / 32; ++i) {
-      const auto ka = ld8(K + frag_of(w4, i, DK / 32)), qa = ld8(Q + frag_of(w4, i, DK / 32));
+      const auto ka = load_split<TP>(K, tplane, frag_of(w4, i, DK / 32)), qa = load_split<TP>(Q, tplane, frag_of(w4, i, DK / 32));
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (2 * half + j > w4) continue;                // above the diagonal
-        const auto kb = ld8(K + frag_of(2 * half + j, i, DK / 32));
+        const auto kb = load_split<TP>(K, tplane, frag_of(2 * half + j, i, DK / 32));
         kk[j] = mm(ka, kb, kk[j]);
         qk[j] = mm(qa, kb, qk[j]);
       }
@@ -219,17 +216,17 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
     float drv = 0.0f;                                   // dR_i . V_i
 #pragma unroll 2
     for (int i = 0; i < nv; ++i) {
-      const auto ga = ld8(GO + frag_of(w4, i, nv));
-      const Frag ra_f = Sp<T>::ld(DR, up, frag_of(w4, i, nv));
+      const auto ga = load_split<TP>(GO, up, frag_of(w4, i, nv));
+      const auto ra_f = load_split<kFull>(DR, up, frag_of(w4, i, nv));
       if (half == 0) {
         const auto va = ld8(V + (int64_t)rac * p.ldv + 32 * i + 8 * g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) drv += Sp<T>::at(ra_f, e) * (float)va[e];
+        for (int e = 0; e < 8; ++e) drv += at(ra_f, e) * (float)va[e];
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (2 * half + j > w4) continue;
-        const Frag ub = Sp<T>::ld(U, up, frag_of(2 * half + j, i, nv));
+        const auto ub = load_split<kFull>(U, up, frag_of(2 * half + j, i, nv));
         da[j] = mm(ga, ub, da[j]);
         dl[j] = mm(ra_f, ub, dl[j]);
       }
@@ -290,7 +287,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
 #pragma unroll
     for (int r = 0; r < 4; ++r) dq_dot[a][r] = dr_dot[a][r] = du_dot[a][r] = 0.0f;
   float wg = 0.0f;                                      // <W0, G>, by the first half
-  const int64_t so = ch * split_bytes<T>((int64_t)DK * p.dv), sp = (int64_t)DK * p.dv * 2;
+  const float *W0 = p.w0t + ch * (DK * p.dv), *G = p.gwt + ch * (DK * p.dv);
 #pragma unroll 1
   for (int i = 0; i < NT; ++i) {
     int zero = 0;                       // opaque: keeps what is the same for every tile out of registers between them
@@ -301,20 +298,21 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
     for (int a = 0; a < 2; ++a) aq[a] = ar[a] = au[a] = zero4();
 #pragma unroll 2
     for (int ks = 0; ks < nv; ++ks) {
-      const Frag wf = Sp<T>::ld(p.w0t + so, sp, frag_of(rt, ks, nv)), gf = Sp<T>::ld(p.gwt + so, sp, frag_of(rt, ks, nv));
+      const f32x8 w8 = ld8(W0 + frag_of(rt, ks, nv)), g8 = ld8(G + frag_of(rt, ks, nv));
       if (half == 0)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wg += Sp<T>::at(wf, e) * Sp<T>::at(gf, e);
+        for (int e = 0; e < 8; ++e) wg += w8[e] * g8[e];
+      const auto wf = split_of<kFull>(w8), gf = split_of<kFull>(g8);
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         const int f = frag_of(2 * half + a, ks, nv) + zero;
-        aq[a] = mm(ld8(GO + f), wf, aq[a]);
-        ar[a] = mm(Sp<T>::ld(DR, up, f), wf, ar[a]);
-        au[a] = mm(Sp<T>::ld(U, up, f), gf, au[a]);
+        aq[a] = mm(load_split<TP>(GO, up, f), wf, aq[a]);
+        ar[a] = mm(load_split<kFull>(DR, up, f), wf, ar[a]);
+        au[a] = mm(load_split<kFull>(U, up, f), gf, au[a]);
       }
     }
-    const auto k0 = ld8(KT + frag_of(rt, 0, 2)), k1 = ld8(KT + frag_of(rt, 1, 2));
-    const auto q0 = ld8(QT + frag_of(rt, 0, 2)), q1 = ld8(QT + frag_of(rt, 1, 2));
+    const auto k0 = load_split<TP>(KT, tplane, frag_of(rt, 0, 2)), k1 = load_split<TP>(KT, tplane, frag_of(rt, 1, 2));
+    const auto q0 = load_split<TP>(QT, tplane, frag_of(rt, 0, 2)), q1 = load_split<TP>(QT, tplane, frag_of(rt, 1, 2));
     const int col = rt * 16 + li;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
@@ -332,15 +330,25 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
       const f32x4 eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + r0);
       const f32x4 el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + r0);
       const f32x4 be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + r0);
-      const T *kv = KT + frag_at(col, r0, 2), *qv = QT + frag_at(col, r0, 2);     // four tokens' elements
+      f32x4 kv = zero4(), qv = zero4();             // four tokens' elements
+#pragma unroll
+      for (int x = TP - 1; x >= 0; --x) {
+        const int64_t e = frag_at(col, r0, 2) * 2 + x * tplane;
+        const bf16x4 kx = *reinterpret_cast<const bf16x4 *>(KT + e), qx = *reinterpret_cast<const bf16x4 *>(QT + e);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          kv[r] += (float)kx[r];
+          qv[r] += (float)qx[r];
+        }
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (r0 + r >= ck.len) continue;
         const int64_t tk = ck.tok0 + r0 + r;
         const float dqi = p.scale * eg[r] * aq[a][r], dui = el[r] * au[a][r];
-        dq_dot[a][r] += to_f32(qv[r]) * dqi;
-        dr_dot[a][r] += to_f32(kv[r]) * ar[a][r];
-        du_dot[a][r] += to_f32(kv[r]) * dui;
+        dq_dot[a][r] += qv[r] * dqi;
+        dr_dot[a][r] += kv[r] * ar[a][r];
+        du_dot[a][r] += kv[r] * dui;
         const float dq = dqi + xq[r], dk = dui - be[r] * eg[r] * ar[a][r] + xk[r];
         if (p.gqp) {
           p.gqp[(tk * p.heads + h) * DK + col] = dq;
