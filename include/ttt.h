@@ -311,11 +311,11 @@ int ttt_stream_ex(int32_t heads, int32_t d, int32_t m,
  *   and to a running maximum, so that any values name disjoint rows.  A sequence may be
  *   empty (its state passes through).  Rows of no sequence are not read; of o they are
  *   left as they were, or set to zero with TTT_DELTA_ZERO_UNUSED; gradients of them are zero.
- * Precision: fp32 states and sums.  fp32 tokens run on fp32 MFMA.  Beside bf16 tokens the
- *   computed operands keep 17 bits (two bf16 parts), so states and rate gradients are good
- *   to about 1e-5 relative; o and token gradients are rounded to bf16 once.
+ * Precision: fp32 states and sums; products take fp32 operands as three bf16 parts (24 bits),
+ *   what only reaches bf16 outputs as two.  States, rate gradients and fp32 outputs are as exact
+ *   as fp32 arithmetic gives; bf16 outputs are rounded once.
  * Deterministic: the same inputs give the same bits.  n <= 2^31 - 65; chunks x H and
- *   sequences x H x dv/16 below 2^24.
+ *   sequences x H x dv/16 below 2^24; in the chunked calls 64 rows span < 2 GiB.
  */
 enum { TTT_DELTA_ZERO_UNUSED = 1 };
 /* Bytes of workspace of ttt_delta (backward = 0) or ttt_delta_backward (backward = 1). */

@@ -36,6 +36,15 @@ int check_row(const Rows &r, int64_t n) {
   return TTT_OK;
 }
 
+// The delta-rule kernels reach the 64 rows of a chunk by 32-bit offsets.
+int check_chunk_row(const Rows &r, int64_t n) {
+  const int st = check_row(r, n);
+  if (st) return st;
+  if (r.ld * (int64_t)r.es >= (int64_t(1) << 31) / kDeltaChunk)
+    return fail(TTT_EUNSUPPORTED, "row stride of %s too large (64 rows must span < 2 GiB)", r.name);
+  return TTT_OK;
+}
+
 // Whether two sets of n rows share bytes.  Column slices of one buffer (equal strides) do not
 // where their columns are apart.
 bool rows_overlap(const Rows &a, const Rows &b, int64_t n) {
@@ -141,7 +150,7 @@ int delta_params(int H, int Hk, int dk, int dv, const float *w, const Rows &q, c
   if (!std::isfinite(scale)) return fail(TTT_EINVAL, "scale must be finite");
   if (!w) return fail(TTT_EINVAL, "w is null");
   if ((st = check_aligned(w, "w"))) return st;
-  if ((st = check_row(q, n)) || (st = check_row(k, n)) || (st = check_row(v, n))) return st;
+  if ((st = check_chunk_row(q, n)) || (st = check_chunk_row(k, n)) || (st = check_chunk_row(v, n))) return st;
   if (n > 0 && !beta) return fail(TTT_EINVAL, "beta is null");
   if (bhs < 0 || dhs < 0) return fail(TTT_EINVAL, "head strides must be >= 0");
   if ((st = check_ws(ws, ws_bytes, P.total))) return st;
@@ -204,7 +213,7 @@ int ttt_delta(int32_t heads, int32_t key_heads, int32_t dk, int32_t dv, const fl
   if ((st = delta_params(heads, key_heads, dk, dv, w, rq, rk, rv, beta, beta_head_stride, decay, decay_head_stride, n,
                          cu_seqlens, sequences, scale, dtype, false, workspace, workspace_bytes, &p)))
     return st;
-  if ((st = check_row(ro, n)) || (st = check_aligned(w_out, "w_out"))) return st;
+  if ((st = check_chunk_row(ro, n)) || (st = check_aligned(w_out, "w_out"))) return st;
   if (!w_out) return fail(TTT_EINVAL, "w_out is null");
   const size_t wb = (size_t)sequences * heads * dv * dk * 4;
   if (w != w_out && overlap(w, wb, w_out, wb)) return fail(TTT_EINVAL, "w_out must equal w or not overlap it");
@@ -235,9 +244,9 @@ int ttt_delta_backward(int32_t heads, int32_t key_heads, int32_t dk, int32_t dv,
   if ((st = delta_params(heads, key_heads, dk, dv, w, in[0], in[1], in[2], beta, beta_head_stride, decay,
                          decay_head_stride, n, cu_seqlens, sequences, scale, dtype, true, workspace, workspace_bytes, &p)))
     return st;
-  if ((st = check_row(in[3], n))) return st;
+  if ((st = check_chunk_row(in[3], n))) return st;
   for (const Rows &r : out)
-    if ((st = check_row(r, n))) return st;
+    if ((st = check_chunk_row(r, n))) return st;
   if (!grad_w) return fail(TTT_EINVAL, "grad_w is null");
   if ((st = check_aligned(grad_w, "grad_w")) || (st = check_aligned(grad_w_out, "grad_w_out"))) return st;
   if (n > 0 && !grad_beta) return fail(TTT_EINVAL, "grad_beta is null");

@@ -342,39 +342,37 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
   constexpr bool kHoldQ = !BWD && (TP == 1 || DK < 256);
   const int slices = p.dv / SL, item = xcd_item(gridDim.x);
   const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
-  const int t = threadIdx.x, w = (t >> 6) & 3, l = t & 63, g = l >> 4, li = l & 15;
+  const int wave = wave_id(), w = wave & 3, l = threadIdx.x & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
   const DeltaSeq sq = seq_of(p, b);
   const int chunks = (sq.len + C - 1) / C;
   const int64_t ch0 = (int64_t)sq.chunk0 * p.heads + h, ck0 = (int64_t)sq.chunk0 * p.key_heads + kh;
   const int64_t plane = C * C * 2;
-  if (t < 256) {
+  if (wave < 4) {
     const int t4 = 16 * w + 4 * g;      // this lane's four rows of every 64 x 16 product
     Split<TP> kf[NK], qf[kHoldQ ? NK : 1];
     Split<kFull> tf[2];
     Split<kOut<T>> af[2];
     T v[4];
     f32x4 eg, el, be;
+    const Rows4<T> v_rows(t4, li, p.ldv), o_rows(t4, li, BWD ? 0 : p.ldo);
     const auto load_token = [&](const char *tok, int c, int i) {
-      return load_split<TP>(tok + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, frag_of(w, i, NK));
+      return load_frag<TP>(tok + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, w * NK + i);
     };
     const auto load_values = [&](int c) {
       const int64_t o = (ch0 + (int64_t)c * p.heads) * C + t4;
       eg = *reinterpret_cast<const f32x4 *>(p.eg + o);
       el = *reinterpret_cast<const f32x4 *>(p.el + o);
       be = *reinterpret_cast<const f32x4 *>(p.be + o);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int x = c * C + t4 + r;
-        const int64_t tk = (int64_t)sq.start + (x < sq.len ? x : sq.len - 1);
-        v[r] = static_cast<const T *>(p.v)[tk * p.ldv + h * p.dv + sl * SL + li];
-      }
+      v_rows.load(static_cast<const T *>(p.v) + ((int64_t)sq.start + c * C) * p.ldv + h * p.dv + sl * SL, t4,
+                  sq.len - c * C, v);
     };
     const auto load_square = [&](const char *m, int c, auto &f) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)       // the second half is above the diagonal for the first two waves
-        if (i == 0 || w >= 2)
-          f[i] = load_split<sizeof(f[0]) / 16>(m + (ch0 + (int64_t)c * p.heads) * kSquare, plane, frag_of(w, i, 2));
+      // (the second half is zero for the first two waves, whose products leave it out; loads under a
+      // condition would make every later wait one for all loads)
+      for (int i = 0; i < 2; ++i)
+        f[i] = load_frag<sizeof(f[0]) / 16>(m + (ch0 + (int64_t)c * p.heads) * kSquare, plane, w * 2 + i);
     };
     if (chunks > 0) {
 #pragma unroll
@@ -391,22 +389,23 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
     for (int c = 0; c < chunks; ++c) {
       const int len = sq.len - c * C < C ? sq.len - c * C : C, nx = c + 1 < chunks ? c + 1 : c;
       const SplitTile<kFull, SL, DK> &W0 = s_w[BWD ? 0 : c & 1];
-      Sums<kFull> pa[2];
+      Sums<kFull> pa;
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
-        pa[i & 1].add(kf[i], W0.ld(li, 32 * i + 8 * g));
+        pa.add(kf[i], W0.ld(li, 32 * i + 8 * g));
         kf[i] = load_token(p.kp, nx, i);
       }
-      f32x4 rr = pa[0].sum() + pa[1].sum();
+      f32x4 rr = pa.sum();
 #pragma unroll
       for (int r = 0; r < 4; ++r) rr[r] = t4 + r < len ? be[r] * (to_f32(v[r]) - eg[r] * rr[r]) : 0.0f;
       const f32x4 eg_now = eg, el_now = el;
       s_r.st4(li, t4, rr);
       lds_barrier();
       load_values(nx);
-      f32x4 u = zero4();
-      u = mm(tf[0], s_r.ld(li, 8 * g), u);
-      if (w >= 2) u = mm(tf[1], s_r.ld(li, 32 + 8 * g), u);
+      Sums<kFull> tr;
+      tr.add(tf[0], s_r.ld(li, 8 * g));
+      if (w >= 2) tr.add(tf[1], s_r.ld(li, 32 + 8 * g));
+      const f32x4 u = tr.sum();
       s_ul.st4(li, t4, u * el_now);
       s_u.st4(li, t4, u);
       load_square(p.tm, nx, tf);
@@ -425,14 +424,12 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
             qa[i & 1].add(load_token(p.qp, c, i), W0.template ld<kOut<T>>(li, 32 * i + 8 * g));
           }
         }
-        f32x4 o = (qa[0].sum() + qa[1].sum()) * eg_now * p.scale;
-        o = mm(af[0], s_u.ld(li, 8 * g), o);
-        if (w >= 2) o = mm(af[1], s_u.ld(li, 32 + 8 * g), o);
+        Sums<kOut<T>> au;
+        au.add(af[0], s_u.ld(li, 8 * g));
+        if (w >= 2) au.add(af[1], s_u.ld(li, 32 + 8 * g));
+        const f32x4 o = (qa[0].sum() + qa[1].sum()) * eg_now * p.scale + au.sum();
         load_square(p.am, nx, af);
-        T *out = static_cast<T *>(p.o) + ((int64_t)sq.start + c * C + t4) * p.ldo + h * p.dv + sl * SL + li;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (t4 + r < len) out[r * p.ldo] = from_f32<T>(o[r]);
+        o_rows.store(static_cast<T *>(p.o) + ((int64_t)sq.start + c * C) * p.ldo + h * p.dv + sl * SL, t4, len, o);
       }
       lds_barrier();
     }
@@ -442,7 +439,7 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
     Split<TP> ktf[NT][2];
     float ec = 0.0f;
     const auto load_transposed = [&](int c, int i, int x) {
-      return load_split<TP>(p.kt + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, frag_of(w * NT + i, x, 2));
+      return load_frag<TP>(p.kt + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, (w * NT + i) * 2 + x);
     };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {

@@ -24,9 +24,11 @@ constexpr int SL = kDeltaSlice;
 constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 matrix
 
 // ------------------------------------------------------------------ state gradients
-// The reverse of the states kernel, with the same split, layout and order of loads.
+// The reverse of the states kernel, with the same split, layout, waves and order of loads:
+//   rows: K G^T, dU        rows: dR = T^T dU;  state: G <- e^gamma_last G + (scale eg o go)^T Q
+//   state: G += dP^T K;  rows: the next chunk's go
 template <typename T, int DK>
-__global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
+__global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delta_gstate_kernel(DeltaParams p) {
   constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>;
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, DK> s_g;
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, C> s_goe[2], s_du, s_dr, s_dp;
@@ -34,139 +36,150 @@ __global__ __launch_bounds__(256, 1) void delta_gstate_kernel(DeltaParams p) {
   constexpr int64_t tokens = DK * C * 2 * TP, tplane = DK * C * 2;      // bytes of a chunk's tokens and a part
   const int slices = p.dv / SL, item = xcd_item(gridDim.x);
   const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
-  const int t = threadIdx.x, w = t >> 6, l = t & 63, g = l >> 4, li = l & 15;
+  const int wave = wave_id(), w = wave & 3, l = threadIdx.x & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
   const DeltaSeq sq = seq_of(p, b);
-  const int64_t wrow = (((int64_t)b * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
-  f32x4 st[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    st[i] = p.gw_out ? *reinterpret_cast<const f32x4 *>(p.gw_out + wrow + 16 * i) : zero4();
-    s_g.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
-  }
+  const int chunks = (sq.len + C - 1) / C;
+  const int64_t ch0 = (int64_t)sq.chunk0 * p.heads + h, ck0 = (int64_t)sq.chunk0 * p.key_heads + kh;
   const int64_t plane = C * C * 2;
-  const int t4 = 16 * w + 4 * g;
-
-  Split<TP> kf[NK], ktf[NT][2], qtf[NT][2];
-  Split<kFull> tf[2], af[2];
-  T gv[4];
-  float ec = 0.0f;
-  f32x4 be, eg, el;
-  const auto load_tokens = [&](int c0) {
-    const char *K = p.kp + ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * tokens;
+  if (wave < 4) {
+    const int t4 = 16 * w + 4 * g;
+    Split<TP> kf[NK];
+    Split<kFull> tf[2], af[2];
+    T gv[4];
+    f32x4 be, eg, el;
+    const Rows4<T> go_rows(t4, li, p.ldgo), gv_rows(t4, li, p.ldgv);
+    const auto load_token = [&](int c, int i) {
+      return load_frag<TP>(p.kp + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, w * NK + i);
+    };
+    const auto load_values = [&](int c) {
+      const int64_t o = (ch0 + (int64_t)c * p.heads) * C + t4;
+      eg = *reinterpret_cast<const f32x4 *>(p.eg + o);
+      el = *reinterpret_cast<const f32x4 *>(p.el + o);
+      be = *reinterpret_cast<const f32x4 *>(p.be + o);
+      go_rows.load(static_cast<const T *>(p.go) + ((int64_t)sq.start + c * C) * p.ldgo + h * p.dv + sl * SL, t4,
+                   sq.len - c * C, gv);
+    };
+    // the chunk's go, 0 past its end, to LDS (as it is, and as the state's update takes it)
+    const auto store_go = [&](int c, int buf) {
+      f32x4 go;
 #pragma unroll
-    for (int i = 0; i < NK; ++i) kf[i] = load_split<TP>(K, tplane, frag_of(w, i, NK));
-  };
-  const auto load_values = [&](int c0) {
-    const int len = sq.len - c0 < C ? sq.len - c0 : C;
-    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
-    eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + t4);
-    el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + t4);
-    be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + t4);
-    ec = p.eg[ch * C + C - 1];
+      for (int r = 0; r < 4; ++r) go[r] = c * C + t4 + r < sq.len ? to_f32(gv[r]) : 0.0f;
+      s_go.st4(li, t4, go);
+      s_goe[buf].st4(li, t4, go * eg * p.scale);
+    };
+    const auto load_square = [&](const char *m, int c, Split<kFull> (&f)[2]) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t tk = (int64_t)sq.start + c0 + (t4 + r < len ? t4 + r : len - 1);
-      gv[r] = static_cast<const T *>(p.go)[tk * p.ldgo + h * p.dv + sl * SL + li];
+      for (int i = 0; i < 2; ++i)       // (the first half is zero for the last two waves)
+        f[i] = load_frag<kFull>(m + (ch0 + (int64_t)c * p.heads) * kSquare, plane, w * 2 + i);
+    };
+    if (chunks > 0) {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) kf[i] = load_token(chunks - 1, i);
+      load_values(chunks - 1);
+      load_square(p.am, chunks - 1, af);
+      load_square(p.tt, chunks - 1, tf);
+      store_go(chunks - 1, (chunks - 1) & 1);
     }
-  };
-  // the chunk's go, 0 past its end, to LDS (as it is, and as the state's update takes it)
-  const auto store_go = [&](int c0, int buf) {
-    const int len = sq.len - c0 < C ? sq.len - c0 : C;
-    f32x4 go;
+    lds_barrier();
+    for (int c = chunks - 1; c >= 0; --c) {
+      const int nx = c > 0 ? c - 1 : 0, left = sq.len - c * C;
+      Sums<kFull> kg;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) go[r] = t4 + r < len ? to_f32(gv[r]) : 0.0f;
-    s_go.st4(li, t4, go);
-    s_goe[buf].st4(li, t4, go * eg * p.scale);
-  };
-  const auto load_square = [&](const char *m, int c0, Split<kFull> (&f)[2]) {
-    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)         // the first half is below the diagonal for the last two waves
-      if (i == 1 || w < 2) f[i] = load_split<kFull>(m + ch * kSquare, plane, frag_of(w, i, 2));
-  };
-  const auto load_transposed = [&](int c0) {
-    const int64_t o = ((int64_t)(sq.chunk0 + c0 / C) * p.key_heads + kh) * tokens;
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        ktf[i][x] = load_split<TP>(p.kt + o, tplane, frag_of(w * NT + i, x, 2));
-        qtf[i][x] = load_split<TP>(p.qt + o, tplane, frag_of(w * NT + i, x, 2));
+      for (int i = 0; i < NK; ++i) {
+        kg.add(kf[i], s_g.ld(li, 32 * i + 8 * g));
+        kf[i] = load_token(nx, i);
       }
-  };
-  const int first = sq.len > 0 ? (sq.len - 1) / C * C : -1;
-  if (first >= 0) {
-    load_tokens(first);
-    load_values(first);
-    load_square(p.am, first, af);
-    load_square(p.tt, first, tf);
-    load_transposed(first);
-    store_go(first, 0);
-  }
-  lds_barrier();
-  int buf = 0;
-  for (int c0 = first; c0 >= 0; c0 -= C, buf ^= 1) {
-    const int len = sq.len - c0 < C ? sq.len - c0 : C, nx = c0 > 0 ? c0 - C : 0;
-    const int64_t ch = (int64_t)(sq.chunk0 + c0 / C) * p.heads + h;
-    const int64_t tok0 = sq.start + c0;
-    Sums<kFull> kg[2];
+      f32x4 du = kg.sum();
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      kg[i & 1].add(kf[i], s_g.ld(li, 32 * i + 8 * g));
+      for (int r = 0; r < 4; ++r) du[r] = t4 + r < left ? du[r] * el[r] : 0.0f;
+      Sums<kFull> ag;
+      if (w < 2) ag.add(af[0], s_go.ld(li, 8 * g));
+      ag.add(af[1], s_go.ld(li, 32 + 8 * g));
+      load_square(p.am, nx, af);
+      s_du.st4(li, t4, du + ag.sum());
+      lds_barrier();
+      Sums<kFull> td;
+      if (w < 2) td.add(tf[0], s_du.ld(li, 8 * g));
+      td.add(tf[1], s_du.ld(li, 32 + 8 * g));
+      const f32x4 dr = td.sum();
+      load_square(p.tt, nx, tf);
+      s_dp.st4(li, t4, dr * be * eg * -1.0f);
+      s_dr.st4(li, t4, dr);
+      const f32x4 dv = be * dr;
+      load_values(nx);
+      lds_barrier();
+      gv_rows.store(static_cast<T *>(p.gv) + ((int64_t)sq.start + c * C) * p.ldgv + h * p.dv + sl * SL, t4, left, dv);
+      s_dr.copy_t4(0, 16 * w, p.dr + (ch0 + (int64_t)c * p.heads) * (C * p.dv * 2 * kFull), (int64_t)C * p.dv * 2,
+                   frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
+      store_go(nx, ~c & 1);
+      lds_barrier();
     }
-    f32x4 du = kg[0].sum() + kg[1].sum();
-    load_tokens(nx);
-    {                                   // the gradient after the chunk, dk x dv
-      float *o = p.gwt + ch * (DK * p.dv);
+  } else {
+    const int64_t wrow = (((int64_t)b * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
+    f32x4 st[NT];
+    Split<TP> ktf[NT][2], qtf[NT][2];
+    float ec = 0.0f;
+    const auto load_transposed = [&](const char *m, int c, int i, int x) {
+      return load_frag<TP>(m + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, (w * NT + i) * 2 + x);
+    };
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      st[i] = p.gw_out ? *reinterpret_cast<const f32x4 *>(p.gw_out + wrow + 16 * i) : zero4();
+      s_g.st4(li, (w * NT + i) * 16 + 4 * g, st[i]);
+    }
+    if (chunks > 0) {
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        s_g.copy_t4(0, (w * NT + i) * 16, o + frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          qtf[i][x] = load_transposed(p.qt, chunks - 1, i, x);
+          ktf[i][x] = load_transposed(p.kt, chunks - 1, i, x);
+        }
+      ec = p.eg[(ch0 + (int64_t)(chunks - 1) * p.heads) * C + C - 1];
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) du[r] = t4 + r < len ? du[r] * el[r] : 0.0f;
-    if (w < 2) du = mm(af[0], s_go.ld(li, 8 * g), du);
-    du = mm(af[1], s_go.ld(li, 32 + 8 * g), du);
-    load_square(p.am, nx, af);
-    s_du.st4(li, t4, du);
-    const float ec_now = ec;
-    f32x4 dp;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) dp[r] = -be[r] * eg[r];
-    const f32x4 be_now = be;
-    load_values(nx);
     lds_barrier();
-    f32x4 dr = zero4();
-    if (w < 2) dr = mm(tf[0], s_du.ld(li, 8 * g), dr);
-    dr = mm(tf[1], s_du.ld(li, 32 + 8 * g), dr);
-    load_square(p.tt, nx, tf);
-    s_dp.st4(li, t4, dr * dp);
-    s_dr.st4(li, t4, dr);
+    for (int c = chunks - 1; c >= 0; --c) {
+      const int nx = c > 0 ? c - 1 : 0;
+      {                                 // the gradient after the chunk, dk x dv
+        float *o = p.gwt + (ch0 + (int64_t)c * p.heads) * (DK * p.dv);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (t4 + r < len)
-        static_cast<T *>(p.gv)[(tok0 + t4 + r) * p.ldgv + h * p.dv + sl * SL + li] = from_f32<T>(be_now[r] * dr[r]);
-    lds_barrier();
-    {
+        for (int i = 0; i < NT; ++i)
+          s_g.copy_t4(0, (w * NT + i) * 16, o + frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
+      }
+      {
+        const Split<kFull> g0 = s_goe[c & 1].ld(li, 8 * g), g1 = s_goe[c & 1].ld(li, 32 + 8 * g);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          Sums<kFull> d;
+          d.add(qtf[i][0], g0);
+          d.add(qtf[i][1], g1);
+          st[i] = st[i] * ec + d.sum();
+#pragma unroll
+          for (int x = 0; x < 2; ++x) qtf[i][x] = load_transposed(p.qt, nx, i, x);
+        }
+        ec = p.eg[(ch0 + (int64_t)nx * p.heads) * C + C - 1];
+      }
+      lds_barrier();
+      lds_barrier();
       const Split<kFull> p0 = s_dp.ld(li, 8 * g), p1 = s_dp.ld(li, 32 + 8 * g);
-      const Split<kFull> g0 = s_goe[buf].ld(li, 8 * g), g1 = s_goe[buf].ld(li, 32 + 8 * g);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        st[i] = mm(ktf[i][0], p0, st[i] * ec_now);
-        st[i] = mm(ktf[i][1], p1, st[i]);
-        st[i] = mm(qtf[i][0], g0, st[i]);
-        st[i] = mm(qtf[i][1], g1, st[i]);
-        s_g.st4(li, w * (DK / 4) + 16 * i + 4 * g, st[i]);
+        Sums<kFull> d;
+        d.add(ktf[i][0], p0);
+        d.add(ktf[i][1], p1);
+        st[i] += d.sum();
+        s_g.st4(li, (w * NT + i) * 16 + 4 * g, st[i]);
       }
-    }
-    load_transposed(nx);
-    s_dr.copy_t4(0, 16 * w, p.dr + ch * (C * p.dv * 2 * kFull), (int64_t)C * p.dv * 2,
-                 frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
-    store_go(nx, buf ^ 1);
-    lds_barrier();
-  }
+      lds_barrier();
 #pragma unroll
-  for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(p.gw + wrow + 16 * i) = st[i];
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(p.kt, nx, i, x);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(p.gw + wrow + 16 * i) = st[i];
+  }
 }
 
 // ------------------------------------------------------------------ token gradients
@@ -185,7 +198,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
   const int item = xcd_item(gridDim.x), h = item % p.heads, c = item / p.heads;
   const DeltaChunk ck = chunk_of(p, c);
   if (ck.len == 0) return;
-  const int t = threadIdx.x, w4 = (t >> 6) & 3, half = t >> 8, l = t & 63, g = l >> 4, li = l & 15;
+  const int t = threadIdx.x, wave = wave_id(), w4 = wave & 3, half = wave >> 2, l = t & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
   const int64_t ch = (int64_t)c * p.heads + h;
   const int last = ck.len - 1, nv = p.dv / 32;
@@ -204,11 +217,11 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
     const int ra = 16 * w4 + li, rac = ra < last ? ra : last;
 #pragma unroll 2
     for (int i = 0; i < DK / 32; ++i) {
-      const auto ka = load_split<TP>(K, tplane, frag_of(w4, i, DK / 32)), qa = load_split<TP>(Q, tplane, frag_of(w4, i, DK / 32));
+      const auto ka = load_frag<TP>(K, tplane, w4 * (DK / 32) + i), qa = load_frag<TP>(Q, tplane, w4 * (DK / 32) + i);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (2 * half + j > w4) continue;                // above the diagonal
-        const auto kb = load_split<TP>(K, tplane, frag_of(2 * half + j, i, DK / 32));
+        const auto kb = load_frag<TP>(K, tplane, (2 * half + j) * (DK / 32) + i);
         kk[j] = mm(ka, kb, kk[j]);
         qk[j] = mm(qa, kb, qk[j]);
       }
@@ -216,8 +229,8 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
     float drv = 0.0f;                                   // dR_i . V_i
 #pragma unroll 2
     for (int i = 0; i < nv; ++i) {
-      const auto ga = load_split<TP>(GO, up, frag_of(w4, i, nv));
-      const auto ra_f = load_split<kFull>(DR, up, frag_of(w4, i, nv));
+      const auto ga = load_frag<TP>(GO, up, w4 * nv + i);
+      const auto ra_f = load_frag<kFull>(DR, up, w4 * nv + i);
       if (half == 0) {
         const auto va = ld8(V + (int64_t)rac * p.ldv + 32 * i + 8 * g);
 #pragma unroll
@@ -226,7 +239,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (2 * half + j > w4) continue;
-        const auto ub = load_split<kFull>(U, up, frag_of(2 * half + j, i, nv));
+        const auto ub = load_frag<kFull>(U, up, (2 * half + j) * nv + i);
         da[j] = mm(ga, ub, da[j]);
         dl[j] = mm(ra_f, ub, dl[j]);
       }
@@ -298,21 +311,21 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
     for (int a = 0; a < 2; ++a) aq[a] = ar[a] = au[a] = zero4();
 #pragma unroll 2
     for (int ks = 0; ks < nv; ++ks) {
-      const f32x8 w8 = ld8(W0 + frag_of(rt, ks, nv)), g8 = ld8(G + frag_of(rt, ks, nv));
+      const f32x8 w8 = load_frag(W0, rt * nv + ks), g8 = load_frag(G, rt * nv + ks);
       if (half == 0)
 #pragma unroll
         for (int e = 0; e < 8; ++e) wg += w8[e] * g8[e];
       const auto wf = split_of<kFull>(w8), gf = split_of<kFull>(g8);
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const int f = frag_of(2 * half + a, ks, nv) + zero;
-        aq[a] = mm(load_split<TP>(GO, up, f), wf, aq[a]);
-        ar[a] = mm(load_split<kFull>(DR, up, f), wf, ar[a]);
-        au[a] = mm(load_split<kFull>(U, up, f), gf, au[a]);
+        const int f = (2 * half + a) * nv + ks;
+        aq[a] = mm(load_frag<TP>(GO, up, f), wf, aq[a]);
+        ar[a] = mm(load_frag<kFull>(DR, up, f), wf, ar[a]);
+        au[a] = mm(load_frag<kFull>(U, up, f), gf, au[a]);
       }
     }
-    const auto k0 = load_split<TP>(KT, tplane, frag_of(rt, 0, 2)), k1 = load_split<TP>(KT, tplane, frag_of(rt, 1, 2));
-    const auto q0 = load_split<TP>(QT, tplane, frag_of(rt, 0, 2)), q1 = load_split<TP>(QT, tplane, frag_of(rt, 1, 2));
+    const auto k0 = load_frag<TP>(KT, tplane, rt * 2 + 0), k1 = load_frag<TP>(KT, tplane, rt * 2 + 1);
+    const auto q0 = load_frag<TP>(QT, tplane, rt * 2 + 0), q1 = load_frag<TP>(QT, tplane, rt * 2 + 1);
     const int col = rt * 16 + li;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
@@ -448,7 +461,7 @@ __global__ __launch_bounds__(256) void delta_sum_rates_kernel(DeltaParams p) {
 
 template <typename T, int DK>
 hipError_t gstate_impl(const DeltaParams &p, hipStream_t s) {
-  hipLaunchKernelGGL((delta_gstate_kernel<T, DK>), dim3((unsigned)((int64_t)p.nseq * p.heads * (p.dv / SL))), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((delta_gstate_kernel<T, DK>), dim3((unsigned)((int64_t)p.nseq * p.heads * (p.dv / SL))), dim3(512), 0, s, p);
   return hipGetLastError();
 }
 template <typename T, int DK>

@@ -86,6 +86,20 @@ __device__ __forceinline__ int frag_of(int rt, int kt, int nk) { return ((rt * n
 __device__ __forceinline__ int64_t frag_at(int row, int k, int nk) {
   return ((int64_t)((row >> 4) * nk + (k >> 5)) * 64 + ((k >> 3) & 3) * 16 + (row & 15)) * 8 + (k & 7);
 }
+// Fragment f of a split (or fp32) matrix.  `base` and f are the same for the whole wave, so that the address
+// is a scalar base and the lane's 32-bit offset.
+template <int P> __device__ __forceinline__ Split<P> load_frag(const char *base, int64_t plane, int f) {
+  const unsigned lane = (threadIdx.x & 63) * 16;
+  const char *b = base + (int64_t)f * 1024;
+  Split<P> s;
+#pragma unroll
+  for (int i = 0; i < P; ++i) s.p[i] = *reinterpret_cast<const bf16x8 *>(b + i * plane + lane);
+  return s;
+}
+__device__ __forceinline__ f32x8 load_frag(const float *base, int f) {
+  const unsigned lane = (threadIdx.x & 63) * 32;
+  return ld8(reinterpret_cast<const float *>(reinterpret_cast<const char *>(base + (int64_t)f * 512) + lane));
+}
 template <int P> __device__ __forceinline__ Split<P> load_split(const char *base, int64_t plane, int64_t e) {
   Split<P> f;
 #pragma unroll
@@ -96,6 +110,9 @@ template <int P> __device__ __forceinline__ void store_split(char *base, int64_t
 #pragma unroll
   for (int i = 0; i < P; ++i) *reinterpret_cast<bf16x8 *>(reinterpret_cast<__bf16 *>(base + i * plane) + e) = f.p[i];
 }
+
+// The wave's index in its workgroup, known to be the same for all its lanes.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // Launch-order block id -> work item, so that consecutive items (which read the same tokens and
 // chunk terms) run on one XCD: workgroups go round the 8 XCDs.
@@ -152,6 +169,28 @@ template <int P, int R, int Ccols> struct SplitTile {
       for (int x = 0; x < 4; ++x) v[x] += (float)h[x];
     }
     *reinterpret_cast<f32x4 *>(dst) = v;
+  }
+};
+
+// One lane's column of four rows (t4 .. t4 + 3) of a chunk's token rows: 32-bit byte offsets from the
+// chunk's first row (64 rows span less than 2 GiB), the base is the same for the wave.
+template <typename T> struct Rows4 {
+  unsigned off[4], col;
+  __device__ __forceinline__ Rows4(int t4, int li, int64_t ld) {
+    col = li * sizeof(T);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) off[r] = (unsigned)(t4 + r) * (unsigned)(ld * sizeof(T)) + col;
+  }
+  // rows past `left` repeat the first
+  __device__ __forceinline__ void load(const T *base, int t4, int left, T (&v)[4]) const {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      v[r] = *reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + (t4 + r < left ? off[r] : col));
+  }
+  __device__ __forceinline__ void store(T *base, int t4, int left, const f32x4 v) const {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (t4 + r < left) *reinterpret_cast<T *>(reinterpret_cast<char *>(base) + off[r]) = from_f32<T>(v[r]);
   }
 };
 
