@@ -11,9 +11,9 @@ struct OrthPlan {
   bool bf16, tall;                  // tall: rows > cols, X is the transpose of G
   int r, c;                         // X is r x c, r <= c
   int tile, tile_sym;               // tile of B X, and of the symmetric products
-  int rp, cp, parts;                // padded sizes, bf16 parts of an operand
+  int rp, cp;                       // padded sizes
   int norm_blocks;                  // partial sums of squares a matrix
-  size_t off_norm, off_x[2], off_xt[2], off_a, off_b, total;
+  size_t off_norm, off_rest, off_x[2], off_xt[2], off_a, off_b, total;
 };
 OrthPlan plan_orth(int rows, int cols, int batch, bool bf16);
 

@@ -2,10 +2,17 @@
 //   X = G / (|G|_F + eps) (transposed while G has more rows than columns), then `steps` times
 //   A = X X^T,  B = a I + b A + c A A,  X <- B X.
 //
-// All products run on bf16 MFMA with fp32 accumulation, on operands split into bf16 parts:
-// two for bf16 matrices (17 bits: products h*h + h*l + l*h), three for fp32 ones (24 bits, six
-// products, 2.5 times the rate of fp32 MFMA).  One part would not do: the five steps multiply
-// what is lost in the small singular directions by up to 3.4445^5 = 485.
+// All products run on fp16 MFMA with fp32 accumulation, on operands of two fp16 parts,
+// x = h + l, l = fp16(x - h): 22 bits, products h*h + h*l + l*h.  Every matrix here has a spectral
+// norm below 4 (X 1.2, A 1.5, B 3.45): stored times 4096 its elements stay below 2^14, and an element
+// above 2^-15 keeps its low part out of the subnormal range; what smaller ones lose is below 2^-36.
+// One part would not do throughout: the steps multiply what is lost along small singular directions
+// by up to 3.4445 each, 485 in five.  It does in the last two steps of bf16 matrices, where what
+// is lost (2^-12) is multiplied by 3.4 at most and the result has 8 bits; and bf16 matrices enter the
+// first step exactly in one part, times a power of two, with the rest of 1 / |G| applied to A and X.
+// Measured off the definition in 64 bits, 2 x 1300 x 1200 fp32: 2.1e-6 (fp32 arithmetic 3.2e-6, three bf16
+// parts and six products 3.0e-6 at 1.6 times the time); 4 x 4096 x 1024 bf16: 1.76e-3 (the rounding of the result
+// alone 1.66e-3).
 // The parts are written as planes by the kernel that computes a matrix, so that the main loop
 // copies tiles from memory straight into LDS.  Every product is C[i][j] = sum_k P[i][k] Q[j][k]
 // of row panels: X X^T, A A (A is symmetric) and B X from the stored X^T; A and B are
@@ -17,14 +24,21 @@
 namespace ttt {
 namespace {
 
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f32x4 mma(const f16x8 a, const f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
 constexpr int KS = 32;              // reduction elements a stage
+constexpr float kUnit = 4096.0f;    // a stored element for 1
 
 // Split matrix: one plane a part.  A plane is cut in fragments of 16 rows x 32 columns, 1 KB each in
 // the order in which lanes take them (lane = 16 (column / 8 % 4) + row % 16, eight columns a lane),
 // the nrt fragments of 32 columns one after another: a stage's panel is one piece of memory.  (With
 // plain rows a copy of 16 rows meets one channel of the L2 where the row length is a power of two:
-// 93 against 91 us for the symmetric
-// products of four 1024 x 4096 matrices, 64 x 64 tiles of 512-wide ones 13.7 against 11.9.)
+// 93 against 91 us for the symmetric products of four 1024 x 4096 matrices, 64 x 64 tiles of 512-wide
+// ones 13.7 against 11.9.)
 struct Mat {
   char *p;
   int64_t plane, bs;                // bytes from plane to plane, from matrix to matrix
@@ -32,26 +46,27 @@ struct Mat {
 };
 __device__ __forceinline__ int64_t frag_byte(const Mat &m, int rt, int kt) { return ((int64_t)kt * m.nrt + rt) * 1024; }
 
-// Eight values as one lane's piece of a fragment, part by part.
-template <int P> __device__ __forceinline__ void put8(char *p, int64_t plane, float (&v)[8]) {
+// Eight values as one lane's piece of a fragment, in `parts` parts.
+__device__ __forceinline__ void put8(char *p, int64_t plane, int parts, float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    bf16x8 h;
+  for (int i = 0; i < 2; ++i) {
+    if (i >= parts) break;
+    f16x8 h;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      h[r] = (__bf16)v[r];
+      h[r] = (_Float16)v[r];
       v[r] -= (float)h[r];
     }
-    *reinterpret_cast<bf16x8 *>(p + i * plane) = h;
+    *reinterpret_cast<f16x8 *>(p + i * plane) = h;
   }
 }
-// Elements (row, col .. col + 3), col % 4 == 0.
+// Elements (row, col .. col + 3), col % 4 == 0, of a matrix of P parts.
 template <int P> __device__ __forceinline__ f32x4 get4(const Mat &m, int64_t base, int row, int col) {
   const char *p = m.p + base + frag_byte(m, row >> 4, col >> 5) + (((col >> 3) & 3) * 16 + (row & 15)) * 16 + (col & 7) * 2;
   f32x4 v = f32x4{0, 0, 0, 0};
 #pragma unroll
   for (int i = P - 1; i >= 0; --i) {
-    const bf16x4 h = *reinterpret_cast<const bf16x4 *>(p + i * m.plane);
+    const f16x4 h = *reinterpret_cast<const f16x4 *>(p + i * m.plane);
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] += (float)h[r];
   }
@@ -101,17 +116,18 @@ __global__ __launch_bounds__(256) void orth_norm_kernel(OrthParams p, double *pa
 }
 
 // 1 / (|G| + eps) of matrix b, by every wave (the partials in one fixed order).
-__device__ __forceinline__ float orth_scale(const OrthParams &p, const double *part, int b) {
+__device__ __forceinline__ double orth_scale(const OrthParams &p, const double *part, int b) {
   double s = 0.0;
   for (int i = threadIdx.x & 63; i < p.plan.norm_blocks; i += 64) s += part[(int64_t)b * p.plan.norm_blocks + i];
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
-  return (float)(1.0 / (sqrt(s) + (double)p.eps));
+  return 1.0 / (sqrt(s) + (double)p.eps);
 }
 
-// X and X^T of the first step: G scaled, split and padded.  64 x 64 tiles of [rows][cols].
-template <typename T, int P>
-__global__ __launch_bounds__(256) void orth_load_kernel(OrthParams p, const double *part, Mat x, Mat xt) {
+// X and X^T of the first step: G scaled, split and padded.  64 x 64 tiles of [rows][cols].  bf16
+// matrices are scaled by the power of two below 1 / |G|, exactly; the factor left over goes to rest[b].
+template <typename T>
+__global__ __launch_bounds__(256) void orth_load_kernel(OrthParams p, const double *part, float *rest, Mat x, Mat xt) {
   __shared__ float tile[64][65];
   const OrthPlan &q = p.plan;
   const int b = blockIdx.z;
@@ -123,12 +139,20 @@ __global__ __launch_bounds__(256) void orth_load_kernel(OrthParams p, const doub
     const int r = r0 + w + 4 * i, c = c0 + tx;
     in[i] = r < q.rows && c < q.cols ? to_f32(g[(int64_t)r * p.ldg + c]) : 0.0f;
   }
-  const float scale = orth_scale(p, part, b);
+  double scale = orth_scale(p, part, b);
+  if (sizeof(T) == 2) {
+    int e;
+    const double f = frexp(scale, &e);                        // scale = f 2^e, f in [1/2, 1)
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) rest[b] = (float)(2.0 * f);
+    scale = ldexp(1.0, e - 1);
+    if (!(f == f)) scale = f;                                 // NaN stays NaN
+  }
+  scale *= (double)kUnit;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) tile[w + 4 * i][tx] = in[i] * scale;
+  for (int i = 0; i < 16; ++i) tile[w + 4 * i][tx] = (float)((double)in[i] * scale);
   __syncthreads();
   const Mat &m = q.tall ? xt : x, &mt = q.tall ? x : xt;      // G's own layout, and its transpose
-  const int gr = tx >> 4, li = tx & 15;
+  const int gr = tx >> 4, li = tx & 15, parts = sizeof(T) == 2 ? 1 : 2;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {                               // wave w: fragment rows w
     float v[8], u[8];
@@ -137,8 +161,8 @@ __global__ __launch_bounds__(256) void orth_load_kernel(OrthParams p, const doub
       v[e] = tile[16 * w + li][32 * k + 8 * gr + e];
       u[e] = tile[32 * k + 8 * gr + e][16 * w + li];
     }
-    put8<P>(m.p + b * m.bs + frag_byte(m, r0 / 16 + w, c0 / 32 + k) + tx * 16, m.plane, v);
-    put8<P>(mt.p + b * mt.bs + frag_byte(mt, c0 / 16 + w, r0 / 32 + k) + tx * 16, mt.plane, u);
+    put8(m.p + b * m.bs + frag_byte(m, r0 / 16 + w, c0 / 32 + k) + tx * 16, m.plane, parts, v);
+    put8(mt.p + b * mt.bs + frag_byte(mt, c0 / 16 + w, r0 / 32 + k) + tx * 16, mt.plane, parts, u);
   }
 }
 
@@ -147,6 +171,8 @@ enum Kind { kGram, kPoly, kNext, kLast };   // A;  B = a I + b A + c A A;  X and
 struct Product {
   Mat P, Q;                         // C = P Q^T
   Mat c, ct;                        // results: [i][j] and [j][i] (the same matrix where C is symmetric)
+  int parts;                        // of the results
+  const float *rest;                // [matrix] factor of each X in it (1 in kNext, 2 in kGram), or null
   int K, ti, tj;                    // reduction length, tiles along i and j
   int tiles;                        // tiles a matrix
 };
@@ -162,15 +188,15 @@ template <int TM_, int TN_, int WR_, int WC_, int NST_> struct Geo {
   static constexpr int TM = TM_, TN = TN_, WR = WR_, WC = WC_, NST = NST_, kThreads = WR * WC * 64;
   static constexpr int WM = TM / WR, WN = TN / WC, FM = WM / 16, FN = WN / 16;
 };
-template <int TILE, int P> struct GeoOf;
-template <int P> struct GeoOf<64, P> { typedef Geo<64, 64, 2, 2, P == 2 ? 5 : 3> type; };
-template <int P> struct GeoOf<128, P> { typedef Geo<128, 128, 4, 2, P == 2 ? 4 : 3> type; };
-template <> struct GeoOf<256, 2> { typedef Geo<256, 256, 4, 2, 2> type; };
-template <> struct GeoOf<256, 3> { typedef Geo<256, 128, 4, 2, 2> type; };
+// N: parts of both operands together (2, 3 or 4): the deeper ring where a stage is smaller
+template <int TILE, int N> struct GeoOf;
+template <int N> struct GeoOf<64, N> { typedef Geo<64, 64, 2, 2, N == 4 ? 5 : 6> type; };
+template <int N> struct GeoOf<128, N> { typedef Geo<128, 128, 4, 2, N == 4 ? 4 : N == 3 ? 3 : 5> type; };
+template <int N> struct GeoOf<256, N> { typedef Geo<256, 256, 4, 2, N == 2 ? 4 : 2> type; };
 
-template <typename T, typename G, int P, int KIND>
+template <typename T, typename G, int PA, int PB, int KIND>
 __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_kernel(OrthParams p, Product q) {
-  constexpr int kRows = (G::TM + G::TN) * P, kStage = kRows * 64, kWaves = G::kThreads / 64;
+  constexpr int kRows = G::TM * PA + G::TN * PB, kStage = kRows * 64, kWaves = G::kThreads / 64;
   constexpr int PPW = kRows / 16 / kWaves;        // copies of 16 rows a wave and stage
   constexpr int kPitch = G::WN * 2 + 16;          // epilogue: a row of a wave's tile of one part
   constexpr int kEpi = kWaves * G::WM * kPitch;
@@ -194,14 +220,14 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
 #pragma unroll
   for (int x = 0; x < PPW; ++x) {
     const int f = w * PPW + x;                    // fragment of the stage
-    const bool second = f >= G::TM / 16 * P;
-    const int r = second ? f - G::TM / 16 * P : f, nf = second ? G::TN / 16 : G::TM / 16;
+    const bool second = f >= G::TM / 16 * PA;
+    const int r = second ? f - G::TM / 16 * PA : f, nf = second ? G::TN / 16 : G::TM / 16;
     const Mat &m = second ? q.Q : q.P;
     src[x] = m.p + b * m.bs + r / nf * m.plane + frag_byte(m, (second ? bj : bi) * nf + r % nf, 0) + l * 16;
   }
   const int nk = q.K / KS;
   const auto copy = [&](int x, int kc) {
-    const bool second = w * PPW + x >= G::TM / 16 * P;
+    const bool second = w * PPW + x >= G::TM / 16 * PA;
     copy16_to_lds_untracked(src[x] + kc * step_bytes[second], s + kc % G::NST * kStage + (w * PPW + x) * 1024);
   };
   f32x4 acc[G::FM][G::FN];
@@ -216,16 +242,18 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
 #pragma unroll
       for (int x = 0; x < PPW; ++x) copy(x, k);
   const auto read = [&](const unsigned char *st, int row) {     // the fragment of a stage's row
-    return *reinterpret_cast<const bf16x8 *>(st + row * 64 + l * 16);
+    return *reinterpret_cast<const f16x8 *>(st + row * 64 + l * 16);
   };
   // products with the fragments of one column tile, the small ones first
-  const auto products = [&](int j, const bf16x8 (&fa)[G::FM][P], const bf16x8 (&fb)[P]) {
+  constexpr int ND = PA > PB ? PA : PB;
+  const auto products = [&](int j, const f16x8 (&fa)[G::FM][PA], const f16x8 (&fb)[PB]) {
 #pragma unroll
-    for (int d = P - 1; d >= 0; --d)
+    for (int d = ND - 1; d >= 0; --d)
 #pragma unroll
       for (int x = 0; x <= d; ++x)
+        if (x < PA && d - x < PB)
 #pragma unroll
-        for (int i = 0; i < G::FM; ++i) acc[i][j] = mma(fb[d - x], fa[i][x], acc[i][j]);
+          for (int i = 0; i < G::FM; ++i) acc[i][j] = mma(fb[d - x], fa[i][x], acc[i][j]);
   };
   for (int kc = 0; kc < nk; ++kc) {
     // this wave's copies of stage kc have arrived (those of the NST - 2 stages after it may be in flight)
@@ -233,18 +261,19 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
     bare_barrier();                             // everyone's have, and the stage before is free
     const unsigned char *st = s + kc % G::NST * kStage;
     const bool more = kc + G::NST - 1 < nk;
-    bf16x8 fa[G::FM][P], fb[2][P];
+    f16x8 fa[G::FM][PA], fb[2][PB];
+    const auto read_b = [&](int j, f16x8 (&f)[PB]) {
 #pragma unroll
-    for (int x = 0; x < P; ++x) {
+      for (int x = 0; x < PB; ++x) f[x] = read(st, G::TM * PA + x * G::TN + wj + 16 * j);
+    };
+#pragma unroll
+    for (int x = 0; x < PA; ++x)
 #pragma unroll
       for (int i = 0; i < G::FM; ++i) fa[i][x] = read(st, x * G::TM + wi + 16 * i);
-      fb[0][x] = read(st, G::TM * P + x * G::TN + wj);
-    }
+    read_b(0, fb[0]);
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) {
-      if (j + 1 < G::FN)
-#pragma unroll
-        for (int x = 0; x < P; ++x) fb[(j + 1) & 1][x] = read(st, G::TM * P + x * G::TN + wj + 16 * (j + 1));
+      if (j + 1 < G::FN) read_b(j + 1, fb[(j + 1) & 1]);
       // the next stage's copies, spread over the products
 #pragma unroll
       for (int x = 0; x < PPW; ++x)
@@ -261,10 +290,19 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
 #pragma unroll
       for (int j = 0; j < G::FN; ++j) {
         const int row = r0 + 16 * i + li, col = c0 + 16 * j + 4 * g;
-        const f32x4 a = get4<P>(q.P, b * q.P.bs, row, col);
+        const f32x4 a = get4<PA>(q.P, b * q.P.bs, row, col);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = p.c * acc[i][j][r] + (p.b * a[r] + (row == col + r ? p.a : 0.0f));
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = (p.c / kUnit) * acc[i][j][r] + (p.b * a[r] + (row == col + r ? p.a * kUnit : 0.0f));
       }
+  } else {
+    // back to one kUnit (the result: none)
+    float f = KIND == kLast ? 1.0f / (kUnit * kUnit) : 1.0f / kUnit;
+    if (q.rest) f *= KIND == kGram ? q.rest[b] * q.rest[b] : q.rest[b];
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < G::FN; ++j) acc[i][j] *= f;
   }
   if constexpr (KIND == kLast) {
     T *out = static_cast<T *>(p.out) + b * p.bso;
@@ -286,18 +324,19 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
   unsigned char *mine = s + w * (G::WM * kPitch);
   const bool both = KIND == kNext || bi != bj;
 #pragma unroll
-  for (int x = 0; x < P; ++x) {
+  for (int x = 0; x < 2; ++x) {
+    if (x >= q.parts) break;
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
 #pragma unroll
       for (int j = 0; j < G::FN; ++j) {
-        bf16x4 h;
+        f16x4 h;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          h[r] = (__bf16)acc[i][j][r];
+          h[r] = (_Float16)acc[i][j][r];
           acc[i][j][r] -= (float)h[r];
         }
-        *reinterpret_cast<bf16x4 *>(mine + (16 * i + li) * kPitch + (16 * j + 4 * g) * 2) = h;
+        *reinterpret_cast<f16x4 *>(mine + (16 * i + li) * kPitch + (16 * j + 4 * g) * 2) = h;
       }
     char *c = q.c.p + b * q.c.bs + x * q.c.plane + l * 16;
 #pragma unroll
@@ -325,72 +364,79 @@ template <typename T>
 __global__ __launch_bounds__(256) void orth_scale_kernel(OrthParams p, const double *part) {
   const OrthPlan &q = p.plan;
   const int b = blockIdx.y;
-  const float scale = orth_scale(p, part, b);
+  const double scale = orth_scale(p, part, b);
   const int64_t total = (int64_t)q.rows * q.cols;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
     const int64_t r = e / q.cols, c = e % q.cols;
     static_cast<T *>(p.out)[b * p.bso + r * p.ldo + c] =
-        from_f32<T>(to_f32(static_cast<const T *>(p.g)[b * p.bsg + r * p.ldg + c]) * scale);
+        from_f32<T>((float)((double)to_f32(static_cast<const T *>(p.g)[b * p.bsg + r * p.ldg + c]) * scale));
   }
 }
 
-template <typename T, int P, int KIND, int TILE> void product_of(const OrthParams &p, Product q, int rows, int cols, hipStream_t s) {
-  typedef typename GeoOf<TILE, P>::type G;
+template <typename T, int PA, int PB, int KIND, int TILE>
+void product_of(const OrthParams &p, Product q, int rows, int cols, hipStream_t s) {
+  typedef typename GeoOf<TILE, PA + PB>::type G;
   const bool sym = KIND == kGram || KIND == kPoly;
   q.ti = rows / G::TM, q.tj = cols / G::TN;
   q.tiles = sym ? q.ti * (q.ti + 1) / 2 : q.ti * q.tj;
-  hipLaunchKernelGGL((orth_product_kernel<T, G, P, KIND>), dim3((unsigned)(p.plan.batch * q.tiles)), dim3(G::kThreads), 0, s, p, q);
+  hipLaunchKernelGGL((orth_product_kernel<T, G, PA, PB, KIND>), dim3((unsigned)(p.plan.batch * q.tiles)),
+                     dim3(G::kThreads), 0, s, p, q);
 }
-template <typename T, int P, int KIND> void product(const OrthParams &p, const Product &q, int rows, int cols, hipStream_t s) {
+template <typename T, int PA, int PB, int KIND>
+void product(const OrthParams &p, const Product &q, int rows, int cols, hipStream_t s) {
   // symmetric results: square tiles of at most 128, so that half of them stay away
   const int tile = KIND == kGram || KIND == kPoly ? p.plan.tile_sym : p.plan.tile;
   if constexpr (KIND == kNext || KIND == kLast) {
-    if (tile == 256) return product_of<T, P, KIND, 256>(p, q, rows, cols, s);
+    if (tile == 256) return product_of<T, PA, PB, KIND, 256>(p, q, rows, cols, s);
   }
-  if (tile == 128) return product_of<T, P, KIND, 128>(p, q, rows, cols, s);
-  product_of<T, P, KIND, 64>(p, q, rows, cols, s);
+  if (tile == 128) return product_of<T, PA, PB, KIND, 128>(p, q, rows, cols, s);
+  product_of<T, PA, PB, KIND, 64>(p, q, rows, cols, s);
 }
 
-template <typename T, int P> hipError_t steps_of(const OrthParams &p, hipStream_t s) {
-  const OrthPlan &q = p.plan;
-  const int64_t xb = (int64_t)q.rp * q.cp * 2, ab = (int64_t)q.rp * q.rp * 2;
-  Mat x[2], xt[2];
-  for (int i = 0; i < 2; ++i) {
-    x[i] = Mat{p.ws + q.off_x[i], xb, xb * P, q.rp / 16};
-    xt[i] = Mat{p.ws + q.off_xt[i], xb, xb * P, q.cp / 16};
-  }
-  const Mat A{p.ws + q.off_a, ab, ab * P, q.rp / 16}, B{p.ws + q.off_b, ab, ab * P, q.rp / 16};
-  const double *part = reinterpret_cast<const double *>(p.ws + q.off_norm);
-  const int pr = q.tall ? q.cp : q.rp, pc = q.tall ? q.rp : q.cp;       // padded sizes of G
-  hipLaunchKernelGGL((orth_load_kernel<T, P>), dim3(pc / 64, pr / 64, q.batch), dim3(256), 0, s, p, part, x[0], xt[0]);
-  for (int i = 0; i < p.steps; ++i) {
-    const int cur = i & 1;
-    product<T, P, kGram>(p, Product{x[cur], x[cur], A, A, q.cp}, q.rp, q.rp, s);
-    product<T, P, kPoly>(p, Product{A, A, B, B, q.rp}, q.rp, q.rp, s);
-    const Product nx{B, xt[cur], x[cur ^ 1], xt[cur ^ 1], q.rp};
-    if (i + 1 < p.steps)
-      product<T, P, kNext>(p, nx, q.rp, q.cp, s);
-    else
-      product<T, P, kLast>(p, nx, q.rp, q.cp, s);
-  }
-  return hipGetLastError();
-}
-
-template <typename T, int P> hipError_t run_orth(const OrthParams &p, hipStream_t s) {
+template <typename T> hipError_t run_orth(const OrthParams &p, hipStream_t s) {
   const OrthPlan &q = p.plan;
   double *part = reinterpret_cast<double *>(p.ws + q.off_norm);
+  float *rest = reinterpret_cast<float *>(p.ws + q.off_rest);
   constexpr int V = 16 / (int)sizeof(T);
+  constexpr bool kBf16 = sizeof(T) == 2;
   if ((uintptr_t)p.g % 16 == 0 && q.cols % V == 0 && p.ldg % V == 0 && p.bsg % V == 0)
     hipLaunchKernelGGL((orth_norm_kernel<T, V>), dim3(q.norm_blocks, q.batch), dim3(256), 0, s, p, part);
   else
     hipLaunchKernelGGL((orth_norm_kernel<T, 1>), dim3(q.norm_blocks, q.batch), dim3(256), 0, s, p, part);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   if (p.steps == 0) {
     hipLaunchKernelGGL(orth_scale_kernel<T>, dim3(q.norm_blocks, q.batch), dim3(256), 0, s, p, part);
     return hipGetLastError();
   }
-  return steps_of<T, P>(p, s);
+  const int64_t xb = (int64_t)q.rp * q.cp * 2, ab = (int64_t)q.rp * q.rp * 2;
+  Mat x[2], xt[2];
+  for (int i = 0; i < 2; ++i) {
+    x[i] = Mat{p.ws + q.off_x[i], xb, 2 * xb, q.rp / 16};
+    xt[i] = Mat{p.ws + q.off_xt[i], xb, 2 * xb, q.cp / 16};
+  }
+  const Mat A{p.ws + q.off_a, ab, 2 * ab, q.rp / 16}, B{p.ws + q.off_b, ab, 2 * ab, q.rp / 16};
+  const int pr = q.tall ? q.cp : q.rp, pc = q.tall ? q.rp : q.cp;       // padded sizes of G
+  hipLaunchKernelGGL(orth_load_kernel<T>, dim3(pc / 64, pr / 64, q.batch), dim3(256), 0, s, p, part, rest, x[0], xt[0]);
+  for (int i = 0; i < p.steps; ++i) {
+    const int cur = i & 1, left = p.steps - i;
+    const bool one = kBf16 && left <= 2;                      // one part from here on
+    const bool xone = one || (kBf16 && i == 0);               // X is one part
+    const float *f = kBf16 && i == 0 ? rest : nullptr;
+    const Product gram{x[cur], x[cur], A, A, one ? 1 : 2, f, q.cp}, poly{A, A, B, B, one ? 1 : 2, nullptr, q.rp};
+    const Product next{B, xt[cur], x[cur ^ 1], xt[cur ^ 1], kBf16 && left <= 3 ? 1 : 2, f, q.rp};
+    if (xone) product<float, 1, 1, kGram>(p, gram, q.rp, q.rp, s); else product<float, 2, 2, kGram>(p, gram, q.rp, q.rp, s);
+    if (one) product<float, 1, 1, kPoly>(p, poly, q.rp, q.rp, s); else product<float, 2, 2, kPoly>(p, poly, q.rp, q.rp, s);
+    if (left == 1) {
+      constexpr int P = kBf16 ? 1 : 2;
+      product<T, P, P, kLast>(p, next, q.rp, q.cp, s);
+    } else if (one) {
+      product<float, 1, 1, kNext>(p, next, q.rp, q.cp, s);
+    } else if (xone) {
+      product<float, 2, 1, kNext>(p, next, q.rp, q.cp, s);
+    } else {
+      product<float, 2, 2, kNext>(p, next, q.rp, q.cp, s);
+    }
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -400,10 +446,8 @@ OrthPlan plan_orth(int rows, int cols, int batch, bool bf16) {
   q.rows = rows, q.cols = cols, q.batch = batch, q.bf16 = bf16;
   q.tall = rows > cols;
   q.r = q.tall ? cols : rows, q.c = q.tall ? rows : cols;
-  q.parts = bf16 ? 2 : 3;
   const auto tiles = [&](int tm, int tn) { return (int64_t)batch * ((q.r + tm - 1) / tm) * ((q.c + tn - 1) / tn); };
-  const int tn = bf16 ? 256 : 128;
-  q.tile = tiles(256, tn) >= 200 ? 256 : (tiles(128, 128) >= 200 ? 128 : 64);
+  q.tile = tiles(256, 256) >= 200 ? 256 : (tiles(128, 128) >= 200 ? 128 : 64);
   const int64_t nr = (q.r + 127) / 128;
   q.tile_sym = batch * (nr * (nr + 1) / 2) >= 100 ? 128 : 64;
   const int pad = q.tile > q.tile_sym ? q.tile : q.tile_sym;
@@ -411,9 +455,10 @@ OrthPlan plan_orth(int rows, int cols, int batch, bool bf16) {
   const int64_t elems = (int64_t)rows * cols, blocks = (elems + 4095) / 4096;
   q.norm_blocks = (int)(blocks < 1 ? 1 : (blocks > 256 ? 256 : blocks));
   const auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t xb = (size_t)q.rp * q.cp * 2 * q.parts * batch, ab = (size_t)q.rp * q.rp * 2 * q.parts * batch;
+  const size_t xb = (size_t)q.rp * q.cp * 4 * batch, ab = (size_t)q.rp * q.rp * 4 * batch;
   size_t o = 0;
   q.off_norm = o, o = al(o + (size_t)batch * q.norm_blocks * 8);
+  q.off_rest = o, o = al(o + (size_t)batch * 4);
   for (int i = 0; i < 2; ++i) {
     q.off_x[i] = o, o = al(o + xb);
     q.off_xt[i] = o, o = al(o + xb);
@@ -425,7 +470,7 @@ OrthPlan plan_orth(int rows, int cols, int batch, bool bf16) {
 }
 
 hipError_t launch_orth(const OrthParams &p, hipStream_t s) {
-  return p.plan.bf16 ? run_orth<__bf16, 2>(p, s) : run_orth<float, 3>(p, s);
+  return p.plan.bf16 ? run_orth<__bf16>(p, s) : run_orth<float>(p, s);
 }
 
 }  // namespace ttt
