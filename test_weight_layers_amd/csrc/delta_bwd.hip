@@ -193,7 +193,7 @@ template <typename T, int DK>
 __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kernel(DeltaParams p) {
   constexpr int NT = DK / 64, TP = kTok<T>;
   __shared__ __attribute__((aligned(16))) SplitTile<kOut<T>, C, C> s_x, s_xt, s_y, s_yt;
-  __shared__ float s_row[3][4][C];      // partials of q.(go W0), k.(dR W0), k.(U G)
+  __shared__ __attribute__((aligned(16))) float s_row[3][4][C];      // partials of q.(go W0), k.(dR W0), k.(U G)
   __shared__ float s_rs[2][C], s_db[2][C], s_cs[4][C], s_red[4];
   const int item = xcd_item(gridDim.x), h = item % p.heads, c = item / p.heads;
   const DeltaChunk ck = chunk_of(p, c);
@@ -277,12 +277,10 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
       if (g == 0) s_cs[w4][col] = cs;
     }
 #pragma unroll
-    for (int m = 1; m < 16; m <<= 1)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        rs[r] += __shfl_xor(rs[r], m);
-        dbs[r] += __shfl_xor(dbs[r], m);
-      }
+    for (int r = 0; r < 4; ++r) {
+      rs[r] = sum16(rs[r]);
+      dbs[r] = sum16(dbs[r]);
+    }
     if (li == 0)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -294,11 +292,6 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
   __syncthreads();
 
   // ---- dq, dk: rows 32 half .. + 31, column tiles w4, w4 + 4, ..
-  float dq_dot[2][4], dr_dot[2][4], du_dot[2][4];       // [row tile][r]: this lane's column of the row sums
-#pragma unroll
-  for (int a = 0; a < 2; ++a)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) dq_dot[a][r] = dr_dot[a][r] = du_dot[a][r] = 0.0f;
   float wg = 0.0f;                                      // <W0, G>, by the first half
   const float *W0 = p.w0t + ch * (DK * p.dv), *G = p.gwt + ch * (DK * p.dv);
 #pragma unroll 1
@@ -343,6 +336,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
       const f32x4 eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + r0);
       const f32x4 el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + r0);
       const f32x4 be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + r0);
+      f32x4 dots[3] = {zero4(), zero4(), zero4()};      // of q with aq, k with ar, k with au: this lane's column
       f32x4 kv = zero4(), qv = zero4();             // four tokens' elements
 #pragma unroll
       for (int x = TP - 1; x >= 0; --x) {
@@ -359,9 +353,9 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
         if (r0 + r >= ck.len) continue;
         const int64_t tk = ck.tok0 + r0 + r;
         const float dqi = p.scale * eg[r] * aq[a][r], dui = el[r] * au[a][r];
-        dq_dot[a][r] += qv[r] * dqi;
-        dr_dot[a][r] += kv[r] * ar[a][r];
-        du_dot[a][r] += kv[r] * dui;
+        dots[0][r] = qv[r] * dqi;
+        dots[1][r] = kv[r] * ar[a][r];
+        dots[2][r] = kv[r] * dui;
         const float dq = dqi + xq[r], dk = dui - be[r] * eg[r] * ar[a][r] + xk[r];
         if (p.gqp) {
           p.gqp[(tk * p.heads + h) * DK + col] = dq;
@@ -371,26 +365,19 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
           static_cast<T *>(p.gk)[tk * p.ldgk + kh * DK + col] = from_f32<T>(dk);
         }
       }
+      // row sums over the tile's columns, added to this wave's (kept in registers over the tiles they would
+      // spill, and every reload wait for the loads before it)
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dots[x][r] = sum16(dots[x][r]);
+        if (li == 0) {
+          f32x4 *s = reinterpret_cast<f32x4 *>(&s_row[x][w4][r0]);
+          *s = i == 0 ? dots[x] : *s + dots[x];
+        }
+      }
     }
   }
-#pragma unroll
-  for (int a = 0; a < 2; ++a)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float x = dq_dot[a][r], y = dr_dot[a][r], z = du_dot[a][r];
-#pragma unroll
-      for (int m = 1; m < 16; m <<= 1) {
-        x += __shfl_xor(x, m);
-        y += __shfl_xor(y, m);
-        z += __shfl_xor(z, m);
-      }
-      if (li == 0) {
-        const int row = 32 * half + 16 * a + 4 * g + r;
-        s_row[0][w4][row] = x;
-        s_row[1][w4][row] = y;
-        s_row[2][w4][row] = z;
-      }
-    }
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) wg += __shfl_xor(wg, m);
   if (l == 0 && half == 0) s_red[w4] = wg;

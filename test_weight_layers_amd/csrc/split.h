@@ -172,27 +172,41 @@ template <int P, int R, int Ccols> struct SplitTile {
   }
 };
 
-// One lane's column of four rows (t4 .. t4 + 3) of a chunk's token rows: 32-bit byte offsets from the
-// chunk's first row (64 rows span less than 2 GiB), the base is the same for the wave.
+// One lane's column of four rows (t4 .. t4 + 3) of a chunk's token rows, `left` of which exist: a base
+// that is the same for the wave and a 32-bit byte offset (64 rows span less than 2 GiB).
 template <typename T> struct Rows4 {
-  unsigned off[4], col;
+  unsigned off, col, step;
   __device__ __forceinline__ Rows4(int t4, int li, int64_t ld) {
+    step = (unsigned)(ld * sizeof(T));
     col = li * sizeof(T);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) off[r] = (unsigned)(t4 + r) * (unsigned)(ld * sizeof(T)) + col;
+    off = (unsigned)t4 * step + col;
   }
-  // rows past `left` repeat the first
+  // rows past the chunk repeat its first
   __device__ __forceinline__ void load(const T *base, int t4, int left, T (&v)[4]) const {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      v[r] = *reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + (t4 + r < left ? off[r] : col));
+    for (int r = 0; r < 4; ++r) {
+      const char *b = reinterpret_cast<const char *>(base) + (int64_t)(r < left ? r : 0) * step;
+      v[r] = *reinterpret_cast<const T *>(b + (t4 + r < left ? off : col));
+    }
   }
   __device__ __forceinline__ void store(T *base, int t4, int left, const f32x4 v) const {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (t4 + r < left) *reinterpret_cast<T *>(reinterpret_cast<char *>(base) + off[r]) = from_f32<T>(v[r]);
+      if (t4 + r < left) *reinterpret_cast<T *>(reinterpret_cast<char *>(base) + (int64_t)r * step + off) = from_f32<T>(v[r]);
   }
 };
+
+// The sum over the 16 lanes of a lane group, in every one of them (row rotations, no LDS).
+__device__ __forceinline__ float sum16(float v) {
+#define TTT_ROR_ADD(N) \
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + N, 0xf, 0xf, false))
+  TTT_ROR_ADD(8);
+  TTT_ROR_ADD(4);
+  TTT_ROR_ADD(2);
+  TTT_ROR_ADD(1);
+#undef TTT_ROR_ADD
+  return v;
+}
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0, 0, 0, 0}; }
 

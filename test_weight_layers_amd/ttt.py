@@ -495,7 +495,7 @@ def delta(w: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, be
     _offsets(cu_seqlens, S, dev)
     flags, ldo = 0, H * dv
     if out is None:
-        out = torch.empty((n, H * dv), dtype=q.dtype, device=q.device)
+        out = q.new_empty((n, H * dv))
         flags = DELTA_ZERO_UNUSED
     else:
         ldo = _row(out, q.dtype, dev, n, H * dv, "out")
@@ -567,7 +567,7 @@ def delta_step(w: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
         raise ValueError(f"slots must be a contiguous int32 tensor [{n}] on cuda:{dev}")
     flags, ldo = 0, H * dv
     if out is None:
-        out = torch.empty((n, H * dv), dtype=q.dtype, device=q.device)
+        out = q.new_empty((n, H * dv))
         flags = DELTA_ZERO_UNUSED
     else:
         ldo = _row(out, q.dtype, dev, n, H * dv, "out")
@@ -605,7 +605,7 @@ def gated_residual(x: torch.Tensor, o: torch.Tensor, z: Optional[torch.Tensor] =
     gamma_next = _channel(gamma_next, C, dev, "gamma_next")
     ldy = ldh = C
     if out is None:
-        out = torch.empty((n, C), dtype=dtype, device=x.device)
+        out = x.new_empty((n, C))
     else:
         ldy = _row(out, dtype, dev, n, C, "out")
     if h_out is not None:
@@ -613,7 +613,7 @@ def gated_residual(x: torch.Tensor, o: torch.Tensor, z: Optional[torch.Tensor] =
             raise ValueError("h_out needs gamma_next")
         ldh = _row(h_out, dtype, dev, n, C, "h_out")
     elif gamma_next is not None:
-        h_out = torch.empty((n, C), dtype=dtype, device=x.device)
+        h_out = x.new_empty((n, C))
     _check(load().ttt_gated_residual(C, C if norm_width is None else int(norm_width), x.data_ptr(), ldx, o.data_ptr(),
                                      ldo, _ptr(z), ldz, gamma, alpha, gamma_next, float(eps), out.data_ptr(), ldy,
                                      _ptr(h_out), ldh, n, code, _stream()))
