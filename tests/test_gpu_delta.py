@@ -41,7 +41,7 @@ def inputs(lens, H, Hk, dk, dv, dtype, seed=0, tail=0, rate=0.2):
     rn = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)
     n = sum(lens) + tail
     unit = lambda t: t / t.norm(dim=-1, keepdim=True)
-    d = dict(q=unit(rn(n, Hk, dk)).reshape(n, -1), k=unit(rn(n, Hk, dk)).reshape(n, -1), v=rn(n, H * dv),
+    d = dict(q=unit(rn(n, Hk, dk)).reshape(n, Hk * dk), k=unit(rn(n, Hk, dk)).reshape(n, Hk * dk), v=rn(n, H * dv),
              go=rn(n, H * dv))
     d = {x: t.to(dtype) for x, t in d.items()}
     d["beta"] = torch.sigmoid(rn(H, n)).float()
@@ -400,3 +400,61 @@ def test_refusals():
         ttt.delta_step(w, q, k, v, be, de)
     with pytest.raises(ValueError, match="slots"):
         ttt.delta_step(w, q, k, v, be, de, slots=cu)
+
+
+def test_no_rows_and_no_sequences_with_rows():
+    from test_weight_layers_amd import ttt
+    d = dev(inputs([0, 0, 0], 2, 1, 64, 64, torch.bfloat16, seed=18))
+    args = [d[x] for x in ("w", "q", "k", "v", "beta", "decay")]
+    o, w = ttt.delta(*args, key_heads=1, cu_seqlens=d["cu"])
+    assert o.shape == (0, 128) and torch.equal(w, d["w"])
+    got = ttt.delta_backward(*args, d["go"], d["gw"], key_heads=1, cu_seqlens=d["cu"])
+    assert got[0].shape == (0, 64) and torch.equal(got[5], d["gw"])
+    got = ttt.delta_backward(*args, d["go"], None, key_heads=1, cu_seqlens=d["cu"])
+    assert (got[5] == 0).all()
+    assert ttt.delta_step(d["w"], *args[1:], key_heads=1).shape == (0, 128)
+    # rows, but every sequence empty
+    d = dev(inputs([20], 2, 1, 64, 64, torch.bfloat16, seed=19))
+    cu = torch.tensor([7, 7], dtype=torch.int32, device="cuda")
+    args = [d[x] for x in ("w", "q", "k", "v", "beta", "decay")]
+    o, w = ttt.delta(*args, key_heads=1, cu_seqlens=cu)
+    assert (o == 0).all() and torch.equal(w, d["w"])
+    got = ttt.delta_backward(*args, d["go"], d["gw"], key_heads=1, cu_seqlens=cu)
+    assert all((got[i] == 0).all() for i in range(5)) and torch.equal(got[5], d["gw"])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_wide_values(dtype):
+    from test_weight_layers_amd import ttt
+    d = inputs([100], 1, 1, 64, 1024, dtype, seed=20)
+    o_ref, w_ref = reference(d, 1)
+    gref = reference(d, 1, gradient=True)
+    g = dev(d)
+    args = [g[x] for x in ("w", "q", "k", "v", "beta", "decay")]
+    o, w = ttt.delta(*args)
+    assert rel(o, o_ref) <= TOL[dtype][dtype] and rel(w, w_ref) <= TOL[dtype][torch.float32]
+    got = ttt.delta_backward(*args, g["go"], g["gw"])
+    for x, r in zip(got, gref):
+        assert rel(x, r) <= TOL[dtype][x.dtype]
+
+
+def test_sequences_do_not_reach_each_other():
+    """A NaN in one sequence leaves the others' bits."""
+    from test_weight_layers_amd import ttt
+    d = dev(inputs([40, 30, 50], 1, 1, 64, 64, torch.bfloat16, seed=21))
+    args = [d[x] for x in ("w", "q", "k", "v", "beta", "decay")]
+    ref = ttt.delta(*args, cu_seqlens=d["cu"])
+    gref = ttt.delta_backward(*args, d["go"], d["gw"], cu_seqlens=d["cu"])
+    for x in ("q", "k", "v", "go"):
+        d[x][45] = float("nan")
+    d["beta"][:, 46], d["decay"][:, 47] = float("nan"), float("nan")
+    o, w = ttt.delta(*args, cu_seqlens=d["cu"])
+    got = ttt.delta_backward(*args, d["go"], d["gw"], cu_seqlens=d["cu"])
+    keep = torch.ones(120, dtype=torch.bool, device="cuda")
+    keep[40:70] = False
+    assert torch.equal(o[keep], ref[0][keep]) and torch.equal(w[[0, 2]], ref[1][[0, 2]])
+    for i in range(3):
+        assert torch.equal(got[i][keep], gref[i][keep])
+    for i in (3, 4):
+        assert torch.equal(got[i][:, keep], gref[i][:, keep])
+    assert torch.equal(got[5][[0, 2]], gref[5][[0, 2]])
