@@ -4,8 +4,9 @@
 //
 // All products run on fp16 MFMA with fp32 accumulation, on operands of two fp16 parts,
 // x = h + l, l = fp16(x - h): 22 bits, products h*h + h*l + l*h.  Every matrix here has a spectral
-// norm below 4 (X 1.2, A 1.5, B 3.45): stored times 4096 its elements stay below 2^14, and an element
-// above 2^-15 keeps its low part out of the subnormal range; what smaller ones lose is below 2^-36.
+// norm below 3.9 (X 1.2, A 1.5, B 3.45): stored times 2^14 its elements stay in fp16's range, and an element
+// above 2^-17 keeps its low part out of the subnormal numbers; what smaller ones lose is below 2^-38.
+// (X is that small throughout only where |G| is below 1e-10, where 1e-7 beside it leaves X near zero.)
 // One part would not do throughout: the steps multiply what is lost along small singular directions
 // by up to 3.4445 each, 485 in five.  It does in the last two steps of bf16 matrices, where what
 // is lost (2^-12) is multiplied by 3.4 at most and the result has 8 bits; and bf16 matrices enter the
@@ -31,7 +32,7 @@ __device__ __forceinline__ f32x4 mma(const f16x8 a, const f16x8 b, f32x4 c) {
 }
 
 constexpr int KS = 32;              // reduction elements a stage
-constexpr float kUnit = 4096.0f;    // a stored element for 1
+constexpr float kUnit = 16384.0f;   // a stored element for 1
 
 // Split matrix: one plane a part.  A plane is cut in fragments of 16 rows x 32 columns, 1 KB each in
 // the order in which lanes take them (lane = 16 (column / 8 % 4) + row % 16, eight columns a lane),
