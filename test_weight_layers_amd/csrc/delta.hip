@@ -338,8 +338,6 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, C> s_r, s_ul;
   __shared__ __attribute__((aligned(16))) SplitTile<UP, SL, C> s_u;
   constexpr int64_t tokens = DK * C * 2 * TP, tplane = DK * C * 2;      // bytes of a chunk's tokens and a part
-  // the operands of Q wait in registers too, but for fp32 tokens of 256, which would not fit
-  constexpr bool kHoldQ = !BWD && (TP == 1 || DK < 256);
   const int slices = p.dv / SL, item = xcd_item(gridDim.x);
   const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
   const int wave = wave_id(), w = wave & 3, l = threadIdx.x & 63, g = l >> 4, li = l & 15;
@@ -350,7 +348,7 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
   const int64_t plane = C * C * 2;
   if (wave < 4) {
     const int t4 = 16 * w + 4 * g;      // this lane's four rows of every 64 x 16 product
-    Split<TP> kf[NK], qf[kHoldQ ? NK : 1];
+    Split<TP> kf[NK], qf[BWD ? 1 : NK];
     Split<kFull> tf[2];
     Split<kOut<T>> af[2];
     T v[4];
@@ -379,11 +377,6 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
       for (int i = 0; i < NK; ++i) kf[i] = load_token(p.kp, 0, i);
       load_values(0);
       load_square(p.tm, 0, tf);
-      if constexpr (kHoldQ) {
-#pragma unroll
-        for (int i = 0; i < NK; ++i) qf[i] = load_token(p.qp, 0, i);
-      }
-      if (!BWD) load_square(p.am, 0, af);
     }
     lds_barrier();
     for (int c = 0; c < chunks; ++c) {
@@ -393,7 +386,8 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
         pa.add(kf[i], W0.ld(li, 32 * i + 8 * g));
-        kf[i] = load_token(p.kp, nx, i);
+        if constexpr (BWD) kf[i] = load_token(p.kp, nx, i);
+        else qf[i] = load_token(p.qp, c, i);
       }
       f32x4 rr = pa.sum();
 #pragma unroll
@@ -408,7 +402,8 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
       const f32x4 u = tr.sum();
       s_ul.st4(li, t4, u * el_now);
       s_u.st4(li, t4, u);
-      load_square(p.tm, nx, tf);
+      if (BWD) load_square(p.tm, nx, tf);
+      else load_square(p.am, c, af);
       lds_barrier();
       if (BWD) {
         s_u.copy_t4(0, 16 * w, p.u + (ch0 + (int64_t)c * p.heads) * (C * p.dv * 2 * kFull), (int64_t)C * p.dv * 2,
@@ -417,18 +412,14 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
         Sums<kOut<T>> qa[2];
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-          if constexpr (kHoldQ) {
-            qa[i & 1].add(qf[i], W0.template ld<kOut<T>>(li, 32 * i + 8 * g));
-            qf[i] = load_token(p.qp, nx, i);
-          } else {
-            qa[i & 1].add(load_token(p.qp, c, i), W0.template ld<kOut<T>>(li, 32 * i + 8 * g));
-          }
+          qa[i & 1].add(qf[i], W0.template ld<kOut<T>>(li, 32 * i + 8 * g));
+          kf[i] = load_token(p.kp, nx, i);
         }
         Sums<kOut<T>> au;
         au.add(af[0], s_u.ld(li, 8 * g));
         if (w >= 2) au.add(af[1], s_u.ld(li, 32 + 8 * g));
         const f32x4 o = (qa[0].sum() + qa[1].sum()) * eg_now * p.scale + au.sum();
-        load_square(p.am, nx, af);
+        load_square(p.tm, nx, tf);
         o_rows.store(static_cast<T *>(p.o) + ((int64_t)sq.start + c * C) * p.ldo + h * p.dv + sl * SL, t4, len, o);
       }
       lds_barrier();
