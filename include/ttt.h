@@ -313,7 +313,9 @@ int ttt_stream_ex(int32_t heads, int32_t d, int32_t m,
  *   left as they were, or set to zero with TTT_DELTA_ZERO_UNUSED; gradients of them are zero.
  * Precision: fp32 states and sums; products take fp32 operands as three bf16 parts (24 bits),
  *   what only reaches bf16 outputs as two.  States, rate gradients and fp32 outputs are as exact
- *   as fp32 arithmetic gives; bf16 outputs are rounded once.
+ *   as fp32 arithmetic gives; bf16 outputs are rounded once.  Tokens are taken 64 at a time: a NaN
+ *   or an infinity in a token or rate may also reach the rows before it in its chunk of 64 (of
+ *   that sequence; of its own column of v only, where it stands in v).
  * Deterministic: the same inputs give the same bits.  n <= 2^31 - 65; chunks x H and
  *   sequences x H x dv/16 below 2^24; in the chunked calls 64 rows span < 2 GiB.
  */
@@ -396,8 +398,8 @@ int ttt_gated_residual_backward(int32_t channels, int32_t norm_width, const void
  * g, out  : [batch][rows][cols] device, `dtype`; element (i, r, c) at i * bs + r * ld + c
  *           (bs >= 0, ld >= cols).  out may be g with the same strides, or must not overlap it.
  * steps   : >= 0 (0: only the normalisation).
- * Precision: every product accumulates in fp32 on operands of 17 bits (bf16 matrices) or
- *           24 bits (fp32 matrices); the norm is summed in 64 bits.  Deterministic.
+ * Precision: every product accumulates in fp32 on operands of two fp16 parts (22 bits; one part
+ *           in the last two steps of bf16 matrices); the norm is summed in 64 bits.  Deterministic.
  * workspace: >= ttt_orthogonalise_workspace_bytes(rows, cols, batch, dtype).
  */
 int ttt_orthogonalise_workspace_bytes(int32_t rows, int32_t cols, int32_t batch, int32_t dtype, size_t *bytes);

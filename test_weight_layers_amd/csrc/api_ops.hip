@@ -86,8 +86,36 @@ int check_delta_shape(int H, int Hk, int dk, int dv, int dtype) {
 struct DeltaPlan {
   int nchunk;
   size_t off_seqs, off_chunks, off_used, off_eg, off_el, off_be, off_gam, off_tm, off_am, off_tt, off_kp, off_qp, off_kt, off_qt;
-  size_t off_gop, off_w0t, off_gwt, off_u, off_dr, off_gqp, off_gkp, off_gb, off_gd, total;
+  size_t off_gop, off_w0t, off_gwt, off_u, off_dr, off_gqp, off_gkp, off_gb, off_gd, off_su, off_sm, total;
+  int segs;
 };
+
+// Segments that the chunks of a sequence are cut in for the forward pass (1: none), from what the
+// states of a chunk take where the order of the chunks bounds them (c us), how many workgroups run at
+// once on 256 CUs of one or two each, and what a further segment costs (its start, j us; o both launches).
+// Measured with and without: 687 chunks x 4 heads of 256 1680 and 940 us (5 segments), 313 x 2 heads of
+// 128 477 and 110 (16); not taken for 9 sequences of 35 chunks x 2 heads of 128 (66, with 3 74).
+int delta_segments(int H, int dk, int dv, int64_t nc, int64_t nseq, bool bf16) {
+  const int slices = dv / kDeltaSlice, size = dk == 64 ? 0 : dk == 128 ? 1 : 2;
+  const int64_t wgs = nseq * H * slices;
+  if (wgs > 256) return 1;
+  constexpr double kChunkUs[2][3] = {{1.35, 1.55, 2.05}, {1.8, 2.6, 4.0}}, kJoinUs[3] = {1.0, 1.4, 4.0}, kBothUs[3] = {2, 4, 0};
+  const auto rounds = [](int64_t x) {
+    const int64_t r = x % 512;
+    return (double)(x / 512) * 1.6 + (r == 0 ? 0.0 : r <= 256 ? 1.0 : 1.5);
+  };
+  const double us = kChunkUs[bf16 ? 0 : 1][size];
+  const int64_t per = (nc + nseq - 1) / nseq;
+  int best = 1;
+  double least = us * (double)per * rounds(wgs);
+  for (int s = 3; s <= 64 && s <= per; ++s) {
+    const double t = us * (double)((per + s - 1) / s) *
+                         (rounds(nseq * H * (slices + (int64_t)(s - 2) * (slices + dk / kDeltaSlice))) + rounds(wgs * (s - 1))) +
+                     kBothUs[size] + s * kJoinUs[size];
+    if (t < least) least = t, best = s;
+  }
+  return best;
+}
 
 int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype, bool backward, DeltaPlan *out) {
   if (n < 0 || nseq < 1) return fail(TTT_EINVAL, "n must be >= 0 and sequences >= 1");
@@ -118,6 +146,11 @@ int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype
   P.off_kp = take(tok);
   P.off_qp = take(tok);
   P.off_kt = take(tok);
+  P.segs = backward ? 1 : delta_segments(H, dk, dv, nc, nseq, dtype == TTT_BF16);
+  if (P.segs > 2) {
+    P.off_su = take((size_t)nseq * (P.segs - 1) * H * dv * dk * 4);
+    P.off_sm = take((size_t)nseq * (P.segs - 2) * H * dk * dk * sb);
+  }
   if (backward) {
     P.off_gop = take(cc * kDeltaChunk * dv * tb);
     P.off_gam = take(cc * kDeltaChunk * 8);
@@ -168,6 +201,8 @@ int delta_params(int H, int Hk, int dk, int dv, const float *w, const Rows &q, c
   p->tm = b + P.off_tm, p->am = b + P.off_am, p->kt = b + P.off_kt;
   p->be = reinterpret_cast<float *>(b + P.off_be);
   p->kp = b + P.off_kp, p->qp = b + P.off_qp;
+  p->segs = P.segs;
+  p->seg_u = reinterpret_cast<float *>(b + P.off_su), p->seg_m = b + P.off_sm;
   if (backward) {
     p->gam = reinterpret_cast<double *>(b + P.off_gam);
     p->gop = b + P.off_gop;

@@ -49,6 +49,9 @@ struct DeltaParams {
   char *tt;                         // T^T (backward)
   char *kp, *qp;                    // [nchunk][Hk] split tokens 64 x dk, 0 past the chunk
   char *kt, *qt;                    // [nchunk][Hk] the same transposed, dk x 64 (qt: backward)
+  int segs;                         // segments of a sequence that run at once (forward); < 3: none
+  float *seg_u;                     // [nseq][segs - 1][H][dv][dk]
+  char *seg_m;                      // [nseq][segs - 2][H] split M^T, dk x dk
   // backward
   const void *go;                   // gradient of o
   int64_t ldgo;

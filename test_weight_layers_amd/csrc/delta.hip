@@ -11,6 +11,8 @@
 // Three kernels: the packed sequences are laid out in chunks (plan), T and A of every chunk at
 // once (chunk), then the states in order of the chunks, split over heads and 16-column slices of
 // dv, which do not depend on one another (states).
+#include <type_traits>
+
 #include "delta.h"
 #include "delta_layout.h"
 #include "split.h"
@@ -331,101 +333,169 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
 // as this chunk's have been used.  Bound by the order of the chunks, and within one by the 64
 // bytes a clock at which a CU takes its operands.
 // BWD writes the states and U that the gradient needs, in place of the outputs.
-template <typename T, int DK, bool BWD>
+//
+// Where sequences are long and few, the chunks of one are cut in segments that run at once (the state is
+// linear in the one before): W after a segment = W before it times M + U, U the state that the segment
+// alone leaves and M the one that a unit matrix becomes in it with v = 0.
+//   kFirst: the first segment, outputs and all; U and M of the others but the last, of which M is
+//           dk / 16 more slices of rows
+//   kSecond: the others, each from its own starting state, (W_1 M_1 + U_1) M_2 + U_2 ..
+enum { kForward, kBackward, kFirst, kSecond };
+template <typename T, int DK, int MODE>
 __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
+  constexpr bool BWD = MODE == kBackward;
   constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>, UP = BWD ? kFull : kOut<T>;
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, DK> s_w[2];
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, C> s_r, s_ul;
   __shared__ __attribute__((aligned(16))) SplitTile<UP, SL, C> s_u;
   constexpr int64_t tokens = DK * C * 2 * TP, tplane = DK * C * 2;      // bytes of a chunk's tokens and a part
   const int slices = p.dv / SL, item = xcd_item(gridDim.x);
-  const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
   const int wave = wave_id(), w = wave & 3, l = threadIdx.x & 63, g = l >> 4, li = l & 15;
+  int bh, sl, seg = 0;
+  bool unit = false;                    // rows of M
+  if constexpr (MODE == kFirst) {
+    const int each = slices + DK / SL, all = slices + (p.segs - 2) * each;
+    bh = item / all, sl = item % all;
+    if (sl >= slices) {
+      sl -= slices;
+      seg = 1 + sl / each, sl %= each;
+      unit = sl >= slices;
+      if (unit) sl -= slices;
+    }
+  } else if constexpr (MODE == kSecond) {
+    const int all = (p.segs - 1) * slices;
+    bh = item / all, sl = item % slices;
+    seg = 1 + item % all / slices;
+  } else {
+    bh = item / slices, sl = item % slices;
+  }
+  const int h = bh % p.heads, b = bh / p.heads;
   const int kh = h / (p.heads / p.key_heads);
   const DeltaSeq sq = seq_of(p, b);
   const int chunks = (sq.len + C - 1) / C;
+  int c_first = 0, c_end = chunks;
+  if constexpr (MODE == kFirst || MODE == kSecond) {
+    const int per = (chunks + p.segs - 1) / p.segs;
+    c_first = seg * per, c_end = c_first + per < chunks ? c_first + per : chunks;
+    if (seg > 0 && (c_first >= c_end || (MODE == kFirst && c_end == chunks))) return;   // empty, or the last
+  }
   const int64_t ch0 = (int64_t)sq.chunk0 * p.heads + h, ck0 = (int64_t)sq.chunk0 * p.key_heads + kh;
   const int64_t plane = C * C * 2;
+  constexpr int64_t mplane = DK * DK * 2;
+  // U (this lane's row) and M of segment j
+  const auto u_of = [&](int j) {
+    return p.seg_u + (((int64_t)(b * (p.segs - 1) + j) * p.heads + h) * p.dv + sl * SL + li) * DK + 4 * g;
+  };
+  const auto m_of = [&](int j) { return p.seg_m + ((int64_t)(b * (p.segs - 2) + j - 1) * p.heads + h) * (DK * DK * 2 * kFull); };
+  if constexpr (MODE == kSecond) {      // the starting state, into s_w[0]: 16 of its columns a tile, over all waves
+    constexpr int NW = (DK / 16 + 7) / 8;
+    for (int j = 0; j < seg; ++j) {
+      const SplitTile<kFull, SL, DK> &W = s_w[(seg - j) & 1];
+      const char *m = m_of(j > 0 ? j : 1);
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const int tile = wave * NW + i;
+        if (tile >= DK / 16) break;
+        f32x4 x = *reinterpret_cast<const f32x4 *>(u_of(j) + 16 * tile);
+        if (j > 0) {
+          Sums<kFull> d;
+#pragma unroll 4
+          for (int k = 0; k < NK; ++k) d.add(load_frag<kFull>(m, mplane, tile * NK + k), W.ld(li, 32 * k + 8 * g));
+          x += d.sum();
+        }
+        s_w[(seg - 1 - j) & 1].st4(li, 16 * tile + 4 * g, x);
+      }
+      lds_barrier();
+    }
+  }
   if (wave < 4) {
     const int t4 = 16 * w + 4 * g;      // this lane's four rows of every 64 x 16 product
-    Split<TP> kf[NK], qf[BWD ? 1 : NK];
-    Split<kFull> tf[2];
-    Split<kOut<T>> af[2];
-    T v[4];
-    f32x4 eg, el, be;
+    const int vcol = h * p.dv + (unit ? 0 : sl * SL);
     const Rows4<T> v_rows(t4, li, p.ldv), o_rows(t4, li, BWD ? 0 : p.ldo);
-    const auto load_token = [&](const char *tok, int c, int i) {
-      return load_frag<TP>(tok + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, w * NK + i);
-    };
-    const auto load_values = [&](int c) {
-      const int64_t o = (ch0 + (int64_t)c * p.heads) * C + t4;
-      eg = *reinterpret_cast<const f32x4 *>(p.eg + o);
-      el = *reinterpret_cast<const f32x4 *>(p.el + o);
-      be = *reinterpret_cast<const f32x4 *>(p.be + o);
-      v_rows.load(static_cast<const T *>(p.v) + ((int64_t)sq.start + c * C) * p.ldv + h * p.dv + sl * SL, t4,
-                  sq.len - c * C, v);
-    };
-    const auto load_square = [&](const char *m, int c, auto &f) {
+    const auto rows = [&](auto with_outputs) {
+      constexpr bool OUT = decltype(with_outputs)::value;
+      Split<TP> kf[NK], qf[OUT ? NK : 1];
+      Split<kFull> tf[2];
+      Split<kOut<T>> af[2];
+      T v[4];
+      f32x4 eg, el, be;
+      const auto load_token = [&](const char *tok, int c, int i) {
+        return load_frag<TP>(tok + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, w * NK + i);
+      };
+      const auto load_values = [&](int c) {
+        const int64_t o = (ch0 + (int64_t)c * p.heads) * C + t4;
+        eg = *reinterpret_cast<const f32x4 *>(p.eg + o);
+        el = *reinterpret_cast<const f32x4 *>(p.el + o);
+        be = *reinterpret_cast<const f32x4 *>(p.be + o);
+        v_rows.load(static_cast<const T *>(p.v) + ((int64_t)sq.start + c * C) * p.ldv + vcol, t4, sq.len - c * C, v);
+      };
+      const auto load_square = [&](const char *m, int c, auto &f) {
 #pragma unroll
-      // (the second half is zero for the first two waves, whose products leave it out; loads under a
-      // condition would make every later wait one for all loads)
-      for (int i = 0; i < 2; ++i)
-        f[i] = load_frag<sizeof(f[0]) / 16>(m + (ch0 + (int64_t)c * p.heads) * kSquare, plane, w * 2 + i);
-    };
-    if (chunks > 0) {
+        // (the second half is zero for the first two waves, whose products leave it out; loads under a
+        // condition would make every later wait one for all loads)
+        for (int i = 0; i < 2; ++i)
+          f[i] = load_frag<sizeof(f[0]) / 16>(m + (ch0 + (int64_t)c * p.heads) * kSquare, plane, w * 2 + i);
+      };
+      if (c_first < c_end) {
 #pragma unroll
-      for (int i = 0; i < NK; ++i) kf[i] = load_token(p.kp, 0, i);
-      load_values(0);
-      load_square(p.tm, 0, tf);
-    }
-    lds_barrier();
-    for (int c = 0; c < chunks; ++c) {
-      const int len = sq.len - c * C < C ? sq.len - c * C : C, nx = c + 1 < chunks ? c + 1 : c;
-      const SplitTile<kFull, SL, DK> &W0 = s_w[BWD ? 0 : c & 1];
-      Sums<kFull> pa;
-#pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        pa.add(kf[i], W0.ld(li, 32 * i + 8 * g));
-        if constexpr (BWD) kf[i] = load_token(p.kp, nx, i);
-        else qf[i] = load_token(p.qp, c, i);
+        for (int i = 0; i < NK; ++i) kf[i] = load_token(p.kp, c_first, i);
+        load_values(c_first);
+        load_square(p.tm, c_first, tf);
       }
-      f32x4 rr = pa.sum();
-#pragma unroll
-      for (int r = 0; r < 4; ++r) rr[r] = t4 + r < len ? be[r] * (to_f32(v[r]) - eg[r] * rr[r]) : 0.0f;
-      const f32x4 eg_now = eg, el_now = el;
-      s_r.st4(li, t4, rr);
       lds_barrier();
-      load_values(nx);
-      Sums<kFull> tr;
-      tr.add(tf[0], s_r.ld(li, 8 * g));
-      if (w >= 2) tr.add(tf[1], s_r.ld(li, 32 + 8 * g));
-      const f32x4 u = tr.sum();
-      s_ul.st4(li, t4, u * el_now);
-      s_u.st4(li, t4, u);
-      if (BWD) load_square(p.tm, nx, tf);
-      else load_square(p.am, c, af);
-      lds_barrier();
-      if (BWD) {
-        s_u.copy_t4(0, 16 * w, p.u + (ch0 + (int64_t)c * p.heads) * (C * p.dv * 2 * kFull), (int64_t)C * p.dv * 2,
-                    frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
-      } else {
-        Sums<kOut<T>> qa[2];
+      for (int c = c_first; c < c_end; ++c) {
+        const int len = sq.len - c * C < C ? sq.len - c * C : C, nx = c + 1 < c_end ? c + 1 : c;
+        const SplitTile<kFull, SL, DK> &W0 = s_w[BWD ? 0 : (c - c_first) & 1];
+        Sums<kFull> pa;
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-          qa[i & 1].add(qf[i], W0.template ld<kOut<T>>(li, 32 * i + 8 * g));
-          kf[i] = load_token(p.kp, nx, i);
+          pa.add(kf[i], W0.ld(li, 32 * i + 8 * g));
+          if constexpr (OUT) qf[i] = load_token(p.qp, c, i);    // into the registers that K leaves
+          else kf[i] = load_token(p.kp, nx, i);
         }
-        Sums<kOut<T>> au;
-        au.add(af[0], s_u.ld(li, 8 * g));
-        if (w >= 2) au.add(af[1], s_u.ld(li, 32 + 8 * g));
-        const f32x4 o = (qa[0].sum() + qa[1].sum()) * eg_now * p.scale + au.sum();
-        load_square(p.tm, nx, tf);
-        o_rows.store(static_cast<T *>(p.o) + ((int64_t)sq.start + c * C) * p.ldo + h * p.dv + sl * SL, t4, len, o);
+        f32x4 rr = pa.sum();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float vr = unit ? 0.0f : to_f32(v[r]);
+          rr[r] = t4 + r < len ? be[r] * (vr - eg[r] * rr[r]) : 0.0f;
+        }
+        const f32x4 eg_now = eg, el_now = el;
+        s_r.st4(li, t4, rr);
+        lds_barrier();
+        load_values(nx);
+        Sums<kFull> tr;
+        tr.add(tf[0], s_r.ld(li, 8 * g));
+        if (w >= 2) tr.add(tf[1], s_r.ld(li, 32 + 8 * g));
+        const f32x4 u = tr.sum();
+        s_ul.st4(li, t4, u * el_now);
+        if (OUT || BWD) s_u.st4(li, t4, u);
+        if constexpr (OUT) load_square(p.am, c, af);
+        else load_square(p.tm, nx, tf);
+        lds_barrier();
+        if constexpr (BWD)
+          s_u.copy_t4(0, 16 * w, p.u + (ch0 + (int64_t)c * p.heads) * (C * p.dv * 2 * kFull), (int64_t)C * p.dv * 2,
+                      frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
+        if constexpr (OUT) {
+          Sums<kOut<T>> qa[2];
+#pragma unroll
+          for (int i = 0; i < NK; ++i) {
+            qa[i & 1].add(qf[i], W0.template ld<kOut<T>>(li, 32 * i + 8 * g));
+            kf[i] = load_token(p.kp, nx, i);
+          }
+          Sums<kOut<T>> au;
+          au.add(af[0], s_u.template ld<kOut<T>>(li, 8 * g));
+          if (w >= 2) au.add(af[1], s_u.template ld<kOut<T>>(li, 32 + 8 * g));
+          const f32x4 o = (qa[0].sum() + qa[1].sum()) * eg_now * p.scale + au.sum();
+          load_square(p.tm, nx, tf);
+          o_rows.store(static_cast<T *>(p.o) + ((int64_t)sq.start + c * C) * p.ldo + h * p.dv + sl * SL, t4, len, o);
+        }
+        lds_barrier();
       }
-      lds_barrier();
-    }
+    };
+    if (MODE == kForward || MODE == kSecond || (MODE == kFirst && seg == 0)) rows(std::true_type{});
+    else rows(std::false_type{});
   } else {
-    const int64_t wrow = (((int64_t)b * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
+    const int64_t wrow = ((int64_t)bh * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
     f32x4 st[NT];
     Split<TP> ktf[NT][2];
     float ec = 0.0f;
@@ -434,19 +504,29 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
     };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      st[i] = *reinterpret_cast<const f32x4 *>(p.w + wrow + 16 * i);
-      s_w[0].st4(li, (w * NT + i) * 16 + 4 * g, st[i]);
+      const int col = (w * NT + i) * 16 + 4 * g;
+      if constexpr (MODE == kSecond) {
+        st[i] = s_w[0].at4(li, col);
+      } else {
+        if (MODE == kFirst && seg > 0) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) st[i][r] = unit && col + r == sl * SL + li ? 1.0f : 0.0f;
+        } else {
+          st[i] = *reinterpret_cast<const f32x4 *>(p.w + wrow + 16 * i);
+        }
+        s_w[0].st4(li, col, st[i]);
+      }
     }
-    if (chunks > 0) {
+    if (c_first < c_end) {
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(0, i, x);
-      ec = p.eg[ch0 * C + C - 1];
+        for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(c_first, i, x);
+      ec = p.eg[(ch0 + (int64_t)c_first * p.heads) * C + C - 1];
     }
     lds_barrier();
-    for (int c = 0; c < chunks; ++c) {
-      const int nx = c + 1 < chunks ? c + 1 : c;
+    for (int c = c_first; c < c_end; ++c) {
+      const int nx = c + 1 < c_end ? c + 1 : c;
       if (BWD) {    // the state before the chunk, dk x dv
         float *o = p.w0t + (ch0 + (int64_t)c * p.heads) * (DK * p.dv);
 #pragma unroll
@@ -455,7 +535,7 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
       }
       lds_barrier();
       lds_barrier();
-      SplitTile<kFull, SL, DK> &W1 = s_w[BWD ? 0 : ~c & 1];
+      SplitTile<kFull, SL, DK> &W1 = s_w[BWD ? 0 : ~(c - c_first) & 1];
       const Split<kFull> u0 = s_ul.ld(li, 8 * g), u1 = s_ul.ld(li, 32 + 8 * g);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
@@ -472,9 +552,19 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
         for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(nx, i, x);
       ec = p.eg[(ch0 + (int64_t)nx * p.heads) * C + C - 1];
     }
-    if (!BWD)
+    if constexpr (!BWD) {
+      if (MODE == kFirst && unit) {     // M^T: rows dk, k = the rows that this slice has
+        const SplitTile<kFull, SL, DK> &W = s_w[(c_end - c_first) & 1];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(p.w_out + wrow + 16 * i) = st[i];
+        for (int i = 0; i < NT; ++i)
+          W.copy_t4(0, (w * NT + i) * 16, m_of(seg), mplane, frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, NK));
+      } else {
+        float *o = MODE == kFirst && c_end < chunks ? u_of(seg) + w * (DK / 4) : p.w_out + wrow;
+        if (MODE == kForward || c_end == chunks || MODE == kFirst)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(o + 16 * i) = st[i];
+      }
+    }
   }
 }
 
@@ -590,11 +680,18 @@ hipError_t chunk_impl(const DeltaParams &p, bool backward, hipStream_t s) {
 
 template <typename T, int DK>
 hipError_t states_impl(const DeltaParams &p, bool backward, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.nseq * p.heads * (p.dv / SL)));
-  if (backward)
-    hipLaunchKernelGGL((delta_state_kernel<T, DK, true>), grid, dim3(512), 0, s, p);
-  else
-    hipLaunchKernelGGL((delta_state_kernel<T, DK, false>), grid, dim3(512), 0, s, p);
+  const int bh = p.nseq * p.heads, slices = p.dv / SL;
+  if (backward) {
+    hipLaunchKernelGGL((delta_state_kernel<T, DK, kBackward>), dim3(bh * slices), dim3(512), 0, s, p);
+  } else if (p.segs < 3) {
+    hipLaunchKernelGGL((delta_state_kernel<T, DK, kForward>), dim3(bh * slices), dim3(512), 0, s, p);
+  } else {
+    hipLaunchKernelGGL((delta_state_kernel<T, DK, kFirst>), dim3(bh * (slices + (p.segs - 2) * (slices + DK / SL))), dim3(512),
+                       0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((delta_state_kernel<T, DK, kSecond>), dim3(bh * (p.segs - 1) * slices), dim3(512), 0, s, p);
+  }
   return hipGetLastError();
 }
 

@@ -149,6 +149,16 @@ template <int P, int R, int Ccols> struct SplitTile {
       v -= (float)h;
     }
   }
+  __device__ __forceinline__ f32x4 at4(int r, int c) const {
+    f32x4 v = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = P - 1; i >= 0; --i) {
+      const bf16x4 h = *reinterpret_cast<const bf16x4 *>(b + i * kPlane + (r * kPitch + c) * 2);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] += (float)h[x];
+    }
+    return v;
+  }
   // Lane (g, li)'s rows r0 + 4 g .. + 3 of column c0 + li: to element e of a split matrix in memory, or
   // (their sum, which is the fp32 value for three parts) to fp32 memory.
   __device__ __forceinline__ bf16x4 t4(int part, int r0, int c0) const {

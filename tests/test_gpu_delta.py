@@ -458,3 +458,37 @@ def test_sequences_do_not_reach_each_other():
     for i in (3, 4):
         assert torch.equal(got[i][:, keep], gref[i][:, keep])
     assert torch.equal(got[5][[0, 2]], gref[5][[0, 2]])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lens,H,Hk,dk,dv", [([2000], 1, 1, 64, 64), ([1537], 2, 1, 128, 192), ([1700], 1, 1, 256, 64),
+                                             ([2500, 0, 1, 70, 1900], 1, 1, 64, 64), ([0, 64, 1601], 1, 1, 64, 128)])
+def test_long_sequences(lens, H, Hk, dk, dv, dtype):
+    """Few long sequences, whose segments run at once and are joined; short and empty ones beside them."""
+    from test_weight_layers_amd import ttt
+    d = inputs(lens, H, Hk, dk, dv, dtype, seed=22, tail=3, rate=0.02)
+    o_ref, w_ref = reference(d, Hk)
+    g = dev(d)
+    args = [g[x] for x in ("w", "q", "k", "v", "beta", "decay")]
+    o, w = ttt.delta(*args, key_heads=Hk, cu_seqlens=g["cu"])
+    assert rel(o, o_ref) <= TOL[dtype][dtype]
+    for s in range(len(lens)):
+        assert rel(w[s], w_ref[s]) <= TOL[dtype][torch.float32], s
+    assert torch.equal(ttt.delta(*args, key_heads=Hk, cu_seqlens=g["cu"])[1], w)
+    ttt.delta(*args, key_heads=Hk, cu_seqlens=g["cu"], w_out=g["w"])
+    assert torch.equal(g["w"], w)
+
+
+def test_long_sequence_keeps_nan_to_its_rows():
+    """Not a number in a value or a starting state stays in that row of the state, through the joins too."""
+    from test_weight_layers_amd import ttt
+    d = dev(inputs([3000], 1, 1, 64, 64, torch.float32, seed=23, rate=0.02))
+    args = [d[x] for x in ("w", "q", "k", "v", "beta", "decay")]
+    ref = ttt.delta(*args)
+    d["v"][700, 5], d["w"][0, 0, 40, 3] = float("nan"), float("inf")
+    o, w = ttt.delta(*args)
+    keep = torch.ones(64, dtype=torch.bool, device="cuda")
+    keep[5] = keep[40] = False
+    assert torch.equal(w[0, 0][keep], ref[1][0, 0][keep]) and not torch.isfinite(w[0, 0, [5, 40]]).any()
+    assert torch.equal(o[:, keep], ref[0][:, keep]) and torch.equal(o[:640, 5], ref[0][:640, 5])    # 640: its chunk
+    assert not torch.isfinite(o[700:, 5]).any() and not torch.isfinite(o[:, 40]).any()
