@@ -90,28 +90,28 @@ struct DeltaPlan {
   int segs;
 };
 
-// Segments that the chunks of a sequence are cut in for the forward pass (1: none), from what the
-// states of a chunk take where the order of the chunks bounds them (c us), how many workgroups run at
-// once on 256 CUs of one or two each, and what a further segment costs (its start, j us; o both launches).
-// Measured with and without: 687 chunks x 4 heads of 256 1680 and 940 us (5 segments), 313 x 2 heads of
-// 128 477 and 110 (16); not taken for 9 sequences of 35 chunks x 2 heads of 128 (66, with 3 74).
-int delta_segments(int H, int dk, int dv, int64_t nc, int64_t nseq, bool bf16) {
+// Segments that the chunks of a sequence are cut in (1: none), from what the states of a chunk take where
+// the order of the chunks bounds them (us), half as much again for their gradients, how many workgroups
+// run at once on 256 CUs of one or two each, and what a further segment (its start) and the second launch
+// cost.  Measured with and without: 687 chunks x 4 heads of 256 1680 and 940 us (5 segments), 313 x 2
+// heads of 128 477 and 110 (16), its gradient over 94 373 and 169; not taken for 9 sequences of 35 chunks
+// x 2 heads of 128 (66, with 3 74).
+int delta_segments(int H, int dk, int dv, int64_t nc, int64_t nseq, bool bf16, bool backward) {
   const int slices = dv / kDeltaSlice, size = dk == 64 ? 0 : dk == 128 ? 1 : 2;
-  const int64_t wgs = nseq * H * slices;
+  const int64_t wgs = nseq * H * slices, per = (nc + nseq - 1) / nseq;
   if (wgs > 256) return 1;
   constexpr double kChunkUs[2][3] = {{1.35, 1.55, 2.05}, {1.8, 2.6, 4.0}}, kJoinUs[3] = {1.0, 1.4, 4.0}, kBothUs[3] = {2, 4, 0};
   const auto rounds = [](int64_t x) {
     const int64_t r = x % 512;
     return (double)(x / 512) * 1.6 + (r == 0 ? 0.0 : r <= 256 ? 1.0 : 1.5);
   };
-  const double us = kChunkUs[bf16 ? 0 : 1][size];
-  const int64_t per = (nc + nseq - 1) / nseq;
   int best = 1;
-  double least = us * (double)per * rounds(wgs);
+  double least = (double)per * rounds(wgs) * (backward ? 2.5 : 1.0);
   for (int s = 3; s <= 64 && s <= per; ++s) {
-    const double t = us * (double)((per + s - 1) / s) *
-                         (rounds(nseq * H * (slices + (int64_t)(s - 2) * (slices + dk / kDeltaSlice))) + rounds(wgs * (s - 1))) +
-                     kBothUs[size] + s * kJoinUs[size];
+    const double state = rounds(nseq * H * (slices + (int64_t)(s - 2) * (slices + dk / kDeltaSlice))) + rounds(wgs * (s - 1));
+    const double grad = backward ? 1.5 * 2.0 * rounds(wgs * (s - 1)) : 0.0;
+    const double more = (kBothUs[size] + s * kJoinUs[size]) * (backward ? 2.5 : 1.0);
+    const double t = (double)((per + s - 1) / s) * (state + grad) + more / kChunkUs[bf16 ? 0 : 1][size];
     if (t < least) least = t, best = s;
   }
   return best;
@@ -146,10 +146,10 @@ int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype
   P.off_kp = take(tok);
   P.off_qp = take(tok);
   P.off_kt = take(tok);
-  P.segs = backward ? 1 : delta_segments(H, dk, dv, nc, nseq, dtype == TTT_BF16);
+  P.segs = delta_segments(H, dk, dv, nc, nseq, dtype == TTT_BF16, backward);
   if (P.segs > 2) {
     P.off_su = take((size_t)nseq * (P.segs - 1) * H * dv * dk * 4);
-    P.off_sm = take((size_t)nseq * (P.segs - 2) * H * dk * dk * sb);
+    P.off_sm = take((size_t)nseq * (P.segs - 2) * H * dk * dk * sb * (backward ? 2 : 1));
   }
   if (backward) {
     P.off_gop = take(cc * kDeltaChunk * dv * tb);

@@ -18,6 +18,9 @@ constexpr int kDeltaSlice = 16;
 constexpr int kDeltaParts = 3;
 constexpr int delta_token_parts(bool bf16) { return bf16 ? 1 : 3; }
 
+// What a launch of the sequential kernels does: everything, or the first or second part of segments.
+enum DeltaPart { kWhole, kFirst, kSecond };
+
 struct DeltaSeq {      // one packed sequence: rows [start, start + len), its chunks from chunk0 on
   int start, len, chunk0, pad;
 };
@@ -49,9 +52,9 @@ struct DeltaParams {
   char *tt;                         // T^T (backward)
   char *kp, *qp;                    // [nchunk][Hk] split tokens 64 x dk, 0 past the chunk
   char *kt, *qt;                    // [nchunk][Hk] the same transposed, dk x 64 (qt: backward)
-  int segs;                         // segments of a sequence that run at once (forward); < 3: none
-  float *seg_u;                     // [nseq][segs - 1][H][dv][dk]
-  char *seg_m;                      // [nseq][segs - 2][H] split M^T, dk x dk
+  int segs;                         // segments of a sequence that run at once; < 3: none
+  float *seg_u;                     // [nseq][segs - 1][H][dv][dk] what segments leave (see delta.hip)
+  char *seg_m;                      // [nseq][segs - 2][H] split dk x dk: M^T, and M (backward)
   // backward
   const void *go;                   // gradient of o
   int64_t ldgo;

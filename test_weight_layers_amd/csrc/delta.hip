@@ -340,10 +340,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
 //   kFirst: the first segment, outputs and all; U and M of the others but the last, of which M is
 //           dk / 16 more slices of rows
 //   kSecond: the others, each from its own starting state, (W_1 M_1 + U_1) M_2 + U_2 ..
-enum { kForward, kBackward, kFirst, kSecond };
-template <typename T, int DK, int MODE>
+template <typename T, int DK, bool BWD, int PART>
 __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
-  constexpr bool BWD = MODE == kBackward;
   constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>, UP = BWD ? kFull : kOut<T>;
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, DK> s_w[2];
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, C> s_r, s_ul;
@@ -353,7 +351,7 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
   const int wave = wave_id(), w = wave & 3, l = threadIdx.x & 63, g = l >> 4, li = l & 15;
   int bh, sl, seg = 0;
   bool unit = false;                    // rows of M
-  if constexpr (MODE == kFirst) {
+  if constexpr (PART == kFirst) {
     const int each = slices + DK / SL, all = slices + (p.segs - 2) * each;
     bh = item / all, sl = item % all;
     if (sl >= slices) {
@@ -362,7 +360,7 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
       unit = sl >= slices;
       if (unit) sl -= slices;
     }
-  } else if constexpr (MODE == kSecond) {
+  } else if constexpr (PART == kSecond) {
     const int all = (p.segs - 1) * slices;
     bh = item / all, sl = item % slices;
     seg = 1 + item % all / slices;
@@ -374,10 +372,10 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
   const DeltaSeq sq = seq_of(p, b);
   const int chunks = (sq.len + C - 1) / C;
   int c_first = 0, c_end = chunks;
-  if constexpr (MODE == kFirst || MODE == kSecond) {
+  if constexpr (PART != kWhole) {
     const int per = (chunks + p.segs - 1) / p.segs;
     c_first = seg * per, c_end = c_first + per < chunks ? c_first + per : chunks;
-    if (seg > 0 && (c_first >= c_end || (MODE == kFirst && c_end == chunks))) return;   // empty, or the last
+    if (seg > 0 && (c_first >= c_end || (PART == kFirst && c_end == chunks))) return;   // empty, or the last
   }
   const int64_t ch0 = (int64_t)sq.chunk0 * p.heads + h, ck0 = (int64_t)sq.chunk0 * p.key_heads + kh;
   const int64_t plane = C * C * 2;
@@ -386,34 +384,16 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
   const auto u_of = [&](int j) {
     return p.seg_u + (((int64_t)(b * (p.segs - 1) + j) * p.heads + h) * p.dv + sl * SL + li) * DK + 4 * g;
   };
-  const auto m_of = [&](int j) { return p.seg_m + ((int64_t)(b * (p.segs - 2) + j - 1) * p.heads + h) * (DK * DK * 2 * kFull); };
-  if constexpr (MODE == kSecond) {      // the starting state, into s_w[0]: 16 of its columns a tile, over all waves
-    constexpr int NW = (DK / 16 + 7) / 8;
-    for (int j = 0; j < seg; ++j) {
-      const SplitTile<kFull, SL, DK> &W = s_w[(seg - j) & 1];
-      const char *m = m_of(j > 0 ? j : 1);
-#pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        const int tile = wave * NW + i;
-        if (tile >= DK / 16) break;
-        f32x4 x = *reinterpret_cast<const f32x4 *>(u_of(j) + 16 * tile);
-        if (j > 0) {
-          Sums<kFull> d;
-#pragma unroll 4
-          for (int k = 0; k < NK; ++k) d.add(load_frag<kFull>(m, mplane, tile * NK + k), W.ld(li, 32 * k + 8 * g));
-          x += d.sum();
-        }
-        s_w[(seg - 1 - j) & 1].st4(li, 16 * tile + 4 * g, x);
-      }
-      lds_barrier();
-    }
-  }
+  const auto m_of = [&](int j) {
+    return p.seg_m + ((int64_t)(b * (p.segs - 2) + j - 1) * p.heads + h) * (mplane * kFull * (BWD ? 2 : 1));
+  };
+  if constexpr (PART == kSecond) join_segments<DK>(s_w, seg, u_of, m_of);
   if (wave < 4) {
     const int t4 = 16 * w + 4 * g;      // this lane's four rows of every 64 x 16 product
     const int vcol = h * p.dv + (unit ? 0 : sl * SL);
     const Rows4<T> v_rows(t4, li, p.ldv), o_rows(t4, li, BWD ? 0 : p.ldo);
-    const auto rows = [&](auto with_outputs) {
-      constexpr bool OUT = decltype(with_outputs)::value;
+    const auto rows = [&](auto live) {
+      constexpr bool OUT = decltype(live)::value && !BWD, RECORD = decltype(live)::value && BWD;
       Split<TP> kf[NK], qf[OUT ? NK : 1];
       Split<kFull> tf[2];
       Split<kOut<T>> af[2];
@@ -468,11 +448,11 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
         if (w >= 2) tr.add(tf[1], s_r.ld(li, 32 + 8 * g));
         const f32x4 u = tr.sum();
         s_ul.st4(li, t4, u * el_now);
-        if (OUT || BWD) s_u.st4(li, t4, u);
+        if (OUT || RECORD) s_u.st4(li, t4, u);
         if constexpr (OUT) load_square(p.am, c, af);
         else load_square(p.tm, nx, tf);
         lds_barrier();
-        if constexpr (BWD)
+        if constexpr (RECORD)
           s_u.copy_t4(0, 16 * w, p.u + (ch0 + (int64_t)c * p.heads) * (C * p.dv * 2 * kFull), (int64_t)C * p.dv * 2,
                       frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
         if constexpr (OUT) {
@@ -492,7 +472,7 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
         lds_barrier();
       }
     };
-    if (MODE == kForward || MODE == kSecond || (MODE == kFirst && seg == 0)) rows(std::true_type{});
+    if (PART != kFirst || seg == 0) rows(std::true_type{});
     else rows(std::false_type{});
   } else {
     const int64_t wrow = ((int64_t)bh * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
@@ -505,10 +485,10 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int col = (w * NT + i) * 16 + 4 * g;
-      if constexpr (MODE == kSecond) {
+      if constexpr (PART == kSecond) {
         st[i] = s_w[0].at4(li, col);
       } else {
-        if (MODE == kFirst && seg > 0) {
+        if (PART == kFirst && seg > 0) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) st[i][r] = unit && col + r == sl * SL + li ? 1.0f : 0.0f;
         } else {
@@ -517,53 +497,57 @@ __global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
         s_w[0].st4(li, col, st[i]);
       }
     }
-    if (c_first < c_end) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(c_first, i, x);
-      ec = p.eg[(ch0 + (int64_t)c_first * p.heads) * C + C - 1];
-    }
-    lds_barrier();
-    for (int c = c_first; c < c_end; ++c) {
-      const int nx = c + 1 < c_end ? c + 1 : c;
-      if (BWD) {    // the state before the chunk, dk x dv
-        float *o = p.w0t + (ch0 + (int64_t)c * p.heads) * (DK * p.dv);
+    const auto chain = [&](auto live) {
+      if (c_first < c_end) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-          s_w[0].copy_t4(0, (w * NT + i) * 16, o + frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(c_first, i, x);
+        ec = p.eg[(ch0 + (int64_t)c_first * p.heads) * C + C - 1];
       }
       lds_barrier();
-      lds_barrier();
-      SplitTile<kFull, SL, DK> &W1 = s_w[BWD ? 0 : ~(c - c_first) & 1];
-      const Split<kFull> u0 = s_ul.ld(li, 8 * g), u1 = s_ul.ld(li, 32 + 8 * g);
+      for (int c = c_first; c < c_end; ++c) {
+        const int nx = c + 1 < c_end ? c + 1 : c;
+        if constexpr (decltype(live)::value && BWD) {    // the state before the chunk, dk x dv
+          float *o = p.w0t + (ch0 + (int64_t)c * p.heads) * (DK * p.dv);
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            s_w[0].copy_t4(0, (w * NT + i) * 16, o + frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, p.dv / 32));
+        }
+        lds_barrier();
+        lds_barrier();
+        SplitTile<kFull, SL, DK> &W1 = s_w[BWD ? 0 : ~(c - c_first) & 1];
+        const Split<kFull> u0 = s_ul.ld(li, 8 * g), u1 = s_ul.ld(li, 32 + 8 * g);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          Sums<kFull> d;
+          d.add(ktf[i][0], u0);
+          d.add(ktf[i][1], u1);
+          st[i] = st[i] * ec + d.sum();
+          W1.st4(li, (w * NT + i) * 16 + 4 * g, st[i]);
+        }
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(nx, i, x);
+        ec = p.eg[(ch0 + (int64_t)nx * p.heads) * C + C - 1];
+      }
+    };
+    if (!BWD || PART != kFirst || seg == 0) chain(std::true_type{});
+    else chain(std::false_type{});
+    if (PART == kFirst && unit) {       // M^T: rows dk, k = the rows that this slice has; M for the gradient
+      const SplitTile<kFull, SL, DK> &W = s_w[BWD ? 0 : (c_end - c_first) & 1];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        Sums<kFull> d;
-        d.add(ktf[i][0], u0);
-        d.add(ktf[i][1], u1);
-        st[i] = st[i] * ec + d.sum();
-        W1.st4(li, (w * NT + i) * 16 + 4 * g, st[i]);
+        const int col = (w * NT + i) * 16;
+        W.copy_t4(0, col, m_of(seg), mplane, frag_at(col + li, sl * SL + 4 * g, NK));
+        if (BWD) W.copy4(li, col + 4 * g, m_of(seg) + kFull * mplane, mplane, frag_at(sl * SL + li, col + 4 * g, NK));
       }
-      lds_barrier();
+    } else if ((PART == kFirst && c_end < chunks) || (!BWD && c_end == chunks)) {
+      float *o = PART == kFirst && c_end < chunks ? u_of(seg) + w * (DK / 4) : p.w_out + wrow;
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(nx, i, x);
-      ec = p.eg[(ch0 + (int64_t)nx * p.heads) * C + C - 1];
-    }
-    if constexpr (!BWD) {
-      if (MODE == kFirst && unit) {     // M^T: rows dk, k = the rows that this slice has
-        const SplitTile<kFull, SL, DK> &W = s_w[(c_end - c_first) & 1];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          W.copy_t4(0, (w * NT + i) * 16, m_of(seg), mplane, frag_at((w * NT + i) * 16 + li, sl * SL + 4 * g, NK));
-      } else {
-        float *o = MODE == kFirst && c_end < chunks ? u_of(seg) + w * (DK / 4) : p.w_out + wrow;
-        if (MODE == kForward || c_end == chunks || MODE == kFirst)
-#pragma unroll
-          for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(o + 16 * i) = st[i];
-      }
+      for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(o + 16 * i) = st[i];
     }
   }
 }
@@ -678,21 +662,23 @@ hipError_t chunk_impl(const DeltaParams &p, bool backward, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T, int DK, bool BWD>
+hipError_t states_of(const DeltaParams &p, hipStream_t s) {
+  const int bh = p.nseq * p.heads, slices = p.dv / SL;
+  if (p.segs < 3) {
+    hipLaunchKernelGGL((delta_state_kernel<T, DK, BWD, kWhole>), dim3(bh * slices), dim3(512), 0, s, p);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((delta_state_kernel<T, DK, BWD, kFirst>), dim3(bh * (slices + (p.segs - 2) * (slices + DK / SL))),
+                     dim3(512), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((delta_state_kernel<T, DK, BWD, kSecond>), dim3(bh * (p.segs - 1) * slices), dim3(512), 0, s, p);
+  return hipGetLastError();
+}
 template <typename T, int DK>
 hipError_t states_impl(const DeltaParams &p, bool backward, hipStream_t s) {
-  const int bh = p.nseq * p.heads, slices = p.dv / SL;
-  if (backward) {
-    hipLaunchKernelGGL((delta_state_kernel<T, DK, kBackward>), dim3(bh * slices), dim3(512), 0, s, p);
-  } else if (p.segs < 3) {
-    hipLaunchKernelGGL((delta_state_kernel<T, DK, kForward>), dim3(bh * slices), dim3(512), 0, s, p);
-  } else {
-    hipLaunchKernelGGL((delta_state_kernel<T, DK, kFirst>), dim3(bh * (slices + (p.segs - 2) * (slices + DK / SL))), dim3(512),
-                       0, s, p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((delta_state_kernel<T, DK, kSecond>), dim3(bh * (p.segs - 1) * slices), dim3(512), 0, s, p);
-  }
-  return hipGetLastError();
+  return backward ? states_of<T, DK, true>(p, s) : states_of<T, DK, false>(p, s);
 }
 
 }  // namespace

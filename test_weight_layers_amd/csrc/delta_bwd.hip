@@ -27,19 +27,46 @@ constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 
 // The reverse of the states kernel, with the same split, layout, waves and order of loads:
 //   rows: K G^T, dU        rows: dR = T^T dU;  state: G <- e^gamma_last G + (scale eg o go)^T Q
 //   state: G += dP^T K;  rows: the next chunk's go
-template <typename T, int DK>
+// Segments of few long sequences (see there) run at once here too: G before a segment is G after it times
+// M^T plus what the segment alone has.  kFirst: the last segment, and the others but the first from G = 0;
+// kSecond: all but the last, over what the first launch wrote for their rows.
+template <typename T, int DK, int PART>
 __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delta_gstate_kernel(DeltaParams p) {
   constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>;
-  __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, DK> s_g;
+  __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, DK> s_gs[PART == kSecond ? 2 : 1];
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, C> s_goe[2], s_du, s_dr, s_dp;
   __shared__ __attribute__((aligned(16))) SplitTile<TP, SL, C> s_go;
   constexpr int64_t tokens = DK * C * 2 * TP, tplane = DK * C * 2;      // bytes of a chunk's tokens and a part
   const int slices = p.dv / SL, item = xcd_item(gridDim.x);
-  const int sl = item % slices, h = item / slices % p.heads, b = item / slices / p.heads;
+  SplitTile<kFull, SL, DK> &s_g = s_gs[0];
+  const int all = PART == kWhole ? slices : (p.segs - 1) * slices;
+  const int sl = item % slices, bh = item / all, h = bh % p.heads, b = bh / p.heads;
   const int wave = wave_id(), w = wave & 3, l = threadIdx.x & 63, g = l >> 4, li = l & 15;
   const int kh = h / (p.heads / p.key_heads);
   const DeltaSeq sq = seq_of(p, b);
   const int chunks = (sq.len + C - 1) / C;
+  int seg = item % all / slices, c_first = 0, c_end = chunks;
+  bool live = true;                     // its gradients are the sequence's
+  if constexpr (PART != kWhole) {
+    const int per = (chunks + p.segs - 1) / p.segs, last = chunks > 0 ? (chunks - 1) / per : 0;
+    if constexpr (PART == kFirst) {
+      if (last > 0) ++seg;              // (the only segment is the first launch's)
+      if (seg > last) return;
+      live = seg == last;
+    } else {
+      if (seg >= last) return;
+    }
+    c_first = seg * per, c_end = c_first + per < chunks ? c_first + per : chunks;
+    if constexpr (PART == kSecond)
+      join_segments<DK>(
+          s_gs, last - seg,
+          [&](int j) { return p.seg_u + (((int64_t)(b * (p.segs - 1) + last - j - 1) * p.heads + h) * p.dv + sl * SL + li) * DK + 4 * g; },
+          [&](int j) {
+            // (no M is read for the first step; its index then is one that exists)
+            return p.seg_m + ((int64_t)(b * (p.segs - 2) + (last - j > 0 ? last - j : 1) - 1) * p.heads + h) * (DK * DK * 4 * kFull) +
+                   DK * DK * 2 * kFull;
+          });
+  }
   const int64_t ch0 = (int64_t)sq.chunk0 * p.heads + h, ck0 = (int64_t)sq.chunk0 * p.key_heads + kh;
   const int64_t plane = C * C * 2;
   if (wave < 4) {
@@ -73,17 +100,17 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
       for (int i = 0; i < 2; ++i)       // (the first half is zero for the last two waves)
         f[i] = load_frag<kFull>(m + (ch0 + (int64_t)c * p.heads) * kSquare, plane, w * 2 + i);
     };
-    if (chunks > 0) {
+    if (c_first < c_end) {
 #pragma unroll
-      for (int i = 0; i < NK; ++i) kf[i] = load_token(chunks - 1, i);
-      load_values(chunks - 1);
-      load_square(p.am, chunks - 1, af);
-      load_square(p.tt, chunks - 1, tf);
-      store_go(chunks - 1, (chunks - 1) & 1);
+      for (int i = 0; i < NK; ++i) kf[i] = load_token(c_end - 1, i);
+      load_values(c_end - 1);
+      load_square(p.am, c_end - 1, af);
+      load_square(p.tt, c_end - 1, tf);
+      store_go(c_end - 1, (c_end - 1) & 1);
     }
     lds_barrier();
-    for (int c = chunks - 1; c >= 0; --c) {
-      const int nx = c > 0 ? c - 1 : 0, left = sq.len - c * C;
+    for (int c = c_end - 1; c >= c_first; --c) {
+      const int nx = c > c_first ? c - 1 : c, left = sq.len - c * C;
       Sums<kFull> kg;
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
@@ -125,22 +152,27 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
     };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      st[i] = p.gw_out ? *reinterpret_cast<const f32x4 *>(p.gw_out + wrow + 16 * i) : zero4();
-      s_g.st4(li, (w * NT + i) * 16 + 4 * g, st[i]);
+      const int col = (w * NT + i) * 16 + 4 * g;
+      if constexpr (PART == kSecond) {
+        st[i] = s_g.at4(li, col);
+      } else {
+        st[i] = live && p.gw_out ? *reinterpret_cast<const f32x4 *>(p.gw_out + wrow + 16 * i) : zero4();
+        s_g.st4(li, col, st[i]);
+      }
     }
-    if (chunks > 0) {
+    if (c_first < c_end) {
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          qtf[i][x] = load_transposed(p.qt, chunks - 1, i, x);
-          ktf[i][x] = load_transposed(p.kt, chunks - 1, i, x);
+          qtf[i][x] = load_transposed(p.qt, c_end - 1, i, x);
+          ktf[i][x] = load_transposed(p.kt, c_end - 1, i, x);
         }
-      ec = p.eg[(ch0 + (int64_t)(chunks - 1) * p.heads) * C + C - 1];
+      ec = p.eg[(ch0 + (int64_t)(c_end - 1) * p.heads) * C + C - 1];
     }
     lds_barrier();
-    for (int c = chunks - 1; c >= 0; --c) {
-      const int nx = c > 0 ? c - 1 : 0;
+    for (int c = c_end - 1; c >= c_first; --c) {
+      const int nx = c > c_first ? c - 1 : c;
       {                                 // the gradient after the chunk, dk x dv
         float *o = p.gwt + (ch0 + (int64_t)c * p.heads) * (DK * p.dv);
 #pragma unroll
@@ -177,8 +209,12 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
 #pragma unroll
         for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(p.kt, nx, i, x);
     }
+    float *o = p.gw + wrow;
+    if (PART == kFirst && seg > 0)
+      o = p.seg_u + (((int64_t)(b * (p.segs - 1) + seg - 1) * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
+    if (PART != kSecond || seg == 0)
 #pragma unroll
-    for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(p.gw + wrow + 16 * i) = st[i];
+      for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(o + 16 * i) = st[i];
   }
 }
 
@@ -448,7 +484,15 @@ __global__ __launch_bounds__(256) void delta_sum_rates_kernel(DeltaParams p) {
 
 template <typename T, int DK>
 hipError_t gstate_impl(const DeltaParams &p, hipStream_t s) {
-  hipLaunchKernelGGL((delta_gstate_kernel<T, DK>), dim3((unsigned)((int64_t)p.nseq * p.heads * (p.dv / SL))), dim3(512), 0, s, p);
+  const int wgs = p.nseq * p.heads * (p.dv / SL);
+  if (p.segs < 3) {
+    hipLaunchKernelGGL((delta_gstate_kernel<T, DK, kWhole>), dim3(wgs), dim3(512), 0, s, p);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((delta_gstate_kernel<T, DK, kFirst>), dim3(wgs * (p.segs - 1)), dim3(512), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((delta_gstate_kernel<T, DK, kSecond>), dim3(wgs * (p.segs - 1)), dim3(512), 0, s, p);
   return hipGetLastError();
 }
 template <typename T, int DK>

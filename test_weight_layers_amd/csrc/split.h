@@ -159,6 +159,12 @@ template <int P, int R, int Ccols> struct SplitTile {
     }
     return v;
   }
+  // four elements to element e of a split matrix in memory
+  __device__ __forceinline__ void copy4(int r, int c, char *dst, int64_t plane, int64_t e) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      *reinterpret_cast<bf16x4 *>(dst + i * plane + e * 2) = *reinterpret_cast<const bf16x4 *>(b + i * kPlane + (r * kPitch + c) * 2);
+  }
   // Lane (g, li)'s rows r0 + 4 g .. + 3 of column c0 + li: to element e of a split matrix in memory, or
   // (their sum, which is the fp32 value for three parts) to fp32 memory.
   __device__ __forceinline__ bf16x4 t4(int part, int r0, int c0) const {
@@ -218,14 +224,41 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
-__device__ __forceinline__ f32x4 zero4() { return f32x4{0, 0, 0, 0}; }
-
 // Workgroup barrier that waits for this wave's LDS traffic only: loads from memory stay in flight.
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));      // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0, 0, 0, 0}; }
+
+// The state that `count` segments before one leave it, into s[0]: what the first leaves, u_of(0), then
+// times M plus U of each other, (u_of(0) m_of(1) + u_of(1)) m_of(2) + ..  Eight waves, a 16 x 16 tile each at
+// a time; u_of: this lane's row, m_of: split dk x dk, rows = columns of the product.
+template <int DK, typename U, typename M>
+__device__ __forceinline__ void join_segments(SplitTile<kFull, kDeltaSlice, DK> (&s)[2], int count, const U &u_of, const M &m_of) {
+  constexpr int NK = DK / 32, NW = (DK / 16 + 7) / 8;
+  const int wave = wave_id(), l = threadIdx.x & 63, g = l >> 4, li = l & 15;
+  for (int j = 0; j < count; ++j) {
+    const SplitTile<kFull, kDeltaSlice, DK> &W = s[(count - j) & 1];
+    const char *m = m_of(j > 0 ? j : 1);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int tile = wave * NW + i;
+      if (tile >= DK / 16) break;
+      f32x4 x = *reinterpret_cast<const f32x4 *>(u_of(j) + 16 * tile);
+      if (j > 0) {
+        Sums<kFull> d;
+#pragma unroll 4
+        for (int k = 0; k < NK; ++k) d.add(load_frag<kFull>(m, (int64_t)DK * DK * 2, tile * NK + k), W.ld(li, 32 * k + 8 * g));
+        x += d.sum();
+      }
+      s[(count - 1 - j) & 1].st4(li, 16 * tile + 4 * g, x);
+    }
+    lds_barrier();
+  }
 }
 
 // e^x for a difference of cumulative log decays held in 64 bits.

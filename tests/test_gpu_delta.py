@@ -492,3 +492,22 @@ def test_long_sequence_keeps_nan_to_its_rows():
     assert torch.equal(w[0, 0][keep], ref[1][0, 0][keep]) and not torch.isfinite(w[0, 0, [5, 40]]).any()
     assert torch.equal(o[:, keep], ref[0][:, keep]) and torch.equal(o[:640, 5], ref[0][:640, 5])    # 640: its chunk
     assert not torch.isfinite(o[700:, 5]).any() and not torch.isfinite(o[:, 40]).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lens,H,Hk,dk,dv", [([1537], 2, 1, 64, 64), ([1300], 1, 1, 128, 192), ([1900], 1, 1, 256, 64),
+                                             ([2200, 0, 1, 70, 1500], 1, 1, 64, 64), ([0, 64, 1601], 1, 1, 64, 128)])
+def test_long_sequences_backward(lens, H, Hk, dk, dv, dtype):
+    from test_weight_layers_amd import ttt
+    d = inputs(lens, H, Hk, dk, dv, dtype, seed=24, tail=3, rate=0.02)
+    ref = reference(d, Hk, gradient=True)
+    g = dev(d)
+    args = [g[x] for x in ("w", "q", "k", "v", "beta", "decay", "go", "gw")]
+    got = ttt.delta_backward(*args, key_heads=Hk, cu_seqlens=g["cu"])
+    for name, x, r in zip(("q", "k", "v", "beta", "decay", "w"), got, ref):
+        assert rel(x, r) <= TOL[dtype][x.dtype], name
+        assert name == "w" or (x[-3:] if name in "qkv" else x[:, -3:]).abs().max() == 0
+    for s in range(len(lens)):
+        assert rel(got[5][s], ref[5][s]) <= TOL[dtype][torch.float32], s
+    again = ttt.delta_backward(*args, key_heads=Hk, cu_seqlens=g["cu"])
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
