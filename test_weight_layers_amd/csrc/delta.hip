@@ -341,7 +341,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
 //           dk / 16 more slices of rows
 //   kSecond: the others, each from its own starting state, (W_1 M_1 + U_1) M_2 + U_2 ..
 template <typename T, int DK, bool BWD, int PART>
-__global__ __launch_bounds__(512, 2) void delta_state_kernel(DeltaParams p) {
+__global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_state_kernel(DeltaParams p) {
   constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>, UP = BWD ? kFull : kOut<T>;
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, DK> s_w[2];
   __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, C> s_r, s_ul;

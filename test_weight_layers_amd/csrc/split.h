@@ -120,14 +120,24 @@ __device__ __forceinline__ int xcd_item(int n) {
   return n % 8 == 0 ? (blockIdx.x & 7) * (n >> 3) + (blockIdx.x >> 3) : blockIdx.x;
 }
 
-// A split matrix in LDS: P parts of R rows of Ccols elements, rows padded by 16 bytes (a
-// ds_read_b128 of 16 rows at one column then meets 16 distinct bank groups for every Ccols that is
-// a multiple of 64).
+// A split matrix in LDS: P parts of R rows of Ccols elements (a multiple of 64).  A ds_read_b128 is served 16
+// lanes at a time, which are not 16 lanes on end: eight rows of one 16-byte column and the other eight of the
+// column beside it (rows padded by 16 bytes then meet one bank twice: half of the LDS cycles were
+// conflicts).  The 16-byte units of a row therefore stand in an order of the row's, by xor: those of 128 bytes
+// in tiles of 64 columns, two rows to the 64 banks; those of 64 bytes in wider tiles, whose rows are padded
+// by 64 bytes, so that four rows turn round the banks and the column's multiple of 32 elements stays an
+// immediate offset (0 2 3 1 for the row's bits 2 and 3).
 template <int P, int R, int Ccols> struct SplitTile {
-  static constexpr int kPitch = Ccols + 8, kPlane = R * kPitch * 2;
+  static constexpr int kPitch = Ccols * 2 + (Ccols > 64 ? 64 : 0), kPlane = R * kPitch;
+  // byte offset of element (r, c) in a part
+  static __device__ __forceinline__ int at_byte(int r, int c) {
+    if (Ccols == 64) return r * kPitch + ((c * 2) ^ ((r >> 1 & 7) << 4));
+    const int x = (r >> 1 & 2) ^ (r & 8 ? 3 : 0);
+    return r * kPitch + (c >> 5) * 64 + (((c >> 3 & 3) ^ x) << 4) + (c & 7) * 2;
+  }
   char b[P * kPlane];
   template <int Q = P> __device__ __forceinline__ Split<Q> ld(int r, int c) const {     // its first Q parts
-    return load_split<Q>(b, kPlane, r * kPitch + c);
+    return load_split<Q>(b, kPlane, at_byte(r, c) / 2);
   }
   __device__ __forceinline__ void st4(int r, int c, f32x4 v) {
 #pragma unroll
@@ -138,14 +148,14 @@ template <int P, int R, int Ccols> struct SplitTile {
         h[x] = (__bf16)v[x];
         v[x] -= (float)h[x];
       }
-      *reinterpret_cast<bf16x4 *>(b + i * kPlane + (r * kPitch + c) * 2) = h;
+      *reinterpret_cast<bf16x4 *>(b + i * kPlane + at_byte(r, c)) = h;
     }
   }
   __device__ __forceinline__ void st1(int r, int c, float v) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const __bf16 h = (__bf16)v;
-      *reinterpret_cast<__bf16 *>(b + i * kPlane + (r * kPitch + c) * 2) = h;
+      *reinterpret_cast<__bf16 *>(b + i * kPlane + at_byte(r, c)) = h;
       v -= (float)h;
     }
   }
@@ -153,7 +163,7 @@ template <int P, int R, int Ccols> struct SplitTile {
     f32x4 v = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int i = P - 1; i >= 0; --i) {
-      const bf16x4 h = *reinterpret_cast<const bf16x4 *>(b + i * kPlane + (r * kPitch + c) * 2);
+      const bf16x4 h = *reinterpret_cast<const bf16x4 *>(b + i * kPlane + at_byte(r, c));
 #pragma unroll
       for (int x = 0; x < 4; ++x) v[x] += (float)h[x];
     }
@@ -163,13 +173,13 @@ template <int P, int R, int Ccols> struct SplitTile {
   __device__ __forceinline__ void copy4(int r, int c, char *dst, int64_t plane, int64_t e) const {
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      *reinterpret_cast<bf16x4 *>(dst + i * plane + e * 2) = *reinterpret_cast<const bf16x4 *>(b + i * kPlane + (r * kPitch + c) * 2);
+      *reinterpret_cast<bf16x4 *>(dst + i * plane + e * 2) = *reinterpret_cast<const bf16x4 *>(b + i * kPlane + at_byte(r, c));
   }
   // Lane (g, li)'s rows r0 + 4 g .. + 3 of column c0 + li: to element e of a split matrix in memory, or
   // (their sum, which is the fp32 value for three parts) to fp32 memory.
   __device__ __forceinline__ bf16x4 t4(int part, int r0, int c0) const {
     const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
-    const int o = ((r0 + 4 * g + (li >> 2)) * kPitch + c0 + 4 * (li & 3)) * 2;
+    const int o = at_byte(r0 + 4 * g + (li >> 2), c0 + 4 * (li & 3));
     return lds_read_tr16(reinterpret_cast<const unsigned char *>(b) + part * kPlane + o);
   }
   __device__ __forceinline__ void copy_t4(int r0, int c0, char *dst, int64_t plane, int64_t e) const {
