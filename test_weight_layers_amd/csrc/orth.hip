@@ -11,7 +11,7 @@
 // by up to 3.4445 each, 485 in five.  It does in the last two steps of bf16 matrices, where what
 // is lost (2^-12) is multiplied by 3.4 at most and the result has 8 bits; and bf16 matrices enter the
 // first step exactly in one part, times a power of two, with the rest of 1 / |G| applied to A and X.
-// Measured off the definition in 64 bits, 2 x 1300 x 1200 fp32: 2.1e-6 (fp32 arithmetic 3.2e-6, three bf16
+// Measured off the definition in 64 bits, 2 x 1300 x 1200 fp32: 1.2e-6 (fp32 arithmetic 3.2e-6, three bf16
 // parts and six products 3.0e-6 at 1.6 times the time); 4 x 4096 x 1024 bf16: 1.76e-3 (the rounding of the result
 // alone 1.66e-3).
 // The parts are written as planes by the kernel that computes a matrix, so that the main loop
@@ -236,6 +236,14 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
   for (int i = 0; i < G::FM; ++i)
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  // The products of low parts in sums of their own, where registers allow it: a large sum then is rounded
+  // once a stage, not three times (2 x 36 x 1216 fp32: 3.2e-6 -> 2.2e-6 off, 2 x 1300 x 1200 2.1e-6 -> 1.2e-6).
+  constexpr bool kLow = PA == 2 && PB == 2 && G::TM <= 128;
+  f32x4 low[kLow ? G::FM : 1][kLow ? G::FN : 1];
+#pragma unroll
+  for (auto &row : low)
+#pragma unroll
+    for (auto &v : row) v = f32x4{0, 0, 0, 0};
   const int wi = (w / G::WC) * G::WM, wj = (w % G::WC) * G::WN;
 #pragma unroll
   for (int k = 0; k < G::NST - 1; ++k)
@@ -254,7 +262,10 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
       for (int x = 0; x <= d; ++x)
         if (x < PA && d - x < PB)
 #pragma unroll
-          for (int i = 0; i < G::FM; ++i) acc[i][j] = mma(fb[d - x], fa[i][x], acc[i][j]);
+          for (int i = 0; i < G::FM; ++i) {
+            f32x4 &sum = kLow && d > 0 ? low[kLow ? i : 0][kLow ? j : 0] : acc[i][j];
+            sum = mma(fb[d - x], fa[i][x], sum);
+          }
   };
   for (int kc = 0; kc < nk; ++kc) {
     // this wave's copies of stage kc have arrived (those of the NST - 2 stages after it may be in flight)
@@ -283,6 +294,11 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
     }
   }
   __syncthreads();                                // the ring is free
+  if constexpr (kLow)
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < G::FN; ++j) acc[i][j] += low[i][j];
   // lane (g, li) holds C[16 i + li][16 j + 4 g + r], r = 0 .. 3, of the wave's tile
   const int r0 = bi * G::TM + wi, c0 = bj * G::TN + wj;
   if constexpr (KIND == kPoly) {
