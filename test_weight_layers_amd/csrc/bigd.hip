@@ -21,10 +21,12 @@
 // The intermediates cost 2 x 2 B per element of [n][m] (written once, read once),
 // under 15% of the MFMA time at these widths.
 #include "common.h"
+#include "dma.h"
 #include "kernels.h"
 
 namespace ttt {
 namespace {
+
 
 // Launch-order block -> work item: blocks go round-robin over the 8 XCDs, so
 // item (b % 8) * per + b / 8 puts consecutive items (which share operand rows)
