@@ -8,9 +8,9 @@
 //   R = beta o (V - e^gamma o (K W0^T)),  U = T R
 //   O = scale e^gamma o (Q W0^T) + A U
 //   W = e^gamma_last W0 + (e^(gamma_last - gamma) o U)^T K
-// Three kernels: the packed sequences are laid out in chunks (plan), T and A of every chunk at
-// once (chunk), then the states in order of the chunks, split over heads and 16-column slices of
-// dv, which do not depend on one another (states).
+// Two kernels: T and A of every chunk at once (chunk), then the states in order of the chunks, split
+// over heads and 16-column slices of dv, which do not depend on one another (states).  Every wave lays
+// the packed sequences out in chunks for itself; for more than 63 of them a first kernel does (plan).
 #include <type_traits>
 
 #include "delta.h"
@@ -94,6 +94,8 @@ constexpr int kZeroBlocks = 64;     // workgroups of the chunk kernel's launch t
 // One workgroup per chunk and head: e^gamma, T = (I + L)^-1 by block substitution in fp32 and A,
 // and (once per key head) the tokens and their transposes in fragment order.
 // Substitution, not products of powers of L: those grow without bound where keys repeat.
+// 687 chunks of 4 heads of 256, bf16: 108 us for 565 MB, 5.2 TB/s, what a copy reaches; 22 chunks 16.5 us,
+// the latency of the loads and the substitution.
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kernel(DeltaParams p) {
   constexpr int kPitch = DK + 16 / (int)sizeof(T), NK = DK / 32, kA = C + 4, TP = kTok<T>;
@@ -330,8 +332,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
 //   rows: P = K W0^T, R        rows: U = T R        state: W += (el o U)^T K;  rows: O = Q W0^T, A U
 // so two waves share a SIMD and one works while the other waits or loads.  Tokens and chunk terms
 // go from memory straight into operand registers (each is used once), the next chunk's as soon
-// as this chunk's have been used.  Bound by the order of the chunks, and within one by the 64
-// bytes a clock at which a CU takes its operands.
+// as this chunk's have been used, Q into the registers that K leaves, A into those of T.  Bound by the
+// order of the chunks: 2.45 us each, heads of 256, of which the matrix cores work 0.5 and the operands,
+// 138 KB, take 0.9 at the 64 bytes a clock of a CU; the rest is the three exchanges, one after another.
 // BWD writes the states and U that the gradient needs, in place of the outputs.
 //
 // Where sequences are long and few, the chunks of one are cut in segments that run at once (the state is
@@ -340,6 +343,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
 //   kFirst: the first segment, outputs and all; U and M of the others but the last, of which M is
 //           dk / 16 more slices of rows
 //   kSecond: the others, each from its own starting state, (W_1 M_1 + U_1) M_2 + U_2 ..
+// 687 chunks of 4 heads of 256: 1680 us whole, 534 + 398 in five segments (448 and 256 workgroups; a CU's
+// two then take 3.9 us a chunk).
 template <typename T, int DK, bool BWD, int PART>
 __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_state_kernel(DeltaParams p) {
   constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>, UP = BWD ? kFull : kOut<T>;
@@ -556,7 +561,9 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_state_kerne
 // The recurrent form for one token of each row's sequence: one read and one write of the state.
 //   o = scale (a W q + beta e (k.q)),  W <- a W + beta e k^T,  e = v - a W k
 // 16 lanes hold one dv row of W; rows that name the same state are applied in row order by the
-// workgroups of the first of them.
+// workgroups of the first of them.  Bound by memory: 300 rows of 8 heads of 128 x 128 move 316 MB in
+// 70 us (4.5 TB/s; 49 while the 157 MB of states stay in the 256 MB cache), one row of 4 heads of
+// 256 x 256 takes the 6.3 us of a launch and two memory latencies.
 template <typename T, int DK>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
   constexpr int V4 = DK / 64;           // float4 a lane and dv row

@@ -27,6 +27,8 @@ constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 
 // The reverse of the states kernel, with the same split, layout, waves and order of loads:
 //   rows: K G^T, dU        rows: dR = T^T dU;  state: G <- e^gamma_last G + (scale eg o go)^T Q
 //   state: G += dP^T K;  rows: the next chunk's go
+// 16 chunks a sequence, 6 heads of 128 and 8 sequences (384 workgroups): 80 us, 5 a chunk with two
+// workgroups to a CU; 7 to 8 chunks of 4 heads of 64, fp32: 51 us.
 // Segments of few long sequences (see there) run at once here too: G before a segment is G after it times
 // M^T plus what the segment alone has.  kFirst: the last segment, and the others but the first from G = 0;
 // kSecond: all but the last, over what the first launch wrote for their rows.
@@ -223,8 +225,9 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
 // row tile w % 4 and half of the column tiles), which pass through LDS as operands both ways round,
 // then dq and dk: wave w has the rows of half w / 4 and every fourth 16-wide column tile.  Operands
 // come from memory in fragment order; bound by their latency, so registers are kept few enough for
-// four waves a SIMD (one wave of 4 x 2 tiles a SIMD took 175 us where this takes %US% for 128 chunks
-// of 6 heads of 128).
+// four waves a SIMD (one wave of 4 x 2 tiles a SIMD took 175 us where this takes 124 for 128 chunks
+// of 6 heads of 128; of its 278 MB, 55 us at a copy's rate, the products take 15 us and the vector
+// operations 30).
 template <typename T, int DK>
 __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kernel(DeltaParams p) {
   constexpr int NT = DK / 64, TP = kTok<T>;

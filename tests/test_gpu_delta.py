@@ -3,12 +3,13 @@ token in 64 bits, and the gradient against automatic differentiation of that rec
 differences of the call itself.
 
 Tolerances (relative 2-norm over a tensor).  A bf16 output is rounded once: at most eps/2 = 2^-8 of each
-element.  Its inputs are exact, and what is computed before carries 17 bits in every operand: a product
+element.  Its inputs are exact, and operands of at least 17 bits (two bf16 parts) stand before it: a product
 of two such operands is off by at most 3 * 2^-17 of the sum of its terms' sizes, and an output is reached
 through at most five of them in a row (K W0^T, T, the states' update, A U and Q W0^T): 15 * 2^-17 = 1.2e-4
 worst, were all errors alike.  They are independent over the 64 to 256 terms of a product, so the 2-norm
-stays below a tenth of it, and fp32 results (states, rate gradients) are held to 2e-5.  fp32 tokens run on
-fp32 products: five of up to 256 terms, 5 * 256 * 2^-24 = 7.6e-5 worst, by the same argument held to 5e-6.
+stays below a tenth of it, and fp32 results (states, rate gradients) are held to 2e-5 (their operands carry
+24 bits, three parts: they come to 3e-7).  fp32 tokens run on 24 bits throughout, as fp32 products have:
+five of up to 256 terms, 5 * 256 * 2^-24 = 7.6e-5 worst, by the same argument held to 5e-6.
 """
 import math
 

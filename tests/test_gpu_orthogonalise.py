@@ -1,12 +1,13 @@
 """Newton-Schulz orthogonalisation (ttt.orthogonalise) against the same steps in 64 bits.
 
-Tolerances (relative 2-norm).  Operands carry 24 bits (fp32 matrices) or 17 (bf16 ones).  The five steps
+Tolerances (relative 2-norm).  Operands carry 22 bits (two fp16 parts; one part, 11 bits, in the last two
+steps of bf16 matrices, whose errors grow by 3.4 at most).  The five steps
 multiply what is lost along small singular directions by at most 3.4445^5 = 485, while the result's norm
 is at least 0.68 sqrt(r) against X's norm 1 before: an error of p in every operand, three products a step,
 leaves at most 485 * 3 p / (0.68 sqrt(r)) of it.  With sums of up to c terms (random signs, a root of c
-roundings of 2^-24): fp32, r = 16, c = 700: 485 * 3 * 2^-24 / 2.7 = 3.2e-5, worst over directions that
-all matrices here fill only in part: held to 1e-5.  bf16: 2^-17 in place of 2^-24 in one part of the
-norm's directions, and the result is rounded by at most 2^-8: held to 2^-8 + 2^-10.
+roundings of 2^-24): fp32, r = 16, c = 700: 485 * 3 * 2^-23 / 2.7 = 6.4e-5, worst over directions that
+all matrices here fill only in part: held to 1e-5.  bf16: 3.4 * 2^-12 from the last steps, and the result is
+rounded by at most 2^-8: held to 2^-8 + 2^-10.
 """
 import pytest
 import torch
