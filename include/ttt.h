@@ -316,11 +316,12 @@ int ttt_stream_ex(int32_t heads, int32_t d, int32_t m,
  *   as fp32 arithmetic gives; bf16 outputs are rounded once.  Tokens are taken 64 at a time: a NaN
  *   or an infinity in a token or rate may also reach the rows before it in its chunk of 64 (of
  *   that sequence; of its own column of v only, where it stands in v).
- * Deterministic: the same inputs give the same bits.  n <= 2^31 - 65; chunks x H and
- *   sequences x H x dv/16 below 2^24; in the chunked calls 64 rows span < 2 GiB.
+ * Deterministic: the same inputs give the same bits.  n <= 2^31 - 65; chunks x H, sequences x H x
+ *   dv/16 and (one token) rows x H x dv/64 below 2^23; in the chunked calls 64 rows span < 2 GiB.
  */
 enum { TTT_DELTA_ZERO_UNUSED = 1 };
-/* Bytes of workspace of ttt_delta (backward = 0) or ttt_delta_backward (backward = 1). */
+/* Bytes of workspace of ttt_delta (backward = 0) or ttt_delta_backward (backward = 1).  They do not
+ * fall as n grows; fewer sequences of the same rows may need more (long ones are cut in segments). */
 int ttt_delta_workspace_bytes(int32_t heads, int32_t key_heads, int32_t dk, int32_t dv, int64_t n,
                               int32_t sequences, int32_t dtype, int32_t backward, size_t *bytes);
 /* The rule over every sequence, in chunks of 64 tokens.  w_out: final states, equal to w

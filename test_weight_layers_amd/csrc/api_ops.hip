@@ -14,8 +14,8 @@ using namespace ttt;
 
 namespace {
 
-// A launch has at most 2^32 - 1 work-items in a direction: below 2^24 workgroups of 256.
-constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
+// A launch has at most 2^32 - 1 work-items in a direction: below 2^23 workgroups of 512.
+constexpr int64_t kMaxGroups = (int64_t(1) << 23) - 1;
 constexpr int64_t kMaxRows = 2147483647LL - 64;
 
 // Rows [n][ld] of `width` elements of `es` bytes.
@@ -95,7 +95,8 @@ struct DeltaPlan {
 // run at once on 256 CUs of one or two each, and what a further segment (its start) and the second launch
 // cost.  Measured with and without: 687 chunks x 4 heads of 256 1680 and 940 us (5 segments), 313 x 2
 // heads of 128 477 and 110 (16), its gradient over 94 373 and 169; not taken for 9 sequences of 35 chunks
-// x 2 heads of 128 (66, with 3 74).
+// x 2 heads of 128 (66, with 3 74).  (Without rounding per / s up the number never falls as rows are
+// added, so that a workspace for more rows of as many sequences serves fewer.)
 int delta_segments(int H, int dk, int dv, int64_t nc, int64_t nseq, bool bf16, bool backward) {
   const int slices = dv / kDeltaSlice, size = dk == 64 ? 0 : dk == 128 ? 1 : 2;
   const int64_t wgs = nseq * H * slices, per = (nc + nseq - 1) / nseq;
@@ -111,7 +112,7 @@ int delta_segments(int H, int dk, int dv, int64_t nc, int64_t nseq, bool bf16, b
     const double state = rounds(nseq * H * (slices + (int64_t)(s - 2) * (slices + dk / kDeltaSlice))) + rounds(wgs * (s - 1));
     const double grad = backward ? 1.5 * 2.0 * rounds(wgs * (s - 1)) : 0.0;
     const double more = (kBothUs[size] + s * kJoinUs[size]) * (backward ? 2.5 : 1.0);
-    const double t = (double)((per + s - 1) / s) * (state + grad) + more / kChunkUs[bf16 ? 0 : 1][size];
+    const double t = (double)per / s * (state + grad) + more / kChunkUs[bf16 ? 0 : 1][size];
     if (t < least) least = t, best = s;
   }
   return best;

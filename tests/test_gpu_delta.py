@@ -512,3 +512,52 @@ def test_long_sequences_backward(lens, H, Hk, dk, dv, dtype):
         assert rel(got[5][s], ref[5][s]) <= TOL[dtype][torch.float32], s
     again = ttt.delta_backward(*args, key_heads=Hk, cu_seqlens=g["cu"])
     assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_long_sequences_captured_and_replayed():
+    """Segments are laid out on the device: other lengths at a replay are other segments."""
+    from test_weight_layers_amd import ttt
+    d = dev(inputs([1500, 700], 1, 1, 64, 64, torch.bfloat16, seed=25, rate=0.02))
+    args = [d[x] for x in ("w", "q", "k", "v", "beta", "decay")]
+    run = lambda: (*ttt.delta(*args, cu_seqlens=d["cu"]),
+                   *ttt.delta_backward(*args, d["go"], d["gw"], cu_seqlens=d["cu"]))
+    for _ in range(2):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run()
+    for i, cut in enumerate([1500, 0, 2200, 64, 1301, 1500]):
+        d["cu"][1] = cut
+        d["v"].mul_(1.0 if i % 2 else -0.5)
+        want = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), cut
+
+
+def test_long_sequences_with_offsets_out_of_order():
+    """Any offsets name disjoint rows, in segments too: clamped to the rows and to a running maximum."""
+    from test_weight_layers_amd import ttt
+    d = dev(inputs([1400, 600, 100], 1, 1, 64, 64, torch.bfloat16, seed=26, rate=0.02))
+    args = [d[x] for x in ("w", "q", "k", "v", "beta", "decay")]
+    for cu, same in (([0, 1800, 900, 1 << 30], [0, 1800, 1800, 2100]), ([-5, 1400, -7, 2000], [0, 1400, 1400, 2000]),
+                     ([500, 300, 2100, 2100], [500, 500, 2100, 2100])):
+        a, b = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (cu, same))
+        got = (*ttt.delta(*args, cu_seqlens=a), *ttt.delta_backward(*args, d["go"], d["gw"], cu_seqlens=a))
+        want = (*ttt.delta(*args, cu_seqlens=b), *ttt.delta_backward(*args, d["go"], d["gw"], cu_seqlens=b))
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), cu
+
+
+def test_many_sequences_backward():
+    """More sequences than a wave lays out for itself, empty ones among them."""
+    from test_weight_layers_amd import ttt
+    lens = [3, 0, 70, 1] * 17 + [64]
+    d = inputs(lens, 2, 1, 64, 64, torch.float32, seed=27, tail=2)
+    ref = reference(d, 1, gradient=True)
+    g = dev(d)
+    got = ttt.delta_backward(*[g[x] for x in ("w", "q", "k", "v", "beta", "decay", "go", "gw")], key_heads=1,
+                             cu_seqlens=g["cu"])
+    for x, r in zip(got, ref):
+        assert rel(x, r) <= TOL[torch.float32][torch.float32]

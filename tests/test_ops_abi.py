@@ -36,6 +36,23 @@ def test_delta_workspace(lib):
     assert ws(lib, "ttt_delta_workspace_bytes", 4, 4, 64, 64, 0, 1, F32, 1)[0] == 0
 
 
+@pytest.mark.parametrize("backward", [0, 1])
+@pytest.mark.parametrize("H,dk,dv,nseq", [(1, 64, 64, 1), (4, 256, 256, 1), (2, 128, 192, 3), (1, 256, 64, 2), (8, 128, 128, 1)])
+def test_delta_workspace_grows_with_rows(lib, H, dk, dv, nseq, backward):
+    """A workspace for more rows serves fewer."""
+    last = 0
+    for n in list(range(nseq, 9000, 61)) + [20000, 44000, 100000, 1000000]:
+        st, b = ws(lib, "ttt_delta_workspace_bytes", H, H, dk, dv, n, nseq, BF16, backward)
+        assert st == 0 and b >= last, n
+        last = b
+
+
+def test_delta_launches_fit(lib):
+    """Workgroups of 512: 2^23 of them and more are refused, one fewer is not."""
+    assert ws(lib, "ttt_delta_workspace_bytes", 1, 1, 64, 1024, 10, 1 << 17, BF16, 0)[0] == -2
+    assert ws(lib, "ttt_delta_workspace_bytes", 1, 1, 64, 1024, 10, (1 << 17) - 1, BF16, 0)[0] == 0
+
+
 @pytest.mark.parametrize("args,code", [
     ((4, 3, 64, 64, 10, 1, BF16, 0), -1),         # heads not a multiple of key heads
     ((0, 1, 64, 64, 10, 1, BF16, 0), -1),
