@@ -148,6 +148,8 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
     const int64_t wrow = (((int64_t)b * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
     f32x4 st[NT];
     Split<TP> ktf[NT][2], qtf[NT][2];
+    // fp32 tokens of 256: K^T follows Q^T through the same registers (held side by side they spill)
+    constexpr bool kShare = TP == 3 && DK == 256;
     float ec = 0.0f;
     const auto load_transposed = [&](const char *m, int c, int i, int x) {
       return load_frag<TP>(m + (ck0 + (int64_t)c * p.key_heads) * tokens, tplane, (w * NT + i) * 2 + x);
@@ -168,7 +170,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           qtf[i][x] = load_transposed(p.qt, c_end - 1, i, x);
-          ktf[i][x] = load_transposed(p.kt, c_end - 1, i, x);
+          if (!kShare) ktf[i][x] = load_transposed(p.kt, c_end - 1, i, x);
         }
       ec = p.eg[(ch0 + (int64_t)(c_end - 1) * p.heads) * C + C - 1];
     }
@@ -190,7 +192,10 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
           d.add(qtf[i][1], g1);
           st[i] = st[i] * ec + d.sum();
 #pragma unroll
-          for (int x = 0; x < 2; ++x) qtf[i][x] = load_transposed(p.qt, nx, i, x);
+          for (int x = 0; x < 2; ++x) {
+            if constexpr (kShare) ktf[i][x] = load_transposed(p.kt, c, i, x);
+            else qtf[i][x] = load_transposed(p.qt, nx, i, x);
+          }
         }
         ec = p.eg[(ch0 + (int64_t)nx * p.heads) * C + C - 1];
       }
@@ -209,7 +214,10 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) ktf[i][x] = load_transposed(p.kt, nx, i, x);
+        for (int x = 0; x < 2; ++x) {
+          if constexpr (kShare) qtf[i][x] = load_transposed(p.qt, nx, i, x);
+          else ktf[i][x] = load_transposed(p.kt, nx, i, x);
+        }
     }
     float *o = p.gw + wrow;
     if (PART == kFirst && seg > 0)
