@@ -86,7 +86,7 @@ int check_delta_shape(int H, int Hk, int dk, int dv, int dtype) {
 struct DeltaPlan {
   int nchunk;
   size_t off_seqs, off_chunks, off_used, off_eg, off_el, off_be, off_gam, off_tm, off_am, off_tt, off_kp, off_qp, off_kt, off_qt;
-  size_t off_gop, off_w0t, off_gwt, off_u, off_dr, off_gqp, off_gkp, off_gb, off_gd, off_su, off_sm, total;
+  size_t off_gop, off_w0t, off_gwt, off_u, off_dr, off_gqp, off_gkp, off_gb, off_gd, off_su, off_sg, off_sm, total;
   int segs;
 };
 
@@ -123,7 +123,7 @@ int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype
   if (n > kMaxRows) return fail(TTT_EUNSUPPORTED, "n=%lld exceeds %lld rows", (long long)n, (long long)kMaxRows);
   // a sequence of len rows has at most len / 64 + 1 chunks, an empty one none
   const int64_t nc = n / kDeltaChunk + (nseq < n ? nseq : n);
-  if (nc * H > kMaxGroups || nseq * H * (dv / kDeltaSlice) > kMaxGroups)
+  if (nc * H > kMaxGroups || nseq * H * (dv / kDeltaSlice) * (backward ? 2 : 1) > kMaxGroups)
     return fail(TTT_EUNSUPPORTED, "too many chunks or sequences for %d heads in one call", H);
   DeltaPlan P{};
   P.nchunk = (int)nc;
@@ -150,6 +150,7 @@ int plan_delta(int H, int Hk, int dk, int dv, int64_t n, int64_t nseq, int dtype
   P.segs = delta_segments(H, dk, dv, nc, nseq, dtype == TTT_BF16, backward);
   if (P.segs > 2) {
     P.off_su = take((size_t)nseq * (P.segs - 1) * H * dv * dk * 4);
+    if (backward) P.off_sg = take((size_t)nseq * (P.segs - 1) * H * dv * dk * 4);
     P.off_sm = take((size_t)nseq * (P.segs - 2) * H * dk * dk * sb * (backward ? 2 : 1));
   }
   if (backward) {
@@ -203,7 +204,7 @@ int delta_params(int H, int Hk, int dk, int dv, const float *w, const Rows &q, c
   p->be = reinterpret_cast<float *>(b + P.off_be);
   p->kp = b + P.off_kp, p->qp = b + P.off_qp;
   p->segs = P.segs;
-  p->seg_u = reinterpret_cast<float *>(b + P.off_su), p->seg_m = b + P.off_sm;
+  p->seg_u = reinterpret_cast<float *>(b + P.off_su), p->seg_g = reinterpret_cast<float *>(b + P.off_sg), p->seg_m = b + P.off_sm;
   if (backward) {
     p->gam = reinterpret_cast<double *>(b + P.off_gam);
     p->gop = b + P.off_gop;

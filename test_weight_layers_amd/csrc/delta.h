@@ -53,7 +53,7 @@ struct DeltaParams {
   char *kp, *qp;                    // [nchunk][Hk] split tokens 64 x dk, 0 past the chunk
   char *kt, *qt;                    // [nchunk][Hk] the same transposed, dk x 64 (qt: backward)
   int segs;                         // segments of a sequence that run at once; < 3: none
-  float *seg_u;                     // [nseq][segs - 1][H][dv][dk] what segments leave (see delta.hip)
+  float *seg_u, *seg_g;             // [nseq][segs - 1][H][dv][dk] what segments leave (see delta_state.h), and their gradients
   char *seg_m;                      // [nseq][segs - 2][H] split dk x dk: M^T, and M (backward)
   // backward
   const void *go;                   // gradient of o
@@ -101,6 +101,5 @@ hipError_t launch_delta_step(const DeltaStepParams &p, bool bf16, hipStream_t s)
 // Forward pieces that the backward pass runs again.
 hipError_t launch_delta_plan(const DeltaParams &p, hipStream_t s);
 hipError_t launch_delta_chunk(const DeltaParams &p, bool bf16, bool backward, hipStream_t s);
-hipError_t launch_delta_states(const DeltaParams &p, bool bf16, bool backward, hipStream_t s);
 
 }  // namespace ttt

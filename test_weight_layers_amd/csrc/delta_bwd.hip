@@ -12,16 +12,10 @@
 //              + rowsum_i(M) - colsum_i(M),  M = X o Q K^T + Y o K K^T,
 //   dgamma_last += e^gamma_last <W0, G> + sum_j k_j.(second of dk)_j,   dg_i = sum_{j >= i} dgamma_j
 // (k_i.(dR W0)_i is dR_i.P_i, so P itself is not needed).
-#include "delta.h"
-#include "delta_layout.h"
-#include "split.h"
+#include "delta_state.h"
 
 namespace ttt {
 namespace {
-
-constexpr int C = kDeltaChunk;
-constexpr int SL = kDeltaSlice;
-constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 matrix
 
 // ------------------------------------------------------------------ state gradients
 // The reverse of the states kernel, with the same split, layout, waves and order of loads:
@@ -32,14 +26,20 @@ constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 
 // Segments of few long sequences (see there) run at once here too: G before a segment is G after it times
 // M^T plus what the segment alone has.  kFirst: the last segment, and the others but the first from G = 0;
 // kSecond: all but the last, over what the first launch wrote for their rows.
+template <typename T, int DK, int PART> struct GradLds {
+  SplitTile<kFull, SL, DK> g[PART == kSecond ? 2 : 1];
+  SplitTile<kFull, SL, C> goe[2], du, dr, dp;
+  SplitTile<kTok<T>, SL, C> go;
+};
 template <typename T, int DK, int PART>
-__global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delta_gstate_kernel(DeltaParams p) {
+__device__ __forceinline__ void delta_gstates(const DeltaParams &p, GradLds<T, DK, PART> &lds, int id, int count) {
   constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>;
-  __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, DK> s_gs[PART == kSecond ? 2 : 1];
-  __shared__ __attribute__((aligned(16))) SplitTile<kFull, SL, C> s_goe[2], s_du, s_dr, s_dp;
-  __shared__ __attribute__((aligned(16))) SplitTile<TP, SL, C> s_go;
+  auto &s_gs = lds.g;
+  auto &s_goe = lds.goe;
+  auto &s_du = lds.du, &s_dr = lds.dr, &s_dp = lds.dp;
+  auto &s_go = lds.go;
   constexpr int64_t tokens = DK * C * 2 * TP, tplane = DK * C * 2;      // bytes of a chunk's tokens and a part
-  const int slices = p.dv / SL, item = xcd_item(gridDim.x);
+  const int slices = p.dv / SL, item = xcd_item(id, count);
   SplitTile<kFull, SL, DK> &s_g = s_gs[0];
   const int all = PART == kWhole ? slices : (p.segs - 1) * slices;
   const int sl = item % slices, bh = item / all, h = bh % p.heads, b = bh / p.heads;
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
     if constexpr (PART == kSecond)
       join_segments<DK>(
           s_gs, last - seg,
-          [&](int j) { return p.seg_u + (((int64_t)(b * (p.segs - 1) + last - j - 1) * p.heads + h) * p.dv + sl * SL + li) * DK + 4 * g; },
+          [&](int j) { return p.seg_g + (((int64_t)(b * (p.segs - 1) + last - j - 1) * p.heads + h) * p.dv + sl * SL + li) * DK + 4 * g; },
           [&](int j) {
             // (no M is read for the first step; its index then is one that exists)
             return p.seg_m + ((int64_t)(b * (p.segs - 2) + (last - j > 0 ? last - j : 1) - 1) * p.heads + h) * (DK * DK * 4 * kFull) +
@@ -221,11 +221,25 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
     }
     float *o = p.gw + wrow;
     if (PART == kFirst && seg > 0)
-      o = p.seg_u + (((int64_t)(b * (p.segs - 1) + seg - 1) * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
+      o = p.seg_g + (((int64_t)(b * (p.segs - 1) + seg - 1) * p.heads + h) * p.dv + sl * SL + li) * DK + w * (DK / 4) + 4 * g;
     if (PART != kSecond || seg == 0)
 #pragma unroll
       for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(o + 16 * i) = st[i];
   }
+}
+
+// The states and their gradients do not depend on one another (but for M, which the first launch leaves to the
+// second): one launch for both, the gradients' workgroups, which take longer, first.
+template <typename T, int DK, int PART>
+__global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delta_chain_kernel(DeltaParams p, int grads) {
+  union Lds {
+    StateLds<T, DK, true> states;
+    GradLds<T, DK, PART> grads;
+  };
+  __shared__ __attribute__((aligned(16))) Lds lds;
+  const int id = blockIdx.x;
+  if (id < grads) delta_gstates<T, DK, PART>(p, lds.grads, id, grads);
+  else delta_states<T, DK, true, PART>(p, lds.states, id - grads, gridDim.x - grads);
 }
 
 // ------------------------------------------------------------------ token gradients
@@ -242,7 +256,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
   __shared__ __attribute__((aligned(16))) SplitTile<kOut<T>, C, C> s_x, s_xt, s_y, s_yt;
   __shared__ __attribute__((aligned(16))) float s_row[3][4][C];      // partials of q.(go W0), k.(dR W0), k.(U G)
   __shared__ float s_rs[2][C], s_db[2][C], s_cs[4][C], s_red[4];
-  const int item = xcd_item(gridDim.x), h = item % p.heads, c = item / p.heads;
+  const int item = xcd_item(blockIdx.x, gridDim.x), h = item % p.heads, c = item / p.heads;
   const DeltaChunk ck = chunk_of(p, c);
   if (ck.len == 0) return;
   const int t = threadIdx.x, wave = wave_id(), w4 = wave & 3, half = wave >> 2, l = t & 63, g = l >> 4, li = l & 15;
@@ -494,16 +508,18 @@ __global__ __launch_bounds__(256) void delta_sum_rates_kernel(DeltaParams p) {
 }
 
 template <typename T, int DK>
-hipError_t gstate_impl(const DeltaParams &p, hipStream_t s) {
+hipError_t chain_impl(const DeltaParams &p, hipStream_t s) {
   const int wgs = p.nseq * p.heads * (p.dv / SL);
-  if (p.segs < 3) {
-    hipLaunchKernelGGL((delta_gstate_kernel<T, DK, kWhole>), dim3(wgs), dim3(512), 0, s, p);
+  if (p.segs < 3) {     // (without chunks only the gradients, which pass through)
+    hipLaunchKernelGGL((delta_chain_kernel<T, DK, kWhole>), dim3(wgs + (p.nchunk > 0 ? state_wgs(p, kWhole) : 0)), dim3(512), 0, s,
+                       p, wgs);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((delta_gstate_kernel<T, DK, kFirst>), dim3(wgs * (p.segs - 1)), dim3(512), 0, s, p);
+  const int grads = wgs * (p.segs - 1);
+  hipLaunchKernelGGL((delta_chain_kernel<T, DK, kFirst>), dim3(grads + state_wgs(p, kFirst)), dim3(512), 0, s, p, grads);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((delta_gstate_kernel<T, DK, kSecond>), dim3(wgs * (p.segs - 1)), dim3(512), 0, s, p);
+  hipLaunchKernelGGL((delta_chain_kernel<T, DK, kSecond>), dim3(grads + state_wgs(p, kSecond)), dim3(512), 0, s, p, grads);
   return hipGetLastError();
 }
 template <typename T, int DK>
@@ -522,8 +538,7 @@ hipError_t group_impl(const DeltaParams &p, hipStream_t s) {
 hipError_t launch_delta_backward(const DeltaParams &p, bool bf16, hipStream_t s) {
   hipError_t e = launch_delta_plan(p, s);
   if (e == hipSuccess) e = launch_delta_chunk(p, bf16, true, s);
-  if (e == hipSuccess && p.nchunk > 0) e = launch_delta_states(p, bf16, true, s);
-  if (e == hipSuccess) e = TTT_DELTA_BY_DK(gstate_impl, p, p, s);
+  if (e == hipSuccess) e = TTT_DELTA_BY_DK(chain_impl, p, p, s);
   if (e == hipSuccess && p.nchunk > 0) e = TTT_DELTA_BY_DK(gtoken_impl, p, p, s);
   if (e == hipSuccess && p.nchunk > 0 && p.gqp) e = bf16 ? group_impl<__bf16>(p, s) : group_impl<float>(p, s);
   if (p.n == 0) return e;

@@ -116,9 +116,7 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 
 // Launch-order block id -> work item, so that consecutive items (which read the same tokens and
 // chunk terms) run on one XCD: workgroups go round the 8 XCDs.
-__device__ __forceinline__ int xcd_item(int n) {
-  return n % 8 == 0 ? (blockIdx.x & 7) * (n >> 3) + (blockIdx.x >> 3) : blockIdx.x;
-}
+__device__ __forceinline__ int xcd_item(int id, int n) { return n % 8 == 0 ? (id & 7) * (n >> 3) + (id >> 3) : id; }
 
 // A split matrix in LDS: P parts of R rows of Ccols elements (a multiple of 64).  A ds_read_b128 is served 16
 // lanes at a time, which are not 16 lanes on end: eight rows of one 16-byte column and the other eight of the
