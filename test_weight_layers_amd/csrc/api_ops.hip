@@ -91,11 +91,11 @@ struct DeltaPlan {
 };
 
 // Segments that the chunks of a sequence are cut in (1: none), from what the states of a chunk take where
-// the order of the chunks bounds them (us), half as much again for their gradients, how many workgroups
-// run at once on 256 CUs of one or two each, and what a further segment (its start) and the second launch
-// cost.  Measured with and without: 687 chunks x 4 heads of 256 1680 and 940 us (5 segments), 313 x 2
-// heads of 128 477 and 110 (16), its gradient over 94 373 and 169; not taken for 9 sequences of 35 chunks
-// x 2 heads of 128 (66, with 3 74).  (Without rounding per / s up the number never falls as rows are
+// the order of the chunks bounds them (us), half as much again for their gradients (whose workgroups run
+// beside the states'), how many workgroups run at once on 256 CUs of one or two each, and what a further
+// segment (its start) and the second launch cost.  Measured with and without: 687 chunks x 4 heads of 256
+// 1680 and 910 us (5 segments), 313 x 2 heads of 128 477 and 110 (16), the gradient call over 94 232 and
+// 118 (12); not taken for 9 sequences of 35 chunks x 2 heads of 128 (66, with 3 74).  (Without rounding per / s up the number never falls as rows are
 // added, so that a workspace for more rows of as many sequences serves fewer.)
 int delta_segments(int H, int dk, int dv, int64_t nc, int64_t nseq, bool bf16, bool backward) {
   const int slices = dv / kDeltaSlice, size = dk == 64 ? 0 : dk == 128 ? 1 : 2;
@@ -107,12 +107,12 @@ int delta_segments(int H, int dk, int dv, int64_t nc, int64_t nseq, bool bf16, b
     return (double)(x / 512) * 1.6 + (r == 0 ? 0.0 : r <= 256 ? 1.0 : 1.5);
   };
   int best = 1;
-  double least = (double)per * rounds(wgs) * (backward ? 2.5 : 1.0);
+  const double chunk = kChunkUs[bf16 ? 0 : 1][size] * (backward ? 1.5 : 1.0);
+  double least = chunk * (double)per * rounds(backward ? 2 * wgs : wgs);
   for (int s = 3; s <= 64 && s <= per; ++s) {
-    const double state = rounds(nseq * H * (slices + (int64_t)(s - 2) * (slices + dk / kDeltaSlice))) + rounds(wgs * (s - 1));
-    const double grad = backward ? 1.5 * 2.0 * rounds(wgs * (s - 1)) : 0.0;
-    const double more = (kBothUs[size] + s * kJoinUs[size]) * (backward ? 2.5 : 1.0);
-    const double t = (double)per / s * (state + grad) + more / kChunkUs[bf16 ? 0 : 1][size];
+    const int64_t g = backward ? wgs * (s - 1) : 0;
+    const double both = rounds(nseq * H * (slices + (int64_t)(s - 2) * (slices + dk / kDeltaSlice)) + g) + rounds(wgs * (s - 1) + g);
+    const double t = chunk * (double)per / s * both + (kBothUs[size] + s * kJoinUs[size]) * (backward ? 2.0 : 1.0);
     if (t < least) least = t, best = s;
   }
   return best;
