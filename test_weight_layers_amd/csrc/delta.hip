@@ -9,7 +9,7 @@
 //   O = scale e^gamma o (Q W0^T) + A U
 //   W = e^gamma_last W0 + (e^(gamma_last - gamma) o U)^T K
 // Two kernels: T and A of every chunk at once (chunk), then the states in order of the chunks, split
-// over heads and 16-column slices of dv, which do not depend on one another (states).  Every wave lays
+// over heads and 16-column slices of dv, which do not depend on one another (states, delta_state.h).  Every wave lays
 // the packed sequences out in chunks for itself; for more than 63 of them a first kernel does (plan).
 #include "delta_state.h"
 

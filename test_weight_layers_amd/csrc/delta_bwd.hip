@@ -21,8 +21,6 @@ namespace {
 // The reverse of the states kernel, with the same split, layout, waves and order of loads:
 //   rows: K G^T, dU        rows: dR = T^T dU;  state: G <- e^gamma_last G + (scale eg o go)^T Q
 //   state: G += dP^T K;  rows: the next chunk's go
-// 16 chunks a sequence, 6 heads of 128 and 8 sequences (384 workgroups): 80 us, 5 a chunk with two
-// workgroups to a CU; 7 to 8 chunks of 4 heads of 64, fp32: 51 us.
 // Segments of few long sequences (see there) run at once here too: G before a segment is G after it times
 // M^T plus what the segment alone has.  kFirst: the last segment, and the others but the first from G = 0;
 // kSecond: all but the last, over what the first launch wrote for their rows.
@@ -229,7 +227,9 @@ __device__ __forceinline__ void delta_gstates(const DeltaParams &p, GradLds<T, D
 }
 
 // The states and their gradients do not depend on one another (but for M, which the first launch leaves to the
-// second): one launch for both, the gradients' workgroups, which take longer, first.
+// second): one launch for both, the gradients' workgroups, which take longer, first.  8 sequences of 16
+// chunks, 6 heads of 128: 110 us for 768 workgroups, two to a CU (132 one after the other); 6 ragged
+// sequences, 4 heads of 64, fp32: 68 (86).
 template <typename T, int DK, int PART>
 __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delta_chain_kernel(DeltaParams p, int grads) {
   union Lds {
@@ -248,8 +248,8 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
 // then dq and dk: wave w has the rows of half w / 4 and every fourth 16-wide column tile.  Operands
 // come from memory in fragment order; bound by their latency, so registers are kept few enough for
 // four waves a SIMD (one wave of 4 x 2 tiles a SIMD took 175 us where this takes 124 for 128 chunks
-// of 6 heads of 128; of its 278 MB, 55 us at a copy's rate, the products take 15 us and the vector
-// operations 30).
+// of 6 heads of 128; of that its 278 MB are 55 us at a copy's rate, the products 15 and the vector
+// operations 30.  Two column tiles at once, two fifths fewer operand loads, took as long).
 template <typename T, int DK>
 __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kernel(DeltaParams p) {
   constexpr int NT = DK / 64, TP = kTok<T>;

@@ -32,7 +32,7 @@ constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 
 //   kFirst: the first segment, outputs and all; U and M of the others but the last, of which M is
 //           dk / 16 more slices of rows
 //   kSecond: the others, each from its own starting state, (W_1 M_1 + U_1) M_2 + U_2 ..
-// 687 chunks of 4 heads of 256: 1680 us whole, 534 + 398 in five segments (448 and 256 workgroups; a CU's
+// 687 chunks of 4 heads of 256: 1680 us whole, 521 + 388 in five segments (448 and 256 workgroups; a CU's
 // two then take 3.9 us a chunk).
 // `id` of `count`: this workgroup among those that do this.
 template <typename T, int DK, bool BWD> struct StateLds {
