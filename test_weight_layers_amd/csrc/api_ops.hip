@@ -206,7 +206,7 @@ int delta_params(int H, int Hk, int dk, int dv, const float *w, const Rows &q, c
   p->segs = P.segs;
   p->seg_u = reinterpret_cast<float *>(b + P.off_su), p->seg_g = reinterpret_cast<float *>(b + P.off_sg), p->seg_m = b + P.off_sm;
   if (backward) {
-    p->gam = reinterpret_cast<double *>(b + P.off_gam);
+    p->gam = reinterpret_cast<float2 *>(b + P.off_gam);
     p->gop = b + P.off_gop;
     p->tt = b + P.off_tt, p->qt = b + P.off_qt, p->w0t = reinterpret_cast<float *>(b + P.off_w0t), p->gwt = reinterpret_cast<float *>(b + P.off_gwt);
     p->u = b + P.off_u, p->dr = b + P.off_dr;

@@ -47,7 +47,7 @@ struct DeltaParams {
   DeltaChunk *chunks;               // [nchunk]
   int *used;                        // one past the last row of the last sequence
   float *eg, *el, *be;              // [nchunk][H][64]: e^gamma_i, e^(gamma_last - gamma_i), beta (0 past the chunk)
-  double *gam;                      // gamma_i (backward)
+  float2 *gam;                      // gamma_i in base 2, two floats (backward)
   char *tm, *am;                    // [nchunk][H] split 64 x 64: T, A (forward) or A^T (backward)
   char *tt;                         // T^T (backward)
   char *kp, *qp;                    // [nchunk][Hk] split tokens 64 x dk, 0 past the chunk

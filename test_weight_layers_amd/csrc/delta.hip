@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
   constexpr int kPitch = DK + 16 / (int)sizeof(T), NK = DK / 32, kA = C + 4, TP = kTok<T>;
   constexpr int kTokBytes = C * kPitch * (int)sizeof(T), kABytes = C * kA * 4;
   __shared__ __attribute__((aligned(16))) unsigned char s_raw[kTokBytes > kABytes ? kTokBytes : kABytes];
-  __shared__ double s_gam[C];
+  __shared__ float2 s_gam[C];
   __shared__ float s_beta[C];
   __shared__ __attribute__((aligned(16))) float s_l[C][kA], s_t[C][kA], s_x[32][36];
   T *s_tok = reinterpret_cast<T *>(s_raw);              // [64][kPitch]
@@ -144,25 +144,27 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
   u32x4 xq[NP], xk[NP];
   fetch(p.q, p.ldq, xq);
   fetch(p.k, p.ldk, xk);
-  if (t < C) {
-    const bool ok = t < ck.len;
-    double gam = 0.0;
-    if (ok && p.decay) {
-      const float x = p.decay[h * p.decay_hs + ck.tok0 + t];
-      gam = x < -200.0f ? -200.0 : (double)x;           // e^-200 is 0 in fp32; -inf would leave inf - inf
-    }
+  float rate = 0.0f, be = 0.0f;
+  if (t < ck.len) {
+    if (p.decay) rate = p.decay[h * p.decay_hs + ck.tok0 + t];
+    be = p.beta[h * p.beta_hs + ck.tok0 + t];
+  }
+  // the first wave, which has the least of the products, sums the decays after them
+  const auto rates = [&] {
+    double gam = rate < -200.0f ? -200.0 : (double)rate;        // e^-200 is 0 in fp32; -inf would leave inf - inf
+#pragma unroll
     for (int d = 1; d < C; d <<= 1) {
       const double x = __shfl_up(gam, d);
       if (t >= d) gam += x;
     }
-    s_gam[t] = gam;
-    const float be = ok ? p.beta[h * p.beta_hs + ck.tok0 + t] : 0.0f;
+    const float2 lg = log_of(gam);
+    s_gam[t] = lg;
     s_beta[t] = be;
     p.be[ch * C + t] = be;
-    if (BWD) p.gam[ch * C + t] = gam;
+    if (BWD) p.gam[ch * C + t] = lg;
     p.eg[ch * C + t] = exp_of(gam);
     p.el[ch * C + t] = exp_of(__shfl(gam, 63) - gam);
-  }
+  };
   // the transposed operand: row = column of the tokens, k = token
   const auto write_transposed = [&](char *dst) {
 #pragma unroll
@@ -210,19 +212,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
       qk[j] = mm(qa[i], kb, qk[j]);
     }
   }
+  if (t < C) rates();
   if (writer) write_transposed(p.kt);
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int col = 16 * j + li;
+    const float2 gc = s_gam[col];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * w + 4 * g + r;
-      const float d = exp_of(row >= col ? s_gam[row] - s_gam[col] : 0.0);
+      s_t[row][col] = 0.0f;
+      if (j > w) {                                      // above the diagonal; L there is not read
+        s_a[row * kA + col] = 0.0f;
+        continue;
+      }
       const bool in = row < ck.len && col <= row;
+      const float d = exp_of(s_gam[row], gc);           // (below the diagonal; elsewhere not used)
       s_l[row][col] = in && col < row ? s_beta[row] * d * kk[j][r] : 0.0f;
       s_a[row * kA + col] = in ? p.scale * d * qk[j][r] : 0.0f;
-      s_t[row][col] = 0.0f;
     }
   }
   __syncthreads();

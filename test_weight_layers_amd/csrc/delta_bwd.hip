@@ -255,7 +255,8 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
   constexpr int NT = DK / 64, TP = kTok<T>;
   __shared__ __attribute__((aligned(16))) SplitTile<kOut<T>, C, C> s_x, s_xt, s_y, s_yt;
   __shared__ __attribute__((aligned(16))) float s_row[3][4][C];      // partials of q.(go W0), k.(dR W0), k.(U G)
-  __shared__ float s_rs[2][C], s_db[2][C], s_cs[4][C], s_red[4];
+  __shared__ float s_rs[2][C], s_db[2][C], s_cs[4][C], s_red[4], s_be[C];
+  __shared__ float2 s_gam[C];
   const int item = xcd_item(blockIdx.x, gridDim.x), h = item % p.heads, c = item / p.heads;
   const DeltaChunk ck = chunk_of(p, c);
   if (ck.len == 0) return;
@@ -270,6 +271,10 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
   const int64_t up = (int64_t)C * p.dv * 2;
   const char *GO = p.gop + ch * up * TP, *U = p.u + ch * up * kFull, *DR = p.dr + ch * up * kFull;
 
+  if (t < C) {
+    s_gam[t] = p.gam[ch * C + t];
+    s_be[t] = p.be[ch * C + t];
+  }
   // ---- X, Y and the sums over them: row tile w4, column tiles 2 half, 2 half + 1
   {
     f32x4 kk[2], qk[2], da[2], dl[2];
@@ -308,6 +313,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
     drv += __shfl_xor(drv, 16);
     drv += __shfl_xor(drv, 32);
     if (g == 0) s_db[half][ra] = drv;
+    __syncthreads();                                    // s_gam, s_be
     f32x4 rs = zero4(), dbs = zero4();
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -318,8 +324,8 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
       for (int r = 0; r < 4; ++r) {
         const int row = 16 * w4 + 4 * g + r;
         const bool in = row < ck.len && col <= row;
-        const float d = in ? exp_of(p.gam[ch * C + row] - p.gam[ch * C + col]) : 0.0f;
-        const float be = p.be[ch * C + row];
+        const float d = in ? exp_of(s_gam[row], s_gam[col]) : 0.0f;
+        const float be = s_be[row];
         x[r] = in ? p.scale * d * da[j][r] : 0.0f;
         const float dn = in && col < row ? -d * dl[j][r] : 0.0f;
         y[r] = be * dn;

@@ -269,7 +269,15 @@ __device__ __forceinline__ void join_segments(SplitTile<kFull, kDeltaSlice, DK> 
   }
 }
 
-// e^x for a difference of cumulative log decays held in 64 bits.
+// Cumulative log decays are summed in 64 bits and kept as two floats, in base 2: their differences, small
+// beside them, then are exact to 2^-23, without 64-bit arithmetic for every pair of tokens.
+__device__ __forceinline__ float2 log_of(double gam) {
+  const double x = gam * 1.4426950408889634;
+  const float h = (float)x;
+  return float2{h, (float)(x - (double)h)};
+}
+// e^(gamma_a - gamma_b)
+__device__ __forceinline__ float exp_of(float2 a, float2 b) { return __builtin_amdgcn_exp2f((a.x - b.x) + (a.y - b.y)); }
 __device__ __forceinline__ float exp_of(double x) { return __builtin_amdgcn_exp2f((float)(x * 1.4426950408889634)); }
 
 }  // namespace ttt
