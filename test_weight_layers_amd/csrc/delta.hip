@@ -86,7 +86,7 @@ constexpr int kZeroBlocks = 64;     // workgroups of the chunk kernel's launch t
 // One workgroup per chunk and head: e^gamma, T = (I + L)^-1 by block substitution in fp32 and A,
 // and (once per key head) the tokens and their transposes in fragment order.
 // Substitution, not products of powers of L: those grow without bound where keys repeat.
-// 687 chunks of 4 heads of 256, bf16: 108 us for 565 MB, 5.2 TB/s, what a copy reaches; 22 chunks 16.5 us,
+// 687 chunks of 4 heads of 256, bf16: 99 us for 565 MB, 5.7 TB/s, a copy reaches 5.1; 22 chunks 14.7 us,
 // the latency of the loads and the substitution.
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kernel(DeltaParams p) {
@@ -215,10 +215,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
   if (t < C) rates();
   if (writer) write_transposed(p.kt);
   __syncthreads();
+  float2 gr[4], gcol[4];                                // (read ahead of the stores, which may be to the same LDS for all
+  float br[4];                                          // that the compiler knows)
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    gr[r] = s_gam[16 * w + 4 * g + r];
+    gcol[r] = s_gam[16 * r + li];
+    br[r] = s_beta[16 * w + 4 * g + r];
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int col = 16 * j + li;
-    const float2 gc = s_gam[col];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * w + 4 * g + r;
@@ -228,8 +235,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
         continue;
       }
       const bool in = row < ck.len && col <= row;
-      const float d = exp_of(s_gam[row], gc);           // (below the diagonal; elsewhere not used)
-      s_l[row][col] = in && col < row ? s_beta[row] * d * kk[j][r] : 0.0f;
+      const float d = exp_of(gr[r], gcol[j]);           // (below the diagonal; elsewhere not used)
+      s_l[row][col] = in && col < row ? br[r] * d * kk[j][r] : 0.0f;
       s_a[row * kA + col] = in ? p.scale * d * qk[j][r] : 0.0f;
     }
   }

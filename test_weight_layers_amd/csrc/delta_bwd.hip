@@ -247,7 +247,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
 // row tile w % 4 and half of the column tiles), which pass through LDS as operands both ways round,
 // then dq and dk: wave w has the rows of half w / 4 and every fourth 16-wide column tile.  Operands
 // come from memory in fragment order; bound by their latency, so registers are kept few enough for
-// four waves a SIMD (one wave of 4 x 2 tiles a SIMD took 175 us where this takes 124 for 128 chunks
+// four waves a SIMD (one wave of 4 x 2 tiles a SIMD took 175 us where this takes 120 for 128 chunks
 // of 6 heads of 128; of that its 278 MB are 55 us at a copy's rate, the products 15 and the vector
 // operations 30.  Two column tiles at once, two fifths fewer operand loads, took as long).
 template <typename T, int DK>
@@ -315,20 +315,27 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
     if (g == 0) s_db[half][ra] = drv;
     __syncthreads();                                    // s_gam, s_be
     f32x4 rs = zero4(), dbs = zero4();
+    float2 gr[4];                                       // (read ahead of the stores to LDS)
+    float br[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      gr[r] = s_gam[16 * w4 + 4 * g + r];
+      br[r] = s_be[16 * w4 + 4 * g + r];
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int col = 16 * (2 * half + j) + li;
       f32x4 x, y;
+      const float2 gc = s_gam[col];
       float cs = 0.0f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = 16 * w4 + 4 * g + r;
         const bool in = row < ck.len && col <= row;
-        const float d = in ? exp_of(s_gam[row], s_gam[col]) : 0.0f;
-        const float be = s_be[row];
+        const float d = in ? exp_of(gr[r], gc) : 0.0f;
         x[r] = in ? p.scale * d * da[j][r] : 0.0f;
         const float dn = in && col < row ? -d * dl[j][r] : 0.0f;
-        y[r] = be * dn;
+        y[r] = br[r] * dn;
         const float qkr = in ? qk[j][r] : 0.0f, kkr = in ? kk[j][r] : 0.0f;
         const float m = x[r] * qkr + y[r] * kkr;
         rs[r] += m;
