@@ -7,6 +7,10 @@
 // norm below 3.9 (X 1.2, A 1.5, B 3.45): stored times 2^14 its elements stay in fp16's range, and an element
 // above 2^-17 keeps its low part out of the subnormal numbers; what smaller ones lose is below 2^-38.
 // (X is that small throughout only where |G| is below 1e-10, where 1e-7 beside it leaves X near zero.)
+// A and B of fp32 matrices of at most 64 rows or columns take three parts: the sums are short, so that the 22
+// bits are what is off (1 x 1400 x 50: 2.3e-6 with two parts, fp32 arithmetic 1.4e-6), most where b A and a I
+// cancel (1.7e-6 with three), and 64 x 64 matrices cost little: 2 x 36 x 1216 101 -> 108 us (X in three parts
+// too: no better, 136).
 // One part would not do throughout: the steps multiply what is lost along small singular directions
 // by up to 3.4445 each, 485 in five.  It does in the last two steps of bf16 matrices, where what
 // is lost (2^-12) is multiplied by 3.4 at most and the result has 8 bits; and bf16 matrices enter the
@@ -192,9 +196,9 @@ template <int TM_, int TN_, int WR_, int WC_, int NST_> struct Geo {
   static constexpr int TM = TM_, TN = TN_, WR = WR_, WC = WC_, NST = NST_, kThreads = WR * WC * 64;
   static constexpr int WM = TM / WR, WN = TN / WC, FM = WM / 16, FN = WN / 16;
 };
-// N: parts of both operands together (2, 3 or 4): the deeper ring where a stage is smaller
+// N: parts of both operands together (2 to 6): the deeper ring where a stage is smaller
 template <int TILE, int N> struct GeoOf;
-template <int N> struct GeoOf<64, N> { typedef Geo<64, 64, 2, 2, N == 4 ? 5 : 6> type; };
+template <int N> struct GeoOf<64, N> { typedef Geo<64, 64, 2, 2, N >= 4 ? 5 : 6> type; };
 template <int N> struct GeoOf<128, N> { typedef Geo<128, 128, 4, 2, N == 4 ? 4 : N == 3 ? 3 : 5> type; };
 template <int N> struct GeoOf<256, N> { typedef Geo<256, 256, 4, 2, N == 2 ? 4 : 2> type; };
 
@@ -241,7 +245,7 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   // The products of low parts in sums of their own, where registers allow it: a large sum then is rounded
   // once a stage, not three times (2 x 36 x 1216 fp32: 3.2e-6 -> 2.2e-6 off, 2 x 1300 x 1200 2.1e-6 -> 1.2e-6).
-  constexpr bool kLow = PA == 2 && PB == 2 && G::TM <= 128;
+  constexpr bool kLow = PA >= 2 && PB >= 2 && G::TM <= 128;
   f32x4 low[kLow ? G::FM : 1][kLow ? G::FN : 1];
 #pragma unroll
   for (auto &row : low)
@@ -344,7 +348,7 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
   unsigned char *mine = s + w * (G::WM * kPitch);
   const bool both = KIND == kNext || bi != bj;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 0; x < (G::TM == 64 ? 3 : 2); ++x) {
     if (x >= q.parts) break;
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
@@ -404,13 +408,17 @@ void product_of(const OrthParams &p, Product q, int rows, int cols, hipStream_t 
 }
 template <typename T, int PA, int PB, int KIND>
 void product(const OrthParams &p, const Product &q, int rows, int cols, hipStream_t s) {
-  // symmetric results: square tiles of at most 128, so that half of them stay away
-  const int tile = KIND == kGram || KIND == kPoly ? p.plan.tile_sym : p.plan.tile;
-  if constexpr (KIND == kNext || KIND == kLast) {
-    if (tile == 256) return product_of<T, PA, PB, KIND, 256>(p, q, rows, cols, s);
+  if constexpr (PA == 3) {     // (at most 64 rows)
+    product_of<T, PA, PB, KIND, 64>(p, q, rows, cols, s);
+  } else {
+    // symmetric results: square tiles of at most 128, so that half of them stay away
+    const int tile = KIND == kGram || KIND == kPoly ? p.plan.tile_sym : p.plan.tile;
+    if constexpr (KIND == kNext || KIND == kLast) {
+      if (tile == 256) return product_of<T, PA, PB, KIND, 256>(p, q, rows, cols, s);
+    }
+    if (tile == 128) return product_of<T, PA, PB, KIND, 128>(p, q, rows, cols, s);
+    product_of<T, PA, PB, KIND, 64>(p, q, rows, cols, s);
   }
-  if (tile == 128) return product_of<T, PA, PB, KIND, 128>(p, q, rows, cols, s);
-  product_of<T, PA, PB, KIND, 64>(p, q, rows, cols, s);
 }
 
 template <typename T> hipError_t run_orth(const OrthParams &p, hipStream_t s) {
@@ -433,7 +441,7 @@ template <typename T> hipError_t run_orth(const OrthParams &p, hipStream_t s) {
     x[i] = Mat{p.ws + q.off_x[i], xb, 2 * xb, q.rp / 16};
     xt[i] = Mat{p.ws + q.off_xt[i], xb, 2 * xb, q.cp / 16};
   }
-  const Mat A{p.ws + q.off_a, ab, 2 * ab, q.rp / 16}, B{p.ws + q.off_b, ab, 2 * ab, q.rp / 16};
+  const Mat A{p.ws + q.off_a, ab, q.parts * ab, q.rp / 16}, B{p.ws + q.off_b, ab, q.parts * ab, q.rp / 16};
   const int pr = q.tall ? q.cp : q.rp, pc = q.tall ? q.rp : q.cp;       // padded sizes of G
   hipLaunchKernelGGL(orth_load_kernel<T>, dim3(pc / 64, pr / 64, q.batch), dim3(256), 0, s, p, part, rest, x[0], xt[0]);
   for (int i = 0; i < p.steps; ++i) {
@@ -441,8 +449,16 @@ template <typename T> hipError_t run_orth(const OrthParams &p, hipStream_t s) {
     const bool one = kBf16 && left <= 2;                      // one part from here on
     const bool xone = one || (kBf16 && i == 0);               // X is one part
     const float *f = kBf16 && i == 0 ? rest : nullptr;
-    const Product gram{x[cur], x[cur], A, A, one ? 1 : 2, f, q.cp}, poly{A, A, B, B, one ? 1 : 2, nullptr, q.rp};
+    const Product gram{x[cur], x[cur], A, A, one ? 1 : q.parts, f, q.cp}, poly{A, A, B, B, one ? 1 : q.parts, nullptr, q.rp};
     const Product next{B, xt[cur], x[cur ^ 1], xt[cur ^ 1], kBf16 && left <= 3 ? 1 : 2, f, q.rp};
+    if constexpr (!kBf16)
+      if (q.parts == 3) {
+        product<float, 2, 2, kGram>(p, gram, q.rp, q.rp, s);
+        product<float, 3, 3, kPoly>(p, poly, q.rp, q.rp, s);
+        if (left == 1) product<T, 3, 2, kLast>(p, next, q.rp, q.cp, s);
+        else product<float, 3, 2, kNext>(p, next, q.rp, q.cp, s);
+        continue;
+      }
     if (xone) product<float, 1, 1, kGram>(p, gram, q.rp, q.rp, s); else product<float, 2, 2, kGram>(p, gram, q.rp, q.rp, s);
     if (one) product<float, 1, 1, kPoly>(p, poly, q.rp, q.rp, s); else product<float, 2, 2, kPoly>(p, poly, q.rp, q.rp, s);
     if (left == 1) {
@@ -470,12 +486,14 @@ OrthPlan plan_orth(int rows, int cols, int batch, bool bf16) {
   q.tile = tiles(256, 256) >= 200 ? 256 : (tiles(128, 128) >= 200 ? 128 : 64);
   const int64_t nr = (q.r + 127) / 128;
   q.tile_sym = batch * (nr * (nr + 1) / 2) >= 100 ? 128 : 64;
+  if (q.r <= 64) q.tile = q.tile_sym = 64;        // (a tile of 128 is half empty or more)
+  q.parts = !bf16 && q.r <= 64 ? 3 : 2;
   const int pad = q.tile > q.tile_sym ? q.tile : q.tile_sym;
   q.rp = (q.r + pad - 1) / pad * pad, q.cp = (q.c + pad - 1) / pad * pad;
   const int64_t elems = (int64_t)rows * cols, blocks = (elems + 4095) / 4096;
   q.norm_blocks = (int)(blocks < 1 ? 1 : (blocks > 256 ? 256 : blocks));
   const auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t xb = (size_t)q.rp * q.cp * 4 * batch, ab = (size_t)q.rp * q.rp * 4 * batch;
+  const size_t xb = (size_t)q.rp * q.cp * 4 * batch, ab = (size_t)q.rp * q.rp * 2 * q.parts * batch;
   size_t o = 0;
   q.off_norm = o, o = al(o + (size_t)batch * q.norm_blocks * 8);
   q.off_rest = o, o = al(o + (size_t)batch * 4);

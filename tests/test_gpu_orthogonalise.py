@@ -140,3 +140,19 @@ def test_refusals():
         ttt.orthogonalise(g, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="GPU"):
         ttt.orthogonalise(g.cpu())
+
+
+@pytest.mark.parametrize("shape", [(2, 36, 1216), (1, 1097, 34), (1, 1400, 50), (1, 16, 1400), (200, 64, 100), (200, 100, 64),
+                                   (1, 65, 1300)], ids=str)
+def test_long_and_narrow(shape):
+    """fp32 matrices of few rows or columns, as exact as fp32 steps.  B = a I + b A + c A A is 0.7 where A is
+    near I, of terms of 3.4, 4.8 and 2.0, each rounded by 2^-24: 8.7e-7 a step, of which the last two
+    remain (an error there is multiplied by about 1).  A's sums of up to 1400 terms are rounded 44 times, a root
+    of that at random: 6.6 * 2^-24 * 4.8 / 0.7 = 2.7e-6.  Together below 5e-6."""
+    from test_weight_layers_amd import ttt
+    g = 1e-3 * torch.randn(*shape, generator=torch.Generator().manual_seed(3))
+    err = rel(ttt.orthogonalise(g.cuda()), reference(g))
+    print(f"{shape}: {err:.2e}")
+    assert err <= 5e-6
+    half = g.bfloat16()
+    assert rel(ttt.orthogonalise(half.cuda()), reference(half)) <= TOL[torch.bfloat16]
