@@ -399,9 +399,9 @@ int ttt_gated_residual_backward(int32_t channels, int32_t norm_width, const void
  * g, out  : [batch][rows][cols] device, `dtype`; element (i, r, c) at i * bs + r * ld + c
  *           (bs >= 0, ld >= cols).  out may be g with the same strides, or must not overlap it.
  * steps   : >= 0 (0: only the normalisation).
- * Precision: every product accumulates in fp32 on operands of two fp16 parts (22 bits; A and A A of
- *           fp32 matrices of at most 64 rows or columns three, all of bf16 matrices one in the last
- *           two steps); the norm is summed in 64 bits.  Deterministic.
+ * Precision: every product accumulates in fp32 on operands of two fp16 parts (22 bits; three of A
+ *           and B of narrow matrices, one of larger bf16 matrices in the last two steps); the norm
+ *           is summed in 64 bits.  Deterministic.
  * workspace: >= ttt_orthogonalise_workspace_bytes(rows, cols, batch, dtype).
  */
 int ttt_orthogonalise_workspace_bytes(int32_t rows, int32_t cols, int32_t batch, int32_t dtype, size_t *bytes);

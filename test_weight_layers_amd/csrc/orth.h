@@ -9,7 +9,7 @@ namespace ttt {
 struct OrthPlan {
   int rows, cols, batch;
   bool bf16, tall;                  // tall: rows > cols, X is the transpose of G
-  int parts;                        // of A and B in memory
+  bool narrow;                      // a launch a step
   int r, c;                         // X is r x c, r <= c
   int tile, tile_sym;               // tile of B X, and of the symmetric products
   int rp, cp;                       // padded sizes

@@ -7,10 +7,6 @@
 // norm below 3.9 (X 1.2, A 1.5, B 3.45): stored times 2^14 its elements stay in fp16's range, and an element
 // above 2^-17 keeps its low part out of the subnormal numbers; what smaller ones lose is below 2^-38.
 // (X is that small throughout only where |G| is below 1e-10, where 1e-7 beside it leaves X near zero.)
-// A and B of fp32 matrices of at most 64 rows or columns take three parts: the sums are short, so that the 22
-// bits are what is off (1 x 1400 x 50: 2.3e-6 with two parts, fp32 arithmetic 1.4e-6), most where b A and a I
-// cancel (1.7e-6 with three), and 64 x 64 matrices cost little: 2 x 36 x 1216 101 -> 108 us (X in three parts
-// too: no better, 136).
 // One part would not do throughout: the steps multiply what is lost along small singular directions
 // by up to 3.4445 each, 485 in five.  It does in the last two steps of bf16 matrices, where what
 // is lost (2^-12) is multiplied by 3.4 at most and the result has 8 bits; and bf16 matrices enter the
@@ -25,6 +21,8 @@
 // where matrices are large: 4 x 4096 x 1024 bf16, five steps, 279 GFLOP (571 with the parts, tiles above the
 // diagonal left out) in 751 us, 760 TFLOP/s; small ones by their 17 launches: 12 x 512 x 256 fp32 119 us.
 // Sizes are padded with zeros to whole tiles.
+#include <type_traits>
+
 #include "common.h"
 #include "dma.h"
 #include "orth.h"
@@ -148,7 +146,8 @@ __global__ __launch_bounds__(256) void orth_load_kernel(OrthParams p, const doub
     in[i] = r < q.rows && c < q.cols ? to_f32(g[(int64_t)r * p.ldg + c]) : 0.0f;
   }
   double scale = orth_scale(p, part, b);
-  if (sizeof(T) == 2) {
+  const bool exact = sizeof(T) == 2 && !q.narrow;
+  if (exact) {
     int e;
     const double f = frexp(scale, &e);                        // scale = f 2^e, f in [1/2, 1)
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) rest[b] = (float)(2.0 * f);
@@ -160,7 +159,7 @@ __global__ __launch_bounds__(256) void orth_load_kernel(OrthParams p, const doub
   for (int i = 0; i < 16; ++i) tile[w + 4 * i][tx] = (float)((double)in[i] * scale);
   __syncthreads();
   const Mat &m = q.tall ? xt : x, &mt = q.tall ? x : xt;      // G's own layout, and its transpose
-  const int gr = tx >> 4, li = tx & 15, parts = sizeof(T) == 2 ? 1 : 2;
+  const int gr = tx >> 4, li = tx & 15, parts = exact ? 1 : 2;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {                               // wave w: fragment rows w
     float v[8], u[8];
@@ -196,9 +195,9 @@ template <int TM_, int TN_, int WR_, int WC_, int NST_> struct Geo {
   static constexpr int TM = TM_, TN = TN_, WR = WR_, WC = WC_, NST = NST_, kThreads = WR * WC * 64;
   static constexpr int WM = TM / WR, WN = TN / WC, FM = WM / 16, FN = WN / 16;
 };
-// N: parts of both operands together (2 to 6): the deeper ring where a stage is smaller
+// N: parts of both operands together (2, 3 or 4): the deeper ring where a stage is smaller
 template <int TILE, int N> struct GeoOf;
-template <int N> struct GeoOf<64, N> { typedef Geo<64, 64, 2, 2, N >= 4 ? 5 : 6> type; };
+template <int N> struct GeoOf<64, N> { typedef Geo<64, 64, 2, 2, N == 4 ? 5 : 6> type; };
 template <int N> struct GeoOf<128, N> { typedef Geo<128, 128, 4, 2, N == 4 ? 4 : N == 3 ? 3 : 5> type; };
 template <int N> struct GeoOf<256, N> { typedef Geo<256, 256, 4, 2, N == 2 ? 4 : 2> type; };
 
@@ -245,7 +244,7 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   // The products of low parts in sums of their own, where registers allow it: a large sum then is rounded
   // once a stage, not three times (2 x 36 x 1216 fp32: 3.2e-6 -> 2.2e-6 off, 2 x 1300 x 1200 2.1e-6 -> 1.2e-6).
-  constexpr bool kLow = PA >= 2 && PB >= 2 && G::TM <= 128;
+  constexpr bool kLow = PA == 2 && PB == 2 && G::TM <= 128;
   f32x4 low[kLow ? G::FM : 1][kLow ? G::FN : 1];
 #pragma unroll
   for (auto &row : low)
@@ -348,7 +347,7 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
   unsigned char *mine = s + w * (G::WM * kPitch);
   const bool both = KIND == kNext || bi != bj;
 #pragma unroll
-  for (int x = 0; x < (G::TM == 64 ? 3 : 2); ++x) {
+  for (int x = 0; x < 2; ++x) {
     if (x >= q.parts) break;
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
@@ -383,6 +382,162 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
   }
 }
 
+// ------------------------------------------------------------------ at most 64 rows
+// A whole step in one launch, a workgroup per 64 columns: A is the sum of what the tiles gave (in tile order),
+// B = a I + b A + c A A, this tile's B X, and its part of the next A.  A and B are 64 x 64 and computed by every
+// workgroup; they take three parts (22 bits are what would be off: where b A and a I cancel, 1 x 1400 x 50 fp32
+// 2.3e-6 with two, 1.3e-6 with three, fp32 arithmetic 1.4e-6).  Bound by latency: the sum, four products and their
+// exchanges; 2 x 36 x 1216 fp32 61 us in 8 launches, as large matrices are done 101 in 17.
+// Matrices in LDS in fragments too: [part][column / 32][row / 16], 1 KB each.
+template <typename T>
+__global__ __launch_bounds__(256) void orth_narrow_kernel(OrthParams p, Mat x, Mat xt, const float *in, float *out, bool first,
+                                                          bool last) {
+  __shared__ __attribute__((aligned(16))) unsigned char s_m[3 * 8 * 1024], s_x[2 * 8 * 1024];
+  const OrthPlan &q = p.plan;
+  const int nt = q.cp / 64, b = blockIdx.x / nt, tile = blockIdx.x % nt, t = threadIdx.x;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6), l = t & 63, g = l >> 4, li = l & 15;
+  const int rt0 = (w >> 1) * 2, ct0 = (w & 1) * 2;      // this wave's 32 x 32 of every product, in fragments
+  // element (row, col .. col + 3) of a part
+  const auto at = [&](unsigned char *m, int part, int row, int col) {
+    return m + (part * 8 + (col >> 5) * 4 + (row >> 4)) * 1024 + ((col >> 3 & 3) * 16 + (row & 15)) * 16 + (col & 7) * 2;
+  };
+  // lane (g, li) has C[16 i + li][16 j + 4 g + r] of its wave's tiles
+  const auto put = [&](unsigned char *m, int parts, const f32x4 (&c)[2][2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        f32x4 v = c[i][j];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          if (k >= parts) break;
+          f16x4 h;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            h[r] = (_Float16)v[r];
+            v[r] -= (float)h[r];
+          }
+          *reinterpret_cast<f16x4 *>(at(m, k, 16 * (rt0 + i) + li, 16 * (ct0 + j) + 4 * g)) = h;
+        }
+      }
+  };
+  const auto frag = [&](const unsigned char *m, int part, int rt, int kt) {
+    return *reinterpret_cast<const f16x8 *>(m + (part * 8 + kt * 4 + rt) * 1024 + l * 16);
+  };
+  // C = P Q^T over 64, P of PP parts in LDS, Q of PQ from `qf`(part, fragment row, kt)
+  const auto product = [&](auto pp, auto pq, const unsigned char *P, auto qf, f32x4 (&c)[2][2]) {
+    constexpr int PP = decltype(pp)::value, PQ = decltype(pq)::value, N = PP > PQ ? PP : PQ;
+    f32x4 low[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) c[i][j] = low[i][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      f16x8 fa[2][PP], fb[2][PQ];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int k = 0; k < PP; ++k) fa[i][k] = frag(P, k, rt0 + i, kt);
+#pragma unroll
+        for (int k = 0; k < PQ; ++k) fb[i][k] = qf(k, ct0 + i, kt);
+      }
+#pragma unroll
+      for (int d = N - 1; d >= 0; --d)
+#pragma unroll
+        for (int k = 0; k <= d; ++k)
+          if (k < PP && d - k < PQ)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                f32x4 &sum = d > 0 ? low[i][j] : c[i][j];
+                sum = mma(fb[j][d - k], fa[i][k], sum);
+              }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) c[i][j] += low[i][j];
+  };
+  typedef std::integral_constant<int, 2> Two;
+  typedef std::integral_constant<int, 3> Three;
+  f32x4 c[2][2];
+  if (first) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {                       // X's fragments as they are
+      const int f = w + 4 * e, part = f >> 3, kt = f >> 2 & 1, rt = f & 3;
+      *reinterpret_cast<u32x4 *>(s_x + f * 1024 + l * 16) =
+          *reinterpret_cast<const u32x4 *>(x.p + b * x.bs + part * x.plane + frag_byte(x, rt, 2 * tile + kt) + l * 16);
+    }
+  } else {
+    f32x4 a[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) a[i][j] = f32x4{0, 0, 0, 0};
+    const float *src = in + (int64_t)b * nt * 4096 + t * 4;
+#pragma unroll 4
+    for (int k = 0; k < nt; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) a[i][j] += *reinterpret_cast<const f32x4 *>(src + (int64_t)k * 4096 + (2 * i + j) * 1024);
+    put(s_m, 3, a);
+    __syncthreads();
+    product(Three{}, Three{}, s_m, [&](int k, int rt, int kt) { return frag(s_m, k, rt, kt); }, c);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          c[i][j][r] = (p.c / kUnit) * c[i][j][r] +
+                       (p.b * a[i][j][r] + (16 * (rt0 + i) + li == 16 * (ct0 + j) + 4 * g + r ? p.a * kUnit : 0.0f));
+    __syncthreads();
+    put(s_m, 3, c);
+    __syncthreads();
+    product(Three{}, Two{}, s_m, [&](int k, int rt, int kt) {
+      return *reinterpret_cast<const f16x8 *>(xt.p + b * xt.bs + k * xt.plane + frag_byte(xt, 4 * tile + rt, kt) + l * 16);
+    }, c);
+    const float f = last ? 1.0f / (kUnit * kUnit) : 1.0f / kUnit;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) c[i][j] *= f;
+    if (last) {
+      T *o = static_cast<T *>(p.out) + b * p.bso;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = 16 * (rt0 + i) + li, col = 64 * tile + 16 * (ct0 + j) + 4 * g + r;
+            if (row < q.r && col < q.c) o[q.tall ? (int64_t)col * p.ldo + row : (int64_t)row * p.ldo + col] = from_f32<T>(c[i][j][r]);
+          }
+      return;
+    }
+    put(s_x, 2, c);
+  }
+  __syncthreads();
+  if (!first) {         // X^T of the tile, in place: only this workgroup reads it, and has
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int f = w + 4 * e, part = f >> 3, kt = f >> 2 & 1, rt = f & 3;
+      const int row = 32 * kt + 8 * g + (li >> 2), col = 16 * rt + 4 * (li & 3);
+      *reinterpret_cast<bf16x8 *>(xt.p + b * xt.bs + part * xt.plane + frag_byte(xt, 4 * tile + rt, kt) + l * 16) =
+          cat8(lds_read_tr16(at(s_x, part, row, col)), lds_read_tr16(at(s_x, part, row + 4, col)));
+    }
+  }
+  product(Two{}, Two{}, s_x, [&](int k, int rt, int kt) { return frag(s_x, k, rt, kt); }, c);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<f32x4 *>(out + ((int64_t)b * nt + tile) * 4096 + (2 * i + j) * 1024 + t * 4) = c[i][j] * (1.0f / kUnit);
+}
+
 // G as it is (steps = 0): only scaled.
 template <typename T>
 __global__ __launch_bounds__(256) void orth_scale_kernel(OrthParams p, const double *part) {
@@ -408,17 +563,13 @@ void product_of(const OrthParams &p, Product q, int rows, int cols, hipStream_t 
 }
 template <typename T, int PA, int PB, int KIND>
 void product(const OrthParams &p, const Product &q, int rows, int cols, hipStream_t s) {
-  if constexpr (PA == 3) {     // (at most 64 rows)
-    product_of<T, PA, PB, KIND, 64>(p, q, rows, cols, s);
-  } else {
-    // symmetric results: square tiles of at most 128, so that half of them stay away
-    const int tile = KIND == kGram || KIND == kPoly ? p.plan.tile_sym : p.plan.tile;
-    if constexpr (KIND == kNext || KIND == kLast) {
-      if (tile == 256) return product_of<T, PA, PB, KIND, 256>(p, q, rows, cols, s);
-    }
-    if (tile == 128) return product_of<T, PA, PB, KIND, 128>(p, q, rows, cols, s);
-    product_of<T, PA, PB, KIND, 64>(p, q, rows, cols, s);
+  // symmetric results: square tiles of at most 128, so that half of them stay away
+  const int tile = KIND == kGram || KIND == kPoly ? p.plan.tile_sym : p.plan.tile;
+  if constexpr (KIND == kNext || KIND == kLast) {
+    if (tile == 256) return product_of<T, PA, PB, KIND, 256>(p, q, rows, cols, s);
   }
+  if (tile == 128) return product_of<T, PA, PB, KIND, 128>(p, q, rows, cols, s);
+  product_of<T, PA, PB, KIND, 64>(p, q, rows, cols, s);
 }
 
 template <typename T> hipError_t run_orth(const OrthParams &p, hipStream_t s) {
@@ -441,24 +592,24 @@ template <typename T> hipError_t run_orth(const OrthParams &p, hipStream_t s) {
     x[i] = Mat{p.ws + q.off_x[i], xb, 2 * xb, q.rp / 16};
     xt[i] = Mat{p.ws + q.off_xt[i], xb, 2 * xb, q.cp / 16};
   }
-  const Mat A{p.ws + q.off_a, ab, q.parts * ab, q.rp / 16}, B{p.ws + q.off_b, ab, q.parts * ab, q.rp / 16};
+  const Mat A{p.ws + q.off_a, ab, 2 * ab, q.rp / 16}, B{p.ws + q.off_b, ab, 2 * ab, q.rp / 16};
   const int pr = q.tall ? q.cp : q.rp, pc = q.tall ? q.rp : q.cp;       // padded sizes of G
   hipLaunchKernelGGL(orth_load_kernel<T>, dim3(pc / 64, pr / 64, q.batch), dim3(256), 0, s, p, part, rest, x[0], xt[0]);
+  if (q.narrow) {       // the sums over tiles take the room of the other X and X^T
+    float *sums[2] = {reinterpret_cast<float *>(p.ws + q.off_x[1]), reinterpret_cast<float *>(p.ws + q.off_xt[1])};
+    const dim3 grid((unsigned)((int64_t)q.batch * (q.cp / 64)));
+    for (int i = 0; i <= p.steps; ++i)
+      hipLaunchKernelGGL((orth_narrow_kernel<T>), grid, dim3(256), 0, s, p, x[0], xt[0], sums[~i & 1], sums[i & 1], i == 0,
+                         i == p.steps);
+    return hipGetLastError();
+  }
   for (int i = 0; i < p.steps; ++i) {
     const int cur = i & 1, left = p.steps - i;
     const bool one = kBf16 && left <= 2;                      // one part from here on
     const bool xone = one || (kBf16 && i == 0);               // X is one part
     const float *f = kBf16 && i == 0 ? rest : nullptr;
-    const Product gram{x[cur], x[cur], A, A, one ? 1 : q.parts, f, q.cp}, poly{A, A, B, B, one ? 1 : q.parts, nullptr, q.rp};
+    const Product gram{x[cur], x[cur], A, A, one ? 1 : 2, f, q.cp}, poly{A, A, B, B, one ? 1 : 2, nullptr, q.rp};
     const Product next{B, xt[cur], x[cur ^ 1], xt[cur ^ 1], kBf16 && left <= 3 ? 1 : 2, f, q.rp};
-    if constexpr (!kBf16)
-      if (q.parts == 3) {
-        product<float, 2, 2, kGram>(p, gram, q.rp, q.rp, s);
-        product<float, 3, 3, kPoly>(p, poly, q.rp, q.rp, s);
-        if (left == 1) product<T, 3, 2, kLast>(p, next, q.rp, q.cp, s);
-        else product<float, 3, 2, kNext>(p, next, q.rp, q.cp, s);
-        continue;
-      }
     if (xone) product<float, 1, 1, kGram>(p, gram, q.rp, q.rp, s); else product<float, 2, 2, kGram>(p, gram, q.rp, q.rp, s);
     if (one) product<float, 1, 1, kPoly>(p, poly, q.rp, q.rp, s); else product<float, 2, 2, kPoly>(p, poly, q.rp, q.rp, s);
     if (left == 1) {
@@ -486,14 +637,15 @@ OrthPlan plan_orth(int rows, int cols, int batch, bool bf16) {
   q.tile = tiles(256, 256) >= 200 ? 256 : (tiles(128, 128) >= 200 ? 128 : 64);
   const int64_t nr = (q.r + 127) / 128;
   q.tile_sym = batch * (nr * (nr + 1) / 2) >= 100 ? 128 : 64;
-  if (q.r <= 64) q.tile = q.tile_sym = 64;        // (a tile of 128 is half empty or more)
-  q.parts = !bf16 && q.r <= 64 ? 3 : 2;
+  // one tile of rows, and few enough of columns that every workgroup sums all of theirs: a launch a step
+  q.narrow = q.r <= 64 && q.c <= 8192;
+  if (q.narrow) q.tile = q.tile_sym = 64;
   const int pad = q.tile > q.tile_sym ? q.tile : q.tile_sym;
   q.rp = (q.r + pad - 1) / pad * pad, q.cp = (q.c + pad - 1) / pad * pad;
   const int64_t elems = (int64_t)rows * cols, blocks = (elems + 4095) / 4096;
   q.norm_blocks = (int)(blocks < 1 ? 1 : (blocks > 256 ? 256 : blocks));
   const auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t xb = (size_t)q.rp * q.cp * 4 * batch, ab = (size_t)q.rp * q.rp * 2 * q.parts * batch;
+  const size_t xb = (size_t)q.rp * q.cp * 4 * batch, ab = (size_t)q.rp * q.rp * 4 * batch;
   size_t o = 0;
   q.off_norm = o, o = al(o + (size_t)batch * q.norm_blocks * 8);
   q.off_rest = o, o = al(o + (size_t)batch * 4);

@@ -143,7 +143,7 @@ def test_refusals():
 
 
 @pytest.mark.parametrize("shape", [(2, 36, 1216), (1, 1097, 34), (1, 1400, 50), (1, 16, 1400), (200, 64, 100), (200, 100, 64),
-                                   (1, 65, 1300)], ids=str)
+                                   (1, 65, 1300), (2, 40, 2048), (1, 8192, 33), (1, 33, 8193), (3, 1, 500)], ids=str)
 def test_long_and_narrow(shape):
     """fp32 matrices of few rows or columns, as exact as fp32 steps.  B = a I + b A + c A A is 0.7 where A is
     near I, of terms of 3.4, 4.8 and 2.0, each rounded by 2^-24: 8.7e-7 a step, of which the last two
