@@ -316,7 +316,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kerne
       store_split(p.tt + mat, plane, e, split_of<kFull>(x));
       store_split(p.am + mat, plane, e, split_of<kFull>(y));
     } else {
-      store_split(p.am + mat, plane, e, split_of<kOut<T>>(ld8(s_a + row * kA + k0)));
+      store_split(p.am + mat, plane, e, split_of<kFull>(ld8(s_a + row * kA + k0)));
     }
   }
   if (BWD) {

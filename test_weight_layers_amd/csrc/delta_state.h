@@ -37,15 +37,13 @@ constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 
 // `id` of `count`: this workgroup among those that do this.
 template <typename T, int DK, bool BWD> struct StateLds {
   SplitTile<kFull, SL, DK> w[2];
-  SplitTile<kFull, SL, C> r, ul;
-  SplitTile<BWD ? kFull : kOut<T>, SL, C> u;
+  SplitTile<kFull, SL, C> r, ul, u;
 };
 template <typename T, int DK, bool BWD, int PART>
 __device__ __forceinline__ void delta_states(const DeltaParams &p, StateLds<T, DK, BWD> &lds, int id, int count) {
   constexpr int NT = DK / 64, NK = DK / 32, TP = kTok<T>;
   auto &s_w = lds.w;
-  auto &s_r = lds.r, &s_ul = lds.ul;
-  auto &s_u = lds.u;
+  auto &s_r = lds.r, &s_ul = lds.ul, &s_u = lds.u;
   constexpr int64_t tokens = DK * C * 2 * TP, tplane = DK * C * 2;      // bytes of a chunk's tokens and a part
   const int slices = p.dv / SL, item = xcd_item(id, count);
   const int wave = wave_id(), w = wave & 3, l = threadIdx.x & 63, g = l >> 4, li = l & 15;
@@ -95,8 +93,7 @@ __device__ __forceinline__ void delta_states(const DeltaParams &p, StateLds<T, D
     const auto rows = [&](auto live) {
       constexpr bool OUT = decltype(live)::value && !BWD, RECORD = decltype(live)::value && BWD;
       Split<TP> kf[NK], qf[OUT ? NK : 1];
-      Split<kFull> tf[2];
-      Split<kOut<T>> af[2];
+      Split<kFull> tf[2], af[2];
       T v[4];
       f32x4 eg, el, be;
       const auto load_token = [&](const char *tok, int c, int i) {
@@ -109,12 +106,12 @@ __device__ __forceinline__ void delta_states(const DeltaParams &p, StateLds<T, D
         be = *reinterpret_cast<const f32x4 *>(p.be + o);
         v_rows.load(static_cast<const T *>(p.v) + ((int64_t)sq.start + c * C) * p.ldv + vcol, t4, sq.len - c * C, v);
       };
-      const auto load_square = [&](const char *m, int c, auto &f) {
+      const auto load_square = [&](const char *m, int c, Split<kFull> (&f)[2]) {
 #pragma unroll
         // (the second half is zero for the first two waves, whose products leave it out; loads under a
         // condition would make every later wait one for all loads)
         for (int i = 0; i < 2; ++i)
-          f[i] = load_frag<sizeof(f[0]) / 16>(m + (ch0 + (int64_t)c * p.heads) * kSquare, plane, w * 2 + i);
+          f[i] = load_frag<kFull>(m + (ch0 + (int64_t)c * p.heads) * kSquare, plane, w * 2 + i);
       };
       if (c_first < c_end) {
 #pragma unroll
@@ -156,15 +153,15 @@ __device__ __forceinline__ void delta_states(const DeltaParams &p, StateLds<T, D
           s_u.copy_t4(0, 16 * w, p.u + (ch0 + (int64_t)c * p.heads) * (C * p.dv * 2 * kFull), (int64_t)C * p.dv * 2,
                       frag_at(16 * w + li, sl * SL + 4 * g, p.dv / 32));
         if constexpr (OUT) {
-          Sums<kOut<T>> qa[2];
+          Sums<kFull> qa[2];
 #pragma unroll
           for (int i = 0; i < NK; ++i) {
-            qa[i & 1].add(qf[i], W0.template ld<kOut<T>>(li, 32 * i + 8 * g));
+            qa[i & 1].add(qf[i], W0.ld(li, 32 * i + 8 * g));
             kf[i] = load_token(p.kp, nx, i);
           }
-          Sums<kOut<T>> au;
-          au.add(af[0], s_u.template ld<kOut<T>>(li, 8 * g));
-          if (w >= 2) au.add(af[1], s_u.template ld<kOut<T>>(li, 32 + 8 * g));
+          Sums<kFull> au;
+          au.add(af[0], s_u.ld(li, 8 * g));
+          if (w >= 2) au.add(af[1], s_u.ld(li, 32 + 8 * g));
           const f32x4 o = (qa[0].sum() + qa[1].sum()) * eg_now * p.scale + au.sum();
           load_square(p.tm, nx, tf);
           o_rows.store(static_cast<T *>(p.o) + ((int64_t)sq.start + c * C) * p.ldo + h * p.dv + sl * SL, t4, len, o);

@@ -2,10 +2,11 @@
 //
 // Sums and states are fp32; products run on bf16 MFMA, on operands written as sums of bf16 parts,
 // x = p0 + p1 + p2, p0 = bf16(x), p1 = bf16(x - p0), .. (8 bits of significand each).  bf16 tokens
-// are one part, exactly.  fp32 tokens, and what is computed on the way (states, U, T, ..), are three
-// parts, 24 bits: an fp32 result then is as good as from fp32 products, at 2.7 times the rate of
-// fp32 MFMA (six products of 16 clocks against one of 256 for 32 reduction elements).  What only
-// reaches bf16 outputs is two parts (17 bits); one would add 2^-9 to their rounding of 2^-9.
+// are one part, exactly.  fp32 tokens, and what is computed on the way (states, U, T, A, ..), are three
+// parts, 24 bits: a result before its rounding then is as good as from fp32 products, at 2.7 times the
+// rate of fp32 MFMA (six products of 16 clocks against one of 256 for 32 reduction elements).  Two parts
+// (17 bits) of what only reaches bf16 outputs leave these as far from 64 bits, but round a few of them to the
+// other neighbour (outputs 1.3e-4 off the 64-bit ones rounded, with three 1.1e-5 to 3.1e-5).
 // A product of two operands takes the part pairs (i, j) with i + j below the larger part count.
 // Measured beside bf16 tokens with two parts everywhere: fp32 states 4.0e-6 off and gradients of
 // the rates 6.9e-6, with three 1.1e-7 and 3.1e-7 (fp32 arithmetic: 2.2e-7 and 4.0e-7).
@@ -18,7 +19,7 @@ namespace ttt {
 template <int P> struct Split {
   bf16x8 p[P];
 };
-// Parts of T tokens, and of what only reaches T outputs.
+// Parts of T tokens, and of X and Y in the token gradients.
 template <typename T> constexpr int kTok = sizeof(T) == 2 ? 1 : 3;
 template <typename T> constexpr int kOut = sizeof(T) == 2 ? 2 : 3;
 constexpr int kFull = kDeltaParts;

@@ -1,0 +1,118 @@
+"""How exact the operators beside the layer are beyond the rounding of their outputs.
+
+bf16 outputs are compared with the 64-bit values rounded to bf16.  Before its one rounding a value v is off by
+some e: it rounds to another number only where a border lies between, with probability |e| / u for a spacing
+u <= 2^-7 |v|, and the difference then is u.  The sum of squares of the differences is at most
+sum |e| u <= 2^-7 |e|_2 |v|_2, so arithmetic held to a relative error E leaves at most sqrt(2^-7 E) between the two.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from test_weight_layers_amd import ttt
+    ttt.load()
+
+
+def rel(x, ref):
+    x, ref = x.double(), ref.double()
+    assert torch.isfinite(x).all()
+    return ((x - ref).norm() / ref.norm()).item()
+
+
+def borders(x, ref):
+    """How far x is from the 64-bit reference rounded as x is."""
+    return rel(x, ref.to(x.dtype))
+
+
+def limit(e):
+    return math.sqrt(2.0 ** -7 * e)
+
+
+# ------------------------------------------------------------------ gated delta rule
+def delta_inputs(lens, H, Hk, dk, dv, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.float64)
+    n = sum(lens)
+    unit = lambda t: t / t.norm(dim=-1, keepdim=True)
+    d = dict(q=unit(rn(n, Hk, dk)).reshape(n, -1), k=unit(rn(n, Hk, dk)).reshape(n, -1), v=rn(n, H * dv), go=rn(n, H * dv))
+    d = {x: t.bfloat16() for x, t in d.items()}
+    d["beta"] = torch.sigmoid(rn(H, n)).float()
+    d["decay"] = (-0.05 * torch.exp(rn(H, n))).float()
+    for x in ("w", "gw"):
+        d[x] = (rn(len(lens), H, dv, dk) / math.sqrt(dk)).float()
+    d["cu"] = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    return d
+
+
+def delta_reference(d, lens, Hk):
+    """Outputs, states and gradients token by token in 64 bits."""
+    S, H, dv, dk = d["w"].shape
+    n, r = d["q"].shape[0], H // Hk
+    heads = lambda t, m: t.double().view(n, -1, m).repeat_interleave(H // (t.shape[1] // m), 1)
+    q, k, v, go = heads(d["q"], dk), heads(d["k"], dk), heads(d["v"], dv), heads(d["go"], dv)
+    be, a = d["beta"].double().t(), d["decay"].double().exp().t()
+    o, dq, dk_, dvv = torch.zeros_like(v), torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    dbe, dde = torch.zeros_like(be), torch.zeros_like(be)
+    wf, gw0 = [], []
+    at = 0
+    for s in range(S):
+        w, kept = d["w"][s].double(), []
+        for t in range(at, at + lens[s]):
+            kept.append(w * a[t][:, None, None])
+            e = v[t] - (kept[-1] * k[t][:, None, :]).sum(-1)
+            w = kept[-1] + (be[t][:, None] * e)[:, :, None] * k[t][:, None, :]
+            o[t] = (w * q[t][:, None, :]).sum(-1)
+        wf.append(w)
+        dw = d["gw"][s].double()
+        for t in reversed(range(at, at + lens[s])):
+            p = kept[t - at]
+            e = v[t] - (p * k[t][:, None, :]).sum(-1)
+            w = p + (be[t][:, None] * e)[:, :, None] * k[t][:, None, :]
+            dq[t] = (go[t][:, :, None] * w).sum(1)
+            dw = dw + go[t][:, :, None] * q[t][:, None, :]
+            g = (dw * k[t][:, None, :]).sum(-1)
+            dbe[t] = (g * e).sum(-1)
+            dvv[t] = be[t][:, None] * g
+            dk_[t] = ((be[t][:, None] * e)[:, :, None] * dw - dvv[t][:, :, None] * p).sum(1)
+            dw = dw - dvv[t][:, :, None] * k[t][:, None, :]
+            dde[t] = (dw * p).sum((1, 2))
+            dw = dw * a[t][:, None, None]
+        gw0.append(dw)
+        at += lens[s]
+    shared = lambda t: t.view(n, Hk, r, dk).sum(2).reshape(n, -1)
+    grads = shared(dq), shared(dk_), dvv.reshape(n, -1), dbe.t(), dde.t(), torch.stack(gw0)
+    return o.reshape(n, -1), torch.stack(wf), grads
+
+
+# The first is cut in segments that run at once, the others are not.
+DELTA = [([1100], 4, 4, 64, 256), ([300, 0, 1, 200], 6, 2, 128, 128), ([260, 250], 4, 4, 256, 256)]
+
+
+@pytest.mark.parametrize("case", DELTA, ids=str)
+def test_delta(case):
+    """Arithmetic as exact as fp32 has it.  Operands carry 24 bits; a sum of up to 256 products is rounded once a
+    matrix instruction, at most 48 times (8 blocks of 32 terms, 6 pairs of parts), of random sign: 7 * 2^-24 =
+    4.1e-7, and five such sums follow one another (their errors add as a root): 9.3e-7.  Outputs and states are held to
+    1e-6; the gradients pass through the forward's five and the backward's five, 1.4e-6, and of a rate through a
+    sum that cancels in part: 2e-6."""
+    from test_weight_layers_amd import ttt
+    lens, H, Hk, dk, dv = case
+    d = delta_inputs(lens, H, Hk, dk, dv, 1)
+    o_ref, w_ref, g_ref = delta_reference(d, lens, Hk)
+    args = [d[x] for x in ("w", "q", "k", "v", "beta", "decay")]
+    o, w = ttt.delta(*args, key_heads=Hk, cu_seqlens=d["cu"])
+    grads = ttt.delta_backward(*args, d["go"], d["gw"], key_heads=Hk, cu_seqlens=d["cu"])
+    names = ("q", "k", "v", "beta", "decay", "w")
+    got = {"o": (borders(o, o_ref), limit(1e-6)), "states": (rel(w, w_ref), 1e-6)}
+    for x, g, r in zip(names, grads, g_ref):
+        got["grad " + x] = (borders(g, r), limit(2e-6)) if x in "qkv" else (rel(g, r), 2e-6)
+    print({x: f"{a:.2e} of {b:.2e}" for x, (a, b) in got.items()})
+    assert all(a <= b for a, b in got.values()), got
