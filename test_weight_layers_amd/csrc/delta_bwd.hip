@@ -244,7 +244,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
 
 // ------------------------------------------------------------------ token gradients
 // One workgroup of eight waves per chunk and head.  First the 64 x 64 matrices X and Y (wave w has
-// row tile w % 4 and half of the column tiles), which pass through LDS as operands both ways round,
+// row tile w % 4 and half of the column tiles), which pass through LDS and are read both ways round,
 // then dq and dk: wave w has the rows of half w / 4 and every fourth 16-wide column tile.  Operands
 // come from memory in fragment order; bound by their latency, so registers are kept few enough for
 // four waves a SIMD (one wave of 4 x 2 tiles a SIMD took 175 us where this takes 120 for 128 chunks
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
 template <typename T, int DK>
 __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kernel(DeltaParams p) {
   constexpr int NT = DK / 64, TP = kTok<T>;
-  __shared__ __attribute__((aligned(16))) SplitTile<kOut<T>, C, C> s_x, s_xt, s_y, s_yt;
+  __shared__ __attribute__((aligned(16))) SplitTile<kFull, C, C> s_xt, s_yt;      // X^T, Y^T
   __shared__ __attribute__((aligned(16))) float s_row[3][4][C];      // partials of q.(go W0), k.(dR W0), k.(U G)
   __shared__ float s_rs[2][C], s_db[2][C], s_cs[4][C], s_red[4], s_be[C];
   __shared__ float2 s_gam[C];
@@ -341,8 +341,6 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
         rs[r] += m;
         cs += m;
         dbs[r] += dn * kkr;
-        s_x.st1(row, col, x[r]);
-        s_y.st1(row, col, y[r]);
       }
       s_xt.st4(col, 16 * w4 + 4 * g, x);
       s_yt.st4(col, 16 * w4 + 4 * g, y);
@@ -397,16 +395,16 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void delta_gtoken_kern
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       f32x4 xq = zero4(), xk = zero4();
-      const int row = 32 * half + 16 * a + li + zero;
-      xq = mm(s_x.ld(row, 8 * g), k0, xq);
-      xq = mm(s_x.ld(row, 32 + 8 * g), k1, xq);
+      const int r16 = 32 * half + 16 * a + zero, row = r16 + li;
+      xq = mm(s_xt.ld_t(0, r16), k0, xq);
+      xq = mm(s_xt.ld_t(32, r16), k1, xq);
       xk = mm(s_xt.ld(row, 8 * g), q0, xk);
       xk = mm(s_xt.ld(row, 32 + 8 * g), q1, xk);
-      xk = mm(s_y.ld(row, 8 * g), k0, xk);
-      xk = mm(s_y.ld(row, 32 + 8 * g), k1, xk);
+      xk = mm(s_yt.ld_t(0, r16), k0, xk);
+      xk = mm(s_yt.ld_t(32, r16), k1, xk);
       xk = mm(s_yt.ld(row, 8 * g), k0, xk);
       xk = mm(s_yt.ld(row, 32 + 8 * g), k1, xk);
-      const int r0 = 32 * half + 16 * a + 4 * g + zero;
+      const int r0 = r16 + 4 * g;
       const f32x4 eg = *reinterpret_cast<const f32x4 *>(p.eg + ch * C + r0);
       const f32x4 el = *reinterpret_cast<const f32x4 *>(p.el + ch * C + r0);
       const f32x4 be = *reinterpret_cast<const f32x4 *>(p.be + ch * C + r0);

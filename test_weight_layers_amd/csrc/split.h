@@ -19,9 +19,8 @@ namespace ttt {
 template <int P> struct Split {
   bf16x8 p[P];
 };
-// Parts of T tokens, and of X and Y in the token gradients.
+// Parts of T tokens.
 template <typename T> constexpr int kTok = sizeof(T) == 2 ? 1 : 3;
-template <typename T> constexpr int kOut = sizeof(T) == 2 ? 2 : 3;
 constexpr int kFull = kDeltaParts;
 
 template <int A, int B> __device__ __forceinline__ f32x4 mm(const Split<A> &a, const Split<B> &b, f32x4 c) {
@@ -150,14 +149,6 @@ template <int P, int R, int Ccols> struct SplitTile {
       *reinterpret_cast<bf16x4 *>(b + i * kPlane + at_byte(r, c)) = h;
     }
   }
-  __device__ __forceinline__ void st1(int r, int c, float v) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const __bf16 h = (__bf16)v;
-      *reinterpret_cast<__bf16 *>(b + i * kPlane + at_byte(r, c)) = h;
-      v -= (float)h;
-    }
-  }
   __device__ __forceinline__ f32x4 at4(int r, int c) const {
     f32x4 v = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -180,6 +171,17 @@ template <int P, int R, int Ccols> struct SplitTile {
     const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
     const int o = at_byte(r0 + 4 * g + (li >> 2), c0 + 4 * (li & 3));
     return lds_read_tr16(reinterpret_cast<const unsigned char *>(b) + part * kPlane + o);
+  }
+  // Lane (g, li)'s eight rows r0 + 8 g .. + 7 of column c0 + li: an operand of the transposed matrix.
+  __device__ __forceinline__ Split<P> ld_t(int r0, int c0) const {
+    const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
+    const int r = r0 + 8 * g + (li >> 2), c = c0 + 4 * (li & 3);
+    const unsigned char *lo = reinterpret_cast<const unsigned char *>(b) + at_byte(r, c);
+    const unsigned char *hi = reinterpret_cast<const unsigned char *>(b) + at_byte(r + 4, c);
+    Split<P> f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) f.p[i] = cat8(lds_read_tr16(lo + i * kPlane), lds_read_tr16(hi + i * kPlane));
+    return f;
   }
   __device__ __forceinline__ void copy_t4(int r0, int c0, char *dst, int64_t plane, int64_t e) const {
 #pragma unroll
