@@ -399,7 +399,7 @@ int ttt_gated_residual_backward(int32_t channels, int32_t norm_width, const void
  *           (bs >= 0, ld >= cols).  out may be g with the same strides, or must not overlap it.
  * steps   : >= 0 (0: only the normalisation).
  * Precision: every product accumulates in fp32 on operands of two fp16 parts (22 bits; three of A
- *           and B of narrow matrices, one of larger bf16 matrices in the last two steps); the norm
+ *           and B of narrow matrices, one where bf16 matrices enter the first step exactly); the norm
  *           is summed in 64 bits.  Deterministic.
  * workspace: >= ttt_orthogonalise_workspace_bytes(rows, cols, batch, dtype).
  */

@@ -7,13 +7,15 @@
 // norm below 3.9 (X 1.2, A 1.5, B 3.45): stored times 2^14 its elements stay in fp16's range, and an element
 // above 2^-17 keeps its low part out of the subnormal numbers; what smaller ones lose is below 2^-38.
 // (X is that small throughout only where |G| is below 1e-10, where 1e-7 beside it leaves X near zero.)
-// One part would not do throughout: the steps multiply what is lost along small singular directions
-// by up to 3.4445 each, 485 in five.  It does in the last two steps of bf16 matrices, where what
-// is lost (2^-12) is multiplied by 3.4 at most and the result has 8 bits; and bf16 matrices enter the
-// first step exactly in one part, times a power of two, with the rest of 1 / |G| applied to A and X.
+// One part would not do: the steps multiply what is lost along small singular directions by up to 3.4445
+// each, 485 in five, and even one part in only the last two steps of bf16 matrices, where that is 3.4 and the
+// result has 8 bits, left it 1.57e-3 off the 64-bit result rounded (4 x 4096 x 1024), with two 1.0e-4 (fp32
+// arithmetic 1.3e-4).
+// bf16 matrices enter the first step exactly in one part, times a power of two, with the rest of 1 / |G|
+// applied to A and X.
 // Measured off the definition in 64 bits, 2 x 1300 x 1200 fp32: 1.2e-6 (fp32 arithmetic 3.2e-6, three bf16
-// parts and six products 3.0e-6 at 1.6 times the time); 4 x 4096 x 1024 bf16: 1.76e-3 (the rounding of the result
-// alone 1.66e-3).
+// parts and six products 3.0e-6 at 1.6 times the time); 4 x 4096 x 1024 bf16: 1.66e-3, the rounding of the
+// result alone.
 // The parts are written as planes by the kernel that computes a matrix, so that the main loop
 // copies tiles from memory straight into LDS.  Every product is C[i][j] = sum_k P[i][k] Q[j][k]
 // of row panels: X X^T, A A (A is symmetric) and B X from the stored X^T; A and B are
@@ -178,7 +180,6 @@ enum Kind { kGram, kPoly, kNext, kLast };   // A;  B = a I + b A + c A A;  X and
 struct Product {
   Mat P, Q;                         // C = P Q^T
   Mat c, ct;                        // results: [i][j] and [j][i] (the same matrix where C is symmetric)
-  int parts;                        // of the results
   const float *rest;                // [matrix] factor of each X in it (1 in kNext, 2 in kGram), or null
   int K, ti, tj;                    // reduction length, tiles along i and j
   int tiles;                        // tiles a matrix
@@ -348,7 +349,6 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
   const bool both = KIND == kNext || bi != bj;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    if (x >= q.parts) break;
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
 #pragma unroll
@@ -604,23 +604,17 @@ template <typename T> hipError_t run_orth(const OrthParams &p, hipStream_t s) {
     return hipGetLastError();
   }
   for (int i = 0; i < p.steps; ++i) {
-    const int cur = i & 1, left = p.steps - i;
-    const bool one = kBf16 && left <= 2;                      // one part from here on
-    const bool xone = one || (kBf16 && i == 0);               // X is one part
-    const float *f = kBf16 && i == 0 ? rest : nullptr;
-    const Product gram{x[cur], x[cur], A, A, one ? 1 : 2, f, q.cp}, poly{A, A, B, B, one ? 1 : 2, nullptr, q.rp};
-    const Product next{B, xt[cur], x[cur ^ 1], xt[cur ^ 1], kBf16 && left <= 3 ? 1 : 2, f, q.rp};
-    if (xone) product<float, 1, 1, kGram>(p, gram, q.rp, q.rp, s); else product<float, 2, 2, kGram>(p, gram, q.rp, q.rp, s);
-    if (one) product<float, 1, 1, kPoly>(p, poly, q.rp, q.rp, s); else product<float, 2, 2, kPoly>(p, poly, q.rp, q.rp, s);
-    if (left == 1) {
-      constexpr int P = kBf16 ? 1 : 2;
-      product<T, P, P, kLast>(p, next, q.rp, q.cp, s);
-    } else if (one) {
-      product<float, 1, 1, kNext>(p, next, q.rp, q.cp, s);
-    } else if (xone) {
-      product<float, 2, 1, kNext>(p, next, q.rp, q.cp, s);
+    const int cur = i & 1;
+    const bool one = kBf16 && i == 0;                         // X is one part, exactly
+    const float *f = one ? rest : nullptr;
+    const Product gram{x[cur], x[cur], A, A, f, q.cp}, poly{A, A, B, B, nullptr, q.rp};
+    const Product next{B, xt[cur], x[cur ^ 1], xt[cur ^ 1], f, q.rp};
+    if (one) product<float, 1, 1, kGram>(p, gram, q.rp, q.rp, s); else product<float, 2, 2, kGram>(p, gram, q.rp, q.rp, s);
+    product<float, 2, 2, kPoly>(p, poly, q.rp, q.rp, s);
+    if (i + 1 < p.steps) {
+      if (one) product<float, 2, 1, kNext>(p, next, q.rp, q.cp, s); else product<float, 2, 2, kNext>(p, next, q.rp, q.cp, s);
     } else {
-      product<float, 2, 2, kNext>(p, next, q.rp, q.cp, s);
+      if (one) product<T, 2, 1, kLast>(p, next, q.rp, q.cp, s); else product<T, 2, 2, kLast>(p, next, q.rp, q.cp, s);
     }
   }
   return hipGetLastError();

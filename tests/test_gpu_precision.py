@@ -133,3 +133,26 @@ def test_delta_gradients_inside_a_chunk():
     off = borders(got[0], ref[0]), borders(got[1], ref[1])
     print(f"q {off[0]:.2e} of {limit(7e-7):.2e}, k {off[1]:.2e} of {limit(9e-7):.2e}")
     assert off[0] <= limit(7e-7) and off[1] <= limit(9e-7)
+
+
+# ------------------------------------------------------------------ orthogonalisation
+def orth_reference(g, steps):
+    x = g.double()
+    x = x / (x.norm(dim=(-2, -1), keepdim=True) + 1e-7)
+    tall = x.shape[-2] > x.shape[-1]
+    x = x.mT.contiguous() if tall else x
+    for _ in range(steps):
+        a = torch.matmul(x, x.mT.contiguous())
+        x = 3.4445 * x + torch.matmul(-4.7750 * a + 2.0315 * torch.matmul(a, a), x)
+    return x.mT if tall else x
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 5])
+@pytest.mark.parametrize("shape", [(5, 200, 300), (2, 700, 400)], ids=str)
+def test_orthogonalise_bf16(shape, steps):
+    """As exact as fp32 matrices are (1e-5), then one rounding."""
+    from test_weight_layers_amd import ttt
+    g = (1e-3 * torch.randn(*shape, generator=torch.Generator().manual_seed(5))).bfloat16().cuda()
+    off = borders(ttt.orthogonalise(g, steps=steps), orth_reference(g, steps))
+    print(f"{off:.2e} of {limit(1e-5):.2e}")
+    assert off <= limit(1e-5)
