@@ -9,7 +9,7 @@
 // (X is that small throughout only where |G| is below 1e-10, where 1e-7 beside it leaves X near zero.)
 // One part would not do: the steps multiply what is lost along small singular directions by up to 3.4445
 // each, 485 in five, and even one part in only the last two steps of bf16 matrices, where that is 3.4 and the
-// result has 8 bits, left it 1.57e-3 off the 64-bit result rounded (4 x 4096 x 1024), with two 1.0e-4 (fp32
+// result has 8 bits, left it 1.57e-3 off the 64-bit result rounded (4 x 4096 x 1024), with two 7.7e-5 (fp32
 // arithmetic 1.3e-4).
 // bf16 matrices enter the first step exactly in one part, times a power of two, with the rest of 1 / |G|
 // applied to A and X.
@@ -37,6 +37,11 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ f32x4 mma(const f16x8 a, const f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
+
+// Called on a value before it is split in h and l.  Folded into the conversions, the arithmetic before gives an h
+// rounded once (v_fma_mix) for the one of its two uses and twice (v_mul, v_cvt) for the other: where they differ,
+// one value in some thousands, l is taken from another h than the one stored, and 2^-11 is lost.
+__device__ __forceinline__ void settle(f32x4 &v) { asm("" : "+v"(v)); }
 
 constexpr int KS = 32;              // reduction elements a stage
 constexpr float kUnit = 16384.0f;   // a stored element for 1
@@ -345,6 +350,10 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
   }
   // Parts, one at a time, through the wave's own piece of LDS: whole rows of C out of it as they
   // are, and of C^T by transposing reads.
+#pragma unroll
+  for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < G::FN; ++j) settle(acc[i][j]);
   unsigned char *mine = s + w * (G::WM * kPitch);
   const bool both = KIND == kNext || bi != bj;
 #pragma unroll
@@ -408,6 +417,7 @@ __global__ __launch_bounds__(256) void orth_narrow_kernel(OrthParams p, Mat x, M
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         f32x4 v = c[i][j];
+        settle(v);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
           if (k >= parts) break;

@@ -156,3 +156,39 @@ def test_orthogonalise_bf16(shape, steps):
     off = borders(ttt.orthogonalise(g, steps=steps), orth_reference(g, steps))
     print(f"{off:.2e} of {limit(1e-5):.2e}")
     assert off <= limit(1e-5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(3, 100, 200), (1, 300, 280)], ids=str)
+def test_orthogonalise_small_directions_beside_a_large_one(shape, dtype):
+    """A matrix of rank one and noise of a hundredth of its size, which the steps multiply by up to 3.4445^5 = 485
+    while the large direction stays near 1: what is lost of the large elements shows in the noise.  With p lost of
+    every operand (22 bits: 2^-23), three products a step and a result of norm 0.25 sqrt(r) at least, off by
+    485 * 3 p / (0.25 sqrt(r)): 6.9e-5 for r = 100, 4.1e-5 for 280."""
+    from test_weight_layers_amd import ttt
+    b, r, c = shape
+    gen = torch.Generator().manual_seed(6)
+    rn = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64)
+    g = (rn(b, r, 1) * rn(b, 1, c) + 1e-2 * rn(b, r, c)).to(dtype).cuda()
+    ref = orth_reference(g, 5)
+    assert ref.norm() >= 0.25 * math.sqrt(b * min(r, c))
+    got, e = ttt.orthogonalise(g), 485 * 3 * 2.0 ** -23 / (0.25 * math.sqrt(min(r, c)))
+    off, most = (borders(got, ref), limit(e)) if dtype == torch.bfloat16 else (rel(got, ref), e)
+    print(f"{off:.2e} of {most:.2e}")
+    assert off <= most
+
+
+def test_orthogonalise_elements_of_bf16():
+    """Diagonal matrices, whose elements stay apart: each is a product of numbers of 22 bits, off by at most 3 * 2^-22
+    in each of the six products of two steps (4.3e-6, held to 1e-5) before it is rounded, by at most half a spacing."""
+    from test_weight_layers_amd import ttt
+    d = (0.5 + 0.5 * torch.rand(3000, 100, generator=torch.Generator().manual_seed(7))).bfloat16().cuda()
+    got = ttt.orthogonalise(torch.diag_embed(d), steps=2)
+    x = d.double() / (d.double().norm(dim=1, keepdim=True) + 1e-7)
+    for _ in range(2):
+        x = x * (3.4445 - 4.7750 * x ** 2 + 2.0315 * x ** 4)
+    half = 2.0 ** (torch.floor(torch.log2(x)) - 8)
+    off = (got.diagonal(dim1=1, dim2=2).double() - x).abs() - half
+    print(f"{(off > 1e-5 * x).sum().item()} of {x.numel()} elements, {(off / x).max().item():.1e}")
+    assert (off <= 1e-5 * x).all()
+    assert got.count_nonzero() == x.numel()
