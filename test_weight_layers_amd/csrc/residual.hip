@@ -45,6 +45,17 @@ __device__ __forceinline__ float dot8(f32x8 a, f32x8 b) {
 }
 __device__ __forceinline__ f32x8 splat8(float x) { return f32x8{x, x, x, x, x, x, x, x}; }
 
+// 1 / (1 + e^-z) and what it lacks of 1, both as exact as fp32 has them: e^-|z| = 2^p (1 + r ln 2), p + r = -|z| log2 e
+// in two floats (with p alone it is 3.7e-6 off at |z| = 80; 137400 rows of 1024 in 268 us for 260).  e^-128 is 0
+// beside 1 and in fp32.
+__device__ __forceinline__ float2 sigmoid(float z) {
+  const float a = fmaxf(-fabsf(z), -128.0f), p = a * 1.4426950408889634f;
+  const float r = __builtin_fmaf(a, 1.9259630e-8f, __builtin_fmaf(a, 1.4426950408889634f, -p));
+  const float e2 = __builtin_amdgcn_exp2f(p), e = __builtin_fmaf(e2, r * 0.6931471805599453f, e2);
+  const float large = __builtin_amdgcn_rcpf(1.0f + e), small = e * large;
+  return z < 0.0f ? float2{small, large} : float2{large, small};
+}
+
 // Threads of a workgroup: 256, or one row's lanes.
 constexpr int threads_of(int lpr) { return lpr > 256 ? lpr : 256; }
 
@@ -147,7 +158,7 @@ __global__ __launch_bounds__(threads_of(LPR)) void residual_kernel(ResidualParam
       f32x8 u = o[j] * ag[j] * r;
       if (p.z)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] *= z[j][i] * sigmoid_fast(z[j][i]);
+        for (int i = 0; i < 8; ++i) u[i] *= z[j][i] * sigmoid(z[j][i]).x;
       x[j] += u;
       if (c < p.channels) sy += dot8(x[j], x[j]);
       if (live && c < p.channels) store8(static_cast<T *>(p.y) + row * p.ldy + c, x[j]);
@@ -248,9 +259,10 @@ __global__ __launch_bounds__(threads_of(LPR)) void residual_backward_kernel(Resi
         f32x8 dz;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float sg = sigmoid_fast(z[j][i]), zi = z[j][i];
-          dz[i] = gx[j][i] * ag[j][i] * o[j][i] * (sg * (1.0f + zi * (1.0f - sg)));
-          q[j][i] *= zi * sg;
+          const float zi = z[j][i];
+          const float2 sg = sigmoid(zi);
+          dz[i] = gx[j][i] * ag[j][i] * o[j][i] * (sg.x * (1.0f + zi * sg.y));
+          q[j][i] *= zi * sg.x;
         }
         if (in) store8(static_cast<T *>(p.gz) + row * p.ldgz + c, dz);
       }

@@ -135,6 +135,35 @@ def test_delta_gradients_inside_a_chunk():
     assert off[0] <= limit(7e-7) and off[1] <= limit(9e-7)
 
 
+# ------------------------------------------------------------------ gated residual tail
+def test_gate_of_fp32_rows():
+    """o = +-1 and no eps: the norm is exactly 1, and y is the gate alone, z / (1 + e^-z): an exponential (2^-23),
+    a sum, a quotient and a product (2^-24 each), and the square root's and quotient's of the norm: 8 * 2^-24 of every
+    element.  The gradient of z adds the sigmoid of -z, two products and a sum: 16 * 2^-24, its largest being
+    1.1."""
+    from test_weight_layers_amd import ttt
+    C = 256
+    z = torch.linspace(-80.0, 80.0, 64 * C, device="cuda").view(64, C)
+    o = torch.where(torch.arange(C, device="cuda") % 3 == 0, -1.0, 1.0).expand(64, C).contiguous()
+    y, _ = ttt.gated_residual(torch.zeros_like(z), o, z, eps=0.0)
+    zd = z.double()
+    s = torch.sigmoid(zd)
+    ref = o.double() * zd * s
+    off = ((y.double() - ref).abs() / ref.abs()).max().item()
+    gz = ttt.gated_residual_backward(torch.ones_like(z), None, y, o, z, eps=0.0)[2]
+    want = o.double() * s * (1 + zd * (1 - s))
+    goff = (gz.double() - want).abs().max().item()
+    print(f"gate {off:.2e}, gradient {goff:.2e}")
+    assert off <= 8 * 2.0 ** -24 and goff <= 16 * 2.0 ** -24
+    # beyond what an exponential reaches: z itself, 0, infinity, and not a number only where it stands
+    far = torch.tensor([200.0, 3e38, math.inf, -200.0, -3e38, math.nan, 0.0, 1.0], device="cuda")[None]
+    y, _ = ttt.gated_residual(torch.zeros_like(far), torch.ones_like(far), far, eps=0.0)
+    assert torch.equal(y[0, :5], torch.tensor([200.0, 3e38, math.inf, 0.0, 0.0], device="cuda"))
+    assert y[0, 5].isnan() and y[0, 6] == 0 and abs(y[0, 7].item() - 1 / (1 + math.exp(-1))) <= 8 * 2.0 ** -24
+    gz = ttt.gated_residual_backward(torch.ones_like(far), None, y, torch.ones_like(far), far, eps=0.0)[2]
+    assert torch.equal(gz[0, [0, 1, 3, 4, 6]], torch.tensor([1.0, 1.0, 0.0, 0.0, 0.5], device="cuda")) and gz[0, 5].isnan()
+
+
 # ------------------------------------------------------------------ orthogonalisation
 def orth_reference(g, steps):
     x = g.double()
