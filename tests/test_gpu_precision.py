@@ -164,6 +164,44 @@ def test_gate_of_fp32_rows():
     assert torch.equal(gz[0, [0, 1, 3, 4, 6]], torch.tensor([1.0, 1.0, 0.0, 0.0, 0.5], device="cuda")) and gz[0, 5].isnan()
 
 
+@pytest.mark.parametrize("C,norm", [(8192, 4096), (8176, 4088), (2048, 1024)], ids=str)
+def test_wide_groups(C, norm):
+    """One element of eight is 3967 / 2048, whose square is exact: added one after another the squares of 512 such
+    round the same way again and again (7.6e-6 of the sum).  40 roundings in a row at most, halved by the root, and
+    8 after it: 28 * 2^-24."""
+    from test_weight_layers_amd import ttt
+    o = torch.zeros(3, C, device="cuda")
+    o[:, ::8] = 3967 / 2048
+    y, _ = ttt.gated_residual(torch.zeros_like(o), o, eps=0.0, norm_width=norm)
+    off = (y[:, ::8].double() / math.sqrt(8.0) - 1.0).abs().max().item()
+    print(f"{off:.2e}")
+    assert off <= 28 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("C,norm", [(8176, 4088), (6144, 2048), (7200, 2400), (2048, 1024), (4096, 1024), (2040, 680),
+                                    (600, 120)], ids=str)
+def test_groups_of_many_lanes(C, norm):
+    """Values and gradients against the formula, the groups apart from one another.  Under 64 roundings of 2^-24 in a
+    row: 8 squares of a lane, two levels of at most 23 sums, the root, a quotient and the products."""
+    from test_weight_layers_amd import ttt
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    n = 5
+    x, z, gy = rn(n, C), rn(n, C), rn(n, C)
+    # each group of a size of its own
+    o = rn(n, C) * torch.logspace(-2, 2, n * (C // norm), device="cuda").view(n, -1).repeat_interleave(norm, 1)
+    y, _ = ttt.gated_residual(x, o, z, norm_width=norm)
+    od, zd = o.double().requires_grad_(True), z.double().requires_grad_(True)
+    og = od.view(n, -1, norm)
+    u = (og / torch.sqrt((og * og).mean(-1, keepdim=True) + 1e-6)).view(n, C) * zd * torch.sigmoid(zd)
+    go_ref, gz_ref = torch.autograd.grad(u, (od, zd), gy.double())
+    got = ttt.gated_residual_backward(gy, None, y, o, z, norm_width=norm)
+    scale = o.double().abs()        # the gradient of a group is as large as its o is small
+    off = rel(y, x.double() + u.detach()), rel(got[1].double() * scale, go_ref * scale), rel(got[2], gz_ref)
+    print([f"{e:.1e}" for e in off])
+    assert max(off) <= 64 * 2.0 ** -24
+
+
 # ------------------------------------------------------------------ orthogonalisation
 def orth_reference(g, steps):
     x = g.double()
