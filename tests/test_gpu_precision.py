@@ -259,3 +259,32 @@ def test_orthogonalise_elements_of_bf16():
     print(f"{(off > 1e-5 * x).sum().item()} of {x.numel()} elements, {(off / x).max().item():.1e}")
     assert (off <= 1e-5 * x).all()
     assert got.count_nonzero() == x.numel()
+
+
+# Every pair of tile sizes: of B X, and of the symmetric A and B.
+TILES = [((3, 200, 300), 64, 64), ((120, 100, 120), 64, 128), ((5, 1300, 1390), 128, 128), ((30, 190, 1000), 128, 64),
+         ((2, 1300, 5100), 256, 128), ((2, 5100, 1300), 256, 128), ((3, 200, 20000), 256, 64)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape,tile,sym", TILES, ids=str)
+def test_orthogonalise_tiles(shape, tile, sym, dtype):
+    """Each step has products of its own (X enters the first in one part where it is bf16, the last writes the result):
+    1, 2 and 5 of them.  Sizes leave a part of the last tile empty.  fp32 is held to 1e-5."""
+    from test_weight_layers_amd import ttt
+    b, r, c = shape
+    # the tiles are chosen as the padded sizes in the workspace say
+    pad = max(tile, sym)
+    rp, cp = (-(-x // pad) * pad for x in (min(r, c), max(r, c)))
+    up = lambda x: -(-x // 256) * 256
+    blocks = min(256, -(-r * c // 4096))
+    assert ttt.orthogonalise_workspace_bytes(r, c, b, dtype) == (up(b * blocks * 8) + up(b * 4) + 4 * up(rp * cp * 4 * b)
+                                                                 + 2 * up(rp * rp * 4 * b))
+    g = torch.randn(*shape, generator=torch.Generator().manual_seed(9)).to(dtype).cuda()
+    for steps in (1, 2, 5):
+        ref = orth_reference(g, steps)
+        got = ttt.orthogonalise(g, steps=steps)
+        off, most = (borders(got, ref), limit(1e-5)) if dtype == torch.bfloat16 else (rel(got, ref), 1e-5)
+        print(f"{steps}: {off:.2e} of {most:.2e}")
+        assert off <= most
+        assert torch.equal(got, ttt.orthogonalise(g, steps=steps))
