@@ -637,10 +637,18 @@ OrthPlan plan_orth(int rows, int cols, int batch, bool bf16) {
   q.rows = rows, q.cols = cols, q.batch = batch, q.bf16 = bf16;
   q.tall = rows > cols;
   q.r = q.tall ? cols : rows, q.c = q.tall ? rows : cols;
-  const auto tiles = [&](int tm, int tn) { return (int64_t)batch * ((q.r + tm - 1) / tm) * ((q.c + tn - 1) / tn); };
-  q.tile = tiles(256, 256) >= 200 ? 256 : (tiles(128, 128) >= 200 ? 128 : 64);
-  const int64_t nr = (q.r + 127) / 128;
-  q.tile_sym = batch * (nr * (nr + 1) / 2) >= 100 ? 128 : 64;
+  // The largest tile that still fills the card and is not mostly padding: the products' work, rows^2 x columns in
+  // whole tiles, may be a third above that in tiles of 64, which is what a larger tile's rate makes up for.  bf16,
+  // with that limit and without: 64 x 128 x 1024 201 and 408 us, 200 x 100 x 120 153 and 478, 64 x 300 x 1024 734 and
+  // 1137, 40 x 300 x 1400 640 and 1008; 8 x 768 x 2048 616 in tiles of 256 and 697 of 64, 2 x 1300 x 5100 (1.31 times
+  // the work) 1165 and 1273.
+  const auto up = [](int64_t x, int t) { return (x + t - 1) / t * t; };
+  const auto tiles = [&](int t) { return batch * (up(q.r, t) / t) * (up(q.c, t) / t); };
+  const auto work = [&](int t) { return up(q.r, t) * up(q.r, t) * up(q.c, t); };
+  const auto fits = [&](int t) { return 3 * work(t) <= 4 * work(64); };
+  q.tile = tiles(256) >= 200 && fits(256) ? 256 : (tiles(128) >= 200 && fits(128) ? 128 : 64);
+  const int64_t nr = up(q.r, 128) / 128;
+  q.tile_sym = batch * (nr * (nr + 1) / 2) >= 100 && fits(128) ? 128 : 64;
   // one tile of rows, and few enough of columns that every workgroup sums all of theirs: a launch a step
   q.narrow = q.r <= 64 && q.c <= 8192;
   if (q.narrow) q.tile = q.tile_sym = 64;

@@ -158,6 +158,19 @@ def test_orthogonalise_refusals(lib):
     assert st == 0 and n > 3 * 100 * 200 * 4
 
 
+@pytest.mark.parametrize("rows,cols,batch,rp,cp", [
+    (128, 1024, 64, 128, 1024), (768, 128, 96, 128, 768), (128, 16384, 4, 128, 16384), (100, 120, 200, 128, 128),
+    (300, 1024, 64, 320, 1024), (190, 1000, 50, 192, 1024),           # a larger tile would be mostly padding
+    (768, 2048, 8, 768, 2048), (1300, 5100, 2, 1536, 5120), (4096, 1024, 4, 1024, 4096)])
+def test_orthogonalise_is_not_mostly_padding(lib, rows, cols, batch, rp, cp):
+    """The workspace holds two X and X^T and one A and B of padded sizes, two fp16 parts each."""
+    up = lambda x: -(-x // 256) * 256
+    st, b = ws(lib, "ttt_orthogonalise_workspace_bytes", rows, cols, batch, BF16)
+    blocks = min(256, -(-rows * cols // 4096))
+    assert st == 0
+    assert b == up(batch * blocks * 8) + up(batch * 4) + 4 * up(rp * cp * 4 * batch) + 2 * up(rp * rp * 4 * batch)
+
+
 def test_binding_refuses_host_tensors():
     t = torch.zeros(4, 64)
     w = torch.zeros(1, 1, 64, 64)
