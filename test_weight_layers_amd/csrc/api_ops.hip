@@ -324,6 +324,9 @@ int ttt_delta_step(int32_t heads, int32_t key_heads, int32_t dk, int32_t dv, flo
   if (n < 0 || pool < 1) return fail(TTT_EINVAL, "n must be >= 0 and pool >= 1");
   if (n > kMaxRows || n * heads * (dv / 64) > kMaxGroups)
     return fail(TTT_EUNSUPPORTED, "too many rows (%lld) for %d heads in one call", (long long)n, heads);
+  // every workgroup looks for rows of the same state among all slots: 2^42 looks take a second
+  if (slots && n * n > (int64_t(1) << 42) / ((int64_t)heads * (dv / 64)))
+    return fail(TTT_EUNSUPPORTED, "too many rows (%lld) with slots for %d heads in one call", (long long)n, heads);
   if (!slots && n > pool) return fail(TTT_EINVAL, "%lld rows without slots need as many states (pool %d)", (long long)n, pool);
   if (!std::isfinite(scale)) return fail(TTT_EINVAL, "scale must be finite");
   const size_t es = esize(dtype);

@@ -118,6 +118,19 @@ def test_delta_step_refusals(lib):
 
 
 @cpu_only
+def test_delta_step_of_too_many_slots(lib):
+    """Rows of one state are looked for among all slots: more than 2^42 looks, seconds of work, are refused."""
+    def call(n, slots, dv=64):
+        # (no q: the last check before a launch would refuse it)
+        return lib.ttt_delta_step(1, 1, 64, dv, 1 << 30, 1 << 30, slots, None, 64, 5 << 20, 64, 6 << 20, dv, 7 << 20, 10, None, 0,
+                                  8 << 20, dv, n, 1.0, F32, 0, None)
+    assert call((1 << 21) + 1, 3 << 20) == -2 and b"slots" in lib.ttt_last_error()
+    assert call((1 << 20) + 1, 3 << 20, 256) == -2 and b"slots" in lib.ttt_last_error()
+    for n, slots, dv in ((1 << 21, 3 << 20, 64), (1 << 20, 3 << 20, 256), ((1 << 21) + 1, None, 64)):
+        assert call(n, slots, dv) == -1 and b"q is null" in lib.ttt_last_error()
+
+
+@cpu_only
 def test_gated_residual_refusals(lib):
     def call(C=64, norm=64, x=1 << 20, o=2 << 20, z=None, gamma=None, gn=None, eps=1e-6, y=3 << 20, h=None, ld=64, n=10):
         return lib.ttt_gated_residual(C, norm, x, ld, o, ld, z, ld, gamma, None, gn, eps, y, ld, h, ld, n, F32, None)
