@@ -140,24 +140,24 @@ def _weights(w: Sequence[torch.Tensor]) -> Tuple[int, int, int]:
     return H, d, m
 
 
-def _eta_stride(eta: torch.Tensor, H: int, n: int, device, on_gpu: bool = True) -> int:
+def _eta_stride(eta: torch.Tensor, H: int, n: int, device, on_gpu: bool = True, name: str = "eta") -> int:
     """Head stride of the rates: [H, >=n] with unit token stride, or [>=n] shared by every head."""
     if eta.dtype != torch.float32:
-        raise ValueError("eta must be float32")
+        raise ValueError(f"{name} must be float32")
     if on_gpu:
         if not eta.is_cuda or (device is not None and eta.device != torch.device(device)):
-            raise ValueError("eta must be on the same GPU as the tokens")
+            raise ValueError(f"{name} must be on the same GPU as the tokens")
     elif eta.is_cuda:
-        raise ValueError("eta must be in host memory")
+        raise ValueError(f"{name} must be in host memory")
     if eta.dim() == 2:
         if eta.shape[0] != H or eta.shape[1] < n or (n > 1 and eta.stride(1) != 1) or eta.stride(0) < 0:
-            raise ValueError(f"eta must be [H={H}, >={n}] with unit token stride")
+            raise ValueError(f"{name} must be [H={H}, >={n}] with unit token stride")
         return eta.stride(0)
     if eta.dim() == 1:
         if eta.shape[0] < n or (n > 1 and eta.stride(0) != 1):
-            raise ValueError(f"eta must be [>={n}] with unit stride")
+            raise ValueError(f"{name} must be [>={n}] with unit stride")
         return 0
-    raise ValueError("eta must be [H, N] or [N]")
+    raise ValueError(f"{name} must be [H, N] or [N]")
 
 
 def _same_rows(t: torch.Tensor, like: torch.Tensor, rows: int, width: int, name: str) -> int:
@@ -424,13 +424,13 @@ def _row(t: torch.Tensor, dtype: torch.dtype, dev: int, n: int, width: int, name
     raise ValueError(f"{name} must be [{n}, >={width}] with unit column stride, got {tuple(shape)}")
 
 
-def _rate(t: torch.Tensor, H: int, n: int, dev: int) -> int:
+def _rate(t: torch.Tensor, H: int, n: int, dev: int, name: str) -> int:
     """Head stride of a rate tensor (as _eta_stride)."""
     shape, stride = t.shape, t.stride()
     if len(shape) == 2 and shape[0] == H and shape[1] >= n and stride[1] == 1 and t.dtype == torch.float32 \
             and t.get_device() == dev:
         return stride[0]
-    return _eta_stride(t, H, n, torch.device("cuda", dev))
+    return _eta_stride(t, H, n, torch.device("cuda", dev), name=name)
 
 
 def _bytes(workspace: torch.Tensor, dev: int) -> int:
@@ -458,8 +458,8 @@ def _delta_args(w, q, k, v, beta, decay, key_heads):
         raise ValueError("q must be a 2-D tensor of token rows")
     n = q.shape[0]
     return (dev, S, H, Hk, dv, dk, n, code, _row(q, dtype, dev, n, Hk * dk, "q"), _row(k, dtype, dev, n, Hk * dk, "k"),
-            _row(v, dtype, dev, n, H * dv, "v"), _rate(beta, H, n, dev),
-            0 if decay is None else _rate(decay, H, n, dev))
+            _row(v, dtype, dev, n, H * dv, "v"), _rate(beta, H, n, dev, "beta"),
+            0 if decay is None else _rate(decay, H, n, dev, "decay"))
 
 
 def _offsets(cu, sequences: int, dev: int) -> None:

@@ -193,3 +193,13 @@ def test_binding_refuses_host_tensors():
                  lambda: ttt.gated_residual_backward(t, None, t, t), lambda: ttt.orthogonalise(t)):
         with pytest.raises((ValueError, RuntimeError, AssertionError)):
             call()
+
+
+def test_rates_are_refused_by_their_names():
+    good = torch.zeros(2, 5)
+    for name in ("beta", "decay"):
+        for t in (good.double(), good, good[:, :3], good.t(), good[None]):
+            with pytest.raises(ValueError, match=f"^{name} must be"):
+                ttt._rate(t, 2, 4, 0, name)
+    with pytest.raises(ValueError, match="^eta must be float32"):
+        ttt._eta_stride(good.double(), 2, 4, None)
