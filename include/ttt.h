@@ -312,9 +312,9 @@ int ttt_stream_ex(int32_t heads, int32_t d, int32_t m,
  *   empty (its state passes through).  Rows of no sequence are not read; of o they are
  *   left as they were, or set to zero with TTT_DELTA_ZERO_UNUSED; gradients of them are zero.
  * Precision: fp32 states and sums; products take fp32 operands as three bf16 parts (24 bits).  States,
- *   rate gradients, and outputs before their one rounding are as exact as fp32 arithmetic gives.  Tokens are taken 64 at a time: a NaN
- *   or an infinity in a token or rate may also reach the rows before it in its chunk of 64 (of
- *   that sequence; of its own column of v only, where it stands in v).
+ *   rate gradients, and outputs before their one rounding are as exact as fp32 arithmetic gives.
+ *   Tokens are taken 64 at a time: a NaN or an infinity in a token or rate may also reach the rows
+ *   before it in its chunk of 64 (of that sequence; of its own column of v only, where it stands in v).
  * Deterministic: the same inputs give the same bits.  n <= 2^31 - 65; chunks x H, sequences x H x
  *   dv/16 and (one token) rows x H x dv/64 below 2^23; in the chunked calls 64 rows span < 2 GiB.
  */

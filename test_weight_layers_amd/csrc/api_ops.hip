@@ -93,10 +93,12 @@ struct DeltaPlan {
 // Segments that the chunks of a sequence are cut in (1: none), from what the states of a chunk take where
 // the order of the chunks bounds them (us), half as much again for their gradients (whose workgroups run
 // beside the states'), how many workgroups run at once on 256 CUs of one or two each, and what a further
-// segment (its start) and the second launch cost.  Measured with and without: 687 chunks x 4 heads of 256
-// 1680 and 910 us (5 segments), 313 x 2 heads of 128 477 and 110 (16), the gradient call over 94 232 and
-// 118 (12); not taken for 9 sequences of 35 chunks x 2 heads of 128 (66, with 3 74).  (Without rounding per / s up the number never falls as rows are
-// added, so that a workspace for more rows of as many sequences serves fewer.)
+// segment (its start) and the second launch cost.  Whole calls without and with: 687 chunks x 4 heads of 256
+// 2054 and 1051 us (5 segments), 313 x 2 heads of 128 518 and 122 (17), the gradient over 94 232 and 122; not
+// taken for 9 sequences of 35 chunks x 2 heads of 128 (82, with 3 89).  (Without rounding per / s up the number
+// never falls as rows are added, so that a workspace for more rows of as many sequences serves fewer.)
+// The lengths are on the device, so the rule goes by the mean: a long sequence packed with enough short ones
+// runs uncut, in the time of its own chunks.
 int delta_segments(int H, int dk, int dv, int64_t nc, int64_t nseq, bool bf16, bool backward) {
   const int slices = dv / kDeltaSlice, size = dk == 64 ? 0 : dk == 128 ? 1 : 2;
   const int64_t wgs = nseq * H * slices, per = (nc + nseq - 1) / nseq;

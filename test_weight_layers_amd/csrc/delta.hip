@@ -86,7 +86,7 @@ constexpr int kZeroBlocks = 64;     // workgroups of the chunk kernel's launch t
 // One workgroup per chunk and head: e^gamma, T = (I + L)^-1 by block substitution in fp32 and A,
 // and (once per key head) the tokens and their transposes in fragment order.
 // Substitution, not products of powers of L: those grow without bound where keys repeat.
-// 687 chunks of 4 heads of 256, bf16: 99 us for 565 MB, 5.7 TB/s, a copy reaches 5.1; 22 chunks 14.7 us,
+// 687 chunks of 4 heads of 256, bf16: 99 us for 588 MB, 5.9 TB/s, a copy reaches 5.1; 22 chunks 14.9 us,
 // the latency of the loads and the substitution.
 template <typename T, int DK, bool BWD>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_chunk_kernel(DeltaParams p) {

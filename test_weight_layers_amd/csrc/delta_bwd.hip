@@ -229,7 +229,7 @@ __device__ __forceinline__ void delta_gstates(const DeltaParams &p, GradLds<T, D
 // The states and their gradients do not depend on one another (but for M, which the first launch leaves to the
 // second): one launch for both, the gradients' workgroups, which take longer, first.  8 sequences of 16
 // chunks, 6 heads of 128: 110 us for 768 workgroups, two to a CU (132 one after the other); 6 ragged
-// sequences, 4 heads of 64, fp32: 68 (86).
+// sequences, 4 heads of 64, fp32: 69 (86).  fp32 heads of 256 whole take all 256 registers and spill 2.
 template <typename T, int DK, int PART>
 __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delta_chain_kernel(DeltaParams p, int grads) {
   union Lds {
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && DK <= 128 ? 4 : 2) void delt
 // row tile w % 4 and half of the column tiles), which pass through LDS and are read both ways round,
 // then dq and dk: wave w has the rows of half w / 4 and every fourth 16-wide column tile.  Operands
 // come from memory in fragment order; bound by their latency, so registers are kept few enough for
-// four waves a SIMD (one wave of 4 x 2 tiles a SIMD took 175 us where this takes 120 for 128 chunks
+// four waves a SIMD (one wave of 4 x 2 tiles a SIMD took 175 us where this takes 123 for 128 chunks
 // of 6 heads of 128; of that its 278 MB are 55 us at a copy's rate, the products 15 and the vector
 // operations 30.  Two column tiles at once, two fifths fewer operand loads, took as long).
 template <typename T, int DK>

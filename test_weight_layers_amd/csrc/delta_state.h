@@ -22,8 +22,8 @@ constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 
 // so two waves share a SIMD and one works while the other waits or loads.  Tokens and chunk terms
 // go from memory straight into operand registers (each is used once), the next chunk's as soon
 // as this chunk's have been used, Q into the registers that K leaves, A into those of T.  Bound by the
-// order of the chunks: 2.45 us each, heads of 256, of which the matrix cores work 0.5 and the operands,
-// 138 KB, take 0.9 at the 64 bytes a clock of a CU; the rest is the three exchanges, one after another.
+// order of the chunks: 2.85 us each, heads of 256, of which the matrix cores work 0.6 and the operands,
+// 146 KB, take 1.0 at the 64 bytes a clock of a CU; the rest is the three exchanges, one after another.
 // BWD writes the states and U that the gradient needs, in place of the outputs.
 //
 // Where sequences are long and few, the chunks of one are cut in segments that run at once (the state is
@@ -32,8 +32,8 @@ constexpr int64_t kSquare = C * C * 2 * kFull;      // bytes of a split 64 x 64 
 //   kFirst: the first segment, outputs and all; U and M of the others but the last, of which M is
 //           dk / 16 more slices of rows
 //   kSecond: the others, each from its own starting state, (W_1 M_1 + U_1) M_2 + U_2 ..
-// 687 chunks of 4 heads of 256: 1680 us whole, 521 + 388 in five segments (448 and 256 workgroups; a CU's
-// two then take 3.9 us a chunk).
+// 687 chunks of 4 heads of 256: 1955 us whole, 558 + 465 in five segments (448 and 256 workgroups; a CU's
+// two then take 4.0 us a chunk).
 // `id` of `count`: this workgroup among those that do this.
 template <typename T, int DK, bool BWD> struct StateLds {
   SplitTile<kFull, SL, DK> w[2];

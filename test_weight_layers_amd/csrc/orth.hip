@@ -20,8 +20,9 @@
 // copies tiles from memory straight into LDS.  Every product is C[i][j] = sum_k P[i][k] Q[j][k]
 // of row panels: X X^T, A A (A is symmetric) and B X from the stored X^T; A and B are
 // symmetric, so only their tiles on and below the diagonal are computed.  Bound by the matrix cores
-// where matrices are large: 4 x 4096 x 1024 bf16, five steps, 279 GFLOP (571 with the parts, tiles above the
-// diagonal left out) in 751 us, 760 TFLOP/s; small ones by their 17 launches: 12 x 512 x 256 fp32 119 us.
+// where matrices are large: 4 x 4096 x 1024 bf16, five steps, 279 GFLOP (805 with the parts, tiles above the
+// diagonal left out) in 895 us, 900 TFLOP/s (B X about 1000, A 640 and B 510, whose 144 tiles leave 112 of the
+// CUs out); small ones by their 17 launches: 12 x 512 x 256 fp32 119 us.
 // Sizes are padded with zeros to whole tiles.
 #include <type_traits>
 
@@ -250,6 +251,8 @@ __global__ __launch_bounds__(G::kThreads, G::kThreads / 256) void orth_product_k
     for (int j = 0; j < G::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   // The products of low parts in sums of their own, where registers allow it: a large sum then is rounded
   // once a stage, not three times (2 x 36 x 1216 fp32: 3.2e-6 -> 2.2e-6 off, 2 x 1300 x 1200 2.1e-6 -> 1.2e-6).
+  // Tiles of 256, whose sums take half of the registers, go without: 4 x 4096 x 1024 fp32 1.4e-6 off and 2 x 2000 x
+  // 3900 1.8e-6, where fp32 arithmetic is 3.7e-6 and 4.4e-6.
   constexpr bool kLow = PA == 2 && PB == 2 && G::TM <= 128;
   f32x4 low[kLow ? G::FM : 1][kLow ? G::FN : 1];
 #pragma unroll
@@ -649,7 +652,8 @@ OrthPlan plan_orth(int rows, int cols, int batch, bool bf16) {
   q.tile = tiles(256) >= 200 && fits(256) ? 256 : (tiles(128) >= 200 && fits(128) ? 128 : 64);
   const int64_t nr = up(q.r, 128) / 128;
   q.tile_sym = batch * (nr * (nr + 1) / 2) >= 100 && fits(128) ? 128 : 64;
-  // one tile of rows, and few enough of columns that every workgroup sums all of theirs: a launch a step
+  // one tile of rows, and few enough of columns that every workgroup sums all of theirs: a launch a step (1 x 64 x
+  // 8192 fp32 139 us; as larger matrices are done, 1 x 64 x 8200 362)
   q.narrow = q.r <= 64 && q.c <= 8192;
   if (q.narrow) q.tile = q.tile_sym = 64;
   const int pad = q.tile > q.tile_sym ? q.tile : q.tile_sym;

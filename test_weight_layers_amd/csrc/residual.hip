@@ -3,9 +3,9 @@
 // rms(a) = sqrt(mean(a^2) + eps), over groups of `norm` channels for o (a head, or the row).
 // Bound by memory: a row stays in registers between its two reductions (8 channels a lane and
 // vector), every tensor is read or written once.  Sums of squares, the gates and y up to h are
-// fp32; y and h are rounded once, at their stores.  Measured, bf16: 137400 rows of 1024 1.41 GB in 260 us
-// (5.4 TB/s; a copy reaches 5.1), the gradient of 43968 rows 0.72 GB in 153 us (4.7 TB/s); fp32, 8192
-// rows of 768 without z 151 MB in 32 us and 5 more for the sums over rows; 1374 rows 7 us, a launch.
+// fp32; y and h are rounded once, at their stores.  Measured, bf16: 137400 rows of 1024 1.41 GB in 268 us
+// (5.2 TB/s; a copy reaches 5.1), the gradient of 43968 rows 0.72 GB in 155 us (4.6 TB/s); fp32, 8192
+// rows of 768 without z 151 MB in 32 us and 5 more for the sums over rows; 1374 rows 8 us, a launch.
 //
 // Gradient (gy, gh given; y is the stored output; r = 1 / rms):
 //   t = gh gamma_next,  yn = y r2,   gx = gy + r2 (t - yn mean(t yn))
