@@ -411,6 +411,123 @@ int ttt_orthogonalise(int32_t rows, int32_t cols, int32_t batch, const void *g, 
                       void *out, int64_t ld_out, int64_t bs_out, int32_t steps, int32_t dtype,
                       void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Windowed attention: softmax attention over packed sequences where a query sees the blocks around its own, and the
+ * first keys.  [LoGeR]'s attention over the previous and the current chunk, [ZipMap]'s local window attention and the
+ * per-frame attention of all these models (block = tokens of a frame; before = after = 0: the frame itself), beside the
+ * fast-weight layer that carries the rest.
+ *
+ * A sequence has Lq query and Lk key rows; query i stands at position p = i + Lk - Lq (the queries are the last
+ * rows), in block b = floor(p / block).  Key j is visible iff
+ *   j < (b + after + 1) * block  and  (j >= (b - before) * block  or  j < sinks);
+ * before, after < 0: no limit on that side.  Over the visible keys
+ *   s_ij = scale q_i k_j,  lse_i = ln sum_j e^s_ij,  o_i = sum_j e^(s_ij - lse_i) v_j.
+ * A query that sees no key has o = 0, lse = -infinity and no gradient.
+ *
+ * Shapes.  heads H, key_heads Hk with H % Hk == 0 (head h uses key head h / (H / Hk)); d in {64, 128, 256}.
+ *   q, o: rows of H*d columns; k, v: Hk*d (row conventions above; 64 rows span < 2 GiB).  lse: fp32 [H][nq].
+ * cu_seqlens, cu_seqlens_k: int32 DEVICE, [sequences + 1] row offsets of q and of k, v (cu_seqlens_k NULL: those of
+ *   q), or both NULL (one sequence of all rows).  Read on the device, clamped to the rows and to a running maximum.
+ *   Rows of no sequence are not read; their o is left as it was, or set to zero with TTT_ATTENTION_ZERO_UNUSED; their
+ *   lse is -infinity and their gradients are zero.
+ * Precision: fp32 scores, statistics and sums (a q k beyond fp32's range is infinite).  bf16: the probabilities (and dS) are rounded once to bf16 as operands
+ *   of the second products.  fp32: fp32 products.
+ *   The gradient takes e^(s - lse) from an fp32 lse: its relative error grows as |lse| 2^-24.
+ * A value that is not finite reaches only rows that see its key.  Deterministic: the same inputs give the same bits.
+ * n <= 2^31 - 65; tiles x heads (x ranges of keys or queries) below 2^23.
+ */
+enum { TTT_ATTENTION_ZERO_UNUSED = 1 };
+/* Bytes of workspace of ttt_window_attention (backward = 0) or its gradient (backward = 1) for these shapes. */
+int ttt_window_attention_workspace_bytes(int32_t heads, int32_t key_heads, int32_t d, int64_t nq, int64_t nk,
+                                         int32_t sequences, int32_t block, int32_t before, int32_t after,
+                                         int32_t sinks, int32_t dtype, int32_t backward, size_t *bytes);
+/* scale: finite, > 0.  lse may be NULL.  o must not overlap q, k or v. */
+int ttt_window_attention(int32_t heads, int32_t key_heads, int32_t d, const void *q, int64_t ld_q,
+                         const void *k, int64_t ld_k, const void *v, int64_t ld_v, void *o, int64_t ld_o, float *lse,
+                         int64_t nq, int64_t nk, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
+                         int32_t sequences, int32_t block, int32_t before, int32_t after, int32_t sinks, float scale,
+                         int32_t dtype, uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);
+/* Gradient, from the forward's o and lse.  grad_q, grad_k, grad_v: rows like q, k, v (a key head's gradient sums the
+ * heads that share it).  No output may overlap an input or another output. */
+int ttt_window_attention_backward(int32_t heads, int32_t key_heads, int32_t d, const void *q, int64_t ld_q,
+                                  const void *k, int64_t ld_k, const void *v, int64_t ld_v, const void *o,
+                                  int64_t ld_o, const float *lse, const void *grad_o, int64_t ld_grad_o,
+                                  void *grad_q, int64_t ld_grad_q, void *grad_k, int64_t ld_grad_k, void *grad_v,
+                                  int64_t ld_grad_v, int64_t nq, int64_t nk, const int32_t *cu_seqlens,
+                                  const int32_t *cu_seqlens_k, int32_t sequences, int32_t block, int32_t before,
+                                  int32_t after, int32_t sinks, float scale, int32_t dtype, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+/* One token for each of n rows, over rolling caches of keys and values.
+ * k_cache, v_cache: [pool] caches of `capacity` rows of Hk*d columns, ld_cache elements from row to row and pool_stride
+ *   from cache to cache; position x of a sequence stands in row x (x < sinks) or sinks + (x - sinks) mod (capacity -
+ *   sinks) of its cache.  capacity > sinks.
+ * slots: int32 DEVICE, the cache of each row (NULL: row i has cache i, n <= pool); positions: int32 DEVICE, the position
+ *   of each row's token.  The token sees itself and the earlier positions that are visible as above (without `after`)
+ *   and still in the cache; then its k and v are written to its place.
+ * The rows of a call read the caches as they were before it; where several name one place of a cache the last one's
+ * token stays.  A row whose slot is outside [0, pool) or whose position is negative is padding: nothing is read or
+ * written for it (TTT_ATTENTION_ZERO_UNUSED sets its o to zero).  Nothing may overlap the caches or o.
+ * n^2 <= 2^42 with slots (the later rows of one place are found by comparing all). */
+int ttt_window_attention_step_workspace_bytes(int32_t heads, int32_t key_heads, int32_t d, int64_t n,
+                                              int32_t capacity, int32_t dtype, size_t *bytes);
+int ttt_window_attention_step(int32_t heads, int32_t key_heads, int32_t d, void *k_cache, void *v_cache,
+                              int64_t ld_cache, int64_t pool_stride, int32_t pool, int32_t capacity,
+                              const int32_t *slots, const int32_t *positions, const void *q, int64_t ld_q,
+                              const void *k, int64_t ld_k, const void *v, int64_t ld_v, void *o, int64_t ld_o,
+                              int64_t n, int32_t block, int32_t before, int32_t sinks, float scale, int32_t dtype,
+                              uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ttt_layer_norm -- y = gamma (x - mean) / sqrt(var + eps) + beta over groups of norm_width columns: the norm before
+ * attention and MLP, and the one of every head's q and k that [VGG-T3] 关键设计 1 starts from (norm_width = d).
+ *
+ * x, y    : [n][ld] device rows, `dtype`, columns [0, channels); y may be x (same pointer and row stride), no other
+ *           overlap.
+ * gamma, beta: [norm_width] fp32, device, 16-byte aligned, shared by the groups; NULL: 1 and 0.
+ * Requires 1 <= norm_width <= 8192, channels % norm_width == 0, and norm_width % 8 == 0 where there is more than one
+ * group; the row alignment of the conventions above.  Statistics in fp32, from what is left of x after its mean.
+ */
+int ttt_layer_norm(int32_t channels, int32_t norm_width, const void *x, int64_t ld_x, const float *gamma,
+                   const float *beta, float eps, void *y, int64_t ld_y, int64_t n, int32_t dtype, void *stream);
+/* Gradient: grad_x rows (may be grad_y; no other overlap); grad_gamma, grad_beta: [norm_width] fp32, each may be
+ * NULL, summed over rows and groups in a fixed order. */
+int ttt_layer_norm_backward_workspace_bytes(int32_t channels, int32_t norm_width, int64_t n, size_t *bytes);
+int ttt_layer_norm_backward(int32_t channels, int32_t norm_width, const void *grad_y, int64_t ld_grad_y,
+                            const void *x, int64_t ld_x, const float *gamma, float eps, void *grad_x,
+                            int64_t ld_grad_x, float *grad_gamma, float *grad_beta, int64_t n, int32_t dtype,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ttt_adamw_step -- one AdamW step over many tensors, for the outer weights that ttt_orthogonalise does not step:
+ *   m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2   (g: the gradient times *grad_scale, where that is given)
+ *   w <- w (1 - lr weight_decay) - lr / (1 - b1^step) m / (sqrt(v) / sqrt(1 - b2^step) + eps)
+ *
+ * tensors : HOST table, read before the call returns.  param, grad: `dtype`; master: the fp32 weights that are stepped
+ *           and then rounded to param, or NULL (param itself is stepped); all tensors of a call with or without.
+ *           Pointers need the alignment of their elements only; 16 bytes (8-bit states: 8) are faster.
+ * bits    : 32 (exp_avg, exp_avg_sq fp32) or 8: exp_avg int8 [n], exp_avg_sq uint8 [n], with a scale s for each 256
+ *           elements in exp_avg_scale, exp_avg_sq_scale (fp32 [ceil(n / 256)]):  m = s c |c| / 127^2, s = max |m|;
+ *           sqrt(v) = s (c / 255)^2, s = max sqrt(v); codes c to the nearest root.  Zeros are the state to start from.
+ *           An infinity or a NaN in a gradient makes its block's state one.
+ * step    : >= 1, counted from 1; step_device (int64 DEVICE, may be NULL) replaces it, and lr_device (fp32 DEVICE,
+ *           may be NULL) lr, at the time the kernels run (for captured steps).
+ * workspace: 16 bytes DEVICE (256-byte aligned) where step_device or lr_device is given; else may be NULL.
+ * ttt_adamw_check refuses a table whose written arrays overlap one another or a gradient; the step does not look.
+ */
+typedef struct {
+  void *param;
+  const void *grad;
+  void *exp_avg, *exp_avg_sq;
+  float *exp_avg_scale, *exp_avg_sq_scale;   /* bits = 8, else NULL */
+  float *master;
+  int64_t n;
+} ttt_adamw_tensor;
+int ttt_adamw_check(const ttt_adamw_tensor *tensors, int32_t count, int32_t bits, int32_t dtype);
+int ttt_adamw_step(const ttt_adamw_tensor *tensors, int32_t count, int64_t step, const int64_t *step_device, double lr,
+                   const float *lr_device, double beta1, double beta2, double eps, double weight_decay,
+                   const float *grad_scale, int32_t bits, int32_t dtype, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
 /*
  * Process-wide tuning / testing switches.
  *   TTT_OPT_FORCE_GENERAL: value != 0 routes every call through the general
@@ -436,7 +553,8 @@ int ttt_set_option(int32_t option, int64_t value);
 typedef enum {
   TTT_K_CONV = 0, TTT_K_CAST = 1, TTT_K_GRAD = 2, TTT_K_REDUCE = 3,
   TTT_K_NS = 4, TTT_K_APPLY = 5, TTT_K_GATE = 6,
-  TTT_K_DELTA = 7, TTT_K_RESIDUAL = 8, TTT_K_ORTH = 9, TTT_K_COUNT = 10
+  TTT_K_DELTA = 7, TTT_K_RESIDUAL = 8, TTT_K_ORTH = 9,
+  TTT_K_ATTENTION = 10, TTT_K_NORM = 11, TTT_K_ADAMW = 12, TTT_K_COUNT = 13
 } ttt_kernel_kind;
 int ttt_profile_enable(int32_t on);
 int ttt_profile_reset(void);

@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libttt.so")
 SOURCES = ("grad.hip", "apply.hip", "ns.hip", "conv.hip", "gate.hip", "bigd.hip", "probe.hip",
-           "delta.hip", "delta_bwd.hip", "residual.hip", "orth.hip", "api.hip", "api_ops.hip")
+           "delta.hip", "delta_bwd.hip", "residual.hip", "orth.hip", "attention.hip",
+           "attention_bwd.hip", "attention_step.hip", "norm.hip", "adamw.hip", "api.hip", "api_ops.hip", "api_block.hip")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc" if os.path.exists("/opt/rocm/bin/hipcc") else "hipcc")
 FLAGS = [

@@ -1,0 +1,73 @@
+// Windowed attention: parameters of the launchers in attention.hip, attention_bwd.hip and attention_step.hip.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ttt {
+
+constexpr int kAttnLaneSeqs = 63;   // up to here every wave lays the sequences out for itself
+
+// One packed sequence: its query and key rows, its first query and key tile.
+struct AttnSeq {
+  int qs, ql, ks, kl, qt0, kt0;
+};
+
+struct AttnParams {
+  const void *q, *k, *v;            // rows [n][ld]: heads * d, key_heads * d columns
+  int64_t ldq, ldk, ldv;
+  void *o;
+  int64_t ldo;
+  float *lse;                       // [heads][nq]
+  int nq, nk, nseq;
+  const int *cu_q, *cu_k;           // [nseq + 1]; both null: one sequence of all rows
+  int heads, key_heads, d;
+  int block, before, after, sinks;  // before, after < 0: no limit
+  float scale;
+  bool zero_unused;
+  AttnSeq *seqs;                    // [nseq + 1], more than kAttnLaneSeqs sequences
+  int qrows, krows;                 // rows of a query tile and of a key tile
+  int qtiles, ktiles;               // at most so many
+  // forward: the keys of a tile in `splits` ranges, joined from these
+  int splits;
+  float *part_o;                    // [splits][heads][nq][d]
+  float2 *part_ml;                  // [splits][heads][nq]
+  // backward
+  const void *go;
+  int64_t ldgo;
+  void *gq, *gk, *gv;
+  int64_t ldgq, ldgk, ldgv;
+  float *delta;                     // [heads][nq]
+  int parts, sink_parts, sink_tiles;// ranges of a key tile's queries; of a sink tile's beyond the window; tiles of sinks
+  float *part;                      // [parts][nk][key_heads][2][d], parts > 1
+  float *spart;                     // [nseq][sink_tiles][key_heads][1 + sink_parts][krows][2][d]
+};
+
+struct AttnStepParams {
+  void *kc, *vc;                    // [pool] caches of [capacity][ld] rows, `pool_stride` elements apart
+  int64_t ldc, pool_stride;
+  const int *slots, *positions;     // slots may be null (row i: cache i)
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv;
+  void *o;
+  int64_t ldo;
+  int n, pool, capacity, heads, key_heads, d;
+  int block, before, sinks;
+  float scale;
+  bool zero_unused;
+  int splits;
+  float *part_o;                    // [splits][n][heads][d]
+  float2 *part_ml;                  // [splits][n][heads]
+};
+
+// Rows of the tiles that the launchers use.
+int attn_query_rows(int d, bool bf16, bool small);
+int attn_grad_query_rows(int d, bool bf16);
+int attn_grad_key_rows(int d, bool bf16);
+hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s);
+hipError_t launch_attention_backward(const AttnParams &p, bool bf16, hipStream_t s);
+hipError_t launch_attention_step(const AttnStepParams &p, bool bf16, hipStream_t s);
+// Lays out more than kAttnLaneSeqs sequences (p.seqs).
+hipError_t launch_attention_plan(const AttnParams &p, hipStream_t s);
+
+}  // namespace ttt

@@ -1,0 +1,329 @@
+// Windowed attention over packed sequences: one pass over the keys with a running maximum and sum.
+//   s_ij = scale q_i k_j over the keys that i sees,  o_i = sum_j e^(s_ij - lse_i) v_j,  lse_i = ln sum_j e^s_ij
+// See attn_tile.h for the orientation of the products and attention.h for the parameters.
+#include "attn_tile.h"
+
+namespace ttt {
+namespace {
+
+constexpr int kZeroBlocks = 32;     // workgroups that fill rows of no sequence
+
+// Four waves of NC x 16 queries each; BK keys at a time through two LDS buffers.
+template <typename T, int D, int NC, int BK>
+__global__ __launch_bounds__(256) void attn_forward_kernel(AttnParams p) {
+  typedef AttnTile<T, D> Tile;
+  typedef typename FragOf<T>::type Frag;
+  constexpr int NK = D / 32, ND = D / 16, NU = BK / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
+  __shared__ __attribute__((aligned(256))) unsigned char s_k[2][kTile], s_v[2][kTile];
+  const int items = p.qtiles * p.heads * p.splits;
+  if ((int)blockIdx.x >= items) {
+    const int blk = blockIdx.x - items;
+    const int2 used = used_rows<false>(p);
+    if (p.zero_unused) zero_unused_rows<T>(used, p.nq, p.o, p.ldo, p.heads * D, blk, kZeroBlocks);
+    if (p.lse)
+      for (int h = 0; h < p.heads; ++h)
+        for (int64_t i = blk * 256 + threadIdx.x; i < used.x + (int64_t)(p.nq - used.y); i += kZeroBlocks * 256)
+          p.lse[(int64_t)h * p.nq + (i < used.x ? i : used.y + (i - used.x))] = -__builtin_inff();
+    return;
+  }
+  const int item = attn_item(blockIdx.x, items), split = item % p.splits, rest = item / p.splits;
+  const int h = rest / p.qtiles, kh = h / (p.heads / p.key_heads);
+  AttnSeq s;
+  int tile, seq;
+  // late tiles first: without a window they see the most keys
+  if (!tile_of<false>(p, p.qtiles - 1 - rest % p.qtiles, &s, &tile, &seq)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g = l >> 4, li = l & 15;
+  const int t0 = tile * QR, row0 = t0 + wave * 16 * NC;
+  const T *kb = static_cast<const T *>(p.k) + (int64_t)s.ks * p.ldk + kh * D;
+  const T *vb = static_cast<const T *>(p.v) + (int64_t)s.ks * p.ldv + kh * D;
+
+  Frag q[NC][NK];
+  own_rows<T, D, NC>(q, static_cast<const T *>(p.q) + (int64_t)s.qs * p.ldq + h * D, p.ldq, row0, s.ql);
+  int lo[NC], hi[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int i = row0 + 16 * c + li;
+    const int2 r = i < s.ql ? seen_keys(p, s, i) : int2{0, 0};
+    lo[c] = r.x, hi[c] = r.y;
+  }
+  // the workgroup's keys: sinks [0, se) and the window [k0, k1); this wave's: from its first and last row
+  const int last = t0 + QR < s.ql ? t0 + QR : s.ql, wlast = row0 + 16 * NC < s.ql ? row0 + 16 * NC : s.ql;
+  const int k0 = seen_keys(p, s, t0).x, k1 = seen_keys(p, s, last - 1).y, se = p.sinks < k0 ? p.sinks : k0;
+  const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
+  const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
+  const int first = (int)((int64_t)nt * split / p.splits), end = (int)((int64_t)nt * (split + 1) / p.splits);
+  const auto range = [&](int t) {
+    const int j = t < ns ? t * BK : k0 + (t - ns) * BK, e = t < ns ? se : k1;
+    return int2{j, j + BK < e ? j + BK : e};
+  };
+  const auto fetch = [&](int t) {
+    const int2 r = range(t);
+    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, s_k[t & 1]);
+    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, s_v[t & 1]);
+  };
+
+  const float c2 = p.scale * kLog2e;
+  f32x4 o[ND][NC];
+  float m[NC], sum[NC];
+  bool huge = false;
+  // A second pass where the first left an infinity or a NaN: a value of v that is not finite reaches, as a zero times it,
+  // rows that do not see its key.  In tiles that are not seen whole it is then added to those that see it and removed.
+  for (int careful = 0; careful < 2; ++careful) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      m[c] = -__builtin_inff(), sum[c] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d][c] = zero_f4();
+    }
+    __syncthreads();
+    if (first < end) fetch(first);
+    for (int t = first; t < end; ++t) {
+      __syncthreads();                                // this tile has landed, and nobody reads the other buffer
+      if (t + 1 < end) fetch(t + 1);
+      const int2 r = range(t);
+      const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
+      const bool none = !(r.x < wb.y && (r.y > wa.x || r.x < p.sinks));
+      const unsigned char *kt = s_k[t & 1];
+      unsigned char *vt = s_v[t & 1];
+      Frag pr[NU / 2][NC];
+      if (!none) {
+        f32x4 sc[NU][NC];
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) sc[u][c] = zero_f4();
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            const Frag a = Tile::rows(kt, 16 * u + li, 32 * k + 8 * g);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) sc[u][c] = mma(a, q[c][k], sc[u][c]);
+          }
+        }
+        if (!full) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int e = hi[c] < r.y ? hi[c] : r.y;
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int j = r.x + 16 * u + 4 * g + x;
+                if (!(j < e && (j >= lo[c] || j < p.sinks))) sc[u][c][x] = -__builtin_inff();
+              }
+          }
+        }
+        float mx[NC];
+        bool up = false;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          mx[c] = -__builtin_inff();
+#pragma unroll
+          for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mx[c] = fmaxf(mx[c], sc[u][c][x]);
+          mx[c] = fmaxf(mx[c], __shfl_xor(mx[c], 16));
+          mx[c] = fmaxf(mx[c], __shfl_xor(mx[c], 32));
+          up |= (mx[c] - m[c]) * c2 > 8.0f;
+        }
+        // the sums are kept relative to m, which follows a column's maximum only where that grew by more than 2^8: P
+        // stays below 2^8, which costs no digits
+        if (__any(up)) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float to = (mx[c] - m[c]) * c2 > 8.0f ? mx[c] : m[c], a = to == m[c] ? 1.0f : __builtin_amdgcn_exp2f((m[c] - to) * c2);
+            m[c] = to, sum[c] *= a;
+            huge |= fabsf(to) * c2 > kHuge && to > -__builtin_inff();
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d][c] *= a;
+          }
+          huge = __any(huge);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float top = m[c] == -__builtin_inff() ? 0.0f : m[c];
+          float base = -top * c2;
+          if (huge) {                                 // in some column: there the maximum is taken off first
+            const bool off = fabsf(base) > kHuge;
+            base = off ? 0.0f : base;
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) sc[u][c][x] -= off ? top : 0.0f;
+          }
+#pragma unroll
+          for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              sc[u][c][x] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][c][x], c2, base));
+              sum[c] += sc[u][c][x];
+            }
+#pragma unroll
+          for (int u = 0; u < NU; u += 2) pr[u / 2][c] = pack44<T>(sc[u][c], sc[u + 1][c]);
+        }
+      }
+      if (careful) {
+        const bool whole = r.y - r.x == BK && seen_keys(p, s, t0).y >= r.y && (seen_keys(p, s, last - 1).x <= r.x || r.y <= p.sinks);
+        if (!whole) {
+          if (!none)
+            for (int x = 0; x < BK; ++x) {
+              const int j = r.x + x;
+#pragma unroll
+              for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const float f = to_f32(*reinterpret_cast<const T *>(vt + Tile::elem(x, 16 * d + 4 * g + y)));
+                  if (fabsf(f) < __builtin_inff()) continue;
+#pragma unroll
+                  for (int c = 0; c < NC; ++c)
+                    if (j < r.y && j < hi[c] && (j >= lo[c] || j < p.sinks)) o[d][c][y] += f;
+                }
+            }
+          __syncthreads();
+          Tile::settle(vt, 0, BK);
+          __syncthreads();
+        }
+      }
+      if (!none) {
+#pragma unroll
+        for (int u = 0; u < NU / 2; ++u)
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const Frag a = Tile::cols(vt, 32 * u, 16 * d);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[d][c] = mma(a, pr[u][c], o[d][c]);
+          }
+      }
+    }
+    bool odd = false;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) odd |= !(fabsf(o[d][c][x]) < __builtin_inff());
+    if (!__syncthreads_or(odd)) break;
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    sum[c] += __shfl_xor(sum[c], 16);
+    sum[c] += __shfl_xor(sum[c], 32);
+    const int i = row0 + 16 * c + li;
+    if (i >= s.ql) continue;
+    const bool empty = hi[c] == lo[c] && (p.sinks == 0 || lo[c] == 0);
+    const int64_t row = s.qs + i;
+    if (p.splits > 1) {
+      const int64_t at = ((int64_t)split * p.heads + h) * p.nq + row;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) store4(p.part_o + at * D + 16 * d + 4 * g, o[d][c]);
+      if (g == 0) p.part_ml[at] = float2{m[c], empty ? -1.0f : sum[c]};
+      continue;
+    }
+    const float inv = empty ? 0.0f : 1.0f / sum[c];
+    T *out = static_cast<T *>(p.o) + row * p.ldo + h * D + 4 * g;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) store4(out + 16 * d, o[d][c] * inv);
+    if (p.lse && g == 0)
+      p.lse[(int64_t)h * p.nq + row] = empty ? -__builtin_inff() : (m[c] * c2 + __builtin_amdgcn_logf(sum[c])) * kLn2;
+  }
+}
+
+// Joins the splits, in their order: D / 4 lanes a row and head.
+template <typename T, int D> __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
+  constexpr int L = D / 4;
+  const int64_t at = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int c = threadIdx.x % L;
+  const int2 used = used_rows<false>(p);
+  if (at >= (int64_t)p.nq * p.heads) return;
+  const int h = (int)(at % p.heads);
+  const int64_t row = at / p.heads, step = (int64_t)p.heads * p.nq, first = (int64_t)h * p.nq + row;
+  if (row < used.x || row >= used.y) return;
+  const float c2 = p.scale * kLog2e;
+  float m = -__builtin_inff(), sum = 0.0f;
+  for (int i = 0; i < p.splits; ++i) m = fmaxf(m, p.part_ml[first + i * step].x);
+  f32x4 o = zero_f4();
+  bool empty = false;
+  for (int i = 0; i < p.splits; ++i) {
+    const float2 ml = p.part_ml[first + i * step];
+    empty |= ml.y < 0.0f;
+    const float w = ml.x == m ? 1.0f : __builtin_amdgcn_exp2f((ml.x - m) * c2);
+    sum += ml.y * w;
+    o += *reinterpret_cast<const f32x4 *>(p.part_o + (first + i * step) * D + 4 * c) * w;
+  }
+  const float inv = empty ? 0.0f : 1.0f / sum;
+  store4(static_cast<T *>(p.o) + row * p.ldo + h * D + 4 * c, o * inv);
+  if (p.lse && c == 0) p.lse[first] = empty ? -__builtin_inff() : (m * c2 + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// More sequences than a wave has lanes: one workgroup writes the table.
+__global__ __launch_bounds__(1024) void attn_plan_kernel(AttnParams p) {
+  __shared__ int s_a[1024], s_b[1024];
+  const int t = threadIdx.x;
+  int mq = 0, mk = 0, cq = 0, ck = 0;           // maxima and tile counts of all before
+  // an inclusive scan of two values over the workgroup
+  const auto scan = [&](int &a, int &b, bool sum) {
+    for (int d = 1; d < 1024; d <<= 1) {
+      __syncthreads();
+      s_a[t] = a, s_b[t] = b;
+      __syncthreads();
+      if (t < d) continue;
+      const int x = s_a[t - d], y = s_b[t - d];
+      a = sum ? a + x : (x > a ? x : a), b = sum ? b + y : (y > b ? y : b);
+    }
+    __syncthreads();
+    s_a[t] = a, s_b[t] = b;
+    __syncthreads();
+  };
+  // sequences in groups of 1023: the last lane has the next group's first offset
+  for (int b0 = 0; b0 <= p.nseq; b0 += 1023) {
+    const int i = b0 + t;
+    int q = i <= p.nseq ? attn_offset(p.cu_q, i, p.nq) : 0, k = i <= p.nseq ? attn_offset(p.cu_k, i, p.nk) : 0;
+    q = q > mq ? q : mq, k = k > mk ? k : mk;
+    scan(q, k, false);
+    const bool own = t < 1023 && i < p.nseq;
+    const int ql = own ? s_a[t + 1] - q : 0, kl = own ? s_b[t + 1] - k : 0;
+    mq = s_a[1023], mk = s_b[1023];
+    int tq = tiles_of(ql, p.qrows), tk = tiles_of(kl, p.krows);
+    const int wq = tq, wk = tk;
+    scan(tq, tk, true);
+    if (t < 1023 && i <= p.nseq) p.seqs[i] = AttnSeq{q, ql, k, kl, cq + tq - wq, ck + tk - wk};
+    cq += s_a[1023], ck += s_b[1023];
+    __syncthreads();
+  }
+}
+
+template <typename T, int D, int NC, int BK> hipError_t go(const AttnParams &p, hipStream_t s) {
+  const int items = p.qtiles * p.heads * p.splits;
+  hipLaunchKernelGGL((attn_forward_kernel<T, D, NC, BK>), dim3(items + (p.cu_q ? kZeroBlocks : 0)), dim3(256), 0, s, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1 || p.nq == 0) return e;
+  hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)(((int64_t)p.nq * p.heads + 1024 / D - 1) / (1024 / D))), dim3(256),
+                     0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int attn_query_rows(int d, bool bf16, bool small) { return small || (!bf16 && d == 256) ? 64 : 128; }
+
+hipError_t launch_attention_plan(const AttnParams &p, hipStream_t s) {
+  if (p.cu_q == nullptr || p.nseq <= kAttnLaneSeqs) return hipSuccess;
+  hipLaunchKernelGGL(attn_plan_kernel, dim3(1), dim3(1024), 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s) {
+  if (p.nq == 0) return hipSuccess;
+  const hipError_t e = launch_attention_plan(p, s);
+  if (e != hipSuccess) return e;
+  const bool small = p.qrows == 64;
+  if (bf16) {
+    if (p.d == 64) return small ? go<__bf16, 64, 1, 64>(p, s) : go<__bf16, 64, 2, 64>(p, s);
+    if (p.d == 128) return small ? go<__bf16, 128, 1, 64>(p, s) : go<__bf16, 128, 2, 64>(p, s);
+    return small ? go<__bf16, 256, 1, 32>(p, s) : go<__bf16, 256, 2, 32>(p, s);
+  }
+  if (p.d == 64) return small ? go<float, 64, 1, 32>(p, s) : go<float, 64, 2, 32>(p, s);
+  if (p.d == 128) return small ? go<float, 128, 1, 32>(p, s) : go<float, 128, 2, 32>(p, s);
+  return go<float, 256, 1, 32>(p, s);
+}
+
+}  // namespace ttt

@@ -1,0 +1,433 @@
+// Gradient of windowed attention, from the forward's lse and output:
+//   delta_i = sum_d do_id o_id,  P_ij = e^(s_ij - lse_i),  dS_ij = P_ij (do_i v_j - delta_i)
+//   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,   dv_j = sum_i P_ij do_i
+// Two kernels, each with its own rows' gradients in registers (the scores are computed twice; with one kernel
+// the other side's gradients would be added by atomics, in no fixed order): dq by query tile, dk and dv by key tile,
+// where the heads that share a key head follow one another in one sum.
+#include "attn_tile.h"
+
+namespace ttt {
+namespace {
+
+constexpr int kZeroBlocks = 64;
+
+// delta, D / 8 lanes a row and head; the workgroups behind write the zeros of rows of no sequence.
+template <typename T, int D> __global__ __launch_bounds__(256) void attn_delta_kernel(AttnParams p, int blocks) {
+  constexpr int L = D / 8;
+  const int2 used = used_rows<false>(p);
+  if ((int)blockIdx.x >= blocks) {
+    const int blk = blockIdx.x - blocks;
+    const int2 keys = used_rows<true>(p);
+    zero_unused_rows<T>(used, p.nq, p.gq, p.ldgq, p.heads * D, blk, kZeroBlocks);
+    zero_unused_rows<T>(keys, p.nk, p.gk, p.ldgk, p.key_heads * D, blk, kZeroBlocks);
+    zero_unused_rows<T>(keys, p.nk, p.gv, p.ldgv, p.key_heads * D, blk, kZeroBlocks);
+    return;
+  }
+  const int64_t at = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (at >= (int64_t)p.nq * p.heads) return;
+  const int h = (int)(at % p.heads), c = threadIdx.x % L;
+  const int64_t row = at / p.heads;
+  if (row < used.x || row >= used.y) return;
+  const auto a = ld8(static_cast<const T *>(p.go) + row * p.ldgo + h * D + 8 * c);
+  const auto b = ld8(static_cast<const T *>(p.o) + row * p.ldo + h * D + 8 * c);
+  float v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v += (float)a[i] * (float)b[i];
+#pragma unroll
+  for (int m = 1; m < L; m <<= 1) v += __shfl_xor(v, m);
+  if (c == 0) p.delta[(int64_t)h * p.nq + row] = v;
+}
+
+// Four waves of NC x 16 queries; BK keys at a time, 32 of them through the registers.
+template <typename T, int D, int NC, int BK>
+__global__ __launch_bounds__(256) void attn_dq_kernel(AttnParams p) {
+  typedef AttnTile<T, D> Tile;
+  typedef typename FragOf<T>::type Frag;
+  constexpr int NK = D / 32, ND = D / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
+  __shared__ __attribute__((aligned(256))) unsigned char s_k[2][kTile], s_v[2][kTile];
+  const int item = attn_item(blockIdx.x, p.qtiles * p.heads), h = item / p.qtiles, kh = h / (p.heads / p.key_heads);
+  AttnSeq s;
+  int tile, seq;
+  if (!tile_of<false>(p, p.qtiles - 1 - item % p.qtiles, &s, &tile, &seq)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g = l >> 4, li = l & 15;
+  const int t0 = tile * QR, row0 = t0 + wave * 16 * NC;
+  const T *kb = static_cast<const T *>(p.k) + (int64_t)s.ks * p.ldk + kh * D;
+  const T *vb = static_cast<const T *>(p.v) + (int64_t)s.ks * p.ldv + kh * D;
+  Frag q[NC][NK], go[NC][NK];
+  own_rows<T, D, NC>(q, static_cast<const T *>(p.q) + (int64_t)s.qs * p.ldq + h * D, p.ldq, row0, s.ql);
+  own_rows<T, D, NC>(go, static_cast<const T *>(p.go) + (int64_t)s.qs * p.ldgo + h * D, p.ldgo, row0, s.ql);
+  int lo[NC], hi[NC];
+  float lse[NC], delta[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int i = row0 + 16 * c + li;
+    const bool in = i < s.ql;
+    const int2 r = in ? seen_keys(p, s, i) : int2{0, 0};
+    lo[c] = r.x, hi[c] = r.y;
+    const int64_t at = (int64_t)h * p.nq + s.qs + i;
+    lse[c] = in ? p.lse[at] * -kLog2e : -__builtin_inff();
+    delta[c] = in ? p.delta[at] : 0.0f;
+  }
+  const int last = t0 + QR < s.ql ? t0 + QR : s.ql, wlast = row0 + 16 * NC < s.ql ? row0 + 16 * NC : s.ql;
+  const int k0 = seen_keys(p, s, t0).x, k1 = seen_keys(p, s, last - 1).y, se = p.sinks < k0 ? p.sinks : k0;
+  const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
+  const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
+  const auto range = [&](int t) {
+    const int j = t < ns ? t * BK : k0 + (t - ns) * BK, e = t < ns ? se : k1;
+    return int2{j, j + BK < e ? j + BK : e};
+  };
+  const auto fetch = [&](int t) {
+    const int2 r = range(t);
+    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, s_k[t & 1]);
+    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, s_v[t & 1]);
+  };
+  const float c2 = p.scale * kLog2e;
+  f32x4 dq[ND][NC];
+  for (int careful = 0; careful < 2; ++careful) {     // as in the forward, for k that is not finite
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int d = 0; d < ND; ++d) dq[d][c] = zero_f4();
+    __syncthreads();
+    if (nt > 0) fetch(0);
+    for (int t = 0; t < nt; ++t) {
+      __syncthreads();
+      if (t + 1 < nt) fetch(t + 1);
+      const int2 r = range(t);
+      const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
+      const bool none = !(r.x < wb.y && (r.y > wa.x || r.x < p.sinks));
+      unsigned char *kt = s_k[t & 1];
+      const unsigned char *vt = s_v[t & 1];
+#pragma unroll
+      for (int x0 = 0; x0 < BK; x0 += 32) {
+        Frag ds[NC];
+        if (!none) {
+          f32x4 sc[2][NC], dp[2][NC];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) sc[u][c] = dp[u][c] = zero_f4();
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+              const Frag a = Tile::rows(kt, x0 + 16 * u + li, 32 * k + 8 * g), b = Tile::rows(vt, x0 + 16 * u + li, 32 * k + 8 * g);
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+                sc[u][c] = mma(a, q[c][k], sc[u][c]);
+                dp[u][c] = mma(b, go[c][k], dp[u][c]);
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int e = hi[c] < r.y ? hi[c] : r.y;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][c][x], c2, lse[c]));
+                float v = pr * (dp[u][c][x] - delta[c]);
+                if (!full) {
+                  const int j = r.x + x0 + 16 * u + 4 * g + x;
+                  if (!(j < e && (j >= lo[c] || j < p.sinks))) v = 0.0f;
+                }
+                sc[u][c][x] = v;
+              }
+            ds[c] = pack44<T>(sc[0][c], sc[1][c]);
+          }
+        }
+        if (careful) {
+          const bool whole = r.y - r.x == BK && seen_keys(p, s, t0).y >= r.y && (seen_keys(p, s, last - 1).x <= r.x || r.y <= p.sinks);
+          if (!whole) {
+            __syncthreads();
+            Tile::settle(kt, x0, 32);
+            __syncthreads();
+          }
+        }
+        if (!none) {
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const Frag a = Tile::cols(kt, x0, 16 * d);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) dq[d][c] = mma(a, ds[c], dq[d][c]);
+          }
+        }
+      }
+    }
+    bool odd = false;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) odd |= !(fabsf(dq[d][c][x]) < __builtin_inff());
+    if (!__syncthreads_or(odd)) break;
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int i = row0 + 16 * c + li;
+    if (i >= s.ql) continue;
+    T *out = static_cast<T *>(p.gq) + (int64_t)(s.qs + i) * p.ldgq + h * D + 4 * g;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) store4(out + 16 * d, dq[d][c] * p.scale);
+  }
+}
+
+// Four waves of NC x 16 keys of a key head; BQ queries of one head at a time.
+template <typename T, int D, int NC, int BQ>
+__global__ __launch_bounds__(256) void attn_dkv_kernel(AttnParams p) {
+  typedef AttnTile<T, D> Tile;
+  typedef typename FragOf<T>::type Frag;
+  constexpr int NK = D / 32, ND = D / 16, kTile = BQ * Tile::kRow, KR = 64 * NC;
+  __shared__ __attribute__((aligned(256))) unsigned char s_q[2][kTile], s_o[2][kTile];
+  __shared__ __attribute__((aligned(256))) float s_lse[2][64], s_del[2][64];
+  const int window_items = p.ktiles * p.key_heads * p.parts, grp = p.heads / p.key_heads;
+  const bool sink_item = (int)blockIdx.x >= window_items;
+  AttnSeq s;
+  int tile, seq, kh, part, parts;
+  if (!sink_item) {
+    const int item = attn_item(blockIdx.x, window_items), rest = item / p.parts;
+    part = item % p.parts, parts = p.parts, kh = rest / p.ktiles;
+    if (!tile_of<true>(p, rest % p.ktiles, &s, &tile, &seq)) return;
+  } else {
+    const int item = attn_item(blockIdx.x - window_items, gridDim.x - window_items), rest = item / p.sink_parts;
+    part = item % p.sink_parts, parts = p.sink_parts, kh = rest % p.key_heads;
+    tile = rest / p.key_heads % p.sink_tiles, seq = rest / p.key_heads / p.sink_tiles;
+    s = seq_of(p, seq);
+    if (tile * KR >= s.kl) return;
+  }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g = l >> 4, li = l & 15;
+  const int t0 = tile * KR, row0 = t0 + wave * 16 * NC;
+  const int last = (t0 + KR < s.kl ? t0 + KR : s.kl) - 1, wlast = (row0 + 16 * NC < s.kl ? row0 + 16 * NC : s.kl) - 1;
+  Frag k[NC][NK], v[NC][NK];
+  own_rows<T, D, NC>(k, static_cast<const T *>(p.k) + (int64_t)s.ks * p.ldk + kh * D, p.ldk, row0, s.kl);
+  own_rows<T, D, NC>(v, static_cast<const T *>(p.v) + (int64_t)s.ks * p.ldv + kh * D, p.ldv, row0, s.kl);
+  // The queries that see key j: [x, y) in their window and, for a sink, all behind.
+  const bool with_sinks = (sink_item || p.sink_parts == 0) && p.before >= 0 && t0 < p.sinks;
+  int lo[NC], hi[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = row0 + 16 * c + li;
+    const int2 r = j < s.kl ? seeing_queries(p, s, j) : int2{0, 0};
+    lo[c] = r.x, hi[c] = r.y;
+  }
+  const int2 ta = seeing_queries(p, s, t0), tb = seeing_queries(p, s, last);
+  const int2 wa = row0 < s.kl ? seeing_queries(p, s, row0) : int2{0, 0}, wb = row0 < s.kl ? seeing_queries(p, s, wlast) : int2{0, 0};
+  // a head's tiles: na over the window [ta.x, tb.y), nb over what is behind the first key's window [ta.y, ql)
+  const int na = sink_item ? 0 : tiles_of(tb.y - ta.x, BQ), nb = with_sinks ? tiles_of(s.ql - ta.y, BQ) : 0, per = na + nb;
+  const int first = (int)((int64_t)per * grp * part / parts), end = (int)((int64_t)per * grp * (part + 1) / parts);
+  const auto range = [&](int t) {                     // its rows, in the window or not
+    const int x = t % per;
+    const int i = x < na ? ta.x + x * BQ : ta.y + (x - na) * BQ, e = x < na ? tb.y : s.ql;
+    return int2{i, i + BQ < e ? i + BQ : e};
+  };
+  const auto fetch = [&](int t) {
+    const int2 r = range(t);
+    const int h = kh * grp + t / per, n = r.y - r.x;
+    const int64_t row = s.qs + r.x;
+    Tile::template fetch<BQ>(static_cast<const T *>(p.q) + row * p.ldq + h * D, p.ldq, n, s_q[t & 1]);
+    Tile::template fetch<BQ>(static_cast<const T *>(p.go) + row * p.ldgo + h * D, p.ldgo, n, s_o[t & 1]);
+    if (wave < 2) {                                   // 64 values each (zeros behind the last)
+      const __amdgpu_buffer_rsrc_t view = buffer_view((wave ? p.delta : p.lse) + (int64_t)h * p.nq + row, n * 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          view, (__attribute__((address_space(3))) void *)(wave ? s_del[t & 1] : s_lse[t & 1]), 4, l * 4, 0, 0, 0);
+    }
+  };
+  const float c2 = p.scale * kLog2e;
+  f32x4 dk[ND][NC], dv[ND][NC];
+  for (int careful = 0; careful < 2; ++careful) {     // as in the forward, for q and do that are not finite
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int d = 0; d < ND; ++d) dk[d][c] = dv[d][c] = zero_f4();
+    __syncthreads();
+    if (first < end) fetch(first);
+    for (int t = first; t < end; ++t) {
+      __syncthreads();
+      if (t + 1 < end) fetch(t + 1);
+      const int2 r = range(t);
+      const bool window = t % per < na;
+      // this wave's keys are seen by queries from .. to: by all of them [a, b), by any [x, y)
+      int all_x, all_y, any_x, any_y;
+      if (window) {
+        all_x = wb.x, all_y = wa.y, any_x = wa.x, any_y = wb.y;
+      } else {
+        all_x = wlast < p.sinks ? wb.y : s.ql, all_y = s.ql, any_x = wa.y, any_y = row0 < p.sinks && row0 < s.kl ? s.ql : 0;
+      }
+      const bool full = r.y - r.x == BQ && all_x <= r.x && all_y >= r.y, none = row0 >= s.kl || !(any_x < r.y && any_y > r.x);
+      unsigned char *qt = s_q[t & 1], *ot = s_o[t & 1];
+      const float *lse = s_lse[t & 1], *del = s_del[t & 1];
+#pragma unroll
+      for (int x0 = 0; x0 < BQ; x0 += 32) {
+        Frag pr[NC], ds[NC];
+        if (!none) {
+          f32x4 sc[2][NC], dp[2][NC];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) sc[u][c] = dp[u][c] = zero_f4();
+#pragma unroll
+            for (int x = 0; x < NK; ++x) {
+              const Frag a = Tile::rows(qt, x0 + 16 * u + li, 32 * x + 8 * g), b = Tile::rows(ot, x0 + 16 * u + li, 32 * x + 8 * g);
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+                sc[u][c] = mma(a, k[c][x], sc[u][c]);
+                dp[u][c] = mma(b, v[c][x], dp[u][c]);
+              }
+            }
+            const f32x4 l4 = *reinterpret_cast<const f32x4 *>(lse + x0 + 16 * u + 4 * g) * kLog2e;
+            const f32x4 d4 = *reinterpret_cast<const f32x4 *>(del + x0 + 16 * u + 4 * g);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][c][x], c2, -l4[x]));
+                float f = e * (dp[u][c][x] - d4[x]);
+                if (!full) {
+                  const int i = r.x + x0 + 16 * u + 4 * g + x, j = row0 + 16 * c + li;
+                  const bool sees = i < r.y && (window ? i >= lo[c] && i < hi[c] : i >= hi[c] && j < p.sinks && j < s.kl);
+                  if (!sees) e = f = 0.0f;
+                }
+                sc[u][c][x] = e, dp[u][c][x] = f;
+              }
+          }
+#pragma unroll
+          for (int c = 0; c < NC; ++c) pr[c] = pack44<T>(sc[0][c], sc[1][c]), ds[c] = pack44<T>(dp[0][c], dp[1][c]);
+        }
+        if (careful && !(r.y - r.x == BQ && (window ? tb.x <= r.x && ta.y >= r.y : last < p.sinks && tb.y <= r.x))) {
+          if (!none)
+            for (int x = x0; x < x0 + 32; ++x) {
+              const int i = r.x + x;
+#pragma unroll
+              for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const float f = to_f32(*reinterpret_cast<const T *>(ot + Tile::elem(x, 16 * d + 4 * g + y)));
+                  if (fabsf(f) < __builtin_inff()) continue;
+#pragma unroll
+                  for (int c = 0; c < NC; ++c) {
+                    const int j = row0 + 16 * c + li;
+                    if (i < r.y && (window ? i >= lo[c] && i < hi[c] : i >= hi[c] && j < p.sinks && j < s.kl)) dv[d][c][y] += f;
+                  }
+                }
+            }
+          __syncthreads();
+          Tile::settle(qt, x0, 32);
+          Tile::settle(ot, x0, 32);
+          __syncthreads();
+        }
+        if (!none) {
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const Frag a = Tile::cols(ot, x0, 16 * d), b = Tile::cols(qt, x0, 16 * d);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              dv[d][c] = mma(a, pr[c], dv[d][c]);
+              dk[d][c] = mma(b, ds[c], dk[d][c]);
+            }
+          }
+        }
+      }
+    }
+    bool odd = false;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) odd |= !(fabsf(dk[d][c][x]) + fabsf(dv[d][c][x]) < __builtin_inff());
+    if (!__syncthreads_or(odd)) break;
+  }
+  const bool apart = p.sink_parts > 0 && tile < p.sink_tiles;       // this tile's sinks are other items' work
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = row0 + 16 * c + li;
+    if (j >= s.kl) continue;
+    const int64_t row = s.ks + j;
+    if (!sink_item && p.parts == 1 && !apart) {
+      T *ok = static_cast<T *>(p.gk) + row * p.ldgk + kh * D + 4 * g, *ov = static_cast<T *>(p.gv) + row * p.ldgv + kh * D + 4 * g;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) store4(ok + 16 * d, dk[d][c] * p.scale), store4(ov + 16 * d, dv[d][c]);
+      continue;
+    }
+    float *out;
+    if (sink_item || p.parts == 1)
+      out = p.spart + (((((int64_t)seq * p.sink_tiles + tile) * p.key_heads + kh) * (1 + p.sink_parts) + (sink_item ? 1 + part : 0)) * KR +
+                       (j - t0)) * 2 * D;
+    else
+      out = p.part + (((int64_t)part * p.nk + row) * p.key_heads + kh) * 2 * D;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+      store4(out + 16 * d + 4 * g, dk[d][c] * p.scale), store4(out + D + 16 * d + 4 * g, dv[d][c]);
+  }
+}
+
+// The sums over ranges of queries, in their order: a workgroup a key tile (of sinks only, where the window is one range)
+// and key head, D / 2 lanes a row.
+template <typename T, int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(AttnParams p) {
+  AttnSeq s;
+  int tile, seq;
+  const int kh = blockIdx.x % p.key_heads, x = blockIdx.x / p.key_heads;
+  if (p.parts > 1) {
+    if (!tile_of<true>(p, x, &s, &tile, &seq)) return;
+  } else {
+    tile = x % p.sink_tiles, seq = x / p.sink_tiles;
+    s = seq_of(p, seq);
+  }
+  const bool apart = p.sink_parts > 0 && tile < p.sink_tiles;
+  constexpr int L = D / 2;
+  const int c = threadIdx.x % L * 4;
+  for (int r = threadIdx.x / L; r < p.krows && tile * p.krows + r < s.kl; r += 256 / L) {
+    const int64_t row = s.ks + tile * p.krows + r;
+    f32x4 v = zero_f4();
+    if (p.parts > 1)
+      for (int i = 0; i < p.parts; ++i)
+        v += *reinterpret_cast<const f32x4 *>(p.part + (((int64_t)i * p.nk + row) * p.key_heads + kh) * 2 * D + c);
+    if (apart)
+      for (int i = p.parts > 1 ? 1 : 0; i <= p.sink_parts; ++i)
+        v += *reinterpret_cast<const f32x4 *>(
+            p.spart + (((((int64_t)seq * p.sink_tiles + tile) * p.key_heads + kh) * (1 + p.sink_parts) + i) * p.krows + r) * 2 * D + c);
+    if (c < D)
+      store4(static_cast<T *>(p.gk) + row * p.ldgk + kh * D + c, v);
+    else
+      store4(static_cast<T *>(p.gv) + row * p.ldgv + kh * D + c - D, v);
+  }
+}
+
+template <typename T, int D, int NC, int BK, int NCK, int BQ> hipError_t go(const AttnParams &p, hipStream_t s) {
+  const int blocks = (int)(((int64_t)p.nq * p.heads + 2048 / D - 1) / (2048 / D));
+  if (blocks > 0 || p.cu_q) {
+    hipLaunchKernelGGL((attn_delta_kernel<T, D>), dim3(blocks + (p.cu_q ? kZeroBlocks : 0)), dim3(256), 0, s, p, blocks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (p.nq > 0) {
+    hipLaunchKernelGGL((attn_dq_kernel<T, D, NC, BK>), dim3(p.qtiles * p.heads), dim3(256), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (p.nk == 0) return hipSuccess;
+  const int sinks = p.nseq * p.sink_tiles * p.key_heads;
+  hipLaunchKernelGGL((attn_dkv_kernel<T, D, NCK, BQ>), dim3(p.ktiles * p.key_heads * p.parts + sinks * p.sink_parts), dim3(256), 0, s, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (p.parts == 1 && p.sink_parts == 0)) return e;
+  hipLaunchKernelGGL((attn_dkv_sum_kernel<T, D>), dim3(p.parts > 1 ? p.ktiles * p.key_heads : sinks), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int attn_grad_query_rows(int d, bool bf16) { return d == 256 ? 64 : 128; }
+int attn_grad_key_rows(int d, bool bf16) { return d == 256 || (!bf16 && d == 128) ? 64 : 128; }
+
+hipError_t launch_attention_backward(const AttnParams &p, bool bf16, hipStream_t s) {
+  const hipError_t e = launch_attention_plan(p, s);
+  if (e != hipSuccess) return e;
+  if (bf16) {
+    if (p.d == 64) return go<__bf16, 64, 2, 64, 2, 64>(p, s);
+    return p.d == 128 ? go<__bf16, 128, 2, 32, 2, 32>(p, s) : go<__bf16, 256, 1, 32, 1, 32>(p, s);
+  }
+  if (p.d == 64) return go<float, 64, 2, 32, 2, 32>(p, s);
+  return p.d == 128 ? go<float, 128, 2, 32, 1, 32>(p, s) : go<float, 256, 1, 32, 1, 32>(p, s);
+}
+
+}  // namespace ttt

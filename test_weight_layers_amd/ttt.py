@@ -19,22 +19,33 @@ LIB_PATH = os.path.join(_HERE, "libttt.so")
 
 TTT_F32, TTT_BF16 = 0, 1
 OPT_FORCE_GENERAL, OPT_SPLITS, OPT_NS_UNFUSED = 0, 1, 2
-KERNEL_KINDS = ("conv", "cast", "grad", "reduce", "ns", "apply", "gate", "delta", "residual", "orthogonalise")
+KERNEL_KINDS = ("conv", "cast", "grad", "reduce", "ns", "apply", "gate", "delta", "residual", "orthogonalise",
+                "attention", "norm", "adamw")
 NORM_PRESERVE = 1
 DELTA_ZERO_UNUSED = 1
+ATTENTION_ZERO_UNUSED = 1
 EXPORTS = ("ttt_last_error", "ttt_update_workspace_bytes", "ttt_apply_workspace_bytes", "ttt_update",
            "ttt_update_ex", "ttt_update_host_workspace_bytes", "ttt_update_host", "ttt_apply", "ttt_output_gate", "ttt_shortconv2d", "ttt_stream_workspace_bytes",
            "ttt_stream", "ttt_stream_ex", "ttt_set_option", "ttt_profile_enable", "ttt_profile_reset",
            "ttt_profile_read", "ttt_update_noalloc", "ttt_noalloc_scratch_bytes", "ttt_mfma_rate_probe",
            "ttt_delta_workspace_bytes", "ttt_delta", "ttt_delta_backward", "ttt_delta_step", "ttt_gated_residual",
            "ttt_gated_residual_backward_workspace_bytes", "ttt_gated_residual_backward",
-           "ttt_orthogonalise_workspace_bytes", "ttt_orthogonalise")
+           "ttt_orthogonalise_workspace_bytes", "ttt_orthogonalise", "ttt_window_attention_workspace_bytes",
+           "ttt_window_attention", "ttt_window_attention_backward", "ttt_window_attention_step_workspace_bytes",
+           "ttt_window_attention_step", "ttt_layer_norm", "ttt_layer_norm_backward_workspace_bytes",
+           "ttt_layer_norm_backward", "ttt_adamw_check", "ttt_adamw_step")
 
 _lib = None
 
 
 class TTTError(RuntimeError):
     pass
+
+
+class _AdamwTensor(ctypes.Structure):
+    """ttt_adamw_tensor."""
+    _fields_ = [(x, ctypes.c_void_p) for x in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                               "exp_avg_sq_scale", "master")] + [("n", ctypes.c_int64)]
 
 
 def load() -> ctypes.CDLL:
@@ -89,6 +100,21 @@ def load() -> ctypes.CDLL:
                                                        sz, vp]),
         "ttt_orthogonalise_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i32, szp]),
         "ttt_orthogonalise": (ctypes.c_int, [i32, i32, i32, vp, i64, i64, vp, i64, i64, i32, i32, vp, sz, vp]),
+        "ttt_window_attention_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i64, i64] + 7 * [i32] + [szp]),
+        "ttt_window_attention": (ctypes.c_int, [i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, vp,
+                                                i32, i32, i32, i32, i32, f32, i32, u32, vp, sz, vp]),
+        "ttt_window_attention_backward": (ctypes.c_int, [i32, i32, i32] + 4 * [vp, i64] + [vp] + 4 * [vp, i64] +
+                                          [i64, i64, vp, vp, i32, i32, i32, i32, i32, f32, i32, vp, sz, vp]),
+        "ttt_window_attention_step_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i64, i32, i32, szp]),
+        "ttt_window_attention_step": (ctypes.c_int, [i32, i32, i32, vp, vp, i64, i64, i32, i32, vp, vp] +
+                                      4 * [vp, i64] + [i64, i32, i32, i32, f32, i32, u32, vp, sz, vp]),
+        "ttt_layer_norm": (ctypes.c_int, [i32, i32, vp, i64, vp, vp, f32, vp, i64, i64, i32, vp]),
+        "ttt_layer_norm_backward_workspace_bytes": (ctypes.c_int, [i32, i32, i64, szp]),
+        "ttt_layer_norm_backward": (ctypes.c_int, [i32, i32, vp, i64, vp, i64, vp, f32, vp, i64, vp, vp, i64, i32, vp,
+                                                   sz, vp]),
+        "ttt_adamw_check": (ctypes.c_int, [ctypes.POINTER(_AdamwTensor), i32, i32, i32]),
+        "ttt_adamw_step": (ctypes.c_int, [ctypes.POINTER(_AdamwTensor), i32, i64, vp] + [ctypes.c_double, vp] +
+                           4 * [ctypes.c_double] + [vp, i32, i32, vp, sz, vp]),
         "ttt_mfma_rate_probe": (ctypes.c_int, [i32, vp, ctypes.POINTER(ctypes.c_double)]),
     }
     for name, (res, args) in sig.items():
@@ -688,6 +714,308 @@ def orthogonalise(g: torch.Tensor, steps: int = 5, out: Optional[torch.Tensor] =
                                     int(steps), code, _ptr(workspace),
                                     0 if workspace is None else _bytes(workspace, dev), _stream()))
     return out
+
+
+# ------------------------------------------------------------------ windowed attention
+def _limit(x: Optional[int], name: str) -> int:
+    if x is None:
+        return -1
+    if x < 0:
+        raise ValueError(f"{name} must be >= 0, or None for no limit")
+    return int(x)
+
+
+def _heads(q: torch.Tensor, heads: int, key_heads: Optional[int]) -> Tuple[int, int, int]:
+    """(heads, key_heads, d) of query rows."""
+    if q.dim() != 2:
+        raise ValueError("q must be a 2-D tensor of token rows")
+    H = int(heads)
+    if H < 1 or q.shape[1] % H != 0:
+        raise ValueError(f"q rows of {q.shape[1]} columns do not hold {heads} heads")
+    return H, H if key_heads is None else int(key_heads), q.shape[1] // H
+
+
+def _attention_args(q, k, v, heads, key_heads, block, before, after, sinks, scale, cu, cu_k):
+    """Checks shared by windowed attention and its gradient."""
+    dev, dtype, code = _gpu(q, "q"), q.dtype, _dtype_code(q)
+    H, Hk, d = _heads(q, heads, key_heads)
+    nq, nk = q.shape[0], k.shape[0]
+    ld = (_row(q, dtype, dev, nq, H * d, "q"), _row(k, dtype, dev, nk, Hk * d, "k"), _row(v, dtype, dev, nk, Hk * d, "v"))
+    S = 1
+    if cu is not None:
+        if cu.dim() != 1 or cu.shape[0] < 2 or cu.dtype != torch.int32 or not cu.is_contiguous() or cu.get_device() != dev:
+            raise ValueError(f"cu_seqlens must be a contiguous int32 tensor [sequences + 1] on cuda:{dev}")
+        S = cu.shape[0] - 1
+    if cu_k is not None and (cu is None or cu_k.shape != cu.shape or cu_k.dtype != torch.int32
+                             or not cu_k.is_contiguous() or cu_k.get_device() != dev):
+        raise ValueError("cu_seqlens_k must be a contiguous int32 tensor like cu_seqlens")
+    mask = (int(block), _limit(before, "before"), _limit(after, "after"), int(sinks))
+    return dev, dtype, code, H, Hk, d, nq, nk, ld, S, mask, d ** -0.5 if scale is None else float(scale)
+
+
+def window_attention_workspace_bytes(heads: int, key_heads: int, d: int, nq: int, nk: int, sequences: int, block: int,
+                                     before: Optional[int], after: Optional[int], sinks: int, dtype: torch.dtype,
+                                     backward: bool = False) -> int:
+    out = ctypes.c_size_t()
+    code = TTT_BF16 if dtype == torch.bfloat16 else TTT_F32
+    _check(load().ttt_window_attention_workspace_bytes(heads, key_heads, d, nq, nk, sequences, block,
+                                                       _limit(before, "before"), _limit(after, "after"), sinks, code,
+                                                       int(backward), ctypes.byref(out)))
+    return out.value
+
+
+def _attention_workspace(H, Hk, d, nq, nk, S, mask, code, backward, device) -> torch.Tensor:
+    out = ctypes.c_size_t()
+    _check(load().ttt_window_attention_workspace_bytes(H, Hk, d, nq, nk, S, *mask, code, backward, ctypes.byref(out)))
+    return torch.empty(out.value, dtype=torch.uint8, device=device)
+
+
+def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, heads: int, key_heads: Optional[int] = None,
+                     block: int = 1, before: Optional[int] = None, after: Optional[int] = 0, sinks: int = 0,
+                     scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                     cu_seqlens_k: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     lse_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Softmax attention over packed sequences within a window of blocks; returns (o, lse).
+
+    q rows of heads * d columns, k and v rows of key_heads * d.  A query of block b (``block`` tokens each; the queries
+    are the last rows of their sequence's keys) sees the keys of blocks b - before .. b + after (None: no limit) and,
+    of those before, the first ``sinks``: before = after = 0 is attention inside a frame, block = 1 a causal window of
+    tokens.  scale None: d ** -0.5.  lse [heads, nq] float32.  Rows outside the sequences stay as they are in a given
+    ``out`` and are zero in a new one; their lse is -inf.
+    """
+    dev, dtype, code, H, Hk, d, nq, nk, ld, S, mask, scale = _attention_args(
+        q, k, v, heads, key_heads, block, before, after, sinks, scale, cu_seqlens, cu_seqlens_k)
+    flags, ldo = 0, H * d
+    if out is None:
+        out = q.new_empty((nq, H * d))
+        flags = ATTENTION_ZERO_UNUSED
+    else:
+        ldo = _row(out, dtype, dev, nq, H * d, "out")
+    if lse_out is None:
+        lse_out = torch.empty((H, nq), dtype=torch.float32, device=q.device)
+    elif lse_out.dtype != torch.float32 or lse_out.shape != (H, nq) or not lse_out.is_contiguous() or lse_out.get_device() != dev:
+        raise ValueError(f"lse_out must be a contiguous float32 tensor [{H}, {nq}] on cuda:{dev}")
+    if workspace is None:
+        workspace = _attention_workspace(H, Hk, d, nq, nk, S, mask, code, 0, q.device)
+    _check(load().ttt_window_attention(H, Hk, d, q.data_ptr(), ld[0], k.data_ptr(), ld[1], v.data_ptr(), ld[2],
+                                       out.data_ptr(), ldo, lse_out.data_ptr(), nq, nk, _ptr(cu_seqlens),
+                                       _ptr(cu_seqlens_k), S, *mask, scale, code, flags, workspace.data_ptr(),
+                                       _bytes(workspace, dev), _stream()))
+    return out, lse_out
+
+
+def window_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
+                              grad_o: torch.Tensor, *, heads: int, key_heads: Optional[int] = None, block: int = 1,
+                              before: Optional[int] = None, after: Optional[int] = 0, sinks: int = 0,
+                              scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                              cu_seqlens_k: Optional[torch.Tensor] = None,
+                              out: Optional[Sequence[torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradients (grad_q, grad_k, grad_v) of ``window_attention``, from its outputs o and lse.
+
+    ``out`` gives the rows to write to (slices of one buffer, say).
+    """
+    dev, dtype, code, H, Hk, d, nq, nk, ld, S, mask, scale = _attention_args(
+        q, k, v, heads, key_heads, block, before, after, sinks, scale, cu_seqlens, cu_seqlens_k)
+    ldo, ldgo = _row(o, dtype, dev, nq, H * d, "o"), _row(grad_o, dtype, dev, nq, H * d, "grad_o")
+    if lse.dtype != torch.float32 or lse.shape != (H, nq) or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError(f"lse must be a contiguous float32 tensor [{H}, {nq}] on cuda:{dev}")
+    if out is None:
+        out = tuple(torch.empty((n, w), dtype=dtype, device=q.device) for n, w in ((nq, H * d), (nk, Hk * d), (nk, Hk * d)))
+    gq, gk, gv = out
+    if workspace is None:
+        workspace = _attention_workspace(H, Hk, d, nq, nk, S, mask, code, 1, q.device)
+    _check(load().ttt_window_attention_backward(
+        H, Hk, d, q.data_ptr(), ld[0], k.data_ptr(), ld[1], v.data_ptr(), ld[2], o.data_ptr(), ldo, lse.data_ptr(),
+        grad_o.data_ptr(), ldgo, gq.data_ptr(), _row(gq, dtype, dev, nq, H * d, "grad_q"), gk.data_ptr(),
+        _row(gk, dtype, dev, nk, Hk * d, "grad_k"), gv.data_ptr(), _row(gv, dtype, dev, nk, Hk * d, "grad_v"), nq, nk,
+        _ptr(cu_seqlens), _ptr(cu_seqlens_k), S, *mask, scale, code, workspace.data_ptr(), _bytes(workspace, dev),
+        _stream()))
+    return gq, gk, gv
+
+
+def window_attention_step(k_cache: torch.Tensor, v_cache: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                          v: torch.Tensor, positions: torch.Tensor, *, heads: int, key_heads: Optional[int] = None,
+                          slots: Optional[torch.Tensor] = None, block: int = 1, before: Optional[int] = None,
+                          sinks: int = 0, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token for each row over rolling caches [pool, capacity, key_heads * d], which take its k and v; returns o.
+
+    Row i has cache ``slots[i]`` (int32; None: cache i) and its token position ``positions[i]`` (int32).  Position x
+    of a sequence stands in row x of its cache (x < sinks) or sinks + (x - sinks) % (capacity - sinks).  Slots outside
+    the pool and negative positions are padding: such rows stay as they are in a given ``out`` and are zero in a new
+    one.  The rows of a call read the caches as they were before it.
+    """
+    dev, dtype, code = _gpu(q, "q"), q.dtype, _dtype_code(q)
+    H, Hk, d = _heads(q, heads, key_heads)
+    n = q.shape[0]
+    ldq, ldk, ldv = (_row(q, dtype, dev, n, H * d, "q"), _row(k, dtype, dev, n, Hk * d, "k"),
+                     _row(v, dtype, dev, n, Hk * d, "v"))
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != 3 or shape[2] < Hk * d or stride[2] != 1 or stride[0] < 0 or stride[1] < 0 or v_cache.shape != shape \
+            or v_cache.stride() != stride or k_cache.dtype != dtype or v_cache.dtype != dtype \
+            or k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError(f"k_cache and v_cache must be [pool, capacity, >={Hk * d}] {dtype} tensors of the same shape "
+                         f"and strides, unit column stride, on cuda:{dev}")
+    if positions.dtype != torch.int32 or positions.shape != (n,) or not positions.is_contiguous() \
+            or positions.get_device() != dev:
+        raise ValueError(f"positions must be a contiguous int32 tensor [{n}] on cuda:{dev}")
+    if slots is not None and (slots.dtype != torch.int32 or slots.shape != (n,) or not slots.is_contiguous()
+                              or slots.get_device() != dev):
+        raise ValueError(f"slots must be a contiguous int32 tensor [{n}] on cuda:{dev}")
+    flags, ldo = 0, H * d
+    if out is None:
+        out = q.new_empty((n, H * d))
+        flags = ATTENTION_ZERO_UNUSED
+    else:
+        ldo = _row(out, dtype, dev, n, H * d, "out")
+    L = load()
+    if workspace is None:
+        size = ctypes.c_size_t()
+        _check(L.ttt_window_attention_step_workspace_bytes(H, Hk, d, n, shape[1], code, ctypes.byref(size)))
+        workspace = torch.empty(size.value, dtype=torch.uint8, device=q.device)
+    _check(L.ttt_window_attention_step(H, Hk, d, k_cache.data_ptr(), v_cache.data_ptr(), stride[1], stride[0], shape[0],
+                                       shape[1], _ptr(slots), positions.data_ptr(), q.data_ptr(), ldq, k.data_ptr(),
+                                       ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, n, int(block),
+                                       _limit(before, "before"), int(sinks), d ** -0.5 if scale is None else float(scale),
+                                       code, flags, workspace.data_ptr(), _bytes(workspace, dev), _stream()))
+    return out
+
+
+# ------------------------------------------------------------------ layer norm
+def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+               eps: float = 1e-6, *, norm_width: Optional[int] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """gamma * (x - mean) / sqrt(var + eps) + beta over groups of ``norm_width`` columns (default: the row).
+
+    gamma, beta [norm_width] float32, shared by the groups (None: 1, 0).  ``out`` may be ``x`` (in place).
+    """
+    code, dtype, dev = _dtype_code(x), x.dtype, _gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor of rows")
+    n, C = x.shape
+    w = C if norm_width is None else int(norm_width)
+    ldx = _row(x, dtype, dev, n, C, "x")
+    gamma, beta = _channel(gamma, w, dev, "gamma"), _channel(beta, w, dev, "beta")
+    if out is None:
+        ldy = -(-C // 8) * 8                            # rows begin on 16 bytes
+        out = x.new_empty((n, C)) if ldy == C else x.new_empty((n, ldy))[:, :C]
+    else:
+        ldy = _row(out, dtype, dev, n, C, "out")
+    _check(load().ttt_layer_norm(C, w, x.data_ptr(), ldx, gamma, beta, float(eps), out.data_ptr(), ldy, n, code,
+                                 _stream()))
+    return out
+
+
+def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        *, norm_width: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None):
+    """Gradients (grad_x, grad_gamma, grad_beta) of ``layer_norm``.  ``out`` (grad_x) may be ``grad_y`` (in place)."""
+    code, dtype, dev = _dtype_code(x), x.dtype, _gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor of rows")
+    n, C = x.shape
+    w = C if norm_width is None else int(norm_width)
+    ldx, ldg = _row(x, dtype, dev, n, C, "x"), _row(grad_y, dtype, dev, n, C, "grad_y")
+    gamma = _channel(gamma, w, dev, "gamma")
+    if out is None:
+        ldo = -(-C // 8) * 8
+        out = x.new_empty((n, C)) if ldo == C else x.new_empty((n, ldo))[:, :C]
+    else:
+        ldo = _row(out, dtype, dev, n, C, "out")
+    L = load()
+    if workspace is None:
+        size = ctypes.c_size_t()
+        _check(L.ttt_layer_norm_backward_workspace_bytes(C, w, n, ctypes.byref(size)))
+        workspace = _workspace(size.value, x.device)
+    ggamma = torch.empty(w, dtype=torch.float32, device=x.device)
+    gbeta = torch.empty(w, dtype=torch.float32, device=x.device)
+    _check(L.ttt_layer_norm_backward(C, w, grad_y.data_ptr(), ldg, x.data_ptr(), ldx, gamma, float(eps), out.data_ptr(),
+                                     ldo, ggamma.data_ptr(), gbeta.data_ptr(), n, code, workspace.data_ptr(),
+                                     _bytes(workspace, dev), _stream()))
+    return out, ggamma, gbeta
+
+
+# ------------------------------------------------------------------ AdamW
+class AdamwTensors:
+    """The tensors of ``adamw_step``: made once by ``adamw_tensors``, it keeps them alive."""
+
+    def __init__(self, table, sizes, dtype, bits, dev, held):
+        self.table, self.sizes, self.dtype, self.bits, self.dev, self.held = table, sizes, dtype, bits, dev, held
+
+
+def adamw_tensors(params: Sequence[torch.Tensor], exp_avg: Sequence[torch.Tensor], exp_avg_sq: Sequence[torch.Tensor], *,
+                  master: Optional[Sequence[torch.Tensor]] = None,
+                  exp_avg_scales: Optional[Sequence[torch.Tensor]] = None,
+                  exp_avg_sq_scales: Optional[Sequence[torch.Tensor]] = None) -> AdamwTensors:
+    """Checks the tensors of an AdamW optimiser and returns their table for ``adamw_step``.
+
+    params bfloat16 or float32 (all of one type), contiguous, any shapes; ``master`` the float32 weights behind them.
+    exp_avg, exp_avg_sq: float32 of the params' sizes, or int8 and uint8 with a float32 scale for each 256 elements
+    (exp_avg_scales, exp_avg_sq_scales).  Zeros are the state to start from.
+    """
+    if not params:
+        raise ValueError("params must hold a tensor")
+    dtype, dev = params[0].dtype, _gpu(params[0], "params")
+    code = _dtype_code(params[0])
+    bits = 8 if exp_avg and exp_avg[0].dtype == torch.int8 else 32
+    types = (torch.int8, torch.uint8) if bits == 8 else (torch.float32, torch.float32)
+    if (exp_avg_scales is None) != (bits == 32) or (exp_avg_sq_scales is None) != (bits == 32):
+        raise ValueError("exp_avg_scales and exp_avg_sq_scales must be given exactly with 8-bit states")
+    lists = [("params", "param", params, dtype), ("exp_avg", "exp_avg", exp_avg, types[0]),
+             ("exp_avg_sq", "exp_avg_sq", exp_avg_sq, types[1]), ("master", "master", master, torch.float32),
+             ("exp_avg_scales", "exp_avg_scale", exp_avg_scales, torch.float32),
+             ("exp_avg_sq_scales", "exp_avg_sq_scale", exp_avg_sq_scales, torch.float32)]
+    table = (_AdamwTensor * len(params))()
+    sizes = [p.numel() for p in params]
+    for name, field, tensors, dt in lists:
+        if tensors is None:
+            continue
+        if len(tensors) != len(params):
+            raise ValueError(f"{name} must hold {len(params)} tensors")
+        for i, t in enumerate(tensors):
+            need = -(-sizes[i] // 256) if name.endswith("scales") else sizes[i]
+            if t.dtype != dt or t.numel() != need or not t.is_contiguous() or t.get_device() != dev:
+                raise ValueError(f"{name}[{i}] must be a contiguous {dt} tensor of {need} elements on cuda:{dev}")
+            setattr(table[i], field, t.data_ptr())
+    for i, n in enumerate(sizes):
+        table[i].n = n
+    _check(load().ttt_adamw_check(table, len(params), bits, code))
+    return AdamwTensors(table, sizes, dtype, bits, dev, [list(x[2]) for x in lists if x[2] is not None])
+
+
+def adamw_step(tensors: AdamwTensors, grads: Sequence[torch.Tensor], *, step, lr, betas: Tuple[float, float] = (0.9, 0.999),
+               eps: float = 1e-8, weight_decay: float = 0.0, grad_scale: Optional[torch.Tensor] = None) -> None:
+    """One AdamW step, in place on the params, masters and states of ``tensors``.
+
+    grads: like the params.  step counts from 1; step (int64) and lr (float32) may be one-element GPU tensors, read when
+    the kernels run (captured steps).  grad_scale: one-element float32 GPU tensor that multiplies every gradient.
+    """
+    dev, dtype, sizes, table = tensors.dev, tensors.dtype, tensors.sizes, tensors.table
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors must be on the current GPU, got cuda:{dev}")
+    if len(grads) != len(sizes):
+        raise ValueError(f"grads must hold {len(sizes)} tensors")
+    for i, g in enumerate(grads):
+        if g.dtype != dtype or g.numel() != sizes[i] or not g.is_contiguous() or g.get_device() != dev:
+            raise ValueError(f"grads[{i}] must be a contiguous {dtype} tensor of {sizes[i]} elements on cuda:{dev}")
+        table[i].grad = g.data_ptr()
+
+    def scalar(t, dt, name):
+        if t.dtype != dt or t.numel() != 1 or t.get_device() != dev:
+            raise ValueError(f"{name} must be a one-element {dt} tensor on cuda:{dev}")
+        return t.data_ptr()
+
+    step_ptr = lr_ptr = workspace = None
+    if isinstance(step, torch.Tensor):
+        step_ptr, step = scalar(step, torch.int64, "step"), 1
+    if isinstance(lr, torch.Tensor):
+        lr_ptr, lr = scalar(lr, torch.float32, "lr"), 0.0
+    if step_ptr is not None or lr_ptr is not None:
+        workspace = torch.empty(16, dtype=torch.uint8, device=torch.device("cuda", dev))
+    _check(load().ttt_adamw_step(table, len(sizes), int(step), step_ptr, float(lr), lr_ptr, float(betas[0]),
+                                 float(betas[1]), float(eps), float(weight_decay),
+                                 None if grad_scale is None else scalar(grad_scale, torch.float32, "grad_scale"),
+                                 tensors.bits, TTT_BF16 if dtype == torch.bfloat16 else TTT_F32, _ptr(workspace),
+                                 0 if workspace is None else 16, _stream()))
 
 
 # ------------------------------------------------------------------ timing
