@@ -155,7 +155,7 @@ int plan_step(int H, int Hk, int d, int64_t n, int capacity, int dtype, StepPlan
   if (n < 0 || capacity < 1) return fail(TTT_EINVAL, "n must be >= 0 and capacity >= 1");
   StepPlan P;
   P.splits = step_splits(H, Hk, n, capacity);
-  if (n > kMaxRows || n * Hk * ceil_div(H / Hk, 16) * P.splits > kMaxGroups || (int64_t)H * d / 1024 > 65535)
+  if (n > kMaxRows || n * Hk * ceil_div(H / Hk, 16) * P.splits > kMaxGroups || H > 65535)
     return fail(TTT_EUNSUPPORTED, "too many rows (%lld) for %d heads in one call", (long long)n, H);
   P.off_ml = align256((size_t)P.splits * n * H * d * 4);
   P.total = std::max<size_t>(256, P.off_ml + align256((size_t)P.splits * n * H * 8));

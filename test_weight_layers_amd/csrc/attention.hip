@@ -9,8 +9,8 @@ namespace {
 constexpr int kZeroBlocks = 32;     // workgroups that fill rows of no sequence
 
 // Four waves of NC x 16 queries each; BK keys at a time through two LDS buffers.
-template <typename T, int D, int NC, int BK>
-__global__ __launch_bounds__(256) void attn_forward_kernel(AttnParams p) {
+template <typename T, int D, int NC, int BK, int OCC>
+__global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
   typedef AttnTile<T, D> Tile;
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, NU = BK / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256) void attn_forward_kernel(AttnParams p) {
     __syncthreads();
     if (first < end) fetch(first);
     for (int t = first; t < end; ++t) {
-      __syncthreads();                                // this tile has landed, and nobody reads the other buffer
+      landed();                                       // this tile, and nobody reads the other buffer
       if (t + 1 < end) fetch(t + 1);
       const int2 r = range(t);
       const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
@@ -100,6 +100,7 @@ __global__ __launch_bounds__(256) void attn_forward_kernel(AttnParams p) {
           }
         }
         if (!full) {
+          rarely();
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const int e = hi[c] < r.y ? hi[c] : r.y;
@@ -108,7 +109,7 @@ __global__ __launch_bounds__(256) void attn_forward_kernel(AttnParams p) {
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const int j = r.x + 16 * u + 4 * g + x;
-                if (!(j < e && (j >= lo[c] || j < p.sinks))) sc[u][c][x] = -__builtin_inff();
+                sc[u][c][x] = (j < e) & ((j >= lo[c]) | (j < p.sinks)) ? sc[u][c][x] : -__builtin_inff();
               }
           }
         }
@@ -142,7 +143,8 @@ __global__ __launch_bounds__(256) void attn_forward_kernel(AttnParams p) {
         for (int c = 0; c < NC; ++c) {
           const float top = m[c] == -__builtin_inff() ? 0.0f : m[c];
           float base = -top * c2;
-          if (huge) {                                 // in some column: there the maximum is taken off first
+          if (huge) {
+            rarely();                                 // in some column: there the maximum is taken off first
             const bool off = fabsf(base) > kHuge;
             base = off ? 0.0f : base;
 #pragma unroll
@@ -291,9 +293,9 @@ __global__ __launch_bounds__(1024) void attn_plan_kernel(AttnParams p) {
   }
 }
 
-template <typename T, int D, int NC, int BK> hipError_t go(const AttnParams &p, hipStream_t s) {
+template <typename T, int D, int NC, int BK, int OCC> hipError_t go(const AttnParams &p, hipStream_t s) {
   const int items = p.qtiles * p.heads * p.splits;
-  hipLaunchKernelGGL((attn_forward_kernel<T, D, NC, BK>), dim3(items + (p.cu_q ? kZeroBlocks : 0)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_forward_kernel<T, D, NC, BK, OCC>), dim3(items + (p.cu_q ? kZeroBlocks : 0)), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1 || p.nq == 0) return e;
   hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)(((int64_t)p.nq * p.heads + 1024 / D - 1) / (1024 / D))), dim3(256),
@@ -317,13 +319,13 @@ hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s) {
   if (e != hipSuccess) return e;
   const bool small = p.qrows == 64;
   if (bf16) {
-    if (p.d == 64) return small ? go<__bf16, 64, 1, 64>(p, s) : go<__bf16, 64, 2, 64>(p, s);
-    if (p.d == 128) return small ? go<__bf16, 128, 1, 64>(p, s) : go<__bf16, 128, 2, 64>(p, s);
-    return small ? go<__bf16, 256, 1, 32>(p, s) : go<__bf16, 256, 2, 32>(p, s);
+    if (p.d == 64) return small ? go<__bf16, 64, 1, 64, 4>(p, s) : go<__bf16, 64, 2, 64, 3>(p, s);
+    if (p.d == 128) return small ? go<__bf16, 128, 1, 64, 2>(p, s) : go<__bf16, 128, 2, 64, 2>(p, s);
+    return small ? go<__bf16, 256, 1, 32, 2>(p, s) : go<__bf16, 256, 2, 32, 2>(p, s);
   }
-  if (p.d == 64) return small ? go<float, 64, 1, 32>(p, s) : go<float, 64, 2, 32>(p, s);
-  if (p.d == 128) return small ? go<float, 128, 1, 32>(p, s) : go<float, 128, 2, 32>(p, s);
-  return go<float, 256, 1, 32>(p, s);
+  if (p.d == 64) return small ? go<float, 64, 1, 32, 4>(p, s) : go<float, 64, 2, 32, 3>(p, s);
+  if (p.d == 128) return small ? go<float, 128, 1, 32, 2>(p, s) : go<float, 128, 2, 32, 2>(p, s);
+  return go<float, 256, 1, 32, 1>(p, s);
 }
 
 }  // namespace ttt

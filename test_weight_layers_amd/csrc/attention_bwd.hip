@@ -39,8 +39,8 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_delta_k
 }
 
 // Four waves of NC x 16 queries; BK keys at a time, 32 of them through the registers.
-template <typename T, int D, int NC, int BK>
-__global__ __launch_bounds__(256) void attn_dq_kernel(AttnParams p) {
+template <typename T, int D, int NC, int BK, int OCC>
+__global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
   typedef AttnTile<T, D> Tile;
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256) void attn_dq_kernel(AttnParams p) {
     __syncthreads();
     if (nt > 0) fetch(0);
     for (int t = 0; t < nt; ++t) {
-      __syncthreads();
+      landed();
       if (t + 1 < nt) fetch(t + 1);
       const int2 r = range(t);
       const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
@@ -125,13 +125,18 @@ __global__ __launch_bounds__(256) void attn_dq_kernel(AttnParams p) {
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][c][x], c2, lse[c]));
-                float v = pr * (dp[u][c][x] - delta[c]);
-                if (!full) {
-                  const int j = r.x + x0 + 16 * u + 4 * g + x;
-                  if (!(j < e && (j >= lo[c] || j < p.sinks))) v = 0.0f;
-                }
-                sc[u][c][x] = v;
+                sc[u][c][x] = pr * (dp[u][c][x] - delta[c]);
               }
+            if (!full) {
+              rarely();
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const int j = r.x + x0 + 16 * u + 4 * g + x;
+                  sc[u][c][x] = (j < e) & ((j >= lo[c]) | (j < p.sinks)) ? sc[u][c][x] : 0.0f;
+                }
+            }
             ds[c] = pack44<T>(sc[0][c], sc[1][c]);
           }
         }
@@ -173,8 +178,8 @@ __global__ __launch_bounds__(256) void attn_dq_kernel(AttnParams p) {
 }
 
 // Four waves of NC x 16 keys of a key head; BQ queries of one head at a time.
-template <typename T, int D, int NC, int BQ>
-__global__ __launch_bounds__(256) void attn_dkv_kernel(AttnParams p) {
+template <typename T, int D, int NC, int BQ, int OCC>
+__global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   typedef AttnTile<T, D> Tile;
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, kTile = BQ * Tile::kRow, KR = 64 * NC;
@@ -227,9 +232,8 @@ __global__ __launch_bounds__(256) void attn_dkv_kernel(AttnParams p) {
     Tile::template fetch<BQ>(static_cast<const T *>(p.q) + row * p.ldq + h * D, p.ldq, n, s_q[t & 1]);
     Tile::template fetch<BQ>(static_cast<const T *>(p.go) + row * p.ldgo + h * D, p.ldgo, n, s_o[t & 1]);
     if (wave < 2) {                                   // 64 values each (zeros behind the last)
-      const __amdgpu_buffer_rsrc_t view = buffer_view((wave ? p.delta : p.lse) + (int64_t)h * p.nq + row, n * 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          view, (__attribute__((address_space(3))) void *)(wave ? s_del[t & 1] : s_lse[t & 1]), 4, l * 4, 0, 0, 0);
+      const BufferView view = untracked_view((wave ? p.delta : p.lse) + (int64_t)h * p.nq + row, n * 4);
+      copy_to_lds_untracked<4>(view, l * 4, reinterpret_cast<unsigned char *>(wave ? s_del[t & 1] : s_lse[t & 1]));
     }
   };
   const float c2 = p.scale * kLog2e;
@@ -242,7 +246,7 @@ __global__ __launch_bounds__(256) void attn_dkv_kernel(AttnParams p) {
     __syncthreads();
     if (first < end) fetch(first);
     for (int t = first; t < end; ++t) {
-      __syncthreads();
+      landed();
       if (t + 1 < end) fetch(t + 1);
       const int2 r = range(t);
       const bool window = t % per < na;
@@ -280,15 +284,25 @@ __global__ __launch_bounds__(256) void attn_dkv_kernel(AttnParams p) {
             for (int c = 0; c < NC; ++c)
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][c][x], c2, -l4[x]));
-                float f = e * (dp[u][c][x] - d4[x]);
-                if (!full) {
-                  const int i = r.x + x0 + 16 * u + 4 * g + x, j = row0 + 16 * c + li;
-                  const bool sees = i < r.y && (window ? i >= lo[c] && i < hi[c] : i >= hi[c] && j < p.sinks && j < s.kl);
-                  if (!sees) e = f = 0.0f;
-                }
-                sc[u][c][x] = e, dp[u][c][x] = f;
+                sc[u][c][x] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][c][x], c2, -l4[x]));
+                dp[u][c][x] = sc[u][c][x] * (dp[u][c][x] - d4[x]);
               }
+          }
+          if (!full) {                                // the queries [first, e) see column c
+            rarely();
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const int j = row0 + 16 * c + li;
+              const int first = window ? lo[c] : (j < p.sinks) & (j < s.kl) ? hi[c] : s.ql, e = window ? (hi[c] < r.y ? hi[c] : r.y) : r.y;
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const int i = r.x + x0 + 16 * u + 4 * g + x;
+                  const bool sees = (i >= first) & (i < e);
+                  sc[u][c][x] = sees ? sc[u][c][x] : 0.0f, dp[u][c][x] = sees ? dp[u][c][x] : 0.0f;
+                }
+            }
           }
 #pragma unroll
           for (int c = 0; c < NC; ++c) pr[c] = pack44<T>(sc[0][c], sc[1][c]), ds[c] = pack44<T>(dp[0][c], dp[1][c]);
@@ -393,7 +407,7 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_dkv_sum
   }
 }
 
-template <typename T, int D, int NC, int BK, int NCK, int BQ> hipError_t go(const AttnParams &p, hipStream_t s) {
+template <typename T, int D, int NC, int BK, int OCC, int NCK, int BQ, int OCCK> hipError_t go(const AttnParams &p, hipStream_t s) {
   const int blocks = (int)(((int64_t)p.nq * p.heads + 2048 / D - 1) / (2048 / D));
   if (blocks > 0 || p.cu_q) {
     hipLaunchKernelGGL((attn_delta_kernel<T, D>), dim3(blocks + (p.cu_q ? kZeroBlocks : 0)), dim3(256), 0, s, p, blocks);
@@ -401,13 +415,13 @@ template <typename T, int D, int NC, int BK, int NCK, int BQ> hipError_t go(cons
     if (e != hipSuccess) return e;
   }
   if (p.nq > 0) {
-    hipLaunchKernelGGL((attn_dq_kernel<T, D, NC, BK>), dim3(p.qtiles * p.heads), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((attn_dq_kernel<T, D, NC, BK, OCC>), dim3(p.qtiles * p.heads), dim3(256), 0, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (p.nk == 0) return hipSuccess;
   const int sinks = p.nseq * p.sink_tiles * p.key_heads;
-  hipLaunchKernelGGL((attn_dkv_kernel<T, D, NCK, BQ>), dim3(p.ktiles * p.key_heads * p.parts + sinks * p.sink_parts), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_dkv_kernel<T, D, NCK, BQ, OCCK>), dim3(p.ktiles * p.key_heads * p.parts + sinks * p.sink_parts), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.parts == 1 && p.sink_parts == 0)) return e;
   hipLaunchKernelGGL((attn_dkv_sum_kernel<T, D>), dim3(p.parts > 1 ? p.ktiles * p.key_heads : sinks), dim3(256), 0, s, p);
@@ -423,11 +437,11 @@ hipError_t launch_attention_backward(const AttnParams &p, bool bf16, hipStream_t
   const hipError_t e = launch_attention_plan(p, s);
   if (e != hipSuccess) return e;
   if (bf16) {
-    if (p.d == 64) return go<__bf16, 64, 2, 64, 2, 64>(p, s);
-    return p.d == 128 ? go<__bf16, 128, 2, 32, 2, 32>(p, s) : go<__bf16, 256, 1, 32, 1, 32>(p, s);
+    if (p.d == 64) return go<__bf16, 64, 2, 64, 3, 2, 64, 2>(p, s);
+    return p.d == 128 ? go<__bf16, 128, 2, 32, 2, 2, 32, 1>(p, s) : go<__bf16, 256, 1, 32, 2, 1, 32, 1>(p, s);
   }
-  if (p.d == 64) return go<float, 64, 2, 32, 2, 32>(p, s);
-  return p.d == 128 ? go<float, 128, 2, 32, 1, 32>(p, s) : go<float, 256, 1, 32, 1, 32>(p, s);
+  if (p.d == 64) return go<float, 64, 2, 32, 2, 2, 32, 1>(p, s);
+  return p.d == 128 ? go<float, 128, 2, 32, 1, 1, 32, 1>(p, s) : go<float, 256, 1, 32, 1, 1, 32, 1>(p, s);
 }
 
 }  // namespace ttt

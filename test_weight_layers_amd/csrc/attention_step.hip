@@ -185,30 +185,44 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_step_ke
   }
 }
 
-// Joins the ranges of keys, in their order, and writes the tokens: workgroups (row, part of its outputs).
+// Joins the ranges of keys and writes the tokens: a workgroup a row and head, D / 4 lanes an output and 1024 / D interleaved
+// parts of the ranges, added in order.
 template <typename T, int D> __global__ __launch_bounds__(256) void attn_step_join_kernel(AttnStepParams p) {
-  const int row = blockIdx.x, t = blockIdx.y * 256 + threadIdx.x;
+  constexpr int L = D / 4, G = 256 / L;
+  __shared__ __attribute__((aligned(16))) float s_o[G][D];
+  __shared__ float s_m[G], s_l[G];
+  const int row = blockIdx.x, h = blockIdx.y, c = threadIdx.x % L, g = threadIdx.x / L;
   const int2 at = step_row(p, row);
-  T *out = static_cast<T *>(p.o) + (int64_t)row * p.ldo;
-  if (t * 4 < p.heads * D) {
-    const int h = t * 4 / D;
-    if (at.x < 0) {
-      if (p.zero_unused) store4(out + 4 * t, zero_f4());
-    } else {
-      const int64_t first = (int64_t)row * p.heads + h, step = (int64_t)p.n * p.heads;
-      float m = -__builtin_inff(), sum = 0.0f;
-      for (int i = 0; i < p.splits; ++i) m = fmaxf(m, p.part_ml[first + i * step].x);
-      f32x4 o = zero_f4();
-      for (int i = 0; i < p.splits; ++i) {
-        const float2 ml = p.part_ml[first + i * step];
-        const float w = ml.x == m ? 1.0f : __builtin_amdgcn_exp2f((ml.x - m) * (p.scale * kLog2e));
-        sum += ml.y * w;
-        o += *reinterpret_cast<const f32x4 *>(p.part_o + (first + i * step) * D + 4 * t % D) * w;
-      }
-      store4(out + 4 * t, o * (1.0f / sum));
-    }
+  T *out = static_cast<T *>(p.o) + (int64_t)row * p.ldo + (int64_t)h * D + 4 * c;
+  if (at.x < 0) {
+    if (p.zero_unused && g == 0) store4(out, zero_f4());
+    return;
   }
-  if (blockIdx.y != 0 || at.x < 0) return;
+  const float c2 = p.scale * kLog2e;
+  const int64_t first = (int64_t)row * p.heads + h, step = (int64_t)p.n * p.heads;
+  float m = -__builtin_inff(), sum = 0.0f;
+  f32x4 o = zero_f4();
+  for (int i = g; i < p.splits; i += G) {
+    const float2 ml = p.part_ml[first + i * step];
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(p.part_o + (first + i * step) * D + 4 * c);
+    const float top = fmaxf(m, ml.x);
+    const float a = m == top ? 1.0f : __builtin_amdgcn_exp2f((m - top) * c2), b = ml.x == top ? 1.0f : __builtin_amdgcn_exp2f((ml.x - top) * c2);
+    m = top, sum = sum * a + ml.y * b, o = o * a + x * b;
+  }
+  *reinterpret_cast<f32x4 *>(&s_o[g][4 * c]) = o;
+  if (c == 0) s_m[g] = m, s_l[g] = sum;
+  __syncthreads();
+  if (g == 0) {
+    for (int i = 1; i < G; ++i) m = fmaxf(m, s_m[i]);
+    sum = 0.0f, o = zero_f4();
+    for (int i = 0; i < G; ++i) {
+      const float a = s_m[i] == m ? 1.0f : __builtin_amdgcn_exp2f((s_m[i] - m) * c2);
+      sum += s_l[i] * a;
+      o += *reinterpret_cast<const f32x4 *>(&s_o[i][4 * c]) * a;
+    }
+    store4(out, o * (1.0f / sum));
+  }
+  if (h != 0) return;
   // of rows with the same place the last is written
   const int place = place_of(p, at.y);
   bool later = false;
@@ -233,7 +247,7 @@ template <typename T, int D> hipError_t go(const AttnStepParams &p, hipStream_t 
   hipLaunchKernelGGL((attn_step_kernel<T, D>), dim3(p.n * p.key_heads * ((grp + 15) / 16) * p.splits), dim3(256), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_step_join_kernel<T, D>), dim3(p.n, (p.heads * D / 4 + 255) / 256), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_step_join_kernel<T, D>), dim3(p.n, p.heads), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

@@ -10,6 +10,7 @@
 #pragma once
 #include "attention.h"
 #include "common.h"
+#include "dma.h"
 
 namespace ttt {
 
@@ -43,16 +44,17 @@ template <typename T, int D> struct AttnTile {
     }
   }
   // Fetches ROWS rows (the first `valid` exist, the others become zero) from memory, `ld` elements apart.
-  // All four waves call this; the copies are asynchronous.
+  // All four waves call this.  The copies are asynchronous and not counted by the compiler: landed() before the barrier
+  // behind which they are read.
   template <int ROWS> static __device__ __forceinline__ void fetch(const T *src, int64_t ld, int valid, unsigned char *t) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const unsigned step = (unsigned)(ld * (int64_t)sizeof(T));
-    const __amdgpu_buffer_rsrc_t view = buffer_view(src, valid > 0 ? (unsigned)(valid - 1) * step + kRow : 0);
+    const BufferView view = untracked_view(src, valid > 0 ? (unsigned)(valid - 1) * step + kRow : 0);
     static_assert(ROWS * kRow % 4096 == 0, "a whole number of copies a wave");
 #pragma unroll
     for (int i = 0; i < ROWS * kRow / 4096; ++i) {
       const int first = (i * 4 + wave) * 64, unit = first + lane, r = unit / kUnits, pos = unit % kUnits;
-      copy16_to_lds(view, (unsigned)r * step + ((pos ^ swz(r)) << 4), t + first * 16);
+      copy_to_lds_untracked<16>(view, (unsigned)r * step + ((pos ^ swz(r)) << 4), t + first * 16);
     }
   }
   // Zeros in place of what is not finite, rows r0 .. r0 + n - 1 (all 256 threads).
@@ -64,6 +66,15 @@ template <typename T, int D> struct AttnTile {
     }
   }
 };
+
+// Stands in a branch that few tiles take: without it the compiler turns the masks into selects for every tile.
+__device__ __forceinline__ void rarely() { asm volatile("s_nop 0"); }
+
+// Waits for this wave's copies to LDS, then for the other waves.
+__device__ __forceinline__ void landed() {
+  wait_vmcnt<0>();
+  __syncthreads();
+}
 
 template <typename T> __device__ __forceinline__ typename FragOf<T>::type pack44(const f32x4 a, const f32x4 b) {
   const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
