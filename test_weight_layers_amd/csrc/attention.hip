@@ -52,14 +52,15 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
   const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
   const int first = (int)((int64_t)nt * split / p.splits), end = (int)((int64_t)nt * (split + 1) / p.splits);
+  const unsigned off_k = Tile::lane_offset(p.ldk), off_v = Tile::lane_offset(p.ldv);
   const auto range = [&](int t) {
     const int j = t < ns ? t * BK : k0 + (t - ns) * BK, e = t < ns ? se : k1;
     return int2{j, j + BK < e ? j + BK : e};
   };
   const auto fetch = [&](int t) {
     const int2 r = range(t);
-    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, s_k[t & 1]);
-    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, s_v[t & 1]);
+    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, off_k, s_k[t & 1]);
+    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, off_v, s_v[t & 1]);
   };
 
   const float c2 = p.scale * kLog2e;
@@ -122,8 +123,6 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
           for (int u = 0; u < NU; ++u)
 #pragma unroll
             for (int x = 0; x < 4; ++x) mx[c] = fmaxf(mx[c], sc[u][c][x]);
-          mx[c] = fmaxf(mx[c], __shfl_xor(mx[c], 16));
-          mx[c] = fmaxf(mx[c], __shfl_xor(mx[c], 32));
           up |= (mx[c] - m[c]) * c2 > 8.0f;
         }
         // the sums are kept relative to m, which follows a column's maximum only where that grew by more than 2^8: P
@@ -131,6 +130,7 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
         if (__any(up)) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
+            mx[c] = column_max(mx[c]);
             const float to = (mx[c] - m[c]) * c2 > 8.0f ? mx[c] : m[c], a = to == m[c] ? 1.0f : __builtin_amdgcn_exp2f((m[c] - to) * c2);
             m[c] = to, sum[c] *= a;
             huge |= fabsf(to) * c2 > kHuge && to > -__builtin_inff();

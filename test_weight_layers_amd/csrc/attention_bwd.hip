@@ -72,14 +72,15 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
   const int k0 = seen_keys(p, s, t0).x, k1 = seen_keys(p, s, last - 1).y, se = p.sinks < k0 ? p.sinks : k0;
   const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
+  const unsigned off_k = Tile::lane_offset(p.ldk), off_v = Tile::lane_offset(p.ldv);
   const auto range = [&](int t) {
     const int j = t < ns ? t * BK : k0 + (t - ns) * BK, e = t < ns ? se : k1;
     return int2{j, j + BK < e ? j + BK : e};
   };
   const auto fetch = [&](int t) {
     const int2 r = range(t);
-    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, s_k[t & 1]);
-    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, s_v[t & 1]);
+    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, off_k, s_k[t & 1]);
+    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, off_v, s_v[t & 1]);
   };
   const float c2 = p.scale * kLog2e;
   f32x4 dq[ND][NC];
@@ -220,6 +221,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   // a head's tiles: na over the window [ta.x, tb.y), nb over what is behind the first key's window [ta.y, ql)
   const int na = sink_item ? 0 : tiles_of(tb.y - ta.x, BQ), nb = with_sinks ? tiles_of(s.ql - ta.y, BQ) : 0, per = na + nb;
   const int first = (int)((int64_t)per * grp * part / parts), end = (int)((int64_t)per * grp * (part + 1) / parts);
+  const unsigned off_q = Tile::lane_offset(p.ldq), off_o = Tile::lane_offset(p.ldgo);
   const auto range = [&](int t) {                     // its rows, in the window or not
     const int x = t % per;
     const int i = x < na ? ta.x + x * BQ : ta.y + (x - na) * BQ, e = x < na ? tb.y : s.ql;
@@ -229,8 +231,8 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
     const int2 r = range(t);
     const int h = kh * grp + t / per, n = r.y - r.x;
     const int64_t row = s.qs + r.x;
-    Tile::template fetch<BQ>(static_cast<const T *>(p.q) + row * p.ldq + h * D, p.ldq, n, s_q[t & 1]);
-    Tile::template fetch<BQ>(static_cast<const T *>(p.go) + row * p.ldgo + h * D, p.ldgo, n, s_o[t & 1]);
+    Tile::template fetch<BQ>(static_cast<const T *>(p.q) + row * p.ldq + h * D, p.ldq, n, off_q, s_q[t & 1]);
+    Tile::template fetch<BQ>(static_cast<const T *>(p.go) + row * p.ldgo + h * D, p.ldgo, n, off_o, s_o[t & 1]);
     if (wave < 2) {                                   // 64 values each (zeros behind the last)
       const BufferView view = untracked_view((wave ? p.delta : p.lse) + (int64_t)h * p.nq + row, n * 4);
       copy_to_lds_untracked<4>(view, l * 4, reinterpret_cast<unsigned char *>(wave ? s_del[t & 1] : s_lse[t & 1]));

@@ -43,18 +43,28 @@ template <typename T, int D> struct AttnTile {
       return v;
     }
   }
-  // Fetches ROWS rows (the first `valid` exist, the others become zero) from memory, `ld` elements apart.
-  // All four waves call this.  The copies are asynchronous and not counted by the compiler: landed() before the barrier
-  // behind which they are read.
-  template <int ROWS> static __device__ __forceinline__ void fetch(const T *src, int64_t ld, int valid, unsigned char *t) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  // A thread's byte offset in the rows that it copies, `ld` elements apart: its unit of a wave's first copy.
+  static __device__ __forceinline__ unsigned lane_offset(int64_t ld) {
+    const int r = threadIdx.x / kUnits, pos = threadIdx.x % kUnits;
+    return (unsigned)r * (unsigned)(ld * (int64_t)sizeof(T)) + ((pos ^ swz(r)) << 4);
+  }
+  // Fetches ROWS rows (the first `valid` exist, the others become zero) from memory: four waves, a KB each at a time, every
+  // copy a multiple of 8 rows behind the one before, where units lie in the same order (rows of 1 KB: of 4, where units
+  // change places with those 8 away).
+  // The copies are asynchronous and not counted by the compiler: landed() before the barrier behind which they are read.
+  template <int ROWS>
+  static __device__ __forceinline__ void fetch(const T *src, int64_t ld, int valid, unsigned lane_off, unsigned char *t) {
+    constexpr int kStep = 4096 / kRow;
+    static_assert(ROWS % kStep == 0 && kStep % (kUnits == 8 ? 8 : 4) == 0, "");
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const unsigned step = (unsigned)(ld * (int64_t)sizeof(T));
-    const BufferView view = untracked_view(src, valid > 0 ? (unsigned)(valid - 1) * step + kRow : 0);
-    static_assert(ROWS * kRow % 4096 == 0, "a whole number of copies a wave");
 #pragma unroll
-    for (int i = 0; i < ROWS * kRow / 4096; ++i) {
-      const int first = (i * 4 + wave) * 64, unit = first + lane, r = unit / kUnits, pos = unit % kUnits;
-      copy_to_lds_untracked<16>(view, (unsigned)r * step + ((pos ^ swz(r)) << 4), t + first * 16);
+    for (int i = 0; i < ROWS / kStep; ++i) {
+      const int left = valid - i * kStep;
+      const BufferView view = untracked_view(reinterpret_cast<const char *>(src) + (int64_t)i * kStep * step,
+                                             left > 0 ? (unsigned)(left - 1) * step + kRow : 0);
+      const unsigned off = kStep % 8 == 0 || i % 2 == 0 ? lane_off : lane_off + (((threadIdx.x % kUnits) ^ swz(threadIdx.x / kUnits)) & 8 ? -128 : 128);
+      copy_to_lds_untracked<16>(view, off, t + (i * 4 + wave) * 1024);
     }
   }
   // Zeros in place of what is not finite, rows r0 .. r0 + n - 1 (all 256 threads).
@@ -186,6 +196,12 @@ __device__ __forceinline__ int2 seeing_queries(const AttnParams &p, const AttnSe
   const int64_t b = j / p.block, off = s.kl - s.ql;
   return int2{p.after < 0 ? 0 : clamp_to((b - p.after) * p.block - off, s.ql),
               p.before < 0 ? s.ql : clamp_to((b + p.before + 1) * p.block - off, s.ql)};
+}
+
+// The largest of a column's four lanes (16 apart), in each of them.
+__device__ __forceinline__ float column_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
 }
 
 // Work items in launch order go round the 8 XCDs: consecutive items (tiles of one head) on one XCD.

@@ -16,7 +16,9 @@ __device__ __forceinline__ void copy16_to_lds_untracked(const void *gsrc, unsign
 }
 
 // The same through a raw buffer view (wave-uniform base and byte range): BYTES (16 or 4) a lane from its own byte offset,
-// zeros past the range.
+// zeros past the range.  The view's registers may come from VALU instructions (readfirstlane, or a spill's readlane), which a
+// memory instruction may read only five wait states later: the compiler, which inserts these elsewhere, does not look into
+// the asm, so they stand in it.
 typedef uint32_t BufferView __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ BufferView untracked_view(const void *base, unsigned bytes) {
   const uint64_t b = (uint64_t)(uintptr_t)base;
@@ -29,9 +31,9 @@ __device__ __forceinline__ void copy_to_lds_untracked(BufferView view, unsigned 
   static_assert(BYTES == 16 || BYTES == 4, "");
   const unsigned m0v = (unsigned)(uintptr_t)(__attribute__((address_space(3))) unsigned char *)lds_wave_base;
   if constexpr (BYTES == 16)
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voffset), "s"(view), "{m0}"(m0v) : "memory");
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voffset), "s"(view), "{m0}"(m0v) : "memory");
   else
-    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voffset), "s"(view), "{m0}"(m0v) : "memory");
+    asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voffset), "s"(view), "{m0}"(m0v) : "memory");
 }
 
 }  // namespace ttt
