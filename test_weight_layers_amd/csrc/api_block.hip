@@ -82,11 +82,13 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     const int64_t wgs = tiles(a.nk, P.krows) * a.key_heads, queries = std::min(lq, window + P.krows);
     if (wgs > 0 && wgs < 256) P.parts = (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, queries * grp / 256, 64}));
     if (P.parts > 1) P.off_part = take((size_t)P.parts * a.nk * a.key_heads * 2 * a.d * 4);
-    // sinks that far more queries see than the window of a key
-    if (a.sinks > 0 && a.before >= 0 && lq > 4 * (window + P.krows)) {
+    // Sinks, which all queries behind their window see: ranges of these of their own, where a sequence may be long beside
+    // the window (lengths are on the device: taken as four times the mean), joined with the window's part by the sums' kernel.
+    if (a.sinks > 0 && a.before >= 0 && a.nq > 2 * (window + P.krows)) {
       P.sink_tiles = (int)ceil_div(std::min<int64_t>(a.sinks, a.nk), P.krows);
-      P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>(64, lq * grp / std::max<int64_t>(window * grp, 1024)));
-      P.off_spart = take((size_t)a.nseq * P.sink_tiles * a.key_heads * (1 + P.sink_parts) * P.krows * 2 * a.d * 4);
+      const int64_t one = (int64_t)a.nseq * P.sink_tiles * a.key_heads * P.krows * 2 * a.d * 4;
+      P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>({32, std::min(a.nq, 4 * lq) * grp / std::max<int64_t>(window * grp / 2, 512), (int64_t(64) << 20) / one}));
+      P.off_spart = take((size_t)one * (1 + P.sink_parts));
     }
   }
   const int64_t qt = tiles(a.nq, P.qrows), kt = tiles(a.nk, P.krows);

@@ -8,13 +8,14 @@ namespace {
 
 constexpr int kZeroBlocks = 32;     // workgroups that fill rows of no sequence
 
-// Four waves of NC x 16 queries each; BK keys at a time through two LDS buffers.
-template <typename T, int D, int NC, int BK, int OCC>
+// Four waves of NC x 16 queries each; BK keys at a time through STAGES LDS buffers.
+template <typename T, int D, int NC, int BK, int STAGES, int OCC>
 __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
   typedef AttnTile<T, D> Tile;
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, NU = BK / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
-  __shared__ __attribute__((aligned(256))) unsigned char s_k[2][kTile], s_v[2][kTile];
+  constexpr int kCopies = 2 * kTile / 4096;           // of a wave for a tile
+  __shared__ __attribute__((aligned(256))) unsigned char s_k[STAGES][kTile], s_v[STAGES][kTile];
   const int items = p.qtiles * p.heads * p.splits;
   if ((int)blockIdx.x >= items) {
     const int blk = blockIdx.x - items;
@@ -30,8 +31,10 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
   const int h = rest / p.qtiles, kh = h / (p.heads / p.key_heads);
   AttnSeq s;
   int tile, seq;
-  // late tiles first: without a window they see the most keys
-  if (!tile_of<false>(p, p.qtiles - 1 - rest % p.qtiles, &s, &tile, &seq)) return;
+  // Without a window late tiles see the most keys: the late half first, then the early half from its first tile on, so
+  // that a CU that takes one of each has as much to do as the others.
+  const int order = rest % p.qtiles, half = (p.qtiles + 1) / 2;
+  if (!tile_of<false>(p, order < half ? p.qtiles - 1 - order : order - half, &s, &tile, &seq)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g = l >> 4, li = l & 15;
   const int t0 = tile * QR, row0 = t0 + wave * 16 * NC;
   const T *kb = static_cast<const T *>(p.k) + (int64_t)s.ks * p.ldk + kh * D;
@@ -57,10 +60,10 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
     const int j = t < ns ? t * BK : k0 + (t - ns) * BK, e = t < ns ? se : k1;
     return int2{j, j + BK < e ? j + BK : e};
   };
-  const auto fetch = [&](int t) {
+  const auto fetch = [&](int t, int stage) {
     const int2 r = range(t);
-    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, off_k, s_k[t & 1]);
-    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, off_v, s_v[t & 1]);
+    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, off_k, s_k[stage]);
+    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, off_v, s_v[stage]);
   };
 
   const float c2 = p.scale * kLog2e;
@@ -77,15 +80,19 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
       for (int d = 0; d < ND; ++d) o[d][c] = zero_f4();
     }
     __syncthreads();
-    if (first < end) fetch(first);
-    for (int t = first; t < end; ++t) {
-      landed();                                       // this tile, and nobody reads the other buffer
-      if (t + 1 < end) fetch(t + 1);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+      if (first + i < end) fetch(first + i, i);
+    int stage = 0;
+    for (int t = first; t < end; ++t, stage = stage + 1 == STAGES ? 0 : stage + 1) {
+      // this tile is there, and nobody reads the one before it any more
+      if (t + STAGES - 2 < end) landed<(STAGES - 2) * kCopies>(); else landed<0>();
+      if (t + STAGES - 1 < end) fetch(t + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
       const int2 r = range(t);
       const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
       const bool none = !(r.x < wb.y && (r.y > wa.x || r.x < p.sinks));
-      const unsigned char *kt = s_k[t & 1];
-      unsigned char *vt = s_v[t & 1];
+      const unsigned char *kt = s_k[stage];
+      unsigned char *vt = s_v[stage];
       Frag pr[NU / 2][NC];
       if (!none) {
         f32x4 sc[NU][NC];
@@ -293,9 +300,9 @@ __global__ __launch_bounds__(1024) void attn_plan_kernel(AttnParams p) {
   }
 }
 
-template <typename T, int D, int NC, int BK, int OCC> hipError_t go(const AttnParams &p, hipStream_t s) {
+template <typename T, int D, int NC, int BK, int STAGES, int OCC> hipError_t go(const AttnParams &p, hipStream_t s) {
   const int items = p.qtiles * p.heads * p.splits;
-  hipLaunchKernelGGL((attn_forward_kernel<T, D, NC, BK, OCC>), dim3(items + (p.cu_q ? kZeroBlocks : 0)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_forward_kernel<T, D, NC, BK, STAGES, OCC>), dim3(items + (p.cu_q ? kZeroBlocks : 0)), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1 || p.nq == 0) return e;
   hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)(((int64_t)p.nq * p.heads + 1024 / D - 1) / (1024 / D))), dim3(256),
@@ -319,13 +326,13 @@ hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s) {
   if (e != hipSuccess) return e;
   const bool small = p.qrows == 64;
   if (bf16) {
-    if (p.d == 64) return small ? go<__bf16, 64, 1, 64, 4>(p, s) : go<__bf16, 64, 2, 64, 3>(p, s);
-    if (p.d == 128) return small ? go<__bf16, 128, 1, 64, 2>(p, s) : go<__bf16, 128, 2, 64, 2>(p, s);
-    return small ? go<__bf16, 256, 1, 32, 2>(p, s) : go<__bf16, 256, 2, 32, 2>(p, s);
+    if (p.d == 64) return small ? go<__bf16, 64, 1, 64, 3, 3>(p, s) : go<__bf16, 64, 2, 64, 3, 3>(p, s);
+    if (p.d == 128) return small ? go<__bf16, 128, 1, 64, 2, 2>(p, s) : go<__bf16, 128, 2, 64, 2, 2>(p, s);
+    return small ? go<__bf16, 256, 1, 32, 2, 2>(p, s) : go<__bf16, 256, 2, 32, 2, 1>(p, s);
   }
-  if (p.d == 64) return small ? go<float, 64, 1, 32, 4>(p, s) : go<float, 64, 2, 32, 3>(p, s);
-  if (p.d == 128) return small ? go<float, 128, 1, 32, 2>(p, s) : go<float, 128, 2, 32, 2>(p, s);
-  return go<float, 256, 1, 32, 1>(p, s);
+  if (p.d == 64) return small ? go<float, 64, 1, 32, 3, 3>(p, s) : go<float, 64, 2, 32, 3, 2>(p, s);
+  if (p.d == 128) return small ? go<float, 128, 1, 32, 2, 2>(p, s) : go<float, 128, 2, 32, 2, 1>(p, s);
+  return go<float, 256, 1, 32, 2, 1>(p, s);
 }
 
 }  // namespace ttt

@@ -377,9 +377,10 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   }
 }
 
-// The sums over ranges of queries, in their order: a workgroup a key tile (of sinks only, where the window is one range)
-// and key head, D / 2 lanes a row.
+// The sums over ranges of queries, in their order: a key tile (of sinks only, where the window is one range) and key head by
+// blockIdx.x, 512 / D of its rows by blockIdx.y, D / 2 lanes a row.
 template <typename T, int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(AttnParams p) {
+  constexpr int L = D / 2;
   AttnSeq s;
   int tile, seq;
   const int kh = blockIdx.x % p.key_heads, x = blockIdx.x / p.key_heads;
@@ -389,24 +390,25 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_dkv_sum
     tile = x % p.sink_tiles, seq = x / p.sink_tiles;
     s = seq_of(p, seq);
   }
-  const bool apart = p.sink_parts > 0 && tile < p.sink_tiles;
-  constexpr int L = D / 2;
-  const int c = threadIdx.x % L * 4;
-  for (int r = threadIdx.x / L; r < p.krows && tile * p.krows + r < s.kl; r += 256 / L) {
-    const int64_t row = s.ks + tile * p.krows + r;
-    f32x4 v = zero_f4();
-    if (p.parts > 1)
-      for (int i = 0; i < p.parts; ++i)
-        v += *reinterpret_cast<const f32x4 *>(p.part + (((int64_t)i * p.nk + row) * p.key_heads + kh) * 2 * D + c);
-    if (apart)
-      for (int i = p.parts > 1 ? 1 : 0; i <= p.sink_parts; ++i)
-        v += *reinterpret_cast<const f32x4 *>(
-            p.spart + (((((int64_t)seq * p.sink_tiles + tile) * p.key_heads + kh) * (1 + p.sink_parts) + i) * p.krows + r) * 2 * D + c);
-    if (c < D)
-      store4(static_cast<T *>(p.gk) + row * p.ldgk + kh * D + c, v);
-    else
-      store4(static_cast<T *>(p.gv) + row * p.ldgv + kh * D + c - D, v);
+  const int c = threadIdx.x % L * 4, r = blockIdx.y * (256 / L) + threadIdx.x / L;
+  if (tile * p.krows + r >= s.kl) return;
+  const int64_t row = s.ks + tile * p.krows + r;
+  f32x4 v = zero_f4();
+  const float *a = p.part + (row * p.key_heads + kh) * 2 * D + c;
+  const int64_t step = (int64_t)p.nk * p.key_heads * 2 * D;
+  if (p.parts > 1)
+#pragma unroll 4
+    for (int i = 0; i < p.parts; ++i) v += *reinterpret_cast<const f32x4 *>(a + i * step);
+  if (p.sink_parts > 0 && tile < p.sink_tiles) {
+    const float *b = p.spart + (((((int64_t)seq * p.sink_tiles + tile) * p.key_heads + kh) * (1 + p.sink_parts)) * p.krows + r) * 2 * D + c;
+    const int64_t next = (int64_t)p.krows * 2 * D;
+#pragma unroll 4
+    for (int i = p.parts > 1 ? 1 : 0; i <= p.sink_parts; ++i) v += *reinterpret_cast<const f32x4 *>(b + i * next);
   }
+  if (c < D)
+    store4(static_cast<T *>(p.gk) + row * p.ldgk + kh * D + c, v);
+  else
+    store4(static_cast<T *>(p.gv) + row * p.ldgv + kh * D + c - D, v);
 }
 
 template <typename T, int D, int NC, int BK, int OCC, int NCK, int BQ, int OCCK> hipError_t go(const AttnParams &p, hipStream_t s) {
@@ -426,7 +428,8 @@ template <typename T, int D, int NC, int BK, int OCC, int NCK, int BQ, int OCCK>
   hipLaunchKernelGGL((attn_dkv_kernel<T, D, NCK, BQ, OCCK>), dim3(p.ktiles * p.key_heads * p.parts + sinks * p.sink_parts), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.parts == 1 && p.sink_parts == 0)) return e;
-  hipLaunchKernelGGL((attn_dkv_sum_kernel<T, D>), dim3(p.parts > 1 ? p.ktiles * p.key_heads : sinks), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_dkv_sum_kernel<T, D>), dim3(p.parts > 1 ? p.ktiles * p.key_heads : sinks, p.krows * D / 512), dim3(256), 0,
+                     s, p);
   return hipGetLastError();
 }
 

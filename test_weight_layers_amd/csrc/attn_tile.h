@@ -80,10 +80,11 @@ template <typename T, int D> struct AttnTile {
 // Stands in a branch that few tiles take: without it the compiler turns the masks into selects for every tile.
 __device__ __forceinline__ void rarely() { asm volatile("s_nop 0"); }
 
-// Waits for this wave's copies to LDS, then for the other waves.
-__device__ __forceinline__ void landed() {
-  wait_vmcnt<0>();
-  __syncthreads();
+// Waits for this wave's copies to LDS but the last LEFT, then for the other waves.
+// (__syncthreads would wait for all of them.)
+template <int LEFT = 0> __device__ __forceinline__ void landed() {
+  wait_vmcnt_lds<LEFT>();
+  bare_barrier();
 }
 
 template <typename T> __device__ __forceinline__ typename FragOf<T>::type pack44(const f32x4 a, const f32x4 b) {
