@@ -70,7 +70,7 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     P.qrows = attn_query_rows(a.d, bf16, small);
     P.krows = 64;
     const int64_t wgs = tiles(a.nq, P.qrows) * a.heads, keys = std::min(lk, window + P.qrows + a.sinks);
-    if (wgs > 0 && wgs < 256) P.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, keys / 256, 64}));
+    P.splits = attn_splits(wgs, a.nq, a.heads, a.d, P.qrows, keys, bf16);
     if (P.splits > 1) {
       P.off_o = take((size_t)P.splits * a.heads * a.nq * a.d * 4);
       P.off_ml = take((size_t)P.splits * a.heads * a.nq * 8);

@@ -8,16 +8,20 @@ namespace {
 
 constexpr int kZeroBlocks = 32;     // workgroups that fill rows of no sequence
 
-// Four waves of NC x 16 queries each; BK keys at a time through STAGES LDS buffers.
-template <typename T, int D, int NC, int BK, int STAGES, int OCC>
-__global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
+// Four waves of NC x 16 queries each; BK keys at a time through two LDS buffers.  KG = 2: eight waves, the second four with
+// the same queries and every other tile of keys, joined at the end: where there are few query tiles a SIMD then has two
+// waves that wait in turn.
+template <typename T, int D, int NC, int BK, int KG, int OCC>
+__global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams p) {
   typedef AttnTile<T, D> Tile;
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, NU = BK / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
-  constexpr int kCopies = 2 * kTile / 4096;           // of a wave for a tile
-  __shared__ __attribute__((aligned(256))) unsigned char s_k[STAGES][kTile], s_v[STAGES][kTile];
+  constexpr int kPitch = D + 4;                       // floats of a query's row of the second four waves' sums
+  __shared__ __attribute__((aligned(256))) unsigned char s_kv[KG][2][2][kTile];
+  static_assert(KG == 1 || QR * (kPitch + 2) * 4 <= (int)sizeof(s_kv), "");
   const int items = p.qtiles * p.heads * p.splits;
   if ((int)blockIdx.x >= items) {
+    if (threadIdx.x >= 256) return;
     const int blk = blockIdx.x - items;
     const int2 used = used_rows<false>(p);
     if (p.zero_unused) zero_unused_rows<T>(used, p.nq, p.o, p.ldo, p.heads * D, blk, kZeroBlocks);
@@ -35,7 +39,8 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
   // that a CU that takes one of each has as much to do as the others.
   const int order = rest % p.qtiles, half = (p.qtiles + 1) / 2;
   if (!tile_of<false>(p, order < half ? p.qtiles - 1 - order : order - half, &s, &tile, &seq)) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g = l >> 4, li = l & 15;
+  const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3, kg = wave8 >> 2;
+  const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
   const int t0 = tile * QR, row0 = t0 + wave * 16 * NC;
   const T *kb = static_cast<const T *>(p.k) + (int64_t)s.ks * p.ldk + kh * D;
   const T *vb = static_cast<const T *>(p.v) + (int64_t)s.ks * p.ldv + kh * D;
@@ -56,14 +61,10 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
   const int first = (int)((int64_t)nt * split / p.splits), end = (int)((int64_t)nt * (split + 1) / p.splits);
   const unsigned off_k = Tile::lane_offset(p.ldk), off_v = Tile::lane_offset(p.ldv);
-  const auto range = [&](int t) {
-    const int j = t < ns ? t * BK : k0 + (t - ns) * BK, e = t < ns ? se : k1;
-    return int2{j, j + BK < e ? j + BK : e};
-  };
-  const auto fetch = [&](int t, int stage) {
-    const int2 r = range(t);
-    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, off_k, s_k[stage]);
-    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, off_v, s_v[stage]);
+  const KeyWalk<T, BK> start(first + kg, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
+  const auto fetch = [&](const KeyWalk<T, BK> &w, int stage) {
+    Tile::template fetch<BK>(w.k, p.ldk, w.end() - w.j, off_k, s_kv[kg][stage][0]);
+    Tile::template fetch<BK>(w.v, p.ldv, w.end() - w.j, off_v, s_kv[kg][stage][1]);
   };
 
   const float c2 = p.scale * kLog2e;
@@ -80,19 +81,20 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
       for (int d = 0; d < ND; ++d) o[d][c] = zero_f4();
     }
     __syncthreads();
+    KeyWalk<T, BK> ahead = start;
+    if (first + kg < end) fetch(ahead, 0);
+    // (with KG = 2 the second four waves' last tile may be none: they go along for the barriers)
+    for (int t = first, stage = 0; t < end; t += KG, stage ^= 1) {
+      const bool there = KG == 1 || t + kg < end;
+      const int2 r{ahead.j, ahead.end()};
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i)
-      if (first + i < end) fetch(first + i, i);
-    int stage = 0;
-    for (int t = first; t < end; ++t, stage = stage + 1 == STAGES ? 0 : stage + 1) {
-      // this tile is there, and nobody reads the one before it any more
-      if (t + STAGES - 2 < end) landed<(STAGES - 2) * kCopies>(); else landed<0>();
-      if (t + STAGES - 1 < end) fetch(t + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-      const int2 r = range(t);
+      for (int i = 0; i < KG; ++i) ahead.next();
+      landed();                                       // this tile is there, and nobody reads the one before it any more
+      if (t + KG + kg < end) fetch(ahead, stage ^ 1);
       const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
-      const bool none = !(r.x < wb.y && (r.y > wa.x || r.x < p.sinks));
-      const unsigned char *kt = s_k[stage];
-      unsigned char *vt = s_v[stage];
+      const bool none = !there || !(r.x < wb.y && (r.y > wa.x || r.x < p.sinks));
+      const unsigned char *kt = s_kv[kg][stage][0];
+      unsigned char *vt = s_kv[kg][stage][1];
       Frag pr[NU / 2][NC];
       if (!none) {
         f32x4 sc[NU][NC];
@@ -172,25 +174,23 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
       }
       if (careful) {
         const bool whole = r.y - r.x == BK && seen_keys(p, s, t0).y >= r.y && (seen_keys(p, s, last - 1).x <= r.x || r.y <= p.sinks);
-        if (!whole) {
-          if (!none)
-            for (int x = 0; x < BK; ++x) {
-              const int j = r.x + x;
+        if (!whole && !none)
+          for (int x = 0; x < BK; ++x) {
+            const int j = r.x + x;
 #pragma unroll
-              for (int d = 0; d < ND; ++d)
+            for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const float f = to_f32(*reinterpret_cast<const T *>(vt + Tile::elem(x, 16 * d + 4 * g + y)));
-                  if (fabsf(f) < __builtin_inff()) continue;
+              for (int y = 0; y < 4; ++y) {
+                const float f = to_f32(*reinterpret_cast<const T *>(vt + Tile::elem(x, 16 * d + 4 * g + y)));
+                if (fabsf(f) < __builtin_inff()) continue;
 #pragma unroll
-                  for (int c = 0; c < NC; ++c)
-                    if (j < r.y && j < hi[c] && (j >= lo[c] || j < p.sinks)) o[d][c][y] += f;
-                }
-            }
-          __syncthreads();
-          Tile::settle(vt, 0, BK);
-          __syncthreads();
-        }
+                for (int c = 0; c < NC; ++c)
+                  if (j < r.y && j < hi[c] && (j >= lo[c] || j < p.sinks)) o[d][c][y] += f;
+              }
+          }
+        __syncthreads();
+        if (!whole && there) Tile::settle(vt, 0, BK);
+        __syncthreads();
       }
       if (!none) {
 #pragma unroll
@@ -216,6 +216,35 @@ __global__ __launch_bounds__(256, OCC) void attn_forward_kernel(AttnParams p) {
   for (int c = 0; c < NC; ++c) {
     sum[c] += __shfl_xor(sum[c], 16);
     sum[c] += __shfl_xor(sum[c], 32);
+  }
+  if constexpr (KG == 2) {                            // (nobody reads the tiles behind the barrier above)
+    float *so = reinterpret_cast<float *>(s_kv);      // a query's sums, then its m and sum
+    if (kg == 1)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float *to = so + (wave * 16 * NC + 16 * c + li) * (kPitch + 2);
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) to[16 * d + 4 * g + x] = o[d][c][x];
+        if (g == 0) to[kPitch] = m[c], to[kPitch + 1] = sum[c];
+      }
+    __syncthreads();
+    if (kg == 1) return;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const float *from = so + (wave * 16 * NC + 16 * c + li) * (kPitch + 2);
+      const float m2 = from[kPitch], top = fmaxf(m[c], m2);
+      const float a = m[c] == top ? 1.0f : __builtin_amdgcn_exp2f((m[c] - top) * c2), b = m2 == top ? 1.0f : __builtin_amdgcn_exp2f((m2 - top) * c2);
+      m[c] = top, sum[c] = sum[c] * a + from[kPitch + 1] * b;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[d][c][x] = o[d][c][x] * a + from[16 * d + 4 * g + x] * b;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
     const int i = row0 + 16 * c + li;
     if (i >= s.ql) continue;
     const bool empty = hi[c] == lo[c] && (p.sinks == 0 || lo[c] == 0);
@@ -300,9 +329,9 @@ __global__ __launch_bounds__(1024) void attn_plan_kernel(AttnParams p) {
   }
 }
 
-template <typename T, int D, int NC, int BK, int STAGES, int OCC> hipError_t go(const AttnParams &p, hipStream_t s) {
+template <typename T, int D, int NC, int BK, int KG, int OCC> hipError_t go(const AttnParams &p, hipStream_t s) {
   const int items = p.qtiles * p.heads * p.splits;
-  hipLaunchKernelGGL((attn_forward_kernel<T, D, NC, BK, STAGES, OCC>), dim3(items + (p.cu_q ? kZeroBlocks : 0)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_forward_kernel<T, D, NC, BK, KG, OCC>), dim3(items + (p.cu_q ? kZeroBlocks : 0)), dim3(256 * KG), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1 || p.nq == 0) return e;
   hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)(((int64_t)p.nq * p.heads + 1024 / D - 1) / (1024 / D))), dim3(256),
@@ -313,6 +342,25 @@ template <typename T, int D, int NC, int BK, int STAGES, int OCC> hipError_t go(
 }  // namespace
 
 int attn_query_rows(int d, bool bf16, bool small) { return small || (!bf16 && d == 256) ? 64 : 128; }
+
+// Ranges that the keys of a query tile are cut in: the rounds that the workgroups of all ranges take on 256 CUs, each for a
+// range's share of the time of a tile's keys at the rate that full CUs reach, and what the join reads and writes (at 4.5 TB/s,
+// with a launch of 4 us).  10992 queries, 8 heads of 128, 17k keys each: 688 workgroups in two rounds of 512, 680 us; in two
+// ranges three rounds of half the time.
+int attn_splits(int64_t workgroups, int64_t nq, int heads, int d, int rows, int64_t keys, bool bf16) {
+  const bool small = rows == 64;
+  const int per_cu = bf16 ? (d == 64 && !small ? 3 : d == 256 ? 1 : 2) : d == 64 ? 2 : 1;
+  const double rate = bf16 ? (d == 64 ? 850e6 : d == 128 ? 950e6 : 400e6) : (d == 64 ? 120e6 : d == 128 ? 105e6 : 55e6);   // flop per us
+  const int64_t slots = 256 * per_cu;
+  const double one = 4.0 * rows * (double)keys * d * (double)slots / rate, bytes = (double)nq * heads * d * 8;
+  int best = 1;
+  double least = (double)((workgroups + slots - 1) / slots) * one;
+  for (int s = 2; s <= 32 && keys / s >= 256; ++s) {
+    const double t = (double)((workgroups * s + slots - 1) / slots) / s * one + 4.0 + s * bytes / 4.5e6;
+    if (t < 0.95 * least) least = t, best = s;
+  }
+  return best;
+}
 
 hipError_t launch_attention_plan(const AttnParams &p, hipStream_t s) {
   if (p.cu_q == nullptr || p.nseq <= kAttnLaneSeqs) return hipSuccess;
@@ -326,13 +374,13 @@ hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s) {
   if (e != hipSuccess) return e;
   const bool small = p.qrows == 64;
   if (bf16) {
-    if (p.d == 64) return small ? go<__bf16, 64, 1, 64, 3, 3>(p, s) : go<__bf16, 64, 2, 64, 3, 3>(p, s);
-    if (p.d == 128) return small ? go<__bf16, 128, 1, 64, 2, 2>(p, s) : go<__bf16, 128, 2, 64, 2, 2>(p, s);
-    return small ? go<__bf16, 256, 1, 32, 2, 2>(p, s) : go<__bf16, 256, 2, 32, 2, 1>(p, s);
+    if (p.d == 64) return small ? go<__bf16, 64, 1, 64, 2, 4>(p, s) : go<__bf16, 64, 2, 64, 1, 3>(p, s);
+    if (p.d == 128) return small ? go<__bf16, 128, 1, 32, 2, 2>(p, s) : go<__bf16, 128, 2, 64, 1, 2>(p, s);
+    return small ? go<__bf16, 256, 1, 32, 2, 2>(p, s) : go<__bf16, 256, 2, 32, 1, 1>(p, s);
   }
-  if (p.d == 64) return small ? go<float, 64, 1, 32, 3, 3>(p, s) : go<float, 64, 2, 32, 3, 2>(p, s);
-  if (p.d == 128) return small ? go<float, 128, 1, 32, 2, 2>(p, s) : go<float, 128, 2, 32, 2, 1>(p, s);
-  return go<float, 256, 1, 32, 2, 1>(p, s);
+  if (p.d == 64) return small ? go<float, 64, 1, 32, 2, 3>(p, s) : go<float, 64, 2, 32, 1, 2>(p, s);
+  if (p.d == 128) return small ? go<float, 128, 1, 32, 2, 2>(p, s) : go<float, 128, 2, 32, 1, 1>(p, s);
+  return go<float, 256, 1, 32, 1, 1>(p, s);
 }
 
 }  // namespace ttt

@@ -73,14 +73,10 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
   const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
   const unsigned off_k = Tile::lane_offset(p.ldk), off_v = Tile::lane_offset(p.ldv);
-  const auto range = [&](int t) {
-    const int j = t < ns ? t * BK : k0 + (t - ns) * BK, e = t < ns ? se : k1;
-    return int2{j, j + BK < e ? j + BK : e};
-  };
-  const auto fetch = [&](int t) {
-    const int2 r = range(t);
-    Tile::template fetch<BK>(kb + (int64_t)r.x * p.ldk, p.ldk, r.y - r.x, off_k, s_k[t & 1]);
-    Tile::template fetch<BK>(vb + (int64_t)r.x * p.ldv, p.ldv, r.y - r.x, off_v, s_v[t & 1]);
+  const KeyWalk<T, BK> start(0, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
+  const auto fetch = [&](const KeyWalk<T, BK> &w, int stage) {
+    Tile::template fetch<BK>(w.k, p.ldk, w.end() - w.j, off_k, s_k[stage]);
+    Tile::template fetch<BK>(w.v, p.ldv, w.end() - w.j, off_v, s_v[stage]);
   };
   const float c2 = p.scale * kLog2e;
   f32x4 dq[ND][NC];
@@ -90,11 +86,13 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
 #pragma unroll
       for (int d = 0; d < ND; ++d) dq[d][c] = zero_f4();
     __syncthreads();
-    if (nt > 0) fetch(0);
+    KeyWalk<T, BK> ahead = start;
+    if (nt > 0) fetch(ahead, 0);
     for (int t = 0; t < nt; ++t) {
+      const int2 r{ahead.j, ahead.end()};
+      ahead.next();
       landed();
-      if (t + 1 < nt) fetch(t + 1);
-      const int2 r = range(t);
+      if (t + 1 < nt) fetch(ahead, (t + 1) & 1);
       const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
       const bool none = !(r.x < wb.y && (r.y > wa.x || r.x < p.sinks));
       unsigned char *kt = s_k[t & 1];
@@ -222,21 +220,30 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   const int na = sink_item ? 0 : tiles_of(tb.y - ta.x, BQ), nb = with_sinks ? tiles_of(s.ql - ta.y, BQ) : 0, per = na + nb;
   const int first = (int)((int64_t)per * grp * part / parts), end = (int)((int64_t)per * grp * (part + 1) / parts);
   const unsigned off_q = Tile::lane_offset(p.ldq), off_o = Tile::lane_offset(p.ldgo);
-  const auto range = [&](int t) {                     // its rows, in the window or not
-    const int x = t % per;
-    const int i = x < na ? ta.x + x * BQ : ta.y + (x - na) * BQ, e = x < na ? tb.y : s.ql;
-    return int2{i, i + BQ < e ? i + BQ : e};
+  struct Walk {                                       // over the heads' tiles
+    int x, i, e;                                      // tile of the head, its rows [i, min(i + BQ, e))
+    const T *q, *o;                                   // its first rows
+    const float *lse, *del;
+    __device__ __forceinline__ int end() const { return i + BQ < e ? i + BQ : e; }
   };
-  const auto fetch = [&](int t) {
-    const int2 r = range(t);
-    const int h = kh * grp + t / per, n = r.y - r.x;
-    const int64_t row = s.qs + r.x;
-    Tile::template fetch<BQ>(static_cast<const T *>(p.q) + row * p.ldq + h * D, p.ldq, n, off_q, s_q[t & 1]);
-    Tile::template fetch<BQ>(static_cast<const T *>(p.go) + row * p.ldgo + h * D, p.ldgo, n, off_o, s_o[t & 1]);
-    if (wave < 2) {                                   // 64 values each (zeros behind the last)
-      const BufferView view = untracked_view((wave ? p.delta : p.lse) + (int64_t)h * p.nq + row, n * 4);
-      copy_to_lds_untracked<4>(view, l * 4, reinterpret_cast<unsigned char *>(wave ? s_del[t & 1] : s_lse[t & 1]));
-    }
+  const auto at = [&](int h, int x) {
+    Walk w;
+    w.x = x, w.i = x < na ? ta.x + x * BQ : ta.y + (x - na) * BQ, w.e = x < na ? tb.y : s.ql;
+    const int64_t row = s.qs + w.i;
+    w.q = static_cast<const T *>(p.q) + row * p.ldq + (kh * grp + h) * D;
+    w.o = static_cast<const T *>(p.go) + row * p.ldgo + (kh * grp + h) * D;
+    w.lse = p.lse + (int64_t)(kh * grp + h) * p.nq + row, w.del = p.delta + (int64_t)(kh * grp + h) * p.nq + row;
+    return w;
+  };
+  const int64_t step_q = BQ * p.ldq, step_o = BQ * p.ldgo;
+  const int h0 = per > 0 ? first / per : 0, x0 = first - h0 * per;
+  const auto fetch = [&](const Walk &w, int stage) {
+    const int n = w.end() - w.i;
+    Tile::template fetch<BQ>(w.q, p.ldq, n, off_q, s_q[stage]);
+    Tile::template fetch<BQ>(w.o, p.ldgo, n, off_o, s_o[stage]);
+    if (wave < 2)                                     // 64 values each (zeros behind the last)
+      copy_to_lds_untracked<4>(untracked_view(wave ? w.del : w.lse, n * 4), l * 4,
+                               reinterpret_cast<unsigned char *>(wave ? s_del[stage] : s_lse[stage]));
   };
   const float c2 = p.scale * kLog2e;
   f32x4 dk[ND][NC], dv[ND][NC];
@@ -246,12 +253,20 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
 #pragma unroll
       for (int d = 0; d < ND; ++d) dk[d][c] = dv[d][c] = zero_f4();
     __syncthreads();
-    if (first < end) fetch(first);
+    int h = h0;
+    Walk ahead = at(h, x0);
+    if (first < end) fetch(ahead, first & 1);
     for (int t = first; t < end; ++t) {
+      const int2 r{ahead.i, ahead.end()};
+      const bool window = ahead.x < na;
+      if (++ahead.x == na || ahead.x == per) {
+        if (ahead.x == per) ++h, ahead.x = 0;
+        ahead = at(h, ahead.x);
+      } else {
+        ahead.i += BQ, ahead.q += step_q, ahead.o += step_o, ahead.lse += BQ, ahead.del += BQ;
+      }
       landed();
-      if (t + 1 < end) fetch(t + 1);
-      const int2 r = range(t);
-      const bool window = t % per < na;
+      if (t + 1 < end) fetch(ahead, (t + 1) & 1);
       // this wave's keys are seen by queries from .. to: by all of them [a, b), by any [x, y)
       int all_x, all_y, any_x, any_y;
       if (window) {

@@ -45,10 +45,10 @@ template <typename T, int D> struct AttnTile {
   }
   // A thread's byte offset in the rows that it copies, `ld` elements apart: its unit of a wave's first copy.
   static __device__ __forceinline__ unsigned lane_offset(int64_t ld) {
-    const int r = threadIdx.x / kUnits, pos = threadIdx.x % kUnits;
+    const int r = (threadIdx.x & 255) / kUnits, pos = threadIdx.x % kUnits;
     return (unsigned)r * (unsigned)(ld * (int64_t)sizeof(T)) + ((pos ^ swz(r)) << 4);
   }
-  // Fetches ROWS rows (the first `valid` exist, the others become zero) from memory: four waves, a KB each at a time, every
+  // Fetches ROWS rows (the first `valid` exist, the others become zero) from memory: four waves (of a workgroup of four or eight), a KB each at a time, every
   // copy a multiple of 8 rows behind the one before, where units lie in the same order (rows of 1 KB: of 4, where units
   // change places with those 8 away).
   // The copies are asynchronous and not counted by the compiler: landed() before the barrier behind which they are read.
@@ -56,20 +56,20 @@ template <typename T, int D> struct AttnTile {
   static __device__ __forceinline__ void fetch(const T *src, int64_t ld, int valid, unsigned lane_off, unsigned char *t) {
     constexpr int kStep = 4096 / kRow;
     static_assert(ROWS % kStep == 0 && kStep % (kUnits == 8 ? 8 : 4) == 0, "");
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
     const unsigned step = (unsigned)(ld * (int64_t)sizeof(T));
 #pragma unroll
     for (int i = 0; i < ROWS / kStep; ++i) {
       const int left = valid - i * kStep;
       const BufferView view = untracked_view(reinterpret_cast<const char *>(src) + (int64_t)i * kStep * step,
                                              left > 0 ? (unsigned)(left - 1) * step + kRow : 0);
-      const unsigned off = kStep % 8 == 0 || i % 2 == 0 ? lane_off : lane_off + (((threadIdx.x % kUnits) ^ swz(threadIdx.x / kUnits)) & 8 ? -128 : 128);
+      const unsigned off = kStep % 8 == 0 || i % 2 == 0 ? lane_off : lane_off + (((threadIdx.x % kUnits) ^ swz((threadIdx.x & 255) / kUnits)) & 8 ? -128 : 128);
       copy_to_lds_untracked<16>(view, off, t + (i * 4 + wave) * 1024);
     }
   }
-  // Zeros in place of what is not finite, rows r0 .. r0 + n - 1 (all 256 threads).
+  // Zeros in place of what is not finite, rows r0 .. r0 + n - 1 (four waves).
   static __device__ void settle(unsigned char *t, int r0, int n) {
-    for (int i = threadIdx.x; i < n * D; i += 256) {
+    for (int i = threadIdx.x & 255; i < n * D; i += 256) {
       T *x = reinterpret_cast<T *>(t + elem(r0 + i / D, i % D));
       const float f = to_f32(*x);
       if (!(fabsf(f) < __builtin_inff())) *x = from_f32<T>(0.0f);
@@ -204,6 +204,28 @@ __device__ __forceinline__ float column_max(float x) {
   x = fmaxf(x, __shfl_xor(x, 16));
   return fmaxf(x, __shfl_xor(x, 32));
 }
+
+// The keys of a query tile, BK at a time: sinks [0, se), then the window [k0, k1).
+template <typename T, int BK> struct KeyWalk {
+  int j, e, k0, k1;                   // the tile's first key, the end of its range, and the window
+  const T *k, *v;                     // rows of key j
+  int64_t dk, dv;                     // from a tile to the next, and to the window's first key
+  const T *kw, *vw;
+  // tile t; n_sinks: tiles of sinks
+  __device__ __forceinline__ KeyWalk(int t, int n_sinks, int se, int k0_, int k1_, const T *kb, const T *vb, int64_t ldk, int64_t ldv) {
+    k0 = k0_, k1 = k1_;
+    const bool sink = t < n_sinks;
+    j = sink ? t * BK : k0 + (t - n_sinks) * BK, e = sink ? se : k1;
+    k = kb + (int64_t)j * ldk, v = vb + (int64_t)j * ldv;
+    dk = BK * ldk, dv = BK * ldv;
+    kw = kb + (int64_t)k0 * ldk, vw = vb + (int64_t)k0 * ldv;
+  }
+  __device__ __forceinline__ int end() const { return j + BK < e ? j + BK : e; }
+  __device__ __forceinline__ void next() {
+    j += BK, k += dk, v += dv;
+    if (j >= e && e != k1) j = k0, e = k1, k = kw, v = vw;      // (sinks end before the window does)
+  }
+};
 
 // Work items in launch order go round the 8 XCDs: consecutive items (tiles of one head) on one XCD.
 __device__ __forceinline__ int attn_item(int id, int n) {
