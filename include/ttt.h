@@ -434,7 +434,7 @@ int ttt_orthogonalise(int32_t rows, int32_t cols, int32_t batch, const void *g, 
  *   of the second products.  fp32: fp32 products.
  *   The gradient takes e^(s - lse) from an fp32 lse: its relative error grows as |lse| 2^-24.
  * A value that is not finite reaches only rows that see its key.  Deterministic: the same inputs give the same bits.
- * n <= 2^31 - 65; tiles x heads (x ranges of keys or queries) below 2^23.
+ * nq, nk <= 2^28; tiles x heads (x ranges of keys or queries) below 2^23.
  */
 enum { TTT_ATTENTION_ZERO_UNUSED = 1 };
 /* Bytes of workspace of ttt_window_attention (backward = 0) or its gradient (backward = 1) for these shapes. */

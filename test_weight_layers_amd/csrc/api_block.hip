@@ -43,7 +43,7 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
   const int st = check_attention_heads(a.heads, a.key_heads, a.d, a.dtype);
   if (st) return st;
   if (a.nq < 0 || a.nk < 0 || a.nseq < 1) return fail(TTT_EINVAL, "nq and nk must be >= 0 and sequences >= 1");
-  if (a.nq > kMaxRows || a.nk > kMaxRows) return fail(TTT_EUNSUPPORTED, "more than %lld rows", (long long)kMaxRows);
+  if (a.nq > kAttnMaxRows || a.nk > kAttnMaxRows) return fail(TTT_EUNSUPPORTED, "more than %lld rows", (long long)kAttnMaxRows);
   if (a.block < 1 || a.sinks < 0) return fail(TTT_EINVAL, "block must be >= 1 and sinks >= 0");
   const bool bf16 = a.dtype == TTT_BF16;
   // a sequence of len rows has at most len / rows + 1 tiles, an empty one none
@@ -131,8 +131,15 @@ int attention_params(const AttnShape &a, bool backward, const Rows &q, const Row
   char *b = static_cast<char *>(ws);
   p.q = q.p, p.k = k.p, p.v = v.p, p.ldq = q.ld, p.ldk = k.ld, p.ldv = v.ld;
   p.nq = (int)a.nq, p.nk = (int)a.nk, p.nseq = a.nseq, p.cu_q = cu, p.cu_k = cu_k ? cu_k : cu;
-  p.heads = a.heads, p.key_heads = a.key_heads, p.d = a.d;
-  p.block = a.block, p.before = a.before < 0 ? -1 : a.before, p.after = a.after < 0 ? -1 : a.after, p.sinks = a.sinks, p.scale = scale;
+  p.heads = a.heads, p.key_heads = a.key_heads, p.d = a.d, p.sinks = a.sinks, p.scale = scale;
+  // (positions lie within kAttnMaxRows of 0: a larger block is as large as 2^28)
+  const int64_t block = std::min<int64_t>(a.block, kAttnMaxRows), most = int64_t(1) << 30;
+  const auto span = [&](int64_t blocks) { return (int)std::min<int64_t>(blocks * block, most); };
+  p.block = fast_div(block), p.group = fast_div(a.heads / a.key_heads);
+  p.back = a.before < 0 ? (int)most : span(a.before), p.ahead = a.after < 0 ? (int)most : span((int64_t)a.after + 1);
+  p.back_q = a.after < 0 ? (int)most : span(a.after), p.ahead_q = a.before < 0 ? (int)most : span((int64_t)a.before + 1);
+  p.per_qtiles = fast_div(P.qtiles), p.per_ktiles = fast_div(P.ktiles), p.per_splits = fast_div(P.splits), p.per_parts = fast_div(P.parts);
+  p.per_sink_parts = fast_div(P.sink_parts), p.per_sink_tiles = fast_div(P.sink_tiles), p.per_key_heads = fast_div(a.key_heads);
   p.seqs = reinterpret_cast<AttnSeq *>(b + P.off_seqs);
   p.qrows = P.qrows, p.krows = P.krows, p.qtiles = P.qtiles, p.ktiles = P.ktiles;
   p.splits = P.splits, p.part_o = reinterpret_cast<float *>(b + P.off_o), p.part_ml = reinterpret_cast<float2 *>(b + P.off_ml);

@@ -8,6 +8,18 @@ namespace ttt {
 
 constexpr int kAttnLaneSeqs = 63;   // up to here every wave lays the sequences out for itself
 
+constexpr int64_t kAttnMaxRows = int64_t(1) << 28;      // positions and spans then add in 32 bits
+
+// a / d for 0 <= a < 2^31 without a division (m = (2^32 - 1) / d: the product is at most one short).  A kernel's start is
+// fetched cold: 2700 instructions of it, most of them divisions, took 20 us.
+struct FastDiv {
+  uint32_t d, m;
+};
+inline FastDiv fast_div(int64_t d) {
+  const uint32_t x = d < 1 ? 1u : (uint32_t)d;
+  return FastDiv{x, 0xffffffffu / x};
+}
+
 // One packed sequence: its query and key rows, its first query and key tile.
 struct AttnSeq {
   int qs, ql, ks, kl, qt0, kt0;
@@ -22,12 +34,16 @@ struct AttnParams {
   int nq, nk, nseq;
   const int *cu_q, *cu_k;           // [nseq + 1]; both null: one sequence of all rows
   int heads, key_heads, d;
-  int block, before, after, sinks;  // before, after < 0: no limit
+  // Query p sees keys [first key of its block - back, that + ahead); key j is seen by queries [first position of its block
+  // - back_q, that + ahead_q).  At most 2^30 each, which is more than all.
+  FastDiv block, group;             // group: heads / key_heads
+  int back, ahead, back_q, ahead_q, sinks;
   float scale;
   bool zero_unused;
   AttnSeq *seqs;                    // [nseq + 1], more than kAttnLaneSeqs sequences
   int qrows, krows;                 // rows of a query tile and of a key tile
   int qtiles, ktiles;               // at most so many
+  FastDiv per_qtiles, per_ktiles, per_splits, per_parts, per_sink_parts, per_sink_tiles, per_key_heads;
   // forward: the keys of a tile in `splits` ranges, joined from these
   int splits;
   float *part_o;                    // [splits][heads][nq][d]
@@ -52,7 +68,7 @@ struct AttnStepParams {
   void *o;
   int64_t ldo;
   int n, pool, capacity, heads, key_heads, d;
-  int block, before, sinks;
+  int block, before, sinks;         // before < 0: no limit
   float scale;
   bool zero_unused;
   int splits;

@@ -31,13 +31,13 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
           p.lse[(int64_t)h * p.nq + (i < used.x ? i : used.y + (i - used.x))] = -__builtin_inff();
     return;
   }
-  const int item = attn_item(blockIdx.x, items), split = item % p.splits, rest = item / p.splits;
-  const int h = rest / p.qtiles, kh = h / (p.heads / p.key_heads);
+  const int item = attn_item(blockIdx.x, items), rest = quotient(item, p.per_splits), split = item - rest * p.splits;
+  const int h = quotient(rest, p.per_qtiles), kh = quotient(h, p.group);
   AttnSeq s;
   int tile, seq;
   // Without a window late tiles see the most keys: the late half first, then the early half from its first tile on, so
   // that a CU that takes one of each has as much to do as the others.
-  const int order = rest % p.qtiles, half = (p.qtiles + 1) / 2;
+  const int order = rest - h * p.qtiles, half = (p.qtiles + 1) / 2;
   if (!tile_of<false>(p, order < half ? p.qtiles - 1 - order : order - half, &s, &tile, &seq)) return;
   const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3, kg = wave8 >> 2;
   const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
   const int k0 = seen_keys(p, s, t0).x, k1 = seen_keys(p, s, last - 1).y, se = p.sinks < k0 ? p.sinks : k0;
   const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
-  const int first = (int)((int64_t)nt * split / p.splits), end = (int)((int64_t)nt * (split + 1) / p.splits);
+  const int share = quotient(nt + p.splits - 1, p.per_splits), first = split * share, end = first + share < nt ? first + share : nt;
   const unsigned off_k = Tile::lane_offset(p.ldk), off_v = Tile::lane_offset(p.ldv);
   const KeyWalk<T, BK> start(first + kg, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
   const auto fetch = [&](const KeyWalk<T, BK> &w, int stage) {

@@ -45,10 +45,10 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
   __shared__ __attribute__((aligned(256))) unsigned char s_k[2][kTile], s_v[2][kTile];
-  const int item = attn_item(blockIdx.x, p.qtiles * p.heads), h = item / p.qtiles, kh = h / (p.heads / p.key_heads);
+  const int item = attn_item(blockIdx.x, p.qtiles * p.heads), h = quotient(item, p.per_qtiles), kh = quotient(h, p.group);
   AttnSeq s;
   int tile, seq;
-  if (!tile_of<false>(p, p.qtiles - 1 - item % p.qtiles, &s, &tile, &seq)) return;
+  if (!tile_of<false>(p, p.qtiles - 1 - (item - h * p.qtiles), &s, &tile, &seq)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g = l >> 4, li = l & 15;
   const int t0 = tile * QR, row0 = t0 + wave * 16 * NC;
   const T *kb = static_cast<const T *>(p.k) + (int64_t)s.ks * p.ldk + kh * D;
@@ -184,18 +184,19 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   constexpr int NK = D / 32, ND = D / 16, kTile = BQ * Tile::kRow, KR = 64 * NC;
   __shared__ __attribute__((aligned(256))) unsigned char s_q[2][kTile], s_o[2][kTile];
   __shared__ __attribute__((aligned(256))) float s_lse[2][64], s_del[2][64];
-  const int window_items = p.ktiles * p.key_heads * p.parts, grp = p.heads / p.key_heads;
+  const int window_items = p.ktiles * p.key_heads * p.parts, grp = (int)p.group.d;
   const bool sink_item = (int)blockIdx.x >= window_items;
   AttnSeq s;
   int tile, seq, kh, part, parts;
   if (!sink_item) {
-    const int item = attn_item(blockIdx.x, window_items), rest = item / p.parts;
-    part = item % p.parts, parts = p.parts, kh = rest / p.ktiles;
-    if (!tile_of<true>(p, rest % p.ktiles, &s, &tile, &seq)) return;
+    const int item = attn_item(blockIdx.x, window_items), rest = quotient(item, p.per_parts);
+    part = item - rest * p.parts, parts = p.parts, kh = quotient(rest, p.per_ktiles);
+    if (!tile_of<true>(p, rest - kh * p.ktiles, &s, &tile, &seq)) return;
   } else {
-    const int item = attn_item(blockIdx.x - window_items, gridDim.x - window_items), rest = item / p.sink_parts;
-    part = item % p.sink_parts, parts = p.sink_parts, kh = rest % p.key_heads;
-    tile = rest / p.key_heads % p.sink_tiles, seq = rest / p.key_heads / p.sink_tiles;
+    const int item = attn_item(blockIdx.x - window_items, gridDim.x - window_items), rest = quotient(item, p.per_sink_parts);
+    const int one = quotient(rest, p.per_key_heads);
+    part = item - rest * p.sink_parts, parts = p.sink_parts, kh = rest - one * p.key_heads;
+    seq = quotient(one, p.per_sink_tiles), tile = one - seq * p.sink_tiles;
     s = seq_of(p, seq);
     if (tile * KR >= s.kl) return;
   }
@@ -206,7 +207,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   own_rows<T, D, NC>(k, static_cast<const T *>(p.k) + (int64_t)s.ks * p.ldk + kh * D, p.ldk, row0, s.kl);
   own_rows<T, D, NC>(v, static_cast<const T *>(p.v) + (int64_t)s.ks * p.ldv + kh * D, p.ldv, row0, s.kl);
   // The queries that see key j: [x, y) in their window and, for a sink, all behind.
-  const bool with_sinks = (sink_item || p.sink_parts == 0) && p.before >= 0 && t0 < p.sinks;
+  const bool with_sinks = (sink_item || p.sink_parts == 0) && t0 < p.sinks;
   int lo[NC], hi[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -218,7 +219,8 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   const int2 wa = row0 < s.kl ? seeing_queries(p, s, row0) : int2{0, 0}, wb = row0 < s.kl ? seeing_queries(p, s, wlast) : int2{0, 0};
   // a head's tiles: na over the window [ta.x, tb.y), nb over what is behind the first key's window [ta.y, ql)
   const int na = sink_item ? 0 : tiles_of(tb.y - ta.x, BQ), nb = with_sinks ? tiles_of(s.ql - ta.y, BQ) : 0, per = na + nb;
-  const int first = (int)((int64_t)per * grp * part / parts), end = (int)((int64_t)per * grp * (part + 1) / parts);
+  const int total = per * grp, share = quotient(total + parts - 1, sink_item ? p.per_sink_parts : p.per_parts);
+  const int first = part * share, end = first + share < total ? first + share : total;
   const unsigned off_q = Tile::lane_offset(p.ldq), off_o = Tile::lane_offset(p.ldgo);
   struct Walk {                                       // over the heads' tiles
     int x, i, e;                                      // tile of the head, its rows [i, min(i + BQ, e))
@@ -398,11 +400,11 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_dkv_sum
   constexpr int L = D / 2;
   AttnSeq s;
   int tile, seq;
-  const int kh = blockIdx.x % p.key_heads, x = blockIdx.x / p.key_heads;
+  const int x = quotient(blockIdx.x, p.per_key_heads), kh = blockIdx.x - x * p.key_heads;
   if (p.parts > 1) {
     if (!tile_of<true>(p, x, &s, &tile, &seq)) return;
   } else {
-    tile = x % p.sink_tiles, seq = x / p.sink_tiles;
+    seq = quotient(x, p.per_sink_tiles), tile = x - seq * p.sink_tiles;
     s = seq_of(p, seq);
   }
   const int c = threadIdx.x % L * 4, r = blockIdx.y * (256 / L) + threadIdx.x / L;

@@ -113,12 +113,18 @@ __device__ __forceinline__ void own_rows(typename FragOf<T>::type (&f)[NC][D / 3
   }
 }
 
+__device__ __forceinline__ int quotient(int a, FastDiv by) {
+  const uint32_t q = __umulhi((uint32_t)a, by.m);
+  return (int)(q + ((uint32_t)a - q * by.d >= by.d ? 1u : 0u));
+}
+
 // ------------------------------------------------------------------ packed sequences
 __device__ __forceinline__ int attn_offset(const int *cu, int i, int n) {
   const int x = cu[i];
   return x < 0 ? 0 : (x > n ? n : x);
 }
-__device__ __forceinline__ int tiles_of(int len, int rows) { return (len + rows - 1) / rows; }
+// (rows: a power of two)
+__device__ __forceinline__ int tiles_of(int len, int rows) { return (len + rows - 1) >> __builtin_ctz(rows); }
 
 // Lane i's sequence (lane nseq: what follows the last); every lane of the wave calls this.  The running maximum of the
 // clamped offsets makes any offsets into disjoint ranges of rows.
@@ -145,8 +151,13 @@ __device__ __forceinline__ AttnSeq read_seq(const AttnSeq &s, int b) {
   return AttnSeq{__builtin_amdgcn_readlane(s.qs, b),  __builtin_amdgcn_readlane(s.ql, b),  __builtin_amdgcn_readlane(s.ks, b),
                  __builtin_amdgcn_readlane(s.kl, b),  __builtin_amdgcn_readlane(s.qt0, b), __builtin_amdgcn_readlane(s.kt0, b)};
 }
-__device__ __forceinline__ AttnSeq seq_of(const AttnParams &p, int b) {
+__device__ __forceinline__ AttnSeq only_seq(const AttnParams &p) {
   if (p.cu_q == nullptr) return AttnSeq{0, p.nq, 0, p.nk, 0, 0};
+  const int qs = attn_offset(p.cu_q, 0, p.nq), qe = attn_offset(p.cu_q, 1, p.nq), ks = attn_offset(p.cu_k, 0, p.nk), ke = attn_offset(p.cu_k, 1, p.nk);
+  return AttnSeq{qs, qe > qs ? qe - qs : 0, ks, ke > ks ? ke - ks : 0, 0, 0};
+}
+__device__ __forceinline__ AttnSeq seq_of(const AttnParams &p, int b) {
+  if (p.nseq == 1) return only_seq(p);
   if (p.nseq > kAttnLaneSeqs) return p.seqs[b];
   return read_seq(lane_seq(p), b);
 }
@@ -154,8 +165,8 @@ __device__ __forceinline__ AttnSeq seq_of(const AttnParams &p, int b) {
 template <bool KEYS> __device__ __forceinline__ bool tile_of(const AttnParams &p, int c, AttnSeq *s, int *tile, int *seq) {
   const int rows = KEYS ? p.krows : p.qrows;
   int b = 0;
-  if (p.cu_q == nullptr) {
-    *s = AttnSeq{0, p.nq, 0, p.nk, 0, 0};
+  if (p.nseq == 1) {
+    *s = only_seq(p);
   } else if (p.nseq <= kAttnLaneSeqs) {
     const AttnSeq x = lane_seq(p);
     const int first = KEYS ? x.kt0 : x.qt0;
@@ -178,25 +189,23 @@ template <bool KEYS> __device__ __forceinline__ bool tile_of(const AttnParams &p
 }
 // The query (key) rows that belong to a sequence: [x, y).
 template <bool KEYS> __device__ __forceinline__ int2 used_rows(const AttnParams &p) {
-  const AttnSeq a = seq_of(p, 0), b = seq_of(p, p.cu_q == nullptr ? 0 : p.nseq - 1);
+  const AttnSeq a = seq_of(p, 0), b = p.nseq == 1 ? a : seq_of(p, p.nseq - 1);
   return KEYS ? int2{a.ks, b.ks + b.kl} : int2{a.qs, b.qs + b.ql};
 }
 
 // ------------------------------------------------------------------ what a query sees
 // Query i of a sequence stands at position i + kl - ql, in block floor(position / block).  It sees keys [lo, hi), and
 // those below min(sinks, hi).
-__device__ __forceinline__ int floor_div(int a, int b) { return a >= 0 ? a / b : -((-(a + 1)) / b) - 1; }
-__device__ __forceinline__ int clamp_to(int64_t x, int n) { return x < 0 ? 0 : (x > n ? n : (int)x); }
+__device__ __forceinline__ int clamp_to(int x, int n) { return x < 0 ? 0 : (x > n ? n : x); }
 __device__ __forceinline__ int2 seen_keys(const AttnParams &p, const AttnSeq &s, int i) {
-  const int64_t b = floor_div(i + s.kl - s.ql, p.block);
-  return int2{p.before < 0 ? 0 : clamp_to((b - p.before) * p.block, s.kl),
-              p.after < 0 ? s.kl : clamp_to((b + p.after + 1) * p.block, s.kl)};
+  const int at = i + s.kl - s.ql, b = at >= 0 ? quotient(at, p.block) : -quotient(-(at + 1), p.block) - 1;
+  const int first = b * (int)p.block.d;
+  return int2{clamp_to(first - p.back, s.kl), clamp_to(first + p.ahead, s.kl)};
 }
 // The queries that see key j inside their window: [x, y).  Those behind y see it if it is a sink.
 __device__ __forceinline__ int2 seeing_queries(const AttnParams &p, const AttnSeq &s, int j) {
-  const int64_t b = j / p.block, off = s.kl - s.ql;
-  return int2{p.after < 0 ? 0 : clamp_to((b - p.after) * p.block - off, s.ql),
-              p.before < 0 ? s.ql : clamp_to((b + p.before + 1) * p.block - off, s.ql)};
+  const int first = quotient(j, p.block) * (int)p.block.d - (s.kl - s.ql);
+  return int2{clamp_to(first - p.back_q, s.ql), clamp_to(first + p.ahead_q, s.ql)};
 }
 
 // The largest of a column's four lanes (16 apart), in each of them.
