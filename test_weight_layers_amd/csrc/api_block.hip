@@ -47,7 +47,7 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
   if (a.block < 1 || a.sinks < 0) return fail(TTT_EINVAL, "block must be >= 1 and sinks >= 0");
   const bool bf16 = a.dtype == TTT_BF16;
   // a sequence of len rows has at most len / rows + 1 tiles, an empty one none
-  const auto tiles = [&](int64_t n, int rows) { return n / rows + (a.nseq < n ? a.nseq : n); };
+  const auto tiles = [&](int64_t n, int rows) { return a.nseq == 1 ? ceil_div(n, rows) : n / rows + std::min<int64_t>(a.nseq, n); };
   // keys that a query sees inside its window, at most, and those of a sequence, at the mean
   const int64_t lk = ceil_div(a.nk, a.nseq), lq = ceil_div(a.nq, a.nseq);
   int64_t window = lk;
