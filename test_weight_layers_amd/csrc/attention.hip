@@ -17,7 +17,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, NU = BK / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
   constexpr int kPitch = D + 4;                       // floats of a query's row of the second four waves' sums
-  __shared__ __attribute__((aligned(256))) unsigned char s_kv[KG][2][2][kTile];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_kv[KG][2][2][kTile];
   static_assert(KG == 1 || QR * (kPitch + 2) * 4 <= (int)sizeof(s_kv), "");
   const int items = p.qtiles * p.heads * p.splits;
   if ((int)blockIdx.x >= items) {
@@ -60,6 +60,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
   const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
   const int share = quotient(nt + p.splits - 1, p.per_splits), first = split * share, end = first + share < nt ? first + share : nt;
+  const typename Tile::Lane lane = Tile::lane();
   const unsigned off_k = Tile::lane_offset(p.ldk), off_v = Tile::lane_offset(p.ldv);
   const KeyWalk<T, BK> start(first + kg, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
   const auto fetch = [&](const KeyWalk<T, BK> &w, int stage) {
@@ -93,8 +94,8 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
       if (t + KG + kg < end) fetch(ahead, stage ^ 1);
       const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
       const bool none = !there || !(r.x < wb.y && (r.y > wa.x || r.x < p.sinks));
-      const unsigned char *kt = s_kv[kg][stage][0];
       unsigned char *vt = s_kv[kg][stage][1];
+      const int ka = Tile::offset(s_kv[kg][stage][0]), va = Tile::offset(vt);
       Frag pr[NU / 2][NC];
       if (!none) {
         f32x4 sc[NU][NC];
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
           for (int c = 0; c < NC; ++c) sc[u][c] = zero_f4();
 #pragma unroll
           for (int k = 0; k < NK; ++k) {
-            const Frag a = Tile::rows(kt, 16 * u + li, 32 * k + 8 * g);
+            const Frag a = Tile::rows(ka, lane, 16 * u, k);
 #pragma unroll
             for (int c = 0; c < NC; ++c) sc[u][c] = mma(a, q[c][k], sc[u][c]);
           }
@@ -119,7 +120,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const int j = r.x + 16 * u + 4 * g + x;
-                sc[u][c][x] = (j < e) & ((j >= lo[c]) | (j < p.sinks)) ? sc[u][c][x] : -__builtin_inff();
+                sc[u][c][x] = ((j < e) & ((j >= lo[c]) | (j < p.sinks))) ? sc[u][c][x] : -__builtin_inff();
               }
           }
         }
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
         for (int u = 0; u < NU / 2; ++u)
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
-            const Frag a = Tile::cols(vt, 32 * u, 16 * d);
+            const Frag a = Tile::cols(va, lane, 32 * u, d);
 #pragma unroll
             for (int c = 0; c < NC; ++c) o[d][c] = mma(a, pr[u][c], o[d][c]);
           }
@@ -376,10 +377,10 @@ hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s) {
   if (bf16) {
     if (p.d == 64) return small ? go<__bf16, 64, 1, 64, 2, 4>(p, s) : go<__bf16, 64, 2, 64, 1, 3>(p, s);
     if (p.d == 128) return small ? go<__bf16, 128, 1, 32, 2, 2>(p, s) : go<__bf16, 128, 2, 64, 1, 2>(p, s);
-    return small ? go<__bf16, 256, 1, 32, 2, 2>(p, s) : go<__bf16, 256, 2, 32, 1, 1>(p, s);
+    return small ? go<__bf16, 256, 1, 32, 2, 2>(p, s) : go<__bf16, 256, 2, 32, 1, 2>(p, s);
   }
-  if (p.d == 64) return small ? go<float, 64, 1, 32, 2, 3>(p, s) : go<float, 64, 2, 32, 1, 2>(p, s);
-  if (p.d == 128) return small ? go<float, 128, 1, 32, 2, 2>(p, s) : go<float, 128, 2, 32, 1, 1>(p, s);
+  if (p.d == 64) return small ? go<float, 64, 1, 32, 2, 3>(p, s) : go<float, 64, 2, 32, 1, 3>(p, s);
+  if (p.d == 128) return small ? go<float, 128, 1, 32, 2, 2>(p, s) : go<float, 128, 2, 32, 1, 2>(p, s);
   return go<float, 256, 1, 32, 1, 1>(p, s);
 }
 

@@ -44,7 +44,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
   typedef AttnTile<T, D> Tile;
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
-  __shared__ __attribute__((aligned(256))) unsigned char s_k[2][kTile], s_v[2][kTile];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_k[2][kTile], s_v[2][kTile];
   const int item = attn_item(blockIdx.x, p.qtiles * p.heads), h = quotient(item, p.per_qtiles), kh = quotient(h, p.group);
   AttnSeq s;
   int tile, seq;
@@ -72,6 +72,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
   const int k0 = seen_keys(p, s, t0).x, k1 = seen_keys(p, s, last - 1).y, se = p.sinks < k0 ? p.sinks : k0;
   const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
+  const typename Tile::Lane lane = Tile::lane();
   const unsigned off_k = Tile::lane_offset(p.ldk), off_v = Tile::lane_offset(p.ldv);
   const KeyWalk<T, BK> start(0, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
   const auto fetch = [&](const KeyWalk<T, BK> &w, int stage) {
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
       const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
       const bool none = !(r.x < wb.y && (r.y > wa.x || r.x < p.sinks));
       unsigned char *kt = s_k[t & 1];
-      const unsigned char *vt = s_v[t & 1];
+      const int ka = Tile::offset(kt), va = Tile::offset(s_v[t & 1]);
 #pragma unroll
       for (int x0 = 0; x0 < BK; x0 += 32) {
         Frag ds[NC];
@@ -108,7 +109,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
             for (int c = 0; c < NC; ++c) sc[u][c] = dp[u][c] = zero_f4();
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
-              const Frag a = Tile::rows(kt, x0 + 16 * u + li, 32 * k + 8 * g), b = Tile::rows(vt, x0 + 16 * u + li, 32 * k + 8 * g);
+              const Frag a = Tile::rows(ka, lane, x0 + 16 * u, k), b = Tile::rows(va, lane, x0 + 16 * u, k);
 #pragma unroll
               for (int c = 0; c < NC; ++c) {
                 sc[u][c] = mma(a, q[c][k], sc[u][c]);
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                   const int j = r.x + x0 + 16 * u + 4 * g + x;
-                  sc[u][c][x] = (j < e) & ((j >= lo[c]) | (j < p.sinks)) ? sc[u][c][x] : 0.0f;
+                  sc[u][c][x] = ((j < e) & ((j >= lo[c]) | (j < p.sinks))) ? sc[u][c][x] : 0.0f;
                 }
             }
             ds[c] = pack44<T>(sc[0][c], sc[1][c]);
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
         if (!none) {
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
-            const Frag a = Tile::cols(kt, x0, 16 * d);
+            const Frag a = Tile::cols(ka, lane, x0, d);
 #pragma unroll
             for (int c = 0; c < NC; ++c) dq[d][c] = mma(a, ds[c], dq[d][c]);
           }
@@ -182,7 +183,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   typedef AttnTile<T, D> Tile;
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, kTile = BQ * Tile::kRow, KR = 64 * NC;
-  __shared__ __attribute__((aligned(256))) unsigned char s_q[2][kTile], s_o[2][kTile];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_q[2][kTile], s_o[2][kTile];
   __shared__ __attribute__((aligned(256))) float s_lse[2][64], s_del[2][64];
   const int window_items = p.ktiles * p.key_heads * p.parts, grp = (int)p.group.d;
   const bool sink_item = (int)blockIdx.x >= window_items;
@@ -221,6 +222,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   const int na = sink_item ? 0 : tiles_of(tb.y - ta.x, BQ), nb = with_sinks ? tiles_of(s.ql - ta.y, BQ) : 0, per = na + nb;
   const int total = per * grp, share = quotient(total + parts - 1, sink_item ? p.per_sink_parts : p.per_parts);
   const int first = part * share, end = first + share < total ? first + share : total;
+  const typename Tile::Lane lane = Tile::lane();
   const unsigned off_q = Tile::lane_offset(p.ldq), off_o = Tile::lane_offset(p.ldgo);
   struct Walk {                                       // over the heads' tiles
     int x, i, e;                                      // tile of the head, its rows [i, min(i + BQ, e))
@@ -278,6 +280,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
       }
       const bool full = r.y - r.x == BQ && all_x <= r.x && all_y >= r.y, none = row0 >= s.kl || !(any_x < r.y && any_y > r.x);
       unsigned char *qt = s_q[t & 1], *ot = s_o[t & 1];
+      const int qa = Tile::offset(qt), oa = Tile::offset(ot);
       const float *lse = s_lse[t & 1], *del = s_del[t & 1];
 #pragma unroll
       for (int x0 = 0; x0 < BQ; x0 += 32) {
@@ -290,12 +293,13 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
             for (int c = 0; c < NC; ++c) sc[u][c] = dp[u][c] = zero_f4();
 #pragma unroll
             for (int x = 0; x < NK; ++x) {
-              const Frag a = Tile::rows(qt, x0 + 16 * u + li, 32 * x + 8 * g), b = Tile::rows(ot, x0 + 16 * u + li, 32 * x + 8 * g);
+              const Frag a = Tile::rows(qa, lane, x0 + 16 * u, x), b = Tile::rows(oa, lane, x0 + 16 * u, x);
 #pragma unroll
               for (int c = 0; c < NC; ++c) {
                 sc[u][c] = mma(a, k[c][x], sc[u][c]);
                 dp[u][c] = mma(b, v[c][x], dp[u][c]);
               }
+              if (D == 256 && x % 2 == 1) __builtin_amdgcn_sched_barrier(0);
             }
             const f32x4 l4 = *reinterpret_cast<const f32x4 *>(lse + x0 + 16 * u + 4 * g) * kLog2e;
             const f32x4 d4 = *reinterpret_cast<const f32x4 *>(del + x0 + 16 * u + 4 * g);
@@ -312,7 +316,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               const int j = row0 + 16 * c + li;
-              const int first = window ? lo[c] : (j < p.sinks) & (j < s.kl) ? hi[c] : s.ql, e = window ? (hi[c] < r.y ? hi[c] : r.y) : r.y;
+              const int first = window ? lo[c] : ((j < p.sinks) & (j < s.kl)) ? hi[c] : s.ql, e = window ? (hi[c] < r.y ? hi[c] : r.y) : r.y;
 #pragma unroll
               for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -351,12 +355,14 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
         if (!none) {
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
-            const Frag a = Tile::cols(ot, x0, 16 * d), b = Tile::cols(qt, x0, 16 * d);
+            const Frag a = Tile::cols(oa, lane, x0, d), b = Tile::cols(qa, lane, x0, d);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               dv[d][c] = mma(a, pr[c], dv[d][c]);
               dk[d][c] = mma(b, ds[c], dk[d][c]);
             }
+            // (wide heads: operands that are all read ahead would take the registers of the second wave)
+            if (D == 256 && d % 2 == 1) __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
@@ -452,18 +458,18 @@ template <typename T, int D, int NC, int BK, int OCC, int NCK, int BQ, int OCCK>
 
 }  // namespace
 
-int attn_grad_query_rows(int d, bool bf16) { return d == 256 ? 64 : 128; }
-int attn_grad_key_rows(int d, bool bf16) { return d == 256 || (!bf16 && d == 128) ? 64 : 128; }
+int attn_grad_query_rows(int d, bool bf16) { return d == 256 || (!bf16 && d == 128) ? 64 : 128; }
+int attn_grad_key_rows(int d, bool bf16) { return d >= 128 ? 64 : 128; }
 
 hipError_t launch_attention_backward(const AttnParams &p, bool bf16, hipStream_t s) {
   const hipError_t e = launch_attention_plan(p, s);
   if (e != hipSuccess) return e;
   if (bf16) {
     if (p.d == 64) return go<__bf16, 64, 2, 64, 3, 2, 64, 2>(p, s);
-    return p.d == 128 ? go<__bf16, 128, 2, 32, 2, 2, 32, 1>(p, s) : go<__bf16, 256, 1, 32, 2, 1, 32, 1>(p, s);
+    return p.d == 128 ? go<__bf16, 128, 2, 32, 2, 1, 32, 3>(p, s) : go<__bf16, 256, 1, 32, 2, 1, 32, 2>(p, s);
   }
-  if (p.d == 64) return go<float, 64, 2, 32, 2, 2, 32, 1>(p, s);
-  return p.d == 128 ? go<float, 128, 2, 32, 1, 1, 32, 1>(p, s) : go<float, 256, 1, 32, 1, 1, 32, 1>(p, s);
+  if (p.d == 64) return go<float, 64, 2, 32, 2, 2, 32, 2>(p, s);
+  return p.d == 128 ? go<float, 128, 1, 32, 2, 1, 32, 2>(p, s) : go<float, 256, 1, 32, 1, 1, 32, 1>(p, s);
 }
 
 }  // namespace ttt

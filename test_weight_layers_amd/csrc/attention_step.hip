@@ -23,7 +23,7 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_step_ke
   typedef typename FragOf<T>::type Frag;
   constexpr int NK = D / 32, ND = D / 16, kTile = 32 * Tile::kRow;
   constexpr bool kStage = sizeof(T) == 2;             // fp32 values go straight to registers
-  __shared__ __attribute__((aligned(256))) unsigned char s_raw[kStage ? 8 * kTile : 4 * 16 * D * 4];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_raw[kStage ? 8 * kTile : 4 * 16 * D * 4];
   __shared__ float s_m[4][16], s_l[4][16];
   const int grp = p.heads / p.key_heads, hgs = (grp + 15) / 16;
   int item = blockIdx.x;
@@ -62,6 +62,7 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_step_ke
     return (int)(c < p.capacity ? c : c - ring);
   };
 
+  const typename Tile::Lane lane = Tile::lane();
   Frag q[NK];
   const int hq = hg * 16 + li;
 #pragma unroll
@@ -148,7 +149,7 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_step_ke
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
       if constexpr (kStage)
-        o[d] = mma(Tile::cols(vt[b], 0, 16 * d), pr, o[d]);
+        o[d] = mma(Tile::cols(Tile::offset(vt[b]), lane, 0, d), pr, o[d]);
       else
         o[d] = mma(vf[d], pr, o[d]);
     }

@@ -25,21 +25,55 @@ template <typename T, int D> struct AttnTile {
     return at(r, e * (int)sizeof(T) >> 4) + (e * (int)sizeof(T) & 15);
   }
 
-  // elements e .. e + 7 (e a multiple of 8) of row r
-  static __device__ __forceinline__ typename FragOf<T>::type rows(const unsigned char *t, int r, int e) {
-    return ld8(reinterpret_cast<const T *>(t + at(r, e * (int)sizeof(T) >> 4)));
-  }
-  // column c0 + li of rows r0 + 4 g .. + 3 and r0 + 16 + 4 g .. + 3
-  static __device__ __forceinline__ typename FragOf<T>::type cols(const unsigned char *t, int r0, int c0) {
+  // Where a lane reads.  The rows' part of an address is a multiple of kRow and a unit changes by xor, so that a lane has one
+  // address for all operands by rows and one (fp32: four) for those by columns, and each read one xor: left to itself the
+  // compiler keeps an address for every operand, 16 to 32 registers of the second wave of a SIMD.
+  static constexpr int kCols = sizeof(T) == 2 ? 1 : 4;
+  struct Lane {
+    int row, col[kCols];
+  };
+  static __device__ __forceinline__ Lane lane() {
     const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
+    Lane a;
+    a.row = elem(li, 8 * g);
     if constexpr (sizeof(T) == 2) {
-      const unsigned char *a = t + at(r0 + 4 * g + (li >> 2), (c0 >> 3) + ((li & 3) >> 1)) + (li & 1) * 8;
-      return cat8(lds_read_tr16(a), lds_read_tr16(a + 16 * kRow));
+      a.col[0] = elem(4 * g + (li >> 2), 4 * (li & 3));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) a.col[i] = elem(4 * g + i, li);
+    }
+    return a;
+  }
+  template <typename V> static __device__ __forceinline__ V lds(int at) {
+    return *(const __attribute__((address_space(3))) V *)(uint32_t)at;
+  }
+  static __device__ __forceinline__ int offset(const unsigned char *t) {
+    return (int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char *)t;
+  }
+  // elements 32 k + 8 g .. + 7 of row r0 + li (r0 a multiple of 16)
+  static __device__ __forceinline__ typename FragOf<T>::type rows(int tile, const Lane &a, int r0, int k) {
+    const int at = xor_here(tile + a.row, k * 32 * (int)sizeof(T)) + r0 * kRow;
+    if constexpr (sizeof(T) == 2) {
+      return lds<bf16x8>(at);
+    } else {
+      const f32x4 x = lds<f32x4>(at), y = lds<f32x4>(at + 16);
+      return f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    }
+  }
+  // column 16 d + li of rows r0 + 4 g .. + 3 and r0 + 16 + 4 g .. + 3 (r0 a multiple of 16)
+  static __device__ __forceinline__ typename FragOf<T>::type cols(int tile, const Lane &a, int r0, int d) {
+    if constexpr (sizeof(T) == 2) {
+      const int at = xor_here(tile + a.col[0], d * 32) + r0 * kRow;
+      const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uint32_t)at);
+      const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uint32_t)(at + 16 * kRow));
+      return cat8(__builtin_bit_cast(bf16x4, x), __builtin_bit_cast(bf16x4, y));
     } else {
       f32x8 v;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = *reinterpret_cast<const float *>(t + elem(r0 + 16 * (e >> 2) + 4 * g + (e & 3), c0 + li));
+      for (int i = 0; i < 4; ++i) {
+        const int at = xor_here(tile + a.col[i], d * 64) + r0 * kRow;
+        v[i] = lds<float>(at), v[4 + i] = lds<float>(at + 16 * kRow);
+      }
       return v;
     }
   }
