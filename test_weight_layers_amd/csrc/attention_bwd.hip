@@ -388,6 +388,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
       for (int d = 0; d < ND; ++d) store4(ok + 16 * d, dk[d][c] * p.scale), store4(ov + 16 * d, dv[d][c]);
       continue;
     }
+    if (sink_item && j >= p.sinks) continue;
     float *out;
     if (sink_item || p.parts == 1)
       out = p.spart + (((((int64_t)seq * p.sink_tiles + tile) * p.key_heads + kh) * (1 + p.sink_parts) + (sink_item ? 1 + part : 0)) * KR +
@@ -426,7 +427,7 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_dkv_sum
     const float *b = p.spart + (((((int64_t)seq * p.sink_tiles + tile) * p.key_heads + kh) * (1 + p.sink_parts)) * p.krows + r) * 2 * D + c;
     const int64_t next = (int64_t)p.krows * 2 * D;
 #pragma unroll 4
-    for (int i = p.parts > 1 ? 1 : 0; i <= p.sink_parts; ++i) v += *reinterpret_cast<const f32x4 *>(b + i * next);
+    for (int i = p.parts > 1 ? 1 : 0; i <= (tile * p.krows + r < p.sinks ? p.sink_parts : 0); ++i) v += *reinterpret_cast<const f32x4 *>(b + i * next);
   }
   if (c < D)
     store4(static_cast<T *>(p.gk) + row * p.ldgk + kh * D + c, v);
