@@ -76,8 +76,9 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
       P.off_ml = take((size_t)P.splits * a.heads * a.nq * 8);
     }
   } else {
-    P.qrows = attn_grad_query_rows(a.d, bf16);
-    P.krows = attn_grad_key_rows(a.d, bf16);
+    const bool small = a.d == 64 && tiles(a.nk, 128) * a.key_heads < 512;
+    P.qrows = attn_grad_query_rows(a.d, bf16, small);
+    P.krows = attn_grad_key_rows(a.d, bf16, small);
     P.off_delta = take((size_t)a.heads * a.nq * 4);
     const int64_t wgs = tiles(a.nk, P.krows) * a.key_heads, queries = std::min(lq, window + P.krows);
     if (wgs > 0 && wgs < 256) P.parts = (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, queries * grp / 256, 64}));

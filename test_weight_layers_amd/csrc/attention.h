@@ -79,8 +79,8 @@ struct AttnStepParams {
 // Rows of the tiles that the launchers use.
 int attn_query_rows(int d, bool bf16, bool small);
 int attn_splits(int64_t workgroups, int64_t nq, int heads, int d, int rows, int64_t keys, bool bf16);
-int attn_grad_query_rows(int d, bool bf16);
-int attn_grad_key_rows(int d, bool bf16);
+int attn_grad_query_rows(int d, bool bf16, bool small);
+int attn_grad_key_rows(int d, bool bf16, bool small);
 hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s);
 hipError_t launch_attention_backward(const AttnParams &p, bool bf16, hipStream_t s);
 hipError_t launch_attention_step(const AttnStepParams &p, bool bf16, hipStream_t s);

@@ -61,11 +61,11 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
   const int share = quotient(nt + p.splits - 1, p.per_splits), first = split * share, end = first + share < nt ? first + share : nt;
   const typename Tile::Lane lane = Tile::lane();
-  const unsigned off_k = Tile::lane_offset(p.ldk), off_v = Tile::lane_offset(p.ldv);
+  const typename Tile::template Copy<BK> copy_k(p.ldk), copy_v(p.ldv);
   const KeyWalk<T, BK> start(first + kg, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
   const auto fetch = [&](const KeyWalk<T, BK> &w, int stage) {
-    Tile::template fetch<BK>(w.k, p.ldk, w.end() - w.j, off_k, s_kv[kg][stage][0]);
-    Tile::template fetch<BK>(w.v, p.ldv, w.end() - w.j, off_v, s_kv[kg][stage][1]);
+    copy_k.fetch(w.k, w.end() - w.j, s_kv[kg][stage][0]);
+    copy_v.fetch(w.v, w.end() - w.j, s_kv[kg][stage][1]);
   };
 
   const float c2 = p.scale * kLog2e;

@@ -73,11 +73,11 @@ __global__ __launch_bounds__(256, OCC) void attn_dq_kernel(AttnParams p) {
   const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
   const typename Tile::Lane lane = Tile::lane();
-  const unsigned off_k = Tile::lane_offset(p.ldk), off_v = Tile::lane_offset(p.ldv);
+  const typename Tile::template Copy<BK> copy_k(p.ldk), copy_v(p.ldv);
   const KeyWalk<T, BK> start(0, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
   const auto fetch = [&](const KeyWalk<T, BK> &w, int stage) {
-    Tile::template fetch<BK>(w.k, p.ldk, w.end() - w.j, off_k, s_k[stage]);
-    Tile::template fetch<BK>(w.v, p.ldv, w.end() - w.j, off_v, s_v[stage]);
+    copy_k.fetch(w.k, w.end() - w.j, s_k[stage]);
+    copy_v.fetch(w.v, w.end() - w.j, s_v[stage]);
   };
   const float c2 = p.scale * kLog2e;
   f32x4 dq[ND][NC];
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   const int total = per * grp, share = quotient(total + parts - 1, sink_item ? p.per_sink_parts : p.per_parts);
   const int first = part * share, end = first + share < total ? first + share : total;
   const typename Tile::Lane lane = Tile::lane();
-  const unsigned off_q = Tile::lane_offset(p.ldq), off_o = Tile::lane_offset(p.ldgo);
+  const typename Tile::template Copy<BQ> copy_q(p.ldq), copy_o(p.ldgo);
   struct Walk {                                       // over the heads' tiles
     int x, i, e;                                      // tile of the head, its rows [i, min(i + BQ, e))
     const T *q, *o;                                   // its first rows
@@ -243,8 +243,8 @@ __global__ __launch_bounds__(256, OCC) void attn_dkv_kernel(AttnParams p) {
   const int h0 = per > 0 ? first / per : 0, x0 = first - h0 * per;
   const auto fetch = [&](const Walk &w, int stage) {
     const int n = w.end() - w.i;
-    Tile::template fetch<BQ>(w.q, p.ldq, n, off_q, s_q[stage]);
-    Tile::template fetch<BQ>(w.o, p.ldgo, n, off_o, s_o[stage]);
+    copy_q.fetch(w.q, n, s_q[stage]);
+    copy_o.fetch(w.o, n, s_o[stage]);
     if (wave < 2)                                     // 64 values each (zeros behind the last)
       copy_to_lds_untracked<4>(untracked_view(wave ? w.del : w.lse, n * 4), l * 4,
                                reinterpret_cast<unsigned char *>(wave ? s_del[stage] : s_lse[stage]));
@@ -459,17 +459,17 @@ template <typename T, int D, int NC, int BK, int OCC, int NCK, int BQ, int OCCK>
 
 }  // namespace
 
-int attn_grad_query_rows(int d, bool bf16) { return d == 256 || (!bf16 && d == 128) ? 64 : 128; }
-int attn_grad_key_rows(int d, bool bf16) { return d >= 128 ? 64 : 128; }
+int attn_grad_query_rows(int d, bool bf16, bool small) { return small || d == 256 || (!bf16 && d == 128) ? 64 : 128; }
+int attn_grad_key_rows(int d, bool bf16, bool small) { return small || d >= 128 ? 64 : 128; }
 
 hipError_t launch_attention_backward(const AttnParams &p, bool bf16, hipStream_t s) {
   const hipError_t e = launch_attention_plan(p, s);
   if (e != hipSuccess) return e;
   if (bf16) {
-    if (p.d == 64) return go<__bf16, 64, 2, 64, 3, 2, 64, 2>(p, s);
+    if (p.d == 64) return p.krows == 64 ? go<__bf16, 64, 1, 64, 4, 1, 64, 4>(p, s) : go<__bf16, 64, 2, 64, 3, 2, 64, 2>(p, s);
     return p.d == 128 ? go<__bf16, 128, 2, 32, 2, 1, 32, 3>(p, s) : go<__bf16, 256, 1, 32, 2, 1, 32, 2>(p, s);
   }
-  if (p.d == 64) return go<float, 64, 2, 32, 2, 2, 32, 2>(p, s);
+  if (p.d == 64) return p.krows == 64 ? go<float, 64, 1, 32, 3, 1, 32, 3>(p, s) : go<float, 64, 2, 32, 2, 2, 32, 2>(p, s);
   return p.d == 128 ? go<float, 128, 1, 32, 2, 1, 32, 2>(p, s) : go<float, 256, 1, 32, 1, 1, 32, 1>(p, s);
 }
 

@@ -77,30 +77,27 @@ template <typename T, int D> struct AttnTile {
       return v;
     }
   }
-  // A thread's byte offset in the rows that it copies, `ld` elements apart: its unit of a wave's first copy.
-  static __device__ __forceinline__ unsigned lane_offset(int64_t ld) {
-    const int r = (threadIdx.x & 255) / kUnits, pos = threadIdx.x % kUnits;
-    return (unsigned)r * (unsigned)(ld * (int64_t)sizeof(T)) + ((pos ^ swz(r)) << 4);
-  }
-  // Fetches ROWS rows (the first `valid` exist, the others become zero) from memory: four waves (of a workgroup of four or eight), a KB each at a time, every
-  // copy a multiple of 8 rows behind the one before, where units lie in the same order (rows of 1 KB: of 4, where units
-  // change places with those 8 away).
-  // The copies are asynchronous and not counted by the compiler: landed() before the barrier behind which they are read.
-  template <int ROWS>
-  static __device__ __forceinline__ void fetch(const T *src, int64_t ld, int valid, unsigned lane_off, unsigned char *t) {
-    constexpr int kStep = 4096 / kRow;
-    static_assert(ROWS % kStep == 0 && kStep % (kUnits == 8 ? 8 : 4) == 0, "");
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
-    const unsigned step = (unsigned)(ld * (int64_t)sizeof(T));
+  // A thread's byte offsets in ROWS rows that it copies, `ld` elements apart: four waves (of a workgroup of four or eight), a KB
+  // each at a time.
+  template <int ROWS> struct Copy {
+    static constexpr int kCopies = ROWS * kRow / 4096, kStep = 4096 / kRow;
+    static_assert(kCopies > 0 && ROWS % kStep == 0, "");
+    unsigned off[kCopies], step;
+    __device__ __forceinline__ explicit Copy(int64_t ld) {
+      step = (unsigned)(ld * (int64_t)sizeof(T));
+      const int r = (threadIdx.x & 255) / kUnits, pos = threadIdx.x % kUnits;
 #pragma unroll
-    for (int i = 0; i < ROWS / kStep; ++i) {
-      const int left = valid - i * kStep;
-      const BufferView view = untracked_view(reinterpret_cast<const char *>(src) + (int64_t)i * kStep * step,
-                                             left > 0 ? (unsigned)(left - 1) * step + kRow : 0);
-      const unsigned off = kStep % 8 == 0 || i % 2 == 0 ? lane_off : lane_off + (((threadIdx.x % kUnits) ^ swz((threadIdx.x & 255) / kUnits)) & 8 ? -128 : 128);
-      copy_to_lds_untracked<16>(view, off, t + (i * 4 + wave) * 1024);
+      for (int i = 0; i < kCopies; ++i) off[i] = (unsigned)(r + i * kStep) * step + ((pos ^ swz(r + i * kStep)) << 4);
     }
-  }
+    // Fetches the rows (the first `valid` exist, the others become zero) from memory.  The copies are asynchronous and not
+    // counted by the compiler: landed() before the barrier behind which they are read.
+    __device__ __forceinline__ void fetch(const T *src, int valid, unsigned char *t) const {
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+      const BufferView view = untracked_view(src, valid > 0 ? (unsigned)(valid - 1) * step + kRow : 0);
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) copy_to_lds_untracked<16>(view, off[i], t + (i * 4 + wave) * 1024);
+    }
+  };
   // Zeros in place of what is not finite, rows r0 .. r0 + n - 1 (four waves).
   static __device__ void settle(unsigned char *t, int r0, int n) {
     for (int i = threadIdx.x & 255; i < n * D; i += 256) {
