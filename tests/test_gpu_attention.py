@@ -4,10 +4,11 @@ Tolerances (relative 2-norm; inputs are independent normal values).
 bf16, eps/2 = 2^-8 a rounding: an output is rounded once (2^-8), and every probability once as an operand: errors
 e_j p_j v_j with |e_j| <= 2^-8, independent of v, add to 2^-8 of the 2-norm of the sum.  Together 2^-7.  A gradient's
 dS = P (dP - delta) is rounded once, the output once, and delta comes from an o rounded to 2^-8: 3 * 2^-8.
-fp32: a score is a sum of up to 256 products (64 roundings of 2^-24 in the matrix instructions' steps of four, of sums
-that grow as the root: below 16 * 2^-24 |q||k| scale, |q||k| scale <= 6 sqrt(d)/sqrt(d)..) and enters an exponential: its absolute
-error, under 2^-18, is the relative one of P.  Sums over keys are sums of such terms: 2^-17 for outputs, and 2^-16 for
-gradients, where dP - delta is a difference of two sums of the same size.  lse: absolute error of the scores, 2^-17.
+fp32: a score is a sum of up to 256 products in 64 steps of four, each with a rounding of 2^-24 of a partial sum that is at
+most about 6 (scores are sums over d of normal values, over sqrt(d)): below 64 * 6 * 2^-24 < 2^-15 at the worst and, as the
+roundings are independent, about 8 * 6 * 2^-24 < 2^-18.  This absolute error is the relative one of P = e^s.  Sums over keys
+are sums of such terms: 2^-17 for outputs, and 2^-16 for gradients, where dP - delta is a difference of two sums of the
+same size.  lse: the absolute error of the scores, 2^-17.
 """
 import math
 
@@ -110,6 +111,16 @@ CASES = [
     (4, 2, 64, [2500, 900], [2500, 900], (10, 3, 0, 300), F32),
     (2, 2, 128, [3], [9000], (1, None, 0, 0), BF),
     (2, 2, 256, [40], [3000], (100, 4, 0, 130), BF),
+    # many heads: the tiles of large calls
+    (128, 128, 64, [1100], [1100], (1, 200, 0, 5), BF),
+    (64, 64, 64, [1100], [1100], (1, None, None, 0), BF),
+    (128, 64, 64, [1100], [1100], (1, None, None, 0), F32),
+    (128, 128, 64, [700, 0, 400], [700, 3, 400], (10, 3, 0, 30), F32),
+    (64, 64, 128, [1100], [1100], (1, None, 0, 0), BF),
+    (64, 32, 128, [600, 501], [600, 501], (1, 300, 0, 8), F32),
+    (64, 32, 256, [1100], [1100], (1, None, 0, 0), BF),
+    (64, 64, 256, [37, 1000], [37, 1000], (8, 20, 2, 9), BF),
+    (64, 64, 256, [520], [520], (1, 100, 0, 3), F32),
 ]
 
 
@@ -191,8 +202,18 @@ def test_gradient_against_differences():
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")], ids=str)
 def test_what_is_not_finite_reaches_only_rows_that_see_it(dtype, value):
+    not_finite(2, 64, dtype, value)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H, d", [(400, 64), (2, 128), (180, 128), (2, 256), (180, 256)])
+def test_what_is_not_finite_in_every_kind_of_tile(H, d, dtype):
+    not_finite(H, d, dtype, float("nan"))
+
+
+def not_finite(H, d, dtype, value):
     from test_weight_layers_amd import ttt
-    H, n, d = 2, 300, 64
+    n = 300
     q, k, v, go = (t.cuda() for t in inputs(n, n, H, H, d, dtype, seed=7))
     kw = dict(heads=H, before=40, sinks=3)
     ok = mask(n, n, 1, 40, 0, 3).cuda()
@@ -204,7 +225,7 @@ def test_what_is_not_finite_reaches_only_rows_that_see_it(dtype, value):
         v2[j, 5] = value
         o2, lse2 = ttt.window_attention(q, k, v2, **kw)
         assert torch.equal(o2[~sees], o[~sees]) and torch.equal(lse2, lse)
-        assert torch.equal(o2[:, torch.arange(2 * d, device="cuda") != 5], o[:, torch.arange(2 * d, device="cuda") != 5])
+        assert torch.equal(o2[:, torch.arange(H * d, device="cuda") != 5], o[:, torch.arange(H * d, device="cuda") != 5])
         assert not torch.isfinite(o2[sees, 5]).any()
         k2 = k.clone()
         k2[j, 7] = value
