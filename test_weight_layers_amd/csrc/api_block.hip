@@ -24,6 +24,7 @@ struct AttnShape {
 };
 
 struct AttnPlan {
+  int64_t whole;
   int qrows, krows, qtiles, ktiles, splits, parts, sink_parts, sink_tiles;
   size_t off_seqs, off_o, off_ml, off_delta, off_part, off_spart, total;
 };
@@ -70,11 +71,12 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     P.qrows = attn_query_rows(a.d, bf16, small);
     P.krows = 64;
     const int64_t wgs = tiles(a.nq, P.qrows) * a.heads, keys = std::min(lk, window + P.qrows + a.sinks);
-    P.splits = attn_splits(wgs, a.nq, a.heads, a.d, P.qrows, keys, bf16);
-    if (P.splits > 1) {
-      P.off_o = take((size_t)P.splits * a.heads * a.nq * a.d * 4);
-      P.off_ml = take((size_t)P.splits * a.heads * a.nq * 8);
-    }
+    // (an end of the window on one side only: tiles see unlike numbers of keys)
+    const AttnCut cut = attn_cut(wgs, ceil_div(a.nq, P.qrows) * a.heads, (a.before < 0) == (a.after < 0), a.d, P.qrows, keys, bf16);
+    P.whole = cut.whole, P.splits = cut.splits;
+    const size_t rows = (size_t)(wgs - cut.whole) * cut.splits * P.qrows;
+    P.off_o = take(rows * a.d * 4);
+    P.off_ml = take(rows * 8);
   } else {
     // Tiles of 64 rows where tiles of 128 are few for 256 CUs, and for twice as many where a mask makes their work uneven
     // (bf16, 64: 8 x 1024 tokens of 12 heads, window 512: 77 us against 91; 8192 tokens of 8 heads, no mask: 589 against 540).
@@ -147,7 +149,7 @@ int attention_params(const AttnShape &a, bool backward, const Rows &q, const Row
   p.per_sink_parts = fast_div(P.sink_parts), p.per_sink_tiles = fast_div(P.sink_tiles), p.per_key_heads = fast_div(a.key_heads);
   p.seqs = reinterpret_cast<AttnSeq *>(b + P.off_seqs);
   p.qrows = P.qrows, p.krows = P.krows, p.qtiles = P.qtiles, p.ktiles = P.ktiles;
-  p.splits = P.splits, p.part_o = reinterpret_cast<float *>(b + P.off_o), p.part_ml = reinterpret_cast<float2 *>(b + P.off_ml);
+  p.whole = (int)P.whole, p.splits = P.splits, p.part_o = reinterpret_cast<float *>(b + P.off_o), p.part_ml = reinterpret_cast<float2 *>(b + P.off_ml);
   p.delta = reinterpret_cast<float *>(b + P.off_delta);
   p.parts = P.parts, p.part = reinterpret_cast<float *>(b + P.off_part);
   p.sink_parts = P.sink_parts, p.sink_tiles = P.sink_tiles, p.spart = reinterpret_cast<float *>(b + P.off_spart);

@@ -44,10 +44,10 @@ struct AttnParams {
   int qrows, krows;                 // rows of a query tile and of a key tile
   int qtiles, ktiles;               // at most so many
   FastDiv per_qtiles, per_ktiles, per_splits, per_parts, per_sink_parts, per_sink_tiles, per_key_heads;
-  // forward: the keys of a tile in `splits` ranges, joined from these
-  int splits;
-  float *part_o;                    // [splits][heads][nq][d]
-  float2 *part_ml;                  // [splits][heads][nq]
+  // forward: the query tiles of all heads from the `whole`th on have their keys in `splits` ranges, joined from these
+  int whole, splits;
+  float *part_o;                    // [tiles in ranges][splits][qrows][d]
+  float2 *part_ml;                  // [tiles in ranges][splits][qrows]
   // backward
   const void *go;
   int64_t ldgo;
@@ -78,7 +78,11 @@ struct AttnStepParams {
 
 // Rows of the tiles that the launchers use.
 int attn_query_rows(int d, bool bf16, bool small);
-int attn_splits(int64_t workgroups, int64_t nq, int heads, int d, int rows, int64_t keys, bool bf16);
+struct AttnCut {
+  int64_t whole;                    // query tiles of all heads that are not cut
+  int splits;                       // ranges of keys of the others
+};
+AttnCut attn_cut(int64_t workgroups, int64_t busy, bool even, int d, int rows, int64_t keys, bool bf16);
 int attn_grad_query_rows(int d, bool bf16, bool small);
 int attn_grad_key_rows(int d, bool bf16, bool small);
 hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s);

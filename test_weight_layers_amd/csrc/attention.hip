@@ -8,6 +8,14 @@ namespace {
 
 constexpr int kZeroBlocks = 32;     // workgroups that fill rows of no sequence
 
+// Query tile `item` of all heads; false: there is none.  Without a window late tiles see the most keys: the late half first,
+// then the early half from its first tile on, so that a CU that takes one of each has as much to do as the others.
+__device__ __forceinline__ bool forward_tile(const AttnParams &p, int item, AttnSeq *s, int *tile, int *seq, int *h) {
+  *h = quotient(item, p.per_qtiles);
+  const int order = item - *h * p.qtiles, half = (p.qtiles + 1) / 2;
+  return tile_of<false>(p, order < half ? p.qtiles - 1 - order : order - half, s, tile, seq);
+}
+
 // Four waves of NC x 16 queries each; BK keys at a time through two LDS buffers.  KG = 2: eight waves, the second four with
 // the same queries and every other tile of keys, joined at the end: where there are few query tiles a SIMD then has two
 // waves that wait in turn.
@@ -19,7 +27,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
   constexpr int kPitch = D + 4;                       // floats of a query's row of the second four waves' sums
   __shared__ __attribute__((aligned(1024))) unsigned char s_kv[KG][2][2][kTile];
   static_assert(KG == 1 || QR * (kPitch + 2) * 4 <= (int)sizeof(s_kv), "");
-  const int items = p.qtiles * p.heads * p.splits;
+  const int cut = (p.qtiles * p.heads - p.whole) * p.splits, items = p.whole + cut;
   if ((int)blockIdx.x >= items) {
     if (threadIdx.x >= 256) return;
     const int blk = blockIdx.x - items;
@@ -31,14 +39,13 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
           p.lse[(int64_t)h * p.nq + (i < used.x ? i : used.y + (i - used.x))] = -__builtin_inff();
     return;
   }
-  const int item = attn_item(blockIdx.x, items), rest = quotient(item, p.per_splits), split = item - rest * p.splits;
-  const int h = quotient(rest, p.per_qtiles), kh = quotient(h, p.group);
+  const bool in_parts = (int)blockIdx.x >= p.whole;
+  const int id = in_parts ? attn_item(blockIdx.x - p.whole, cut) : attn_item(blockIdx.x, p.whole);
+  const int one = in_parts ? quotient(id, p.per_splits) : id, split = in_parts ? id - one * p.splits : 0;
   AttnSeq s;
-  int tile, seq;
-  // Without a window late tiles see the most keys: the late half first, then the early half from its first tile on, so
-  // that a CU that takes one of each has as much to do as the others.
-  const int order = rest - h * p.qtiles, half = (p.qtiles + 1) / 2;
-  if (!tile_of<false>(p, order < half ? p.qtiles - 1 - order : order - half, &s, &tile, &seq)) return;
+  int tile, seq, h;
+  if (!forward_tile(p, in_parts ? p.whole + one : one, &s, &tile, &seq, &h)) return;
+  const int kh = quotient(h, p.group);
   const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3, kg = wave8 >> 2;
   const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
   const int t0 = tile * QR, row0 = t0 + wave * 16 * NC;
@@ -59,7 +66,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
   const int k0 = seen_keys(p, s, t0).x, k1 = seen_keys(p, s, last - 1).y, se = p.sinks < k0 ? p.sinks : k0;
   const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
-  const int share = quotient(nt + p.splits - 1, p.per_splits), first = split * share, end = first + share < nt ? first + share : nt;
+  const int share = in_parts ? quotient(nt + p.splits - 1, p.per_splits) : nt, first = split * share, end = first + share < nt ? first + share : nt;
   const typename Tile::Lane lane = Tile::lane();
   const typename Tile::template Copy<BK> copy_k(p.ldk), copy_v(p.ldv);
   const KeyWalk<T, BK> start(first + kg, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
@@ -250,8 +257,8 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
     if (i >= s.ql) continue;
     const bool empty = hi[c] == lo[c] && (p.sinks == 0 || lo[c] == 0);
     const int64_t row = s.qs + i;
-    if (p.splits > 1) {
-      const int64_t at = ((int64_t)split * p.heads + h) * p.nq + row;
+    if (in_parts) {
+      const int64_t at = (int64_t)id * QR + (i - t0);
 #pragma unroll
       for (int d = 0; d < ND; ++d) store4(p.part_o + at * D + 16 * d + 4 * g, o[d][c]);
       if (g == 0) p.part_ml[at] = float2{m[c], empty ? -1.0f : sum[c]};
@@ -266,31 +273,32 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
   }
 }
 
-// Joins the splits, in their order: D / 4 lanes a row and head.
+// Joins the ranges of keys, in their order: a query tile by blockIdx.x, 1024 / D of its rows by blockIdx.y, D / 4 lanes a row.
 template <typename T, int D> __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   constexpr int L = D / 4;
-  const int64_t at = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int c = threadIdx.x % L;
-  const int2 used = used_rows<false>(p);
-  if (at >= (int64_t)p.nq * p.heads) return;
-  const int h = (int)(at % p.heads);
-  const int64_t row = at / p.heads, step = (int64_t)p.heads * p.nq, first = (int64_t)h * p.nq + row;
-  if (row < used.x || row >= used.y) return;
+  const int c = threadIdx.x % L, r = blockIdx.y * (256 / L) + threadIdx.x / L;
+  AttnSeq s;
+  int tile, seq, h;
+  if (!forward_tile(p, p.whole + blockIdx.x, &s, &tile, &seq, &h)) return;
+  const int i = tile * p.qrows + r;
+  if (i >= s.ql) return;
+  const int64_t row = s.qs + i, first = (int64_t)blockIdx.x * p.splits * p.qrows + r;
   const float c2 = p.scale * kLog2e;
   float m = -__builtin_inff(), sum = 0.0f;
-  for (int i = 0; i < p.splits; ++i) m = fmaxf(m, p.part_ml[first + i * step].x);
+  for (int x = 0; x < p.splits; ++x) m = fmaxf(m, p.part_ml[first + x * p.qrows].x);
   f32x4 o = zero_f4();
   bool empty = false;
-  for (int i = 0; i < p.splits; ++i) {
-    const float2 ml = p.part_ml[first + i * step];
+#pragma unroll 4
+  for (int x = 0; x < p.splits; ++x) {
+    const float2 ml = p.part_ml[first + x * p.qrows];
     empty |= ml.y < 0.0f;
     const float w = ml.x == m ? 1.0f : __builtin_amdgcn_exp2f((ml.x - m) * c2);
     sum += ml.y * w;
-    o += *reinterpret_cast<const f32x4 *>(p.part_o + (first + i * step) * D + 4 * c) * w;
+    o += *reinterpret_cast<const f32x4 *>(p.part_o + (first + x * p.qrows) * D + 4 * c) * w;
   }
   const float inv = empty ? 0.0f : 1.0f / sum;
   store4(static_cast<T *>(p.o) + row * p.ldo + h * D + 4 * c, o * inv);
-  if (p.lse && c == 0) p.lse[first] = empty ? -__builtin_inff() : (m * c2 + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (p.lse && c == 0) p.lse[(int64_t)h * p.nq + row] = empty ? -__builtin_inff() : (m * c2 + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 // More sequences than a wave has lanes: one workgroup writes the table.
@@ -331,12 +339,12 @@ __global__ __launch_bounds__(1024) void attn_plan_kernel(AttnParams p) {
 }
 
 template <typename T, int D, int NC, int BK, int KG, int OCC> hipError_t go(const AttnParams &p, hipStream_t s) {
-  const int items = p.qtiles * p.heads * p.splits;
-  hipLaunchKernelGGL((attn_forward_kernel<T, D, NC, BK, KG, OCC>), dim3(items + (p.cu_q ? kZeroBlocks : 0)), dim3(256 * KG), 0, s, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1 || p.nq == 0) return e;
-  hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)(((int64_t)p.nq * p.heads + 1024 / D - 1) / (1024 / D))), dim3(256),
-                     0, s, p);
+  const int tiles = p.qtiles * p.heads - p.whole;     // in ranges
+  hipLaunchKernelGGL((attn_forward_kernel<T, D, NC, BK, KG, OCC>), dim3(p.whole + tiles * p.splits + (p.cu_q ? kZeroBlocks : 0)),
+                     dim3(256 * KG), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || tiles == 0) return e;
+  hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(tiles, p.qrows * D / 1024), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -344,21 +352,25 @@ template <typename T, int D, int NC, int BK, int KG, int OCC> hipError_t go(cons
 
 int attn_query_rows(int d, bool bf16, bool small) { return small || (!bf16 && d == 256) ? 64 : 128; }
 
-// Ranges that the keys of a query tile are cut in: the rounds that the workgroups of all ranges take on 256 CUs, each for a
-// range's share of the time of a tile's keys at the rate that full CUs reach, and what the join reads and writes (at 4.5 TB/s,
-// with a launch of 4 us).  10992 queries, 8 heads of 128, 17k keys each: 688 workgroups in two rounds of 512, 680 us; in two
-// ranges three rounds of half the time.
-int attn_splits(int64_t workgroups, int64_t nq, int heads, int d, int rows, int64_t keys, bool bf16) {
+// Ranges that the keys of a query tile are cut in, for all tiles or, where these are alike, for those behind the last full
+// round of workgroups on 256 CUs: the rounds that they take, each for a range's share of the time of a tile's keys at the
+// rate that full CUs reach, and what the join reads and writes (at 4.5 TB/s, with a launch of 4 us).  `busy`: workgroups that
+// have a tile.  10992 queries, 8 heads of 128, 9618 keys each: 688 workgroups in rounds of 512, all in two ranges 574 us,
+// the last 176 so 538.  Causal tiles even out by themselves (9600 tokens, 8 heads of 128 on 2: 262 us, cut so 287).
+AttnCut attn_cut(int64_t workgroups, int64_t busy, bool even, int d, int rows, int64_t keys, bool bf16) {
   const bool small = rows == 64;
   const int per_cu = bf16 ? (d == 64 && !small ? 3 : d == 256 ? 1 : 2) : d == 64 ? 2 : 1;
   const double rate = bf16 ? (d == 64 ? 850e6 : d == 128 ? 950e6 : 400e6) : (d == 64 ? 120e6 : d == 128 ? 105e6 : 55e6);   // flop per us
-  const int64_t slots = 256 * per_cu;
-  const double one = 4.0 * rows * (double)keys * d * (double)slots / rate, bytes = (double)nq * heads * d * 8;
-  int best = 1;
-  double least = (double)((workgroups + slots - 1) / slots) * one;
-  for (int s = 2; s <= 32 && keys / s >= 256; ++s) {
-    const double t = (double)((workgroups * s + slots - 1) / slots) / s * one + 4.0 + s * bytes / 4.5e6;
-    if (t < 0.95 * least) least = t, best = s;
+  const int64_t slots = 256 * per_cu, full = even ? busy / slots * slots : 0;
+  const double one = 4.0 * rows * (double)keys * d * (double)slots / rate, bytes = (double)rows * d * 8;
+  AttnCut best{workgroups, 1};
+  double least = (double)((busy + slots - 1) / slots) * one;
+  for (const int64_t whole : {int64_t(0), full}) {
+    const int64_t rest = busy - whole;
+    for (int s = 2; rest > 0 && s <= 32 && keys / s >= 256; ++s) {
+      const double t = ((double)(whole / slots) + (double)((rest * s + slots - 1) / slots) / s) * one + 4.0 + s * rest * bytes / 4.5e6;
+      if (t < 0.95 * least) least = t, best = AttnCut{whole, s};
+    }
   }
   return best;
 }

@@ -121,6 +121,10 @@ CASES = [
     (64, 32, 256, [1100], [1100], (1, None, 0, 0), BF),
     (64, 64, 256, [37, 1000], [37, 1000], (8, 20, 2, 9), BF),
     (64, 64, 256, [520], [520], (1, 100, 0, 3), F32),
+    # more tiles than run at once: the last ones' keys in ranges
+    (40, 20, 128, [2200], [2200], (1, None, None, 0), BF),
+    (40, 40, 64, [2200], [2200], (1, 1500, 0, 10), F32),
+    (60, 60, 64, [1200, 1000], [2400, 1300], (1, None, None, 0), BF),
 ]
 
 
