@@ -26,7 +26,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
   constexpr int NK = D / 32, ND = D / 16, NU = BK / 16, kTile = BK * Tile::kRow, QR = 64 * NC;
   constexpr int kPitch = D + 4;                       // floats of a query's row of the second four waves' sums
   __shared__ __attribute__((aligned(1024))) unsigned char s_kv[KG][2][2][kTile];
-  static_assert(KG == 1 || QR * (kPitch + 2) * 4 <= (int)sizeof(s_kv), "");
+  static_assert(KG == 1 || QR * kPitch * 4 <= (int)sizeof(s_kv), "");
   const int cut = (p.qtiles * p.heads - p.whole) * p.splits, items = p.whole + cut;
   if ((int)blockIdx.x >= items) {
     if (threadIdx.x >= 256) return;
@@ -226,29 +226,25 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
     sum[c] += __shfl_xor(sum[c], 32);
   }
   if constexpr (KG == 2) {                            // (nobody reads the tiles behind the barrier above)
-    float *so = reinterpret_cast<float *>(s_kv);      // a query's sums, then its m and sum
+    float *so = reinterpret_cast<float *>(s_kv) + (wave * 16 * NC + li) * kPitch;       // a query's sums, then its m and sum
     if (kg == 1)
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        float *to = so + (wave * 16 * NC + 16 * c + li) * (kPitch + 2);
+        float *to = so + 16 * c * kPitch;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) to[16 * d + 4 * g + x] = o[d][c][x];
-        if (g == 0) to[kPitch] = m[c], to[kPitch + 1] = sum[c];
+        for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4 *>(to + 16 * d + 4 * g) = o[d][c];
+        if (g == 0) to[D] = m[c], to[D + 1] = sum[c];
       }
     __syncthreads();
     if (kg == 1) return;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const float *from = so + (wave * 16 * NC + 16 * c + li) * (kPitch + 2);
-      const float m2 = from[kPitch], top = fmaxf(m[c], m2);
+      const float *from = so + 16 * c * kPitch;
+      const float m2 = from[D], top = fmaxf(m[c], m2);
       const float a = m[c] == top ? 1.0f : __builtin_amdgcn_exp2f((m[c] - top) * c2), b = m2 == top ? 1.0f : __builtin_amdgcn_exp2f((m2 - top) * c2);
-      m[c] = top, sum[c] = sum[c] * a + from[kPitch + 1] * b;
+      m[c] = top, sum[c] = sum[c] * a + from[D + 1] * b;
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[d][c][x] = o[d][c][x] * a + from[16 * d + 4 * g + x] * b;
+      for (int d = 0; d < ND; ++d) o[d][c] = o[d][c] * a + *reinterpret_cast<const f32x4 *>(from + 16 * d + 4 * g) * b;
     }
   }
 #pragma unroll
