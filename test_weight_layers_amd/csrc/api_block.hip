@@ -92,10 +92,14 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     if (P.parts > 1) P.off_part = take((size_t)P.parts * a.nk * a.key_heads * 2 * a.d * 4);
     // Sinks, which all queries behind their window see: ranges of these of their own, where a sequence may be long beside
     // the window (lengths are on the device: taken as four times the mean), joined with the window's part by the sums' kernel.
-    if (a.sinks > 0 && a.before >= 0 && a.nq > 2 * (window + P.krows)) {
-      P.sink_tiles = (int)ceil_div(std::min<int64_t>(a.sinks, a.nk), P.krows);
-      const int64_t one = (int64_t)a.nseq * P.sink_tiles * a.key_heads * P.krows * 2 * a.d * 4;
-      P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>({32, std::min(a.nq, 4 * lq) * grp / std::max<int64_t>(window * grp / 2, 512), (int64_t(64) << 20) / one}));
+    // Not where one range takes 64 MB already: so many sequences keep the CUs busy without.
+    const int64_t sink_tiles = ceil_div(std::min<int64_t>(a.sinks, a.nk), P.krows);
+    const int64_t most = int64_t(64) << 20;
+    const double bytes = (double)a.nseq * (double)sink_tiles * a.key_heads * P.krows * 2.0 * a.d * 4.0;
+    if (bytes > 0 && bytes <= (double)most && a.before >= 0 && a.nq > 2 * (window + P.krows)) {
+      const int64_t one = (int64_t)bytes;
+      P.sink_tiles = (int)sink_tiles;
+      P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>({32, std::min(a.nq, 4 * lq) * grp / std::max<int64_t>(window * grp / 2, 512), most / one}));
       P.off_spart = take((size_t)one * (1 + P.sink_parts));
     }
   }

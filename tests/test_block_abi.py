@@ -44,6 +44,12 @@ def test_attention_workspace(lib):
         assert ws(lib, ATT, *args)[0] == 0
 
 
+def test_attention_workspace_of_sinks(lib):
+    assert ws(lib, ATT, 2, 1, 64, 1000, 0, 1, 1, 10, 0, 4, BF16, 1)[0] == 0               # sinks, but no keys
+    st, b = ws(lib, ATT, 16, 8, 128, 500000, 500000, 10000, 1, 63, 0, 4, BF16, 1)         # of many sequences
+    assert st == 0 and b < 200 * MB
+
+
 @pytest.mark.parametrize("args,code", [
     ((4, 3, 64, 10, 10, 1, 1, -1, 0, 0, BF16, 0), -1),          # heads not a multiple of key heads
     ((0, 1, 64, 10, 10, 1, 1, -1, 0, 0, BF16, 0), -1),

@@ -336,6 +336,24 @@ def test_no_rows():
                                      heads=1).shape == (0, 64)
 
 
+def test_sinks_without_keys_and_of_many_sequences():
+    from test_weight_layers_amd import ttt
+    x, e = torch.randn(300, 128, device="cuda"), torch.empty(0, 64, device="cuda")
+    kw = dict(heads=2, key_heads=1, before=10, sinks=4)
+    o, lse = ttt.window_attention(x, e, e.clone(), **kw)
+    gq, gk, gv = ttt.window_attention_backward(x, e, e.clone(), o, lse, x.clone(), **kw)
+    assert (o == 0).all() and (gq == 0).all() and gk.shape == gv.shape == (0, 64)
+    # more of them than their sums are kept apart for (64 MB)
+    lens, how = [300, 7] * 300, (1, 20, 0, 4)
+    q, k, v, go = inputs(sum(lens), sum(lens), 4, 4, 64, BF)
+    _, _, ref = reference(q, k, v, 4, 4, lens, lens, how, grad_o=go)
+    q, k, v, go = (t.cuda() for t in (q, k, v, go))
+    kw = dict(heads=4, before=20, sinks=4, cu_seqlens=offsets(lens))
+    o, lse = ttt.window_attention(q, k, v, **kw)
+    for a, r in zip(ttt.window_attention_backward(q, k, v, o, lse, go, **kw), ref):
+        assert rel(a, r) <= GTOL[BF]
+
+
 # ------------------------------------------------------------------ one token
 def ring_place(p, capacity, sinks):
     return p if p < sinks else sinks + (p - sinks) % (capacity - sinks)
