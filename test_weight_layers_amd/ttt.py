@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -764,10 +765,19 @@ def window_attention_workspace_bytes(heads: int, key_heads: int, d: int, nq: int
     return out.value
 
 
-def _attention_workspace(H, Hk, d, nq, nk, S, mask, code, backward, device) -> torch.Tensor:
+# (functions of the sizes alone: a call of a few tokens takes less than asking the library takes)
+@functools.lru_cache(maxsize=4096)
+def _attention_bytes(*sizes: int) -> int:
     out = ctypes.c_size_t()
-    _check(load().ttt_window_attention_workspace_bytes(H, Hk, d, nq, nk, S, *mask, code, backward, ctypes.byref(out)))
-    return torch.empty(out.value, dtype=torch.uint8, device=device)
+    _check(load().ttt_window_attention_workspace_bytes(*sizes, ctypes.byref(out)))
+    return out.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_step_bytes(*sizes: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().ttt_window_attention_step_workspace_bytes(*sizes, ctypes.byref(out)))
+    return out.value
 
 
 def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, heads: int, key_heads: Optional[int] = None,
@@ -792,11 +802,11 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, heads
     else:
         ldo = _row(out, dtype, dev, nq, H * d, "out")
     if lse_out is None:
-        lse_out = torch.empty((H, nq), dtype=torch.float32, device=q.device)
+        lse_out = q.new_empty((H, nq), dtype=torch.float32)
     elif lse_out.dtype != torch.float32 or lse_out.shape != (H, nq) or not lse_out.is_contiguous() or lse_out.get_device() != dev:
         raise ValueError(f"lse_out must be a contiguous float32 tensor [{H}, {nq}] on cuda:{dev}")
     if workspace is None:
-        workspace = _attention_workspace(H, Hk, d, nq, nk, S, mask, code, 0, q.device)
+        workspace = q.new_empty((_attention_bytes(H, Hk, d, nq, nk, S, *mask, code, 0),), dtype=torch.uint8)
     _check(load().ttt_window_attention(H, Hk, d, q.data_ptr(), ld[0], k.data_ptr(), ld[1], v.data_ptr(), ld[2],
                                        out.data_ptr(), ldo, lse_out.data_ptr(), nq, nk, _ptr(cu_seqlens),
                                        _ptr(cu_seqlens_k), S, *mask, scale, code, flags, workspace.data_ptr(),
@@ -820,10 +830,10 @@ def window_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if lse.dtype != torch.float32 or lse.shape != (H, nq) or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError(f"lse must be a contiguous float32 tensor [{H}, {nq}] on cuda:{dev}")
     if out is None:
-        out = tuple(torch.empty((n, w), dtype=dtype, device=q.device) for n, w in ((nq, H * d), (nk, Hk * d), (nk, Hk * d)))
+        out = q.new_empty((nq, H * d)), q.new_empty((nk, Hk * d)), q.new_empty((nk, Hk * d))
     gq, gk, gv = out
     if workspace is None:
-        workspace = _attention_workspace(H, Hk, d, nq, nk, S, mask, code, 1, q.device)
+        workspace = q.new_empty((_attention_bytes(H, Hk, d, nq, nk, S, *mask, code, 1),), dtype=torch.uint8)
     _check(load().ttt_window_attention_backward(
         H, Hk, d, q.data_ptr(), ld[0], k.data_ptr(), ld[1], v.data_ptr(), ld[2], o.data_ptr(), ldo, lse.data_ptr(),
         grad_o.data_ptr(), ldgo, gq.data_ptr(), _row(gq, dtype, dev, nq, H * d, "grad_q"), gk.data_ptr(),
@@ -868,16 +878,13 @@ def window_attention_step(k_cache: torch.Tensor, v_cache: torch.Tensor, q: torch
         flags = ATTENTION_ZERO_UNUSED
     else:
         ldo = _row(out, dtype, dev, n, H * d, "out")
-    L = load()
     if workspace is None:
-        size = ctypes.c_size_t()
-        _check(L.ttt_window_attention_step_workspace_bytes(H, Hk, d, n, shape[1], code, ctypes.byref(size)))
-        workspace = torch.empty(size.value, dtype=torch.uint8, device=q.device)
-    _check(L.ttt_window_attention_step(H, Hk, d, k_cache.data_ptr(), v_cache.data_ptr(), stride[1], stride[0], shape[0],
-                                       shape[1], _ptr(slots), positions.data_ptr(), q.data_ptr(), ldq, k.data_ptr(),
-                                       ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, n, int(block),
-                                       _limit(before, "before"), int(sinks), d ** -0.5 if scale is None else float(scale),
-                                       code, flags, workspace.data_ptr(), _bytes(workspace, dev), _stream()))
+        workspace = q.new_empty((_attention_step_bytes(H, Hk, d, n, shape[1], code),), dtype=torch.uint8)
+    _check(load().ttt_window_attention_step(
+        H, Hk, d, k_cache.data_ptr(), v_cache.data_ptr(), stride[1], stride[0], shape[0], shape[1], _ptr(slots),
+        positions.data_ptr(), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, n, int(block),
+        _limit(before, "before"), int(sinks), d ** -0.5 if scale is None else float(scale), code, flags,
+        workspace.data_ptr(), _bytes(workspace, dev), _stream()))
     return out
 
 
