@@ -430,11 +430,11 @@ int ttt_orthogonalise(int32_t rows, int32_t cols, int32_t batch, const void *g, 
  *   q), or both NULL (one sequence of all rows).  Read on the device, clamped to the rows and to a running maximum.
  *   Rows of no sequence are not read; their o is left as it was, or set to zero with TTT_ATTENTION_ZERO_UNUSED; their
  *   lse is -infinity and their gradients are zero.
- * Precision: fp32 scores, statistics and sums (a q k beyond fp32's range is infinite).  bf16: the probabilities (and dS) are rounded once to bf16 as operands
- *   of the second products.  fp32: fp32 products.
+ * Precision: fp32 scores, statistics and sums (a q k beyond fp32's range is infinite).  bf16: the probabilities (and
+ *   dS) are rounded once to bf16 as operands of the second products.  fp32: fp32 products.
  *   The gradient takes e^(s - lse) from an fp32 lse: its relative error grows as |lse| 2^-24.
  * A value that is not finite reaches only rows that see its key.  Deterministic: the same inputs give the same bits.
- * nq, nk <= 2^28; tiles x heads (x ranges of keys or queries) below 2^23.
+ * nq, nk <= 2^28; tiles x heads (x ranges of keys or queries; the gradient's of queries and of keys together) below 2^23.
  */
 enum { TTT_ATTENTION_ZERO_UNUSED = 1 };
 /* Bytes of workspace of ttt_window_attention (backward = 0) or its gradient (backward = 1) for these shapes. */

@@ -4,6 +4,9 @@
 // |m| or sqrt(v); an element is s c |c| / 127^2 (m) or, its root, s c^2 / 255^2 (v), c to the nearest: the codes are
 // finer where values are small.  The arithmetic is fp32 without contraction, each step rounded as it is written, so
 // that a code is the formula's also where a value lies next to the border of two.
+// Bound by memory: bf16 with fp32 masters and 8-bit states, 16 bytes an element read and written, 151 million elements in
+// three launches 495 us (4.9 TB/s, a copy's rate); fp32 with 32-bit states, 7.1 million elements 32 us (28 bytes each; part
+// of it stays in the last level of cache from call to call).  Up to 48 tensors go in a launch, as its argument.
 #include <cmath>
 
 #include "adamw.h"

