@@ -85,10 +85,15 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     P.qrows = attn_grad_query_rows(a.d, bf16, small);
     P.krows = attn_grad_key_rows(a.d, bf16, small);
     P.off_delta = take((size_t)a.heads * a.nq * 4);
-    const int64_t wgs = tiles(a.nk, P.krows) * a.key_heads, queries = std::min(lq, window + P.krows);
-    // Few key tiles: ranges of queries, 512 or more each, whose sums are written and added (1024 x 1024, 4 heads of 256: 87 us
-    // with ranges of 256, 65 of 512; 4096 x 4096 causal, 16 heads of 64 on 2: 758 us with one range, 243 with four).
-    if (wgs > 0 && wgs < 256) P.parts = (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, queries * grp / 512, 64}));
+    // (lengths are on the device: the longest sequence is taken as twice the mean)
+    const bool bounded = a.before >= 0 && a.after >= 0;
+    const int64_t longest = a.nseq == 1 ? lq : std::min(a.nq, 2 * lq), span = bounded ? ((int64_t)a.before + a.after + 1) * a.block : longest;
+    AttnGradWork w;
+    w.key_items = ceil_div(a.nk, P.krows) * a.key_heads, w.query_items = ceil_div(a.nq, P.qrows) * a.heads;
+    w.queries = std::min(longest, span + P.krows) * grp, w.keys = std::min(longest, span + P.qrows);
+    const double half = bounded || (a.before < 0 && a.after < 0) ? 1.0 : 0.6;           // of the rows, where one side ends the window
+    w.mean_queries = std::min(lq, window + P.krows) * grp * half, w.mean_keys = std::min(lk, window + P.qrows) * half;
+    P.parts = attn_grad_parts(w, a.d, bf16, P.qrows, P.krows, (double)a.nk * a.key_heads * 2 * a.d * 4);
     if (P.parts > 1) P.off_part = take((size_t)P.parts * a.nk * a.key_heads * 2 * a.d * 4);
     // Sinks, which all queries behind their window see: ranges of these of their own, where a sequence may be long beside
     // the window (lengths are on the device: taken as four times the mean), joined with the window's part by the sums' kernel.

@@ -83,6 +83,12 @@ struct AttnCut {
   int splits;                       // ranges of keys of the others
 };
 AttnCut attn_cut(int64_t workgroups, int64_t busy, bool even, int d, int rows, int64_t keys, bool bf16);
+struct AttnGradWork {
+  int64_t key_items, query_items;               // key tiles of all key heads, query tiles of all heads
+  int64_t queries, keys;                        // that the longest of them walk over
+  double mean_queries, mean_keys;
+};
+int attn_grad_parts(const AttnGradWork &w, int d, bool bf16, int qrows, int krows, double bytes);
 int attn_grad_query_rows(int d, bool bf16, bool small);
 int attn_grad_key_rows(int d, bool bf16, bool small);
 hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s);

@@ -9,6 +9,9 @@
 // Bound by the products, 7 of 2 d operations a visible pair where the formula has 5.  8192 x 8192 without a mask, bf16: 8 heads
 // of 64 540 us, 8 of 128 1040, 4 of 256 1710 (890, 925 and 560 TFLOP/s of the 7; a large product reaches 1216); fp32: 3560,
 // 7260 and 8840 us (135, 132 and 109 of 137).
+#include <algorithm>
+#include <cmath>
+
 #include "attn_tile.h"
 
 namespace ttt {
@@ -456,6 +459,29 @@ template <typename T, int D, int NCQ, int BK, int NCK, int BQ, int OCC> hipError
 }
 
 }  // namespace
+
+// Ranges that the queries of a key tile (all heads of its key head) are cut in, each a workgroup of its own whose sums are
+// written and added (`bytes` a range, both at 2.5 TB/s together, 4 us the launch): as many as bring the longest workgroup
+// down to what the others keep the 256 CUs busy with.  Times of 32 rows of the other axis for a tile of 64 of its own on a CU
+// alone, and how many such a CU does at once, are measured; a larger tile takes less than in proportion and dq three
+// quarters of dk and dv.  Of 28 shapes of both types and all d, 100 to 8192 rows, the times are 2% over the best number of
+// ranges' in the mean and 9% at most (1024 x 1024, 4 heads of 256, bf16: 87 us in one range, 71 in two, 93 in six; fp32, 2 heads of
+// 256 on 1, 1974 tokens in 5 sequences: 755, 390 and 302).
+int attn_grad_parts(const AttnGradWork &w, int d, bool bf16, int qrows, int krows, double bytes) {
+  const double key = (bf16 ? (d == 64 ? 0.7 : d == 128 ? 1.1 : 2.1) : d == 64 ? 3.0 : d == 128 ? 4.7 : 9.3) * std::pow(krows / 64.0, 0.8) / 32;
+  const double query = 0.75 * key * std::pow((double)qrows / krows, 0.8);
+  const double at_once = bf16 ? (d == 64 ? 3.0 : d == 128 ? 2.0 : 1.2) : d == 64 ? 1.5 : d == 128 ? 1.3 : 1.15;
+  const double mean = (w.key_items * w.mean_queries * key + w.query_items * w.mean_keys * query) / (256 * at_once);
+  int best = 1;
+  double least = 0.0;
+  for (int parts = 1; parts <= 32; ++parts) {
+    const double longest = std::max((double)w.queries / parts * key, w.keys * query);
+    const double t = (w.key_items * parts + w.query_items > 256 ? std::max(longest, mean + longest / 2) : longest) +
+                     (parts > 1 ? 4.0 + parts * bytes / 2.5e6 : 0.0);
+    if (parts == 1 || t < 0.97 * least) least = t, best = parts;
+  }
+  return best;
+}
 
 int attn_grad_query_rows(int d, bool bf16, bool small) { return small || (!bf16 && d >= 128) ? 64 : 128; }
 int attn_grad_key_rows(int d, bool bf16, bool small) { return small || d >= 128 ? 64 : 128; }
