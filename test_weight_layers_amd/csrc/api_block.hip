@@ -51,11 +51,9 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
   const auto tiles = [&](int64_t n, int rows) { return a.nseq == 1 ? ceil_div(n, rows) : n / rows + std::min<int64_t>(a.nseq, n); };
   // keys that a query sees inside its window, at most, and those of a sequence, at the mean
   const int64_t lk = ceil_div(a.nk, a.nseq), lq = ceil_div(a.nq, a.nseq);
-  int64_t window = lk;
-  if (a.before >= 0 && a.after >= 0) {
-    const int64_t w = ((int64_t)a.before + a.after + 1) * a.block;
-    window = w < lk ? w : lk;
-  }
+  // limited on one side only, a window's rows see unlike numbers of keys, about half of all in the mean
+  const bool bounded = a.before >= 0 && a.after >= 0, limited = a.before >= 0 || a.after >= 0;
+  const int64_t span = bounded ? std::min(((int64_t)a.before + a.after + 1) * a.block, int64_t(1) << 40) : 0, window = bounded ? std::min(span, lk) : lk;
   AttnPlan P{};
   P.splits = P.parts = 1;
   size_t o = 0;
@@ -70,9 +68,12 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     const bool small = tiles(a.nq, attn_query_rows(a.d, bf16, false)) * a.heads < 512;
     P.qrows = attn_query_rows(a.d, bf16, small);
     P.krows = 64;
-    const int64_t wgs = tiles(a.nq, P.qrows) * a.heads, keys = std::min(lk, window + P.qrows + a.sinks);
-    // (an end of the window on one side only: tiles see unlike numbers of keys)
-    const AttnCut cut = attn_cut(wgs, ceil_div(a.nq, P.qrows) * a.heads, (a.before < 0) == (a.after < 0), a.d, P.qrows, keys, bf16);
+    const int64_t longest = a.nseq == 1 ? lk : std::min(a.nk, lk + lk / 2), wgs = tiles(a.nq, P.qrows) * a.heads;
+    AttnWork w;
+    w.tiles = wgs, w.busy = ceil_div(a.nq, P.qrows) * a.heads, w.even = a.nseq == 1 && (bounded || !limited);
+    w.keys = std::min(longest, (bounded ? span : longest) + P.qrows + a.sinks);
+    w.mean_keys = std::min(lk, window + P.qrows + a.sinks) * (bounded || !limited ? 1.0 : 0.55);
+    const AttnCut cut = attn_cut(w, a.d, P.qrows, bf16);
     P.whole = cut.whole, P.splits = cut.splits;
     const size_t rows = (size_t)(wgs - cut.whole) * cut.splits * P.qrows;
     P.off_o = take(rows * a.d * 4);
@@ -80,18 +81,17 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
   } else {
     // Tiles of 64 rows where tiles of 128 are few for 256 CUs, and for twice as many where a mask makes their work uneven
     // (bf16, 64: 8 x 1024 tokens of 12 heads, window 512: 77 us against 91; 8192 tokens of 8 heads, no mask: 589 against 540).
-    const int64_t few = a.before >= 0 || a.after >= 0 ? 1024 : 512;
+    const int64_t few = limited ? 1024 : 512;
     const bool small = a.d == 64 ? tiles(a.nk, 128) * a.key_heads < few : a.d == 256 && tiles(a.nq, 128) * a.heads < 256;
     P.qrows = attn_grad_query_rows(a.d, bf16, small);
     P.krows = attn_grad_key_rows(a.d, bf16, small);
     P.off_delta = take((size_t)a.heads * a.nq * 4);
     // (lengths are on the device: the longest sequence is taken as twice the mean)
-    const bool bounded = a.before >= 0 && a.after >= 0;
-    const int64_t longest = a.nseq == 1 ? lq : std::min(a.nq, 2 * lq), span = bounded ? ((int64_t)a.before + a.after + 1) * a.block : longest;
+    const int64_t longest = a.nseq == 1 ? std::max(lq, lk) : std::min(std::max(a.nq, a.nk), 2 * std::max(lq, lk));
     AttnGradWork w;
     w.key_items = ceil_div(a.nk, P.krows) * a.key_heads, w.query_items = ceil_div(a.nq, P.qrows) * a.heads;
-    w.queries = std::min(longest, span + P.krows) * grp, w.keys = std::min(longest, span + P.qrows);
-    const double half = bounded || (a.before < 0 && a.after < 0) ? 1.0 : 0.6;           // of the rows, where one side ends the window
+    w.queries = std::min(longest, (bounded ? span : longest) + P.krows) * grp, w.keys = std::min(longest, (bounded ? span : longest) + P.qrows);
+    const double half = bounded || !limited ? 1.0 : 0.6;
     w.mean_queries = std::min(lq, window + P.krows) * grp * half, w.mean_keys = std::min(lk, window + P.qrows) * half;
     P.parts = attn_grad_parts(w, a.d, bf16, P.qrows, P.krows, (double)a.nk * a.key_heads * 2 * a.d * 4);
     if (P.parts > 1) P.off_part = take((size_t)P.parts * a.nk * a.key_heads * 2 * a.d * 4);

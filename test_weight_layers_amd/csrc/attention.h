@@ -82,7 +82,13 @@ struct AttnCut {
   int64_t whole;                    // query tiles of all heads that are not cut
   int splits;                       // ranges of keys of the others
 };
-AttnCut attn_cut(int64_t workgroups, int64_t busy, bool even, int d, int rows, int64_t keys, bool bf16);
+struct AttnWork {
+  int64_t tiles, busy;              // query tiles of all heads, at most and at least
+  bool even;                        // they see about as many keys
+  int64_t keys;                     // that the longest sees
+  double mean_keys;
+};
+AttnCut attn_cut(const AttnWork &w, int d, int rows, bool bf16);
 struct AttnGradWork {
   int64_t key_items, query_items;               // key tiles of all key heads, query tiles of all heads
   int64_t queries, keys;                        // that the longest of them walk over

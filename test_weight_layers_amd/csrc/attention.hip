@@ -7,6 +7,8 @@
 // reads as much as by products); fp32, 8 heads of 64 1056 us and of 128 2028 (130 and 135 of 137 TFLOP/s of a large product).
 // What was tried and did not pay: three LDS stages, touching tiles ahead for L2, wave priorities (4% at d = 256 alone), eight
 // waves that take turns at products and exponentials (25% slower: a barrier makes both halves as long as the longer).
+#include <algorithm>
+
 #include "attn_tile.h"
 
 namespace ttt {
@@ -355,25 +357,44 @@ template <typename T, int D, int NC, int BK, int KG, int OCC> hipError_t go(cons
 int attn_query_rows(int d, bool bf16, bool small) { return small || (!bf16 && d == 256) ? 64 : 128; }
 
 // Ranges that the keys of a query tile are cut in, for all tiles or, where these are alike, for those behind the last full
-// round of workgroups on 256 CUs: the rounds that they take, each for a range's share of the time of a tile's keys at the
-// rate that full CUs reach, and what the join reads and writes (at 4.5 TB/s, with a launch of 4 us).  `busy`: workgroups that
-// have a tile.  10992 queries, 8 heads of 128, 9618 keys each: 688 workgroups in rounds of 512, all in two ranges 574 us,
-// the last 176 so 538.  Causal tiles even out by themselves (9600 tokens, 8 heads of 128 on 2: 262 us, cut so 287).
-AttnCut attn_cut(int64_t workgroups, int64_t busy, bool even, int d, int rows, int64_t keys, bool bf16) {
+// round of workgroups on 256 CUs: what takes least by the time of a tile on a CU alone (measured, as is how many such a CU
+// does at once), the rounds of equal workgroups, or of unequal ones the longest and what all keep the CUs busy with, and what
+// the ranges' sums cost (at 3 TB/s, with a launch of 4 us).  Of 35 shapes of both types and all d, 100 to 8192 rows, the times
+// are 2% over the best number of ranges' in the mean and 29% at most.  10992 queries, 8 heads of 128, 9618 keys each: 688
+// workgroups in rounds of 512, all in two ranges 574 us, the last 176 so 538; fp32, 2 heads of 256 on 1, 1974 tokens in 5
+// sequences: 209 us in one range, 97 in four.
+AttnCut attn_cut(const AttnWork &w, int d, int rows, bool bf16) {
   const bool small = rows == 64;
   const int per_cu = bf16 ? (d == 64 && !small ? 3 : d == 256 ? 1 : 2) : d == 64 ? 2 : 1;
-  const double rate = bf16 ? (d == 64 ? 850e6 : d == 128 ? 950e6 : 400e6) : (d == 64 ? 120e6 : d == 128 ? 105e6 : 55e6);   // flop per us
-  const int64_t slots = 256 * per_cu, full = even ? busy / slots * slots : 0;
-  const double one = 4.0 * rows * (double)keys * d * (double)slots / rate, bytes = (double)rows * d * 8;
-  AttnCut best{workgroups, 1};
-  double least = (double)((busy + slots - 1) / slots) * one;
-  for (const int64_t whole : {int64_t(0), full}) {
-    const int64_t rest = busy - whole;
-    for (int s = 2; rest > 0 && s <= 32 && keys / s >= 256; ++s) {
-      const double t = ((double)(whole / slots) + (double)((rest * s + slots - 1) / slots) / s) * one + 4.0 + s * rest * bytes / 4.5e6;
-      if (t < 0.95 * least) least = t, best = AttnCut{whole, s};
-    }
+  // us of a tile and 32 keys, and tiles at once
+  double alone, at_once;
+  if (bf16) {
+    alone = small ? (d == 64 ? 0.29 : d == 128 ? 0.45 : 0.84) : d == 64 ? 0.8 : d == 128 ? 0.9 : 1.76;
+    at_once = small ? (d == 64 ? 1.4 : d == 128 ? 1.6 : 1.0) : d == 64 ? 2.5 : d == 128 ? 1.6 : 1.0;
+  } else {
+    alone = small ? (d == 64 ? 1.16 : d == 128 ? 2.2 : 5.1) : d == 64 ? 2.4 : 4.4;
+    at_once = d == 64 ? 1.18 : d == 128 && !small ? 1.1 : 1.0;
   }
+  const int64_t slots = 256 * per_cu, full = w.even ? w.busy / slots * slots : 0;
+  const double longest = w.keys / 32.0 * alone, mean = w.mean_keys / 32.0 * alone, round = per_cu / at_once;
+  const auto time = [&](int64_t whole, int s) {
+    const int64_t n = (w.busy - whole) * s;
+    const double one = longest / s;
+    double t = (double)(whole / slots) * round * longest;
+    if (w.even)
+      t += (double)(n / slots) * round * one + (n % slots ? std::max(1.0, (double)((n % slots + 255) / 256) / at_once) * one : 0.0);
+    else
+      t += n <= 256 ? one : std::max(one * std::max(1.0, std::min<double>(per_cu, (double)((n + 255) / 256)) / at_once),
+                                     (double)w.busy * mean / (256 * at_once) + one / 2);
+    return s == 1 ? t : t + 4.0 + 0.1 * s + (double)n * rows * d * 8 / 3e6;
+  };
+  AttnCut best{w.tiles, 1};
+  double least = time(0, 1);
+  for (const int64_t whole : {int64_t(0), full})
+    for (int s = 2; whole < w.busy && s <= 64 && w.keys / s >= 32; ++s) {
+      const double t = time(whole, s);
+      if (t < 0.97 * least) least = t, best = AttnCut{whole, s};
+    }
   return best;
 }
 
