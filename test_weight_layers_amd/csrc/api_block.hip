@@ -168,7 +168,7 @@ int attention_params(const AttnShape &a, bool backward, const Rows &q, const Row
 
 int step_splits(int H, int Hk, int64_t n, int capacity) {
   const int64_t wgs = n * Hk * ceil_div(H / Hk, 16);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({1024 / std::max<int64_t>(wgs, 1), ceil_div(capacity, 128), 64}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({2048 / std::max<int64_t>(wgs, 1), ceil_div(capacity, 128), 64}));
 }
 struct StepPlan {
   int splits;

@@ -4,9 +4,10 @@
 // read the caches as they were before it.
 // Bound by reading the visible keys and values once.  The heads of a key head are the columns of the products of
 // attn_tile.h; keys go from memory to registers, 32 a wave, values through the wave's own part of LDS.  Ranges of 128 keys
-// or more until there are 1024 workgroups: 4096 keys of one token, 16 heads of 64, take 8 + 4 us (the launches; 3.5 us of
-// bytes), 64 tokens over caches of 4096 rows of which a third are visible, 16 heads of 128 on 4, 39 + 5 us (190 MB at
-// 4.9 TB/s, a copy's rate).  2048 keys of one token in one range would take 31 us against 9.
+// or more until there are 2048 workgroups: 4096 keys of one token, 16 heads of 64, take 8 + 4 us (the launches; 3.5 us of
+// bytes); 64 tokens over caches of 4096 rows, 16 heads of 128 on 4, 116 us (537 MB at 4.6 TB/s; a copy reaches 4.9), and 54
+// where a third is visible (185 MB; 55 with 1024 workgroups, 66 with 4096: short ranges are bound by their start). 2048 keys
+// of one token in one range would take 31 us against 9.
 #include "attn_tile.h"
 
 namespace ttt {
@@ -44,6 +45,12 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_step_ke
   const int lo = lo64 < 0 ? 0 : (int)lo64, se = p.sinks < lo ? p.sinks : lo;
   const int ns = tiles_of(se, 32), nt = ns + (int)(((int64_t)pos + 1 - lo + 31) / 32), lo_place = place_of(p, lo);
   const int first = (int)((int64_t)nt * split / p.splits), end = (int)((int64_t)nt * (split + 1) / p.splits);
+  const int heads = grp - hg * 16 < 16 ? grp - hg * 16 : 16;
+  const int64_t out = ((int64_t)split * p.n + row) * p.heads + kh * grp + hg * 16;
+  if (first >= end) {                                 // a range without keys (the row is short): no sums, which nobody takes
+    if ((int)threadIdx.x < heads) p.part_ml[out + threadIdx.x] = float2{-__builtin_inff(), 0.0f};
+    return;
+  }
   const T *kc = static_cast<const T *>(p.kc) + (int64_t)at.x * p.pool_stride + kh * D;
   const T *vc = static_cast<const T *>(p.vc) + (int64_t)at.x * p.pool_stride + kh * D;
   const T *kn = static_cast<const T *>(p.k) + (int64_t)row * p.ldk + kh * D;
@@ -170,8 +177,6 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_step_ke
 #pragma unroll
   for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4 *>(so + (wave * 16 + li) * D + 16 * d + 4 * g) = o[d] * a;
   __syncthreads();
-  const int heads = grp - hg * 16 < 16 ? grp - hg * 16 : 16;
-  const int64_t out = ((int64_t)split * p.n + row) * p.heads + kh * grp + hg * 16;
   for (int i = threadIdx.x; i < heads * D / 4; i += 256) {
     f32x4 v = zero_f4();
 #pragma unroll
@@ -208,7 +213,8 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_step_jo
   f32x4 o = zero_f4();
   for (int i = g; i < p.splits; i += G) {
     const float2 ml = p.part_ml[first + i * step];
-    const f32x4 x = *reinterpret_cast<const f32x4 *>(p.part_o + (first + i * step) * D + 4 * c);
+    const f32x4 sums = *reinterpret_cast<const f32x4 *>(p.part_o + (first + i * step) * D + 4 * c);
+    const f32x4 x = ml.x == -__builtin_inff() && ml.y == 0.0f ? zero_f4() : sums;
     const float top = fmaxf(m, ml.x);
     const float a = m == top ? 1.0f : __builtin_amdgcn_exp2f((m - top) * c2), b = ml.x == top ? 1.0f : __builtin_amdgcn_exp2f((ml.x - top) * c2);
     m = top, sum = sum * a + ml.y * b, o = o * a + x * b;
