@@ -3,11 +3,10 @@
 // and its own token; the second kernel joins the ranges of keys and then writes the tokens, so that the rows of a call
 // read the caches as they were before it.
 // Bound by reading the visible keys and values once.  The heads of a key head are the columns of the products of
-// attn_tile.h; keys go from memory to registers, 32 a wave, values through the wave's own part of LDS.  Ranges of 128 keys
-// or more until there are 2048 workgroups: 4096 keys of one token, 16 heads of 64, take 8 + 4 us (the launches; 3.5 us of
-// bytes); 64 tokens over caches of 4096 rows, 16 heads of 128 on 4, 116 us (537 MB at 4.6 TB/s; a copy reaches 4.9), and 54
-// where a third is visible (185 MB; 55 with 1024 workgroups, 66 with 4096: short ranges are bound by their start). 2048 keys
-// of one token in one range would take 31 us against 9.
+// attn_tile.h; keys go from memory to registers, 32 a wave, values through the wave's own part of LDS.
+// The keys go in ranges of 512 (api_block.hip): 4096 keys of one token, 16 heads of 64, take 8 + 4 us (the launches; 3.5 us
+// of bytes); 64 tokens over caches of 4096 rows, 16 heads of 128 on 4, 116 us (537 MB at 4.6 TB/s; a copy reaches 4.9), and
+// 54 where a third is visible (185 MB; 66 in ranges of 256, which are bound by their start).
 #include "attn_tile.h"
 
 namespace ttt {
