@@ -912,6 +912,13 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _norm_backward_bytes(*sizes: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().ttt_layer_norm_backward_workspace_bytes(*sizes, ctypes.byref(out)))
+    return out.value
+
+
 def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
                         *, norm_width: Optional[int] = None, out: Optional[torch.Tensor] = None,
                         workspace: Optional[torch.Tensor] = None):
@@ -928,16 +935,12 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, gamma: Optional[t
         out = x.new_empty((n, C)) if ldo == C else x.new_empty((n, ldo))[:, :C]
     else:
         ldo = _row(out, dtype, dev, n, C, "out")
-    L = load()
     if workspace is None:
-        size = ctypes.c_size_t()
-        _check(L.ttt_layer_norm_backward_workspace_bytes(C, w, n, ctypes.byref(size)))
-        workspace = _workspace(size.value, x.device)
-    ggamma = torch.empty(w, dtype=torch.float32, device=x.device)
-    gbeta = torch.empty(w, dtype=torch.float32, device=x.device)
-    _check(L.ttt_layer_norm_backward(C, w, grad_y.data_ptr(), ldg, x.data_ptr(), ldx, gamma, float(eps), out.data_ptr(),
-                                     ldo, ggamma.data_ptr(), gbeta.data_ptr(), n, code, workspace.data_ptr(),
-                                     _bytes(workspace, dev), _stream()))
+        workspace = x.new_empty((_norm_backward_bytes(C, w, n),), dtype=torch.uint8)
+    ggamma, gbeta = x.new_empty((w,), dtype=torch.float32), x.new_empty((w,), dtype=torch.float32)
+    _check(load().ttt_layer_norm_backward(C, w, grad_y.data_ptr(), ldg, x.data_ptr(), ldx, gamma, float(eps),
+                                          out.data_ptr(), ldo, ggamma.data_ptr(), gbeta.data_ptr(), n, code,
+                                          workspace.data_ptr(), _bytes(workspace, dev), _stream()))
     return out, ggamma, gbeta
 
 
