@@ -41,7 +41,8 @@
  *   Every call is asynchronous on that stream; the caller synchronises.
  * Workspace.  The library allocates no device memory.  Entry points that need
  *   scratch take a caller-owned DEVICE buffer of at least the size reported
- *   by the matching *_workspace_bytes query (256-byte aligned).
+ *   by the matching *_workspace_bytes query (256-byte aligned).  It serves one
+ *   call at a time: calls and captured graphs that may run at once take one each.
  * Errors.  Every function returns a ttt_status.  Nothing is launched when the
  *   return is TTT_EINVAL / TTT_EUNSUPPORTED / TTT_EWORKSPACE.  TTT_EHIP means a
  *   HIP launch failed; ttt_last_error() then holds hipGetErrorString's text.
