@@ -25,8 +25,8 @@ struct AttnShape {
 
 struct AttnPlan {
   int64_t whole;
-  int qrows, krows, qtiles, ktiles, splits, parts, sink_parts, sink_tiles;
-  size_t off_seqs, off_o, off_ml, off_delta, off_part, off_spart, total;
+  int qrows, krows, qtiles, ktiles, splits, parts, qparts, sink_parts, sink_tiles;
+  size_t off_seqs, off_o, off_ml, off_delta, off_part, off_qpart, off_spart, total;
 };
 
 int check_attention_heads(int H, int Hk, int d, int dtype) {
@@ -55,7 +55,7 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
   const bool bounded = a.before >= 0 && a.after >= 0, limited = a.before >= 0 || a.after >= 0;
   const int64_t span = bounded ? std::min(((int64_t)a.before + a.after + 1) * a.block, int64_t(1) << 40) : 0, window = bounded ? std::min(span, lk) : lk;
   AttnPlan P{};
-  P.splits = P.parts = 1;
+  P.splits = P.parts = P.qparts = 1;
   size_t o = 0;
   const auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -93,7 +93,9 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     w.queries = std::min(longest, (bounded ? span : longest) + P.krows) * grp, w.keys = std::min(longest, (bounded ? span : longest) + P.qrows);
     const double half = bounded || !limited ? 1.0 : 0.6;
     w.mean_queries = std::min(lq, window + P.krows) * grp * half, w.mean_keys = std::min(lk, window + P.qrows) * half;
-    P.parts = attn_grad_parts(w, a.d, bf16, P.qrows, P.krows, (double)a.nk * a.key_heads * 2 * a.d * 4);
+    const AttnGradCut cut = attn_grad_cut(w, a.d, bf16, P.qrows, P.krows);
+    P.parts = cut.parts, P.qparts = cut.qparts;
+    if (P.qparts > 1) P.off_qpart = take((size_t)tiles(a.nq, P.qrows) * a.heads * P.qparts * P.qrows * a.d * 4);
     if (P.parts > 1) P.off_part = take((size_t)P.parts * a.nk * a.key_heads * 2 * a.d * 4);
     // Sinks, which all queries behind their window see: ranges of these of their own, where a sequence may be long beside
     // the window (lengths are on the device: taken as four times the mean), joined with the window's part by the sums' kernel.
@@ -109,7 +111,7 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     }
   }
   const int64_t qt = tiles(a.nq, P.qrows), kt = tiles(a.nk, P.krows);
-  if (qt * a.heads * P.splits + (backward ? kt * a.key_heads * P.parts + (int64_t)a.nseq * P.sink_tiles * a.key_heads * P.sink_parts : 0) > kMaxGroups ||
+  if (qt * a.heads * P.splits * P.qparts + (backward ? kt * a.key_heads * P.parts + (int64_t)a.nseq * P.sink_tiles * a.key_heads * P.sink_parts : 0) > kMaxGroups ||
       a.nq * a.heads / (1024 / a.d) > kMaxGroups)
     return fail(TTT_EUNSUPPORTED, "too many rows or sequences for %d heads in one call", a.heads);
   P.qtiles = (int)qt, P.ktiles = (int)kt;
@@ -154,13 +156,14 @@ int attention_params(const AttnShape &a, bool backward, const Rows &q, const Row
   p.block = fast_div(block), p.group = fast_div(a.heads / a.key_heads);
   p.back = a.before < 0 ? (int)most : span(a.before), p.ahead = a.after < 0 ? (int)most : span((int64_t)a.after + 1);
   p.back_q = a.after < 0 ? (int)most : span(a.after), p.ahead_q = a.before < 0 ? (int)most : span((int64_t)a.before + 1);
-  p.per_qtiles = fast_div(P.qtiles), p.per_ktiles = fast_div(P.ktiles), p.per_splits = fast_div(P.splits), p.per_parts = fast_div(P.parts);
+  p.per_qtiles = fast_div(P.qtiles), p.per_ktiles = fast_div(P.ktiles), p.per_splits = fast_div(P.splits), p.per_parts = fast_div(P.parts), p.per_qparts = fast_div(P.qparts);
   p.per_sink_parts = fast_div(P.sink_parts), p.per_sink_tiles = fast_div(P.sink_tiles), p.per_key_heads = fast_div(a.key_heads);
   p.seqs = reinterpret_cast<AttnSeq *>(b + P.off_seqs);
   p.qrows = P.qrows, p.krows = P.krows, p.qtiles = P.qtiles, p.ktiles = P.ktiles;
   p.whole = (int)P.whole, p.splits = P.splits, p.part_o = reinterpret_cast<float *>(b + P.off_o), p.part_ml = reinterpret_cast<float2 *>(b + P.off_ml);
   p.delta = reinterpret_cast<float *>(b + P.off_delta);
   p.parts = P.parts, p.part = reinterpret_cast<float *>(b + P.off_part);
+  p.qparts = P.qparts, p.qpart = reinterpret_cast<float *>(b + P.off_qpart);
   p.sink_parts = P.sink_parts, p.sink_tiles = P.sink_tiles, p.spart = reinterpret_cast<float *>(b + P.off_spart);
   *out = p;
   return TTT_OK;

@@ -43,7 +43,7 @@ struct AttnParams {
   AttnSeq *seqs;                    // [nseq + 1], more than kAttnLaneSeqs sequences
   int qrows, krows;                 // rows of a query tile and of a key tile
   int qtiles, ktiles;               // at most so many
-  FastDiv per_qtiles, per_ktiles, per_splits, per_parts, per_sink_parts, per_sink_tiles, per_key_heads;
+  FastDiv per_qtiles, per_ktiles, per_splits, per_parts, per_qparts, per_sink_parts, per_sink_tiles, per_key_heads;
   // forward: the query tiles of all heads from the `whole`th on have their keys in `splits` ranges, joined from these
   int whole, splits;
   float *part_o;                    // [tiles in ranges][splits][qrows][d]
@@ -54,6 +54,8 @@ struct AttnParams {
   void *gq, *gk, *gv;
   int64_t ldgq, ldgk, ldgv;
   float *delta;                     // [heads][nq]
+  int qparts;                       // ranges of a query tile's keys
+  float *qpart;                     // [query tiles of all heads][qparts][qrows][d]
   int parts, sink_parts, sink_tiles;// ranges of a key tile's queries; of a sink tile's beyond the window; tiles of sinks
   float *part;                      // [parts][nk][key_heads][2][d], parts > 1
   float *spart;                     // [nseq][sink_tiles][key_heads][1 + sink_parts][krows][2][d]
@@ -94,7 +96,10 @@ struct AttnGradWork {
   int64_t queries, keys;                        // that the longest of them walk over
   double mean_queries, mean_keys;
 };
-int attn_grad_parts(const AttnGradWork &w, int d, bool bf16, int qrows, int krows, double bytes);
+struct AttnGradCut {
+  int parts, qparts;                            // ranges of queries of a key tile, of keys of a query tile
+};
+AttnGradCut attn_grad_cut(const AttnGradWork &w, int d, bool bf16, int qrows, int krows);
 int attn_grad_query_rows(int d, bool bf16, bool small);
 int attn_grad_key_rows(int d, bool bf16, bool small);
 hipError_t launch_attention(const AttnParams &p, bool bf16, hipStream_t s);

@@ -273,12 +273,12 @@ __global__ __launch_bounds__(256, OCC) void attn_grads_kernel(AttnParams p, int 
         store4(out + 16 * d + 4 * g, dk[d][c] * p.scale), store4(out + D + 16 * d + 4 * g, dv[d][c]);
     }
   } else {
-    const int block = blockIdx.x - keys, blocks = p.qtiles * p.heads;
     constexpr int QR = 64 * NCQ;
-    const int item = attn_item(block, blocks), h = quotient(item, p.per_qtiles), kh = quotient(h, p.group);
+    const int item = attn_item(blockIdx.x - keys, p.qtiles * p.heads * p.qparts), rest = p.qparts > 1 ? quotient(item, p.per_qparts) : item, part = item - rest * p.qparts;
+    const int h = quotient(rest, p.per_qtiles), kh = quotient(h, p.group);
     AttnSeq s;
     int tile, seq;
-    if (!tile_of<false>(p, p.qtiles - 1 - (item - h * p.qtiles), &s, &tile, &seq)) return;
+    if (!tile_of<false>(p, p.qtiles - 1 - (rest - h * p.qtiles), &s, &tile, &seq)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g = l >> 4, li = l & 15;
     const int t0 = tile * QR, row0 = t0 + wave * 16 * NCQ;
     const T *kb = static_cast<const T *>(p.k) + (int64_t)s.ks * p.ldk + kh * D;
@@ -302,9 +302,11 @@ __global__ __launch_bounds__(256, OCC) void attn_grads_kernel(AttnParams p, int 
     const int k0 = seen_keys(p, s, t0).x, k1 = seen_keys(p, s, last - 1).y, se = p.sinks < k0 ? p.sinks : k0;
     const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
     const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
+    const int share = p.qparts > 1 ? quotient(nt + p.qparts - 1, p.per_qparts) : nt, first = part * share;
+    const int count = first + share < nt ? share : nt - first;                // of its tiles (below 1: none)
     const typename Tile::Lane lane = Tile::lane();
     const typename Tile::template Copy<BK> copy_k(p.ldk), copy_v(p.ldv);
-    const KeyWalk<T, BK> start(0, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
+    const KeyWalk<T, BK> start(first, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
     const auto fetch = [&](const KeyWalk<T, BK> &w, int stage) {
       copy_k.fetch(w.k, w.end() - w.j, s_a[stage]);
       copy_v.fetch(w.v, w.end() - w.j, s_b[stage]);
@@ -318,12 +320,12 @@ __global__ __launch_bounds__(256, OCC) void attn_grads_kernel(AttnParams p, int 
         for (int d = 0; d < ND; ++d) dq[d][c] = zero_f4();
       __syncthreads();
       KeyWalk<T, BK> ahead = start;
-      if (nt > 0) fetch(ahead, 0);
-      for (int t = 0; t < nt; ++t) {
+      if (count > 0) fetch(ahead, 0);
+      for (int t = 0; t < count; ++t) {
         const int2 r{ahead.j, ahead.end()};
         ahead.next();
         landed();
-        if (t + 1 < nt) fetch(ahead, (t + 1) & 1);
+        if (t + 1 < count) fetch(ahead, (t + 1) & 1);
         const bool full = r.y - r.x == BK && wa.y >= r.y && (wb.x <= r.x || r.y <= p.sinks);
         const bool none = !(r.x < wb.y && (r.y > wa.x || r.x < p.sinks));
         unsigned char *kt = s_a[t & 1];
@@ -401,6 +403,12 @@ __global__ __launch_bounds__(256, OCC) void attn_grads_kernel(AttnParams p, int 
     for (int c = 0; c < NCQ; ++c) {
       const int i = row0 + 16 * c + li;
       if (i >= s.ql) continue;
+      if (p.qparts > 1) {
+        float *out = p.qpart + ((int64_t)item * QR + (i - t0)) * D + 4 * g;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) store4(out + 16 * d, dq[d][c] * p.scale);
+        continue;
+      }
       T *out = static_cast<T *>(p.gq) + (int64_t)(s.qs + i) * p.ldgq + h * D + 4 * g;
 #pragma unroll
       for (int d = 0; d < ND; ++d) store4(out + 16 * d, dq[d][c] * p.scale);
@@ -408,20 +416,37 @@ __global__ __launch_bounds__(256, OCC) void attn_grads_kernel(AttnParams p, int 
   }
 }
 
-// The sums over ranges of queries, in their order: a key tile (of sinks only, where the window is one range) and key head by
-// blockIdx.x, 512 / D of its rows by blockIdx.y, D / 2 lanes a row.
-template <typename T, int D> __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(AttnParams p) {
+// The sums over ranges, in their order.  The first `keys` workgroups those of queries: a key tile (of sinks only, where the window
+// is one range) and key head, 512 / D of its rows, D / 2 lanes a row; behind them those of keys: a query tile, 1024 / D of its
+// rows, D / 4 lanes a row.
+template <typename T, int D> __global__ __launch_bounds__(256) void attn_sum_kernel(AttnParams p, int keys) {
+  if ((int)blockIdx.x >= keys) {
+    constexpr int L = D / 4;
+    const int b = blockIdx.x - keys, per = p.qrows * D / 1024, item = b >> __builtin_ctz(per), y = b & (per - 1), h = quotient(item, p.per_qtiles);
+    AttnSeq s;
+    int tile, seq;
+    if (!tile_of<false>(p, p.qtiles - 1 - (item - h * p.qtiles), &s, &tile, &seq)) return;
+    const int c = threadIdx.x % L * 4, r = y * (256 / L) + threadIdx.x / L;
+    if (tile * p.qrows + r >= s.ql) return;
+    const float *a = p.qpart + ((int64_t)item * p.qparts * p.qrows + r) * D + c;
+    f32x4 v = zero_f4();
+#pragma unroll 4
+    for (int i = 0; i < p.qparts; ++i) v += *reinterpret_cast<const f32x4 *>(a + (int64_t)i * p.qrows * D);
+    store4(static_cast<T *>(p.gq) + (int64_t)(s.qs + tile * p.qrows + r) * p.ldgq + h * D + c, v);
+    return;
+  }
   constexpr int L = D / 2;
+  const int per = p.krows * D / 512, bx = blockIdx.x >> __builtin_ctz(per), by = blockIdx.x & (per - 1);      // (a power of two)
   AttnSeq s;
   int tile, seq;
-  const int x = quotient(blockIdx.x, p.per_key_heads), kh = blockIdx.x - x * p.key_heads;
+  const int x = quotient(bx, p.per_key_heads), kh = bx - x * p.key_heads;
   if (p.parts > 1) {
     if (!tile_of<true>(p, x, &s, &tile, &seq)) return;
   } else {
     seq = quotient(x, p.per_sink_tiles), tile = x - seq * p.sink_tiles;
     s = seq_of(p, seq);
   }
-  const int c = threadIdx.x % L * 4, r = blockIdx.y * (256 / L) + threadIdx.x / L;
+  const int c = threadIdx.x % L * 4, r = by * (256 / L) + threadIdx.x / L;
   if (tile * p.krows + r >= s.kl) return;
   const int64_t row = s.ks + tile * p.krows + r;
   f32x4 v = zero_f4();
@@ -449,37 +474,44 @@ template <typename T, int D, int NCQ, int BK, int NCK, int BQ, int OCC> hipError
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int sinks = p.nseq * p.sink_tiles * p.key_heads, queries = p.qtiles * p.heads, keys = p.ktiles * p.key_heads * p.parts + sinks * p.sink_parts;
+  const int sinks = p.nseq * p.sink_tiles * p.key_heads, tiles = p.qtiles * p.heads;
+  const int keys = p.ktiles * p.key_heads * p.parts + sinks * p.sink_parts, queries = tiles * p.qparts;
   if (queries + keys > 0) hipLaunchKernelGGL((attn_grads_kernel<T, D, NCQ, BK, NCK, BQ, OCC>), dim3(queries + keys), dim3(256), 0, s, p, keys);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || keys == 0 || (p.parts == 1 && p.sink_parts == 0)) return e;
-  hipLaunchKernelGGL((attn_dkv_sum_kernel<T, D>), dim3(p.parts > 1 ? p.ktiles * p.key_heads : sinks, p.krows * D / 512), dim3(256), 0,
-                     s, p);
+  const int key_sums = (p.parts > 1 ? p.ktiles * p.key_heads : p.sink_parts > 0 ? sinks : 0) * (p.krows * D / 512);
+  const int sums = key_sums + (p.qparts > 1 ? tiles * (p.qrows * D / 1024) : 0);
+  if (e != hipSuccess || sums == 0) return e;
+  hipLaunchKernelGGL((attn_sum_kernel<T, D>), dim3(sums), dim3(256), 0, s, p, key_sums);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Ranges that the queries of a key tile (all heads of its key head) are cut in, each a workgroup of its own whose sums are
-// written and added (`bytes` a range, both at 2.5 TB/s together, 4 us the launch): as many as bring the longest workgroup
-// down to what the others keep the 256 CUs busy with.  Times of 32 rows of the other axis for a tile of 64 of its own on a CU
+// Ranges that the queries of a key tile (all heads of its key head) and the keys of a query tile are cut in, each a workgroup
+// of its own whose sums are written and added (2.5 TB/s together, 6 us the launch): as many as bring the longest workgroup
+// down to what all keep the 256 CUs busy with.  Times of 32 rows of the other axis for a tile of 64 of its own on a CU
 // alone, and how many such a CU does at once, are measured; a larger tile takes less than in proportion and dq three
-// quarters of dk and dv.  Of 28 shapes of both types and all d, 100 to 8192 rows, the times are 2% over the best number of
-// ranges' in the mean and 9% at most (1024 x 1024, 4 heads of 256, bf16: 87 us in one range, 71 in two, 93 in six; fp32, 2 heads of
-// 256 on 1, 1974 tokens in 5 sequences: 755, 390 and 302).
-int attn_grad_parts(const AttnGradWork &w, int d, bool bf16, int qrows, int krows, double bytes) {
+// quarters of dk and dv.  fp32, 2 heads of 256 on 1, 1974 tokens in 5 sequences: 755 us uncut, 298 with the queries cut, 221
+// with both; bf16, 2 heads of 128 on 1, 2048 tokens, causal: 89 with the queries cut, 42 with both.  Where all take longer
+// than the longest they even out by themselves (8192 tokens, 8 heads of 64: 527 us, 559 cut).
+AttnGradCut attn_grad_cut(const AttnGradWork &w, int d, bool bf16, int qrows, int krows) {
   const double key = (bf16 ? (d == 64 ? 0.7 : d == 128 ? 1.1 : 2.1) : d == 64 ? 3.0 : d == 128 ? 4.7 : 9.3) * std::pow(krows / 64.0, 0.8) / 32;
   const double query = 0.75 * key * std::pow((double)qrows / krows, 0.8);
   const double at_once = bf16 ? (d == 64 ? 3.0 : d == 128 ? 2.0 : 1.2) : d == 64 ? 1.5 : d == 128 ? 1.3 : 1.15;
   const double mean = (w.key_items * w.mean_queries * key + w.query_items * w.mean_keys * query) / (256 * at_once);
-  int best = 1;
+  const double key_sum = w.key_items * (double)krows * 2 * d * 4 / 2.5e6, query_sum = w.query_items * (double)qrows * d * 4 / 2.5e6;
+  static constexpr int kRanges[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
+  AttnGradCut best{1, 1};
+  if (std::max((double)w.queries * key, (double)w.keys * query) <= mean) return best;
   double least = 0.0;
-  for (int parts = 1; parts <= 32; ++parts) {
-    const double longest = std::max((double)w.queries / parts * key, w.keys * query);
-    const double t = (w.key_items * parts + w.query_items > 256 ? std::max(longest, mean + longest / 2) : longest) +
-                     (parts > 1 ? 4.0 + parts * bytes / 2.5e6 : 0.0);
-    if (parts == 1 || t < 0.97 * least) least = t, best = parts;
-  }
+  for (const int q : kRanges)
+    for (const int k : kRanges) {
+      if (q > 1 && w.keys / q < 32) break;
+      const double longest = std::max((double)w.queries / k * key, (double)w.keys / q * query);
+      const double t = (w.key_items * k + w.query_items * q > 256 ? std::max(longest, mean + longest / 2) : longest) +
+                       (k > 1 || q > 1 ? 6.0 : 0.0) + (k > 1 ? k * key_sum : 0.0) + (q > 1 ? q * query_sum : 0.0);
+      if (k * q == 1 || t < 0.97 * least) least = t, best = AttnGradCut{k, q};
+    }
   return best;
 }
 
