@@ -53,7 +53,8 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
   const int64_t lk = ceil_div(a.nk, a.nseq), lq = ceil_div(a.nq, a.nseq);
   // limited on one side only, a window's rows see unlike numbers of keys, about half of all in the mean
   const bool bounded = a.before >= 0 && a.after >= 0, limited = a.before >= 0 || a.after >= 0;
-  const int64_t span = bounded ? std::min(((int64_t)a.before + a.after + 1) * a.block, int64_t(1) << 40) : 0, window = bounded ? std::min(span, lk) : lk;
+  const int64_t span = bounded ? std::min(((int64_t)a.before + a.after + 1) * a.block, int64_t(1) << 40) : 0;
+  const int64_t window = bounded ? std::min(span, lk) : lk;
   AttnPlan P{};
   P.splits = P.parts = P.qparts = 1;
   size_t o = 0;
@@ -106,12 +107,14 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     if (bytes > 0 && bytes <= (double)most && a.before >= 0 && a.nq > 2 * (window + P.krows)) {
       const int64_t one = (int64_t)bytes;
       P.sink_tiles = (int)sink_tiles;
-      P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>({32, std::min(a.nq, 4 * lq) * grp / std::max<int64_t>(window * grp / 2, 512), most / one}));
+      const int64_t behind = std::min(a.nq, 4 * lq) * grp / std::max<int64_t>(window * grp / 2, 512);
+      P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>({32, behind, most / one}));
       P.off_spart = take((size_t)one * (1 + P.sink_parts));
     }
   }
   const int64_t qt = tiles(a.nq, P.qrows), kt = tiles(a.nk, P.krows);
-  if (qt * a.heads * P.splits * P.qparts + (backward ? kt * a.key_heads * P.parts + (int64_t)a.nseq * P.sink_tiles * a.key_heads * P.sink_parts : 0) > kMaxGroups ||
+  const int64_t key_items = kt * a.key_heads * P.parts + (int64_t)a.nseq * P.sink_tiles * a.key_heads * P.sink_parts;
+  if (qt * a.heads * P.splits * P.qparts + (backward ? key_items : 0) > kMaxGroups ||
       a.nq * a.heads / (1024 / a.d) > kMaxGroups)
     return fail(TTT_EUNSUPPORTED, "too many rows or sequences for %d heads in one call", a.heads);
   P.qtiles = (int)qt, P.ktiles = (int)kt;
@@ -156,11 +159,13 @@ int attention_params(const AttnShape &a, bool backward, const Rows &q, const Row
   p.block = fast_div(block), p.group = fast_div(a.heads / a.key_heads);
   p.back = a.before < 0 ? (int)most : span(a.before), p.ahead = a.after < 0 ? (int)most : span((int64_t)a.after + 1);
   p.back_q = a.after < 0 ? (int)most : span(a.after), p.ahead_q = a.before < 0 ? (int)most : span((int64_t)a.before + 1);
-  p.per_qtiles = fast_div(P.qtiles), p.per_ktiles = fast_div(P.ktiles), p.per_splits = fast_div(P.splits), p.per_parts = fast_div(P.parts), p.per_qparts = fast_div(P.qparts);
+  p.per_qtiles = fast_div(P.qtiles), p.per_ktiles = fast_div(P.ktiles), p.per_splits = fast_div(P.splits);
+  p.per_parts = fast_div(P.parts), p.per_qparts = fast_div(P.qparts);
   p.per_sink_parts = fast_div(P.sink_parts), p.per_sink_tiles = fast_div(P.sink_tiles), p.per_key_heads = fast_div(a.key_heads);
   p.seqs = reinterpret_cast<AttnSeq *>(b + P.off_seqs);
   p.qrows = P.qrows, p.krows = P.krows, p.qtiles = P.qtiles, p.ktiles = P.ktiles;
-  p.whole = (int)P.whole, p.splits = P.splits, p.part_o = reinterpret_cast<float *>(b + P.off_o), p.part_ml = reinterpret_cast<float2 *>(b + P.off_ml);
+  p.whole = (int)P.whole, p.splits = P.splits;
+  p.part_o = reinterpret_cast<float *>(b + P.off_o), p.part_ml = reinterpret_cast<float2 *>(b + P.off_ml);
   p.delta = reinterpret_cast<float *>(b + P.off_delta);
   p.parts = P.parts, p.part = reinterpret_cast<float *>(b + P.off_part);
   p.qparts = P.qparts, p.qpart = reinterpret_cast<float *>(b + P.off_qpart);
@@ -226,7 +231,8 @@ int ttt_window_attention(int32_t heads, int32_t key_heads, int32_t d, const void
   if ((st = check_row(ro, nq))) return st;
   if (rows_overlap(ro, rq, nq)) return fail(TTT_EINVAL, "o must not overlap q");
   for (const Rows *r : {&rk, &rv})
-    if (nq > 0 && nk > 0 && rows_overlap_span(*r, nk, o, (size_t)(((nq - 1) * ld_o + qw) * (int64_t)es)) && rows_overlap(ro, *r, std::max(nq, nk)))
+    if (nq > 0 && nk > 0 && rows_overlap_span(*r, nk, o, (size_t)(((nq - 1) * ld_o + qw) * (int64_t)es)) &&
+        rows_overlap(ro, *r, std::max(nq, nk)))
       return fail(TTT_EINVAL, "o must not overlap %s", r->name);
   p.o = o, p.ldo = ld_o, p.lse = lse, p.zero_unused = (flags & TTT_ATTENTION_ZERO_UNUSED) != 0;
   hipStream_t s = static_cast<hipStream_t>(stream);

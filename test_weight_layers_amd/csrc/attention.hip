@@ -74,7 +74,8 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
   const int k0 = seen_keys(p, s, t0).x, k1 = seen_keys(p, s, last - 1).y, se = p.sinks < k0 ? p.sinks : k0;
   const int2 wa = row0 < s.ql ? seen_keys(p, s, row0) : int2{0, 0}, wb = row0 < s.ql ? seen_keys(p, s, wlast - 1) : int2{0, 0};
   const int ns = tiles_of(se, BK), nt = ns + tiles_of(k1 - k0, BK);
-  const int share = in_parts ? quotient(nt + p.splits - 1, p.per_splits) : nt, first = split * share, end = first + share < nt ? first + share : nt;
+  const int share = in_parts ? quotient(nt + p.splits - 1, p.per_splits) : nt, first = split * share;
+  const int end = first + share < nt ? first + share : nt;
   const typename Tile::Lane lane = Tile::lane();
   const typename Tile::template Copy<BK> copy_k(p.ldk), copy_v(p.ldv);
   const KeyWalk<T, BK> start(first + kg, ns, se, k0, k1, kb, vb, p.ldk, p.ldv);
@@ -249,7 +250,8 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
     for (int c = 0; c < NC; ++c) {
       const float *from = so + 16 * c * kPitch;
       const float m2 = from[D], top = fmaxf(m[c], m2);
-      const float a = m[c] == top ? 1.0f : __builtin_amdgcn_exp2f((m[c] - top) * c2), b = m2 == top ? 1.0f : __builtin_amdgcn_exp2f((m2 - top) * c2);
+      const float a = m[c] == top ? 1.0f : __builtin_amdgcn_exp2f((m[c] - top) * c2);
+      const float b = m2 == top ? 1.0f : __builtin_amdgcn_exp2f((m2 - top) * c2);
       m[c] = top, sum[c] = sum[c] * a + from[D + 1] * b;
 #pragma unroll
       for (int d = 0; d < ND; ++d) o[d][c] = o[d][c] * a + *reinterpret_cast<const f32x4 *>(from + 16 * d + 4 * g) * b;

@@ -274,7 +274,8 @@ __global__ __launch_bounds__(256, OCC) void attn_grads_kernel(AttnParams p, int 
     }
   } else {
     constexpr int QR = 64 * NCQ;
-    const int item = attn_item(blockIdx.x - keys, p.qtiles * p.heads * p.qparts), rest = p.qparts > 1 ? quotient(item, p.per_qparts) : item, part = item - rest * p.qparts;
+    const int item = attn_item(blockIdx.x - keys, p.qtiles * p.heads * p.qparts);
+    const int rest = p.qparts > 1 ? quotient(item, p.per_qparts) : item, part = item - rest * p.qparts;
     const int h = quotient(rest, p.per_qtiles), kh = quotient(h, p.group);
     AttnSeq s;
     int tile, seq;
@@ -422,7 +423,8 @@ __global__ __launch_bounds__(256, OCC) void attn_grads_kernel(AttnParams p, int 
 template <typename T, int D> __global__ __launch_bounds__(256) void attn_sum_kernel(AttnParams p, int keys) {
   if ((int)blockIdx.x >= keys) {
     constexpr int L = D / 4;
-    const int b = blockIdx.x - keys, per = p.qrows * D / 1024, item = b >> __builtin_ctz(per), y = b & (per - 1), h = quotient(item, p.per_qtiles);
+    const int b = blockIdx.x - keys, per = p.qrows * D / 1024, item = b >> __builtin_ctz(per), y = b & (per - 1);
+    const int h = quotient(item, p.per_qtiles);
     AttnSeq s;
     int tile, seq;
     if (!tile_of<false>(p, p.qtiles - 1 - (item - h * p.qtiles), &s, &tile, &seq)) return;
@@ -459,7 +461,8 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_sum_ker
     const float *b = p.spart + (((((int64_t)seq * p.sink_tiles + tile) * p.key_heads + kh) * (1 + p.sink_parts)) * p.krows + r) * 2 * D + c;
     const int64_t next = (int64_t)p.krows * 2 * D;
 #pragma unroll 4
-    for (int i = p.parts > 1 ? 1 : 0; i <= (tile * p.krows + r < p.sinks ? p.sink_parts : 0); ++i) v += *reinterpret_cast<const f32x4 *>(b + i * next);
+    for (int i = p.parts > 1 ? 1 : 0; i <= (tile * p.krows + r < p.sinks ? p.sink_parts : 0); ++i)
+      v += *reinterpret_cast<const f32x4 *>(b + i * next);
   }
   if (c < D)
     store4(static_cast<T *>(p.gk) + row * p.ldgk + kh * D + c, v);

@@ -184,7 +184,8 @@ __device__ __forceinline__ AttnSeq read_seq(const AttnSeq &s, int b) {
 }
 __device__ __forceinline__ AttnSeq only_seq(const AttnParams &p) {
   if (p.cu_q == nullptr) return AttnSeq{0, p.nq, 0, p.nk, 0, 0};
-  const int qs = attn_offset(p.cu_q, 0, p.nq), qe = attn_offset(p.cu_q, 1, p.nq), ks = attn_offset(p.cu_k, 0, p.nk), ke = attn_offset(p.cu_k, 1, p.nk);
+  const int qs = attn_offset(p.cu_q, 0, p.nq), qe = attn_offset(p.cu_q, 1, p.nq);
+  const int ks = attn_offset(p.cu_k, 0, p.nk), ke = attn_offset(p.cu_k, 1, p.nk);
   return AttnSeq{qs, qe > qs ? qe - qs : 0, ks, ke > ks ? ke - ks : 0, 0, 0};
 }
 __device__ __forceinline__ AttnSeq seq_of(const AttnParams &p, int b) {
