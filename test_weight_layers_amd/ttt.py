@@ -718,12 +718,28 @@ def orthogonalise(g: torch.Tensor, steps: int = 5, out: Optional[torch.Tensor] =
 
 
 # ------------------------------------------------------------------ windowed attention
+# (ctypes takes the low 32 bits of a larger number, without a word)
+_MAX32 = (1 << 31) - 1
+
+
+def _int32(x: int, name: str) -> int:
+    if not -_MAX32 <= x <= _MAX32:
+        raise ValueError(f"{name} must be less than 2^31, got {x}")
+    return int(x)
+
+
 def _limit(x: Optional[int], name: str) -> int:
     if x is None:
         return -1
     if x < 0:
         raise ValueError(f"{name} must be >= 0, or None for no limit")
-    return int(x)
+    return int(x) if x <= _MAX32 else -1                # (no position is as far as 2^31 blocks)
+
+
+def _sinks(x: int) -> int:
+    if x < 0:
+        raise ValueError("sinks must be >= 0")
+    return int(x) if x <= _MAX32 else _MAX32            # (all keys)
 
 
 def _heads(q: torch.Tensor, heads: int, key_heads: Optional[int]) -> Tuple[int, int, int]:
@@ -750,7 +766,7 @@ def _attention_args(q, k, v, heads, key_heads, block, before, after, sinks, scal
     if cu_k is not None and (cu is None or cu_k.shape != cu.shape or cu_k.dtype != torch.int32
                              or not cu_k.is_contiguous() or cu_k.get_device() != dev):
         raise ValueError("cu_seqlens_k must be a contiguous int32 tensor like cu_seqlens")
-    mask = (int(block), _limit(before, "before"), _limit(after, "after"), int(sinks))
+    mask = (_int32(block, "block"), _limit(before, "before"), _limit(after, "after"), _sinks(sinks))
     return dev, dtype, code, H, Hk, d, nq, nk, ld, S, mask, d ** -0.5 if scale is None else float(scale)
 
 
@@ -759,9 +775,9 @@ def window_attention_workspace_bytes(heads: int, key_heads: int, d: int, nq: int
                                      backward: bool = False) -> int:
     out = ctypes.c_size_t()
     code = TTT_BF16 if dtype == torch.bfloat16 else TTT_F32
-    _check(load().ttt_window_attention_workspace_bytes(heads, key_heads, d, nq, nk, sequences, block,
-                                                       _limit(before, "before"), _limit(after, "after"), sinks, code,
-                                                       int(backward), ctypes.byref(out)))
+    _check(load().ttt_window_attention_workspace_bytes(heads, key_heads, d, nq, nk, sequences, _int32(block, "block"),
+                                                       _limit(before, "before"), _limit(after, "after"), _sinks(sinks),
+                                                       code, int(backward), ctypes.byref(out)))
     return out.value
 
 
@@ -882,8 +898,8 @@ def window_attention_step(k_cache: torch.Tensor, v_cache: torch.Tensor, q: torch
         workspace = q.new_empty((_attention_step_bytes(H, Hk, d, n, shape[1], code),), dtype=torch.uint8)
     _check(load().ttt_window_attention_step(
         H, Hk, d, k_cache.data_ptr(), v_cache.data_ptr(), stride[1], stride[0], shape[0], shape[1], _ptr(slots),
-        positions.data_ptr(), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, n, int(block),
-        _limit(before, "before"), int(sinks), d ** -0.5 if scale is None else float(scale), code, flags,
+        positions.data_ptr(), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, n,
+        _int32(block, "block"), _limit(before, "before"), _sinks(sinks), d ** -0.5 if scale is None else float(scale), code, flags,
         workspace.data_ptr(), _bytes(workspace, dev), _stream()))
     return out
 

@@ -192,3 +192,23 @@ def test_binding_refuses_host_tensors():
                  lambda: ttt.layer_norm_backward(t, t), lambda: ttt.adamw_tensors([t], [t], [t])):
         with pytest.raises((ValueError, RuntimeError, AssertionError)):
             call()
+
+
+def test_limits_beyond_32_bits():
+    """Limits that take in everything mean that, whatever their size; they do not wrap."""
+    def ask(before, after=0, sinks=0, block=1, backward=False):
+        return ttt.window_attention_workspace_bytes(8, 2, 128, 1374, 43968, 1, block, before, after, sinks, torch.bfloat16, backward)
+    most = (1 << 31) - 1
+    assert ask(0) != ask(None) and ask(0, sinks=0) != ask(0, sinks=most)
+    for big in (1 << 31, 1 << 32, (1 << 32) + 5, 1 << 40, 1 << 62, 1 << 70):
+        assert ttt._limit(big, "before") == -1 and ttt._sinks(big) == most
+        for backward in (False, True):
+            assert ask(big, backward=backward) == ask(None, backward=backward)
+            assert ask(3, after=big, backward=backward) == ask(3, after=None, backward=backward)
+            assert ask(3, sinks=big, backward=backward) == ask(3, sinks=most, backward=backward)
+        for bad in (dict(block=big), dict(block=-big), dict(block=1 - big), dict(before=-big), dict(after=1 - big), dict(sinks=-big)):
+            with pytest.raises((ValueError, ttt.TTTError)):
+                ask(**{"before": 3, **bad})
+    for name, fn in (("block", ttt._int32), ("before", ttt._limit)):
+        with pytest.raises(ValueError, match=name):
+            fn(-(1 << 32), name)

@@ -559,3 +559,22 @@ def test_refusals():
         step(slots=pos, pos=pos.long())
     with pytest.raises(ValueError, match="slots"):
         step(slots=pos[:3])
+
+
+@pytest.mark.parametrize("big", [1 << 31, 1 << 32, (1 << 40) + 3])
+def test_limits_beyond_32_bits(big):
+    """A limit that takes in everything is none: the same bits as without it."""
+    from test_weight_layers_amd import ttt
+    q, k, v, go = (t.cuda() for t in inputs(70, 300, 2, 1, 64, BF, seed=9))
+    for kw, same in ((dict(before=big), dict(before=None)), (dict(before=3, after=big), dict(before=3, after=None)),
+                     (dict(before=2, sinks=big), dict(before=2, sinks=(1 << 31) - 1))):
+        o, lse = ttt.window_attention(q, k, v, heads=2, key_heads=1, block=5, **kw)
+        o2, lse2 = ttt.window_attention(q, k, v, heads=2, key_heads=1, block=5, **same)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        for a, b in zip(ttt.window_attention_backward(q, k, v, o, lse, go, heads=2, key_heads=1, block=5, **kw),
+                        ttt.window_attention_backward(q, k, v, o, lse, go, heads=2, key_heads=1, block=5, **same)):
+            assert torch.equal(a, b)
+    kc, vc = (torch.randn(70, 40, 64, generator=torch.Generator().manual_seed(i)).to(BF).cuda() for i in (1, 2))
+    at = torch.arange(70, dtype=torch.int32).cuda()
+    step = lambda before: ttt.window_attention_step(kc.clone(), vc.clone(), q, k[:70], v[:70], at, heads=2, key_heads=1, before=before)
+    assert torch.equal(step(big), step(None)) and not torch.equal(step(big), step(0))
