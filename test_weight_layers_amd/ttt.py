@@ -460,6 +460,16 @@ def _rate(t: torch.Tensor, H: int, n: int, dev: int, name: str) -> int:
     return _eta_stride(t, H, n, torch.device("cuda", dev), name=name)
 
 
+# (ctypes takes the low 32 bits of a larger number, without a word)
+_MAX32 = (1 << 31) - 1
+
+
+def _int32(x: int, name: str) -> int:
+    if not -_MAX32 <= x <= _MAX32:
+        raise ValueError(f"{name} must be less than 2^31, got {x}")
+    return int(x)
+
+
 def _bytes(workspace: torch.Tensor, dev: int) -> int:
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on cuda:{dev}")
@@ -641,9 +651,9 @@ def gated_residual(x: torch.Tensor, o: torch.Tensor, z: Optional[torch.Tensor] =
         ldh = _row(h_out, dtype, dev, n, C, "h_out")
     elif gamma_next is not None:
         h_out = x.new_empty((n, C))
-    _check(load().ttt_gated_residual(C, C if norm_width is None else int(norm_width), x.data_ptr(), ldx, o.data_ptr(),
-                                     ldo, _ptr(z), ldz, gamma, alpha, gamma_next, float(eps), out.data_ptr(), ldy,
-                                     _ptr(h_out), ldh, n, code, _stream()))
+    w = C if norm_width is None else _int32(norm_width, "norm_width")
+    _check(load().ttt_gated_residual(C, w, x.data_ptr(), ldx, o.data_ptr(), ldo, _ptr(z), ldz, gamma, alpha,
+                                     gamma_next, float(eps), out.data_ptr(), ldy, _ptr(h_out), ldh, n, code, _stream()))
     return out, h_out
 
 
@@ -670,6 +680,7 @@ def gated_residual_backward(grad_y: Optional[torch.Tensor], grad_h: Optional[tor
     ld = lambda t, name: 0 if t is None else _row(t, dtype, dev, n, C, name)
     ldgy, ldgh, ldy = ld(grad_y, "grad_y"), ld(grad_h, "grad_h"), ld(y, "y")
     ldo, ldz = _row(o, dtype, dev, n, C, "o"), ld(z, "z")
+    w = C if norm_width is None else _int32(norm_width, "norm_width")
     given = gamma is not None, alpha is not None, gamma_next is not None
     gamma, alpha = _channel(gamma, C, dev, "gamma"), _channel(alpha, C, dev, "alpha")
     gamma_next = _channel(gamma_next, C, dev, "gamma_next")
@@ -679,9 +690,9 @@ def gated_residual_backward(grad_y: Optional[torch.Tensor], grad_h: Optional[tor
     if workspace is None:
         workspace = _workspace(gated_residual_backward_workspace_bytes(C, n), y.device)
     _check(load().ttt_gated_residual_backward(
-        C, C if norm_width is None else int(norm_width), _ptr(grad_y), ldgy, _ptr(grad_h), ldgh, y.data_ptr(), ldy,
-        o.data_ptr(), ldo, _ptr(z), ldz, gamma, alpha, gamma_next, float(eps), gx.data_ptr(), C, go.data_ptr(), C,
-        _ptr(gz), C, _ptr(gg), _ptr(ga), _ptr(gn), n, code, workspace.data_ptr(), _bytes(workspace, dev), _stream()))
+        C, w, _ptr(grad_y), ldgy, _ptr(grad_h), ldgh, y.data_ptr(), ldy, o.data_ptr(), ldo, _ptr(z), ldz,
+        gamma, alpha, gamma_next, float(eps), gx.data_ptr(), C, go.data_ptr(), C, _ptr(gz), C, _ptr(gg), _ptr(ga),
+        _ptr(gn), n, code, workspace.data_ptr(), _bytes(workspace, dev), _stream()))
     return gx, go, gz, gg, ga, gn
 
 
@@ -718,16 +729,6 @@ def orthogonalise(g: torch.Tensor, steps: int = 5, out: Optional[torch.Tensor] =
 
 
 # ------------------------------------------------------------------ windowed attention
-# (ctypes takes the low 32 bits of a larger number, without a word)
-_MAX32 = (1 << 31) - 1
-
-
-def _int32(x: int, name: str) -> int:
-    if not -_MAX32 <= x <= _MAX32:
-        raise ValueError(f"{name} must be less than 2^31, got {x}")
-    return int(x)
-
-
 def _limit(x: Optional[int], name: str) -> int:
     if x is None:
         return -1
@@ -915,7 +916,7 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
     if x.dim() != 2:
         raise ValueError("x must be a 2-D tensor of rows")
     n, C = x.shape
-    w = C if norm_width is None else int(norm_width)
+    w = C if norm_width is None else _int32(norm_width, "norm_width")
     ldx = _row(x, dtype, dev, n, C, "x")
     gamma, beta = _channel(gamma, w, dev, "gamma"), _channel(beta, w, dev, "beta")
     if out is None:
@@ -943,7 +944,7 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, gamma: Optional[t
     if x.dim() != 2:
         raise ValueError("x must be a 2-D tensor of rows")
     n, C = x.shape
-    w = C if norm_width is None else int(norm_width)
+    w = C if norm_width is None else _int32(norm_width, "norm_width")
     ldx, ldg = _row(x, dtype, dev, n, C, "x"), _row(grad_y, dtype, dev, n, C, "grad_y")
     gamma = _channel(gamma, w, dev, "gamma")
     if out is None:

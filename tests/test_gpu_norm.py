@@ -144,3 +144,15 @@ def test_refusals():
         ttt.layer_norm_backward(x.clone(), x, out=x)
     with pytest.raises(ValueError, match="grad_y"):
         ttt.layer_norm_backward(x[:3], x)
+
+
+def test_width_beyond_32_bits():
+    """A width of 2^32 + 64 is not one of 64."""
+    from test_weight_layers_amd import ttt
+    x = torch.zeros(4, 64, device="cuda")
+    for width in ((1 << 32) + 64, (1 << 32) + 32, 1 << 31, -(1 << 32) + 64):
+        for call in (lambda: ttt.layer_norm(x, norm_width=width), lambda: ttt.layer_norm_backward(x.clone(), x, norm_width=width),
+                     lambda: ttt.gated_residual(x, x.clone(), norm_width=width),
+                     lambda: ttt.gated_residual_backward(x, None, x.clone(), x.clone(), norm_width=width)):
+            with pytest.raises(ValueError, match="norm_width"):
+                call()
