@@ -504,7 +504,8 @@ int ttt_layer_norm_backward(int32_t channels, int32_t norm_width, const void *gr
  *   w <- w (1 - lr weight_decay) - lr / (1 - b1^step) m / (sqrt(v) / sqrt(1 - b2^step) + eps)
  *
  * tensors : HOST table, read before the call returns.  param, grad: `dtype`; master: the fp32 weights that are stepped
- *           and then rounded to param, or NULL (param itself is stepped); all tensors of a call with or without.
+ *           and then rounded to param, or NULL (param itself is stepped); all tensors of a call with or without
+ *           (but for those of n = 0, whose pointers are not looked at).
  *           Pointers need the alignment of their elements only; 16 bytes (8-bit states: 8) are faster.
  * bits    : 32 (exp_avg, exp_avg_sq fp32) or 8: exp_avg int8 [n], exp_avg_sq uint8 [n], with a scale s for each 256
  *           elements in exp_avg_scale, exp_avg_sq_scale (fp32 [ceil(n / 256)]):  m = s c |c| / 127^2, s = max |m|;

@@ -413,10 +413,13 @@ static int check_adamw(const ttt_adamw_tensor *t, int count, int bits, int dtype
   if (count > 0 && !t) return fail(TTT_EINVAL, "tensors is null");
   const size_t es = esize(dtype), ss = bits == 8 ? 1 : 4;
   const auto off = [](const void *p, size_t a) { return ((uintptr_t)p) % a != 0; };
+  const ttt_adamw_tensor *like = nullptr;             // the first that has elements
   for (int i = 0; i < count; ++i) {
     if (t[i].n < 0 || t[i].n > (int64_t(1) << 34)) return fail(TTT_EINVAL, "tensor %d: n must be in [0, 2^34]", i);
-    if ((t[i].master != nullptr) != (t[0].master != nullptr)) return fail(TTT_EINVAL, "tensor %d: master for all tensors or for none", i);
-    if (t[i].n == 0) continue;
+    if (t[i].n == 0) continue;                        // (whose pointers may all be null)
+    if (!like) like = t + i;
+    if ((t[i].master != nullptr) != (like->master != nullptr))
+      return fail(TTT_EINVAL, "tensor %d: master for all tensors or for none", i);
     if (!t[i].param || !t[i].exp_avg || !t[i].exp_avg_sq || (grads && !t[i].grad))
       return fail(TTT_EINVAL, "tensor %d: param, grad, exp_avg or exp_avg_sq is null", i);
     if (bits == 8 ? !t[i].exp_avg_scale || !t[i].exp_avg_sq_scale : t[i].exp_avg_scale || t[i].exp_avg_sq_scale)

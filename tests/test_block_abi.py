@@ -212,3 +212,20 @@ def test_limits_beyond_32_bits():
     for name, fn in (("block", ttt._int32), ("before", ttt._limit)):
         with pytest.raises(ValueError, match=name):
             fn(-(1 << 32), name)
+
+
+@cpu_only
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_empty_tensors_beside_masters(lib, bits):
+    """An empty tensor has no master, nor any other array: its pointers are null, wherever it stands in the table."""
+    none = dict(param=None, grad=None, exp_avg=None, exp_avg_sq=None, n=0)
+    scales = dict(exp_avg_scale=8 * MB, exp_avg_sq_scale=9 * MB) if bits == 8 else {}
+    first = dict(scales, master=5 * MB)
+    other = dict(param=11 * MB, exp_avg=13 * MB, exp_avg_sq=14 * MB, master=15 * MB,
+                 **{k: v + 10 * MB for k, v in scales.items()})
+    for t in ((first, none), (none, first), (none, first, none, other, none), (none,), (none, dict(none, master=7 * MB))):
+        assert lib.ttt_adamw_check(table(*t), len(t), bits, BF16) == 0, (t, lib.ttt_last_error())
+    bare = {k: v for k, v in other.items() if k != "master"}
+    for t, at in (((none, first, bare), b"tensor 2"), ((none, bare, first), b"tensor 2"), ((first, none, bare), b"tensor 2")):
+        assert lib.ttt_adamw_check(table(*t), len(t), bits, BF16) == -1
+        assert at in lib.ttt_last_error() and b"master" in lib.ttt_last_error()

@@ -225,3 +225,23 @@ def test_refusals():
         ttt.adamw_tensors(s["p"], s["m"][:1], s["v"])
     with pytest.raises(ValueError, match="contiguous"):
         ttt.adamw_tensors([torch.zeros(4, 8, device="cuda").t()], [torch.zeros(32, device="cuda")], [torch.zeros(32, device="cuda")])
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_empty_tensors_beside_masters(dtype, bits):
+    """A table with empty tensors steps the others as the table without them does: the same bits."""
+    from test_weight_layers_amd import ttt
+    sizes = [0, 300, 0, 0, 1029, 0]
+    s, grads = make(sizes, dtype, bits, True)
+    assert s["master"][0].data_ptr() == 0
+    full = [i for i, n in enumerate(sizes) if n]
+    alone = {k: [x[i].clone() for i in full] for k, x in s.items()}
+    h, h2 = handle(s), handle(alone)
+    for step in (1, 2, 3):
+        g = grads()
+        ttt.adamw_step(h, g, step=step, lr=LR, betas=BETAS, eps=EPS, weight_decay=WD)
+        ttt.adamw_step(h2, [g[i] for i in full], step=step, lr=LR, betas=BETAS, eps=EPS, weight_decay=WD)
+    for k, x in s.items():
+        assert all(torch.equal(x[i], y) for i, y in zip(full, alone[k])), k
+    assert s["m"][1].any() and not torch.equal(s["master"][1], make(sizes, dtype, bits, True)[0]["master"][1])
