@@ -467,7 +467,8 @@ int ttt_window_attention_backward(int32_t heads, int32_t key_heads, int32_t d, c
  *   and still in the cache; then its k and v are written to its place.
  * The rows of a call read the caches as they were before it; where several name one place of a cache the last one's
  * token stays.  A row whose slot is outside [0, pool) or whose position is negative is padding: nothing is read or
- * written for it (TTT_ATTENTION_ZERO_UNUSED sets its o to zero).  Nothing may overlap the caches or o.
+ * written for it (TTT_ATTENTION_ZERO_UNUSED sets its o to zero).  Nothing may overlap the caches or o; the two caches may be
+ * column halves of the same rows or stand one after the other in each entry.
  * n^2 <= 2^42 with slots (the later rows of one place are found by comparing all). */
 int ttt_window_attention_step_workspace_bytes(int32_t heads, int32_t key_heads, int32_t d, int64_t n,
                                               int32_t capacity, int32_t dtype, size_t *bytes);

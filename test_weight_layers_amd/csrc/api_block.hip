@@ -324,9 +324,10 @@ int ttt_window_attention_step(int32_t heads, int32_t key_heads, int32_t d, void 
     const int64_t ps = pool > 1 ? pool_stride * (int64_t)es : INT64_MAX;
     int64_t x = (int64_t)((intptr_t)v_cache - (intptr_t)k_cache);
     x = x < 0 ? -x : x;
-    const int64_t cache = (int64_t)(capacity - 1) * ls + wb, in_pool = x % ps;
-    const bool beside = in_pool >= cache && in_pool + cache <= ps;              // one cache after the other in each entry
-    const bool between = ps % ls == 0 && x % ls >= wb && x % ls + wb <= ls;     // column halves of the same rows
+    const int64_t cache = (int64_t)(capacity - 1) * ls + wb, in_pool = x % ps, in_row = in_pool % ls;
+    const bool inside = in_pool + cache <= ps;          // an entry of one lies in one entry of the other's stride
+    const bool beside = inside && in_pool >= cache;     // one cache after the other in each entry
+    const bool between = (inside || ps % ls == 0) && in_row >= wb && in_row + wb <= ls;   // column halves of the same rows
     if (!beside && !between) return fail(TTT_EINVAL, "k_cache must not overlap v_cache");
   }
   if ((st = check_ws(workspace, workspace_bytes, P.total))) return st;

@@ -229,3 +229,30 @@ def test_adamw_empty_tensors_beside_masters(lib, bits):
     for t, at in (((none, first, bare), b"tensor 2"), ((none, bare, first), b"tensor 2"), ((first, none, bare), b"tensor 2")):
         assert lib.ttt_adamw_check(table(*t), len(t), bits, BF16) == -1
         assert at in lib.ttt_last_error() and b"master" in lib.ttt_last_error()
+
+
+@cpu_only
+def test_attention_step_cache_layouts(lib):
+    """k and v in one buffer, for pools of one cache and of more: apart by columns or by entries, or refused."""
+    def call(x, pool, ldc=128, stride=0, cap=20):
+        return lib.ttt_window_attention_step(1, 1, 64, 100 * MB, 100 * MB + x, ldc, stride, pool, cap, 5 * MB, 6 * MB, 1 * MB, 64,
+                                             2 * MB, 64, 3 * MB, 64, 4 * MB, 64, 10, 1, -1, 0, 0.1, F32, 0, None, 0, None)
+    # rows of 64 fp32 values: 256 bytes, 512 from row to row
+    for pool in (1, 2, 4):
+        tight, wide = 20 * 128, 20 * 128 + 64           # entries back to back, and 256 bytes apart
+        for stride in (tight, wide):
+            for x in (256, -256):                       # column halves of the same rows
+                assert call(x, pool, stride=stride) == -3, (pool, stride, x, lib.ttt_last_error())
+            for x in (0, 128, -128, 384, -64):          # columns that both have
+                assert call(x, pool, stride=stride) == -1 and b"overlap" in lib.ttt_last_error(), (pool, stride, x)
+        # halves of the rows of different entries, or of rows further down
+        assert call(tight * 4 + 256, pool, stride=tight) == -3
+        assert call(5 * 512 + 256, pool, stride=tight) == -3
+        # rows moved down in entries that are not whole rows apart: the next entry's columns are others (but for a pool of one)
+        assert call(5 * 512 + 256, pool, stride=wide) == (-3 if pool == 1 else -1)
+        # one cache after the other in each entry
+        assert call(20 * 512, pool, stride=40 * 128) == -3
+        assert call(20 * 512 - 256, pool, stride=40 * 128) == -3          # (its last row ends at 19 * 512 + 256)
+        assert call(20 * 512 - 384, pool, stride=40 * 128) == -1
+    for cap in (1, 2):
+        assert call(256, 1, cap=cap) == -3 and call(128, 1, cap=cap) == -1

@@ -578,3 +578,28 @@ def test_limits_beyond_32_bits(big):
     at = torch.arange(70, dtype=torch.int32).cuda()
     step = lambda before: ttt.window_attention_step(kc.clone(), vc.clone(), q, k[:70], v[:70], at, heads=2, key_heads=1, before=before)
     assert torch.equal(step(big), step(None)) and not torch.equal(step(big), step(0))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("pool,more", [(1, 0), (1, 8), (2, 24)], ids=["one", "one with other columns", "entries apart"])
+def test_step_halves_of_one_buffer(pool, more, dtype):
+    """k and v as column halves of the same rows, of one cache and of entries that are not whole rows apart, round and round:
+    the bits of caches of their own."""
+    from test_weight_layers_amd import ttt
+    H, Hk, d, capacity = 4, 2, 64, 11
+    g = torch.Generator().manual_seed(pool)
+    width, pad = 2 * Hk * d + (8 if more == 8 else 0), 16 if more == 24 else 0
+    flat = torch.full((pool * (capacity * width + pad),), 7.0, dtype=dtype, device="cuda")
+    both = flat.as_strided((pool, capacity, width), (capacity * width + pad, width, 1))
+    kc, vc = both[:, :, :Hk * d], both[:, :, Hk * d:2 * Hk * d]
+    k2, v2 = kc.clone().contiguous(), vc.clone().contiguous()
+    expect = flat.clone()
+    for p in range(30):
+        q, k, v = (torch.randn(pool, h * d, generator=g).to(dtype).cuda() for h in (H, Hk, Hk))
+        at = torch.full((pool,), p, dtype=torch.int32, device="cuda")
+        kw = dict(heads=H, key_heads=Hk, sinks=3)
+        o, o2 = ttt.window_attention_step(kc, vc, q, k, v, at, **kw), ttt.window_attention_step(k2, v2, q, k, v, at, **kw)
+        assert torch.equal(o, o2) and torch.equal(kc, k2) and torch.equal(vc, v2), p
+    view = expect.as_strided(both.shape, both.stride())
+    view[:, :, :Hk * d], view[:, :, Hk * d:2 * Hk * d] = k2, v2
+    assert torch.equal(flat, expect)
