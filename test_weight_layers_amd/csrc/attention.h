@@ -55,7 +55,7 @@ struct AttnParams {
   int64_t ldgq, ldgk, ldgv;
   float *delta;                     // [heads][nq]
   int qparts;                       // ranges of a query tile's keys
-  float *qpart;                     // [query tiles of all heads][qparts][qrows][d]
+  float *qpart;                     // [qparts][nq][heads][d], qparts > 1
   int parts, sink_parts, sink_tiles;// ranges of a key tile's queries; of a sink tile's beyond the window; tiles of sinks
   float *part;                      // [parts][nk][key_heads][2][d], parts > 1
   float *spart;                     // [nseq][sink_tiles][key_heads][1 + sink_parts][krows][2][d]
@@ -92,8 +92,10 @@ struct AttnWork {
 };
 AttnCut attn_cut(const AttnWork &w, int d, int rows, bool bf16);
 struct AttnGradWork {
-  int64_t key_items, query_items;               // key tiles of all key heads, query tiles of all heads
+  int64_t key_tiles, query_tiles;               // key tiles of all key heads, query tiles of all heads
+  int64_t key_items, query_items;               // those of them that have something to do
   int64_t queries, keys;                        // that the longest of them walk over
+  int64_t query_steps;                          // tiles of 32 of these queries, head by head
   double mean_queries, mean_keys;
 };
 struct AttnGradCut {

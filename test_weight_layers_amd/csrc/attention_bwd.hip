@@ -405,7 +405,7 @@ __global__ __launch_bounds__(256, OCC) void attn_grads_kernel(AttnParams p, int 
       const int i = row0 + 16 * c + li;
       if (i >= s.ql) continue;
       if (p.qparts > 1) {
-        float *out = p.qpart + ((int64_t)item * QR + (i - t0)) * D + 4 * g;
+        float *out = p.qpart + (((int64_t)part * p.nq + s.qs + i) * p.heads + h) * D + 4 * g;
 #pragma unroll
         for (int d = 0; d < ND; ++d) store4(out + 16 * d, dq[d][c] * p.scale);
         continue;
@@ -430,11 +430,12 @@ template <typename T, int D> __global__ __launch_bounds__(256) void attn_sum_ker
     if (!tile_of<false>(p, p.qtiles - 1 - (item - h * p.qtiles), &s, &tile, &seq)) return;
     const int c = threadIdx.x % L * 4, r = y * (256 / L) + threadIdx.x / L;
     if (tile * p.qrows + r >= s.ql) return;
-    const float *a = p.qpart + ((int64_t)item * p.qparts * p.qrows + r) * D + c;
+    const int64_t row = s.qs + tile * p.qrows + r, step = (int64_t)p.nq * p.heads * D;
+    const float *a = p.qpart + (row * p.heads + h) * D + c;
     f32x4 v = zero_f4();
 #pragma unroll 4
-    for (int i = 0; i < p.qparts; ++i) v += *reinterpret_cast<const f32x4 *>(a + (int64_t)i * p.qrows * D);
-    store4(static_cast<T *>(p.gq) + (int64_t)(s.qs + tile * p.qrows + r) * p.ldgq + h * D + c, v);
+    for (int i = 0; i < p.qparts; ++i) v += *reinterpret_cast<const f32x4 *>(a + i * step);
+    store4(static_cast<T *>(p.gq) + row * p.ldgq + h * D + c, v);
     return;
   }
   constexpr int L = D / 2;
@@ -502,19 +503,23 @@ AttnGradCut attn_grad_cut(const AttnGradWork &w, int d, bool bf16, int qrows, in
   const double query = 0.75 * key * std::pow((double)qrows / krows, 0.8);
   const double at_once = bf16 ? (d == 64 ? 3.0 : d == 128 ? 2.0 : 1.2) : d == 64 ? 1.5 : d == 128 ? 1.3 : 1.15;
   const double mean = (w.key_items * w.mean_queries * key + w.query_items * w.mean_keys * query) / (256 * at_once);
-  const double key_sum = w.key_items * (double)krows * 2 * d * 4 / 2.5e6, query_sum = w.query_items * (double)qrows * d * 4 / 2.5e6;
+  const double key_sum = w.key_tiles * (double)krows * 2 * d * 4 / 2.5e6, query_sum = w.query_tiles * (double)qrows * d * 4 / 2.5e6;
   static constexpr int kRanges[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
   AttnGradCut best{1, 1};
   if (std::max((double)w.queries * key, (double)w.keys * query) <= mean) return best;
   double least = 0.0;
-  for (const int q : kRanges)
+  for (const int q : kRanges) {
+    if (q > 1 && w.keys / q < 32) break;
+    int before = 0;
     for (const int k : kRanges) {
-      if (q > 1 && w.keys / q < 32) break;
+      if (k > 1 && before >= w.query_steps) break;      // (more ranges than steps: some of nothing)
+      before = k;
       const double longest = std::max((double)w.queries / k * key, (double)w.keys / q * query);
       const double t = (w.key_items * k + w.query_items * q > 256 ? std::max(longest, mean + longest / 2) : longest) +
                        (k > 1 || q > 1 ? 6.0 : 0.0) + (k > 1 ? k * key_sum : 0.0) + (q > 1 ? q * query_sum : 0.0);
       if (k * q == 1 || t < 0.97 * least) least = t, best = AttnGradCut{k, q};
     }
+  }
   return best;
 }
 

@@ -256,3 +256,23 @@ def test_attention_step_cache_layouts(lib):
         assert call(20 * 512 - 384, pool, stride=40 * 128) == -1
     for cap in (1, 2):
         assert call(256, 1, cap=cap) == -3 and call(128, 1, cap=cap) == -1
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("nq,nk,seqs,heads,key_heads,d,before,after", [
+    (64, 8192, 1, 8, 2, 128, -1, 0), (1374, 43968, 1, 8, 8, 128, -1, 0), (256, 131072, 1, 32, 8, 128, -1, 0),
+    (64, 8192, 1, 8, 8, 64, -1, -1), (1, 5000, 1, 8, 2, 128, -1, 0), (986, 603660, 2, 64, 16, 256, -1, 0),
+    (65536, 512, 1, 8, 8, 64, -1, -1), (8192, 64, 1, 8, 2, 128, -1, -1), (5000, 1, 1, 8, 2, 128, -1, -1), (40000, 500, 2, 8, 2, 64, -1, -1)])
+def test_attention_gradient_ranges_of_unequal_rows(lib, nq, nk, seqs, heads, key_heads, d, before, after, dtype):
+    """A few queries are not cut in ranges because there are many keys, nor a few keys because there are many queries: a range
+    holds fp32 gradients of all keys (of all queries), and two take twice that."""
+    st, b = ws(lib, ATT, heads, key_heads, d, nq, nk, seqs, 1, before, after, 0, dtype, 1)
+    keys, queries = nk * key_heads * 2 * d * 4, nq * heads * d * 4
+    assert st == 0 and b < 2 * max(keys, queries), (b, keys, queries)
+
+
+def test_attention_gradient_ranges_of_equal_rows(lib):
+    """Where both walks are long both are cut, as they were."""
+    for dtype, most in ((BF16, 28), (F32, 47)):
+        st, b = ws(lib, ATT, 2, 1, 128, 2048, 2048, 1, 1, -1, 0, 0, dtype, 1)
+        assert st == 0 and 2 * 2048 * 2 * 128 * 4 < b < most * 10 ** 6

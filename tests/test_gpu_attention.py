@@ -603,3 +603,29 @@ def test_step_halves_of_one_buffer(pool, more, dtype):
     view = expect.as_strided(both.shape, both.stride())
     view[:, :, :Hk * d], view[:, :, Hk * d:2 * Hk * d] = k2, v2
     assert torch.equal(flat, expect)
+
+
+# Far fewer queries than keys and far fewer keys than queries: what of the other side a walk is cut by, and tiles beyond a window.
+UNEQUAL = [
+    (8, 2, 128, [64], [4100], (1, None, 0, 0), BF),
+    (8, 2, 128, [64], [4100], (1, None, 0, 0), F32),
+    (4, 4, 64, [33], [5000], (1, None, None, 0), F32),
+    (2, 1, 256, [90], [3000], (1, 700, 0, 4), BF),
+    (4, 1, 256, [150], [2000], (10, 30, 0, 70), F32),
+    (2, 2, 128, [500], [2500], (1, 100, 100, 0), BF),
+    (2, 2, 128, [500], [2500], (7, 10, 10, 30), F32),
+    (2, 1, 64, [1], [3000], (1, None, 0, 0), BF),
+    (8, 2, 128, [4100], [64], (1, None, None, 0), BF),
+    (4, 4, 64, [5000], [33], (1, None, None, 0), F32),
+    (2, 1, 256, [2500], [100], (1, None, None, 0), BF),
+    (4, 2, 128, [1500], [500], (1, None, 0, 0), BF),              # queries before the first key
+    (4, 2, 128, [1500], [500], (8, 5, 60, 20), F32),
+    (2, 2, 64, [3000], [1], (1, None, None, 0), BF),
+    (8, 4, 64, [70, 0, 1, 200], [2000, 10, 1500, 0], (1, None, 0, 3), BF),
+    (4, 4, 64, [3000, 40, 5], [70, 900, 0], (4, None, None, 0), F32),
+]
+
+
+@pytest.mark.parametrize("case", UNEQUAL, ids=str)
+def test_unequal_rows(case):
+    test_forward_and_gradient(case)
