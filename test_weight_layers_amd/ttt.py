@@ -963,10 +963,14 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, gamma: Optional[t
 
 # ------------------------------------------------------------------ AdamW
 class AdamwTensors:
-    """The tensors of ``adamw_step``: made once by ``adamw_tensors``, it keeps them alive."""
+    """The tensors of ``adamw_step``: made once by ``adamw_tensors``, it keeps their memory alive."""
 
-    def __init__(self, table, sizes, dtype, bits, dev, held):
-        self.table, self.sizes, self.dtype, self.bits, self.dev, self.held = table, sizes, dtype, bits, dev, held
+    def __init__(self, table, sizes, dtype, bits, dev, lists, weights):
+        self.table, self.sizes, self.dtype, self.bits, self.dev = table, sizes, dtype, bits, dev
+        # (views of their own: a tensor whose ``data`` is set anew lets go of the memory that the table names)
+        self.held = [t.detach() for x in lists for t in x]
+        self.weights = weights                          # params and masters, which are looked at in every step
+        self.at = [t.data_ptr() for t in weights]
 
 
 def adamw_tensors(params: Sequence[torch.Tensor], exp_avg: Sequence[torch.Tensor], exp_avg_sq: Sequence[torch.Tensor], *,
@@ -977,7 +981,8 @@ def adamw_tensors(params: Sequence[torch.Tensor], exp_avg: Sequence[torch.Tensor
 
     params bfloat16 or float32 (all of one type), contiguous, any shapes; ``master`` the float32 weights behind them.
     exp_avg, exp_avg_sq: float32 of the params' sizes, or int8 and uint8 with a float32 scale for each 256 elements
-    (exp_avg_scales, exp_avg_sq_scales).  Zeros are the state to start from.
+    (exp_avg_scales, exp_avg_sq_scales).  Zeros are the state to start from.  The table names the tensors' memory: make it
+    anew when that is replaced (``p.data = ...``).
     """
     if not params:
         raise ValueError("params must hold a tensor")
@@ -1006,7 +1011,8 @@ def adamw_tensors(params: Sequence[torch.Tensor], exp_avg: Sequence[torch.Tensor
     for i, n in enumerate(sizes):
         table[i].n = n
     _check(load().ttt_adamw_check(table, len(params), bits, code))
-    return AdamwTensors(table, sizes, dtype, bits, dev, [list(x[2]) for x in lists if x[2] is not None])
+    return AdamwTensors(table, sizes, dtype, bits, dev, [x[2] for x in lists if x[2] is not None],
+                        [*params, *(master or ())])
 
 
 def adamw_step(tensors: AdamwTensors, grads: Sequence[torch.Tensor], *, step, lr, betas: Tuple[float, float] = (0.9, 0.999),
@@ -1021,6 +1027,8 @@ def adamw_step(tensors: AdamwTensors, grads: Sequence[torch.Tensor], *, step, lr
         raise ValueError(f"the tensors must be on the current GPU, got cuda:{dev}")
     if len(grads) != len(sizes):
         raise ValueError(f"grads must hold {len(sizes)} tensors")
+    if [t.data_ptr() for t in tensors.weights] != tensors.at:
+        raise ValueError("params or masters have moved to other memory since adamw_tensors")
     for i, g in enumerate(grads):
         if g.dtype != dtype or g.numel() != sizes[i] or not g.is_contiguous() or g.get_device() != dev:
             raise ValueError(f"grads[{i}] must be a contiguous {dtype} tensor of {sizes[i]} elements on cuda:{dev}")

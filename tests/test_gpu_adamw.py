@@ -245,3 +245,24 @@ def test_empty_tensors_beside_masters(dtype, bits):
     for k, x in s.items():
         assert all(torch.equal(x[i], y) for i, y in zip(full, alone[k])), k
     assert s["m"][1].any() and not torch.equal(s["master"][1], make(sizes, dtype, bits, True)[0]["master"][1])
+
+
+@pytest.mark.parametrize("name", ["p", "master"])
+def test_moved_tensors_are_refused(name):
+    """A tensor whose data is set anew is not stepped where it was."""
+    from test_weight_layers_amd import ttt
+    s, grads = make([300, 20], BF, 32, True)
+    h, g = handle(s), grads()
+    ttt.adamw_step(h, g, step=1, lr=LR)
+    held = s[name][1].detach()
+    s[name][1].data = s[name][1].clone()
+    before = held.clone()
+    with pytest.raises(ValueError, match="moved"):
+        ttt.adamw_step(h, g, step=2, lr=LR)
+    assert torch.equal(held, before) and torch.equal(s[name][1], before)
+    ttt.adamw_step(handle(s), g, step=2, lr=LR)
+    s2, grads2 = make([300, 20], BF, 32, True)
+    h2, g2 = handle(s2), grads2()
+    for step in (1, 2):
+        ttt.adamw_step(h2, g2, step=step, lr=LR)
+    assert all(torch.equal(a, b) for k in s for a, b in zip(s[k], s2[k])) and not torch.equal(held, s[name][1])
