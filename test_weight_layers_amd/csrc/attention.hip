@@ -3,8 +3,12 @@
 // See attn_tile.h for the orientation of the products and attention.h for the parameters.
 // Bound by the products (4 d operations a visible pair) and the exponentials: at d = 64 a pair costs as long in e^x and the
 // sums as in the matrix cores, so that two to four waves a SIMD have to overlap the two.  MI355X, bf16, 8192 x 8192, no mask:
-// 8 heads of 64 202 us (680 TFLOP/s; 48 heads 853), 8 of 128 299 (920), 4 of 256 450 (610: one workgroup a CU, bound by LDS
-// reads as much as by products); fp32, 8 heads of 64 1056 us and of 128 2028 (130 and 135 of 137 TFLOP/s of a large product).
+// 8 heads of 64 211 us (650 TFLOP/s; 48 heads 853), 8 of 128 279 (985), 4 of 256 445 (617: one workgroup a CU, bound by LDS
+// reads as much as by products); fp32, 8 heads of 64 1060 us and of 128 2038 (130 and 135 of 137 TFLOP/s of a large product),
+// 4 of 256 2818 (98: tiles of 64 rows in four waves, one a SIMD, which nothing overlaps).
+// bf16 probabilities are rounded once more, to the operands of the second product: half a step each, 2^-8 of a term at most and
+// independent of v.  Outputs are 2.3e-3 off 64 bits, of which their own rounding is 1.7e-3; two operands for one would make
+// three products of two.  Sums of probabilities and of outputs are fp32.
 // What was tried and did not pay: three LDS stages, touching tiles ahead for L2, wave priorities (4% at d = 256 alone), eight
 // waves that take turns at products and exponentials (25% slower: a barrier makes both halves as long as the longer).
 #include <algorithm>
@@ -186,7 +190,7 @@ __global__ __launch_bounds__(256 * KG, OCC) void attn_forward_kernel(AttnParams 
               sum[c] += sc[u][c][x];
             }
 #pragma unroll
-          for (int u = 0; u < NU; u += 2) pr[u / 2][c] = pack44<T>(sc[u][c], sc[u + 1][c]);
+          for (int u = 0; u < NU; u += 2) pr[u / 2][c] = pack44<T>(sc[u][c], sc[u + 1][c]);      // (rounded: see above)
         }
       }
       if (careful) {

@@ -7,8 +7,10 @@
 // the second fills the CUs that the first leaves idle, at its end and where it has few tiles (8192 x 8192 causal, 8 heads of
 // 64: 405 -> 280 us; 8 x 1024 tokens, 12 heads of 64 on 4, window 512: 123 -> 92).
 // Bound by the products, 7 of 2 d operations a visible pair where the formula has 5.  8192 x 8192 without a mask, bf16: 8 heads
-// of 64 540 us, 8 of 128 1040, 4 of 256 1710 (890, 925 and 560 TFLOP/s of the 7; a large product reaches 1216); fp32: 3560,
-// 7260 and 8840 us (135, 132 and 109 of 137).
+// of 64 560 us, 8 of 128 1070, 4 of 256 1750 (860, 900 and 550 TFLOP/s of the 7; a large product reaches 1216); fp32: 3570,
+// 7280 and 8800 us (135, 132 and 109 of 137).
+// bf16 P and dS are rounded once, to the operands of the products that add them up (2^-8 of a term at most): gradients are 2.5e-3
+// off 64 bits, of which their own rounding is 1.7e-3.  All sums are fp32.
 #include <algorithm>
 #include <cmath>
 
@@ -530,7 +532,10 @@ hipError_t launch_attention_backward(const AttnParams &p, bool bf16, hipStream_t
   const hipError_t e = launch_attention_plan(p, s);
   if (e != hipSuccess) return e;
   // Tiles of two columns of 16 rows a wave read LDS half as often, and where they leave few workgroups one column does (256:
-  // 2048 tokens of 4 heads 214 us against 251, 8192 tokens 1939 against 1717).  The occupancies are the most without spills.
+  // 2048 tokens of 4 heads 214 us against 251, 8192 tokens 1939 against 1717).  The occupancies leave the vector registers in
+  // place, but for 4 of bf16 256 in its tiles of 128 queries.  Scalar registers are short, as both kinds of work share a kernel
+  // and its arguments: 82 to 146 of them are kept elsewhere (lanes of vector registers; bf16 128, and fp32 64 in tiles of 128,
+  // have 68 bytes of scratch a lane).
   if (bf16) {
     if (p.d == 64) return p.krows == 64 ? go<__bf16, 64, 1, 64, 1, 64, 4>(p, s) : go<__bf16, 64, 2, 64, 2, 64, 2>(p, s);
     if (p.d == 128) return go<__bf16, 128, 2, 32, 1, 32, 2>(p, s);

@@ -4,9 +4,11 @@
 // read the caches as they were before it.
 // Bound by reading the visible keys and values once.  The heads of a key head are the columns of the products of
 // attn_tile.h; keys go from memory to registers, 32 a wave, values through the wave's own part of LDS.
-// The keys go in ranges of 512 (api_block.hip): 4096 keys of one token, 16 heads of 64, take 8 + 4 us (the launches; 3.5 us
-// of bytes); 64 tokens over caches of 4096 rows, 16 heads of 128 on 4, 116 us (537 MB at 4.6 TB/s; a copy reaches 4.9), and
-// 54 where a third is visible (185 MB; 66 in ranges of 256, which are bound by their start).
+// The keys go in ranges of 512 (api_block.hip): 4096 keys of one token, 16 heads of 64, take 9 + 4 us (the launches; 3.5 us
+// of bytes; fp32 11 + 4); 64 tokens over caches of 4096 rows, 16 heads of 128 on 4, 116 us (537 MB at 4.6 TB/s; a copy reaches
+// 4.9; fp32 205 + 5, 1073 MB at 5.1), and 51 to 54 where a third is visible (185 MB; 66 in ranges of 256, which are bound by
+// their start).  The waves wait for all their copies before a tile's values are used, the next tile's among them: what is read ahead is
+// covered by one tile's scores and exponentials.  bf16 probabilities are rounded as operands, as in the forward.
 #include "attn_tile.h"
 
 namespace ttt {
