@@ -55,6 +55,12 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
   const bool bounded = a.before >= 0 && a.after >= 0, limited = a.before >= 0 || a.after >= 0;
   const int64_t span = bounded ? std::min(((int64_t)a.before + a.after + 1) * a.block, int64_t(1) << 40) : 0;
   const int64_t window = bounded ? std::min(span, lk) : lk;
+  // Tiles that have something to do, of sequences with `mean` such rows: of the side with fewer rows each sequence has a last
+  // tile of its own (gradient of 120 queries on 8694 keys in 70 sequences, 16 heads of 128 on 2, fp32: 178 us with full tiles
+  // counted and 135 so); where both sides are alike the models' times are of full tiles (2441 tokens in 8 sequences 58 and 77).
+  const auto items = [&](int64_t n, int64_t mean, int rows, bool shorter) {
+    return shorter ? std::min(tiles(n, rows), a.nseq * ceil_div(mean, rows)) : ceil_div(std::min(n, a.nseq * mean), rows);
+  };
   AttnPlan P{};
   P.splits = P.parts = P.qparts = 1;
   size_t o = 0;
@@ -71,7 +77,8 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     P.krows = 64;
     const int64_t longest = a.nseq == 1 ? lk : std::min(a.nk, lk + lk / 2), wgs = tiles(a.nq, P.qrows) * a.heads;
     AttnWork w;
-    w.tiles = wgs, w.busy = ceil_div(a.nq, P.qrows) * a.heads, w.even = a.nseq == 1 && (bounded || !limited);
+    // (fewer queries than keys in several sequences: about the mean length each, with a last tile of its own)
+    w.tiles = wgs, w.busy = items(a.nq, lq, P.qrows, a.nq < a.nk) * a.heads, w.even = a.nseq == 1 && (bounded || !limited);
     w.keys = std::min(longest, (bounded ? span : longest) + P.qrows + a.sinks);
     w.mean_keys = std::min(lk, window + P.qrows + a.sinks) * (bounded || !limited ? 1.0 : 0.55);
     const AttnCut cut = attn_cut(w, a.d, P.qrows, bf16);
@@ -96,12 +103,6 @@ int plan_attention(const AttnShape &a, bool backward, AttnPlan *out) {
     const int64_t long_q = a.nseq == 1 ? bq : std::min(a.nq, 2 * bq), long_k = a.nseq == 1 ? bk : std::min(a.nk, 2 * bk);
     AttnGradWork w;
     w.key_tiles = ceil_div(a.nk, P.krows) * a.key_heads, w.query_tiles = ceil_div(a.nq, P.qrows) * a.heads;
-    // (the shorter side's sequences of about the mean length, each with a last tile of its own: 120 queries on 8694 keys in 70
-    // sequences, 16 heads of 128 on 2, fp32 178 us with full tiles counted and 135 so; where both sides are alike the model's
-    // times are of full tiles: 2441 tokens in 8 sequences 58 and 77)
-    const auto items = [&](int64_t n, int64_t mean, int rows, bool shorter) {
-      return shorter ? std::min(tiles(n, rows), a.nseq * ceil_div(mean, rows)) : ceil_div(std::min(n, a.nseq * mean), rows);
-    };
     w.key_items = items(a.nk, bk, P.krows, a.nk < a.nq) * a.key_heads;
     w.query_items = items(a.nq, bq, P.qrows, a.nq < a.nk) * a.heads;
     w.queries = std::min(long_q, (bounded ? span : long_q) + P.krows) * grp, w.keys = std::min(long_k, (bounded ? span : long_k) + P.qrows);

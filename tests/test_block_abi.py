@@ -276,3 +276,13 @@ def test_attention_gradient_ranges_of_equal_rows(lib):
     for dtype, most in ((BF16, 28), (F32, 47)):
         st, b = ws(lib, ATT, 2, 1, 128, 2048, 2048, 1, 1, -1, 0, 0, dtype, 1)
         assert st == 0 and 2 * 2048 * 2 * 128 * 4 < b < most * 10 ** 6
+
+
+@pytest.mark.parametrize("nq,nk,seqs,heads,key_heads,d", [(100, 198494, 70, 64, 4, 128), (91, 7644, 70, 64, 1, 128), (207, 137547, 500, 64, 1, 128),
+                                                          (89, 85264, 70, 64, 2, 256), (57, 18522, 70, 64, 1, 128)])
+def test_attention_ranges_of_few_queries(lib, nq, nk, seqs, heads, key_heads, d):
+    """A few queries in many sequences are a tile each, and so many tiles need no ranges of keys: what they would take is many
+    times the tensors."""
+    for dtype, size in ((F32, 4), (BF16, 2)):
+        st, b = ws(lib, ATT, heads, key_heads, d, nq, nk, seqs, 1, -1, 0, 0, dtype, 0)
+        assert st == 0 and b < 2 * (nq * heads + nk * key_heads) * d * size
