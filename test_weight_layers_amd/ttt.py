@@ -738,9 +738,7 @@ def _limit(x: Optional[int], name: str) -> int:
 
 
 def _sinks(x: int) -> int:
-    if x < 0:
-        raise ValueError("sinks must be >= 0")
-    return int(x) if x <= _MAX32 else _MAX32            # (all keys)
+    return max(-1, min(int(x), _MAX32))                 # (2^31 - 1: all keys; -1 is refused)
 
 
 def _heads(q: torch.Tensor, heads: int, key_heads: Optional[int]) -> Tuple[int, int, int]:
